@@ -238,6 +238,56 @@ lce_status lce_ce_logits(const void *Z, int z_dtype, int64_t ld, const int64_t *
                          const float *dloss, float *loss, float *lse, void *dZ,
                          void *ws, size_t ws_bytes, lce_stream_t stream);
 
+/* One token per row of logits Z [N][ld] (first V columns used, ld >= V elements;
+ * z_dtype as for lce_ce_logits), drawn by inversion from u [N], one given uniform
+ * number in [0, 1) per row. With m the row's largest logit, w_i = exp((z_i - m) / T):
+ *   - the tokens are ordered by logit, largest first, equal logits by index;
+ *   - top-k (k > 0) keeps the first k; top-p (p < 1) keeps, of those, each token
+ *     before which less than p of their weight lies; min-p keeps w_i >= min_p. The
+ *     first token of the order is always kept;
+ *   - tokens[i] is the lowest index at which the kept weight up to and including it
+ *     exceeds u times all kept weight; logprobs[i] (NULL: not written) is the log of
+ *     its share of the kept weight.
+ * T <= 0 (or NaN) is greedy: the lowest index of the largest logit, logprob 0. -inf and NaN
+ * logits are never drawn; a row of nothing else gives token -1 and logprob -inf;
+ * tokens at +inf share a row that has them. u outside [0, 1) counts as the nearest
+ * value inside (NaN: the last kept token); min_p above 1 as 1; a NaN top_p as 1, a NaN
+ * min_p as 0.
+ * temperature / top_k / top_p / min_p: one value per row on the device, or NULL for
+ * the value that follows in *_all for every row.
+ * Cumulative weights are exact sums of weights rounded to 2^-43 of the largest, so a
+ * token does not depend on the order of a sum and is the same in every run.
+ * V up to 2^20. Z needs the alignment of its elements only (faster with 16-byte
+ * aligned rows). No workspace, one launch, nothing is kept between calls. */
+lce_status lce_sample_logits(const void *Z, int z_dtype, int64_t ld, int64_t N, int64_t V,
+                             const float *u, const float *temperature, const int32_t *top_k,
+                             const float *top_p, const float *min_p, float temperature_all,
+                             int32_t top_k_all, float top_p_all, float min_p_all,
+                             int64_t *tokens, float *logprobs, lce_stream_t stream);
+
+/* The global norm of a list of n gradients and clipping by it:
+ *   norm = (sum over all tensors of |g|^p)^(1/p) for p = 2 or 1, or max |g|
+ *   out = g * min(1, max_norm / (norm + eps))
+ * grads, sizes (values) and dtypes (as z_dtype above) are arrays of n on the HOST,
+ * read before the call returns; so is outs (NULL: in place), whose tensors have the
+ * dtypes of their gradients. *norm is a device fp32 word. A NaN or an infinity among
+ * the gradients reaches the norm, and a norm that is NaN (infinite) makes the factor NaN
+ * (0), as the formula says. Squares are formed in fp32: values above 1.8e19 give an
+ * infinite 2-norm. Where the factor is 1, tensors in place are not written.
+ * A tensor that is written may overlap no other tensor of the call, except that an
+ * output may be its own gradient: LCE_ERR_INVALID_ARG. Tensors need the alignment of their
+ * elements only. The result does not depend on the run. Work: one read for the
+ * norm, one read and one write for the scaling. Workspace:
+ * lce_grad_norm_workspace_size(n) bytes, 16-byte aligned, which keeps nothing. */
+enum { LCE_NORM_2 = 0, LCE_NORM_INF = 1, LCE_NORM_1 = 2 };
+lce_status lce_grad_norm_workspace_size(int64_t n, size_t *bytes);
+lce_status lce_grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                         int64_t n, int norm_kind, float *norm, void *ws, size_t ws_bytes,
+                         lce_stream_t stream);
+lce_status lce_clip_grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                              void *const *outs, int64_t n, int norm_kind, float max_norm, float eps,
+                              float *norm, void *ws, size_t ws_bytes, lce_stream_t stream);
+
 /* The final RMSNorm in front of the LM head ("Unsloth Architecture: Manual
  * Triton Backpropagation, Fused Cross-Entropy, and 80% VRAM Cut", pillar 3
  * "Fused RMSNorm & SwiGLU Kernels"): per row of X [N][D] (bf16, row-major),
@@ -329,7 +379,8 @@ enum {
     LCE_KERNEL_LOGITS = 0,   /* chunk logits GEMM with the log-sum-exp / G epilogue */
     LCE_KERNEL_GRAD = 1,     /* dH + dW gradient GEMM tiles */
     LCE_KERNEL_MERGE = 2,    /* slab merge (lse, row loss), G rescale, H-chunk transpose */
-    LCE_KERNEL_OTHER = 3,    /* label scan, loss finalisation, dH combination */
+    LCE_KERNEL_OTHER = 3,    /* label scan, loss finalisation, dH combination; the sampling and
+                                gradient-norm kernels */
     LCE_KERNEL_NORM = 4,     /* RMSNorm forward / backward row kernels, dgamma reduction */
     LCE_KERNEL_PHASE = 5,    /* the second chunk of a pair (two chunk buffers): its dH tiles
                                 beside one dW contraction over both chunks of the pair */

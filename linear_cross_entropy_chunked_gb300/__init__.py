@@ -40,4 +40,6 @@ from ._binding import (  # noqa: F401
     workspace_size_opt,
 )
 from .build_lib import LIB_PATH, build  # noqa: F401
+from .clipping import clip_grad_norm, grad_norm  # noqa: F401
+from .sampling import sample_logits  # noqa: F401
 from .sharded import sharded_fwd_bwd  # noqa: F401

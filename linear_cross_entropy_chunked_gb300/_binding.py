@@ -8,6 +8,7 @@ fallback: without the built library every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -55,6 +56,10 @@ EXPORTED = (
     "lce_norm_fwd_bwd",
     "lce_norm_workspace_size_opt",
     "lce_norm_fwd_bwd_opt",
+    "lce_sample_logits",
+    "lce_grad_norm_workspace_size",
+    "lce_grad_norm",
+    "lce_clip_grad_norm",
     "lce_selftest_wait_timeout",
     "lce_read_status",
     "lce_status_string",
@@ -141,6 +146,12 @@ def lib() -> ctypes.CDLL:
     L.lce_norm_fwd_bwd_opt.argtypes = [_vp, _vp, _f, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64,
                                        ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp,
                                        ctypes.c_size_t, _vp]
+    L.lce_sample_logits.argtypes = [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _f,
+                                    ctypes.c_int32, _f, _f, _vp, _vp, _vp]
+    L.lce_grad_norm_workspace_size.argtypes = [_i64, _sz]
+    L.lce_grad_norm.argtypes = [_vp, _vp, _vp, _i64, ctypes.c_int, _vp, _vp, ctypes.c_size_t, _vp]
+    L.lce_clip_grad_norm.argtypes = [_vp, _vp, _vp, _vp, _i64, ctypes.c_int, _f, _f, _vp, _vp,
+                                     ctypes.c_size_t, _vp]
     L.lce_selftest_wait_timeout.argtypes = [_vp, ctypes.c_size_t, _i64, _vp]
     L.lce_read_status.argtypes = [_vp, _vp]
     L.lce_status_string.argtypes = [ctypes.c_int]
@@ -161,7 +172,9 @@ def lib() -> ctypes.CDLL:
                  "lce_rmsnorm_backward_workspace_size", "lce_rmsnorm_backward",
                  "lce_norm_workspace_size", "lce_norm_fwd_bwd", "lce_norm_workspace_size_opt",
                  "lce_norm_fwd_bwd_opt", "lce_forward_workspace_size", "lce_count_valid",
-                 "lce_fwd_bwd_sharded", "lce_noalloc_read_status", "lce_forward_noalloc"):
+                 "lce_fwd_bwd_sharded", "lce_noalloc_read_status", "lce_forward_noalloc",
+                 "lce_sample_logits", "lce_grad_norm_workspace_size", "lce_grad_norm",
+                 "lce_clip_grad_norm"):
         getattr(L, name).restype = ctypes.c_int
     _LIB = L
     return L
@@ -175,6 +188,18 @@ def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+@contextlib.contextmanager
+def _on(dev, stream):
+    """The device of the tensors and the caller's stream as the current ones (outputs
+    and workspaces allocated inside belong to that stream); gives the stream's handle."""
+    with contextlib.ExitStack() as stack:
+        if dev.index is not None and dev.index != torch.cuda.current_device():
+            stack.enter_context(torch.cuda.device(dev))
+        if stream is not None:
+            stack.enter_context(torch.cuda.stream(stream))
+        yield torch.cuda.current_stream().cuda_stream
 
 
 def _check(st: int, what: str):

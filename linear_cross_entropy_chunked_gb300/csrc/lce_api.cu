@@ -12,9 +12,12 @@
 // one with LCE_LOW_MEMORY.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdlib>
+#include <memory>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "../../include/lce.h"
@@ -67,6 +70,7 @@ lce_status init_device(int *sms, int *pairs) {
         if (gemm_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
         if (aux_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
         if (ce_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
+        if (sample_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
         int np = 0;
         if (gemm_max_pairs(&np) != cudaSuccess) {
             cudaGetLastError();
@@ -1097,6 +1101,119 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
     return LCE_OK;
 }
 
+// ---- gradient norm and clipping
+constexpr int64_t kMaxGrads = 1 << 20;
+
+// Whether a written tensor overlaps another tensor of the call (an output may be its
+// own gradient).
+struct Range {
+    uintptr_t a, b;   // bytes [a, b)
+    bool written;
+};
+lce_status check_overlap(const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                         void *const *outs, int64_t n) {
+    std::unique_ptr<Range[]> r(new (std::nothrow) Range[static_cast<size_t>(2 * n)]);
+    if (!r) return LCE_ERR_CUDA;
+    int64_t k = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        if (!sizes[i]) continue;
+        const uintptr_t bytes = static_cast<uintptr_t>(sizes[i]) * (dtypes[i] == CE_FP32 ? 4 : 2);
+        const uintptr_t in = reinterpret_cast<uintptr_t>(grads[i]);
+        const uintptr_t out = outs ? reinterpret_cast<uintptr_t>(outs[i]) : in;
+        r[k++] = {out, out + bytes, true};
+        if (out != in) r[k++] = {in, in + bytes, false};
+    }
+    std::sort(r.get(), r.get() + k, [](const Range &x, const Range &y) { return x.a < y.a; });
+    uintptr_t end = 0, written_end = 0;   // of the ranges so far
+    for (int64_t i = 0; i < k; ++i) {
+        if (r[i].a < (r[i].written ? end : written_end)) return LCE_ERR_INVALID_ARG;
+        end = std::max(end, r[i].b);
+        if (r[i].written) written_end = std::max(written_end, r[i].b);
+    }
+    return LCE_OK;
+}
+
+lce_status grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                     void *const *outs, int64_t n, int kind, bool clip, float max_norm, float eps,
+                     float *norm, void *ws, size_t ws_bytes, lce_stream_t stream) {
+    g_launches = 0;
+    if (n < 0 || n > kMaxGrads || !norm || !ws) return LCE_ERR_INVALID_ARG;
+    if (n > 0 && (!grads || !sizes || !dtypes)) return LCE_ERR_INVALID_ARG;
+    if (kind < LCE_NORM_2 || kind > LCE_NORM_1) return LCE_ERR_INVALID_ARG;
+    bool copy = false;
+    for (int64_t i = 0; i < n; ++i) {
+        if (dtypes[i] < CE_BF16 || dtypes[i] > CE_FP16) return LCE_ERR_INVALID_ARG;
+        if (sizes[i] < 0 || sizes[i] > (1ll << 40)) return LCE_ERR_INVALID_ARG;
+        if (!sizes[i]) continue;
+        if (!grads[i] || (outs && !outs[i])) return LCE_ERR_INVALID_ARG;
+        const uintptr_t elem = dtypes[i] == CE_FP32 ? 4 : 2;
+        if (reinterpret_cast<uintptr_t>(grads[i]) % elem) return LCE_ERR_ALIGNMENT;
+        if (outs && reinterpret_cast<uintptr_t>(outs[i]) % elem) return LCE_ERR_ALIGNMENT;
+        copy |= outs && outs[i] != grads[i];
+    }
+    if (!aligned16(ws) || reinterpret_cast<uintptr_t>(norm) % 4) return LCE_ERR_ALIGNMENT;
+    if (ws_bytes < static_cast<size_t>(n > 0 ? cdiv(n, CLIP_MAX_TENSORS) : 1) * CLIP_MAX_PARTS * sizeof(double))
+        return LCE_ERR_WORKSPACE;
+    if (clip) {
+        const lce_status ov = check_overlap(grads, sizes, dtypes, outs, n);
+        if (ov != LCE_OK) return ov;
+    }
+    int sms = 0, pairs = 0;
+    lce_status st = init_device(&sms, &pairs);
+    if (st != LCE_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    double *part = static_cast<double *>(ws);
+    ClipItem items[CLIP_MAX_TENSORS];
+    // the next tensors of one launch, from tensor i on; returns the tensor after them
+    auto batch = [&](int64_t i, int *m) {
+        *m = 0;
+        long long chunks = 0;
+        for (; i < n && *m < CLIP_MAX_TENSORS; ++i) {
+            if (!sizes[i]) continue;
+            const long long c = clip_chunks(grads[i], sizes[i], dtypes[i]);
+            if (*m > 0 && chunks + c > CLIP_MAX_CHUNKS) break;
+            chunks += c;
+            items[(*m)++] = {grads[i], outs ? outs[i] : const_cast<void *>(grads[i]), sizes[i], dtypes[i], c};
+        }
+        return i;
+    };
+    int nparts = 0, m = 0;
+    int64_t i = 0;
+    bool one_batch = true;
+    do {
+        i = batch(i, &m);
+        one_batch = one_batch && i >= n;
+        if (nparts + CLIP_MAX_PARTS > static_cast<long long>(ws_bytes / sizeof(double))) return LCE_ERR_WORKSPACE;
+        if (m > 0) {
+            int wrote = 0;
+            LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s,
+                            launch_grad_norm(items, m, kind, part + nparts, sms, &wrote, s));
+            nparts += wrote;
+        }
+    } while (i < n);
+    ClipScale c;
+    c.kind = kind;
+    c.part = part;
+    c.nparts = nparts;
+    c.max_norm = max_norm;
+    c.eps = eps;
+    c.copy = copy ? 1 : 0;
+    c.tell = 1;
+    c.norm_out = norm;
+    if (!clip) {
+        LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_grad_scale(items, 0, c, sms, s));
+        return LCE_OK;
+    }
+    i = 0;
+    do {
+        if (!one_batch) i = batch(i, &m);
+        else i = n;
+        LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_grad_scale(items, m, c, sms, s));
+        c.tell = 0;
+    } while (i < n);
+    return LCE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1412,6 +1529,71 @@ lce_status lce_ce_logits(const void *Z, int z_dtype, int64_t ld, const int64_t *
                         launch_loss_finalize(loss_rows, N, hdr, loss,
                                              reduction == LCE_REDUCTION_MEAN, s));
     return LCE_OK;
+}
+
+lce_status lce_sample_logits(const void *Z, int z_dtype, int64_t ld, int64_t N, int64_t V,
+                             const float *u, const float *temperature, const int32_t *top_k,
+                             const float *top_p, const float *min_p, float temperature_all,
+                             int32_t top_k_all, float top_p_all, float min_p_all,
+                             int64_t *tokens, float *logprobs, lce_stream_t stream) {
+    g_launches = 0;
+    if (N < 0 || N > (1ll << 27) || V <= 0 || V > SMP_MAX_V || ld < V) return LCE_ERR_INVALID_ARG;
+    if (z_dtype < CE_BF16 || z_dtype > CE_FP16) return LCE_ERR_INVALID_ARG;
+    if (N > 0 && (!Z || !u || !tokens)) return LCE_ERR_INVALID_ARG;
+    const uintptr_t elem = z_dtype == CE_FP32 ? 4 : 2;
+    const uintptr_t words = reinterpret_cast<uintptr_t>(u) | reinterpret_cast<uintptr_t>(temperature) |
+                            reinterpret_cast<uintptr_t>(top_k) | reinterpret_cast<uintptr_t>(top_p) |
+                            reinterpret_cast<uintptr_t>(min_p) | reinterpret_cast<uintptr_t>(logprobs);
+    if (reinterpret_cast<uintptr_t>(Z) % elem || words % 4 || reinterpret_cast<uintptr_t>(tokens) % 8)
+        return LCE_ERR_ALIGNMENT;
+    int sms = 0, pairs = 0;
+    lce_status st = init_device(&sms, &pairs);
+    if (st != LCE_OK) return st;
+    if (N == 0) return LCE_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    SampleParams p;
+    p.Z = Z;
+    p.ld = ld;
+    p.N = N;
+    p.V = static_cast<int>(V);
+    p.dtype = z_dtype;
+    p.u = u;
+    p.temperature = temperature;
+    p.top_k = top_k;
+    p.top_p = top_p;
+    p.min_p = min_p;
+    p.temperature_all = temperature_all;
+    p.top_k_all = top_k_all;
+    p.top_p_all = top_p_all;
+    p.min_p_all = min_p_all;
+    p.tokens = reinterpret_cast<long long *>(tokens);
+    p.logprobs = logprobs;
+    LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_sample(p, s));
+    return LCE_OK;
+}
+
+lce_status lce_grad_norm_workspace_size(int64_t n, size_t *bytes) {
+    if (!bytes || n < 0 || n > kMaxGrads) return LCE_ERR_INVALID_ARG;
+    *bytes = static_cast<size_t>(n > 0 ? cdiv(n, CLIP_MAX_TENSORS) : 1) * CLIP_MAX_PARTS * sizeof(double);
+    return LCE_OK;
+}
+
+lce_status lce_grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                         int64_t n, int norm_kind, float *norm, void *ws, size_t ws_bytes,
+                         lce_stream_t stream) {
+    return grad_norm(grads, sizes, dtypes, nullptr, n, norm_kind, false, 0.f, 0.f, norm, ws, ws_bytes,
+                     stream);
+}
+
+lce_status lce_clip_grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                              void *const *outs, int64_t n, int norm_kind, float max_norm, float eps,
+                              float *norm, void *ws, size_t ws_bytes, lce_stream_t stream) {
+    if (!(max_norm >= 0.f) || !(eps >= 0.f)) {
+        g_launches = 0;
+        return LCE_ERR_INVALID_ARG;
+    }
+    return grad_norm(grads, sizes, dtypes, outs, n, norm_kind, true, max_norm, eps, norm, ws, ws_bytes,
+                     stream);
 }
 
 lce_status lce_selftest_wait_timeout(void *ws, size_t ws_bytes, int64_t limit_us,

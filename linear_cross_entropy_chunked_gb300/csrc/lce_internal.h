@@ -236,6 +236,63 @@ struct NormParams {
     float eps;
 };
 
+// Drawing one token per row of logits (lce_sample.cu). A null pointer: the value that
+// follows for every row.
+struct SampleParams {
+    const void *Z;
+    long long ld, N;
+    int V;
+    int dtype;                // CE_BF16, CE_FP32 or CE_FP16
+    const float *u;           // [N]
+    const float *temperature; // [N] or null
+    const int *top_k;
+    const float *top_p;
+    const float *min_p;
+    float temperature_all;
+    int top_k_all;
+    float top_p_all, min_p_all;
+    long long *tokens;        // [N]
+    float *logprobs;          // [N] or null
+};
+// 2^(-j / 64) in units of 2^-50 and as fp32; ln(2) / 64 in three parts, and its inverse
+struct SampleTables {
+    unsigned long long fix[64];
+    float flt[64];
+    float c1, c2, c3, inv;
+};
+constexpr long long SMP_MAX_V = 1ll << 20;   // weights of 2^43 in 64-bit sums
+
+// Gradient norm and clipping (lce_clip.cu).
+enum : int { CLIP_NORM_2 = 0, CLIP_NORM_INF = 1, CLIP_NORM_1 = 2 };
+struct ClipItem {
+    const void *src;
+    void *dst;             // where the scaled values go (src: in place)
+    long long n;           // values
+    int dtype;             // CE_BF16, CE_FP32 or CE_FP16
+    long long chunks;
+};
+// The list as it travels in the kernels' parameters (at most 32764 bytes).
+template <int CAP> struct ClipTable {
+    const void *src[CAP];
+    void *dst[CAP];
+    long long count[CAP];  // values * 4 + dtype
+    int first[CAP + 1];    // first chunk
+    int n;
+};
+constexpr int CLIP_FEW_TENSORS = 64;
+constexpr int CLIP_MAX_TENSORS = 1024;   // per launch
+constexpr long long CLIP_MAX_CHUNKS = 1ll << 30;   // per launch
+constexpr int CLIP_MAX_PARTS = 1024;     // partial sums (CTAs) per launch
+struct ClipScale {
+    int kind;
+    const double *part;
+    int nparts;
+    float max_norm, eps;
+    int copy;              // 1: some destination is another place than its source
+    int tell;              // 1: this launch writes the norm
+    float *norm_out;
+};
+
 // launchers (return cudaError_t of the launch)
 // cluster = 1: one CTA per 128 x 256 tile; 2: a CTA pair per 256 x 256 tile
 // (tcgen05 cta_group::2, each CTA loading its own A rows and half of B).
@@ -266,6 +323,14 @@ cudaError_t launch_combine_dh(const float *src, int splits, long long stride, vo
 cudaError_t launch_rmsnorm_fwd(const NormParams &p, cudaStream_t s);
 cudaError_t launch_rmsnorm_bwd(const NormParams &p, cudaStream_t s);
 cudaError_t launch_dgamma_reduce(const float *part, int D, float *dgamma, cudaStream_t s);
+
+cudaError_t sample_set_attributes();
+cudaError_t launch_sample(const SampleParams &p, cudaStream_t s);
+long long clip_chunks(const void *p, long long n, int dtype);
+// *parts: partial sums written to `part`
+cudaError_t launch_grad_norm(const ClipItem *items, int n, int kind, double *part, int sms, int *parts,
+                             cudaStream_t s);
+cudaError_t launch_grad_scale(const ClipItem *items, int n, const ClipScale &c, int sms, cudaStream_t s);
 
 constexpr float LOG2E_F = 1.4426950408889634f;
 
