@@ -265,6 +265,35 @@ lce_status lce_sample_logits(const void *Z, int z_dtype, int64_t ld, int64_t N, 
                              int32_t top_k_all, float top_p_all, float min_p_all,
                              int64_t *tokens, float *logprobs, lce_stream_t stream);
 
+/* Linear layers in 8-bit floating point (e4m3), one fp32 scale per block of 128 values
+ * along the contraction (the last block of a row may be shorter):
+ *   rows:  x[r][k] ~ scale[r][k / 128] * q[r][k],        scale [R][ceil(C / 128)]
+ *   tiles: w[r][k] ~ scale[r / 128][k / 128] * q[r][k],  scale [ceil(R / 128)][ceil(C / 128)]
+ *
+ * lce_fp8_quantize: X [R][ld] (x_dtype as for lce_ce_logits, C columns) to row blocks, or
+ * to tiles (tiles = 1); the scale is the smallest power of two (at least 2^-126) under which the
+ * block's largest finite |x| is at most 448, 1 for a block of zeros; q is x / scale rounded
+ * to the nearest e4m3 value, ties to even; infinities and NaN become NaN. q [R][ldq] and
+ * scale: X in its own layout; qt [C][ldqt] and scale_t: X^T in the same form (row blocks
+ * then run along X's rows); either pair may be NULL. ldq, ldqt: multiples of 16 (bytes); a
+ * row's bytes up to the next multiple of 16 may be written. q, qt 16-byte aligned.
+ *
+ * lce_fp8_matmul: out [M][ldc] (c_dtype) = A B^T with A [M][lda] in row blocks and
+ * B [N][ldb] in tiles or (b_rows = 1) in row blocks, any fp32 scales:
+ *   out[m][n] = sum over blocks b of (sa[m][b] * sb[n or n / 128][b]) * sum_{k in b} A[m][k] B[n][k]
+ * summed in fp32, rounded once. With it: logits = x W^T (x in rows, W in tiles); dx =
+ * dlogits W (dlogits in rows, W^T in tiles); dW = dlogits^T x (both transposed, in rows).
+ * A, B, out 16-byte aligned; lda, ldb and ldc's bytes multiples of 16; K, lda, ldb in
+ * values = bytes. Columns of `out` from N on are left as they were. Workspace: a header
+ * for the device status (lce_read_status), lce_fp8_matmul_workspace_size bytes. */
+lce_status lce_fp8_quantize(const void *X, int x_dtype, int64_t ld, int64_t R, int64_t C, int tiles,
+                            void *q, int64_t ldq, float *scale, void *qt, int64_t ldqt,
+                            float *scale_t, lce_stream_t stream);
+lce_status lce_fp8_matmul_workspace_size(size_t *bytes);
+lce_status lce_fp8_matmul(const void *A, int64_t lda, const float *sa, const void *B, int64_t ldb,
+                          const float *sb, int b_rows, int64_t M, int64_t N, int64_t K, void *out,
+                          int64_t ldc, int c_dtype, void *ws, size_t ws_bytes, lce_stream_t stream);
+
 /* The global norm of a list of n gradients and clipping by it:
  *   norm = (sum over all tensors of |g|^p)^(1/p) for p = 2 or 1, or max |g|
  *   out = g * min(1, max_norm / (norm + eps))
@@ -379,8 +408,8 @@ enum {
     LCE_KERNEL_LOGITS = 0,   /* chunk logits GEMM with the log-sum-exp / G epilogue */
     LCE_KERNEL_GRAD = 1,     /* dH + dW gradient GEMM tiles */
     LCE_KERNEL_MERGE = 2,    /* slab merge (lse, row loss), G rescale, H-chunk transpose */
-    LCE_KERNEL_OTHER = 3,    /* label scan, loss finalisation, dH combination; the sampling and
-                                gradient-norm kernels */
+    LCE_KERNEL_OTHER = 3,    /* label scan, loss finalisation, dH combination; the sampling,
+                                gradient-norm and 8-bit kernels */
     LCE_KERNEL_NORM = 4,     /* RMSNorm forward / backward row kernels, dgamma reduction */
     LCE_KERNEL_PHASE = 5,    /* the second chunk of a pair (two chunk buffers): its dH tiles
                                 beside one dW contraction over both chunks of the pair */

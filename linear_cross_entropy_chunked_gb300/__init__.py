@@ -41,5 +41,13 @@ from ._binding import (  # noqa: F401
 )
 from .build_lib import LIB_PATH, build  # noqa: F401
 from .clipping import clip_grad_norm, grad_norm  # noqa: F401
+from .fp8 import (  # noqa: F401
+    FP8LinearFunction,
+    FP8Weight,
+    fp8_linear,
+    fp8_matmul,
+    fp8_weight,
+    quantize_fp8,
+)
 from .sampling import sample_logits  # noqa: F401
 from .sharded import sharded_fwd_bwd  # noqa: F401

@@ -57,6 +57,9 @@ EXPORTED = (
     "lce_norm_workspace_size_opt",
     "lce_norm_fwd_bwd_opt",
     "lce_sample_logits",
+    "lce_fp8_quantize",
+    "lce_fp8_matmul_workspace_size",
+    "lce_fp8_matmul",
     "lce_grad_norm_workspace_size",
     "lce_grad_norm",
     "lce_clip_grad_norm",
@@ -148,6 +151,11 @@ def lib() -> ctypes.CDLL:
                                        ctypes.c_size_t, _vp]
     L.lce_sample_logits.argtypes = [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _f,
                                     ctypes.c_int32, _f, _f, _vp, _vp, _vp]
+    L.lce_fp8_quantize.argtypes = [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp,
+                                   _vp, _i64, _vp, _vp]
+    L.lce_fp8_matmul_workspace_size.argtypes = [_sz]
+    L.lce_fp8_matmul.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64,
+                                 ctypes.c_int, _vp, ctypes.c_size_t, _vp]
     L.lce_grad_norm_workspace_size.argtypes = [_i64, _sz]
     L.lce_grad_norm.argtypes = [_vp, _vp, _vp, _i64, ctypes.c_int, _vp, _vp, ctypes.c_size_t, _vp]
     L.lce_clip_grad_norm.argtypes = [_vp, _vp, _vp, _vp, _i64, ctypes.c_int, _f, _f, _vp, _vp,
@@ -174,7 +182,8 @@ def lib() -> ctypes.CDLL:
                  "lce_norm_fwd_bwd_opt", "lce_forward_workspace_size", "lce_count_valid",
                  "lce_fwd_bwd_sharded", "lce_noalloc_read_status", "lce_forward_noalloc",
                  "lce_sample_logits", "lce_grad_norm_workspace_size", "lce_grad_norm",
-                 "lce_clip_grad_norm"):
+                 "lce_clip_grad_norm", "lce_fp8_quantize", "lce_fp8_matmul_workspace_size",
+                 "lce_fp8_matmul"):
         getattr(L, name).restype = ctypes.c_int
     _LIB = L
     return L

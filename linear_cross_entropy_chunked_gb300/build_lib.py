@@ -22,7 +22,7 @@ LIB_NAME = "liblce_gb300.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["lce_gemm.cu", "lce_aux.cu", "lce_ce.cu", "lce_norm.cu", "lce_sample.cu",
-           "lce_clip.cu", "lce_api.cu", "lce_noalloc.cu"]
+           "lce_clip.cu", "lce_fp8.cu", "lce_api.cu", "lce_noalloc.cu"]
 HEADERS = [os.path.join(CSRC, "lce_internal.h"), os.path.join(CSRC, "lce_ptx.cuh"),
            os.path.join(INCLUDE, "lce.h")]
 

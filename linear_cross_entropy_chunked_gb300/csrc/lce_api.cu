@@ -71,6 +71,7 @@ lce_status init_device(int *sms, int *pairs) {
         if (aux_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
         if (ce_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
         if (sample_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
+        if (fp8_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
         int np = 0;
         if (gemm_max_pairs(&np) != cudaSuccess) {
             cudaGetLastError();
@@ -213,7 +214,7 @@ bool make_norm_layout(long long N, long long D, long long V, long long chunk, No
 }
 
 // Element types of the tensor maps.
-enum MapType { MAP_BF16, MAP_F16, MAP_F32 };
+enum MapType { MAP_BF16, MAP_F16, MAP_F32, MAP_U8 };
 
 // Tensor map over a row-major array with the 128-byte swizzle of the MMA
 // operand tiles and of the epilogue staging boxes; zero fill out of bounds on
@@ -231,6 +232,7 @@ bool encode_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims
     for (int i = 0; i + 1 < rank; ++i) st[i] = strides_bytes[i];
     const CUtensorMapDataType dt = type == MAP_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : type == MAP_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                   : type == MAP_U8  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     CUresult r = g_encode(m, dt,
                           rank, const_cast<void *>(base), d, st, bx, es,
@@ -239,7 +241,7 @@ bool encode_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims
     return r == CUDA_SUCCESS;
 }
 
-// MMA operand tile load map: 2-D, 16-bit elements (bf16 or fp16), box
+// MMA operand tile load map: 2-D, 16-bit (bf16 or fp16) or 8-bit elements, box
 // {box_inner, box_outer}.
 bool encode_2d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer,
                uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer,
@@ -1569,6 +1571,104 @@ lce_status lce_sample_logits(const void *Z, int z_dtype, int64_t ld, int64_t N, 
     p.tokens = reinterpret_cast<long long *>(tokens);
     p.logprobs = logprobs;
     LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_sample(p, s));
+    return LCE_OK;
+}
+
+lce_status lce_fp8_quantize(const void *X, int x_dtype, int64_t ld, int64_t R, int64_t C, int tiles,
+                            void *q, int64_t ldq, float *scale, void *qt, int64_t ldqt,
+                            float *scale_t, lce_stream_t stream) {
+    g_launches = 0;
+    if (x_dtype < CE_BF16 || x_dtype > CE_FP16) return LCE_ERR_INVALID_ARG;
+    if (R < 0 || C <= 0 || R > 0x7fffffffll || C > 0x7fffffffll || ld < C) return LCE_ERR_INVALID_ARG;
+    if ((!q && !qt) || (R > 0 && !X)) return LCE_ERR_INVALID_ARG;
+    if ((q && (!scale || ldq < C)) || (qt && (!scale_t || ldqt < R))) return LCE_ERR_INVALID_ARG;
+    const uintptr_t elem = x_dtype == CE_FP32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(X) % elem || (q && (!aligned16(q) || ldq % 16)) ||
+        (qt && (!aligned16(qt) || ldqt % 16)) || reinterpret_cast<uintptr_t>(scale) % 4 ||
+        reinterpret_cast<uintptr_t>(scale_t) % 4)
+        return LCE_ERR_ALIGNMENT;
+    int sms = 0, pairs = 0;
+    lce_status st = init_device(&sms, &pairs);
+    if (st != LCE_OK) return st;
+    Fp8QuantParams p;
+    p.X = X;
+    p.ld = ld;
+    p.R = R;
+    p.C = C;
+    p.rblocks = cdiv(R, 128);
+    p.cblocks = cdiv(C, 128);
+    if (p.rblocks * p.cblocks > 0x7fffffffll) return LCE_ERR_INVALID_ARG;
+    p.vec = aligned16(X) && (ld * static_cast<int64_t>(elem)) % 16 == 0 ? 1 : 0;
+    p.q = static_cast<uint8_t *>(q);
+    p.ldq = ldq;
+    p.scale = scale;
+    p.qt = static_cast<uint8_t *>(qt);
+    p.ldqt = ldqt;
+    p.scale_t = scale_t;
+    if (R == 0) return LCE_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_fp8_quantize(p, x_dtype, tiles != 0, s));
+    return LCE_OK;
+}
+
+lce_status lce_fp8_matmul_workspace_size(size_t *bytes) {
+    if (!bytes) return LCE_ERR_INVALID_ARG;
+    *bytes = 1024;
+    return LCE_OK;
+}
+
+lce_status lce_fp8_matmul(const void *A, int64_t lda, const float *sa, const void *B, int64_t ldb,
+                          const float *sb, int b_rows, int64_t M, int64_t N, int64_t K, void *out,
+                          int64_t ldc, int c_dtype, void *ws, size_t ws_bytes, lce_stream_t stream) {
+    g_launches = 0;
+    if (M < 0 || N < 0 || K <= 0 || M > MAX_V || N > MAX_V || K > MAX_V) return LCE_ERR_INVALID_ARG;
+    if (lda < K || ldb < K || ldc < N || c_dtype < CE_BF16 || c_dtype > CE_FP16 || !ws)
+        return LCE_ERR_INVALID_ARG;
+    if (M > 0 && N > 0 && (!A || !sa || !B || !sb || !out)) return LCE_ERR_INVALID_ARG;
+    const int64_t elem = c_dtype == CE_FP32 ? 4 : 2;
+    if (!aligned16(A) || !aligned16(B) || !aligned16(out) || !aligned16(ws) || lda % 16 || ldb % 16 ||
+        (ldc * elem) % 16 || reinterpret_cast<uintptr_t>(sa) % 4 || reinterpret_cast<uintptr_t>(sb) % 4)
+        return LCE_ERR_ALIGNMENT;
+    if (ws_bytes < 1024) return LCE_ERR_WORKSPACE;
+    int sms = 0, pairs = 0;
+    lce_status st = init_device(&sms, &pairs);
+    if (st != LCE_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (M == 0 || N == 0)
+        return cudaMemsetAsync(ws, 0, sizeof(int), s) == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
+
+    Fp8GemmParams p;
+    memset(&p, 0, sizeof(p));
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.KB = static_cast<int>(cdiv(K, 128));
+    const long long pair_tiles = cdiv(M, 256) * cdiv(N, 256), tiles = cdiv(M, 128) * cdiv(N, 128);
+    const bool pair = M > 128 && pairs > 0 && pair_tiles >= pairs / 2;
+    if (tiles > 0x7fffffffll) return LCE_ERR_INVALID_ARG;
+    int split = 1;
+    if (!pair)
+        while (split < 8 && tiles * split * 2 <= sms && p.KB >= split * 4) split *= 2;
+    p.m_tiles = static_cast<int>(pair ? cdiv(M, 256) : cdiv(M, 128));
+    p.n_tiles = static_cast<int>(pair ? cdiv(N, 256) : cdiv(N, 128));
+    p.tiles = static_cast<int>(pair ? pair_tiles : tiles);
+    p.a_box_rows = pair || M >= 128 ? 128 : static_cast<int>(align_up(static_cast<size_t>(M), 8));
+    p.n_bulk = static_cast<int>(N / (16 / elem) * (16 / elem));
+    p.sa = sa;
+    p.sb = sb;
+    p.C = out;
+    p.ldc = ldc;
+    p.c_type = c_dtype;
+    p.hdr = static_cast<int *>(ws);
+    p.timeout_ns = kDefaultTimeoutNs;
+    const MapType ct = c_dtype == CE_FP32 ? MAP_F32 : c_dtype == CE_FP16 ? MAP_F16 : MAP_BF16;
+    if (!encode_2d(&p.tmA, A, K, M, lda, 128, p.a_box_rows, MAP_U8) ||
+        !encode_2d(&p.tmB, B, K, N, ldb, 128, 128, MAP_U8) ||
+        (p.n_bulk > 0 && !encode_store_2d(&p.tmC, out, p.n_bulk, M, ldc * elem, ct, 32)))
+        return LCE_ERR_CUDA;
+    const int cluster = pair ? 2 : split;
+    const int most = pair ? pairs : split > 1 ? p.tiles : sms;
+    const int clusters = p.tiles < most ? p.tiles : most;
+    LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_fp8_matmul(p, pair, b_rows != 0, cluster, clusters, s));
     return LCE_OK;
 }
 

@@ -1,0 +1,728 @@
+// Linear layers in 8-bit floating point (e4m3) with one fp32 scale per block of 128
+// values along the contraction: quantisation, and the product of two such operands.
+//
+//   rows:  x[r, k] ~ s[r, k / 128] * q[r, k]                 (activations, gradients)
+//   tiles: w[n, k] ~ s[n / 128, k / 128] * q[n, k]           (weights)
+//   C[m, n] = sum over k blocks b of sa[m, b] * sb[n, b] * sum_{k in b} qa[m, k] qb[n, k]
+//
+// The scale of a block is the smallest power of two under which its largest finite
+// value is at most 448 (e4m3's largest), so the division is exact and e4m3's own rounding
+// is the only one; the product takes any fp32 scales.
+#include <cuda_fp8.h>
+
+#include "lce_internal.h"
+#include "lce_ptx.cuh"
+
+namespace lce {
+
+// ------------------------------------------------------------------ quantisation
+// One CTA per 128 x 128 tile of X, which its threads hold in registers (8 x 8 values
+// each), so X is read once for up to two outputs: row blocks or tiles in X's own layout,
+// and the same of X^T (blocks along X's rows), turned through shared memory. Bound by
+// HBM bandwidth: 2 (4) bytes read and 1 or 2 written per value.
+
+namespace {
+
+constexpr int QT_THREADS = 256;
+
+// 2^e of a block whose largest finite |x| is amax, and 2^-e.
+struct Pow2 {
+    float scale, inv;
+};
+__device__ __forceinline__ Pow2 block_scale(float amax) {
+    const uint32_t b = __float_as_uint(amax);
+    // amax = 1.m * 2^x; 448 = 1.75 * 2^8
+    int e = static_cast<int>(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+    if (e < -126) e = -126;
+    if (b == 0u) e = 0;
+    Pow2 s;
+    s.scale = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+    s.inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    return s;
+}
+__device__ __forceinline__ float finite_abs(float x) {
+    const float a = fabsf(x);
+    return a < INFINITY ? a : 0.f;   // NaN and infinities do not count
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+template <typename T> __device__ __forceinline__ float qt_float(T v) { return static_cast<float>(v); }
+
+// 8 values of a row; those past `n` are 0; infinities become NaN (e4m3 has none).
+template <typename T>
+__device__ __forceinline__ void qt_load8(const T *p, int n, bool vec, float (&x)[8]) {
+    if (vec && n >= 8) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 a = __ldcs(reinterpret_cast<const float4 *>(p));
+            const float4 b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        } else {
+            const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p));
+            const T *h = reinterpret_cast<const T *>(&u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = qt_float(h[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = j < n ? qt_float(p[j]) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (fabsf(x[j]) == INFINITY) x[j] = __uint_as_float(0x7fffffffu);
+}
+
+template <typename T, bool TILE>
+__global__ void __launch_bounds__(QT_THREADS, 2) lce_fp8_quantize_kernel(const Fp8QuantParams p) {
+    __shared__ __align__(16) uint8_t st[128 * 128];
+    __shared__ float cred[QT_THREADS / 32][128];
+    const int t = threadIdx.x, w = t >> 5, l = t & 31;
+    const int i = t & 15, g = t >> 4;          // columns 8 i .. + 7, rows 8 g .. + 7 of the tile
+    const long long tile = blockIdx.x;
+    const long long rb = tile / p.cblocks, cb = tile - rb * p.cblocks;
+    const long long r0 = rb * 128, c0 = cb * 128;
+    const int nr = p.R - r0 < 128 ? static_cast<int>(p.R - r0) : 128;
+    const int nc = p.C - c0 < 128 ? static_cast<int>(p.C - c0) : 128;
+    const T *X = static_cast<const T *>(p.X) + r0 * p.ld + c0;
+    float x[8][8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int r = g * 8 + k;
+        if (r < nr && i * 8 < nc) {
+            qt_load8<T>(X + static_cast<long long>(r) * p.ld + i * 8, nc - i * 8, p.vec != 0, x[k]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[k][j] = 0.f;
+        }
+    }
+    Pow2 tile_s = {1.f, 1.f};
+    if constexpr (TILE) {
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = fmaxf(m, finite_abs(x[k][j]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (l == 0) cred[0][w] = m;
+        __syncthreads();
+        m = cred[0][l & 7];
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        tile_s = block_scale(m);
+        if (t == 0) {
+            if (p.q) p.scale[rb * p.cblocks + cb] = tile_s.scale;
+            if (p.qt) p.scale_t[cb * p.rblocks + rb] = tile_s.scale;
+        }
+    }
+    if (p.q) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = g * 8 + k;
+            Pow2 s = tile_s;
+            if constexpr (!TILE) {
+                float m = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m = fmaxf(m, finite_abs(x[k][j]));
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                s = block_scale(m);
+                if (i == 0 && r < nr) p.scale[(r0 + r) * p.cblocks + cb] = s.scale;
+            }
+            if (r < nr && i * 8 < nc) {
+                const float f = s.inv;
+                uint2 v;
+                v.x = e4m3x4(x[k][0] * f, x[k][1] * f, x[k][2] * f, x[k][3] * f);
+                v.y = e4m3x4(x[k][4] * f, x[k][5] * f, x[k][6] * f, x[k][7] * f);
+                *reinterpret_cast<uint2 *>(p.q + (r0 + r) * p.ldq + c0 + i * 8) = v;
+            }
+        }
+    }
+    if (p.qt) {
+        float inv[8];
+        if constexpr (TILE) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) inv[j] = tile_s.inv;
+        } else {
+            float m[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                m[j] = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) m[j] = fmaxf(m[j], finite_abs(x[k][j]));
+                m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+            }
+            if (l < 16) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) cred[w][i * 8 + j] = m[j];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float a = 0.f;
+#pragma unroll
+                for (int k = 0; k < QT_THREADS / 32; ++k) a = fmaxf(a, cred[k][i * 8 + j]);
+                const Pow2 s = block_scale(a);
+                inv[j] = s.inv;
+                if (g == 0 && i * 8 + j < nc) p.scale_t[(c0 + i * 8 + j) * p.rblocks + rb] = s.scale;
+            }
+        }
+        // column c's 8-byte unit of rows 8 g .. + 7 goes to unit g ^ (c / 8) of its 128 bytes,
+        // which spreads the 16 columns that a half-warp writes at once over all banks
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float f = inv[j];
+            uint2 v;
+            v.x = e4m3x4(x[0][j] * f, x[1][j] * f, x[2][j] * f, x[3][j] * f);
+            v.y = e4m3x4(x[4][j] * f, x[5][j] * f, x[6][j] * f, x[7][j] * f);
+            *reinterpret_cast<uint2 *>(st + (i * 8 + j) * 128 + ((g ^ i) << 3)) = v;
+        }
+        __syncthreads();
+        const int u = t & 7;   // 16 bytes of a column
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int c = (t >> 3) + 32 * k;
+            const int sw = (c >> 3) & 15;
+            uint4 v = *reinterpret_cast<const uint4 *>(st + c * 128 + ((u ^ (sw >> 1)) << 4));
+            if (sw & 1) v = make_uint4(v.z, v.w, v.x, v.y);
+            if (c < nc && u * 16 < nr) *reinterpret_cast<uint4 *>(p.qt + (c0 + c) * p.ldqt + r0 + u * 16) = v;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_quantize(const Fp8QuantParams &p, int dtype, bool tile, cudaStream_t s) {
+    const long long n = p.rblocks * p.cblocks;
+    if (n <= 0) return cudaSuccess;
+    const unsigned grid = static_cast<unsigned>(n);
+    if (dtype == CE_FP32) {
+        if (tile) lce_fp8_quantize_kernel<float, true><<<grid, QT_THREADS, 0, s>>>(p);
+        else lce_fp8_quantize_kernel<float, false><<<grid, QT_THREADS, 0, s>>>(p);
+    } else if (dtype == CE_FP16) {
+        if (tile) lce_fp8_quantize_kernel<__half, true><<<grid, QT_THREADS, 0, s>>>(p);
+        else lce_fp8_quantize_kernel<__half, false><<<grid, QT_THREADS, 0, s>>>(p);
+    } else {
+        if (tile) lce_fp8_quantize_kernel<__nv_bfloat16, true><<<grid, QT_THREADS, 0, s>>>(p);
+        else lce_fp8_quantize_kernel<__nv_bfloat16, false><<<grid, QT_THREADS, 0, s>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ product
+// tcgen05 kind::f8f6f4 MMAs contract one k block of 128 into a TMEM buffer; the scales
+// differ from block to block, so the tile's sum is kept in fp32 registers: as soon as
+// a block's partial product is complete, the consumer warps read it from TMEM and add
+// sa * sb times it, while the MMAs of the next blocks fill the other buffers.
+//
+// Roles (320 threads): warps 0-7 consumers (TMEM lane quarter = warp % 4, column half
+// = warp / 4), warp 8 TMA producer, warp 9 TMEM owner + MMA issuer. A static persistent
+// schedule: unit u of cluster c is tile c + u * clusters.
+//
+// PAIR: a CTA pair per 256 x 256 tile (cta_group::2; each CTA its own 128 rows of A
+// and half of B's), for products with many tiles. Otherwise 128 x 128 tiles, one CTA
+// each; few tiles are split along k over a cluster of up to 8 CTAs, whose fp32 sums are
+// added through distributed shared memory in rank order.
+// B_ROWS: B's scales are per row (gradient of a weight), read through shared memory.
+// Every mbarrier wait is bounded, as in the bf16 GEMM.
+
+namespace {
+
+constexpr int F8_BK = 128;                 // values (bytes) per k block: one 128-byte swizzle row
+constexpr int F8_OP_BYTES = 128 * F8_BK;   // 128 rows of an operand
+constexpr int F8_STAGE = 2 * F8_OP_BYTES;  // A and B of one k block, per CTA
+constexpr int F8_STAGES = 6;
+constexpr int F8_WARP_BOX = 4096;          // 32 rows x 128 bytes of output per consumer warp
+constexpr int F8_SMEM = F8_STAGES * F8_STAGE + 8 * F8_WARP_BOX + 1024;
+constexpr int F8_GROUP = 16;               // row tiles that run together (they share B in L2)
+
+// Instruction descriptor of tcgen05.mma kind::f8f6f4, e4m3 x e4m3 -> fp32, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+    return (1u << 4)                                // D format: f32
+           | (0u << 7) | (0u << 10)                 // A, B format: e4m3
+           | (static_cast<uint32_t>(N >> 3) << 17)  // N / 8
+           | (static_cast<uint32_t>(M >> 4) << 24); // M / 16
+}
+template <bool PAIR>
+__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t f8_cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+// Tile t: row tiles in groups of F8_GROUP, the rows of a group fastest, then columns.
+__device__ __forceinline__ void f8_tile(const Fp8GemmParams &p, int t, int *mt, int *nt) {
+    const int per = F8_GROUP * p.n_tiles;
+    const int grp = t / per;
+    t -= grp * per;
+    const int rows = min(F8_GROUP, p.m_tiles - grp * F8_GROUP);
+    *nt = t / rows;
+    *mt = grp * F8_GROUP + (t - *nt * rows);
+}
+
+template <bool PAIR, bool B_ROWS>
+__global__ void __launch_bounds__(GEMM_THREADS, 1)
+    lce_fp8_matmul_kernel(const __grid_constant__ Fp8GemmParams p) {
+    constexpr int CL = PAIR ? 2 : 1;
+    constexpr int BNT = PAIR ? 256 : 128;
+    constexpr int NBUF = TMEM_COLS / BNT;      // partial products in flight
+    constexpr int COLS = BNT / 2;              // columns per consumer warp
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full_bar[F8_STAGES];
+    __shared__ __align__(8) uint64_t empty_bar[F8_STAGES];
+    __shared__ __align__(8) uint64_t tfull_bar[NBUF];
+    __shared__ __align__(8) uint64_t tempty_bar[NBUF];
+    __shared__ __align__(8) uint64_t drain_bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort_flag;
+
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank(), csize = f8_cluster_size();
+    const uint32_t crank = PAIR ? rank : 0u;
+    const bool leader = crank == 0;
+    const int cid = static_cast<int>(blockIdx.x / csize), ncl = static_cast<int>(gridDim.x / csize);
+    // this CTA's k blocks: all, or its part of a split product
+    const int kb0 = PAIR ? 0 : static_cast<int>(static_cast<long long>(p.KB) * rank / csize);
+    const int kb1 = PAIR ? p.KB : static_cast<int>(static_cast<long long>(p.KB) * (rank + 1) / csize);
+    const int nk = kb1 - kb0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < F8_STAGES; ++s) {
+            mbar_init(&full_bar[s], 1);
+            mbar_init(&empty_bar[s], 1);
+        }
+        for (int b = 0; b < NBUF; ++b) {
+            mbar_init(&tfull_bar[b], 1);
+            mbar_init(&tempty_bar[b], CL * NUM_EPI_WARPS);
+        }
+        mbar_init(&drain_bar, 1);
+        abort_flag = 0;
+        // cleared here, long before the first wait of any CTA can run out
+        if (blockIdx.x == 0) *(volatile int *)(p.hdr + HDR_FLAG) = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == PRODUCER_WARP && lane == 0) {
+        prefetch_tmap(&p.tmA);
+        prefetch_tmap(&p.tmB);
+        prefetch_tmap(&p.tmC);
+    }
+    if (warp == MMA_WARP) {
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(&tmem_slot)),
+                         "r"(TMEM_COLS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(&tmem_slot)),
+                         "r"(TMEM_COLS)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();   // the peer's barriers exist from here on
+    tc_fence_after();
+    const uint32_t tmem_base = tmem_slot;
+
+    Abort ab;
+    ab.flag_smem = &abort_flag;
+    ab.hdr = p.hdr;
+    ab.limit_ns = p.timeout_ns;
+
+    if (warp == PRODUCER_WARP) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int issued = 0;
+            bool ok = true;
+            const uint32_t bytes = static_cast<uint32_t>(p.a_box_rows * F8_BK + F8_OP_BYTES);
+            for (int t = cid; ok && t < p.tiles; t += ncl) {
+                int mt, nt;
+                f8_tile(p, t, &mt, &nt);
+                const int ya = mt * (CL * 128) + static_cast<int>(crank) * 128;
+                const int yb = nt * BNT + static_cast<int>(crank) * 128;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(&empty_bar[stage], phase ^ 1, ab)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *sA = smem + stage * F8_STAGE;
+                    uint8_t *sB = sA + F8_OP_BYTES;
+                    uint64_t *fb = &full_bar[stage];
+                    if constexpr (PAIR) {
+                        // both CTAs' bytes complete on the leader's barrier
+                        if (leader) mbar_arrive_expect_tx(fb, 2 * bytes);
+                        const uint32_t lfb = map_to_rank(fb, 0);
+                        tma_load_2d_pair(sA, &p.tmA, lfb, kb * F8_BK, ya);
+                        tma_load_2d_pair(sB, &p.tmB, lfb, kb * F8_BK, yb);
+                    } else {
+                        mbar_arrive_expect_tx(fb, bytes);
+                        tma_load_2d(sA, &p.tmA, fb, kb * F8_BK, ya);
+                        tma_load_2d(sB, &p.tmB, fb, kb * F8_BK, yb);
+                    }
+                    ++issued;
+                    if (++stage == F8_STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) {
+                // drain: wait (bounded) for the copies still in flight into each stage
+                const int n = issued < F8_STAGES ? issued : F8_STAGES;
+                for (int i = 0; i < n; ++i) {
+                    if (--stage < 0) {
+                        stage = F8_STAGES - 1;
+                        phase ^= 1;
+                    }
+                    if (leader) mbar_wait_drain(&full_bar[stage], phase, 50000000ull);
+                }
+                if (!leader) {
+                    const uint64_t t0 = global_timer_ns();
+                    while (global_timer_ns() - t0 < 50000000ull) {}
+                }
+            }
+        }
+    } else if (warp == MMA_WARP) {
+        if (lane == 0 && leader) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int buf = 0;
+            uint32_t bphase = 0;
+            bool ok = true, any_mma = false;
+            constexpr uint32_t idesc = idesc_e4m3(CL * 128, BNT);
+            constexpr uint16_t both = static_cast<uint16_t>((1u << CL) - 1u);
+            for (int t = cid; ok && t < p.tiles; t += ncl) {
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!mbar_wait_cluster(&tempty_bar[buf], bphase ^ 1, ab) ||
+                        !mbar_wait(&full_bar[stage], phase, ab)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sA = smem_u32(smem + stage * F8_STAGE);
+                    const uint64_t ad = sdesc(sA, 16u, 1024u);
+                    const uint64_t bd = sdesc(sA + F8_OP_BYTES, 16u, 1024u);
+                    const uint32_t d = tmem_base + buf * BNT;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)   // 32 values (bytes) of k per MMA
+                        umma_e4m3<PAIR>(d, ad + static_cast<uint64_t>(k * 2), bd + static_cast<uint64_t>(k * 2),
+                                        idesc, k != 0 ? 1u : 0u);
+                    any_mma = true;
+                    if constexpr (PAIR) {
+                        umma_commit_pair(&empty_bar[stage], both);
+                        umma_commit_pair(&tfull_bar[buf], both);
+                    } else {
+                        umma_commit(&empty_bar[stage]);
+                        umma_commit(&tfull_bar[buf]);
+                    }
+                    if (++stage == F8_STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                    if (++buf == NBUF) {
+                        buf = 0;
+                        bphase ^= 1;
+                    }
+                }
+            }
+            if (any_mma) {
+                // every MMA (and every arrival it sends to the peer) has completed
+                // before TMEM is freed and the CTAs leave
+                if constexpr (PAIR) umma_commit_pair(&drain_bar, both);
+                else umma_commit(&drain_bar);
+                mbar_wait_drain(&drain_bar, 0, 50000000ull);
+            }
+        }
+    } else {
+        const int quarter = warp & 3, half = warp >> 2;
+        uint8_t *box = smem + F8_STAGES * F8_STAGE + warp * F8_WARP_BOX;
+        // B_ROWS: the scales of the half's columns for two k blocks, in the output box of its
+        // first warp (free between a tile's stores and the next one's)
+        float *sb_smem = reinterpret_cast<float *>(smem + F8_STAGES * F8_STAGE + half * 4 * F8_WARP_BOX);
+        int buf = 0;
+        uint32_t bphase = 0;
+        int par = 0;
+        bool ok = true;
+        for (int t = cid; ok && t < p.tiles; t += ncl) {
+            int mt, nt;
+            f8_tile(p, t, &mt, &nt);
+            const int row0 = mt * (CL * 128) + static_cast<int>(crank) * 128 + quarter * 32;
+            const int col0 = nt * BNT + half * COLS;
+            const bool active = row0 < p.M && col0 < p.N;   // warp-uniform: some output of this warp exists
+            const int row = row0 + lane;
+            const float *sa = p.sa + static_cast<long long>(row < p.M ? row : 0) * p.KB;
+            // tile scales: the warp's columns lie in one block of 128
+            const float *sb = B_ROWS ? p.sb : p.sb + static_cast<long long>(col0 < p.N ? col0 / 128 : 0) * p.KB;
+            float a_next = sa[kb0], b_next = 0.f;
+            const int sb_col = col0 + (threadIdx.x & 127);   // the column whose scales this thread fetches
+            const bool fetch = B_ROWS && (threadIdx.x & 127) < COLS && sb_col < p.N;
+            if constexpr (B_ROWS) {
+                if (lane == 0) bulk_wait_read0();
+                named_bar_sync(1 + half, 128);
+                if (fetch) b_next = p.sb[static_cast<long long>(sb_col) * p.KB + kb0];
+            } else {
+                b_next = sb[kb0];
+            }
+            float2 acc[COLS / 2];
+#pragma unroll
+            for (int j = 0; j < COLS / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                float s = a_next;
+                if constexpr (B_ROWS) {
+                    // (the other parity's scales may still be in use by a slower warp of the half)
+                    if ((threadIdx.x & 127) < COLS) sb_smem[par * COLS + (threadIdx.x & 127)] = b_next;
+                } else {
+                    s *= b_next;
+                }
+                if (kb + 1 < kb1) {
+                    a_next = sa[kb + 1];
+                    if constexpr (B_ROWS) {
+                        if (fetch) b_next = p.sb[static_cast<long long>(sb_col) * p.KB + kb + 1];
+                    } else {
+                        b_next = sb[kb + 1];
+                    }
+                }
+                ok = mbar_wait_cluster(&tfull_bar[buf], bphase, ab);
+                if constexpr (B_ROWS) ok = named_bar_and(1 + half, 128, ok);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                if (active) {
+                    tc_fence_after();
+                    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                           static_cast<uint32_t>(buf * BNT + half * COLS);
+                    const float2 s2 = make_float2(s, s);
+#pragma unroll
+                    for (int c = 0; c < COLS / 32; ++c) {
+                        float v[32];
+                        tmem_ld32(taddr + c * 32, v);
+                        if constexpr (B_ROWS) {
+                            const float4 *b4 = reinterpret_cast<const float4 *>(sb_smem + par * COLS + c * 32);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float4 b = b4[j];
+                                float2 &x = acc[c * 16 + 2 * j], &y = acc[c * 16 + 2 * j + 1];
+                                x = __ffma2_rn(make_float2(v[4 * j], v[4 * j + 1]),
+                                               __fmul2_rn(s2, make_float2(b.x, b.y)), x);
+                                y = __ffma2_rn(make_float2(v[4 * j + 2], v[4 * j + 3]),
+                                               __fmul2_rn(s2, make_float2(b.z, b.w)), y);
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                acc[c * 16 + j] =
+                                    __ffma2_rn(make_float2(v[2 * j], v[2 * j + 1]), s2, acc[c * 16 + j]);
+                        }
+                    }
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR && !leader) mbar_arrive_cluster(map_to_rank(&tempty_bar[buf], 0));
+                    else mbar_arrive(&tempty_bar[buf]);
+                }
+                if (++buf == NBUF) {
+                    buf = 0;
+                    bphase ^= 1;
+                }
+                par ^= 1;
+            }
+            if (!ok) break;
+            if constexpr (B_ROWS) named_bar_sync(1 + half, 128);   // the scales have been read
+            if (!PAIR && csize > 1) {
+                // one tile per cluster: the stages are free (all copies landed, all MMAs done); the
+                // partial sums as 128 x 128 fp32, 16-byte chunk j of row r at j ^ (r % 8)
+                const int r = quarter * 32 + lane;
+                float *dst = reinterpret_cast<float *>(smem) + r * 128;
+#pragma unroll
+                for (int j = 0; j < COLS / 4; ++j)
+                    *reinterpret_cast<float4 *>(dst + (((half * (COLS / 4) + j) ^ (r & 7)) << 2)) =
+                        make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y);
+                break;
+            }
+            if (active) {
+                // 128-byte wide boxes of 32 rows: 64 columns of 16 bits, or 32 of fp32
+                const int per = p.c_type == CE_FP32 ? 32 : 64;
+#pragma unroll
+                for (int c = 0; c < COLS / 32; ++c) {
+                    // a bulk store writes whole 16-byte pieces of a row: what N leaves in its last
+                    // piece is stored value by value
+                    const int tail0 = p.n_bulk - (col0 + c * 32), tail1 = p.N - (col0 + c * 32);
+                    if (tail0 < 32 && tail1 > 0 && tail0 < tail1 && row < p.M) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            if (j < tail0 || j >= tail1) continue;
+                            const float a = (j & 1) ? acc[c * 16 + j / 2].y : acc[c * 16 + j / 2].x;
+                            const long long o = row * p.ldc + col0 + c * 32 + j;
+                            if (p.c_type == CE_FP32) static_cast<float *>(p.C)[o] = a;
+                            else if (p.c_type == CE_FP16) static_cast<__half *>(p.C)[o] = __float2half_rn(a);
+                            else static_cast<__nv_bfloat16 *>(p.C)[o] = __float2bfloat16_rn(a);
+                        }
+                    }
+                    if (col0 + c * 32 / per * per >= p.n_bulk) continue;
+                    const bool first = c * 32 % per == 0, last = (c * 32 + 32) % per == 0;
+                    if (first) {
+                        if (lane == 0) bulk_wait_read0();
+                        __syncwarp();
+                    }
+                    if (p.c_type == CE_FP32) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<float4 *>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                                make_float4(acc[c * 16 + 2 * j].x, acc[c * 16 + 2 * j].y,
+                                            acc[c * 16 + 2 * j + 1].x, acc[c * 16 + 2 * j + 1].y);
+                    } else {
+                        const int jb = (c & 1) * 4;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const float2 a = acc[c * 16 + 4 * j + q];
+                                w[q] = p.c_type == CE_FP16 ? pack_f16x2(a.x, a.y) : pack_bf16x2(a.x, a.y);
+                            }
+                            *reinterpret_cast<uint4 *>(box + lane * 128 + (((jb + j) ^ (lane & 7)) << 4)) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                    if (last) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&p.tmC, box, col0 + c * 32 / per * per, row0);
+                            bulk_commit();
+                        }
+                    }
+                }
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    // no CTA of a pair leaves while the other may still write to it; partial sums are in place
+    if (csize > 1) cluster_sync_all();
+    if (!PAIR && csize > 1) {
+        // rows of this CTA: 128 / csize; a warp adds up one row at a time, 4 columns per lane
+        int mt, nt;
+        f8_tile(p, cid, &mt, &nt);
+        const int rows = 128 / static_cast<int>(csize);
+        const int col = nt * BNT + lane * 4;
+        for (int k = warp; k < rows && warp < NUM_EPI_WARPS; k += NUM_EPI_WARPS) {
+            const int r = static_cast<int>(rank) * rows + k;
+            const long long row = static_cast<long long>(mt) * 128 + r;
+            if (row >= p.M || col >= p.N) continue;
+            const float *src = reinterpret_cast<const float *>(smem) + r * 128 + ((lane ^ (r & 7)) << 2);
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (uint32_t q = 0; q < csize; ++q) {
+                const float4 v = ld_cluster_f4(map_to_rank(src, q));
+                a.x += v.x;
+                a.y += v.y;
+                a.z += v.z;
+                a.w += v.w;
+            }
+            const float f[4] = {a.x, a.y, a.z, a.w};
+            const int n = p.N - col;
+            if (p.c_type == CE_FP32) {
+                float *o = static_cast<float *>(p.C) + row * p.ldc + col;
+                if (n >= 4) *reinterpret_cast<float4 *>(o) = a;
+                else
+                    for (int j = 0; j < n; ++j) o[j] = f[j];
+            } else {
+                uint16_t *o = static_cast<uint16_t *>(p.C) + row * p.ldc + col;
+                uint2 u;
+                u.x = p.c_type == CE_FP16 ? pack_f16x2(a.x, a.y) : pack_bf16x2(a.x, a.y);
+                u.y = p.c_type == CE_FP16 ? pack_f16x2(a.z, a.w) : pack_bf16x2(a.z, a.w);
+                if (n >= 4) *reinterpret_cast<uint2 *>(o) = u;
+                else
+                    for (int j = 0; j < n; ++j)
+                        o[j] = static_cast<uint16_t>((j < 2 ? u.x : u.y) >> (16 * (j & 1)));
+            }
+        }
+        cluster_sync_all();   // no CTA leaves while a peer may still read its partial sums
+    }
+    if (warp == MMA_WARP) {
+        tc_fence_after();
+        if constexpr (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                         "r"(TMEM_COLS)
+                         : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                         "r"(TMEM_COLS)
+                         : "memory");
+    }
+}
+
+using Fp8Kernel = void (*)(const Fp8GemmParams);
+Fp8Kernel fp8_kernel(bool pair, bool b_rows) {
+    if (pair) return b_rows ? lce_fp8_matmul_kernel<true, true> : lce_fp8_matmul_kernel<true, false>;
+    return b_rows ? lce_fp8_matmul_kernel<false, true> : lce_fp8_matmul_kernel<false, false>;
+}
+
+}  // namespace
+
+cudaError_t fp8_set_attributes() {
+    for (int k = 0; k < 4; ++k) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            fp8_kernel(k & 1, k & 2), cudaFuncAttributeMaxDynamicSharedMemorySize, F8_SMEM);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_fp8_matmul(const Fp8GemmParams &p, bool pair, bool b_rows, int cluster, int clusters,
+                              cudaStream_t s) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster * clusters));
+    cfg.blockDim = dim3(GEMM_THREADS);
+    cfg.dynamicSmemBytes = F8_SMEM;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fp8_kernel(pair, b_rows), p);
+}
+
+}  // namespace lce

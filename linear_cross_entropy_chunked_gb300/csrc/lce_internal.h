@@ -293,6 +293,34 @@ struct ClipScale {
     float *norm_out;
 };
 
+// 8-bit linear layers (lce_fp8.cu).
+struct Fp8QuantParams {
+    const void *X;             // [R][ld]
+    long long ld, R, C;
+    long long rblocks, cblocks;   // blocks of 128
+    int vec;                   // rows are 16-byte aligned
+    uint8_t *q;                // [R][ldq] or null
+    long long ldq;
+    float *scale;              // [R][cblocks] (rows) or [rblocks][cblocks] (tiles)
+    uint8_t *qt;               // X^T: [C][ldqt] or null
+    long long ldqt;
+    float *scale_t;            // [C][rblocks] or [cblocks][rblocks]
+};
+struct Fp8GemmParams {
+    CUtensorMap tmA, tmB, tmC;
+    int M, N, KB;              // KB: k blocks of 128
+    int n_bulk;                // columns that tmC stores: N less what does not fill 16 bytes
+    int m_tiles, n_tiles, tiles;
+    int a_box_rows;            // rows of A's load box
+    const float *sa;           // [M][KB]
+    const float *sb;           // [N][KB] or [N / 128][KB]
+    void *C;
+    long long ldc;
+    int c_type;                // CE_BF16, CE_FP32 or CE_FP16
+    int *hdr;
+    unsigned long long timeout_ns;
+};
+
 // launchers (return cudaError_t of the launch)
 // cluster = 1: one CTA per 128 x 256 tile; 2: a CTA pair per 256 x 256 tile
 // (tcgen05 cta_group::2, each CTA loading its own A rows and half of B).
@@ -331,6 +359,13 @@ long long clip_chunks(const void *p, long long n, int dtype);
 cudaError_t launch_grad_norm(const ClipItem *items, int n, int kind, double *part, int sms, int *parts,
                              cudaStream_t s);
 cudaError_t launch_grad_scale(const ClipItem *items, int n, const ClipScale &c, int sms, cudaStream_t s);
+
+cudaError_t fp8_set_attributes();
+cudaError_t launch_fp8_quantize(const Fp8QuantParams &p, int dtype, bool tile, cudaStream_t s);
+// pair: CTA pairs on 256 x 256 tiles (cluster = 2); otherwise 128 x 128 tiles, each split
+// along k over `cluster` CTAs (cluster > 1: one tile per cluster)
+cudaError_t launch_fp8_matmul(const Fp8GemmParams &p, bool pair, bool b_rows, int cluster, int clusters,
+                              cudaStream_t s);
 
 constexpr float LOG2E_F = 1.4426950408889634f;
 

@@ -1,0 +1,233 @@
+"""Linear layers in 8-bit floating point (e4m3, one fp32 scale per block of 128 values along
+the contraction): lce_fp8_quantize and lce_fp8_matmul. Argument marshalling only.
+
+An operand is a pair (q, scale): q [R, C] float8_e4m3fn with a row stride that is a
+multiple of 16, scale fp32 [R, ceil(C / 128)] (row blocks: activations, gradients) or
+[ceil(R / 128), ceil(C / 128)] (tiles: weights)."""
+from __future__ import annotations
+
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import _binding as _b
+
+BLOCK = 128
+_WS_BYTES = 1024
+
+
+class FP8Weight(NamedTuple):
+    """A linear layer's weight [V, D] in tiles of 128 x 128, and (for the gradient of the
+    layer's input) its transpose in the same form."""
+    q: torch.Tensor                          # [V, D] float8_e4m3fn
+    scale: torch.Tensor                      # [ceil(V / 128), ceil(D / 128)] fp32
+    q_t: Optional[torch.Tensor] = None       # [D, V]
+    scale_t: Optional[torch.Tensor] = None   # [ceil(D / 128), ceil(V / 128)]
+
+
+def _blocks(n):
+    return -(-n // BLOCK)
+
+
+def _pad16(n):
+    return -(-n // 16) * 16
+
+
+def _check_dense_rows(name, t, dtypes, what):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {what}")
+    if t.dim() != 2 or t.shape[1] == 0 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if ld < t.shape[1]:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return ld
+
+
+def _operand(R, C, tiles, dev):
+    """(q [R, C] with padded rows, scale) for an operand of that shape."""
+    ld = _pad16(C)
+    q = torch.empty(R * ld, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn).view(R, ld)[:, :C]
+    return q, torch.empty(_blocks(R) if tiles else R, _blocks(C), dtype=torch.float32, device=dev), ld
+
+
+def _quantize(X, tiles, own, transposed, s):
+    """((q, scale) or None, the same of X^T or None) on the current device and stream."""
+    ld = X.stride(0) if X.shape[0] > 1 else X.shape[1]
+    R, C = X.shape
+    q = scale = qt = scale_t = None
+    ldq = ldqt = 0
+    if own:
+        q, scale, ldq = _operand(R, C, tiles, X.device)
+    if transposed:
+        qt, scale_t, ldqt = _operand(C, R, tiles, X.device)
+    if R == 0:
+        return (q, scale), (qt, scale_t)
+    _b._check(_b.lib().lce_fp8_quantize(X.data_ptr(), _b._CE_DTYPES[X.dtype], ld, R, C, 1 if tiles else 0,
+                                        _b._ptr(q), ldq, _b._ptr(scale), _b._ptr(qt), ldqt,
+                                        _b._ptr(scale_t), s), "lce_fp8_quantize")
+    return (q, scale), (qt, scale_t)
+
+
+def quantize_fp8(X, tiles: bool = False, transpose: bool = False, stream=None):
+    """(q, scale) of X [R, C] (bf16, fp16 or fp32, unit column stride, any row stride), or
+    of X^T with transpose=True, in row blocks of 128 values or (tiles=True) in tiles of
+    128 x 128. The scale is the smallest power of two under which the block's largest
+    finite value is at most 448, so only e4m3's rounding (to nearest, ties to even) loses
+    anything; infinities and NaN become NaN."""
+    _check_dense_rows("X", X, _b._CE_DTYPES, "bfloat16, float16 or float32")
+    if transpose and X.shape[0] == 0:
+        raise ValueError("X has no rows to contract over")
+    with _b._on(X.device, stream) as s:
+        own, t = _quantize(X, tiles, not transpose, transpose, s)
+    return t if transpose else own
+
+
+def fp8_weight(W, transpose: bool = True, stream=None) -> FP8Weight:
+    """The weight W [V, D] (bf16, fp16 or fp32) in tiles; with transpose also its
+    transpose, which the gradient of the layer's input needs."""
+    _check_dense_rows("W", W, _b._CE_DTYPES, "bfloat16, float16 or float32")
+    if W.shape[0] == 0:
+        raise ValueError("W has no rows")
+    with _b._on(W.device, stream) as s:
+        own, t = _quantize(W, True, True, transpose, s)
+    return FP8Weight(*own, *t)
+
+
+def _check_operand(name, q, scale, rows_only):
+    """Row stride, and whether the scales are per row."""
+    ld = _check_dense_rows(name, q, (torch.float8_e4m3fn,), "float8_e4m3fn")
+    if q.shape[0] > 1 and ld % 16:
+        raise ValueError(f"{name}'s row stride must be a multiple of 16 (pad its rows)")
+    if q.data_ptr() % 16:
+        raise ValueError(f"{name} must start on a 16-byte boundary")
+    R, KB = q.shape[0], _blocks(q.shape[1])
+    if scale.dtype != torch.float32 or scale.device != q.device or not scale.is_contiguous():
+        raise ValueError(f"{name}'s scale must be a contiguous float32 tensor on its device")
+    rows = scale.shape == (R, KB)
+    if not rows and (rows_only or scale.shape != (_blocks(R), KB)):
+        raise ValueError(f"{name}'s scale must be [{R}, {KB}] (rows)" +
+                         ("" if rows_only else f" or [{_blocks(R)}, {KB}] (tiles)") +
+                         f", not {list(scale.shape)}")
+    return _pad16(ld) if R <= 1 else ld, rows
+
+
+def _matmul(a, a_scale, lda, b, b_scale, ldb, b_rows, out, ws, s):
+    M, K = a.shape
+    N = b.shape[0]
+    ldc = out.stride(0) if M > 1 else -(-N // 8) * 8
+    if ws is None:
+        ws = torch.empty(_WS_BYTES, dtype=torch.uint8, device=a.device)
+    _b._check(_b.lib().lce_fp8_matmul(a.data_ptr(), lda, a_scale.data_ptr(), b.data_ptr(), ldb,
+                                      b_scale.data_ptr(), 1 if b_rows else 0, M, N, K, out.data_ptr(), ldc,
+                                      _b._CE_DTYPES[out.dtype], ws.data_ptr(), ws.numel(), s),
+              "lce_fp8_matmul")
+    return out
+
+
+def _empty_out(M, N, dtype, dev):
+    """[M, N]; the row stride is rounded up so that every row starts on 16 bytes."""
+    per = 16 // dtype.itemsize
+    return torch.empty_strided((M, N), (-(-N // per) * per, 1), dtype=dtype, device=dev)
+
+
+def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, ws=None, stream=None):
+    """a @ b.T in e4m3: a [M, K] with scales per row and block of 128 [M, ceil(K / 128)],
+    b [N, K] with scales per row and block or per tile [ceil(N / 128), ceil(K / 128)]; any
+    fp32 scales, fp32 sums, rounded once to out_dtype (bf16, fp16 or fp32). The result's
+    row stride is N rounded up to 16 bytes. out: where to write it (row stride a multiple of
+    16 bytes). ws: a uint8 tensor of 1024 bytes whose device status read_status returns."""
+    lda, _ = _check_operand("a", a, a_scale, True)
+    ldb, b_rows = _check_operand("b", b, b_scale, False)
+    if a.shape[1] != b.shape[1] or a.device != b.device:
+        raise ValueError(f"a{tuple(a.shape)} and b{tuple(b.shape)} must share their columns and device")
+    if out is not None:
+        ldc = _check_dense_rows("out", out, _b._CE_DTYPES, "bfloat16, float16 or float32") \
+            if out.numel() else out.stride(0)
+        if out.shape != (a.shape[0], b.shape[0]) or out.device != a.device:
+            raise ValueError("out must be [M, N] on the operands' device")
+        if out.data_ptr() % 16 or (out.shape[0] > 1 and ldc * out.element_size() % 16):
+            raise ValueError("out's rows must start on 16-byte boundaries")
+    elif out_dtype not in _b._CE_DTYPES:
+        raise TypeError("out_dtype must be bfloat16, float16 or float32")
+    if ws is not None and (ws.device != a.device or ws.dtype != torch.uint8 or not ws.is_contiguous()
+                           or ws.numel() < _WS_BYTES or ws.data_ptr() % 16):
+        raise ValueError(f"ws must be a contiguous, 16-byte aligned uint8 tensor of {_WS_BYTES} bytes")
+    with _b._on(a.device, stream) as s:
+        if out is None:
+            out = _empty_out(a.shape[0], b.shape[0], out_dtype, a.device)
+        return _matmul(a, a_scale, lda, b, b_scale, ldb, b_rows, out, ws, s)
+
+
+class FP8LinearFunction(torch.autograd.Function):
+    """Z = X W^T with X in row blocks and W in tiles of e4m3; rounding is passed through:
+    dX = dZ W (dZ in row blocks, W^T in tiles) and, for a trained W, dW = dZ^T X (both in
+    blocks along the rows of X)."""
+
+    @staticmethod
+    def forward(ctx, X, W, q, scale, q_t, scale_t):
+        need_dX, need_dW = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
+        with _b._on(X.device, None) as s:
+            if W is not None:
+                (q, scale), (q_t, scale_t) = _quantize(W, True, True, need_dX, s)
+            (xq, xs), (xt, xts) = _quantize(X, False, True, need_dW, s)
+            Z = _empty_out(X.shape[0], q.shape[0], X.dtype, X.device)
+            ldw = q.stride(0) if q.shape[0] > 1 else _pad16(q.shape[1])
+            _matmul(xq, xs, _pad16(X.shape[1]), q, scale, ldw, False, Z, None, s)
+        ctx.save_for_backward(q_t if need_dX else None, scale_t if need_dX else None, xt, xts)
+        ctx.x_dtype, ctx.w_dtype = X.dtype, None if W is None else W.dtype
+        return Z
+
+    @staticmethod
+    def backward(ctx, dZ):
+        wt, wts, xt, xts = ctx.saved_tensors
+        need_dX, need_dW = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
+        if not (need_dX or need_dW):
+            return None, None, None, None, None, None
+        if dZ.stride(1) != 1 or (dZ.shape[0] > 1 and dZ.stride(0) < dZ.shape[1]):
+            dZ = dZ.contiguous()
+        M, V = dZ.shape
+        dX = dW = None
+        with _b._on(dZ.device, None) as s:
+            (zq, zs), (zt, zts) = _quantize(dZ, False, need_dX, need_dW, s)
+            if need_dX:
+                dX = _empty_out(M, wt.shape[0], ctx.x_dtype, dZ.device)
+                ldw = wt.stride(0) if wt.shape[0] > 1 else _pad16(V)
+                _matmul(zq, zs, _pad16(V), wt, wts, ldw, False, dX, None, s)
+            if need_dW:
+                if M == 0:
+                    dW = torch.zeros(V, xt.shape[0], dtype=ctx.w_dtype, device=dZ.device)
+                else:
+                    dW = _empty_out(V, xt.shape[0], ctx.w_dtype, dZ.device)
+                    _matmul(zt, zts, _pad16(M), xt, xts, _pad16(M), True, dW, None, s)
+        return dX, dW, None, None, None, None
+
+
+def fp8_linear(X, W):
+    """X W^T computed in e4m3 with blocks of 128, in X's dtype: logits [M, V] for the hidden
+    states X [M, D] (bf16, fp16 or fp32). W: a weight [V, D] (bf16, fp16 or fp32), quantised in
+    the call and differentiable, or an FP8Weight, which is frozen (its transpose is needed
+    where X requires a gradient). Differentiable in X and W; the gradients are
+    products in e4m3 too. The logits' row stride is V rounded up to 16 bytes."""
+    _check_dense_rows("X", X, _b._CE_DTYPES, "bfloat16, float16 or float32")
+    if isinstance(W, FP8Weight):
+        D = X.shape[1]
+        if W.q.shape[-1] != D or W.q.device != X.device:
+            raise ValueError(f"X{tuple(X.shape)} and W{tuple(W.q.shape)} must share their columns and device")
+        _check_operand("W", W.q, W.scale, False)
+        if tuple(W.scale.shape) != (_blocks(W.q.shape[0]), _blocks(D)):
+            raise ValueError("the scales of W must be per tile of 128 x 128")
+        if X.requires_grad and torch.is_grad_enabled():
+            if W.q_t is None or W.scale_t is None:
+                raise ValueError("the gradient of X needs W's transpose (fp8_weight(W, transpose=True))")
+            _check_operand("W's transpose", W.q_t, W.scale_t, False)
+            if W.q_t.shape != (D, W.q.shape[0]) or W.q_t.device != X.device or \
+                    tuple(W.scale_t.shape) != (_blocks(D), _blocks(W.q.shape[0])):
+                raise ValueError("W's transpose must be [D, V] in tiles of 128 x 128")
+        return FP8LinearFunction.apply(X, None, W.q, W.scale, W.q_t, W.scale_t)
+    _check_dense_rows("W", W, _b._CE_DTYPES, "bfloat16, float16 or float32, or an FP8Weight")
+    if X.shape[1] != W.shape[1] or X.device != W.device or W.shape[0] == 0:
+        raise ValueError(f"X{tuple(X.shape)} and W{tuple(W.shape)} must share their columns and device")
+    return FP8LinearFunction.apply(X, W, None, None, None, None)

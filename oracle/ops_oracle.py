@@ -1,5 +1,5 @@
-"""fp64 CPU oracle of the operators around the LM head: token sampling and gradient
-clipping. Numpy only, written from the formulas of include/lce.h."""
+"""fp64 CPU oracle of the operators around the LM head: token sampling, gradient clipping
+and 8-bit quantisation. Numpy only, written from the formulas of include/lce.h."""
 from __future__ import annotations
 
 import numpy as np
@@ -66,3 +66,40 @@ def clip(grads, max_norm, norm_type=2.0, eps=1e-6):
     norm = grad_norm(grads, norm_type)
     f = min(1.0, max_norm / (norm + eps))
     return norm, [np.asarray(g, np.float64) * f for g in grads]
+
+
+def e4m3(y):
+    """The nearest e4m3 value (ties to even) of each |y| <= 448: 3 bits behind the leading
+    one, exponents -6 to 8, steps of 2^-9 below. NaN and infinities: NaN."""
+    y = np.asarray(y, np.float64)
+    ok = np.isfinite(y)
+    a = np.where(ok, np.abs(y), 0.0)
+    _, e = np.frexp(a)                                  # a = f 2^e, f in [0.5, 1)
+    step = np.ldexp(1.0, np.maximum(e - 1, -6) - 3)
+    r = np.round(a / step) * step                       # numpy rounds ties to even
+    return np.where(ok, np.copysign(r, y), np.nan)
+
+
+def quantize_fp8(X, tiles=False):
+    """(values q, scale) of X [R, C] fp64 in row blocks of 128 or tiles of 128 x 128."""
+    X = np.asarray(X, np.float64)
+    R, C = X.shape
+    rows = 128 if tiles else 1
+    RB, CB = -(-R // rows), -(-C // 128)
+    P = np.zeros((RB * rows, CB * 128))
+    P[:R, :C] = X
+    T = P.reshape(RB, rows, CB, 128)
+    amax = np.where(np.isfinite(T), np.abs(T), 0.0).max(axis=(1, 3))
+    f, e = np.frexp(amax)                               # 448 = 0.875 * 2^9
+    e = np.maximum(e - 9 + (f > 0.875), -126)
+    scale = np.where(amax > 0, np.ldexp(1.0, e), 1.0)
+    q = e4m3(T / scale[:, None, :, None])
+    return q.reshape(P.shape)[:R, :C], scale
+
+
+def dequantize_fp8(q, scale):
+    """Values of an operand: scale [R, CB] or [ceil(R / 128), CB]."""
+    q = np.asarray(q, np.float64)
+    R, C = q.shape
+    s = np.repeat(np.asarray(scale, np.float64), 128, axis=1)[:, :C]
+    return q * (s if s.shape[0] == R else np.repeat(s, 128, axis=0)[:R])
