@@ -219,16 +219,20 @@ cudaError_t launch_fp8_quantize(const Fp8QuantParams &p, int dtype, bool tile, c
 // a block's partial product is complete, the consumer warps read it from TMEM and add
 // sa * sb times it, while the MMAs of the next blocks fill the other buffers.
 //
-// Roles (320 threads): warps 0-7 consumers (TMEM lane quarter = warp % 4, column half
-// = warp / 4), warp 8 TMA producer, warp 9 TMEM owner + MMA issuer. A static persistent
-// schedule: unit u of cluster c is tile c + u * clusters.
+// Roles (384 threads): warps 0-7 consumers (TMEM lane quarter = warp % 4, column half
+// = warp / 4), warp 8 TMA producer, warp 9 TMEM owner + MMA issuer, warps 10 and 11 idle
+// (registers move between whole warpgroups). A static persistent schedule: unit u of
+// cluster c is tile c + u * clusters.
 //
 // PAIR: a CTA pair per 256 x 256 tile (cta_group::2; each CTA its own 128 rows of A
 // and half of B's), for products with many tiles. Otherwise 128 x 128 tiles, one CTA
 // each; few tiles are split along k over a cluster of up to 8 CTAs, whose fp32 sums are
 // added through distributed shared memory in rank order.
 // B_ROWS: B's scales are per row (gradient of a weight), read through shared memory.
-// Every mbarrier wait is bounded, as in the bf16 GEMM.
+// Every mbarrier wait is bounded, as in the bf16 GEMM. The waits for TMEM buffers acquire at
+// CTA scope and their remote arrivals are relaxed: no memory is handed over with them (the
+// tcgen05 fences order TMEM), and cluster scope costs a flush or an L1 invalidation per
+// k block.
 
 namespace {
 
@@ -238,6 +242,12 @@ constexpr int F8_STAGE = 2 * F8_OP_BYTES;  // A and B of one k block, per CTA
 constexpr int F8_STAGES = 6;
 constexpr int F8_WARP_BOX = 4096;          // 32 rows x 128 bytes of output per consumer warp
 constexpr int F8_SMEM = F8_STAGES * F8_STAGE + 8 * F8_WARP_BOX + 1024;
+constexpr int F8_THREADS = 384;
+// Pairs: a consumer thread holds 128 sums and two TMEM loads of 16 values. 384 threads start
+// with 168 registers each; the consumers take 216, the other warpgroup keeps 72:
+// 256 * 216 + 128 * 72 = 384 * 168.
+constexpr int F8_REGS = 168, F8_REGS_CONSUMER = 216, F8_REGS_OTHER = 72;
+static_assert(256 * F8_REGS_CONSUMER + 128 * F8_REGS_OTHER <= F8_THREADS * F8_REGS, "register split");
 constexpr int F8_GROUP = 16;               // row tiles that run together (they share B in L2)
 
 // Instruction descriptor of tcgen05.mma kind::f8f6f4, e4m3 x e4m3 -> fp32, both K-major.
@@ -288,7 +298,7 @@ __device__ __forceinline__ void f8_tile(const Fp8GemmParams &p, int t, int *mt, 
 }
 
 template <bool PAIR, bool B_ROWS>
-__global__ void __launch_bounds__(GEMM_THREADS, 1)
+__global__ void __launch_bounds__(F8_THREADS, 1)
     lce_fp8_matmul_kernel(const __grid_constant__ Fp8GemmParams p) {
     constexpr int CL = PAIR ? 2 : 1;
     constexpr int BNT = PAIR ? 256 : 128;
@@ -362,8 +372,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     ab.hdr = p.hdr;
     ab.limit_ns = p.timeout_ns;
 
-    if (warp == PRODUCER_WARP) {
-        if (lane == 0) {
+    if (warp >= NUM_EPI_WARPS) {
+        if constexpr (PAIR) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F8_REGS_OTHER));
+        if (warp == PRODUCER_WARP && lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
             int issued = 0;
@@ -415,9 +426,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     while (global_timer_ns() - t0 < 50000000ull) {}
                 }
             }
-        }
-    } else if (warp == MMA_WARP) {
-        if (lane == 0 && leader) {
+        } else if (warp == MMA_WARP && leader) {
+            // the whole warp goes along (its loop counters stay in uniform registers, which the
+            // MMAs take their operands from); one lane issues
             int stage = 0;
             uint32_t phase = 0;
             int buf = 0;
@@ -427,28 +438,29 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             constexpr uint16_t both = static_cast<uint16_t>((1u << CL) - 1u);
             for (int t = cid; ok && t < p.tiles; t += ncl) {
                 for (int kb = 0; kb < nk; ++kb) {
-                    if (!mbar_wait_cluster(&tempty_bar[buf], bphase ^ 1, ab) ||
-                        !mbar_wait(&full_bar[stage], phase, ab)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = mbar_wait(&full_bar[stage], phase, ab) && mbar_wait(&tempty_bar[buf], bphase ^ 1, ab);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t sA = smem_u32(smem + stage * F8_STAGE);
                     const uint64_t ad = sdesc(sA, 16u, 1024u);
                     const uint64_t bd = sdesc(sA + F8_OP_BYTES, 16u, 1024u);
                     const uint32_t d = tmem_base + buf * BNT;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)   // 32 values (bytes) of k per MMA
-                        umma_e4m3<PAIR>(d, ad + static_cast<uint64_t>(k * 2), bd + static_cast<uint64_t>(k * 2),
-                                        idesc, k != 0 ? 1u : 0u);
-                    any_mma = true;
-                    if constexpr (PAIR) {
-                        umma_commit_pair(&empty_bar[stage], both);
-                        umma_commit_pair(&tfull_bar[buf], both);
-                    } else {
-                        umma_commit(&empty_bar[stage]);
-                        umma_commit(&tfull_bar[buf]);
+                        for (int k = 0; k < 4; ++k)   // 32 values (bytes) of k per MMA
+                            umma_e4m3<PAIR>(d, ad + static_cast<uint64_t>(k * 2),
+                                            bd + static_cast<uint64_t>(k * 2), idesc, k != 0 ? 1u : 0u);
+                        if constexpr (PAIR) {
+                            umma_commit_pair(&tfull_bar[buf], both);
+                            umma_commit_pair(&empty_bar[stage], both);
+                        } else {
+                            umma_commit(&tfull_bar[buf]);
+                            umma_commit(&empty_bar[stage]);
+                        }
                     }
+                    __syncwarp();
+                    any_mma = true;
                     if (++stage == F8_STAGES) {
                         stage = 0;
                         phase ^= 1;
@@ -462,12 +474,16 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             if (any_mma) {
                 // every MMA (and every arrival it sends to the peer) has completed
                 // before TMEM is freed and the CTAs leave
-                if constexpr (PAIR) umma_commit_pair(&drain_bar, both);
-                else umma_commit(&drain_bar);
+                if (elect_one()) {
+                    if constexpr (PAIR) umma_commit_pair(&drain_bar, both);
+                    else umma_commit(&drain_bar);
+                }
+                __syncwarp();
                 mbar_wait_drain(&drain_bar, 0, 50000000ull);
             }
         }
     } else {
+        if constexpr (PAIR) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F8_REGS_CONSUMER));
         const int quarter = warp & 3, half = warp >> 2;
         uint8_t *box = smem + F8_STAGES * F8_STAGE + warp * F8_WARP_BOX;
         // B_ROWS: the scales of the half's columns for two k blocks, in the output box of its
@@ -486,37 +502,38 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             const int row = row0 + lane;
             const float *sa = p.sa + static_cast<long long>(row < p.M ? row : 0) * p.KB;
             // tile scales: the warp's columns lie in one block of 128
-            const float *sb = B_ROWS ? p.sb : p.sb + static_cast<long long>(col0 < p.N ? col0 / 128 : 0) * p.KB;
-            float a_next = sa[kb0], b_next = 0.f;
+            const float *sb = p.sb + static_cast<long long>(col0 < p.N ? col0 / 128 : 0) * p.KB;
             const int sb_col = col0 + (threadIdx.x & 127);   // the column whose scales this thread fetches
             const bool fetch = B_ROWS && (threadIdx.x & 127) < COLS && sb_col < p.N;
             if constexpr (B_ROWS) {
                 if (lane == 0) bulk_wait_read0();
                 named_bar_sync(1 + half, 128);
-                if (fetch) b_next = p.sb[static_cast<long long>(sb_col) * p.KB + kb0];
-            } else {
-                b_next = sb[kb0];
+                sb = p.sb + static_cast<long long>(fetch ? sb_col : 0) * p.KB;
+            }
+            // scales of the next two k blocks
+            float a0 = sa[kb0], b0 = sb[kb0], a1 = 0.f, b1 = 0.f;
+            if (kb0 + 1 < kb1) {
+                a1 = sa[kb0 + 1];
+                b1 = sb[kb0 + 1];
             }
             float2 acc[COLS / 2];
 #pragma unroll
             for (int j = 0; j < COLS / 2; ++j) acc[j] = make_float2(0.f, 0.f);
             for (int kb = kb0; kb < kb1; ++kb) {
-                float s = a_next;
+                float s = a0;
                 if constexpr (B_ROWS) {
-                    // (the other parity's scales may still be in use by a slower warp of the half)
-                    if ((threadIdx.x & 127) < COLS) sb_smem[par * COLS + (threadIdx.x & 127)] = b_next;
+                    // (the other half of sb_smem may still be in use by a slower warp)
+                    if ((threadIdx.x & 127) < COLS) sb_smem[par * COLS + (threadIdx.x & 127)] = b0;
                 } else {
-                    s *= b_next;
+                    s *= b0;
                 }
-                if (kb + 1 < kb1) {
-                    a_next = sa[kb + 1];
-                    if constexpr (B_ROWS) {
-                        if (fetch) b_next = p.sb[static_cast<long long>(sb_col) * p.KB + kb + 1];
-                    } else {
-                        b_next = sb[kb + 1];
-                    }
+                a0 = a1;
+                b0 = b1;
+                if (kb + 2 < kb1) {
+                    a1 = sa[kb + 2];
+                    b1 = sb[kb + 2];
                 }
-                ok = mbar_wait_cluster(&tfull_bar[buf], bphase, ab);
+                ok = mbar_wait(&tfull_bar[buf], bphase, ab);
                 if constexpr (B_ROWS) ok = named_bar_and(1 + half, 128, ok);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
@@ -527,34 +544,39 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                            static_cast<uint32_t>(buf * BNT + half * COLS);
                     const float2 s2 = make_float2(s, s);
+                    uint32_t v[2][16];   // the load of 16 columns runs beside the arithmetic on the last 16
+                    tmem_ld16_start(taddr, v[0]);
+                    tmem_ld16_wait(v[0]);
 #pragma unroll
-                    for (int c = 0; c < COLS / 32; ++c) {
-                        float v[32];
-                        tmem_ld32(taddr + c * 32, v);
+                    for (int c = 0; c < COLS / 16; ++c) {
+                        if (c + 1 < COLS / 16) tmem_ld16_start(taddr + (c + 1) * 16, v[(c + 1) & 1]);
+                        const uint32_t(&u)[16] = v[c & 1];
                         if constexpr (B_ROWS) {
-                            const float4 *b4 = reinterpret_cast<const float4 *>(sb_smem + par * COLS + c * 32);
+                            const float4 *b4 = reinterpret_cast<const float4 *>(sb_smem + par * COLS + c * 16);
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
+                            for (int j = 0; j < 4; ++j) {
                                 const float4 b = b4[j];
-                                float2 &x = acc[c * 16 + 2 * j], &y = acc[c * 16 + 2 * j + 1];
-                                x = __ffma2_rn(make_float2(v[4 * j], v[4 * j + 1]),
+                                float2 &x = acc[c * 8 + 2 * j], &y = acc[c * 8 + 2 * j + 1];
+                                x = __ffma2_rn(make_float2(__uint_as_float(u[4 * j]), __uint_as_float(u[4 * j + 1])),
                                                __fmul2_rn(s2, make_float2(b.x, b.y)), x);
-                                y = __ffma2_rn(make_float2(v[4 * j + 2], v[4 * j + 3]),
-                                               __fmul2_rn(s2, make_float2(b.z, b.w)), y);
+                                y = __ffma2_rn(
+                                    make_float2(__uint_as_float(u[4 * j + 2]), __uint_as_float(u[4 * j + 3])),
+                                    __fmul2_rn(s2, make_float2(b.z, b.w)), y);
                             }
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                acc[c * 16 + j] =
-                                    __ffma2_rn(make_float2(v[2 * j], v[2 * j + 1]), s2, acc[c * 16 + j]);
+                            for (int j = 0; j < 8; ++j)
+                                acc[c * 8 + j] = __ffma2_rn(
+                                    make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1])), s2,
+                                    acc[c * 8 + j]);
                         }
+                        if (c + 1 < COLS / 16) tmem_ld16_wait(v[(c + 1) & 1]);
                     }
                     tc_fence_before();
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    if (PAIR && !leader) mbar_arrive_cluster(map_to_rank(&tempty_bar[buf], 0));
-                    else mbar_arrive(&tempty_bar[buf]);
+                    mbar_arrive_cluster_relaxed(map_to_rank(&tempty_bar[buf], PAIR ? 0u : rank));
                 }
                 if (++buf == NBUF) {
                     buf = 0;
@@ -701,7 +723,15 @@ Fp8Kernel fp8_kernel(bool pair, bool b_rows) {
 
 cudaError_t fp8_set_attributes() {
     for (int k = 0; k < 4; ++k) {
-        const cudaError_t e = cudaFuncSetAttribute(
+        cudaError_t e;
+        if (k & 1) {
+            // the register split waits forever for registers that the launch does not have
+            cudaFuncAttributes fa{};
+            e = cudaFuncGetAttributes(&fa, fp8_kernel(true, k & 2));
+            if (e != cudaSuccess) return e;
+            if (fa.numRegs < F8_REGS) return cudaErrorInvalidKernelImage;
+        }
+        e = cudaFuncSetAttribute(
             fp8_kernel(k & 1, k & 2), cudaFuncAttributeMaxDynamicSharedMemorySize, F8_SMEM);
         if (e != cudaSuccess) return e;
     }
@@ -717,7 +747,7 @@ cudaError_t launch_fp8_matmul(const Fp8GemmParams &p, bool pair, bool b_rows, in
     at[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(cluster * clusters));
-    cfg.blockDim = dim3(GEMM_THREADS);
+    cfg.blockDim = dim3(F8_THREADS);
     cfg.dynamicSmemBytes = F8_SMEM;
     cfg.stream = s;
     cfg.attrs = at;
