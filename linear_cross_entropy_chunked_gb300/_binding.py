@@ -8,7 +8,6 @@ fallback: without the built library every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -199,16 +198,27 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-@contextlib.contextmanager
-def _on(dev, stream):
+class _on:
     """The device of the tensors and the caller's stream as the current ones (outputs
     and workspaces allocated inside belong to that stream); gives the stream's handle."""
-    with contextlib.ExitStack() as stack:
-        if dev.index is not None and dev.index != torch.cuda.current_device():
-            stack.enter_context(torch.cuda.device(dev))
-        if stream is not None:
-            stack.enter_context(torch.cuda.stream(stream))
-        yield torch.cuda.current_stream().cuda_stream
+    __slots__ = ("_dev", "_stream", "_entered")
+
+    def __init__(self, dev, stream):
+        self._dev, self._stream, self._entered = dev, stream, ()
+
+    def __enter__(self):
+        if self._dev.index is not None and self._dev.index != torch.cuda.current_device():
+            self._entered += (torch.cuda.device(self._dev),)
+            self._entered[-1].__enter__()
+        if self._stream is not None:
+            self._entered += (torch.cuda.stream(self._stream),)
+            self._entered[-1].__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self._entered):
+            c.__exit__(*exc)
+        return False
 
 
 def _check(st: int, what: str):

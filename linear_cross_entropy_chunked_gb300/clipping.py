@@ -4,11 +4,13 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 
 import torch
 
 from . import _binding as _b
 
+_dtype = operator.attrgetter("dtype")
 NORM_KINDS = {2.0: 0, math.inf: 1, 1.0: 2}
 
 
@@ -25,20 +27,26 @@ def _dense(t) -> bool:
 
 
 def _tensors(grads, what):
+    """(list of the tensors, device, whether all are contiguous, and their addresses, sizes
+    and dtype codes). Lists of hundreds are usual: one pass in C per property."""
     grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
     if not grads:
         raise ValueError(f"{what} is empty")
-    dev = grads[0].device
-    for g in grads:
-        if not g.is_cuda:
+    T = torch.Tensor
+    devices = set(map(T.get_device, grads))   # -1: not on a GPU
+    if len(devices) > 1 or -1 in devices:
+        if -1 in devices:
             raise ValueError(f"{what} must be CUDA tensors (there is no CPU path)")
-        if g.dtype not in _b._CE_DTYPES:
+        raise ValueError(f"{what} must be on one device")
+    dtypes = list(map(_dtype, grads))
+    for dt in set(dtypes):
+        if dt not in _b._CE_DTYPES:
             raise TypeError(f"{what} must be bfloat16, float16 or float32")
-        if g.device != dev:
-            raise ValueError(f"{what} must be on one device")
-        if not _dense(g):
-            raise ValueError(f"{what} must fill their memory (contiguous or permuted, no gaps)")
-    return grads, dev
+    plain = all(map(T.is_contiguous, grads))
+    if not plain and not all(map(_dense, grads)):
+        raise ValueError(f"{what} must fill their memory (contiguous or permuted, no gaps)")
+    return (grads, grads[0].device, plain, list(map(T.data_ptr, grads)), list(map(T.numel, grads)),
+            list(map(_b._CE_DTYPES.__getitem__, dtypes)))
 
 
 def _kind(norm_type):
@@ -48,11 +56,9 @@ def _kind(norm_type):
     return kind
 
 
-def _arrays(grads):
-    n = len(grads)
-    return ((ctypes.c_void_p * n)(*[g.data_ptr() for g in grads]),
-            (ctypes.c_int64 * n)(*[g.numel() for g in grads]),
-            (ctypes.c_int32 * n)(*[_b._CE_DTYPES[g.dtype] for g in grads]), n)
+def _arrays(ptrs, sizes, dtypes):
+    n = len(ptrs)
+    return (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*sizes), (ctypes.c_int32 * n)(*dtypes), n
 
 
 def _workspace(n, ws, dev):
@@ -69,8 +75,8 @@ def grad_norm(grads, norm_type=2.0, ws=None, stream=None):
     """The norm (1, 2 or inf) over all values of the gradients, a tensor or a list of
     tensors (bf16, fp16 and fp32 may be mixed): a device fp32 scalar."""
     kind = _kind(norm_type)
-    grads, dev = _tensors(grads, "grads")
-    src, sizes, dtypes, n = _arrays(grads)
+    _, dev, _, *lists = _tensors(grads, "grads")
+    src, sizes, dtypes, n = _arrays(*lists)
     with _b._on(dev, stream) as s:
         ws, ws_bytes = _workspace(n, ws, dev)
         norm = torch.empty((), dtype=torch.float32, device=dev)
@@ -82,7 +88,7 @@ def grad_norm(grads, norm_type=2.0, ws=None, stream=None):
 def clip_grad_norm(grads, max_norm, norm_type=2.0, eps=1e-6, out=None, ws=None, stream=None):
     """Scales the gradients (a tensor or a list, bf16, fp16 and fp32 may be mixed) by
     min(1, max_norm / (norm + eps)), in place or into the tensors `out` of the same
-    dtypes and layouts, and returns their norm (1, 2 or inf over all values; a device fp32
+    dtypes, sizes and layouts, and returns their norm (1, 2 or inf over all values; a device fp32
     scalar; the host does not wait). The factor is formed on the device: gradients
     whose norm is below max_norm stay as they are and are not written in place. A norm
     that is NaN (infinite) makes the factor NaN (0)."""
@@ -90,16 +96,15 @@ def clip_grad_norm(grads, max_norm, norm_type=2.0, eps=1e-6, out=None, ws=None, 
     max_norm, eps = float(max_norm), float(eps)
     if not max_norm >= 0.0 or not 0.0 <= eps < math.inf:
         raise ValueError("max_norm must not be negative, and eps finite and not negative")
-    grads, dev = _tensors(grads, "grads")
-    src, sizes, dtypes, n = _arrays(grads)
+    grads, dev, plain, ptrs, counts, codes = _tensors(grads, "grads")
+    src, sizes, dtypes, n = _arrays(ptrs, counts, codes)
     dst = None
     if out is not None:
-        out, out_dev = _tensors(out, "out")
-        if len(out) != n or out_dev != dev or any(
-                o.dtype != g.dtype or o.shape != g.shape or o.stride() != g.stride()
-                for o, g in zip(out, grads)):
-            raise ValueError("out must match the gradients in number, device, dtypes, shapes and strides")
-        dst = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
+        out, out_dev, out_plain, out_ptrs, out_counts, out_codes = _tensors(out, "out")
+        if out_dev != dev or out_counts != counts or out_codes != codes or not (plain and out_plain or all(
+                o.shape == g.shape and o.stride() == g.stride() for o, g in zip(out, grads))):
+            raise ValueError("out must match the gradients in number, device, dtypes, sizes and layouts")
+        dst = (ctypes.c_void_p * n)(*out_ptrs)
     with _b._on(dev, stream) as s:
         ws, ws_bytes = _workspace(n, ws, dev)
         norm = torch.empty((), dtype=torch.float32, device=dev)

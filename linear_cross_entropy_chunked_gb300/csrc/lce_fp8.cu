@@ -438,14 +438,14 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             constexpr uint16_t both = static_cast<uint16_t>((1u << CL) - 1u);
             for (int t = cid; ok && t < p.tiles; t += ncl) {
                 for (int kb = 0; kb < nk; ++kb) {
-                    ok = mbar_wait(&full_bar[stage], phase, ab) && mbar_wait(&tempty_bar[buf], bphase ^ 1, ab);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    tc_fence_after();
                     const uint32_t sA = smem_u32(smem + stage * F8_STAGE);
                     const uint64_t ad = sdesc(sA, 16u, 1024u);
                     const uint64_t bd = sdesc(sA + F8_OP_BYTES, 16u, 1024u);
                     const uint32_t d = tmem_base + buf * BNT;
+                    ok = mbar_wait(&full_bar[stage], phase, ab) && mbar_wait(&tempty_bar[buf], bphase ^ 1, ab);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)   // 32 values (bytes) of k per MMA
@@ -489,6 +489,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         // B_ROWS: the scales of the half's columns for two k blocks, in the output box of its
         // first warp (free between a tile's stores and the next one's)
         float *sb_smem = reinterpret_cast<float *>(smem + F8_STAGES * F8_STAGE + half * 4 * F8_WARP_BOX);
+        const uint32_t tempty_addr = map_to_rank(&tempty_bar[0], PAIR ? 0u : rank);
         int buf = 0;
         uint32_t bphase = 0;
         int par = 0;
@@ -539,6 +540,11 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                     ok = false;
                     break;
                 }
+                auto release = [&]() {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(tempty_addr + buf * 8);
+                };
                 if (active) {
                     tc_fence_after();
                     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
@@ -549,7 +555,11 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                     tmem_ld16_wait(v[0]);
 #pragma unroll
                     for (int c = 0; c < COLS / 16; ++c) {
-                        if (c + 1 < COLS / 16) tmem_ld16_start(taddr + (c + 1) * 16, v[(c + 1) & 1]);
+                        if (c + 1 < COLS / 16) {
+                            tmem_ld16_start(taddr + (c + 1) * 16, v[(c + 1) & 1]);
+                        } else {
+                            release();   // everything is in registers
+                        }
                         const uint32_t(&u)[16] = v[c & 1];
                         if constexpr (B_ROWS) {
                             const float4 *b4 = reinterpret_cast<const float4 *>(sb_smem + par * COLS + c * 16);
@@ -572,11 +582,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                         }
                         if (c + 1 < COLS / 16) tmem_ld16_wait(v[(c + 1) & 1]);
                     }
-                    tc_fence_before();
-                }
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive_cluster_relaxed(map_to_rank(&tempty_bar[buf], PAIR ? 0u : rank));
+                } else {
+                    release();
                 }
                 if (++buf == NBUF) {
                     buf = 0;

@@ -49,25 +49,26 @@ def _check_dense_rows(name, t, dtypes, what):
 def _operand(R, C, tiles, dev):
     """(q [R, C] with padded rows, scale) for an operand of that shape."""
     ld = _pad16(C)
-    q = torch.empty(R * ld, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn).view(R, ld)[:, :C]
-    return q, torch.empty(_blocks(R) if tiles else R, _blocks(C), dtype=torch.float32, device=dev), ld
+    q = torch.empty((R, ld), dtype=torch.float8_e4m3fn, device=dev)
+    return (q if ld == C else q[:, :C],
+            torch.empty((_blocks(R) if tiles else R, _blocks(C)), dtype=torch.float32, device=dev))
 
 
 def _quantize(X, tiles, own, transposed, s):
     """((q, scale) or None, the same of X^T or None) on the current device and stream."""
-    ld = X.stride(0) if X.shape[0] > 1 else X.shape[1]
     R, C = X.shape
+    ld = X.stride(0) if R > 1 else C
     q = scale = qt = scale_t = None
-    ldq = ldqt = 0
     if own:
-        q, scale, ldq = _operand(R, C, tiles, X.device)
+        q, scale = _operand(R, C, tiles, X.device)
     if transposed:
-        qt, scale_t, ldqt = _operand(C, R, tiles, X.device)
-    if R == 0:
-        return (q, scale), (qt, scale_t)
-    _b._check(_b.lib().lce_fp8_quantize(X.data_ptr(), _b._CE_DTYPES[X.dtype], ld, R, C, 1 if tiles else 0,
-                                        _b._ptr(q), ldq, _b._ptr(scale), _b._ptr(qt), ldqt,
-                                        _b._ptr(scale_t), s), "lce_fp8_quantize")
+        qt, scale_t = _operand(C, R, tiles, X.device)
+    if R:
+        _b._check(_b.lib().lce_fp8_quantize(
+            X.data_ptr(), _b._CE_DTYPES[X.dtype], ld, R, C, tiles,
+            q.data_ptr() if own else None, _pad16(C), scale.data_ptr() if own else None,
+            qt.data_ptr() if transposed else None, _pad16(R), scale_t.data_ptr() if transposed else None,
+            s), "lce_fp8_quantize")
     return (q, scale), (qt, scale_t)
 
 
@@ -161,6 +162,14 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, ws=No
         return _matmul(a, a_scale, lda, b, b_scale, ldb, b_rows, out, ws, s)
 
 
+def _logits(X, q, scale, need_xt, s):
+    """(Z, X^T in row blocks or None): the forward product on the current device and stream."""
+    (xq, xs), xt = _quantize(X, False, True, need_xt, s)
+    Z = _empty_out(X.shape[0], q.shape[0], X.dtype, X.device)
+    ldw = q.stride(0) if q.shape[0] > 1 else _pad16(q.shape[1])
+    return _matmul(xq, xs, _pad16(X.shape[1]), q, scale, ldw, False, Z, None, s), xt
+
+
 class FP8LinearFunction(torch.autograd.Function):
     """Z = X W^T with X in row blocks and W in tiles of e4m3; rounding is passed through:
     dX = dZ W (dZ in row blocks, W^T in tiles) and, for a trained W, dW = dZ^T X (both in
@@ -172,10 +181,7 @@ class FP8LinearFunction(torch.autograd.Function):
         with _b._on(X.device, None) as s:
             if W is not None:
                 (q, scale), (q_t, scale_t) = _quantize(W, True, True, need_dX, s)
-            (xq, xs), (xt, xts) = _quantize(X, False, True, need_dW, s)
-            Z = _empty_out(X.shape[0], q.shape[0], X.dtype, X.device)
-            ldw = q.stride(0) if q.shape[0] > 1 else _pad16(q.shape[1])
-            _matmul(xq, xs, _pad16(X.shape[1]), q, scale, ldw, False, Z, None, s)
+            Z, (xt, xts) = _logits(X, q, scale, need_dW, s)
         ctx.save_for_backward(q_t if need_dX else None, scale_t if need_dX else None, xt, xts)
         ctx.x_dtype, ctx.w_dtype = X.dtype, None if W is None else W.dtype
         return Z
@@ -212,22 +218,25 @@ def fp8_linear(X, W):
     where X requires a gradient). Differentiable in X and W; the gradients are
     products in e4m3 too. The logits' row stride is V rounded up to 16 bytes."""
     _check_dense_rows("X", X, _b._CE_DTYPES, "bfloat16, float16 or float32")
+    D = X.shape[1]
     if isinstance(W, FP8Weight):
-        D = X.shape[1]
-        if W.q.shape[-1] != D or W.q.device != X.device:
-            raise ValueError(f"X{tuple(X.shape)} and W{tuple(W.q.shape)} must share their columns and device")
-        _check_operand("W", W.q, W.scale, False)
-        if tuple(W.scale.shape) != (_blocks(W.q.shape[0]), _blocks(D)):
+        q, scale = W.q, W.scale
+        _check_operand("W", q, scale, False)
+        V = q.shape[0]
+        if q.shape[1] != D or q.device != X.device:
+            raise ValueError(f"X{tuple(X.shape)} and W{tuple(q.shape)} must share their columns and device")
+        if scale.shape != (_blocks(V), _blocks(D)):
             raise ValueError("the scales of W must be per tile of 128 x 128")
-        if X.requires_grad and torch.is_grad_enabled():
-            if W.q_t is None or W.scale_t is None:
-                raise ValueError("the gradient of X needs W's transpose (fp8_weight(W, transpose=True))")
-            _check_operand("W's transpose", W.q_t, W.scale_t, False)
-            if W.q_t.shape != (D, W.q.shape[0]) or W.q_t.device != X.device or \
-                    tuple(W.scale_t.shape) != (_blocks(D), _blocks(W.q.shape[0])):
-                raise ValueError("W's transpose must be [D, V] in tiles of 128 x 128")
-        return FP8LinearFunction.apply(X, None, W.q, W.scale, W.q_t, W.scale_t)
+        if not (X.requires_grad and torch.is_grad_enabled()):
+            with _b._on(X.device, None) as s:
+                return _logits(X.detach(), q, scale, False, s)[0]
+        if W.q_t is None or W.scale_t is None:
+            raise ValueError("the gradient of X needs W's transpose (fp8_weight(W, transpose=True))")
+        _check_operand("W's transpose", W.q_t, W.scale_t, False)
+        if W.q_t.shape != (D, V) or W.q_t.device != X.device or W.scale_t.shape != (_blocks(D), _blocks(V)):
+            raise ValueError("W's transpose must be [D, V] in tiles of 128 x 128")
+        return FP8LinearFunction.apply(X, None, q, scale, W.q_t, W.scale_t)
     _check_dense_rows("W", W, _b._CE_DTYPES, "bfloat16, float16 or float32, or an FP8Weight")
-    if X.shape[1] != W.shape[1] or X.device != W.device or W.shape[0] == 0:
+    if D != W.shape[1] or X.device != W.device or W.shape[0] == 0:
         raise ValueError(f"X{tuple(X.shape)} and W{tuple(W.shape)} must share their columns and device")
     return FP8LinearFunction.apply(X, W, None, None, None, None)
