@@ -1570,7 +1570,7 @@ lce_status lce_sample_logits(const void *Z, int z_dtype, int64_t ld, int64_t N, 
     p.min_p_all = min_p_all;
     p.tokens = reinterpret_cast<long long *>(tokens);
     p.logprobs = logprobs;
-    LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_sample(p, s));
+    LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_sample(p, sms, s));
     return LCE_OK;
 }
 

@@ -254,11 +254,11 @@ struct SampleParams {
     long long *tokens;        // [N]
     float *logprobs;          // [N] or null
 };
-// 2^(-j / 64) in units of 2^-50 and as fp32; ln(2) / 64 in three parts, and its inverse
+// 2^(-j / 64) in units of 2^-31; ln(2) / 64 in three parts (negative), its inverse, the
+// number that rounds to whole numbers, and the polynomial of exp
 struct SampleTables {
-    unsigned long long fix[64];
-    float flt[64];
-    float c1, c2, c3, inv;
+    unsigned fix[64];
+    float2 mc1, mc2, mc3, inv, magic, mmagic, p4, p3, p2, p1;
 };
 constexpr long long SMP_MAX_V = 1ll << 20;   // weights of 2^43 in 64-bit sums
 
@@ -353,7 +353,7 @@ cudaError_t launch_rmsnorm_bwd(const NormParams &p, cudaStream_t s);
 cudaError_t launch_dgamma_reduce(const float *part, int D, float *dgamma, cudaStream_t s);
 
 cudaError_t sample_set_attributes();
-cudaError_t launch_sample(const SampleParams &p, cudaStream_t s);
+cudaError_t launch_sample(const SampleParams &p, int sms, cudaStream_t s);
 long long clip_chunks(const void *p, long long n, int dtype);
 // *parts: partial sums written to `part`
 cudaError_t launch_grad_norm(const ClipItem *items, int n, int kind, double *part, int sms, int *parts,

@@ -14,7 +14,7 @@
 // sum, and a border of the cumulative distribution must lie where the formula
 // puts it. So weights are whole numbers, w_i in units of 2^-43 (64-bit sums
 // of up to 2^20 tokens are exact and the same in any order), and exp is computed
-// to a relative error of about 2^-32: the sum of border displacements over a row
+// to a relative error of about 2^-31: the sum of border displacements over a row
 // of 2^17 equally likely tokens is about 1e-8, which bounds the chance that u falls
 // on the wrong side of one. An fp32 softmax would put it at about 1e-2.
 //
@@ -34,20 +34,22 @@ constexpr int SMP_WARPS = SMP_THREADS / 32;
 constexpr int SMP_MAX_CLUSTER = 8;
 constexpr int SMP_BINS = 256;
 constexpr int SMP_ONE_SHIFT = 43;                    // weight of the largest logit: 2^43
-constexpr int SMP_TAB_SHIFT = 50;                    // the exponential's table is kept in units of 2^-50
 constexpr float SMP_X_END = 31.f;                    // exp(-31) < 2^-44 rounds to weight 0
-constexpr float SMP_BINS_PER_UNIT = 8.f;             // 31 * 8 = 248 bins of x
+// Windows of x in which a cut is searched: 0 .. 6, 6 .. 12, 12 .. 31.
+constexpr float SMP_X1 = 6.f, SMP_X2 = 12.f;
+// A short list of the largest logits, in which most cuts lie: per CTA, and in all.
+constexpr int SMP_LIST_CTA = 256, SMP_LIST = SMP_THREADS;
 constexpr int SMP_LIMB = 15;                         // bits per limb of a weight: 2^17 limbs fit 32 bits
 
-// Constants of the exponential, from their definitions on the host.
+constexpr float SMP_X_CLAMP = 31.18f;                // n = 2879, a shift by 63: weight 0
+
+// Constants of the exponential, from their definitions on the host. Pairs: packed
+// arithmetic takes them from the parameters as they are.
 SampleTables make_sample_tables() {
     SampleTables t;
     const double ln2 = std::log(2.0);
-    for (int j = 0; j < 64; ++j) {
-        const double v = std::exp2(-j / 64.0);
-        t.fix[j] = static_cast<unsigned long long>(std::nearbyint(std::ldexp(v, SMP_TAB_SHIFT)));
-        t.flt[j] = static_cast<float>(v);
-    }
+    for (int j = 0; j < 64; ++j)
+        t.fix[j] = static_cast<unsigned>(std::nearbyint(std::ldexp(std::exp2(-j / 64.0), 31)));
     // ln(2) / 64 in three parts: 12 bits (its product with a whole number below
     // 2^12 is exact), 24 bits, and the rest
     const double step = ln2 / 64.0;
@@ -55,10 +57,23 @@ SampleTables make_sample_tables() {
     std::frexp(step, &e);
     const double ulp = std::ldexp(1.0, e - 12);
     const double c1 = std::floor(step / ulp) * ulp;
-    t.c1 = static_cast<float>(c1);
-    t.c2 = static_cast<float>(step - c1);
-    t.c3 = static_cast<float>(step - c1 - static_cast<double>(t.c2));
-    t.inv = static_cast<float>(64.0 / ln2);
+    const float c2 = static_cast<float>(step - c1);
+    auto two = [](double v) { return make_float2(static_cast<float>(v), static_cast<float>(v)); };
+    t.mc1 = two(-c1);
+    t.mc2 = two(-c2);
+    t.mc3 = two(-(step - c1 - static_cast<double>(c2)));
+    t.inv = two(64.0 / ln2);
+    // 1.5 * 2^23 rounds what it is added to to a whole number n, kept in its low bits; 19 is
+    // added to the n / 64 there: the shift from units of 2^-62 to 2^-43
+    const float magic = 12582912.f + 19 * 64;
+    t.magic = two(magic);
+    t.mmagic = two(-magic);
+    // exp(-r) - 1 = r (-1 + r (1 / 2 + r (-1 / 6 + r / 24))) in units of 2^-31
+    const double S = 2147483648.0;
+    t.p4 = two(S / 24);
+    t.p3 = two(-S / 6);
+    t.p2 = two(S / 2);
+    t.p1 = two(-S);
     return t;
 }
 
@@ -150,45 +165,65 @@ template <typename T> __device__ __forceinline__ float smp_unkey(uint32_t key) {
 
 // ------------------------------------------------------------------ weights
 
-struct SmpTab {            // in shared memory
-    u64 fix[64];
-    float flt[64];
-};
+constexpr u64 SMP_ONE = 1ull << SMP_ONE_SHIFT;
+
 struct SmpRow {
     float m, ih, il;       // largest logit; 1 / temperature in two parts
-    float c1, c2, c3, inv;
+    bool only_max;         // +infinity among the logits, or no finite 1 / temperature:
+                           // the largest logits share the row
 };
 
 // x = (m - z) / temperature, rounded: the same monotone function wherever it is used.
 __device__ __forceinline__ float smp_x(float z, const SmpRow &r) {
-    return z == r.m ? 0.f : (r.m - z) * r.ih;
+    if (r.only_max) return z == r.m ? 0.f : INFINITY;
+    return (r.m - z) * r.ih;
 }
 
-// exp(-(m - z) / temperature) in units of 2^-43. x is carried in two floats (xh + xl);
-// x = n ln(2) / 64 + rr, exp(-x) = 2^-(n / 64) * (1 + q) with q = exp(-rr) - 1,
-// |rr| < 0.0055; the table's part is exact to 2^-51, T * q to 2^-32.
-__device__ __forceinline__ u64 smp_weight(float z, const SmpRow &r, const SmpTab &tab) {
-    if (z == r.m) return 1ull << SMP_ONE_SHIFT;
-    const float d = r.m - z;
-    const float xh = d * r.ih;
-    if (!(xh < SMP_X_END)) return 0ull;
-    const float bb = d - r.m;
-    const float dl = (r.m - (d - bb)) - (z + bb);      // d + dl = m - z exactly
-    float xl = fmaf(d, r.ih, -xh);
-    xl = fmaf(d, r.il, xl);
-    xl = fmaf(dl, r.ih, xl);
-    const float nf = rintf(xh * r.inv);
-    const int n = static_cast<int>(nf);
-    float rr = fmaf(-nf, r.c1, xh);                    // exact
-    xl = fmaf(-nf, r.c3, xl);
-    rr = fmaf(-nf, r.c2, rr) + xl;
-    const float q = rr * fmaf(rr, fmaf(rr, fmaf(rr, 1.f / 24.f, -1.f / 6.f), 0.5f), -1.f);
-    const int j = n & 63, e = n >> 6;
-    const int f = __float2int_rn(tab.flt[j] * q * 274877906944.f);   // T q in units of 2^-38
-    const long long w = static_cast<long long>(tab.fix[j]) +
-                        (static_cast<long long>(f) << (SMP_TAB_SHIFT - 38));
-    const int s = SMP_TAB_SHIFT - SMP_ONE_SHIFT + e;   // 7 .. 52
-    return (static_cast<u64>(w) + (1ull << (s - 1))) >> s;
+// exp(-(m - z) / temperature) in units of 2^-43 of two logits (in packed fp32 arithmetic, which
+// halves the instructions). x is carried in two floats (xh + xl, from m - z = d + dl exactly);
+// x = n ln(2) / 64 + rr, exp(-x) = 2^-(n / 64) * (1 + q) with q = exp(-rr) - 1, |rr| < 0.0055.
+// Table and 1 + q are whole numbers of 31 bits (2^-31), their product exact; the shift by
+// n / 64 rounds to nearest. The largest logit's weight is 2^43 exactly.
+__device__ __forceinline__ u64 smp_finish(float kf, float q31, const unsigned *tab) {
+    const unsigned n = static_cast<unsigned>(__float_as_int(kf));
+    const unsigned f = 0x80000000u + static_cast<unsigned>(__float2int_rn(q31));
+    const u64 y = (static_cast<u64>(tab[n & 63]) * f) >> ((n >> 6) & 63);
+    return (y + 1) & ~1ull;
+}
+__device__ __forceinline__ void smp_weight2(float z0, float z1, const SmpRow &r, const SampleTables &c,
+                                            const unsigned *tab, u64 &w0, u64 &w1) {
+    if (r.only_max) {
+        w0 = z0 == r.m ? SMP_ONE : 0ull;
+        w1 = z1 == r.m ? SMP_ONE : 0ull;
+        return;
+    }
+    auto two = [](float v) { return make_float2(v, v); };
+    const float2 z = make_float2(z0, z1), m = two(r.m), minus = two(-1.f), ih = two(r.ih);
+    const float2 d = __ffma2_rn(z, minus, m);
+    const float2 bb = __ffma2_rn(m, minus, d);
+    const float2 dl = __ffma2_rn(__fadd2_rn(z, bb), minus, __ffma2_rn(__ffma2_rn(bb, minus, d), minus, m));
+    const float2 x = __fmul2_rn(d, ih);
+    float2 xl = __ffma2_rn(d, ih, __fmul2_rn(x, minus));
+    xl = __ffma2_rn(d, two(r.il), xl);
+    xl = __ffma2_rn(dl, ih, xl);
+    // (beyond the end, and for a temperature of infinity, x is a number again: no NaN below)
+    const float2 xh = make_float2(fminf(x.x, SMP_X_CLAMP), fminf(x.y, SMP_X_CLAMP));
+    const float2 k = __ffma2_rn(xh, c.inv, c.magic);
+    const float2 nf = __fadd2_rn(k, c.mmagic);
+    xl = __ffma2_rn(nf, c.mc3, xl);
+    float2 rr = __ffma2_rn(nf, c.mc1, xh);              // exact
+    rr = __fadd2_rn(__ffma2_rn(nf, c.mc2, rr), xl);
+    float2 q = __ffma2_rn(rr, c.p4, c.p3);
+    q = __ffma2_rn(rr, q, c.p2);
+    q = __ffma2_rn(rr, q, c.p1);
+    q = __fmul2_rn(rr, q);
+    w0 = smp_finish(k.x, q.x, tab);
+    w1 = smp_finish(k.y, q.y, tab);
+}
+__device__ __forceinline__ u64 smp_weight(float z, const SmpRow &r, const SampleTables &c, const unsigned *tab) {
+    u64 a, b;
+    smp_weight2(z, z, r, c, tab, a, b);
+    return a;
 }
 
 // floor(f * s) and ceil(f * s) for 0 <= f < 1, exactly.
@@ -222,13 +257,24 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_
                  "r"(c), "r"(d)
                  : "memory");
 }
-__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr)
-                 : "memory");
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
+}
+__device__ __forceinline__ u64 ld_cluster_u64(uint32_t addr) {
+    u64 v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t smp_cluster_size() {
     uint32_t r;
@@ -245,20 +291,30 @@ __device__ __forceinline__ u64 warp_sum64(u64 v) {
     return v;
 }
 
+// What one CTA knows of its part of the row.
+struct alignas(16) SmpSums {
+    u64 w, w1, w2;         // weight of all, of x < SMP_X1, of x < SMP_X2
+    u64 wlist;             // ... of the logits on the list
+    uint32_t c, c1, c2;    // the same as counts
+    uint32_t list;         // logits on the list (more than SMP_LIST_CTA: it overflowed)
+};
 struct SmpShared {
-    uint4 hist[2][SMP_BINS];              // {count, three limbs of the weight}; read by the peers
-    uint4 slot[2][SMP_MAX_CLUSTER];       // one exchanged value per CTA
+    uint32_t hist[2][4][SMP_BINS];        // counts, three limbs of the weights; read by the peers
+    float wmax[SMP_MAX_CLUSTER * SMP_WARPS];   // largest logit of every warp of the cluster
+    SmpSums sums[2][SMP_MAX_CLUSTER];     // of every CTA of the cluster
     uint4 wslot[SMP_MAX_CLUSTER * SMP_WARPS];   // per warp of the cluster: sum above the cut, ties
+    u64 list[SMP_LIST_CTA];               // key and inverted index; rank 0 reads the peers'
+    u64 all[SMP_LIST], allw[SMP_LIST];    // rank 0: the whole list, and its weights
     u64 l0w[SMP_BINS], rw[SMP_BINS];      // weight before each bin: first level, refinement
     uint32_t l0c[SMP_BINS], rc[SMP_BINS]; // count before each bin
-    u64 wsum[SMP_BINS / 32];
-    uint32_t csum[SMP_BINS / 32];
-    u64 bw, bwin;                         // the bin found: weight before it, in it
-    uint32_t bc, bcin;
+    u64 wsum[SMP_WARPS];
+    uint32_t csum[SMP_WARPS];
+    u64 bw;                               // the bin found: weight and count before it
+    uint32_t bc;
     int bin;
-    float red[SMP_WARPS];
-    uint32_t redlo[SMP_WARPS], redhi[SMP_WARPS];
-    SmpTab tab;
+    SmpSums mine;
+    float t0;
+    unsigned tab[64];
 };
 
 // The warp's part of the row: `n` logits from index `first` on, in shared memory
@@ -283,39 +339,33 @@ template <typename T, bool SMEM> struct SmpChunk {
 
 // Adds to the histogram; `b` < 0: nothing. A warp whose lanes all hit one bin (equal
 // logits) adds once.
-template <bool WEIGHTS>
-__device__ __forceinline__ void smp_hist_add(uint4 *hist, int b, u64 w, int lane) {
+__device__ __forceinline__ void smp_hist_add(uint32_t (*hist)[SMP_BINS], int b, bool counts, bool weights, u64 w,
+                                             int lane) {
+    constexpr uint32_t M = (1u << SMP_LIMB) - 1u;
+    uint32_t n = 1, a0 = static_cast<uint32_t>(w) & M, a1 = static_cast<uint32_t>(w >> SMP_LIMB) & M,
+             a2 = static_cast<uint32_t>(w >> (2 * SMP_LIMB));
     const int b0 = __shfl_sync(0xffffffffu, b, 0);
     if (__all_sync(0xffffffffu, b == b0)) {
         if (b0 < 0) return;
-        if constexpr (WEIGHTS) {
-            constexpr uint32_t M = (1u << SMP_LIMB) - 1u;
-            const uint32_t s0 = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(w) & M);
-            const uint32_t s1 =
-                __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(w >> SMP_LIMB) & M);
-            const uint32_t s2 =
-                __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(w >> (2 * SMP_LIMB)));
-            if (lane == 0) {
-                atomicAdd(&hist[b0].y, s0);
-                atomicAdd(&hist[b0].z, s1);
-                atomicAdd(&hist[b0].w, s2);
-            }
+        n = 32;
+        if (weights) {
+            a0 = __reduce_add_sync(0xffffffffu, a0);
+            a1 = __reduce_add_sync(0xffffffffu, a1);
+            a2 = __reduce_add_sync(0xffffffffu, a2);
         }
-        if (lane == 0) atomicAdd(&hist[b0].x, 32u);
-        return;
+        if (lane != 0) return;
     }
     if (b < 0) return;
-    atomicAdd(&hist[b].x, 1u);
-    if constexpr (WEIGHTS) {
-        constexpr uint32_t M = (1u << SMP_LIMB) - 1u;
-        atomicAdd(&hist[b].y, static_cast<uint32_t>(w) & M);
-        atomicAdd(&hist[b].z, static_cast<uint32_t>(w >> SMP_LIMB) & M);
-        atomicAdd(&hist[b].w, static_cast<uint32_t>(w >> (2 * SMP_LIMB)));
+    if (counts) atomicAdd(&hist[0][b], n);
+    if (weights) {
+        atomicAdd(&hist[1][b], a0);
+        atomicAdd(&hist[2][b], a1);
+        if (a2) atomicAdd(&hist[3][b], a2);
     }
 }
 
 template <typename T, bool SMEM>
-__global__ void __launch_bounds__(SMP_THREADS)
+__global__ void __launch_bounds__(SMP_THREADS, 2)
     lce_sample_kernel(const SampleParams p, const __grid_constant__ SampleTables tabs, const int chunk) {
     extern __shared__ __align__(128) uint8_t smp_dyn[];
     __shared__ SmpShared sh;
@@ -330,10 +380,8 @@ __global__ void __launch_bounds__(SMP_THREADS)
     const float min_p = p.min_p ? p.min_p[r] : p.min_p_all;
     const bool greedy = !(temperature > 0.f);
 
-    if (t < 64) {
-        sh.tab.fix[t] = tabs.fix[t];
-        sh.tab.flt[t] = tabs.flt[t];
-    }
+    cluster_arrive();   // waited for before the first write to a peer: it has started
+    if (t < 64) sh.tab[t] = tabs.fix[t];
 
     // the warp's logits: into shared memory (cleaned), and the largest
     const long long first = (static_cast<long long>(rank) * SMP_WARPS + w) * chunk;
@@ -372,51 +420,50 @@ __global__ void __launch_bounds__(SMP_THREADS)
     }
     const int steps = (n + 255) / 256;   // sweeps of the warp over its logits
 
-    int xs = 0;       // exchange slot in use
-    // every CTA gives one value; afterwards sh.slot[xs ^ 1][k] holds that of rank k
-    auto exchange = [&](uint32_t a, uint32_t b) {
-        if (t < static_cast<int>(cl)) st_cluster_v4(map_to_rank(&sh.slot[xs][rank], t), a, b, 0u, 0u);
-        cluster_sync_all();
-        xs ^= 1;
-    };
-
+    // every warp gives its largest logit to every CTA
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (l == 0) sh.red[w] = m;
-    __syncthreads();
-    m = sh.red[l & (SMP_WARPS - 1)];
-#pragma unroll
-    for (int o = SMP_WARPS / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    // (the peers of the cluster have started: their shared memory may be written)
+    const int entries = static_cast<int>(cl) * SMP_WARPS, me = static_cast<int>(rank) * SMP_WARPS + w;
+    cluster_wait();
+    if (l < static_cast<int>(cl)) st_cluster_f32(map_to_rank(&sh.wmax[me], l), m);
     cluster_sync_all();
-    exchange(__float_as_uint(m), 0u);
-    for (uint32_t k = 0; k < cl; ++k) m = fmaxf(m, __uint_as_float(sh.slot[xs ^ 1][k].x));
-
-    if (m == -INFINITY || greedy) {
-        // nothing to draw from, or the lowest index of the largest logit
-        int best = 0x7fffffff;
-        if (m != -INFINITY) {
-            for (int s = 0; s < steps; ++s) {
-                float x[8];
-                ck.load(s * 256 + l * 8, x);
+    constexpr int PER_LANE = SMP_MAX_CLUSTER * SMP_WARPS / 32;
+    float wm[PER_LANE];   // entries 4 l .. 4 l + 3
+    m = -INFINITY;
 #pragma unroll
-                for (int j = 7; j >= 0; --j)
-                    if (x[j] == m && best > s * 256 + l * 8 + j) best = s * 256 + l * 8 + j;
-            }
-            best = __reduce_min_sync(0xffffffffu, best);
-            if (best != 0x7fffffff) best += static_cast<int>(first);
-            if (l == 0) sh.redlo[w] = static_cast<uint32_t>(best);
-            __syncthreads();
-            best = static_cast<int>(sh.redlo[l & (SMP_WARPS - 1)]);
-            best = __reduce_min_sync(0xffffffffu, best);
-            exchange(static_cast<uint32_t>(best), 0u);
-            for (uint32_t k = 0; k < cl; ++k) best = min(best, static_cast<int>(sh.slot[xs ^ 1][k].x));
-        }
+    for (int q = 0; q < PER_LANE; ++q) {
+        wm[q] = l * PER_LANE + q < entries ? sh.wmax[l * PER_LANE + q] : -INFINITY;
+        m = fmaxf(m, wm[q]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+
+    if (m == -INFINITY) {   // nothing to draw from
         if (rank == 0 && t == 0) {
-            p.tokens[r] = m == -INFINITY ? -1 : best;
-            if (p.logprobs) p.logprobs[r] = m == -INFINITY ? -INFINITY : 0.f;
+            p.tokens[r] = -1;
+            if (p.logprobs) p.logprobs[r] = -INFINITY;
         }
-        cluster_sync_all();   // no CTA leaves while a peer may still write into its slots
+        return;   // (nothing of a peer's is touched after the last exchange, here and below)
+    }
+    if (greedy) {   // the first warp that holds the largest logit finds its lowest index
+        int owner = 0x7fffffff;
+#pragma unroll
+        for (int q = PER_LANE - 1; q >= 0; --q)
+            if (wm[q] == m) owner = l * PER_LANE + q;
+        if (static_cast<int>(__reduce_min_sync(0xffffffffu, owner)) != me) return;
+        int best = 0x7fffffff;
+        for (int s = 0; s < steps && best == 0x7fffffff; ++s) {
+            float x[8];
+            ck.load(s * 256 + l * 8, x);
+#pragma unroll
+            for (int j = 7; j >= 0; --j)
+                if (x[j] == m) best = s * 256 + l * 8 + j;
+            best = __reduce_min_sync(0xffffffffu, best);
+        }
+        if (l == 0) {
+            p.tokens[r] = first + best;
+            if (p.logprobs) p.logprobs[r] = 0.f;
+        }
         return;
     }
 
@@ -425,34 +472,260 @@ __global__ void __launch_bounds__(SMP_THREADS)
     rw.ih = 1.f / temperature;
     rw.il = fmaf(-temperature, rw.ih, 1.f) * rw.ih;
     if (!(fabsf(rw.il) < INFINITY)) rw.il = 0.f;   // temperatures near the ends of the type's range
-    rw.c1 = tabs.c1;
-    rw.c2 = tabs.c2;
-    rw.c3 = tabs.c3;
-    rw.inv = tabs.inv;
+    rw.only_max = !(m < INFINITY) || !(rw.ih < INFINITY);
 
     const bool by_count = top_k > 0 && top_k < p.V;
     const bool by_weight = top_p < 1.f;
-    // the cut: all logits with a key above cut_key are kept, and the first cut_ties of
-    // those at it
+    u64 w_min = 0;         // kept: weight at least w_min, ...
+    if (min_p > 0.f) w_min = min_p >= 1.f ? SMP_ONE : smp_mul_floor(min_p, SMP_ONE, true);
+    // ... and the cut: all logits with a key above cut_key, and the first cut_ties of those at it
     bool have_cut = false;
     uint32_t cut_key = 0, cut_ties = 0;
 
+    // writes the answer: token, its logit, and all kept weight
+    auto answer = [&](long long token, float z, u64 total) {
+        p.tokens[r] = token;
+        if (p.logprobs) {
+            constexpr float UNIT = 1.f / static_cast<float>(SMP_ONE);
+            // log(total): the largest logit's weight is 1, so near 0 by log1p
+            const float ls = total < 2 * SMP_ONE ? log1pf(static_cast<float>(total - SMP_ONE) * UNIT)
+                                                 : logf(static_cast<float>(total) * UNIT);
+            p.logprobs[r] = -smp_x(z, rw) - ls;
+        }
+    };
+    // floor(u * total), u inside [0, 1): the token is the first whose cumulative weight exceeds it
+    auto draw_target = [&](u64 total) -> u64 {
+        const float u = p.u[r];
+        if (!(u < 1.f)) return total - 1;
+        return u > 0.f ? smp_mul_floor(u, total, false) : 0ull;
+    };
+    // the weight at which top-p ends, of `pool`
+    auto share = [&](u64 pool) -> u64 {
+        const u64 v = top_p > 0.f ? smp_mul_floor(top_p, pool, true) : 1ull;
+        return v ? v : 1ull;
+    };
+
     if (by_count || by_weight) {
+        // A threshold with at least `want` logits at or above it, and rarely many more: the
+        // want-th largest of the warps' maxima. Those logits go onto the list.
+        const int want = by_count ? top_k : entries / 2;
+        const bool use_list = want <= entries;
+        if (use_list) {
+#pragma unroll
+            for (int q = 0; q < SMP_MAX_CLUSTER; ++q) {
+                const int e = w * SMP_MAX_CLUSTER + q;   // every warp looks at its share of the entries
+                if (e >= entries) break;
+                const float v = sh.wmax[e];
+                int more = 0, same = 0;
+#pragma unroll
+                for (int i = 0; i < PER_LANE; ++i) {
+                    more += __popc(__ballot_sync(0xffffffffu, wm[i] > v));
+                    same += __popc(__ballot_sync(0xffffffffu, wm[i] == v && l * PER_LANE + i < entries));
+                }
+                if (l == 0 && more < want && want <= more + same) sh.t0 = v;   // (all who write, write the same)
+            }
+        }
+        if (t == 0) sh.mine = SmpSums{0, 0, 0, 0, 0, 0, 0, 0};
+        __syncthreads();
+        const float t0 = use_list ? fmaxf(sh.t0, -3.402823466e38f) : INFINITY;   // (masked ones stay out)
+
+        // one pass: sums over the row, and the list
+        int xs = 0;
+        auto sums_pass = [&](bool collect, bool counts, bool weights) {
+            u64 ws = 0, ws1 = 0, ws2 = 0, wl = 0;
+            uint32_t c = 0, c1 = 0, c2 = 0;
+            for (int s = 0; s < steps; ++s) {
+                float x[8];
+                ck.load(s * 256 + l * 8, x);
+                u64 v[8];
+                if (weights) {
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) smp_weight2(x[j], x[j + 1], rw, tabs, sh.tab, v[j], v[j + 1]);
+                }
+                if (counts || weights) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float xx = smp_x(x[j], rw);
+                        if (counts) {
+                            c += xx < SMP_X_END ? 1u : 0u;
+                            c1 += xx < SMP_X1 ? 1u : 0u;
+                            c2 += xx < SMP_X2 ? 1u : 0u;
+                        }
+                        if (weights) {
+                            ws += v[j];
+                            if (xx < SMP_X2) ws2 += v[j];
+                            if (xx < SMP_X1) ws1 += v[j];
+                        }
+                    }
+                }
+                if (collect) {
+                    bool any = false;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) any |= x[j] >= t0;
+                    if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            if (!(x[j] >= t0)) continue;
+                            const uint32_t at = atomicAdd(&sh.mine.list, 1u);
+                            const uint32_t index = static_cast<uint32_t>(first) + s * 256 + l * 8 + j;
+                            if (at < SMP_LIST_CTA) sh.list[at] = (static_cast<u64>(smp_key<T>(x[j])) << 32) | ~index;
+                            if (weights) wl += v[j];
+                        }
+                    }
+                }
+            }
+            if (weights) {
+                ws = warp_sum64(ws);
+                ws1 = warp_sum64(ws1);
+                ws2 = warp_sum64(ws2);
+                wl = warp_sum64(wl);
+                if (l == 0) {
+                    atomicAdd(&sh.mine.w, ws);
+                    atomicAdd(&sh.mine.w1, ws1);
+                    atomicAdd(&sh.mine.w2, ws2);
+                    atomicAdd(&sh.mine.wlist, wl);
+                }
+            }
+            if (counts) {
+                c = __reduce_add_sync(0xffffffffu, c);
+                c1 = __reduce_add_sync(0xffffffffu, c1);
+                c2 = __reduce_add_sync(0xffffffffu, c2);
+                if (l == 0) {
+                    atomicAdd(&sh.mine.c, c);
+                    atomicAdd(&sh.mine.c1, c1);
+                    atomicAdd(&sh.mine.c2, c2);
+                }
+            }
+            __syncthreads();
+            // every CTA gives its sums to every CTA: 16 bytes per thread
+            constexpr int PARTS = sizeof(SmpSums) / 16;
+            if (t < static_cast<int>(cl) * PARTS) {
+                const uint4 v = reinterpret_cast<const uint4 *>(&sh.mine)[t % PARTS];
+                st_cluster_v4(map_to_rank(reinterpret_cast<uint4 *>(&sh.sums[xs][rank]) + t % PARTS, t / PARTS),
+                              v.x, v.y, v.z, v.w);
+            }
+            cluster_sync_all();
+            SmpSums all = {0, 0, 0, 0, 0, 0, 0, 0};
+            bool over = false;
+            for (uint32_t k = 0; k < cl; ++k) {
+                const SmpSums &o = sh.sums[xs][k];
+                all.w += o.w;
+                all.w1 += o.w1;
+                all.w2 += o.w2;
+                all.wlist += o.wlist;
+                all.c += o.c;
+                all.c1 += o.c1;
+                all.c2 += o.c2;
+                all.list += o.list;
+                over |= o.list > SMP_LIST_CTA;
+            }
+            if (over || all.list > SMP_LIST) all.list = 0xffffffffu;
+            xs ^= 1;
+            return all;
+        };
+        SmpSums sum = sums_pass(use_list, !use_list, by_weight && !(use_list && by_count));
+
+        // with top-k the list holds all that it keeps; with top-p alone, all that p keeps if it
+        // weighs enough
+        if (use_list && sum.list != 0xffffffffu && (by_count || sum.wlist >= share(sum.w))) {
+            if (rank == 0) {
+                // thread i: entry i of the list
+                const int n_list = static_cast<int>(sum.list);
+                u64 c = 0, wt = 0;
+                float z = 0.f;
+                if (t < n_list) {
+                    int at = t;
+                    uint32_t k = 0;
+                    while (at >= static_cast<int>(sh.sums[xs ^ 1][k].list)) at -= static_cast<int>(sh.sums[xs ^ 1][k++].list);
+                    c = ld_cluster_u64(map_to_rank(&sh.list[at], k));
+                    z = smp_unkey<T>(static_cast<uint32_t>(c >> 32));
+                    wt = smp_weight(z, rw, tabs, sh.tab);
+                    sh.all[t] = c;
+                    sh.allw[t] = wt;
+                }
+                __syncthreads();
+                int before = 0;    // entries and weight before this one in the order
+                u64 before_w = 0;
+                if (t < n_list)
+                    for (int j = 0; j < n_list; ++j)
+                        if (sh.all[j] > c) {
+                            ++before;
+                            before_w += sh.allw[j];
+                        }
+                // sum over the CTA of one value per thread
+                auto block_sum = [&](u64 v) {
+                    v = warp_sum64(v);
+                    __syncthreads();
+                    if (l == 0) sh.wsum[w] = v;
+                    __syncthreads();
+                    u64 a = 0;
+                    for (int k = 0; k < SMP_WARPS; ++k) a += sh.wsum[k];
+                    return a;
+                };
+                bool keep = t < n_list && (!by_count || before < top_k);
+                if (by_weight) {
+                    const u64 end = share(by_count ? block_sum(keep ? wt : 0ull) : sum.w);
+                    keep = keep && before_w < end;
+                }
+                keep = keep && wt >= w_min;
+                const u64 total = block_sum(keep ? wt : 0ull);   // (all have read sh.allw)
+                if (t < n_list) sh.allw[t] = keep ? wt : 0ull;
+                __syncthreads();
+                const u64 target = draw_target(total);
+                const uint32_t index = ~static_cast<uint32_t>(c);
+                if (keep) {
+                    u64 upto = wt;   // kept weight up to and including this index
+                    for (int j = 0; j < n_list; ++j)
+                        if (~static_cast<uint32_t>(sh.all[j]) < index) upto += sh.allw[j];
+                    if (upto > target && upto - wt <= target) answer(index, z, total);
+                }
+            }
+            cluster_sync_all();   // rank 0 has read the peers' lists
+            return;
+        }
+        if (use_list && by_count) {   // too many for the list: sums are needed after all
+            __syncthreads();
+            if (t == 0) sh.mine = SmpSums{0, 0, 0, 0, 0, 0, 0, 0};
+            __syncthreads();
+            sum = sums_pass(false, true, by_weight);
+        }
+
+        // ---- the general search: histograms of the window that holds the cut
         int hb = 0;   // histogram in use
+        auto clear = [&]() {
+            for (int k = t; k < 4 * SMP_BINS; k += SMP_THREADS) (&sh.hist[hb][0][0])[k] = 0u;
+            __syncthreads();
+        };
         // totals over the cluster of the histogram just filled; exclusive prefixes over
-        // its bins into (pc, pw); then the bin in which `target` (a count, or a weight)
-        // is reached
+        // its bins into (pc, pw)
         auto totals = [&](uint32_t *pc, u64 *pw, uint32_t *tot_c, u64 *tot_w) {
             cluster_sync_all();
             uint32_t c = 0;
             u64 wt = 0;
             if (t < SMP_BINS) {
-                for (uint32_t k = 0; k < cl; ++k) {
-                    const uint4 h = ld_cluster_v4(map_to_rank(&sh.hist[hb][t], k));
-                    c += h.x;
-                    wt += static_cast<u64>(h.y) + (static_cast<u64>(h.z) << SMP_LIMB) +
-                          (static_cast<u64>(h.w) << (2 * SMP_LIMB));
+                // (all loads are under way before the first is used)
+                uint32_t h[4][SMP_MAX_CLUSTER];
+#pragma unroll
+                for (uint32_t k = 0; k < SMP_MAX_CLUSTER; ++k) {
+                    h[0][k] = h[1][k] = h[2][k] = h[3][k] = 0u;
+                    if (k >= cl) continue;
+                    const uint32_t at = map_to_rank(&sh.hist[hb][0][t], k);
+                    if (by_count) h[0][k] = ld_cluster_u32(at);
+                    if (by_weight) {
+                        h[1][k] = ld_cluster_u32(at + 4 * SMP_BINS);
+                        h[2][k] = ld_cluster_u32(at + 8 * SMP_BINS);
+                        h[3][k] = ld_cluster_u32(at + 12 * SMP_BINS);
+                    }
                 }
+                u64 l0 = 0, l1 = 0, l2 = 0;
+#pragma unroll
+                for (uint32_t k = 0; k < SMP_MAX_CLUSTER; ++k) {
+                    c += h[0][k];
+                    l0 += h[1][k];
+                    l1 += h[2][k];
+                    l2 += h[3][k];
+                }
+                wt = l0 + (l1 << SMP_LIMB) + (l2 << (2 * SMP_LIMB));
                 uint32_t ci = c;
                 u64 wi = wt;
 #pragma unroll
@@ -487,6 +760,7 @@ __global__ void __launch_bounds__(SMP_THREADS)
             __syncthreads();
             hb ^= 1;
         };
+        // the bin in which `target` (a count, or a weight) is reached
         auto find = [&](const uint32_t *pc, const u64 *pw, uint32_t tot_c, u64 tot_w, bool count,
                         u64 target) {
             if (t < SMP_BINS) {
@@ -496,85 +770,96 @@ __global__ void __launch_bounds__(SMP_THREADS)
                 if (a < target && target <= b) {
                     sh.bin = t;
                     sh.bc = c0;
-                    sh.bcin = c1 - c0;
                     sh.bw = w0;
-                    sh.bwin = w1 - w0;
                 }
             }
             __syncthreads();
         };
-        auto clear = [&]() {
-            if (t < SMP_BINS) sh.hist[hb][t] = make_uint4(0u, 0u, 0u, 0u);
-            __syncthreads();
+
+        // first level: the window x0 <= x < x1 in steps of (x1 - x0) / 256
+        int loaded = -1;
+        float x0 = 0.f, x1 = 0.f, per_x = 0.f;
+        uint32_t tot_c = 0;
+        u64 tot_w = 0;
+        auto bin_of = [&](float z) {
+            const float xx = smp_x(z, rw);
+            return xx >= x0 && xx < x1 ? min(static_cast<int>((xx - x0) * per_x), SMP_BINS - 1) : -1;
         };
-
-        // first level: x in steps of 1/8
-        clear();
-        for (int s = 0; s < steps; ++s) {
-            float x[8];
-            ck.load(s * 256 + l * 8, x);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float xx = smp_x(x[j], rw);
-                const int b = xx < SMP_X_END ? static_cast<int>(xx * SMP_BINS_PER_UNIT) : -1;
-                if (by_weight) smp_hist_add<true>(sh.hist[hb], b, smp_weight(x[j], rw, sh.tab), l);
-                else smp_hist_add<false>(sh.hist[hb], b, 0ull, l);
-            }
-        }
-        uint32_t tot_c;
-        u64 tot_w;
-        totals(sh.l0c, sh.l0w, &tot_c, &tot_w);
-
-        // the key and the number of equal logits at which `target` is reached
-        auto search = [&](bool count, u64 target, uint32_t *key, uint32_t *ties, u64 *kept_w) {
-            find(sh.l0c, sh.l0w, tot_c, tot_w, count, target);
-            const int b0 = sh.bin;
-            uint32_t base_c = sh.bc;
-            u64 base_w = sh.bw;
-            // the keys in that bin
-            uint32_t klo = 0xffffffffu, khi = 0u;
+        auto first_level = [&](int window) {
+            if (window == loaded) return;
+            loaded = window;
+            x0 = window == 0 ? 0.f : window == 1 ? SMP_X1 : SMP_X2;
+            x1 = window == 0 ? SMP_X1 : window == 1 ? SMP_X2 : SMP_X_END;
+            per_x = static_cast<float>(SMP_BINS) / (x1 - x0);
+            clear();
             for (int s = 0; s < steps; ++s) {
                 float x[8];
+                int bin[8];
+                bool any = false;
                 ck.load(s * 256 + l * 8, x);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float xx = smp_x(x[j], rw);
-                    if (xx < SMP_X_END && static_cast<int>(xx * SMP_BINS_PER_UNIT) == b0) {
-                        const uint32_t k = smp_key<T>(x[j]);
-                        klo = min(klo, k);
-                        khi = max(khi, k);
-                    }
+                    bin[j] = bin_of(x[j]);
+                    any |= bin[j] >= 0;
                 }
+                if (!__any_sync(0xffffffffu, any)) continue;
+                u64 v[8];
+                if (by_weight) {
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) smp_weight2(x[j], x[j + 1], rw, tabs, sh.tab, v[j], v[j + 1]);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (__any_sync(0xffffffffu, bin[j] >= 0))
+                        smp_hist_add(sh.hist[hb], bin[j], by_count, by_weight, by_weight ? v[j] : 0ull, l);
             }
-            klo = __reduce_min_sync(0xffffffffu, klo);
-            khi = __reduce_max_sync(0xffffffffu, khi);
-            if (l == 0) {
-                sh.redlo[w] = klo;
-                sh.redhi[w] = khi;
-            }
+            totals(sh.l0c, sh.l0w, &tot_c, &tot_w);
+        };
+
+        // the key and the number of equal logits at which `target` is reached
+        auto search = [&](bool count, u64 target, uint32_t *key, uint32_t *ties, u64 *kept_w) {
+            const u64 end1 = count ? sum.c1 : sum.w1, end2 = count ? sum.c2 : sum.w2;
+            const int window = target <= end1 ? 0 : target <= end2 ? 1 : 2;
+            uint32_t base_c = window == 0 ? 0u : window == 1 ? sum.c1 : sum.c2;
+            u64 base_w = window == 0 ? 0ull : window == 1 ? sum.w1 : sum.w2;
+            first_level(window);
+            find(sh.l0c, sh.l0w, tot_c, tot_w, count, target - (count ? static_cast<u64>(base_c) : base_w));
+            const int b0 = sh.bin;
+            base_c += sh.bc;
+            base_w += sh.bw;
             __syncthreads();
-            klo = __reduce_min_sync(0xffffffffu, sh.redlo[l & (SMP_WARPS - 1)]);
-            khi = __reduce_max_sync(0xffffffffu, sh.redhi[l & (SMP_WARPS - 1)]);
-            exchange(klo, khi);
-            for (uint32_t k = 0; k < cl; ++k) {
-                klo = min(klo, sh.slot[xs ^ 1][k].x);
-                khi = max(khi, sh.slot[xs ^ 1][k].y);
+            // keys that include those of the bin: its ends in z, with room for the roundings
+            uint32_t klo = smp_key<T>(-3.402823466e38f), khi = smp_key<T>(m);
+            if (rw.only_max) {
+                klo = khi;
+            } else {
+                const float near_x = x0 + static_cast<float>(b0) / per_x;
+                const float far_x = x0 + static_cast<float>(b0 + 1) / per_x;
+                const float room = (fabsf(m) + far_x * temperature) * 1e-6f + 1e-37f;
+                const float zhi = m - near_x * temperature + room, zlo = m - far_x * temperature - room;
+                if (zhi < m) khi = smp_key<T>(zhi + 0.f);
+                if (zlo > -3e38f) klo = smp_key<T>(zlo + 0.f);
             }
-            while (true) {
+            while (klo != khi) {
                 const int bits = 32 - __clz(khi - klo);
                 const int shift = bits > 8 ? bits - 8 : 0;
+                const float zlo = smp_unkey<T>(klo), zhi = smp_unkey<T>(khi);
                 clear();
                 for (int s = 0; s < steps; ++s) {
                     float x[8];
+                    bool any = false;
                     ck.load(s * 256 + l * 8, x);
 #pragma unroll
+                    for (int j = 0; j < 8; ++j) any |= x[j] >= zlo && x[j] <= zhi;
+                    if (!__any_sync(0xffffffffu, any)) continue;
+#pragma unroll
                     for (int j = 0; j < 8; ++j) {
+                        if (!__any_sync(0xffffffffu, x[j] >= zlo && x[j] <= zhi)) continue;
                         const uint32_t k = smp_key<T>(x[j]);
-                        const int b = k >= klo && k <= khi ? static_cast<int>((khi - k) >> shift) : -1;
-                        if (by_weight)
-                            smp_hist_add<true>(sh.hist[hb], b, b >= 0 ? smp_weight(x[j], rw, sh.tab) : 0ull, l);
-                        else
-                            smp_hist_add<false>(sh.hist[hb], b, 0ull, l);
+                        const int b = k >= klo && k <= khi && bin_of(x[j]) == b0
+                                          ? static_cast<int>((khi - k) >> shift) : -1;
+                        smp_hist_add(sh.hist[hb], b, by_count, by_weight,
+                                     by_weight ? smp_weight(x[j], rw, tabs, sh.tab) : 0ull, l);
                     }
                 }
                 uint32_t tc;
@@ -584,34 +869,27 @@ __global__ void __launch_bounds__(SMP_THREADS)
                 const uint32_t b = static_cast<uint32_t>(sh.bin);
                 base_c += sh.bc;
                 base_w += sh.bw;
-                if (shift == 0) {
-                    *key = khi - b;
-                    const u64 one = sh.bwin / sh.bcin;   // equal logits, equal weights
-                    *ties = count ? static_cast<uint32_t>(target) - base_c
-                                  : static_cast<uint32_t>((target - base_w + one - 1) / one);
-                    *kept_w = base_w + static_cast<u64>(*ties) * one;
-                    __syncthreads();
-                    return;
-                }
-                const uint32_t hi = khi - (b << shift);
+                khi -= b << shift;
                 const uint32_t width = (1u << shift) - 1u;
-                klo = hi - klo > width ? hi - width : klo;
-                khi = hi;
+                klo = khi - klo > width ? khi - width : klo;
                 __syncthreads();
             }
+            *key = klo;
+            const u64 one = by_weight ? smp_weight(smp_unkey<T>(klo), rw, tabs, sh.tab) : 1ull;
+            *ties = count ? static_cast<uint32_t>(target) - base_c
+                          : static_cast<uint32_t>((target - base_w + one - 1) / one);
+            *kept_w = base_w + static_cast<u64>(*ties) * one;
         };
 
-        u64 pool = tot_w;   // weight of what top-k keeps
-        if (by_count && static_cast<uint32_t>(top_k) < tot_c) {
+        u64 pool = sum.w;   // weight of what top-k keeps
+        if (by_count && static_cast<uint32_t>(top_k) < sum.c) {
             search(true, static_cast<u64>(top_k), &cut_key, &cut_ties, &pool);
             have_cut = true;
         }
         if (by_weight) {
-            u64 target = top_p > 0.f ? smp_mul_floor(top_p, pool, true) : 1ull;
-            if (target == 0) target = 1;
             uint32_t key, ties;
             u64 kept;
-            search(false, target, &key, &ties, &kept);
+            search(false, share(pool), &key, &ties, &kept);
             if (!have_cut || key > cut_key || (key == cut_key && ties < cut_ties)) {
                 cut_key = key;
                 cut_ties = ties;
@@ -620,25 +898,18 @@ __global__ void __launch_bounds__(SMP_THREADS)
         }
     }
 
-    // kept: weight at least w_min, and the cut
-    u64 w_min = 0;
-    if (min_p > 0.f)
-        w_min = min_p >= 1.f ? 1ull << SMP_ONE_SHIFT : smp_mul_floor(min_p, 1ull << SMP_ONE_SHIFT, true);
-    const u64 tie_w0 = have_cut ? smp_weight(smp_unkey<T>(cut_key), rw, sh.tab) : 0ull;
+    const float cut = have_cut ? smp_unkey<T>(cut_key) : -INFINITY;
+    const u64 tie_w0 = have_cut ? smp_weight(cut, rw, tabs, sh.tab) : 0ull;
     const u64 tie_w = tie_w0 >= w_min ? tie_w0 : 0ull;
-    // weight above the cut (tie: at the cut) of one logit
-    auto kept_weight = [&](float x, bool *tie) -> u64 {
-        *tie = false;
-        if (have_cut) {
-            const uint32_t k = smp_key<T>(x);
-            if (k < cut_key) return 0ull;
-            if (k == cut_key) {
-                *tie = true;
-                return 0ull;
-            }
+    // weights above the cut of 8 logits
+    auto kept_weights = [&](const float (&x)[8], u64 (&v)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) smp_weight2(x[j], x[j + 1], rw, tabs, sh.tab, v[j], v[j + 1]);
+        if (have_cut || w_min) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (!(x[j] > cut) || v[j] < w_min) v[j] = 0ull;
         }
-        const u64 v = smp_weight(x, rw, sh.tab);
-        return v >= w_min ? v : 0ull;
     };
 
     // sums of every warp of the cluster, in index order
@@ -647,12 +918,19 @@ __global__ void __launch_bounds__(SMP_THREADS)
     for (int s = 0; s < steps; ++s) {
         float x[8];
         ck.load(s * 256 + l * 8, x);
+        if (have_cut) {
+            bool any = false;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            bool tie;
-            above += kept_weight(x[j], &tie);
-            ties += tie ? 1u : 0u;
+            for (int j = 0; j < 8; ++j) {
+                any |= x[j] > cut;
+                ties += x[j] == cut ? 1u : 0u;
+            }
+            if (!__any_sync(0xffffffffu, any)) continue;
         }
+        u64 v[8];
+        kept_weights(x, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) above += v[j];
     }
     above = warp_sum64(above);
     ties = __reduce_add_sync(0xffffffffu, ties);
@@ -662,8 +940,6 @@ __global__ void __launch_bounds__(SMP_THREADS)
     cluster_sync_all();
 
     // every warp sums all warps' entries: 4 per lane, in order
-    constexpr int PER_LANE = SMP_MAX_CLUSTER * SMP_WARPS / 32;
-    const int entries = static_cast<int>(cl) * SMP_WARPS;
     u64 ew[PER_LANE];
     uint32_t et[PER_LANE], lane_t = 0;
 #pragma unroll
@@ -681,7 +957,6 @@ __global__ void __launch_bounds__(SMP_THREADS)
         if (l >= o) before_t += v;
     }
     before_t -= lane_t;
-    const int me = static_cast<int>(rank) * SMP_WARPS + w;
     u64 lane_w = 0, my_before = 0;
     uint32_t my_ties_before = 0;
 #pragma unroll
@@ -708,9 +983,7 @@ __global__ void __launch_bounds__(SMP_THREADS)
     const u64 my_sum = above + static_cast<u64>(ties < my_room ? ties : my_room) * tie_w;
 
     // the first index whose cumulative weight exceeds u * total
-    const float u = p.u[r];
-    u64 target = total - 1;
-    if (u < 1.f) target = u > 0.f ? smp_mul_floor(u, total, false) : 0ull;
+    const u64 target = draw_target(total);
     if (target >= my_first && target - my_first < my_sum) {
         u64 run = my_first;
         uint32_t seen = my_ties_before;
@@ -720,12 +993,10 @@ __global__ void __launch_bounds__(SMP_THREADS)
             u64 v[8];
             uint32_t tmask = 0;
             ck.load(i, x);
+            kept_weights(x, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                bool tie;
-                v[j] = kept_weight(x[j], &tie);
-                if (tie) tmask |= 1u << j;
-            }
+            for (int j = 0; j < 8; ++j)
+                if (have_cut && x[j] == cut) tmask |= 1u << j;
             const uint32_t tl = __popc(tmask);
             uint32_t tb = tl;
 #pragma unroll
@@ -762,15 +1033,7 @@ __global__ void __launch_bounds__(SMP_THREADS)
                             z = x[j];
                         }
                     }
-                    p.tokens[r] = first + i + at;
-                    if (p.logprobs) {
-                        constexpr float UNIT = 1.f / static_cast<float>(1ull << SMP_ONE_SHIFT);
-                        const u64 one = 1ull << SMP_ONE_SHIFT;
-                        // log(total): the largest logit's weight is 1, so near 0 by log1p
-                        const float ls = total < 2 * one ? log1pf(static_cast<float>(total - one) * UNIT)
-                                                         : logf(static_cast<float>(total) * UNIT);
-                        p.logprobs[r] = -smp_x(z, rw) - ls;
-                    }
+                    answer(first + i + at, z, total);
                 }
                 break;
             }
@@ -778,7 +1041,7 @@ __global__ void __launch_bounds__(SMP_THREADS)
             seen += __shfl_sync(0xffffffffu, tb, 31);
         }
     }
-    cluster_sync_all();   // no CTA leaves while a peer may still use its shared memory
+    // (nothing of a peer's is touched after the sums' exchange: a CTA may leave)
 }
 
 using SampleKernel = void (*)(const SampleParams, const SampleTables, const int);
@@ -790,6 +1053,7 @@ SampleKernel sample_kernel(int dtype, bool smem) {
 }
 
 constexpr int SMP_MAX_DYN = 160 * 1024;   // a CTA's logits; the rest of its shared memory is static
+constexpr int SMP_TWO_DYN = 88 * 1024;    // the same when two CTAs share an SM
 
 }  // namespace
 
@@ -802,17 +1066,19 @@ cudaError_t sample_set_attributes() {
     return cudaSuccess;
 }
 
-cudaError_t launch_sample(const SampleParams &p, cudaStream_t s) {
+cudaError_t launch_sample(const SampleParams &p, int sms, cudaStream_t s) {
     if (p.N <= 0) return cudaSuccess;
     static const SampleTables tabs = make_sample_tables();
     const long long elem = p.dtype == CE_FP32 ? 4 : 2;
+    // The smallest cluster with which two CTAs fit on an SM; more CTAs per row as long as all rows
+    // run at once and a warp has more than one sweep.
+    auto chunk_of = [&](int c) { return ((p.V + c * SMP_WARPS - 1) / (c * SMP_WARPS) + 7) / 8 * 8; };
     int cl = 1;
-    long long chunk = 0;
-    for (;; cl *= 2) {
-        chunk = (p.V + cl * SMP_WARPS - 1) / (cl * SMP_WARPS);
-        chunk = (chunk + 7) / 8 * 8;
-        if (cl == SMP_MAX_CLUSTER || chunk <= 256) break;
-    }
+    while (cl < SMP_MAX_CLUSTER &&
+           (chunk_of(cl) * SMP_WARPS * elem > SMP_TWO_DYN ||
+            (p.N * cl * 2 <= 2 * sms && chunk_of(cl) > 256)))
+        cl *= 2;
+    const long long chunk = chunk_of(cl);
     const long long bytes = chunk * SMP_WARPS * elem;
     const bool smem = bytes <= SMP_MAX_DYN;
     cudaLaunchAttribute at[1];

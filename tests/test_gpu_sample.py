@@ -217,3 +217,31 @@ def test_graph_stream_and_repeats():
 def test_no_rows():
     tok, lp = lce.sample_logits(torch.empty(0, 100, device="cuda"), torch.empty(0, device="cuda"))
     assert tok.shape == (0,) and lp.shape == (0,)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("std", [0.01, 0.3, 1.0, 6.0, 40.0])
+def test_flat_and_peaked_rows(std, dtype):
+    # cuts among few and among tens of thousands of tokens, near the largest logit and far from it
+    for v in (3000, 60000):
+        Z, u = logits(3, v, int(std * 100) + v, dtype, std=std)
+        Z[0] = (torch.randn(v, generator=torch.Generator().manual_seed(v)) * std).to(Z.dtype)
+        for f in (dict(top_p=0.999), dict(top_p=0.5), dict(top_k=128), dict(top_k=129), dict(top_k=2000, top_p=0.97),
+                  dict(top_k=v - 1), dict(top_k=60, top_p=0.9, min_p=0.3)):
+            check(Z, u, **f)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_ties_around_the_cut(dtype):
+    # more equal logits than the cut leaves room for, few and many
+    for v, n_top, n_tie in ((2000, 3, 40), (70000, 5, 100), (70000, 30, 5000), (70000, 0, 70000)):
+        Z = torch.full((3, v), -4.0)
+        Z[1] = torch.randn(v, generator=torch.Generator().manual_seed(1)) - 4
+        at = torch.randperm(v, generator=torch.Generator().manual_seed(2))
+        Z[:, at[:n_tie]] = 1.5
+        Z[:, at[:n_top]] = 3.0
+        Z = Z.to(DTYPES[dtype])
+        u = torch.tensor([0.999, 0.3, 0.7])
+        for f in (dict(top_k=n_top + 1), dict(top_k=n_top + n_tie // 2 + 1), dict(top_p=0.5), dict(top_p=0.9),
+                  dict(top_k=max(1, n_top), min_p=0.5)):
+            check(Z, u, **f)
