@@ -169,13 +169,10 @@ constexpr u64 SMP_ONE = 1ull << SMP_ONE_SHIFT;
 
 struct SmpRow {
     float m, ih, il;       // largest logit; 1 / temperature in two parts
-    bool only_max;         // +infinity among the logits, or no finite 1 / temperature:
-                           // the largest logits share the row
 };
 
 // x = (m - z) / temperature, rounded: the same monotone function wherever it is used.
 __device__ __forceinline__ float smp_x(float z, const SmpRow &r) {
-    if (r.only_max) return z == r.m ? 0.f : INFINITY;
     return (r.m - z) * r.ih;
 }
 
@@ -192,11 +189,6 @@ __device__ __forceinline__ u64 smp_finish(float kf, float q31, const unsigned *t
 }
 __device__ __forceinline__ void smp_weight2(float z0, float z1, const SmpRow &r, const SampleTables &c,
                                             const unsigned *tab, u64 &w0, u64 &w1) {
-    if (r.only_max) {
-        w0 = z0 == r.m ? SMP_ONE : 0ull;
-        w1 = z1 == r.m ? SMP_ONE : 0ull;
-        return;
-    }
     auto two = [](float v) { return make_float2(v, v); };
     const float2 z = make_float2(z0, z1), m = two(r.m), minus = two(-1.f), ih = two(r.ih);
     const float2 d = __ffma2_rn(z, minus, m);
@@ -312,7 +304,8 @@ struct SmpShared {
     u64 bw;                               // the bin found: weight and count before it
     uint32_t bc;
     int bin;
-    SmpSums mine;
+    SmpSums part[SMP_WARPS];              // of every warp of this CTA
+    uint32_t listed;                      // entries of `list` (or more, if it overflowed)
     float t0;
     unsigned tab[64];
 };
@@ -323,7 +316,18 @@ template <typename T, bool SMEM> struct SmpChunk {
     const T *p;
     int n;
     bool aligned;
+    // The largest logits share the row (one is +infinity, or 1 / temperature is not finite): they
+    // are seen as 0, all others as -infinity.
+    bool only_max;
+    float m;
     __device__ __forceinline__ void load(int i, float (&x)[8]) const {
+        load_plain(i, x);
+        if (only_max) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = x[j] == m ? 0.f : -INFINITY;
+        }
+    }
+    __device__ __forceinline__ void load_plain(int i, float (&x)[8]) const {
         if constexpr (SMEM) {
             if (i < n) {
                 smp_load_vec<T>(p + i, x);
@@ -374,7 +378,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
     const long long r = blockIdx.x / cl;
 
     // settings of the row
-    const float temperature = p.temperature ? p.temperature[r] : p.temperature_all;
+    float temperature = p.temperature ? p.temperature[r] : p.temperature_all;
     const int top_k = p.top_k ? p.top_k[r] : p.top_k_all;
     const float top_p = p.top_p ? p.top_p[r] : p.top_p_all;
     const float min_p = p.min_p ? p.min_p[r] : p.min_p_all;
@@ -392,6 +396,8 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
     SmpChunk<T, SMEM> ck;
     ck.n = n;
     ck.aligned = aligned;
+    ck.only_max = false;
+    ck.m = 0.f;
     float m = -INFINITY;
     if constexpr (SMEM) {
         T *mine = reinterpret_cast<T *>(smp_dyn) + static_cast<size_t>(w) * chunk;
@@ -472,7 +478,17 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
     rw.ih = 1.f / temperature;
     rw.il = fmaf(-temperature, rw.ih, 1.f) * rw.ih;
     if (!(fabsf(rw.il) < INFINITY)) rw.il = 0.f;   // temperatures near the ends of the type's range
-    rw.only_max = !(m < INFINITY) || !(rw.ih < INFINITY);
+    if (!(m < INFINITY) || !(rw.ih < INFINITY)) {
+        ck.only_max = true;
+        ck.m = m;
+        rw.m = 0.f;
+        rw.ih = 1.f;
+        rw.il = 0.f;
+        temperature = 1.f;
+#pragma unroll
+        for (int q = 0; q < PER_LANE; ++q) wm[q] = wm[q] == m ? 0.f : -INFINITY;
+        m = 0.f;
+    }
 
     const bool by_count = top_k > 0 && top_k < p.V;
     const bool by_weight = top_p < 1.f;
@@ -515,7 +531,8 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
             for (int q = 0; q < SMP_MAX_CLUSTER; ++q) {
                 const int e = w * SMP_MAX_CLUSTER + q;   // every warp looks at its share of the entries
                 if (e >= entries) break;
-                const float v = sh.wmax[e];
+                float v = sh.wmax[e];
+                if (ck.only_max) v = v == ck.m ? 0.f : -INFINITY;
                 int more = 0, same = 0;
 #pragma unroll
                 for (int i = 0; i < PER_LANE; ++i) {
@@ -525,7 +542,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                 if (l == 0 && more < want && want <= more + same) sh.t0 = v;   // (all who write, write the same)
             }
         }
-        if (t == 0) sh.mine = SmpSums{0, 0, 0, 0, 0, 0, 0, 0};
+        if (t == 0) sh.listed = 0;
         __syncthreads();
         const float t0 = use_list ? fmaxf(sh.t0, -3.402823466e38f) : INFINITY;   // (masked ones stay out)
 
@@ -566,7 +583,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             if (!(x[j] >= t0)) continue;
-                            const uint32_t at = atomicAdd(&sh.mine.list, 1u);
+                            const uint32_t at = atomicAdd(&sh.listed, 1u);
                             const uint32_t index = static_cast<uint32_t>(first) + s * 256 + l * 8 + j;
                             if (at < SMP_LIST_CTA) sh.list[at] = (static_cast<u64>(smp_key<T>(x[j])) << 32) | ~index;
                             if (weights) wl += v[j];
@@ -579,30 +596,33 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                 ws1 = warp_sum64(ws1);
                 ws2 = warp_sum64(ws2);
                 wl = warp_sum64(wl);
-                if (l == 0) {
-                    atomicAdd(&sh.mine.w, ws);
-                    atomicAdd(&sh.mine.w1, ws1);
-                    atomicAdd(&sh.mine.w2, ws2);
-                    atomicAdd(&sh.mine.wlist, wl);
-                }
             }
             if (counts) {
                 c = __reduce_add_sync(0xffffffffu, c);
                 c1 = __reduce_add_sync(0xffffffffu, c1);
                 c2 = __reduce_add_sync(0xffffffffu, c2);
-                if (l == 0) {
-                    atomicAdd(&sh.mine.c, c);
-                    atomicAdd(&sh.mine.c1, c1);
-                    atomicAdd(&sh.mine.c2, c2);
-                }
             }
+            if (l == 0) sh.part[w] = SmpSums{ws, ws1, ws2, wl, c, c1, c2, 0};
             __syncthreads();
-            // every CTA gives its sums to every CTA: 16 bytes per thread
-            constexpr int PARTS = sizeof(SmpSums) / 16;
-            if (t < static_cast<int>(cl) * PARTS) {
-                const uint4 v = reinterpret_cast<const uint4 *>(&sh.mine)[t % PARTS];
-                st_cluster_v4(map_to_rank(reinterpret_cast<uint4 *>(&sh.sums[xs][rank]) + t % PARTS, t / PARTS),
-                              v.x, v.y, v.z, v.w);
+            // lane k of warp 0 gives the CTA's sums to CTA k
+            if (w == 0) {
+                SmpSums o = l < SMP_WARPS ? sh.part[l] : SmpSums{0, 0, 0, 0, 0, 0, 0, 0};
+                o.w = warp_sum64(o.w);
+                o.w1 = warp_sum64(o.w1);
+                o.w2 = warp_sum64(o.w2);
+                o.wlist = warp_sum64(o.wlist);
+                o.c = __reduce_add_sync(0xffffffffu, o.c);
+                o.c1 = __reduce_add_sync(0xffffffffu, o.c1);
+                o.c2 = __reduce_add_sync(0xffffffffu, o.c2);
+                o.list = sh.listed;
+                if (l < static_cast<int>(cl)) {
+                    const uint32_t at = map_to_rank(&sh.sums[xs][rank], l);
+                    auto hi = [](u64 v) { return static_cast<uint32_t>(v >> 32); };
+                    auto lo = [](u64 v) { return static_cast<uint32_t>(v); };
+                    st_cluster_v4(at, lo(o.w), hi(o.w), lo(o.w1), hi(o.w1));
+                    st_cluster_v4(at + 16, lo(o.w2), hi(o.w2), lo(o.wlist), hi(o.wlist));
+                    st_cluster_v4(at + 32, o.c, o.c1, o.c2, o.list);
+                }
             }
             cluster_sync_all();
             SmpSums all = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -684,9 +704,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
             return;
         }
         if (use_list && by_count) {   // too many for the list: sums are needed after all
-            __syncthreads();
-            if (t == 0) sh.mine = SmpSums{0, 0, 0, 0, 0, 0, 0, 0};
-            __syncthreads();
+            if (t == 0) sh.listed = 0;
             sum = sums_pass(false, true, by_weight);
         }
 
@@ -785,12 +803,14 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
             const float xx = smp_x(z, rw);
             return xx >= x0 && xx < x1 ? min(static_cast<int>((xx - x0) * per_x), SMP_BINS - 1) : -1;
         };
-        auto first_level = [&](int window) {
-            if (window == loaded) return;
-            loaded = window;
+        auto set_window = [&](int window) {
             x0 = window == 0 ? 0.f : window == 1 ? SMP_X1 : SMP_X2;
             x1 = window == 0 ? SMP_X1 : window == 1 ? SMP_X2 : SMP_X_END;
             per_x = static_cast<float>(SMP_BINS) / (x1 - x0);
+        };
+        auto first_level = [&](int window) {
+            if (window == loaded) return;
+            loaded = window;
             clear();
             for (int s = 0; s < steps; ++s) {
                 float x[8];
@@ -822,23 +842,27 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
             const int window = target <= end1 ? 0 : target <= end2 ? 1 : 2;
             uint32_t base_c = window == 0 ? 0u : window == 1 ? sum.c1 : sum.c2;
             u64 base_w = window == 0 ? 0ull : window == 1 ? sum.w1 : sum.w2;
-            first_level(window);
-            find(sh.l0c, sh.l0w, tot_c, tot_w, count, target - (count ? static_cast<u64>(base_c) : base_w));
-            const int b0 = sh.bin;
-            base_c += sh.bc;
-            base_w += sh.bw;
-            __syncthreads();
-            // keys that include those of the bin: its ends in z, with room for the roundings
-            uint32_t klo = smp_key<T>(-3.402823466e38f), khi = smp_key<T>(m);
-            if (rw.only_max) {
-                klo = khi;
-            } else {
-                const float near_x = x0 + static_cast<float>(b0) / per_x;
-                const float far_x = x0 + static_cast<float>(b0 + 1) / per_x;
+            set_window(window);
+            // keys that include those of x from near_x to far_x, with room for the roundings
+            uint32_t klo, khi;
+            auto key_range = [&](float near_x, float far_x) {
+                klo = smp_key<T>(-3.402823466e38f);
+                khi = smp_key<T>(m);
                 const float room = (fabsf(m) + far_x * temperature) * 1e-6f + 1e-37f;
                 const float zhi = m - near_x * temperature + room, zlo = m - far_x * temperature - room;
                 if (zhi < m) khi = smp_key<T>(zhi + 0.f);
                 if (zlo > -3e38f) klo = smp_key<T>(zlo + 0.f);
+            };
+            key_range(x0, x1);
+            int b0 = -1;   // the bin that is searched; -1: the window has so few keys that each gets its bin
+            if (khi - klo >= SMP_BINS) {
+                first_level(window);
+                find(sh.l0c, sh.l0w, tot_c, tot_w, count, target - (count ? static_cast<u64>(base_c) : base_w));
+                b0 = sh.bin;
+                base_c += sh.bc;
+                base_w += sh.bw;
+                __syncthreads();
+                key_range(x0 + static_cast<float>(b0) / per_x, x0 + static_cast<float>(b0 + 1) / per_x);
             }
             while (klo != khi) {
                 const int bits = 32 - __clz(khi - klo);
@@ -856,7 +880,8 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                     for (int j = 0; j < 8; ++j) {
                         if (!__any_sync(0xffffffffu, x[j] >= zlo && x[j] <= zhi)) continue;
                         const uint32_t k = smp_key<T>(x[j]);
-                        const int b = k >= klo && k <= khi && bin_of(x[j]) == b0
+                        const int in = bin_of(x[j]);
+                        const int b = k >= klo && k <= khi && in >= 0 && (b0 < 0 || in == b0)
                                           ? static_cast<int>((khi - k) >> shift) : -1;
                         smp_hist_add(sh.hist[hb], b, by_count, by_weight,
                                      by_weight ? smp_weight(x[j], rw, tabs, sh.tab) : 0ull, l);
