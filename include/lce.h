@@ -267,21 +267,25 @@ lce_status lce_sample_logits(const void *Z, int z_dtype, int64_t ld, int64_t N, 
 
 /* Linear layers in 8-bit floating point (e4m3), one fp32 scale per block of 128 values
  * along the contraction (the last block of a row may be shorter):
- *   rows:  x[r][k] ~ scale[r][k / 128] * q[r][k],        scale [R][ceil(C / 128)]
- *   tiles: w[r][k] ~ scale[r / 128][k / 128] * q[r][k],  scale [ceil(R / 128)][ceil(C / 128)]
+ *   rows:  x[r][k] ~ scale(r, k / 128) * q[r][k]
+ *   tiles: w[r][k] ~ scale(r / 128, k / 128) * q[r][k]
  *
  * lce_fp8_quantize: X [R][ld] (x_dtype as for lce_ce_logits, C columns) to row blocks, or
  * to tiles (tiles = 1); the scale is the smallest power of two (at least 2^-126) under which the
  * block's largest finite |x| is at most 448, 1 for a block of zeros; q is x / scale rounded
  * to the nearest e4m3 value, ties to even; infinities and NaN become NaN. q [R][ldq] and
  * scale: X in its own layout; qt [C][ldqt] and scale_t: X^T in the same form (row blocks
- * then run along X's rows); either pair may be NULL. ldq, ldqt: multiples of 16 (bytes); a
- * row's bytes up to the next multiple of 16 may be written. q, qt 16-byte aligned.
+ * then run along X's rows); either pair may be NULL. Row blocks' scales are stored block by
+ * block, scale [ceil(C / 128)][R] and scale_t [ceil(R / 128)][C], so that the product reads
+ * those of consecutive rows at once; tiles' as scale [ceil(R / 128)][ceil(C / 128)] and
+ * scale_t its transpose. ldq, ldqt: multiples of 16 (bytes); a row's bytes up to the next
+ * multiple of 16 may be written. q, qt 16-byte aligned.
  *
  * lce_fp8_matmul: out [M][ldc] (c_dtype) = A B^T with A [M][lda] in row blocks and
  * B [N][ldb] in tiles or (b_rows = 1) in row blocks, any fp32 scales:
- *   out[m][n] = sum over blocks b of (sa[m][b] * sb[n or n / 128][b]) * sum_{k in b} A[m][k] B[n][k]
- * summed in fp32, rounded once. With it: logits = x W^T (x in rows, W in tiles); dx =
+ *   out[m][n] = sum over blocks b of (sa(m, b) * sb(n or n / 128, b)) * sum_{k in b} A[m][k] B[n][k]
+ * summed in fp32, rounded once; sa(r, b) is at sa[r * sa_row + b * sa_block], sb likewise
+ * (fastest where the scales of consecutive rows lie side by side). With it: logits = x W^T (x in rows, W in tiles); dx =
  * dlogits W (dlogits in rows, W^T in tiles); dW = dlogits^T x (both transposed, in rows).
  * A, B, out 16-byte aligned; lda, ldb and ldc's bytes multiples of 16; K, lda, ldb in
  * values = bytes. Columns of `out` from N on are left as they were. Workspace: a header
@@ -290,9 +294,11 @@ lce_status lce_fp8_quantize(const void *X, int x_dtype, int64_t ld, int64_t R, i
                             void *q, int64_t ldq, float *scale, void *qt, int64_t ldqt,
                             float *scale_t, lce_stream_t stream);
 lce_status lce_fp8_matmul_workspace_size(size_t *bytes);
-lce_status lce_fp8_matmul(const void *A, int64_t lda, const float *sa, const void *B, int64_t ldb,
-                          const float *sb, int b_rows, int64_t M, int64_t N, int64_t K, void *out,
-                          int64_t ldc, int c_dtype, void *ws, size_t ws_bytes, lce_stream_t stream);
+lce_status lce_fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t sa_row,
+                          int64_t sa_block, const void *B, int64_t ldb, const float *sb,
+                          int64_t sb_row, int64_t sb_block, int b_rows, int64_t M, int64_t N,
+                          int64_t K, void *out, int64_t ldc, int c_dtype, void *ws, size_t ws_bytes,
+                          lce_stream_t stream);
 
 /* The global norm of a list of n gradients and clipping by it:
  *   norm = (sum over all tensors of |g|^p)^(1/p) for p = 2 or 1, or max |g|

@@ -153,8 +153,8 @@ def lib() -> ctypes.CDLL:
     L.lce_fp8_quantize.argtypes = [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp,
                                    _vp, _i64, _vp, _vp]
     L.lce_fp8_matmul_workspace_size.argtypes = [_sz]
-    L.lce_fp8_matmul.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64,
-                                 ctypes.c_int, _vp, ctypes.c_size_t, _vp]
+    L.lce_fp8_matmul.argtypes = [_vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, ctypes.c_int,
+                                 _i64, _i64, _i64, _vp, _i64, ctypes.c_int, _vp, ctypes.c_size_t, _vp]
     L.lce_grad_norm_workspace_size.argtypes = [_i64, _sz]
     L.lce_grad_norm.argtypes = [_vp, _vp, _vp, _i64, ctypes.c_int, _vp, _vp, ctypes.c_size_t, _vp]
     L.lce_clip_grad_norm.argtypes = [_vp, _vp, _vp, _vp, _i64, ctypes.c_int, _f, _f, _vp, _vp,

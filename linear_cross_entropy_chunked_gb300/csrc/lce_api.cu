@@ -1617,10 +1617,13 @@ lce_status lce_fp8_matmul_workspace_size(size_t *bytes) {
     return LCE_OK;
 }
 
-lce_status lce_fp8_matmul(const void *A, int64_t lda, const float *sa, const void *B, int64_t ldb,
-                          const float *sb, int b_rows, int64_t M, int64_t N, int64_t K, void *out,
-                          int64_t ldc, int c_dtype, void *ws, size_t ws_bytes, lce_stream_t stream) {
+lce_status lce_fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t sa_row,
+                          int64_t sa_block, const void *B, int64_t ldb, const float *sb,
+                          int64_t sb_row, int64_t sb_block, int b_rows, int64_t M, int64_t N,
+                          int64_t K, void *out, int64_t ldc, int c_dtype, void *ws, size_t ws_bytes,
+                          lce_stream_t stream) {
     g_launches = 0;
+    if (sa_row < 0 || sa_block < 0 || sb_row < 0 || sb_block < 0) return LCE_ERR_INVALID_ARG;
     if (M < 0 || N < 0 || K <= 0 || M > MAX_V || N > MAX_V || K > MAX_V) return LCE_ERR_INVALID_ARG;
     if (lda < K || ldb < K || ldc < N || c_dtype < CE_BF16 || c_dtype > CE_FP16 || !ws)
         return LCE_ERR_INVALID_ARG;
@@ -1653,8 +1656,15 @@ lce_status lce_fp8_matmul(const void *A, int64_t lda, const float *sa, const voi
     p.tiles = static_cast<int>(pair ? pair_tiles : tiles);
     p.a_box_rows = pair || M >= 128 ? 128 : static_cast<int>(align_up(static_cast<size_t>(M), 8));
     p.n_bulk = static_cast<int>(N / (16 / elem) * (16 / elem));
+    // what 192 KB hold of A's rows and 128 rows of B (a multiple of 1 KB each), as barriers allow
+    p.stages = std::min(11, 6 * 32768 / (p.a_box_rows * 128 + 16384));
     p.sa = sa;
     p.sb = sb;
+    p.sa_row = sa_row;
+    p.sa_block = sa_block;
+    p.sb_row = sb_row;
+    p.sb_block = sb_block;
+    p.sb_vec = sb_row == 1 && sb_block % 4 == 0 && aligned16(sb) ? 1 : 0;
     p.C = out;
     p.ldc = ldc;
     p.c_type = c_dtype;

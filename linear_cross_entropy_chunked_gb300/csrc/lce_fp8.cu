@@ -8,6 +8,9 @@
 // The scale of a block is the smallest power of two under which its largest finite
 // value is at most 448 (e4m3's largest), so the division is exact and e4m3's own rounding
 // is the only one; the product takes any fp32 scales.
+#include <cstring>
+#include <type_traits>
+
 #include <cuda_fp8.h>
 
 #include "lce_internal.h"
@@ -40,44 +43,98 @@ __device__ __forceinline__ Pow2 block_scale(float amax) {
     s.inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     return s;
 }
-__device__ __forceinline__ float finite_abs(float x) {
-    const float a = fabsf(x);
-    return a < INFINITY ? a : 0.f;   // NaN and infinities do not count
-}
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+// e4m3 of a * f and b * f, and of c * f and d * f, in order (f a power of two: exact)
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, float f) {
+    const float2 ff = make_float2(f, f);
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(__fmul2_rn(make_float2(a, b), ff), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(__fmul2_rn(make_float2(c, d), ff), __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
 }
 
-template <typename T> __device__ __forceinline__ float qt_float(T v) { return static_cast<float>(v); }
-
-// 8 values of a row; those past `n` are 0; infinities become NaN (e4m3 has none).
-template <typename T>
-__device__ __forceinline__ void qt_load8(const T *p, int n, bool vec, float (&x)[8]) {
-    if (vec && n >= 8) {
-        if constexpr (sizeof(T) == 4) {
+// 8 values of a row as they come (16-bit types stay packed: four words of two), and what the
+// kernel needs of them. Maxima ignore NaN; infinities are turned into NaN first (`mend`,
+// rarely run), as e4m3 has none.
+template <typename T> struct QtVec {
+    uint32_t w[4];
+    static constexpr uint32_t INF2 = sizeof(T) == 2 && std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    __device__ __forceinline__ static uint32_t max2(uint32_t a, uint32_t b) {
+        if constexpr (std::is_same<T, __half>::value) {
+            const __half2 m = __hmax2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+            return *reinterpret_cast<const uint32_t *>(&m);
+        } else {
+            const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                             *reinterpret_cast<const __nv_bfloat162 *>(&b));
+            return *reinterpret_cast<const uint32_t *>(&m);
+        }
+    }
+    __device__ __forceinline__ static float low(uint32_t v) {
+        if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(static_cast<unsigned short>(v)));
+        else return __uint_as_float(v << 16);
+    }
+    __device__ __forceinline__ void load(const T *p, int n, bool vec) {
+        if (vec && n >= 8) {
+            const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p));
+            w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+        } else {
+            const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] = (2 * j < n ? h[2 * j] : 0u) | ((2 * j + 1 < n ? static_cast<uint32_t>(h[2 * j + 1]) : 0u) << 16);
+        }
+    }
+    // largest |x| of column pair j, as two 16-bit values
+    __device__ __forceinline__ uint32_t abs2(int j) const { return w[j] & 0x7fff7fffu; }
+    __device__ __forceinline__ uint32_t row_max() const {
+        return max2(max2(abs2(0), abs2(1)), max2(abs2(2), abs2(3)));
+    }
+    __device__ __forceinline__ void mend() {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if ((w[j] & 0x7fffu) == INF2) w[j] |= 0x7fffu;
+            if (((w[j] >> 16) & 0x7fffu) == INF2) w[j] |= 0x7fff0000u;
+        }
+    }
+    __device__ __forceinline__ float get(int j) const {
+        if constexpr (std::is_same<T, __half>::value) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j >> 1]));
+            return j & 1 ? f.y : f.x;
+        } else {
+            return j & 1 ? __uint_as_float(w[j >> 1] & 0xffff0000u) : __uint_as_float(w[j >> 1] << 16);
+        }
+    }
+};
+template <> struct QtVec<float> {
+    float x[8];
+    __device__ __forceinline__ void load(const float *p, int n, bool vec) {
+        if (vec && n >= 8) {
             const float4 a = __ldcs(reinterpret_cast<const float4 *>(p));
             const float4 b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
             x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
             x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
         } else {
-            const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p));
-            const T *h = reinterpret_cast<const T *>(&u);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = qt_float(h[j]);
+            for (int j = 0; j < 8; ++j) x[j] = j < n ? p[j] : 0.f;
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = j < n ? qt_float(p[j]) : 0.f;
     }
+    __device__ __forceinline__ float row_max() const {
+        float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (fabsf(x[j]) == INFINITY) x[j] = __uint_as_float(0x7fffffffu);
-}
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
+        return m;
+    }
+    __device__ __forceinline__ void mend() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (fabsf(x[j]) == INFINITY) x[j] = __uint_as_float(0x7fffffffu);
+    }
+    __device__ __forceinline__ float get(int j) const { return x[j]; }
+};
 
 template <typename T, bool TILE>
-__global__ void __launch_bounds__(QT_THREADS, 2) lce_fp8_quantize_kernel(const Fp8QuantParams p) {
+__global__ void __launch_bounds__(QT_THREADS, sizeof(T) == 4 ? 2 : 3)
+    lce_fp8_quantize_kernel(const Fp8QuantParams p) {
+    constexpr bool PACKED = sizeof(T) == 2;
+    using V = QtVec<T>;
     __shared__ __align__(16) uint8_t st[128 * 128];
     __shared__ float cred[QT_THREADS / 32][128];
     const int t = threadIdx.x, w = t >> 5, l = t & 31;
@@ -88,56 +145,71 @@ __global__ void __launch_bounds__(QT_THREADS, 2) lce_fp8_quantize_kernel(const F
     const int nr = p.R - r0 < 128 ? static_cast<int>(p.R - r0) : 128;
     const int nc = p.C - c0 < 128 ? static_cast<int>(p.C - c0) : 128;
     const T *X = static_cast<const T *>(p.X) + r0 * p.ld + c0;
-    float x[8][8];
+    V x[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const int r = g * 8 + k;
-        if (r < nr && i * 8 < nc) {
-            qt_load8<T>(X + static_cast<long long>(r) * p.ld + i * 8, nc - i * 8, p.vec != 0, x[k]);
-        } else {
+        if (r < nr && i * 8 < nc) x[k].load(X + static_cast<long long>(r) * p.ld + i * 8, nc - i * 8, p.vec != 0);
+        else memset(&x[k], 0, sizeof(V));
+    }
+    // largest |x| of the thread's part of each row
+    float rmax[8];
+    auto row_maxima = [&]() {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[k][j] = 0.f;
+        for (int k = 0; k < 8; ++k) {
+            if constexpr (PACKED) {
+                const uint32_t m = x[k].row_max();
+                rmax[k] = fmaxf(V::low(m), V::low(m >> 16));
+            } else {
+                rmax[k] = x[k].row_max();
+            }
+            rmax[k] = fmaxf(rmax[k], 0.f);   // (a NaN for a thread of NaN only)
         }
+    };
+    row_maxima();
+    float most = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) most = fmaxf(most, rmax[k]);
+    if (most == INFINITY) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k].mend();
+        row_maxima();
+        most = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) most = fmaxf(most, rmax[k]);
     }
     Pow2 tile_s = {1.f, 1.f};
     if constexpr (TILE) {
-        float m = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m = fmaxf(m, finite_abs(x[k][j]));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (l == 0) cred[0][w] = m;
+        // (the bit patterns of non-negative floats are in their order)
+        const uint32_t mw = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+        if (l == 0) cred[0][w] = __uint_as_float(mw);
         __syncthreads();
-        m = cred[0][l & 7];
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        tile_s = block_scale(m);
+        const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(cred[0][l & 7]));
+        tile_s = block_scale(__uint_as_float(m));
         if (t == 0) {
             if (p.q) p.scale[rb * p.cblocks + cb] = tile_s.scale;
             if (p.qt) p.scale_t[cb * p.rblocks + rb] = tile_s.scale;
         }
     }
     if (p.q) {
+        if constexpr (!TILE) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) rmax[k] = fmaxf(rmax[k], __shfl_xor_sync(0xffffffffu, rmax[k], o));
+        }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int r = g * 8 + k;
             Pow2 s = tile_s;
             if constexpr (!TILE) {
-                float m = 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) m = fmaxf(m, finite_abs(x[k][j]));
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                s = block_scale(m);
-                if (i == 0 && r < nr) p.scale[(r0 + r) * p.cblocks + cb] = s.scale;
+                s = block_scale(rmax[k]);
+                if (i == 0 && r < nr) p.scale[cb * p.R + r0 + r] = s.scale;
             }
             if (r < nr && i * 8 < nc) {
-                const float f = s.inv;
                 uint2 v;
-                v.x = e4m3x4(x[k][0] * f, x[k][1] * f, x[k][2] * f, x[k][3] * f);
-                v.y = e4m3x4(x[k][4] * f, x[k][5] * f, x[k][6] * f, x[k][7] * f);
+                v.x = e4m3x4(x[k].get(0), x[k].get(1), x[k].get(2), x[k].get(3), s.inv);
+                v.y = e4m3x4(x[k].get(4), x[k].get(5), x[k].get(6), x[k].get(7), s.inv);
                 *reinterpret_cast<uint2 *>(p.q + (r0 + r) * p.ldq + c0 + i * 8) = v;
             }
         }
@@ -149,36 +221,53 @@ __global__ void __launch_bounds__(QT_THREADS, 2) lce_fp8_quantize_kernel(const F
             for (int j = 0; j < 8; ++j) inv[j] = tile_s.inv;
         } else {
             float m[8];
+            if constexpr (PACKED) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                m[j] = 0.f;
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t c = x[0].abs2(j);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) m[j] = fmaxf(m[j], finite_abs(x[k][j]));
-                m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+                    for (int k = 1; k < 8; ++k) c = V::max2(c, x[k].abs2(j));
+                    c = V::max2(c, __shfl_xor_sync(0xffffffffu, c, 16));
+                    m[2 * j] = fmaxf(V::low(c), 0.f);
+                    m[2 * j + 1] = fmaxf(V::low(c >> 16), 0.f);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    m[j] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) m[j] = fmaxf(m[j], fabsf(x[k].get(j)));
+                    m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+                }
             }
             if (l < 16) {
+                *reinterpret_cast<float4 *>(&cred[w][i * 8]) = make_float4(m[0], m[1], m[2], m[3]);
+                *reinterpret_cast<float4 *>(&cred[w][i * 8 + 4]) = make_float4(m[4], m[5], m[6], m[7]);
+            }
+            __syncthreads();
+            // thread c: column c's scale, kept in the first row of cred
+            if (t < 128) {
+                float a = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) cred[w][i * 8 + j] = m[j];
+                for (int k = 0; k < QT_THREADS / 32; ++k) a = fmaxf(a, cred[k][t]);
+                const Pow2 s = block_scale(a);
+                cred[0][t] = s.inv;
+                if (t < nc) p.scale_t[rb * p.C + c0 + t] = s.scale;
             }
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float a = 0.f;
-#pragma unroll
-                for (int k = 0; k < QT_THREADS / 32; ++k) a = fmaxf(a, cred[k][i * 8 + j]);
-                const Pow2 s = block_scale(a);
-                inv[j] = s.inv;
-                if (g == 0 && i * 8 + j < nc) p.scale_t[(c0 + i * 8 + j) * p.rblocks + rb] = s.scale;
+            for (int j = 0; j < 8; j += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(&cred[0][i * 8 + j]);
+                inv[j] = v.x; inv[j + 1] = v.y; inv[j + 2] = v.z; inv[j + 3] = v.w;
             }
         }
         // column c's 8-byte unit of rows 8 g .. + 7 goes to unit g ^ (c / 8) of its 128 bytes,
         // which spreads the 16 columns that a half-warp writes at once over all banks
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float f = inv[j];
             uint2 v;
-            v.x = e4m3x4(x[0][j] * f, x[1][j] * f, x[2][j] * f, x[3][j] * f);
-            v.y = e4m3x4(x[4][j] * f, x[5][j] * f, x[6][j] * f, x[7][j] * f);
+            v.x = e4m3x4(x[0].get(j), x[1].get(j), x[2].get(j), x[3].get(j), inv[j]);
+            v.y = e4m3x4(x[4].get(j), x[5].get(j), x[6].get(j), x[7].get(j), inv[j]);
             *reinterpret_cast<uint2 *>(st + (i * 8 + j) * 128 + ((g ^ i) << 3)) = v;
         }
         __syncthreads();
@@ -228,7 +317,8 @@ cudaError_t launch_fp8_quantize(const Fp8QuantParams &p, int dtype, bool tile, c
 // and half of B's), for products with many tiles. Otherwise 128 x 128 tiles, one CTA
 // each; few tiles are split along k over a cluster of up to 8 CTAs, whose fp32 sums are
 // added through distributed shared memory in rank order.
-// B_ROWS: B's scales are per row (gradient of a weight), read through shared memory.
+// B_ROWS: B's scales are per row (gradient of a weight); every warp brings those of its
+// columns into shared memory of its own.
 // Every mbarrier wait is bounded, as in the bf16 GEMM. The waits for TMEM buffers acquire at
 // CTA scope and their remote arrivals are relaxed: no memory is handed over with them (the
 // tcgen05 fences order TMEM), and cluster scope costs a flush or an L1 invalidation per
@@ -239,7 +329,8 @@ namespace {
 constexpr int F8_BK = 128;                 // values (bytes) per k block: one 128-byte swizzle row
 constexpr int F8_OP_BYTES = 128 * F8_BK;   // 128 rows of an operand
 constexpr int F8_STAGE = 2 * F8_OP_BYTES;  // A and B of one k block, per CTA
-constexpr int F8_STAGES = 6;
+constexpr int F8_STAGES = 6;               // pairs; otherwise as many as fit when A has few rows
+constexpr int F8_MAX_STAGES = 11;
 constexpr int F8_WARP_BOX = 4096;          // 32 rows x 128 bytes of output per consumer warp
 constexpr int F8_SMEM = F8_STAGES * F8_STAGE + 8 * F8_WARP_BOX + 1024;
 constexpr int F8_THREADS = 384;
@@ -305,8 +396,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     constexpr int NBUF = TMEM_COLS / BNT;      // partial products in flight
     constexpr int COLS = BNT / 2;              // columns per consumer warp
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full_bar[F8_STAGES];
-    __shared__ __align__(8) uint64_t empty_bar[F8_STAGES];
+    __shared__ __align__(8) uint64_t full_bar[F8_MAX_STAGES];
+    __shared__ __align__(8) uint64_t empty_bar[F8_MAX_STAGES];
     __shared__ __align__(8) uint64_t tfull_bar[NBUF];
     __shared__ __align__(8) uint64_t tempty_bar[NBUF];
     __shared__ __align__(8) uint64_t drain_bar;
@@ -325,9 +416,14 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     const int kb0 = PAIR ? 0 : static_cast<int>(static_cast<long long>(p.KB) * rank / csize);
     const int kb1 = PAIR ? p.KB : static_cast<int>(static_cast<long long>(p.KB) * (rank + 1) / csize);
     const int nk = kb1 - kb0;
+    // A single token's A takes 1 KB of a stage, not 16: more stages, more bytes of B under way.
+    // (The MMA reads 128 rows of A all the same, the rest of them out of B: rows of no output.)
+    const int a_bytes = PAIR ? F8_OP_BYTES : p.a_box_rows * F8_BK;
+    const int stage_bytes = PAIR ? F8_STAGE : a_bytes + F8_OP_BYTES;
+    const int nstages = PAIR ? F8_STAGES : p.stages;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < F8_STAGES; ++s) {
+        for (int s = 0; s < nstages; ++s) {
             mbar_init(&full_bar[s], 1);
             mbar_init(&empty_bar[s], 1);
         }
@@ -379,7 +475,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             uint32_t phase = 0;
             int issued = 0;
             bool ok = true;
-            const uint32_t bytes = static_cast<uint32_t>(p.a_box_rows * F8_BK + F8_OP_BYTES);
+            const uint32_t bytes = static_cast<uint32_t>(stage_bytes);
             for (int t = cid; ok && t < p.tiles; t += ncl) {
                 int mt, nt;
                 f8_tile(p, t, &mt, &nt);
@@ -390,8 +486,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                         ok = false;
                         break;
                     }
-                    uint8_t *sA = smem + stage * F8_STAGE;
-                    uint8_t *sB = sA + F8_OP_BYTES;
+                    uint8_t *sA = smem + stage * stage_bytes;
+                    uint8_t *sB = sA + a_bytes;
                     uint64_t *fb = &full_bar[stage];
                     if constexpr (PAIR) {
                         // both CTAs' bytes complete on the leader's barrier
@@ -405,7 +501,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                         tma_load_2d(sB, &p.tmB, fb, kb * F8_BK, yb);
                     }
                     ++issued;
-                    if (++stage == F8_STAGES) {
+                    if (++stage == nstages) {
                         stage = 0;
                         phase ^= 1;
                     }
@@ -413,10 +509,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             }
             if (!ok) {
                 // drain: wait (bounded) for the copies still in flight into each stage
-                const int n = issued < F8_STAGES ? issued : F8_STAGES;
+                const int n = issued < nstages ? issued : nstages;
                 for (int i = 0; i < n; ++i) {
                     if (--stage < 0) {
-                        stage = F8_STAGES - 1;
+                        stage = nstages - 1;
                         phase ^= 1;
                     }
                     if (leader) mbar_wait_drain(&full_bar[stage], phase, 50000000ull);
@@ -438,9 +534,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             constexpr uint16_t both = static_cast<uint16_t>((1u << CL) - 1u);
             for (int t = cid; ok && t < p.tiles; t += ncl) {
                 for (int kb = 0; kb < nk; ++kb) {
-                    const uint32_t sA = smem_u32(smem + stage * F8_STAGE);
+                    const uint32_t sA = smem_u32(smem + stage * stage_bytes);
                     const uint64_t ad = sdesc(sA, 16u, 1024u);
-                    const uint64_t bd = sdesc(sA + F8_OP_BYTES, 16u, 1024u);
+                    const uint64_t bd = sdesc(sA + a_bytes, 16u, 1024u);
                     const uint32_t d = tmem_base + buf * BNT;
                     ok = mbar_wait(&full_bar[stage], phase, ab) && mbar_wait(&tempty_bar[buf], bphase ^ 1, ab);
                     ok = __all_sync(0xffffffffu, ok);
@@ -461,7 +557,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                     }
                     __syncwarp();
                     any_mma = true;
-                    if (++stage == F8_STAGES) {
+                    if (++stage == nstages) {
                         stage = 0;
                         phase ^= 1;
                     }
@@ -486,9 +582,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         if constexpr (PAIR) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F8_REGS_CONSUMER));
         const int quarter = warp & 3, half = warp >> 2;
         uint8_t *box = smem + F8_STAGES * F8_STAGE + warp * F8_WARP_BOX;
-        // B_ROWS: the scales of the half's columns for two k blocks, in the output box of its
-        // first warp (free between a tile's stores and the next one's)
-        float *sb_smem = reinterpret_cast<float *>(smem + F8_STAGES * F8_STAGE + half * 4 * F8_WARP_BOX);
+        // B_ROWS: the scales of the warp's columns for two k blocks, in its output box (free
+        // between a tile's store and the next one's)
+        float *sb_smem = reinterpret_cast<float *>(box);
         const uint32_t tempty_addr = map_to_rank(&tempty_bar[0], PAIR ? 0u : rank);
         int buf = 0;
         uint32_t bphase = 0;
@@ -501,21 +597,42 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             const int col0 = nt * BNT + half * COLS;
             const bool active = row0 < p.M && col0 < p.N;   // warp-uniform: some output of this warp exists
             const int row = row0 + lane;
-            const float *sa = p.sa + static_cast<long long>(row < p.M ? row : 0) * p.KB;
-            // tile scales: the warp's columns lie in one block of 128
-            const float *sb = p.sb + static_cast<long long>(col0 < p.N ? col0 / 128 : 0) * p.KB;
-            const int sb_col = col0 + (threadIdx.x & 127);   // the column whose scales this thread fetches
-            const bool fetch = B_ROWS && (threadIdx.x & 127) < COLS && sb_col < p.N;
+            const float *sa = p.sa + static_cast<long long>(row < p.M ? row : 0) * p.sa_row;
+            const long long sak = p.sa_block, sbk = p.sb_block;
+            // tile scales: the warp's columns lie in one block of 128; row scales: VEC columns per lane
+            constexpr int VEC = COLS / 32;
+            const int sb_col = col0 + lane * VEC;
+            const float *sb = p.sb + (B_ROWS ? static_cast<long long>(sb_col < p.N ? sb_col : 0)
+                                             : static_cast<long long>(col0 < p.N ? col0 / 128 : 0)) * p.sb_row;
+            auto load_sb = [&](float (&b)[VEC], int kb) {
+                const float *at = sb + kb * sbk;
+                if constexpr (!B_ROWS) {
+                    b[0] = *at;
+                } else if (p.sb_vec && sb_col + VEC <= p.N) {
+                    if constexpr (VEC == 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(at);
+                        b[0] = v.x; b[1] = v.y; b[2] = v.z; b[3] = v.w;
+                    } else {
+                        const float2 v = *reinterpret_cast<const float2 *>(at);
+                        b[0] = v.x; b[1] = v.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) b[j] = sb_col + j < p.N ? at[j * p.sb_row] : 0.f;
+                }
+            };
             if constexpr (B_ROWS) {
                 if (lane == 0) bulk_wait_read0();
-                named_bar_sync(1 + half, 128);
-                sb = p.sb + static_cast<long long>(fetch ? sb_col : 0) * p.KB;
+                __syncwarp();
             }
             // scales of the next two k blocks
-            float a0 = sa[kb0], b0 = sb[kb0], a1 = 0.f, b1 = 0.f;
+            float a0 = sa[kb0 * sak], a1 = 0.f, b0[VEC], b1[VEC];
+            load_sb(b0, kb0);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) b1[j] = 0.f;
             if (kb0 + 1 < kb1) {
-                a1 = sa[kb0 + 1];
-                b1 = sb[kb0 + 1];
+                a1 = sa[(kb0 + 1) * sak];
+                load_sb(b1, kb0 + 1);
             }
             float2 acc[COLS / 2];
 #pragma unroll
@@ -523,19 +640,24 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             for (int kb = kb0; kb < kb1; ++kb) {
                 float s = a0;
                 if constexpr (B_ROWS) {
-                    // (the other half of sb_smem may still be in use by a slower warp)
-                    if ((threadIdx.x & 127) < COLS) sb_smem[par * COLS + (threadIdx.x & 127)] = b0;
+                    // (the other k block's half may still be in use by a slower lane)
+                    if constexpr (VEC == 4)
+                        *reinterpret_cast<float4 *>(sb_smem + par * COLS + lane * 4) =
+                            make_float4(b0[0], b0[1], b0[2], b0[3]);
+                    else
+                        *reinterpret_cast<float2 *>(sb_smem + par * COLS + lane * 2) = make_float2(b0[0], b0[1]);
+                    __syncwarp();
                 } else {
-                    s *= b0;
+                    s *= b0[0];
                 }
                 a0 = a1;
-                b0 = b1;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) b0[j] = b1[j];
                 if (kb + 2 < kb1) {
-                    a1 = sa[kb + 2];
-                    b1 = sb[kb + 2];
+                    a1 = sa[(kb + 2) * sak];
+                    load_sb(b1, kb + 2);
                 }
                 ok = mbar_wait(&tfull_bar[buf], bphase, ab);
-                if constexpr (B_ROWS) ok = named_bar_and(1 + half, 128, ok);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
@@ -592,7 +714,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                 par ^= 1;
             }
             if (!ok) break;
-            if constexpr (B_ROWS) named_bar_sync(1 + half, 128);   // the scales have been read
+            if constexpr (B_ROWS) __syncwarp();   // the scales have been read
             if (!PAIR && csize > 1) {
                 // one tile per cluster: the stages are free (all copies landed, all MMAs done); the
                 // partial sums as 128 x 128 fp32, 16-byte chunk j of row r at j ^ (r % 8)

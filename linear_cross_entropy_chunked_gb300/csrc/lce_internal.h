@@ -301,10 +301,10 @@ struct Fp8QuantParams {
     int vec;                   // rows are 16-byte aligned
     uint8_t *q;                // [R][ldq] or null
     long long ldq;
-    float *scale;              // [R][cblocks] (rows) or [rblocks][cblocks] (tiles)
+    float *scale;              // [cblocks][R] (rows) or [rblocks][cblocks] (tiles)
     uint8_t *qt;               // X^T: [C][ldqt] or null
     long long ldqt;
-    float *scale_t;            // [C][rblocks] or [cblocks][rblocks]
+    float *scale_t;            // [rblocks][C] or [cblocks][rblocks]
 };
 struct Fp8GemmParams {
     CUtensorMap tmA, tmB, tmC;
@@ -312,8 +312,11 @@ struct Fp8GemmParams {
     int n_bulk;                // columns that tmC stores: N less what does not fill 16 bytes
     int m_tiles, n_tiles, tiles;
     int a_box_rows;            // rows of A's load box
-    const float *sa;           // [M][KB]
-    const float *sb;           // [N][KB] or [N / 128][KB]
+    int stages;                // of the pipeline (one CTA per tile)
+    const float *sa;           // of A's row m and block b: sa[m * sa_row + b * sa_block]
+    const float *sb;           // of B's row (or 128 rows) n and block b
+    long long sa_row, sa_block, sb_row, sb_block;
+    int sb_vec;                // scales of consecutive rows of B lie side by side, 16-byte aligned
     void *C;
     long long ldc;
     int c_type;                // CE_BF16, CE_FP32 or CE_FP16

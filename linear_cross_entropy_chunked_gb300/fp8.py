@@ -3,7 +3,8 @@ the contraction): lce_fp8_quantize and lce_fp8_matmul. Argument marshalling only
 
 An operand is a pair (q, scale): q [R, C] float8_e4m3fn with a row stride that is a
 multiple of 16, scale fp32 [R, ceil(C / 128)] (row blocks: activations, gradients) or
-[ceil(R / 128), ceil(C / 128)] (tiles: weights)."""
+[ceil(R / 128), ceil(C / 128)] (tiles: weights), with any strides (row blocks come from
+quantize_fp8 stored block by block: the product reads those of consecutive rows at once)."""
 from __future__ import annotations
 
 from typing import NamedTuple, Optional
@@ -50,8 +51,11 @@ def _operand(R, C, tiles, dev):
     """(q [R, C] with padded rows, scale) for an operand of that shape."""
     ld = _pad16(C)
     q = torch.empty((R, ld), dtype=torch.float8_e4m3fn, device=dev)
-    return (q if ld == C else q[:, :C],
-            torch.empty((_blocks(R) if tiles else R, _blocks(C)), dtype=torch.float32, device=dev))
+    if tiles:
+        scale = torch.empty((_blocks(R), _blocks(C)), dtype=torch.float32, device=dev)
+    else:   # stored block by block
+        scale = torch.empty((_blocks(C), R), dtype=torch.float32, device=dev).t()
+    return q if ld == C else q[:, :C], scale
 
 
 def _quantize(X, tiles, own, transposed, s):
@@ -105,8 +109,8 @@ def _check_operand(name, q, scale, rows_only):
     if q.data_ptr() % 16:
         raise ValueError(f"{name} must start on a 16-byte boundary")
     R, KB = q.shape[0], _blocks(q.shape[1])
-    if scale.dtype != torch.float32 or scale.device != q.device or not scale.is_contiguous():
-        raise ValueError(f"{name}'s scale must be a contiguous float32 tensor on its device")
+    if scale.dtype != torch.float32 or scale.device != q.device:
+        raise ValueError(f"{name}'s scale must be a float32 tensor on its device")
     rows = scale.shape == (R, KB)
     if not rows and (rows_only or scale.shape != (_blocks(R), KB)):
         raise ValueError(f"{name}'s scale must be [{R}, {KB}] (rows)" +
@@ -121,10 +125,10 @@ def _matmul(a, a_scale, lda, b, b_scale, ldb, b_rows, out, ws, s):
     ldc = out.stride(0) if M > 1 else -(-N // 8) * 8
     if ws is None:
         ws = torch.empty(_WS_BYTES, dtype=torch.uint8, device=a.device)
-    _b._check(_b.lib().lce_fp8_matmul(a.data_ptr(), lda, a_scale.data_ptr(), b.data_ptr(), ldb,
-                                      b_scale.data_ptr(), 1 if b_rows else 0, M, N, K, out.data_ptr(), ldc,
-                                      _b._CE_DTYPES[out.dtype], ws.data_ptr(), ws.numel(), s),
-              "lce_fp8_matmul")
+    _b._check(_b.lib().lce_fp8_matmul(a.data_ptr(), lda, a_scale.data_ptr(), *a_scale.stride(), b.data_ptr(),
+                                      ldb, b_scale.data_ptr(), *b_scale.stride(), 1 if b_rows else 0, M, N, K,
+                                      out.data_ptr(), ldc, _b._CE_DTYPES[out.dtype], ws.data_ptr(), ws.numel(),
+                                      s), "lce_fp8_matmul")
     return out
 
 
