@@ -395,10 +395,13 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     constexpr int BNT = PAIR ? 256 : 128;
     constexpr int NBUF = TMEM_COLS / BNT;      // partial products in flight
     constexpr int COLS = BNT / 2;              // columns per consumer warp
+    static_assert(F8_STAGES >= NBUF, "a stage's phase must outlive its TMEM buffer");
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[F8_MAX_STAGES];
-    __shared__ __align__(8) uint64_t empty_bar[F8_MAX_STAGES];
-    __shared__ __align__(8) uint64_t tfull_bar[NBUF];
+    // the MMAs of a stage have ended: the producer may fill it again, and the consumers may read
+    // its TMEM buffer (one commit for both; a stage comes around no sooner than its buffer, which
+    // the consumers have released by then, so no phase can be missed)
+    __shared__ __align__(8) uint64_t done_bar[F8_MAX_STAGES];
     __shared__ __align__(8) uint64_t tempty_bar[NBUF];
     __shared__ __align__(8) uint64_t drain_bar;
     __shared__ uint32_t tmem_slot;
@@ -425,12 +428,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < nstages; ++s) {
             mbar_init(&full_bar[s], 1);
-            mbar_init(&empty_bar[s], 1);
+            mbar_init(&done_bar[s], 1);
         }
-        for (int b = 0; b < NBUF; ++b) {
-            mbar_init(&tfull_bar[b], 1);
-            mbar_init(&tempty_bar[b], CL * NUM_EPI_WARPS);
-        }
+        for (int b = 0; b < NBUF; ++b) mbar_init(&tempty_bar[b], CL * NUM_EPI_WARPS);
         mbar_init(&drain_bar, 1);
         abort_flag = 0;
         // cleared here, long before the first wait of any CTA can run out
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                 const int ya = mt * (CL * 128) + static_cast<int>(crank) * 128;
                 const int yb = nt * BNT + static_cast<int>(crank) * 128;
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(&empty_bar[stage], phase ^ 1, ab)) {
+                    if (!mbar_wait(&done_bar[stage], phase ^ 1, ab)) {
                         ok = false;
                         break;
                     }
@@ -547,13 +547,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                         for (int k = 0; k < 4; ++k)   // 32 values (bytes) of k per MMA
                             umma_e4m3<PAIR>(d, ad + static_cast<uint64_t>(k * 2),
                                             bd + static_cast<uint64_t>(k * 2), idesc, k != 0 ? 1u : 0u);
-                        if constexpr (PAIR) {
-                            umma_commit_pair(&tfull_bar[buf], both);
-                            umma_commit_pair(&empty_bar[stage], both);
-                        } else {
-                            umma_commit(&tfull_bar[buf]);
-                            umma_commit(&empty_bar[stage]);
-                        }
+                        if constexpr (PAIR) umma_commit_pair(&done_bar[stage], both);
+                        else umma_commit(&done_bar[stage]);
                     }
                     __syncwarp();
                     any_mma = true;
@@ -586,8 +581,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         // between a tile's store and the next one's)
         float *sb_smem = reinterpret_cast<float *>(box);
         const uint32_t tempty_addr = map_to_rank(&tempty_bar[0], PAIR ? 0u : rank);
-        int buf = 0;
-        uint32_t bphase = 0;
+        int buf = 0, stage = 0;
+        uint32_t phase = 0;
         int par = 0;
         bool ok = true;
         for (int t = cid; ok && t < p.tiles; t += ncl) {
@@ -657,7 +652,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                     a1 = sa[(kb + 2) * sak];
                     load_sb(b1, kb + 2);
                 }
-                ok = mbar_wait(&tfull_bar[buf], bphase, ab);
+                ok = mbar_wait(&done_bar[stage], phase, ab);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
@@ -707,9 +702,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                 } else {
                     release();
                 }
-                if (++buf == NBUF) {
-                    buf = 0;
-                    bphase ^= 1;
+                if (++buf == NBUF) buf = 0;
+                if (++stage == nstages) {
+                    stage = 0;
+                    phase ^= 1;
                 }
                 par ^= 1;
             }
