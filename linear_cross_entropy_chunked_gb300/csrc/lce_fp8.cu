@@ -318,7 +318,10 @@ cudaError_t launch_fp8_quantize(const Fp8QuantParams &p, int dtype, bool tile, c
 // each; few tiles are split along k over a cluster of up to 8 CTAs, whose fp32 sums are
 // added through distributed shared memory in rank order.
 // B_ROWS: B's scales are per row (gradient of a weight); every warp brings those of its
-// columns into shared memory of its own.
+// columns into shared memory of its own. With a whole row of 128 columns per thread, as
+// the tiles' path has it, every thread would read all 128 scales per k block: 512 bytes per warp
+// and load, 1024 cycles of the shared memory's return path for the CTA. So TMEM is read in the
+// layout of matrix fragments: a thread holds 4 rows x 32 columns and reads a quarter of the scales.
 // Every mbarrier wait is bounded, as in the bf16 GEMM. The waits for TMEM buffers acquire at
 // CTA scope and their remote arrivals are relaxed: no memory is handed over with them (the
 // tcgen05 fences order TMEM), and cluster scope costs a flush or an L1 invalidation per
@@ -591,9 +594,18 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             const int row0 = mt * (CL * 128) + static_cast<int>(crank) * 128 + quarter * 32;
             const int col0 = nt * BNT + half * COLS;
             const bool active = row0 < p.M && col0 < p.N;   // warp-uniform: some output of this warp exists
-            const int row = row0 + lane;
+            // rows of this thread: one, or (fragments) four, 8 apart
+            constexpr int ROWS = B_ROWS ? 4 : 1;
+            const int row = row0 + (B_ROWS ? lane / 4 : lane);
             const float *sa = p.sa + static_cast<long long>(row < p.M ? row : 0) * p.sa_row;
-            const long long sak = p.sa_block, sbk = p.sb_block;
+            auto load_sa = [&](float (&a)[ROWS], int kb) {
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i)   // (four pointers would be kept in registers that are not there)
+                    a[i] = B_ROWS ? p.sa[static_cast<long long>(row + 8 * i < p.M ? row + 8 * i : 0) * p.sa_row +
+                                         kb * p.sa_block]
+                                  : sa[kb * p.sa_block];
+            };
+            const long long sbk = p.sb_block;
             // tile scales: the warp's columns lie in one block of 128; row scales: VEC columns per lane
             constexpr int VEC = COLS / 32;
             const int sb_col = col0 + lane * VEC;
@@ -620,20 +632,24 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                 if (lane == 0) bulk_wait_read0();
                 __syncwarp();
             }
-            // scales of the next two k blocks
-            float a0 = sa[kb0 * sak], a1 = 0.f, b0[VEC], b1[VEC];
+            // scales of the next k block, and (where registers allow) of the one after it
+            constexpr int AHEAD = B_ROWS ? 1 : 2;
+            float a0[ROWS], a1[ROWS], b0[VEC], b1[VEC];
+            load_sa(a0, kb0);
             load_sb(b0, kb0);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) b1[j] = 0.f;
-            if (kb0 + 1 < kb1) {
-                a1 = sa[(kb0 + 1) * sak];
+            if (AHEAD > 1 && kb0 + 1 < kb1) {
+                load_sa(a1, kb0 + 1);
                 load_sb(b1, kb0 + 1);
             }
+            // the thread's sums: columns 2 j and 2 j + 1 of its row, or (fragments) of group g of 8
+            // columns and row i: acc[4 g + i]
             float2 acc[COLS / 2];
 #pragma unroll
             for (int j = 0; j < COLS / 2; ++j) acc[j] = make_float2(0.f, 0.f);
             for (int kb = kb0; kb < kb1; ++kb) {
-                float s = a0;
+                float s[ROWS];
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i) s[i] = a0[i];
                 if constexpr (B_ROWS) {
                     // (the other k block's half may still be in use by a slower lane)
                     if constexpr (VEC == 4)
@@ -643,14 +659,17 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                         *reinterpret_cast<float2 *>(sb_smem + par * COLS + lane * 2) = make_float2(b0[0], b0[1]);
                     __syncwarp();
                 } else {
-                    s *= b0[0];
+                    s[0] *= b0[0];
                 }
-                a0 = a1;
+                if constexpr (AHEAD > 1) {
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) b0[j] = b1[j];
-                if (kb + 2 < kb1) {
-                    a1 = sa[(kb + 2) * sak];
-                    load_sb(b1, kb + 2);
+                    for (int i = 0; i < ROWS; ++i) a0[i] = a1[i];
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) b0[j] = b1[j];
+                }
+                if (kb + AHEAD < kb1) {
+                    load_sa(AHEAD > 1 ? a1 : a0, kb + AHEAD);
+                    load_sb(AHEAD > 1 ? b1 : b0, kb + AHEAD);
                 }
                 ok = mbar_wait(&done_bar[stage], phase, ab);
                 if (!__all_sync(0xffffffffu, ok)) {
@@ -666,38 +685,52 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                     tc_fence_after();
                     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                            static_cast<uint32_t>(buf * BNT + half * COLS);
-                    const float2 s2 = make_float2(s, s);
-                    uint32_t v[2][16];   // the load of 16 columns runs beside the arithmetic on the last 16
-                    tmem_ld16_start(taddr, v[0]);
-                    tmem_ld16_wait(v[0]);
+                    // (each load runs beside the arithmetic on the last one)
+                    uint32_t v[2][16];
+                    if constexpr (B_ROWS) {
+                        // loads: 32 columns of rows 0-15, then of rows 16-31 of the quarter
+                        constexpr int LOADS = COLS / 16;
+                        tmem_ldfrag_start(taddr, v[0]);
+                        tmem_ld16_wait(v[0]);
 #pragma unroll
-                    for (int c = 0; c < COLS / 16; ++c) {
-                        if (c + 1 < COLS / 16) {
-                            tmem_ld16_start(taddr + (c + 1) * 16, v[(c + 1) & 1]);
-                        } else {
-                            release();   // everything is in registers
-                        }
-                        const uint32_t(&u)[16] = v[c & 1];
-                        if constexpr (B_ROWS) {
-                            const float4 *b4 = reinterpret_cast<const float4 *>(sb_smem + par * COLS + c * 16);
+                        for (int c = 0; c < LOADS; ++c) {
+                            if (c + 1 < LOADS)
+                                tmem_ldfrag_start(taddr + ((c + 1) / 2) * 32 + ((c + 1) % 2) * (16u << 16), v[(c + 1) & 1]);
+                            else
+                                release();   // everything is in registers
+                            const uint32_t(&u)[16] = v[c & 1];
+                            const int i0 = (c % 2) * 2;   // rows i0 and i0 + 1 of the thread
+                            const float2 sa0 = make_float2(s[i0], s[i0]), sa1 = make_float2(s[i0 + 1], s[i0 + 1]);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float4 b = b4[j];
-                                float2 &x = acc[c * 8 + 2 * j], &y = acc[c * 8 + 2 * j + 1];
-                                x = __ffma2_rn(make_float2(__uint_as_float(u[4 * j]), __uint_as_float(u[4 * j + 1])),
-                                               __fmul2_rn(s2, make_float2(b.x, b.y)), x);
+                            for (int q = 0; q < 4; ++q) {
+                                const int g = (c / 2) * 4 + q;
+                                const float2 b = *reinterpret_cast<const float2 *>(sb_smem + par * COLS + g * 8 +
+                                                                                   (lane & 3) * 2);
+                                float2 &x = acc[4 * g + i0], &y = acc[4 * g + i0 + 1];
+                                x = __ffma2_rn(make_float2(__uint_as_float(u[4 * q]), __uint_as_float(u[4 * q + 1])),
+                                               __fmul2_rn(sa0, b), x);
                                 y = __ffma2_rn(
-                                    make_float2(__uint_as_float(u[4 * j + 2]), __uint_as_float(u[4 * j + 3])),
-                                    __fmul2_rn(s2, make_float2(b.z, b.w)), y);
+                                    make_float2(__uint_as_float(u[4 * q + 2]), __uint_as_float(u[4 * q + 3])),
+                                    __fmul2_rn(sa1, b), y);
                             }
-                        } else {
+                            if (c + 1 < LOADS) tmem_ld16_wait(v[(c + 1) & 1]);
+                        }
+                    } else {
+                        const float2 s2 = make_float2(s[0], s[0]);
+                        tmem_ld16_start(taddr, v[0]);
+                        tmem_ld16_wait(v[0]);
+#pragma unroll
+                        for (int c = 0; c < COLS / 16; ++c) {
+                            if (c + 1 < COLS / 16) tmem_ld16_start(taddr + (c + 1) * 16, v[(c + 1) & 1]);
+                            else release();   // everything is in registers
+                            const uint32_t(&u)[16] = v[c & 1];
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
                                 acc[c * 8 + j] = __ffma2_rn(
                                     make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1])), s2,
                                     acc[c * 8 + j]);
+                            if (c + 1 < COLS / 16) tmem_ld16_wait(v[(c + 1) & 1]);
                         }
-                        if (c + 1 < COLS / 16) tmem_ld16_wait(v[(c + 1) & 1]);
                     }
                 } else {
                     release();
@@ -714,12 +747,23 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             if (!PAIR && csize > 1) {
                 // one tile per cluster: the stages are free (all copies landed, all MMAs done); the
                 // partial sums as 128 x 128 fp32, 16-byte chunk j of row r at j ^ (r % 8)
-                const int r = quarter * 32 + lane;
-                float *dst = reinterpret_cast<float *>(smem) + r * 128;
+                if constexpr (B_ROWS) {
 #pragma unroll
-                for (int j = 0; j < COLS / 4; ++j)
-                    *reinterpret_cast<float4 *>(dst + (((half * (COLS / 4) + j) ^ (r & 7)) << 2)) =
-                        make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y);
+                    for (int g = 0; g < COLS / 8; ++g)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = quarter * 32 + lane / 4 + 8 * i, col = half * COLS + g * 8 + (lane & 3) * 2;
+                            *reinterpret_cast<float2 *>(reinterpret_cast<float *>(smem) + r * 128 +
+                                                        (((col >> 2) ^ (r & 7)) << 2) + (col & 2)) = acc[4 * g + i];
+                        }
+                } else {
+                    const int r = quarter * 32 + lane;
+                    float *dst = reinterpret_cast<float *>(smem) + r * 128;
+#pragma unroll
+                    for (int j = 0; j < COLS / 4; ++j)
+                        *reinterpret_cast<float4 *>(dst + (((half * (COLS / 4) + j) ^ (r & 7)) << 2)) =
+                            make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y);
+                }
                 break;
             }
             if (active) {
@@ -727,27 +771,30 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                 const int per = p.c_type == CE_FP32 ? 32 : 64;
 #pragma unroll
                 for (int c = 0; c < COLS / 32; ++c) {
-                    // a bulk store writes whole 16-byte pieces of a row: what N leaves in its last
-                    // piece is stored value by value
-                    const int tail0 = p.n_bulk - (col0 + c * 32), tail1 = p.N - (col0 + c * 32);
-                    if (tail0 < 32 && tail1 > 0 && tail0 < tail1 && row < p.M) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            if (j < tail0 || j >= tail1) continue;
-                            const float a = (j & 1) ? acc[c * 16 + j / 2].y : acc[c * 16 + j / 2].x;
-                            const long long o = row * p.ldc + col0 + c * 32 + j;
-                            if (p.c_type == CE_FP32) static_cast<float *>(p.C)[o] = a;
-                            else if (p.c_type == CE_FP16) static_cast<__half *>(p.C)[o] = __float2half_rn(a);
-                            else static_cast<__nv_bfloat16 *>(p.C)[o] = __float2bfloat16_rn(a);
-                        }
-                    }
-                    if (col0 + c * 32 / per * per >= p.n_bulk) continue;
+                    const int bx = col0 + c * 32 / per * per;   // the box's first column
+                    if (bx >= p.N) continue;
                     const bool first = c * 32 % per == 0, last = (c * 32 + 32) % per == 0;
                     if (first) {
                         if (lane == 0) bulk_wait_read0();
                         __syncwarp();
                     }
-                    if (p.c_type == CE_FP32) {
+                    if constexpr (B_ROWS) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int r = lane / 4 + 8 * i;
+                                const float2 a = acc[c * 16 + 4 * q + i];
+                                if (p.c_type == CE_FP32) {
+                                    const int j = 2 * q + ((lane & 3) >> 1);
+                                    *reinterpret_cast<float2 *>(box + r * 128 + ((j ^ (r & 7)) << 4) + (lane & 1) * 8) = a;
+                                } else {
+                                    const int j = (c & 1) * 4 + q;
+                                    *reinterpret_cast<uint32_t *>(box + r * 128 + ((j ^ (r & 7)) << 4) + (lane & 3) * 4) =
+                                        p.c_type == CE_FP16 ? pack_f16x2(a.x, a.y) : pack_bf16x2(a.x, a.y);
+                                }
+                            }
+                    } else if (p.c_type == CE_FP32) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             *reinterpret_cast<float4 *>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
@@ -770,9 +817,21 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                     if (last) {
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) {
-                            tma_store_2d(&p.tmC, box, col0 + c * 32 / per * per, row0);
+                        if (lane == 0 && bx < p.n_bulk) {
+                            tma_store_2d(&p.tmC, box, bx, row0);
                             bulk_commit();
+                        }
+                        // a bulk store writes whole 16-byte pieces of a row: what N leaves in its last
+                        // piece is copied value by value
+                        if (p.n_bulk < p.N && bx + per > p.n_bulk && row0 + lane < p.M) {
+                            const int elem = p.c_type == CE_FP32 ? 4 : 2;
+                            for (int col = max(bx, p.n_bulk); col < min(p.N, bx + per); ++col) {
+                                const int o = (col - bx) * elem;
+                                const uint8_t *from = box + lane * 128 + (((o >> 4) ^ (lane & 7)) << 4) + (o & 15);
+                                uint8_t *to = static_cast<uint8_t *>(p.C) + ((row0 + lane) * p.ldc + col) * elem;
+                                if (elem == 4) *reinterpret_cast<uint32_t *>(to) = *reinterpret_cast<const uint32_t *>(from);
+                                else *reinterpret_cast<uint16_t *>(to) = *reinterpret_cast<const uint16_t *>(from);
+                            }
                         }
                     }
                 }

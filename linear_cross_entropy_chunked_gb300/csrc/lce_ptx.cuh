@@ -252,6 +252,18 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
                  : "memory");
 }
 
+// 16 TMEM lanes x 32 columns in the layout of matrix fragments: of the 8-column group g,
+// r[4 g] and r[4 g + 1] are columns 2 (lane % 4) and the next of row lane / 4, r[4 g + 2] and
+// r[4 g + 3] the same of row lane / 4 + 8.
+__device__ __forceinline__ void tmem_ldfrag_start(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&h);
