@@ -300,6 +300,15 @@ lce_status lce_fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t s
                           int64_t K, void *out, int64_t ldc, int c_dtype, void *ws, size_t ws_bytes,
                           lce_stream_t stream);
 
+/* Both in one call: out = X W^T for X [M][ldx] (x_dtype, K columns), which is quantised to row
+ * blocks in the workspace, and W [N][ldw] in tiles; the rest as for lce_fp8_matmul.
+ * Workspace: lce_fp8_linear_workspace_size(M, K) bytes, 16-byte aligned. */
+lce_status lce_fp8_linear_workspace_size(int64_t M, int64_t K, size_t *bytes);
+lce_status lce_fp8_linear(const void *X, int x_dtype, int64_t ldx, const void *W, int64_t ldw,
+                          const float *sw, int64_t sw_row, int64_t sw_block, int64_t M, int64_t N,
+                          int64_t K, void *out, int64_t ldc, int c_dtype, void *ws, size_t ws_bytes,
+                          lce_stream_t stream);
+
 /* The global norm of a list of n gradients and clipping by it:
  *   norm = (sum over all tensors of |g|^p)^(1/p) for p = 2 or 1, or max |g|
  *   out = g * min(1, max_norm / (norm + eps))

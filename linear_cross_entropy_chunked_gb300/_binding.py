@@ -59,6 +59,8 @@ EXPORTED = (
     "lce_fp8_quantize",
     "lce_fp8_matmul_workspace_size",
     "lce_fp8_matmul",
+    "lce_fp8_linear_workspace_size",
+    "lce_fp8_linear",
     "lce_grad_norm_workspace_size",
     "lce_grad_norm",
     "lce_clip_grad_norm",
@@ -155,6 +157,9 @@ def lib() -> ctypes.CDLL:
     L.lce_fp8_matmul_workspace_size.argtypes = [_sz]
     L.lce_fp8_matmul.argtypes = [_vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, ctypes.c_int,
                                  _i64, _i64, _i64, _vp, _i64, ctypes.c_int, _vp, ctypes.c_size_t, _vp]
+    L.lce_fp8_linear_workspace_size.argtypes = [_i64, _i64, _sz]
+    L.lce_fp8_linear.argtypes = [_vp, ctypes.c_int, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _vp,
+                                 _i64, ctypes.c_int, _vp, ctypes.c_size_t, _vp]
     L.lce_grad_norm_workspace_size.argtypes = [_i64, _sz]
     L.lce_grad_norm.argtypes = [_vp, _vp, _vp, _i64, ctypes.c_int, _vp, _vp, ctypes.c_size_t, _vp]
     L.lce_clip_grad_norm.argtypes = [_vp, _vp, _vp, _vp, _i64, ctypes.c_int, _f, _f, _vp, _vp,
@@ -182,7 +187,7 @@ def lib() -> ctypes.CDLL:
                  "lce_fwd_bwd_sharded", "lce_noalloc_read_status", "lce_forward_noalloc",
                  "lce_sample_logits", "lce_grad_norm_workspace_size", "lce_grad_norm",
                  "lce_clip_grad_norm", "lce_fp8_quantize", "lce_fp8_matmul_workspace_size",
-                 "lce_fp8_matmul"):
+                 "lce_fp8_matmul", "lce_fp8_linear_workspace_size", "lce_fp8_linear"):
         getattr(L, name).restype = ctypes.c_int
     _LIB = L
     return L

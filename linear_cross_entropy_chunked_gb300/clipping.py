@@ -5,6 +5,7 @@ from __future__ import annotations
 import ctypes
 import math
 import operator
+from array import array
 
 import torch
 
@@ -38,15 +39,16 @@ def _tensors(grads, what):
         if -1 in devices:
             raise ValueError(f"{what} must be CUDA tensors (there is no CPU path)")
         raise ValueError(f"{what} must be on one device")
-    dtypes = list(map(_dtype, grads))
-    for dt in set(dtypes):
-        if dt not in _b._CE_DTYPES:
-            raise TypeError(f"{what} must be bfloat16, float16 or float32")
+    codes = _b._CE_DTYPES
+    dtypes = set(map(_dtype, grads))
+    if not dtypes <= codes.keys():
+        raise TypeError(f"{what} must be bfloat16, float16 or float32")
     plain = all(map(T.is_contiguous, grads))
     if not plain and not all(map(_dense, grads)):
         raise ValueError(f"{what} must fill their memory (contiguous or permuted, no gaps)")
-    return (grads, grads[0].device, plain, list(map(T.data_ptr, grads)), list(map(T.numel, grads)),
-            list(map(_b._CE_DTYPES.__getitem__, dtypes)))
+    return (grads, grads[0].device, plain, array("Q", map(T.data_ptr, grads)), array("q", map(T.numel, grads)),
+            array("i", [codes[dtypes.pop()]]) * len(grads) if len(dtypes) == 1
+            else array("i", [codes[g.dtype] for g in grads]))
 
 
 def _kind(norm_type):
@@ -56,9 +58,9 @@ def _kind(norm_type):
     return kind
 
 
-def _arrays(ptrs, sizes, dtypes):
-    n = len(ptrs)
-    return (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*sizes), (ctypes.c_int32 * n)(*dtypes), n
+def _at(a):
+    """Address of an array's items (which must outlive the call)."""
+    return a.buffer_info()[0]
 
 
 def _workspace(n, ws, dev):
@@ -75,12 +77,12 @@ def grad_norm(grads, norm_type=2.0, ws=None, stream=None):
     """The norm (1, 2 or inf) over all values of the gradients, a tensor or a list of
     tensors (bf16, fp16 and fp32 may be mixed): a device fp32 scalar."""
     kind = _kind(norm_type)
-    _, dev, _, *lists = _tensors(grads, "grads")
-    src, sizes, dtypes, n = _arrays(*lists)
+    _, dev, _, ptrs, sizes, codes = _tensors(grads, "grads")
+    n = len(ptrs)
     with _b._on(dev, stream) as s:
         ws, ws_bytes = _workspace(n, ws, dev)
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        _b._check(_b.lib().lce_grad_norm(src, sizes, dtypes, n, kind, norm.data_ptr(), ws.data_ptr(),
+        _b._check(_b.lib().lce_grad_norm(_at(ptrs), _at(sizes), _at(codes), n, kind, norm.data_ptr(), ws.data_ptr(),
                                          ws_bytes, s), "lce_grad_norm")
     return norm
 
@@ -96,19 +98,19 @@ def clip_grad_norm(grads, max_norm, norm_type=2.0, eps=1e-6, out=None, ws=None, 
     max_norm, eps = float(max_norm), float(eps)
     if not max_norm >= 0.0 or not 0.0 <= eps < math.inf:
         raise ValueError("max_norm must not be negative, and eps finite and not negative")
-    grads, dev, plain, ptrs, counts, codes = _tensors(grads, "grads")
-    src, sizes, dtypes, n = _arrays(ptrs, counts, codes)
+    grads, dev, plain, ptrs, sizes, codes = _tensors(grads, "grads")
+    n = len(ptrs)
     dst = None
     if out is not None:
-        out, out_dev, out_plain, out_ptrs, out_counts, out_codes = _tensors(out, "out")
-        if out_dev != dev or out_counts != counts or out_codes != codes or not (plain and out_plain or all(
+        out, out_dev, out_plain, out_ptrs, out_sizes, out_codes = _tensors(out, "out")
+        if out_dev != dev or out_sizes != sizes or out_codes != codes or not (plain and out_plain or all(
                 o.shape == g.shape and o.stride() == g.stride() for o, g in zip(out, grads))):
             raise ValueError("out must match the gradients in number, device, dtypes, sizes and layouts")
-        dst = (ctypes.c_void_p * n)(*out_ptrs)
+        dst = _at(out_ptrs)
     with _b._on(dev, stream) as s:
         ws, ws_bytes = _workspace(n, ws, dev)
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        _b._check(_b.lib().lce_clip_grad_norm(src, sizes, dtypes, dst, n, kind, max_norm, eps,
+        _b._check(_b.lib().lce_clip_grad_norm(_at(ptrs), _at(sizes), _at(codes), dst, n, kind, max_norm, eps,
                                               norm.data_ptr(), ws.data_ptr(), ws_bytes, s),
                   "lce_clip_grad_norm")
     return norm

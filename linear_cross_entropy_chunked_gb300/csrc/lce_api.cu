@@ -1103,6 +1103,83 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
     return LCE_OK;
 }
 
+// ---- 8-bit product
+lce_status fp8_matmul_check(const void *A, int64_t lda, const float *sa, int64_t sa_row, int64_t sa_block,
+                            const void *B, int64_t ldb, const float *sb, int64_t sb_row, int64_t sb_block,
+                            int64_t M, int64_t N, int64_t K, const void *out, int64_t ldc, int c_dtype,
+                            const void *ws, size_t ws_bytes) {
+    if (sa_row < 0 || sa_block < 0 || sb_row < 0 || sb_block < 0) return LCE_ERR_INVALID_ARG;
+    if (M < 0 || N < 0 || K <= 0 || M > MAX_V || N > MAX_V || K > MAX_V) return LCE_ERR_INVALID_ARG;
+    if (lda < K || ldb < K || ldc < N || c_dtype < CE_BF16 || c_dtype > CE_FP16 || !ws)
+        return LCE_ERR_INVALID_ARG;
+    if (M > 0 && N > 0 && (!A || !sa || !B || !sb || !out)) return LCE_ERR_INVALID_ARG;
+    const int64_t elem = c_dtype == CE_FP32 ? 4 : 2;
+    if (!aligned16(A) || !aligned16(B) || !aligned16(out) || !aligned16(ws) || lda % 16 || ldb % 16 ||
+        (ldc * elem) % 16 || reinterpret_cast<uintptr_t>(sa) % 4 || reinterpret_cast<uintptr_t>(sb) % 4)
+        return LCE_ERR_ALIGNMENT;
+    if (ws_bytes < 1024) return LCE_ERR_WORKSPACE;
+    return LCE_OK;
+}
+
+// after_quantize: A comes from the quantisation launched just before on the same stream,
+// which the product's prologue may overlap
+lce_status fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t sa_row, int64_t sa_block,
+                      const void *B, int64_t ldb, const float *sb, int64_t sb_row, int64_t sb_block,
+                      int b_rows, int64_t M, int64_t N, int64_t K, void *out, int64_t ldc, int c_dtype,
+                      void *ws, size_t ws_bytes, bool after_quantize, lce_stream_t stream) {
+    lce_status st = fp8_matmul_check(A, lda, sa, sa_row, sa_block, B, ldb, sb, sb_row, sb_block, M, N, K, out, ldc,
+                                     c_dtype, ws, ws_bytes);
+    if (st != LCE_OK) return st;
+    const int64_t elem = c_dtype == CE_FP32 ? 4 : 2;
+    int sms = 0, pairs = 0;
+    st = init_device(&sms, &pairs);
+    if (st != LCE_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (M == 0 || N == 0)
+        return cudaMemsetAsync(ws, 0, sizeof(int), s) == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
+
+    Fp8GemmParams p;
+    memset(&p, 0, sizeof(p));
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.KB = static_cast<int>(cdiv(K, 128));
+    const long long pair_tiles = cdiv(M, 256) * cdiv(N, 256), tiles = cdiv(M, 128) * cdiv(N, 128);
+    const bool pair = M > 128 && pairs > 0 && pair_tiles >= pairs / 2;
+    if (tiles > 0x7fffffffll) return LCE_ERR_INVALID_ARG;
+    int split = 1;
+    if (!pair)
+        while (split < 8 && tiles * split * 2 <= sms && p.KB >= split * 4) split *= 2;
+    p.m_tiles = static_cast<int>(pair ? cdiv(M, 256) : cdiv(M, 128));
+    p.n_tiles = static_cast<int>(pair ? cdiv(N, 256) : cdiv(N, 128));
+    p.tiles = static_cast<int>(pair ? pair_tiles : tiles);
+    p.a_box_rows = pair || M >= 128 ? 128 : static_cast<int>(align_up(static_cast<size_t>(M), 8));
+    p.n_bulk = static_cast<int>(N / (16 / elem) * (16 / elem));
+    // what 192 KB hold of A's rows and 128 rows of B (a multiple of 1 KB each), as barriers allow
+    p.stages = std::min(11, 6 * 32768 / (p.a_box_rows * 128 + 16384));
+    p.sa = sa;
+    p.sb = sb;
+    p.sa_row = sa_row;
+    p.sa_block = sa_block;
+    p.sb_row = sb_row;
+    p.sb_block = sb_block;
+    p.sb_vec = sb_row == 1 && sb_block % 4 == 0 && aligned16(sb) ? 1 : 0;
+    p.C = out;
+    p.ldc = ldc;
+    p.c_type = c_dtype;
+    p.hdr = static_cast<int *>(ws);
+    p.timeout_ns = kDefaultTimeoutNs;
+    const MapType ct = c_dtype == CE_FP32 ? MAP_F32 : c_dtype == CE_FP16 ? MAP_F16 : MAP_BF16;
+    if (!encode_2d(&p.tmA, A, K, M, lda, 128, p.a_box_rows, MAP_U8) ||
+        !encode_2d(&p.tmB, B, K, N, ldb, 128, 128, MAP_U8) ||
+        (p.n_bulk > 0 && !encode_store_2d(&p.tmC, out, p.n_bulk, M, ldc * elem, ct, 32)))
+        return LCE_ERR_CUDA;
+    const int cluster = pair ? 2 : split;
+    const int most = pair ? pairs : split > 1 ? p.tiles : sms;
+    const int clusters = p.tiles < most ? p.tiles : most;
+    LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_fp8_matmul(p, pair, b_rows != 0, cluster, clusters, after_quantize, s));
+    return LCE_OK;
+}
+
 // ---- gradient norm and clipping
 constexpr int64_t kMaxGrads = 1 << 20;
 
@@ -1623,63 +1700,39 @@ lce_status lce_fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t s
                           int64_t K, void *out, int64_t ldc, int c_dtype, void *ws, size_t ws_bytes,
                           lce_stream_t stream) {
     g_launches = 0;
-    if (sa_row < 0 || sa_block < 0 || sb_row < 0 || sb_block < 0) return LCE_ERR_INVALID_ARG;
-    if (M < 0 || N < 0 || K <= 0 || M > MAX_V || N > MAX_V || K > MAX_V) return LCE_ERR_INVALID_ARG;
-    if (lda < K || ldb < K || ldc < N || c_dtype < CE_BF16 || c_dtype > CE_FP16 || !ws)
-        return LCE_ERR_INVALID_ARG;
-    if (M > 0 && N > 0 && (!A || !sa || !B || !sb || !out)) return LCE_ERR_INVALID_ARG;
-    const int64_t elem = c_dtype == CE_FP32 ? 4 : 2;
-    if (!aligned16(A) || !aligned16(B) || !aligned16(out) || !aligned16(ws) || lda % 16 || ldb % 16 ||
-        (ldc * elem) % 16 || reinterpret_cast<uintptr_t>(sa) % 4 || reinterpret_cast<uintptr_t>(sb) % 4)
-        return LCE_ERR_ALIGNMENT;
-    if (ws_bytes < 1024) return LCE_ERR_WORKSPACE;
-    int sms = 0, pairs = 0;
-    lce_status st = init_device(&sms, &pairs);
-    if (st != LCE_OK) return st;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (M == 0 || N == 0)
-        return cudaMemsetAsync(ws, 0, sizeof(int), s) == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
+    return fp8_matmul(A, lda, sa, sa_row, sa_block, B, ldb, sb, sb_row, sb_block, b_rows, M, N, K, out,
+                      ldc, c_dtype, ws, ws_bytes, false, stream);
+}
 
-    Fp8GemmParams p;
-    memset(&p, 0, sizeof(p));
-    p.M = static_cast<int>(M);
-    p.N = static_cast<int>(N);
-    p.KB = static_cast<int>(cdiv(K, 128));
-    const long long pair_tiles = cdiv(M, 256) * cdiv(N, 256), tiles = cdiv(M, 128) * cdiv(N, 128);
-    const bool pair = M > 128 && pairs > 0 && pair_tiles >= pairs / 2;
-    if (tiles > 0x7fffffffll) return LCE_ERR_INVALID_ARG;
-    int split = 1;
-    if (!pair)
-        while (split < 8 && tiles * split * 2 <= sms && p.KB >= split * 4) split *= 2;
-    p.m_tiles = static_cast<int>(pair ? cdiv(M, 256) : cdiv(M, 128));
-    p.n_tiles = static_cast<int>(pair ? cdiv(N, 256) : cdiv(N, 128));
-    p.tiles = static_cast<int>(pair ? pair_tiles : tiles);
-    p.a_box_rows = pair || M >= 128 ? 128 : static_cast<int>(align_up(static_cast<size_t>(M), 8));
-    p.n_bulk = static_cast<int>(N / (16 / elem) * (16 / elem));
-    // what 192 KB hold of A's rows and 128 rows of B (a multiple of 1 KB each), as barriers allow
-    p.stages = std::min(11, 6 * 32768 / (p.a_box_rows * 128 + 16384));
-    p.sa = sa;
-    p.sb = sb;
-    p.sa_row = sa_row;
-    p.sa_block = sa_block;
-    p.sb_row = sb_row;
-    p.sb_block = sb_block;
-    p.sb_vec = sb_row == 1 && sb_block % 4 == 0 && aligned16(sb) ? 1 : 0;
-    p.C = out;
-    p.ldc = ldc;
-    p.c_type = c_dtype;
-    p.hdr = static_cast<int *>(ws);
-    p.timeout_ns = kDefaultTimeoutNs;
-    const MapType ct = c_dtype == CE_FP32 ? MAP_F32 : c_dtype == CE_FP16 ? MAP_F16 : MAP_BF16;
-    if (!encode_2d(&p.tmA, A, K, M, lda, 128, p.a_box_rows, MAP_U8) ||
-        !encode_2d(&p.tmB, B, K, N, ldb, 128, 128, MAP_U8) ||
-        (p.n_bulk > 0 && !encode_store_2d(&p.tmC, out, p.n_bulk, M, ldc * elem, ct, 32)))
-        return LCE_ERR_CUDA;
-    const int cluster = pair ? 2 : split;
-    const int most = pair ? pairs : split > 1 ? p.tiles : sms;
-    const int clusters = p.tiles < most ? p.tiles : most;
-    LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_fp8_matmul(p, pair, b_rows != 0, cluster, clusters, s));
+lce_status lce_fp8_linear_workspace_size(int64_t M, int64_t K, size_t *bytes) {
+    if (!bytes || M < 0 || K <= 0 || M > MAX_V || K > MAX_V) return LCE_ERR_INVALID_ARG;
+    *bytes = 1024 + align_up(sizeof(float) * static_cast<size_t>(M) * cdiv(K, 128), 1024) +
+             static_cast<size_t>(M) * align_up(static_cast<size_t>(K), 16);
     return LCE_OK;
+}
+
+lce_status lce_fp8_linear(const void *X, int x_dtype, int64_t ldx, const void *W, int64_t ldw,
+                          const float *sw, int64_t sw_row, int64_t sw_block, int64_t M, int64_t N,
+                          int64_t K, void *out, int64_t ldc, int c_dtype, void *ws, size_t ws_bytes,
+                          lce_stream_t stream) {
+    g_launches = 0;
+    size_t need = 0;
+    lce_status st = lce_fp8_linear_workspace_size(M, K, &need);
+    if (st != LCE_OK) return st;
+    if (!ws) return LCE_ERR_INVALID_ARG;
+    if (!aligned16(ws)) return LCE_ERR_ALIGNMENT;
+    if (ws_bytes < need) return LCE_ERR_WORKSPACE;
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    float *sx = reinterpret_cast<float *>(w + 1024);
+    uint8_t *xq = w + 1024 + align_up(sizeof(float) * static_cast<size_t>(M) * cdiv(K, 128), 1024);
+    const int64_t ldq = static_cast<int64_t>(align_up(static_cast<size_t>(K), 16));
+    // (the product's arguments are checked before the quantisation is enqueued)
+    st = fp8_matmul_check(xq, ldq, sx, 1, M, W, ldw, sw, sw_row, sw_block, M, N, K, out, ldc, c_dtype, ws, ws_bytes);
+    if (st != LCE_OK) return st;
+    st = lce_fp8_quantize(X, x_dtype, ldx, M, K, 0, xq, ldq, sx, nullptr, 0, nullptr, stream);
+    if (st != LCE_OK) return st;
+    return fp8_matmul(xq, ldq, sx, 1, M, W, ldw, sw, sw_row, sw_block, 0, M, N, K, out, ldc, c_dtype, ws,
+                      ws_bytes, M > 0, stream);
 }
 
 lce_status lce_grad_norm_workspace_size(int64_t n, size_t *bytes) {

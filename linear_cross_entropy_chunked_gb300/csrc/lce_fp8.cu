@@ -139,6 +139,8 @@ __global__ void __launch_bounds__(QT_THREADS, sizeof(T) == 4 ? 2 : 3)
     __shared__ float cred[QT_THREADS / 32][128];
     const int t = threadIdx.x, w = t >> 5, l = t & 31;
     const int i = t & 15, g = t >> 4;          // columns 8 i .. + 7, rows 8 g .. + 7 of the tile
+    // (a product launched to overlap may set itself up while this runs; it waits for the end)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long tile = blockIdx.x;
     const long long rb = tile / p.cblocks, cb = tile - rb * p.cblocks;
     const long long r0 = rb * 128, c0 = cb * 128;
@@ -436,8 +438,6 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         for (int b = 0; b < NBUF; ++b) mbar_init(&tempty_bar[b], CL * NUM_EPI_WARPS);
         mbar_init(&drain_bar, 1);
         abort_flag = 0;
-        // cleared here, long before the first wait of any CTA can run out
-        if (blockIdx.x == 0) *(volatile int *)(p.hdr + HDR_FLAG) = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == PRODUCER_WARP && lane == 0) {
@@ -465,6 +465,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     if constexpr (PAIR) cluster_sync_all();   // the peer's barriers exist from here on
     tc_fence_after();
     const uint32_t tmem_base = tmem_slot;
+    // what was launched before has ended (at once, unless its launch was allowed to overlap)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // cleared here, long before the first wait of any CTA can run out
+    if (blockIdx.x == 0 && threadIdx.x == 0) *(volatile int *)(p.hdr + HDR_FLAG) = 0;
 
     Abort ab;
     ab.flag_smem = &abort_flag;
@@ -923,8 +927,8 @@ cudaError_t fp8_set_attributes() {
 }
 
 cudaError_t launch_fp8_matmul(const Fp8GemmParams &p, bool pair, bool b_rows, int cluster, int clusters,
-                              cudaStream_t s) {
-    cudaLaunchAttribute at[1];
+                              bool overlap, cudaStream_t s) {
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = cluster;
     at[0].val.clusterDim.y = 1;
@@ -936,6 +940,11 @@ cudaError_t launch_fp8_matmul(const Fp8GemmParams &p, bool pair, bool b_rows, in
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    if (overlap) {
+        at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 2;
+    }
     return cudaLaunchKernelEx(&cfg, fp8_kernel(pair, b_rows), p);
 }
 

@@ -367,8 +367,10 @@ cudaError_t fp8_set_attributes();
 cudaError_t launch_fp8_quantize(const Fp8QuantParams &p, int dtype, bool tile, cudaStream_t s);
 // pair: CTA pairs on 256 x 256 tiles (cluster = 2); otherwise 128 x 128 tiles, each split
 // along k over `cluster` CTAs (cluster > 1: one tile per cluster)
+// overlap: the kernel launched just before on the stream is the quantisation of A (its
+// launch may overlap this one's prologue; the kernel waits for its end)
 cudaError_t launch_fp8_matmul(const Fp8GemmParams &p, bool pair, bool b_rows, int cluster, int clusters,
-                              cudaStream_t s);
+                              bool overlap, cudaStream_t s);
 
 constexpr float LOG2E_F = 1.4426950408889634f;
 

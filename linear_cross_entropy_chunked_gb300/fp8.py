@@ -166,12 +166,19 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, ws=No
         return _matmul(a, a_scale, lda, b, b_scale, ldb, b_rows, out, ws, s)
 
 
-def _logits(X, q, scale, need_xt, s):
-    """(Z, X^T in row blocks or None): the forward product on the current device and stream."""
-    (xq, xs), xt = _quantize(X, False, True, need_xt, s)
-    Z = _empty_out(X.shape[0], q.shape[0], X.dtype, X.device)
-    ldw = q.stride(0) if q.shape[0] > 1 else _pad16(q.shape[1])
-    return _matmul(xq, xs, _pad16(X.shape[1]), q, scale, ldw, False, Z, None, s), xt
+def _logits(X, q, scale, s):
+    """X W^T on the current device and stream, for W's tiles."""
+    M, D = X.shape
+    V = q.shape[0]
+    Z = _empty_out(M, V, X.dtype, X.device)
+    code = _b._CE_DTYPES[X.dtype]
+    nbytes = _WS_BYTES + (4 * M * _blocks(D) + 1023) // 1024 * 1024 + M * _pad16(D)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=X.device)
+    _b._check(_b.lib().lce_fp8_linear(
+        X.data_ptr(), code, X.stride(0) if M > 1 else D, q.data_ptr(), q.stride(0) if V > 1 else _pad16(D),
+        scale.data_ptr(), *scale.stride(), M, V, D, Z.data_ptr(), Z.stride(0) if M > 1 else -(-V // 8) * 8, code,
+        ws.data_ptr(), nbytes, s), "lce_fp8_linear")
+    return Z
 
 
 class FP8LinearFunction(torch.autograd.Function):
@@ -185,7 +192,14 @@ class FP8LinearFunction(torch.autograd.Function):
         with _b._on(X.device, None) as s:
             if W is not None:
                 (q, scale), (q_t, scale_t) = _quantize(W, True, True, need_dX, s)
-            Z, (xt, xts) = _logits(X, q, scale, need_dW, s)
+            xt = xts = None
+            if need_dW:   # X's transpose for dW comes from the same pass over X
+                (xq, xs), (xt, xts) = _quantize(X, False, True, True, s)
+                Z = _empty_out(X.shape[0], q.shape[0], X.dtype, X.device)
+                ldw = q.stride(0) if q.shape[0] > 1 else _pad16(q.shape[1])
+                _matmul(xq, xs, _pad16(X.shape[1]), q, scale, ldw, False, Z, None, s)
+            else:
+                Z = _logits(X, q, scale, s)
         ctx.save_for_backward(q_t if need_dX else None, scale_t if need_dX else None, xt, xts)
         ctx.x_dtype, ctx.w_dtype = X.dtype, None if W is None else W.dtype
         return Z
@@ -233,7 +247,7 @@ def fp8_linear(X, W):
             raise ValueError("the scales of W must be per tile of 128 x 128")
         if not (X.requires_grad and torch.is_grad_enabled()):
             with _b._on(X.device, None) as s:
-                return _logits(X.detach(), q, scale, False, s)[0]
+                return _logits(X, q, scale, s)
         if W.q_t is None or W.scale_t is None:
             raise ValueError("the gradient of X needs W's transpose (fp8_weight(W, transpose=True))")
         _check_operand("W's transpose", W.q_t, W.scale_t, False)
