@@ -341,30 +341,15 @@ template <typename T, bool SMEM> struct SmpChunk {
     }
 };
 
-// Adds to the histogram; `b` < 0: nothing. A warp whose lanes all hit one bin (equal
-// logits) adds once.
-__device__ __forceinline__ void smp_hist_add(uint32_t (*hist)[SMP_BINS], int b, bool counts, bool weights, u64 w,
-                                             int lane) {
+// Adds a logit's weight and count to bin b of the histogram.
+__device__ __forceinline__ void smp_hist_add(uint32_t (*hist)[SMP_BINS], int b, bool counts, bool weights, u64 w) {
     constexpr uint32_t M = (1u << SMP_LIMB) - 1u;
-    uint32_t n = 1, a0 = static_cast<uint32_t>(w) & M, a1 = static_cast<uint32_t>(w >> SMP_LIMB) & M,
-             a2 = static_cast<uint32_t>(w >> (2 * SMP_LIMB));
-    const int b0 = __shfl_sync(0xffffffffu, b, 0);
-    if (__all_sync(0xffffffffu, b == b0)) {
-        if (b0 < 0) return;
-        n = 32;
-        if (weights) {
-            a0 = __reduce_add_sync(0xffffffffu, a0);
-            a1 = __reduce_add_sync(0xffffffffu, a1);
-            a2 = __reduce_add_sync(0xffffffffu, a2);
-        }
-        if (lane != 0) return;
-    }
-    if (b < 0) return;
-    if (counts) atomicAdd(&hist[0][b], n);
+    if (counts) atomicAdd(&hist[0][b], 1u);
     if (weights) {
-        atomicAdd(&hist[1][b], a0);
-        atomicAdd(&hist[2][b], a1);
-        if (a2) atomicAdd(&hist[3][b], a2);
+        atomicAdd(&hist[1][b], static_cast<uint32_t>(w) & M);
+        atomicAdd(&hist[2][b], static_cast<uint32_t>(w >> SMP_LIMB) & M);
+        const uint32_t top = static_cast<uint32_t>(w >> (2 * SMP_LIMB));
+        if (top) atomicAdd(&hist[3][b], top);
     }
 }
 
@@ -383,6 +368,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
     const float top_p = p.top_p ? p.top_p[r] : p.top_p_all;
     const float min_p = p.min_p ? p.min_p[r] : p.min_p_all;
     const bool greedy = !(temperature > 0.f);
+    const float u = p.u[r];
 
     cluster_arrive();   // waited for before the first write to a peer: it has started
     if (t < 64) sh.tab[t] = tabs.fix[t];
@@ -511,7 +497,6 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
     };
     // floor(u * total), u inside [0, 1): the token is the first whose cumulative weight exceeds it
     auto draw_target = [&](u64 total) -> u64 {
-        const float u = p.u[r];
         if (!(u < 1.f)) return total - 1;
         return u > 0.f ? smp_mul_floor(u, total, false) : 0ull;
     };
@@ -523,10 +508,28 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
 
     if (by_count || by_weight) {
         // A threshold with at least `want` logits at or above it, and rarely many more: the
-        // want-th largest of the warps' maxima. Those logits go onto the list.
-        const int want = by_count ? top_k : entries / 2;
+        // want-th largest of `entries` maxima of parts of the row, which go onto the list. Up to 32
+        // of them are the lanes' maxima over PER_LANE warps, which every warp sorts for itself;
+        // more are the warps' own, counted against one another.
+        const int groups = (entries + PER_LANE - 1) / PER_LANE;   // lanes with entries
+        const int want = by_count ? top_k : groups - 1;           // (top-p: about 100 logits)
         const bool use_list = want <= entries;
-        if (use_list) {
+        float t0 = INFINITY;
+        if (want <= groups) {
+            float v = wm[0];
+#pragma unroll
+            for (int q = 1; q < PER_LANE; ++q) v = fmaxf(v, wm[q]);
+            // bitonic sort, descending
+#pragma unroll
+            for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+                for (int j = k >> 1; j > 0; j >>= 1) {
+                    const float o = __shfl_xor_sync(0xffffffffu, v, j);
+                    const bool keep_max = ((l & j) == 0) == ((l & k) == 0);
+                    v = keep_max ? fmaxf(v, o) : fminf(v, o);
+                }
+            t0 = __shfl_sync(0xffffffffu, v, want - 1);
+        } else if (use_list) {
 #pragma unroll
             for (int q = 0; q < SMP_MAX_CLUSTER; ++q) {
                 const int e = w * SMP_MAX_CLUSTER + q;   // every warp looks at its share of the entries
@@ -544,7 +547,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
         }
         if (t == 0) sh.listed = 0;
         __syncthreads();
-        const float t0 = use_list ? fmaxf(sh.t0, -3.402823466e38f) : INFINITY;   // (masked ones stay out)
+        if (use_list) t0 = fmaxf(want <= groups ? t0 : sh.t0, -3.402823466e38f);   // (masked ones stay out)
 
         // one pass: sums over the row, and the list
         int xs = 0;
@@ -715,8 +718,9 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
             __syncthreads();
         };
         // totals over the cluster of the histogram just filled; exclusive prefixes over
-        // its bins into (pc, pw)
-        auto totals = [&](uint32_t *pc, u64 *pw, uint32_t *tot_c, u64 *tot_w) {
+        // its bins into (pc, pw). one_key: each bin holds the logits of one key, khi less the
+        // bin's number, and only counts were added: their weight is the key's times the count
+        auto totals = [&](uint32_t *pc, u64 *pw, uint32_t *tot_c, u64 *tot_w, bool one_key, uint32_t khi) {
             cluster_sync_all();
             uint32_t c = 0;
             u64 wt = 0;
@@ -728,8 +732,8 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                     h[0][k] = h[1][k] = h[2][k] = h[3][k] = 0u;
                     if (k >= cl) continue;
                     const uint32_t at = map_to_rank(&sh.hist[hb][0][t], k);
-                    if (by_count) h[0][k] = ld_cluster_u32(at);
-                    if (by_weight) {
+                    if (by_count || one_key) h[0][k] = ld_cluster_u32(at);
+                    if (by_weight && !one_key) {
                         h[1][k] = ld_cluster_u32(at + 4 * SMP_BINS);
                         h[2][k] = ld_cluster_u32(at + 8 * SMP_BINS);
                         h[3][k] = ld_cluster_u32(at + 12 * SMP_BINS);
@@ -744,6 +748,8 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                     l2 += h[3][k];
                 }
                 wt = l0 + (l1 << SMP_LIMB) + (l2 << (2 * SMP_LIMB));
+                if (one_key && by_weight && c)
+                    wt = c * smp_weight(smp_unkey<T>(khi - static_cast<uint32_t>(t)), rw, tabs, sh.tab);
                 uint32_t ci = c;
                 u64 wi = wt;
 #pragma unroll
@@ -830,10 +836,9 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (__any_sync(0xffffffffu, bin[j] >= 0))
-                        smp_hist_add(sh.hist[hb], bin[j], by_count, by_weight, by_weight ? v[j] : 0ull, l);
+                    if (bin[j] >= 0) smp_hist_add(sh.hist[hb], bin[j], by_count, by_weight, by_weight ? v[j] : 0ull);
             }
-            totals(sh.l0c, sh.l0w, &tot_c, &tot_w);
+            totals(sh.l0c, sh.l0w, &tot_c, &tot_w, false, 0u);
         };
 
         // the key and the number of equal logits at which `target` is reached
@@ -878,18 +883,19 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                     if (!__any_sync(0xffffffffu, any)) continue;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        if (!__any_sync(0xffffffffu, x[j] >= zlo && x[j] <= zhi)) continue;
+                        if (!(x[j] >= zlo && x[j] <= zhi)) continue;
                         const uint32_t k = smp_key<T>(x[j]);
                         const int in = bin_of(x[j]);
-                        const int b = k >= klo && k <= khi && in >= 0 && (b0 < 0 || in == b0)
-                                          ? static_cast<int>((khi - k) >> shift) : -1;
-                        smp_hist_add(sh.hist[hb], b, by_count, by_weight,
-                                     by_weight ? smp_weight(x[j], rw, tabs, sh.tab) : 0ull, l);
+                        if (!(k >= klo && k <= khi && in >= 0 && (b0 < 0 || in == b0))) continue;
+                        if (shift == 0) atomicAdd(&sh.hist[hb][0][khi - k], 1u);
+                        else
+                            smp_hist_add(sh.hist[hb], static_cast<int>((khi - k) >> shift), by_count, by_weight,
+                                         by_weight ? smp_weight(x[j], rw, tabs, sh.tab) : 0ull);
                     }
                 }
                 uint32_t tc;
                 u64 tw;
-                totals(sh.rc, sh.rw, &tc, &tw);
+                totals(sh.rc, sh.rw, &tc, &tw, shift == 0, khi);
                 find(sh.rc, sh.rw, tc, tw, count, target - (count ? static_cast<u64>(base_c) : base_w));
                 const uint32_t b = static_cast<uint32_t>(sh.bin);
                 base_c += sh.bc;
