@@ -1084,7 +1084,7 @@ SampleKernel sample_kernel(int dtype, bool smem) {
 }
 
 constexpr int SMP_MAX_DYN = 160 * 1024;   // a CTA's logits; the rest of its shared memory is static
-constexpr int SMP_TWO_DYN = 88 * 1024;    // the same when two CTAs share an SM
+constexpr int SMP_TWO_DYN = 83 * 1024;    // the same when two CTAs share an SM
 
 }  // namespace
 

@@ -234,7 +234,9 @@ def fp8_linear(X, W):
     states X [M, D] (bf16, fp16 or fp32). W: a weight [V, D] (bf16, fp16 or fp32), quantised in
     the call and differentiable, or an FP8Weight, which is frozen (its transpose is needed
     where X requires a gradient). Differentiable in X and W; the gradients are
-    products in e4m3 too. The logits' row stride is V rounded up to 16 bytes."""
+    products in e4m3 too. The logits' row stride is V rounded up to 16 bytes. (A backward pass
+    is captured into a CUDA graph as any other of torch's: no eager graph of the same leaves may
+    live meanwhile; X.detach().requires_grad_() gives a leaf of its own.)"""
     _check_dense_rows("X", X, _b._CE_DTYPES, "bfloat16, float16 or float32")
     D = X.shape[1]
     if isinstance(W, FP8Weight):
