@@ -26,10 +26,10 @@ constexpr int CLIP_THREADS = 512;
 constexpr int CLIP_VECS = 4;                                   // 16-byte vectors per thread and chunk
 constexpr int CLIP_CHUNK = CLIP_THREADS * CLIP_VECS * 16;      // 32 KB
 
-// A tensor's values seen as the 16-byte vectors that hold them: the first and the last
-// may be partly outside.
+// A tensor's values seen as the 16-byte vectors of the 128-byte lines that hold them (a warp
+// reads whole lines): vectors at both ends may be partly or wholly outside.
 struct ClipSpan {
-    const uint8_t *base;   // 16-byte aligned, at or before the first value
+    const uint8_t *base;   // 128-byte aligned, at or before the first value
     uint8_t *out;          // what `base` corresponds to in the destination
     long long lo, hi;      // bytes from base: first value, end
     int dtype;
@@ -40,7 +40,7 @@ template <int CAP> __device__ __forceinline__ ClipSpan clip_span(const ClipTable
     ClipSpan s;
     const uintptr_t a = reinterpret_cast<uintptr_t>(tb.src[i]);
     const uintptr_t b = reinterpret_cast<uintptr_t>(tb.dst[i]);
-    const int off = static_cast<int>(a & 15u);
+    const int off = static_cast<int>(a & 127u);
     s.dtype = static_cast<int>(tb.count[i] & 3);
     s.base = reinterpret_cast<const uint8_t *>(a - off);
     s.out = reinterpret_cast<uint8_t *>(b - off);
@@ -68,7 +68,7 @@ template <bool LAST> __device__ __forceinline__ uint4 clip_load(const ClipSpan &
         const uint4 *a = reinterpret_cast<const uint4 *>(s.base + o);
         return LAST ? __ldcs(a) : *a;
     }
-    if (o >= s.hi) return make_uint4(0u, 0u, 0u, 0u);
+    if (o >= s.hi || o + 16 <= s.lo) return make_uint4(0u, 0u, 0u, 0u);
     uint32_t w[4] = {0u, 0u, 0u, 0u};
     if (s.dtype == CE_FP32) {
 #pragma unroll
@@ -332,7 +332,7 @@ cudaError_t scale_launch(const ClipItem *items, int n, const ClipScale &c, int g
 
 // Chunks of a tensor of n values at address p.
 long long clip_chunks(const void *p, long long n, int dtype) {
-    const long long off = static_cast<long long>(reinterpret_cast<uintptr_t>(p) & 15u);
+    const long long off = static_cast<long long>(reinterpret_cast<uintptr_t>(p) & 127u);
     const long long bytes = off + n * (dtype == CE_FP32 ? 4 : 2);
     return (bytes + CLIP_CHUNK - 1) / CLIP_CHUNK;
 }

@@ -82,6 +82,28 @@ template <typename T> struct QtVec {
                 w[j] = (2 * j < n ? h[2 * j] : 0u) | ((2 * j + 1 < n ? static_cast<uint32_t>(h[2 * j + 1]) : 0u) << 16);
         }
     }
+    // The same for a row that does not start on a 16-byte boundary, by a half-warp whose lane i takes
+    // values 8 i .. 8 i + 7: aligned vectors, of which each lane shifts its own and the next
+    // lane's together (the last lane loads its next one).
+    __device__ __forceinline__ void load_shifted(const T *row, int i, bool last) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(row);
+        const uint32_t off = static_cast<uint32_t>(a & 15u);   // even
+        const uint4 *v = reinterpret_cast<const uint4 *>(a - off) + i;
+        const uint4 u = *v;
+        uint4 nx = make_uint4(__shfl_down_sync(0xffffffffu, u.x, 1, 16), __shfl_down_sync(0xffffffffu, u.y, 1, 16),
+                              __shfl_down_sync(0xffffffffu, u.z, 1, 16), __shfl_down_sync(0xffffffffu, u.w, 1, 16));
+        if (last) nx = v[1];
+        // words off / 4 .. off / 4 + 4 of the eight, then the odd halfword
+        uint32_t y[6] = {u.x, u.y, u.z, u.w, nx.x, nx.y};
+        uint32_t z[5];
+        if (off & 8u) {
+            y[0] = u.z; y[1] = u.w; y[2] = nx.x; y[3] = nx.y; y[4] = nx.z; y[5] = nx.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 5; ++j) z[j] = off & 4u ? y[j + 1] : y[j];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = off & 2u ? __funnelshift_r(z[j], z[j + 1], 16) : z[j];
+    }
     // largest |x| of column pair j, as two 16-bit values
     __device__ __forceinline__ uint32_t abs2(int j) const { return w[j] & 0x7fff7fffu; }
     __device__ __forceinline__ uint32_t row_max() const {
@@ -148,9 +170,19 @@ __global__ void __launch_bounds__(QT_THREADS, sizeof(T) == 4 ? 2 : 3)
     const int nc = p.C - c0 < 128 ? static_cast<int>(p.C - c0) : 128;
     const T *X = static_cast<const T *>(p.X) + r0 * p.ld + c0;
     V x[8];
+    // Rows that start anywhere: the aligned vectors that hold a whole tile's rows, which reach up
+    // to 16 bytes past it on either side, lie within X.
+    const bool shifted = PACKED && !p.vec && nr == 128 && nc == 128 && tile > 0 &&
+                         (c0 + 136 <= p.C || r0 + 128 < p.R);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const int r = g * 8 + k;
+        if constexpr (PACKED) {
+            if (shifted) {
+                x[k].load_shifted(X + static_cast<long long>(r) * p.ld, i, i == 15);
+                continue;
+            }
+        }
         if (r < nr && i * 8 < nc) x[k].load(X + static_cast<long long>(r) * p.ld + i * 8, nc - i * 8, p.vec != 0);
         else memset(&x[k], 0, sizeof(V));
     }

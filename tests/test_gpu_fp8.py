@@ -60,6 +60,19 @@ def test_quantize_strides(dtype):
             check_quantized(lce.quantize_fp8(v, tiles=tiles, transpose=True), v.double().cpu().numpy().T, tiles)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("r,c", [(128, 128), (256, 129), (300, 1001), (129, 263), (384, 392)])
+def test_quantize_rows_that_start_anywhere(r, c, dtype):
+    # every offset of a row's start within 16 bytes, and rows that begin and end with the memory
+    for extra in range(0, 9):
+        flat = torch.randn(r * (c + extra) + 8, generator=torch.Generator().manual_seed(extra)).to(DTYPES[dtype]).cuda()
+        for at in (0, 1, 5):
+            v = flat[at:at + r * (c + extra)].view(r, c + extra)[:, extra:] if extra else flat[at:at + r * c].view(r, c)
+            check_quantized(lce.quantize_fp8(v), v.double().cpu().numpy(), False)
+        check_quantized(lce.quantize_fp8(v, transpose=True), v.double().cpu().numpy().T, False)
+        check_quantized(lce.quantize_fp8(v, tiles=True), v.double().cpu().numpy(), True)
+
+
 @pytest.mark.parametrize("tiles", [False, True])
 def test_quantize_special_values(tiles):
     X = torch.randn(260, 400)
