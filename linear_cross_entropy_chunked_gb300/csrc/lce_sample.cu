@@ -353,7 +353,8 @@ __device__ __forceinline__ void smp_hist_add(uint32_t (*hist)[SMP_BINS], int b, 
     }
 }
 
-template <typename T, bool SMEM>
+// SEARCH: some row has a top-k or a top-p.
+template <typename T, bool SMEM, bool SEARCH>
 __global__ void __launch_bounds__(SMP_THREADS, 2)
     lce_sample_kernel(const SampleParams p, const __grid_constant__ SampleTables tabs, const int chunk) {
     extern __shared__ __align__(128) uint8_t smp_dyn[];
@@ -403,11 +404,15 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
         ck.p = mine;
     } else {
         ck.p = row;
-        for (int i = l * 8; i < n; i += 256) {
-            float x[8];
-            ck.load(i, x);
+        for (int i0 = l * 8; i0 < n; i0 += 4 * 256) {   // (loads of four sweeps under way at once)
+            float x[4][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m = fmaxf(m, x[j]);
+            for (int q = 0; q < 4; ++q)
+                smp_load_global<T>(row + i0 + q * 256, n - i0 - q * 256, aligned, x[q]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m = fmaxf(m, x[q][j]);
         }
     }
     const int steps = (n + 255) / 256;   // sweeps of the warp over its logits
@@ -476,8 +481,8 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
         m = 0.f;
     }
 
-    const bool by_count = top_k > 0 && top_k < p.V;
-    const bool by_weight = top_p < 1.f;
+    const bool by_count = SEARCH && top_k > 0 && top_k < p.V;
+    const bool by_weight = SEARCH && top_p < 1.f;
     u64 w_min = 0;         // kept: weight at least w_min, ...
     if (min_p > 0.f) w_min = min_p >= 1.f ? SMP_ONE : smp_mul_floor(min_p, SMP_ONE, true);
     // ... and the cut: all logits with a key above cut_key, and the first cut_ties of those at it
@@ -1016,60 +1021,92 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
     // the first index whose cumulative weight exceeds u * total
     const u64 target = draw_target(total);
     if (target >= my_first && target - my_first < my_sum) {
+        // the sweep in which the target lies: sums of several sweeps at once, whose loads and
+        // shuffles do not wait for one another
+        constexpr int GROUP = 4;
         u64 run = my_first;
         uint32_t seen = my_ties_before;
-        for (int s = 0; s < steps; ++s) {
-            const int i = s * 256 + l * 8;
-            float x[8];
-            u64 v[8];
-            uint32_t tmask = 0;
-            ck.load(i, x);
-            kept_weights(x, v);
+        int sweep = steps == 1 ? 0 : -1;
+        for (int s0 = 0; sweep < 0 && s0 < steps; s0 += GROUP) {
+            u64 sums[GROUP];
+            uint32_t same[GROUP];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (have_cut && x[j] == cut) tmask |= 1u << j;
-            const uint32_t tl = __popc(tmask);
-            uint32_t tb = tl;
+            for (int g = 0; g < GROUP; ++g) {
+                float x[8];
+                u64 v[8];
+                ck.load((s0 + g) * 256 + l * 8, x);   // (nothing past the end)
+                kept_weights(x, v);
+                sums[g] = 0;
+                same[g] = 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t c = __shfl_up_sync(0xffffffffu, tb, o);
-                if (l >= o) tb += c;
+                for (int j = 0; j < 8; ++j) {
+                    sums[g] += v[j];
+                    same[g] += have_cut && x[j] == cut ? 1u : 0u;
+                }
             }
-            uint32_t mine_seen = seen + tb - tl;
-            u64 sum = 0;
+#pragma unroll
+            for (int g = 0; g < GROUP; ++g) {
+                sums[g] = warp_sum64(sums[g]);
+                if (have_cut) same[g] = __reduce_add_sync(0xffffffffu, same[g]);
+            }
+#pragma unroll
+            for (int g = 0; g < GROUP; ++g) {
+                if (sweep >= 0) continue;
+                const uint32_t room = seen < cut_ties ? cut_ties - seen : 0u;
+                const u64 all = sums[g] + static_cast<u64>(same[g] < room ? same[g] : room) * tie_w;
+                if (run + all > target) {
+                    sweep = s0 + g;
+                } else {
+                    run += all;
+                    seen += same[g];
+                }
+            }
+        }
+        const int i = sweep * 256 + l * 8;
+        float x[8];
+        u64 v[8];
+        uint32_t tmask = 0;
+        ck.load(i, x);
+        kept_weights(x, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (have_cut && x[j] == cut) tmask |= 1u << j;
+        const uint32_t tl = __popc(tmask);
+        uint32_t tb = tl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t c = __shfl_up_sync(0xffffffffu, tb, o);
+            if (l >= o) tb += c;
+        }
+        uint32_t mine_seen = seen + tb - tl;
+        u64 sum = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (tmask >> j & 1u) v[j] = mine_seen++ < cut_ties ? tie_w : 0ull;
+            sum += v[j];
+        }
+        u64 in = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 c = shfl_up64(in, o);
+            if (l >= o) in += c;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, run + in > target);
+        if (l == __ffs(hit) - 1) {
+            u64 c = run + in - sum;
+            int at = 0;
+            float z = x[0];
+            bool found = false;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                if (tmask >> j & 1u) v[j] = mine_seen++ < cut_ties ? tie_w : 0ull;
-                sum += v[j];
-            }
-            u64 in = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const u64 c = shfl_up64(in, o);
-                if (l >= o) in += c;
-            }
-            const uint32_t hit = __ballot_sync(0xffffffffu, run + in > target);
-            if (hit) {
-                if (l == __ffs(hit) - 1) {
-                    u64 c = run + in - sum;
-                    int at = 0;
-                    float z = x[0];
-                    bool found = false;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        c += v[j];
-                        if (!found && c > target) {
-                            found = true;
-                            at = j;
-                            z = x[j];
-                        }
-                    }
-                    answer(first + i + at, z, total);
+                c += v[j];
+                if (!found && c > target) {
+                    found = true;
+                    at = j;
+                    z = x[j];
                 }
-                break;
             }
-            run += __shfl_sync(0xffffffffu, in, 31);
-            seen += __shfl_sync(0xffffffffu, tb, 31);
+            answer(first + i + at, z, total);
         }
     }
     // (nothing of a peer's is touched after the sums' exchange: a CTA may leave)
@@ -1077,10 +1114,14 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
 
 using SampleKernel = void (*)(const SampleParams, const SampleTables, const int);
 
-SampleKernel sample_kernel(int dtype, bool smem) {
-    if (dtype == CE_FP32) return smem ? lce_sample_kernel<float, true> : lce_sample_kernel<float, false>;
-    if (dtype == CE_FP16) return smem ? lce_sample_kernel<__half, true> : lce_sample_kernel<__half, false>;
-    return smem ? lce_sample_kernel<__nv_bfloat16, true> : lce_sample_kernel<__nv_bfloat16, false>;
+template <typename T> SampleKernel sample_kernel_of(bool smem, bool search) {
+    if (smem) return search ? lce_sample_kernel<T, true, true> : lce_sample_kernel<T, true, false>;
+    return search ? lce_sample_kernel<T, false, true> : lce_sample_kernel<T, false, false>;
+}
+SampleKernel sample_kernel(int dtype, bool smem, bool search) {
+    if (dtype == CE_FP32) return sample_kernel_of<float>(smem, search);
+    if (dtype == CE_FP16) return sample_kernel_of<__half>(smem, search);
+    return sample_kernel_of<__nv_bfloat16>(smem, search);
 }
 
 constexpr int SMP_MAX_DYN = 160 * 1024;   // a CTA's logits; the rest of its shared memory is static
@@ -1090,9 +1131,11 @@ constexpr int SMP_TWO_DYN = 83 * 1024;    // the same when two CTAs share an SM
 
 cudaError_t sample_set_attributes() {
     for (int dt = CE_BF16; dt <= CE_FP16; ++dt) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            sample_kernel(dt, true), cudaFuncAttributeMaxDynamicSharedMemorySize, SMP_MAX_DYN);
-        if (e != cudaSuccess) return e;
+        for (int search = 0; search < 2; ++search) {
+            const cudaError_t e = cudaFuncSetAttribute(
+                sample_kernel(dt, true, search != 0), cudaFuncAttributeMaxDynamicSharedMemorySize, SMP_MAX_DYN);
+            if (e != cudaSuccess) return e;
+        }
     }
     return cudaSuccess;
 }
@@ -1109,6 +1152,7 @@ cudaError_t launch_sample(const SampleParams &p, int sms, cudaStream_t s) {
            (chunk_of(cl) * SMP_WARPS * elem > SMP_TWO_DYN ||
             (p.N * cl * 2 <= 2 * sms && chunk_of(cl) > 256)))
         cl *= 2;
+    const bool search = p.top_k || p.top_p || p.top_k_all > 0 || p.top_p_all < 1.f;
     const long long chunk = chunk_of(cl);
     const long long bytes = chunk * SMP_WARPS * elem;
     const bool smem = bytes <= SMP_MAX_DYN;
@@ -1124,7 +1168,7 @@ cudaError_t launch_sample(const SampleParams &p, int sms, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sample_kernel(p.dtype, smem), p, tabs, static_cast<int>(chunk));
+    return cudaLaunchKernelEx(&cfg, sample_kernel(p.dtype, smem, search), p, tabs, static_cast<int>(chunk));
 }
 
 }  // namespace lce
