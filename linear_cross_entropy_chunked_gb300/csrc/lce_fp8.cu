@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     if (warp == PRODUCER_WARP && lane == 0) {
         prefetch_tmap(&p.tmA);
         prefetch_tmap(&p.tmB);
-        prefetch_tmap(&p.tmC);
+        if (p.n_bulk > 0) prefetch_tmap(&p.tmC);
     }
     if (warp == MMA_WARP) {
         if constexpr (PAIR) {

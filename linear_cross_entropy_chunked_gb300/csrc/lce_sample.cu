@@ -796,7 +796,8 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                 const uint32_t c0 = pc[t], c1 = t + 1 < SMP_BINS ? pc[t + 1] : tot_c;
                 const u64 w0 = pw[t], w1 = t + 1 < SMP_BINS ? pw[t + 1] : tot_w;
                 const u64 a = count ? c0 : w0, b = count ? c1 : w1;
-                if (a < target && target <= b) {
+                // (the sums are exact, so one bin always fits; the ends keep any target in range)
+                if ((a < target && target <= b) || (t == 0 && target == 0) || (t == SMP_BINS - 1 && b < target)) {
                     sh.bin = t;
                     sh.bc = c0;
                     sh.bw = w0;
@@ -874,7 +875,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                 __syncthreads();
                 key_range(x0 + static_cast<float>(b0) / per_x, x0 + static_cast<float>(b0 + 1) / per_x);
             }
-            while (klo != khi) {
+            for (int level = 0; klo != khi && level < 4; ++level) {   // 8 bits of the key at a time
                 const int bits = 32 - __clz(khi - klo);
                 const int shift = bits > 8 ? bits - 8 : 0;
                 const float zlo = smp_unkey<T>(klo), zhi = smp_unkey<T>(khi);
@@ -905,7 +906,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                 const uint32_t b = static_cast<uint32_t>(sh.bin);
                 base_c += sh.bc;
                 base_w += sh.bw;
-                khi -= b << shift;
+                khi -= min(b << shift, khi - klo);
                 const uint32_t width = (1u << shift) - 1u;
                 klo = khi - klo > width ? khi - width : klo;
                 __syncthreads();
@@ -1062,7 +1063,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                 }
             }
         }
-        const int i = sweep * 256 + l * 8;
+        const int i = max(sweep, 0) * 256 + l * 8;   // (always found, unless Z changes meanwhile)
         float x[8];
         u64 v[8];
         uint32_t tmask = 0;
@@ -1150,7 +1151,7 @@ cudaError_t launch_sample(const SampleParams &p, int sms, cudaStream_t s) {
     int cl = 1;
     while (cl < SMP_MAX_CLUSTER &&
            (chunk_of(cl) * SMP_WARPS * elem > SMP_TWO_DYN ||
-            (p.N * cl * 2 <= 2 * sms && chunk_of(cl) > 256)))
+            (p.N * cl <= sms && chunk_of(cl) > 256)))
         cl *= 2;
     const bool search = p.top_k || p.top_p || p.top_k_all > 0 || p.top_p_all < 1.f;
     const long long chunk = chunk_of(cl);

@@ -10,6 +10,7 @@ from __future__ import annotations
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _binding as _b
 
@@ -205,6 +206,7 @@ class FP8LinearFunction(torch.autograd.Function):
         return Z
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dZ):
         wt, wts, xt, xts = ctx.saved_tensors
         need_dX, need_dW = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
@@ -234,7 +236,7 @@ def fp8_linear(X, W):
     states X [M, D] (bf16, fp16 or fp32). W: a weight [V, D] (bf16, fp16 or fp32), quantised in
     the call and differentiable, or an FP8Weight, which is frozen (its transpose is needed
     where X requires a gradient). Differentiable in X and W; the gradients are
-    products in e4m3 too. The logits' row stride is V rounded up to 16 bytes. (A backward pass
+    products in e4m3 too, and have no derivatives themselves. The logits' row stride is V rounded up to 16 bytes. (A backward pass
     is captured into a CUDA graph as any other of torch's: no eager graph of the same leaves may
     live meanwhile; X.detach().requires_grad_() gives a leaf of its own.)"""
     _check_dense_rows("X", X, _b._CE_DTYPES, "bfloat16, float16 or float32")
@@ -259,4 +261,6 @@ def fp8_linear(X, W):
     _check_dense_rows("W", W, _b._CE_DTYPES, "bfloat16, float16 or float32, or an FP8Weight")
     if D != W.shape[1] or X.device != W.device or W.shape[0] == 0:
         raise ValueError(f"X{tuple(X.shape)} and W{tuple(W.shape)} must share their columns and device")
+    if not torch.is_grad_enabled():   # (no transposes for a backward pass that cannot come)
+        X, W = X.detach(), W.detach()
     return FP8LinearFunction.apply(X, W, None, None, None, None)

@@ -53,7 +53,7 @@ def sample_logits(Z, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=N
     q, q_all = _setting("min_p", min_p, N, dev, torch.float32)
     if not 0.0 <= t_all < math.inf:
         raise ValueError("temperature must be finite and not negative")
-    if k_all < 0 or int(k_all) != k_all:
+    if not 0 <= k_all < math.inf or int(k_all) != k_all:
         raise ValueError("top_k must be a whole number, 0 for all tokens")
     if not 0.0 <= p_all <= 1.0 or not 0.0 <= q_all <= 1.0:
         raise ValueError("top_p and min_p must lie in [0, 1]")

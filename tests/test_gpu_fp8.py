@@ -242,6 +242,22 @@ def test_gradient_of_broadcast_and_strided_upstream():
     assert torch.equal(a, b) and torch.equal(b, c)
 
 
+def test_second_derivative_is_refused():
+    X = rand(8, 128, 1).cuda().requires_grad_()
+    W = rand(40, 128, 2).cuda().requires_grad_()
+    dX, dW = torch.autograd.grad(lce.fp8_linear(X, W).float().square().sum(), (X, W), create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiate twice"):
+        (dX.float().sum() + dW.float().sum()).backward()
+
+
+def test_without_gradients():
+    X, W = rand(33, 200, 1).cuda().requires_grad_(), rand(300, 200, 2).cuda().requires_grad_()
+    Z = lce.fp8_linear(X, W)
+    with torch.no_grad():
+        Y = lce.fp8_linear(X, W)
+    assert Z.requires_grad and not Y.requires_grad and torch.equal(Y, Z)
+
+
 def test_graph_and_stream():
     a, sa = operand(64, 512, 1, False)
     b, sb = operand(5000, 512, 2, True)

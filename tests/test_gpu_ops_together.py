@@ -223,3 +223,10 @@ def test_clip_refusals():
         lce.clip_grad_norm([g.double()], 1.0)
     with pytest.raises(lce.LCEError):
         lce.grad_norm(g, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+def test_refused_top_k_without_end():
+    Z, u = torch.zeros(2, 10, device="cuda"), torch.zeros(2, device="cuda")
+    for k in (float("inf"), float("nan"), -1, 2.5):
+        with pytest.raises(ValueError):
+            lce.sample_logits(Z, u, top_k=k)
