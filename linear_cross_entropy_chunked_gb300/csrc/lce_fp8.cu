@@ -630,17 +630,11 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             const int row0 = mt * (CL * 128) + static_cast<int>(crank) * 128 + quarter * 32;
             const int col0 = nt * BNT + half * COLS;
             const bool active = row0 < p.M && col0 < p.N;   // warp-uniform: some output of this warp exists
-            // rows of this thread: one, or (fragments) four, 8 apart
+            // each lane brings the scale of one row; a thread's rows are that one or (fragments) four, 8
+            // apart, which it gets from the lanes that have them
             constexpr int ROWS = B_ROWS ? 4 : 1;
-            const int row = row0 + (B_ROWS ? lane / 4 : lane);
+            const int row = row0 + lane;
             const float *sa = p.sa + static_cast<long long>(row < p.M ? row : 0) * p.sa_row;
-            auto load_sa = [&](float (&a)[ROWS], int kb) {
-#pragma unroll
-                for (int i = 0; i < ROWS; ++i)   // (four pointers would be kept in registers that are not there)
-                    a[i] = B_ROWS ? p.sa[static_cast<long long>(row + 8 * i < p.M ? row + 8 * i : 0) * p.sa_row +
-                                         kb * p.sa_block]
-                                  : sa[kb * p.sa_block];
-            };
             const long long sbk = p.sb_block;
             // tile scales: the warp's columns lie in one block of 128; row scales: VEC columns per lane
             constexpr int VEC = COLS / 32;
@@ -670,11 +664,11 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             }
             // scales of the next k block, and (where registers allow) of the one after it
             constexpr int AHEAD = B_ROWS ? 1 : 2;
-            float a0[ROWS], a1[ROWS], b0[VEC], b1[VEC];
-            load_sa(a0, kb0);
+            float a0, a1 = 0.f, b0[VEC], b1[VEC];
+            a0 = sa[kb0 * p.sa_block];
             load_sb(b0, kb0);
             if (AHEAD > 1 && kb0 + 1 < kb1) {
-                load_sa(a1, kb0 + 1);
+                a1 = sa[(kb0 + 1) * p.sa_block];
                 load_sb(b1, kb0 + 1);
             }
             // the thread's sums: columns 2 j and 2 j + 1 of its row, or (fragments) of group g of 8
@@ -685,26 +679,25 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             for (int kb = kb0; kb < kb1; ++kb) {
                 float s[ROWS];
 #pragma unroll
-                for (int i = 0; i < ROWS; ++i) s[i] = a0[i];
+                for (int i = 0; i < ROWS; ++i) s[i] = B_ROWS ? __shfl_sync(0xffffffffu, a0, lane / 4 + 8 * i) : a0;
                 if constexpr (B_ROWS) {
-                    // (the other k block's half may still be in use by a slower lane)
-                    if constexpr (VEC == 4)
-                        *reinterpret_cast<float4 *>(sb_smem + par * COLS + lane * 4) =
-                            make_float4(b0[0], b0[1], b0[2], b0[3]);
-                    else
-                        *reinterpret_cast<float2 *>(sb_smem + par * COLS + lane * 2) = make_float2(b0[0], b0[1]);
+                    // Columns 2 f + 8 q (+ 1) of 32 belong to the lanes with lane % 4 = f: they are kept side by
+                    // side, at 8 f + 2 q. (The other k block's half may still be in use by a slower lane.)
+                    float *to = sb_smem + par * COLS + lane * VEC / 32 * 32 + lane * VEC % 32 / 8 * 2;
+#pragma unroll
+                    for (int j = 0; j < VEC; j += 2)
+                        *reinterpret_cast<float2 *>(to + (lane * VEC % 8 / 2 + j / 2) * 8) = make_float2(b0[j], b0[j + 1]);
                     __syncwarp();
                 } else {
                     s[0] *= b0[0];
                 }
                 if constexpr (AHEAD > 1) {
-#pragma unroll
-                    for (int i = 0; i < ROWS; ++i) a0[i] = a1[i];
+                    a0 = a1;
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) b0[j] = b1[j];
                 }
                 if (kb + AHEAD < kb1) {
-                    load_sa(AHEAD > 1 ? a1 : a0, kb + AHEAD);
+                    (AHEAD > 1 ? a1 : a0) = sa[(kb + AHEAD) * p.sa_block];
                     load_sb(AHEAD > 1 ? b1 : b0, kb + AHEAD);
                 }
                 ok = mbar_wait(&done_bar[stage], phase, ab);
@@ -726,10 +719,17 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                     if constexpr (B_ROWS) {
                         // loads: 32 columns of rows 0-15, then of rows 16-31 of the quarter
                         constexpr int LOADS = COLS / 16;
+                        float4 bq[2];   // scales of the thread's 8 columns of 32
                         tmem_ldfrag_start(taddr, v[0]);
                         tmem_ld16_wait(v[0]);
 #pragma unroll
                         for (int c = 0; c < LOADS; ++c) {
+                            if (c % 2 == 0) {
+                                const float4 *from =
+                                    reinterpret_cast<const float4 *>(sb_smem + par * COLS + c / 2 * 32 + (lane & 3) * 8);
+                                bq[0] = from[0];
+                                bq[1] = from[1];
+                            }
                             if (c + 1 < LOADS)
                                 tmem_ldfrag_start(taddr + ((c + 1) / 2) * 32 + ((c + 1) % 2) * (16u << 16), v[(c + 1) & 1]);
                             else
@@ -740,8 +740,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
                                 const int g = (c / 2) * 4 + q;
-                                const float2 b = *reinterpret_cast<const float2 *>(sb_smem + par * COLS + g * 8 +
-                                                                                   (lane & 3) * 2);
+                                const float2 b = q % 2 ? make_float2(bq[q / 2].z, bq[q / 2].w)
+                                                       : make_float2(bq[q / 2].x, bq[q / 2].y);
                                 float2 &x = acc[4 * g + i0], &y = acc[4 * g + i0 + 1];
                                 x = __ffma2_rn(make_float2(__uint_as_float(u[4 * q]), __uint_as_float(u[4 * q + 1])),
                                                __fmul2_rn(sa0, b), x);
