@@ -23,6 +23,7 @@
 // CTAs exchange maxima, histograms and sums through distributed shared memory. Rows
 // longer than the cluster's shared memory are read again from L2 instead.
 #include <cmath>
+#include <type_traits>
 
 #include "lce_internal.h"
 #include "lce_ptx.cuh"
@@ -41,39 +42,42 @@ constexpr float SMP_X1 = 6.f, SMP_X2 = 12.f;
 constexpr int SMP_LIST_CTA = 256, SMP_LIST = SMP_THREADS;
 constexpr int SMP_LIMB = 15;                         // bits per limb of a weight: 2^17 limbs fit 32 bits
 
-constexpr float SMP_X_CLAMP = 31.18f;                // n = 2879, a shift by 63: weight 0
+constexpr int SMP_STEP_BITS = 8, SMP_STEPS = 1 << SMP_STEP_BITS;   // the exponential's table: 2^(-j / 256)
+constexpr float SMP_X_CLAMP = 31.18f;                // n = 11516, a shift by 63: weight 0
+
+constexpr float SMP_ROUND = 12582912.f;              // 1.5 * 2^23
 
 // Constants of the exponential, from their definitions on the host. Pairs: packed
 // arithmetic takes them from the parameters as they are.
 SampleTables make_sample_tables() {
     SampleTables t;
     const double ln2 = std::log(2.0);
-    for (int j = 0; j < 64; ++j)
-        t.fix[j] = static_cast<unsigned>(std::nearbyint(std::ldexp(std::exp2(-j / 64.0), 31)));
-    // ln(2) / 64 in three parts: 12 bits (its product with a whole number below
-    // 2^12 is exact), 24 bits, and the rest
-    const double step = ln2 / 64.0;
+    for (int j = 0; j < SMP_STEPS; ++j)
+        t.fix[j] = static_cast<unsigned>(std::nearbyint(std::ldexp(std::exp2(-j / static_cast<double>(SMP_STEPS)), 31)));
+    // ln(2) / 256 in three parts: 10 bits (its product with a whole number below
+    // 2^14 is exact), 24 bits, and the rest
+    const double step = ln2 / SMP_STEPS;
     int e;
     std::frexp(step, &e);
-    const double ulp = std::ldexp(1.0, e - 12);
+    const double ulp = std::ldexp(1.0, e - 10);
     const double c1 = std::floor(step / ulp) * ulp;
     const float c2 = static_cast<float>(step - c1);
     auto two = [](double v) { return make_float2(static_cast<float>(v), static_cast<float>(v)); };
     t.mc1 = two(-c1);
     t.mc2 = two(-c2);
     t.mc3 = two(-(step - c1 - static_cast<double>(c2)));
-    t.inv = two(64.0 / ln2);
+    t.inv = two(SMP_STEPS / ln2);
     // 1.5 * 2^23 rounds what it is added to to a whole number n, kept in its low bits; 19 is
-    // added to the n / 64 there: the shift from units of 2^-62 to 2^-43
-    const float magic = 12582912.f + 19 * 64;
+    // added to the n / 256 there: the shift from units of 2^-62 to 2^-43
+    const float magic = SMP_ROUND + 19 * SMP_STEPS;
     t.magic = two(magic);
     t.mmagic = two(-magic);
-    // exp(-r) - 1 = r (-1 + r (1 / 2 + r (-1 / 6 + r / 24))) in units of 2^-31
+    // exp(-r) - 1 = r (-1 + r (1 / 2 - r / 6)) in units of 2^-31, to 2^-42
     const double S = 2147483648.0;
-    t.p4 = two(S / 24);
     t.p3 = two(-S / 6);
     t.p2 = two(S / 2);
     t.p1 = two(-S);
+    t.round = two(SMP_ROUND);
     return t;
 }
 
@@ -83,10 +87,6 @@ typedef unsigned long long u64;
 
 // ------------------------------------------------------------------ logits in vectors of 8
 
-__device__ __forceinline__ float smp_clean(float x) {
-    // NaN becomes -infinity (never drawn), -0 becomes +0 (equal to it in the order)
-    return fmaxf(x, -INFINITY) + 0.f;
-}
 __device__ __forceinline__ void smp_unpack(const uint4 &u, float (&x)[8], const __nv_bfloat16 *) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -104,13 +104,6 @@ __device__ __forceinline__ void smp_unpack(const uint4 &u, float (&x)[8], const 
         x[2 * q + 1] = f.y;
     }
 }
-__device__ __forceinline__ uint32_t smp_pack2(float a, float b, const __nv_bfloat16 *) {
-    return (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xffff0000u);
-}
-__device__ __forceinline__ uint32_t smp_pack2(float a, float b, const __half *) {
-    const __half2 h = __floats2half2_rn(a, b);   // exact: the values are halves
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 // 8 logits at p (aligned to 16 bytes), as they are.
 template <typename T> __device__ __forceinline__ void smp_load_vec(const T *p, float (&x)[8]) {
     if constexpr (sizeof(T) == 4) {
@@ -122,28 +115,56 @@ template <typename T> __device__ __forceinline__ void smp_load_vec(const T *p, f
         smp_unpack(*reinterpret_cast<const uint4 *>(p), x, static_cast<const T *>(nullptr));
     }
 }
-template <typename T> __device__ __forceinline__ void smp_store_vec(T *p, const float (&x)[8]) {
-    if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-        const T *t = nullptr;
-        *reinterpret_cast<uint4 *>(p) = make_uint4(smp_pack2(x[0], x[1], t), smp_pack2(x[2], x[3], t),
-                                                   smp_pack2(x[4], x[5], t), smp_pack2(x[6], x[7], t));
-    }
-}
-// 8 cleaned logits from global memory; those past `n` are -infinity.
+// 8 logits from global memory; those past `n` are -infinity.
 template <typename T>
 __device__ __forceinline__ void smp_load_global(const T *p, int n, bool aligned, float (&x)[8]) {
     if (aligned && n >= 8) {
         smp_load_vec<T>(p, x);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = smp_clean(x[j]);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = j < n ? smp_clean(static_cast<float>(p[j])) : -INFINITY;
+        for (int j = 0; j < 8; ++j) x[j] = j < n ? static_cast<float>(p[j]) : -INFINITY;
     }
 }
+
+// The same as they are, to be copied (16-bit types packed), and the largest, NaN aside.
+template <typename T> struct SmpRaw {
+    uint32_t u[4];
+    __device__ __forceinline__ void load(const T *p, int n, bool aligned) {
+        if (aligned && n >= 8) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p);
+            u[0] = v.x; u[1] = v.y; u[2] = v.z; u[3] = v.w;
+        } else {
+            constexpr uint32_t MINUS_INF = std::is_same<T, __half>::value ? 0xfc00u : 0xff80u;
+            const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                u[j] = (2 * j < n ? h[2 * j] : MINUS_INF) | ((2 * j + 1 < n ? h[2 * j + 1] : MINUS_INF) << 16);
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    __device__ __forceinline__ float largest() const {
+        using V = std::conditional_t<std::is_same<T, __half>::value, __half2, __nv_bfloat162>;
+        const V *v = reinterpret_cast<const V *>(u);
+        const V m = __hmax2(__hmax2(v[0], v[1]), __hmax2(v[2], v[3]));
+        return fmaxf(static_cast<float>(m.x), static_cast<float>(m.y));
+    }
+};
+template <> struct SmpRaw<float> {
+    float x[8];
+    __device__ __forceinline__ void load(const float *p, int n, bool aligned) { smp_load_global<float>(p, n, aligned, x); }
+    __device__ __forceinline__ void store(float *p) const {
+        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    }
+    __device__ __forceinline__ float largest() const {
+        float m = x[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) m = fmaxf(m, x[j]);
+        return m;
+    }
+};
 
 // Order-preserving whole number of a logit. 16-bit types: the 32-bit pattern's low
 // bits, which are the same for all values of the type and sign, are dropped.
@@ -153,7 +174,7 @@ template <> struct SmpKey<__half> { static constexpr int DROP = 13; };
 template <> struct SmpKey<float> { static constexpr int DROP = 0; };
 
 template <typename T> __device__ __forceinline__ uint32_t smp_key(float x) {
-    const uint32_t b = __float_as_uint(x);
+    const uint32_t b = __float_as_uint(x + 0.f);   // (-0 is equal to +0)
     return (b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u)) >> SmpKey<T>::DROP;
 }
 template <typename T> __device__ __forceinline__ float smp_unkey(uint32_t key) {
@@ -178,14 +199,15 @@ __device__ __forceinline__ float smp_x(float z, const SmpRow &r) {
 
 // exp(-(m - z) / temperature) in units of 2^-43 of two logits (in packed fp32 arithmetic, which
 // halves the instructions). x is carried in two floats (xh + xl, from m - z = d + dl exactly);
-// x = n ln(2) / 64 + rr, exp(-x) = 2^-(n / 64) * (1 + q) with q = exp(-rr) - 1, |rr| < 0.0055.
+// x = n ln(2) / 256 + rr, exp(-x) = 2^-(n / 256) * (1 + q) with q = exp(-rr) - 1, |rr| < 0.0014.
 // Table and 1 + q are whole numbers of 31 bits (2^-31), their product exact; the shift by
-// n / 64 rounds to nearest. The largest logit's weight is 2^43 exactly.
+// n / 256 cuts what lies below a unit. The largest logit's weight is 2^43 exactly. (A table
+// of 64 needs one more term of q, and a conversion for the whole number of 1 + q that here
+// comes out of the last addition's rounding: |q| < 2^22 units.) NaN has weight 0.
 __device__ __forceinline__ u64 smp_finish(float kf, float q31, const unsigned *tab) {
     const unsigned n = static_cast<unsigned>(__float_as_int(kf));
-    const unsigned f = 0x80000000u + static_cast<unsigned>(__float2int_rn(q31));
-    const u64 y = (static_cast<u64>(tab[n & 63]) * f) >> ((n >> 6) & 63);
-    return (y + 1) & ~1ull;
+    const unsigned f = static_cast<unsigned>(__float_as_int(q31)) + (0x80000000u - 0x4b400000u);
+    return (static_cast<u64>(tab[n & (SMP_STEPS - 1)]) * f) >> ((n >> SMP_STEP_BITS) & 63);
 }
 __device__ __forceinline__ void smp_weight2(float z0, float z1, const SmpRow &r, const SampleTables &c,
                                             const unsigned *tab, u64 &w0, u64 &w1) {
@@ -205,10 +227,9 @@ __device__ __forceinline__ void smp_weight2(float z0, float z1, const SmpRow &r,
     xl = __ffma2_rn(nf, c.mc3, xl);
     float2 rr = __ffma2_rn(nf, c.mc1, xh);              // exact
     rr = __fadd2_rn(__ffma2_rn(nf, c.mc2, rr), xl);
-    float2 q = __ffma2_rn(rr, c.p4, c.p3);
-    q = __ffma2_rn(rr, q, c.p2);
+    float2 q = __ffma2_rn(rr, c.p3, c.p2);
     q = __ffma2_rn(rr, q, c.p1);
-    q = __fmul2_rn(rr, q);
+    q = __ffma2_rn(rr, q, c.round);
     w0 = smp_finish(k.x, q.x, tab);
     w1 = smp_finish(k.y, q.y, tab);
 }
@@ -307,11 +328,11 @@ struct SmpShared {
     SmpSums part[SMP_WARPS];              // of every warp of this CTA
     uint32_t listed;                      // entries of `list` (or more, if it overflowed)
     float t0;
-    unsigned tab[64];
+    unsigned tab[SMP_STEPS];
 };
 
 // The warp's part of the row: `n` logits from index `first` on, in shared memory
-// (cleaned, filled up to a multiple of 8 with -infinity) or in global memory.
+// (filled up to a multiple of 8 with -infinity) or in global memory.
 template <typename T, bool SMEM> struct SmpChunk {
     const T *p;
     int n;
@@ -372,9 +393,9 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
     const float u = p.u[r];
 
     cluster_arrive();   // waited for before the first write to a peer: it has started
-    if (t < 64) sh.tab[t] = tabs.fix[t];
+    if (t < SMP_STEPS) sh.tab[t] = tabs.fix[t];
 
-    // the warp's logits: into shared memory (cleaned), and the largest
+    // the warp's logits: into shared memory, and the largest (a NaN is never it, nor above any bound)
     const long long first = (static_cast<long long>(rank) * SMP_WARPS + w) * chunk;
     const long long left = p.V - first;
     const int n = left <= 0 ? 0 : left < chunk ? static_cast<int>(left) : chunk;
@@ -389,30 +410,27 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
     if constexpr (SMEM) {
         T *mine = reinterpret_cast<T *>(smp_dyn) + static_cast<size_t>(w) * chunk;
         for (int i0 = l * 8; i0 < n; i0 += 4 * 256) {
-            float x[4][8];
+            SmpRaw<T> x[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                if (i0 + q * 256 < n) smp_load_global<T>(row + i0 + q * 256, n - i0 - q * 256, aligned, x[q]);
+                if (i0 + q * 256 < n) x[q].load(row + i0 + q * 256, n - i0 - q * 256, aligned);
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 if (i0 + q * 256 < n) {
-                    smp_store_vec<T>(mine + i0 + q * 256, x[q]);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) m = fmaxf(m, x[q][j]);
+                    x[q].store(mine + i0 + q * 256);
+                    m = fmaxf(m, x[q].largest());
                 }
         }
         ck.p = mine;
     } else {
         ck.p = row;
         for (int i0 = l * 8; i0 < n; i0 += 4 * 256) {   // (loads of four sweeps under way at once)
-            float x[4][8];
+            SmpRaw<T> x[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                smp_load_global<T>(row + i0 + q * 256, n - i0 - q * 256, aligned, x[q]);
+            for (int q = 0; q < 4; ++q)   // (-infinity past the end)
+                x[q].load(row + i0 + q * 256, n - i0 - q * 256, aligned);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) m = fmaxf(m, x[q][j]);
+            for (int q = 0; q < 4; ++q) m = fmaxf(m, x[q].largest());
         }
     }
     const int steps = (n + 255) / 256;   // sweeps of the warp over its logits
@@ -861,8 +879,8 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                 khi = smp_key<T>(m);
                 const float room = (fabsf(m) + far_x * temperature) * 1e-6f + 1e-37f;
                 const float zhi = m - near_x * temperature + room, zlo = m - far_x * temperature - room;
-                if (zhi < m) khi = smp_key<T>(zhi + 0.f);
-                if (zlo > -3e38f) klo = smp_key<T>(zlo + 0.f);
+                if (zhi < m) khi = smp_key<T>(zhi);
+                if (zlo > -3e38f) klo = smp_key<T>(zlo);
             };
             key_range(x0, x1);
             int b0 = -1;   // the bin that is searched; -1: the window has so few keys that each gets its bin
