@@ -22,6 +22,7 @@
 // so every later pass (the search for the cut, the sums, the draw) stays on chip; the
 // CTAs exchange maxima, histograms and sums through distributed shared memory. Rows
 // longer than the cluster's shared memory are read again from L2 instead.
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -1145,6 +1146,8 @@ SampleKernel sample_kernel(int dtype, bool smem, bool search) {
 
 constexpr int SMP_MAX_DYN = 160 * 1024;   // a CTA's logits; the rest of its shared memory is static
 constexpr int SMP_TWO_DYN = 83 * 1024;    // the same when two CTAs share an SM
+constexpr int SMP_MAX_CTA = 1 << 17;      // logits of a CTA: its histograms' limbs fit 32 bits
+static_assert(SMP_MAX_V <= static_cast<long long>(SMP_MAX_CTA) * SMP_MAX_CLUSTER, "the longest row must fit");
 
 }  // namespace
 
@@ -1163,18 +1166,48 @@ cudaError_t launch_sample(const SampleParams &p, int sms, cudaStream_t s) {
     if (p.N <= 0) return cudaSuccess;
     static const SampleTables tabs = make_sample_tables();
     const long long elem = p.dtype == CE_FP32 ? 4 : 2;
-    // The smallest cluster with which two CTAs fit on an SM; more CTAs per row as long as all rows
-    // run at once and a warp has more than one sweep.
-    auto chunk_of = [&](int c) { return ((p.V + c * SMP_WARPS - 1) / (c * SMP_WARPS) + 7) / 8 * 8; };
-    int cl = 1;
-    while (cl < SMP_MAX_CLUSTER &&
-           (chunk_of(cl) * SMP_WARPS * elem > SMP_TWO_DYN ||
-            (p.N * cl <= sms && chunk_of(cl) > 256)))
-        cl *= 2;
     const bool search = p.top_k || p.top_p || p.top_k_all > 0 || p.top_p_all < 1.f;
+    // CTAs per row: of 1, 2, 4 and 8 the one with the least estimated time (us). A CTA takes 0.235 us
+    // per 1000 logits and a start and exchanges that grow with the cluster; those of an SM follow one
+    // another, but two at once hide the latency that a single one shows (30 %). Rows that do not
+    // fit into shared memory twice per SM (once, where one CTA per SM is all there is) are read again
+    // from L2: 5 % more, and 30 % if the rows under way are more than it holds. Measured, us, CTAs per row
+    // 1 / 2 / 4 / 8 (*: read again):
+    //   1 x 32000 bf16            14.7   10.3    8.7    6.2
+    //   64 x 128256 bf16          60     28.5   24.6   29.3   (32 x 50257 fp16: 25.5 16.8 12.1 12.8)
+    //   100 x 32000 fp32          16.6   15.4   19.4   22.8
+    //   160 x 128256 fp32         75.7*  61.8*  53.9*  65.5
+    //   256 x 128256 bf16         78.0*  74.8*  72.1   90.3
+    //   256 x 128256 fp32         90.6*  79.7*  78.5*  100.1
+    //   512 x 50257 fp16          84.5*  74.0   96.9   146
+    //   600 x 32000 bf16          41.9   49.1   73.7   122
+    //   1024 x 128256 bf16        226*   228*   258    342
+    auto chunk_of = [&](int c) { return ((p.V + c * SMP_WARPS - 1) / (c * SMP_WARPS) + 7) / 8 * 8; };
+    constexpr double PER_LOGIT = 0.235e-3, PER_CTA[4] = {0.9, 0.9, 1.6, 2.5}, L2_ROWS = 96e6;
+    int cl = 1;
+    bool smem = false;
+    double best = 1e30;
+    for (int k = 0; k < 4; ++k) {
+        const int c = 1 << k;
+        if (k > 0 && chunk_of(c / 2) <= 256) break;   // a warp of a smaller cluster has one sweep
+        const double bytes = static_cast<double>(chunk_of(c)) * SMP_WARPS * elem;
+        if (bytes / elem > SMP_MAX_CTA) continue;
+        const long long per_sm = (p.N * c + sms - 1) / sms;
+        const bool fits = bytes <= (per_sm == 1 ? SMP_MAX_DYN : SMP_TWO_DYN);
+        const double logits = static_cast<double>(p.V) / c * PER_LOGIT;
+        double us = per_sm == 1 ? 1.3 * logits : per_sm * (logits + PER_CTA[k]);
+        if (!fits) {
+            const double rows = static_cast<double>(std::min<long long>(p.N * c, 2 * sms)) / c;
+            us *= rows * p.V * elem > L2_ROWS ? 1.3 : 1.05;
+        }
+        if (us < best) {
+            best = us;
+            cl = c;
+            smem = fits;
+        }
+    }
     const long long chunk = chunk_of(cl);
     const long long bytes = chunk * SMP_WARPS * elem;
-    const bool smem = bytes <= SMP_MAX_DYN;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = cl;

@@ -245,3 +245,21 @@ def test_ties_around_the_cut(dtype):
         for f in (dict(top_k=n_top + 1), dict(top_k=n_top + n_tie // 2 + 1), dict(top_p=0.5), dict(top_p=0.9),
                   dict(top_k=max(1, n_top), min_p=0.5)):
             check(Z, u, **f)
+
+
+@pytest.mark.parametrize("kw", [{}, {"top_k": 50}, {"top_k": 5000}, {"top_p": 0.9}, {"top_k": 3000, "top_p": 0.8},
+                                {"min_p": 0.01}, {"temperature": 0.0}])
+@pytest.mark.parametrize("n,v,dtype", [(400, 50257, torch.float32), (330, 100003, torch.bfloat16),
+                                       (170, 60000, torch.float16)])
+def test_a_row_is_drawn_the_same_in_any_batch(n, v, dtype, kw):
+    # few rows are split over many CTAs and stay in shared memory, many are read again
+    g = torch.Generator(device="cuda").manual_seed(n)
+    Z = (torch.randn(n, v, device="cuda", generator=g) * 2).to(dtype)
+    Z[1, 7] = float("nan")
+    Z[2, ::2] = -float("inf")
+    Z[3, ::3] = -0.0
+    u = torch.rand(n, device="cuda", generator=g)
+    tokens, logprobs = lce.sample_logits(Z, u, **kw)
+    for a in (0, n // 2, n - 5):
+        t, lp = lce.sample_logits(Z[a:a + 5], u[a:a + 5], **kw)
+        assert torch.equal(t, tokens[a:a + 5]) and torch.equal(lp, logprobs[a:a + 5])
