@@ -37,8 +37,8 @@ constexpr int SMP_MAX_CLUSTER = 8;
 constexpr int SMP_BINS = 256;
 constexpr int SMP_ONE_SHIFT = 43;                    // weight of the largest logit: 2^43
 constexpr float SMP_X_END = 31.f;                    // exp(-31) < 2^-44 rounds to weight 0
-// Windows of x in which a cut is searched: 0 .. 6, 6 .. 12, 12 .. 31.
-constexpr float SMP_X1 = 6.f, SMP_X2 = 12.f;
+// Bins of x in which a cut is searched: half of them for 0 .. 8, half for 8 .. 31.
+constexpr float SMP_X_MID = 8.f;
 // A short list of the largest logits, in which most cuts lie: per CTA, and in all.
 constexpr int SMP_LIST_CTA = 256, SMP_LIST = SMP_THREADS;
 constexpr int SMP_LIMB = 15;                         // bits per limb of a weight: 2^17 limbs fit 32 bits
@@ -307,9 +307,9 @@ __device__ __forceinline__ u64 warp_sum64(u64 v) {
 
 // What one CTA knows of its part of the row.
 struct alignas(16) SmpSums {
-    u64 w, w1, w2;         // weight of all, of x < SMP_X1, of x < SMP_X2
+    u64 w;                 // weight of all
     u64 wlist;             // ... of the logits on the list
-    uint32_t c, c1, c2;    // the same as counts
+    uint32_t c;            // logits of x < SMP_X_END
     uint32_t list;         // logits on the list (more than SMP_LIST_CTA: it overflowed)
 };
 struct SmpShared {
@@ -576,8 +576,8 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
         // one pass: sums over the row, and the list
         int xs = 0;
         auto sums_pass = [&](bool collect, bool counts, bool weights) {
-            u64 ws = 0, ws1 = 0, ws2 = 0, wl = 0;
-            uint32_t c = 0, c1 = 0, c2 = 0;
+            u64 ws = 0, wl = 0;
+            uint32_t c = 0;
             for (int s = 0; s < steps; ++s) {
                 float x[8];
                 ck.load(s * 256 + l * 8, x);
@@ -586,21 +586,10 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
 #pragma unroll
                     for (int j = 0; j < 8; j += 2) smp_weight2(x[j], x[j + 1], rw, tabs, sh.tab, v[j], v[j + 1]);
                 }
-                if (counts || weights) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float xx = smp_x(x[j], rw);
-                        if (counts) {
-                            c += xx < SMP_X_END ? 1u : 0u;
-                            c1 += xx < SMP_X1 ? 1u : 0u;
-                            c2 += xx < SMP_X2 ? 1u : 0u;
-                        }
-                        if (weights) {
-                            ws += v[j];
-                            if (xx < SMP_X2) ws2 += v[j];
-                            if (xx < SMP_X1) ws1 += v[j];
-                        }
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    if (counts) c += smp_x(x[j], rw) < SMP_X_END ? 1u : 0u;
+                    if (weights) ws += v[j];
                 }
                 if (collect) {
                     bool any = false;
@@ -620,49 +609,34 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
             }
             if (weights) {
                 ws = warp_sum64(ws);
-                ws1 = warp_sum64(ws1);
-                ws2 = warp_sum64(ws2);
                 wl = warp_sum64(wl);
             }
-            if (counts) {
-                c = __reduce_add_sync(0xffffffffu, c);
-                c1 = __reduce_add_sync(0xffffffffu, c1);
-                c2 = __reduce_add_sync(0xffffffffu, c2);
-            }
-            if (l == 0) sh.part[w] = SmpSums{ws, ws1, ws2, wl, c, c1, c2, 0};
+            if (counts) c = __reduce_add_sync(0xffffffffu, c);
+            if (l == 0) sh.part[w] = SmpSums{ws, wl, c, 0};
             __syncthreads();
             // lane k of warp 0 gives the CTA's sums to CTA k
             if (w == 0) {
-                SmpSums o = l < SMP_WARPS ? sh.part[l] : SmpSums{0, 0, 0, 0, 0, 0, 0, 0};
+                SmpSums o = l < SMP_WARPS ? sh.part[l] : SmpSums{0, 0, 0, 0};
                 o.w = warp_sum64(o.w);
-                o.w1 = warp_sum64(o.w1);
-                o.w2 = warp_sum64(o.w2);
                 o.wlist = warp_sum64(o.wlist);
                 o.c = __reduce_add_sync(0xffffffffu, o.c);
-                o.c1 = __reduce_add_sync(0xffffffffu, o.c1);
-                o.c2 = __reduce_add_sync(0xffffffffu, o.c2);
                 o.list = sh.listed;
                 if (l < static_cast<int>(cl)) {
                     const uint32_t at = map_to_rank(&sh.sums[xs][rank], l);
                     auto hi = [](u64 v) { return static_cast<uint32_t>(v >> 32); };
                     auto lo = [](u64 v) { return static_cast<uint32_t>(v); };
-                    st_cluster_v4(at, lo(o.w), hi(o.w), lo(o.w1), hi(o.w1));
-                    st_cluster_v4(at + 16, lo(o.w2), hi(o.w2), lo(o.wlist), hi(o.wlist));
-                    st_cluster_v4(at + 32, o.c, o.c1, o.c2, o.list);
+                    st_cluster_v4(at, lo(o.w), hi(o.w), lo(o.wlist), hi(o.wlist));
+                    st_cluster_v4(at + 16, o.c, o.list, 0u, 0u);
                 }
             }
             cluster_sync_all();
-            SmpSums all = {0, 0, 0, 0, 0, 0, 0, 0};
+            SmpSums all = {0, 0, 0, 0};
             bool over = false;
             for (uint32_t k = 0; k < cl; ++k) {
                 const SmpSums &o = sh.sums[xs][k];
                 all.w += o.w;
-                all.w1 += o.w1;
-                all.w2 += o.w2;
                 all.wlist += o.wlist;
                 all.c += o.c;
-                all.c1 += o.c1;
-                all.c2 += o.c2;
                 all.list += o.list;
                 over |= o.list > SMP_LIST_CTA;
             }
@@ -735,7 +709,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
             sum = sums_pass(false, true, by_weight);
         }
 
-        // ---- the general search: histograms of the window that holds the cut
+        // ---- the general search: a histogram of x, then of the keys in the bin that holds the cut
         int hb = 0;   // histogram in use
         auto clear = [&]() {
             for (int k = t; k < 4 * SMP_BINS; k += SMP_THREADS) (&sh.hist[hb][0][0])[k] = 0u;
@@ -825,54 +799,46 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
             __syncthreads();
         };
 
-        // first level: the window x0 <= x < x1 in steps of (x1 - x0) / 256
-        int loaded = -1;
-        float x0 = 0.f, x1 = 0.f, per_x = 0.f;
+        // first level: bins of x
+        bool loaded = false;
         uint32_t tot_c = 0;
         u64 tot_w = 0;
+        constexpr int HALF = SMP_BINS / 2;
+        constexpr float NEAR = HALF / SMP_X_MID, FAR = HALF / (SMP_X_END - SMP_X_MID);   // bins per unit of x
         auto bin_of = [&](float z) {
             const float xx = smp_x(z, rw);
-            return xx >= x0 && xx < x1 ? min(static_cast<int>((xx - x0) * per_x), SMP_BINS - 1) : -1;
+            if (!(xx < SMP_X_END)) return -1;
+            return xx < SMP_X_MID ? static_cast<int>(xx * NEAR)
+                                  : min(HALF + static_cast<int>((xx - SMP_X_MID) * FAR), SMP_BINS - 1);
         };
-        auto set_window = [&](int window) {
-            x0 = window == 0 ? 0.f : window == 1 ? SMP_X1 : SMP_X2;
-            x1 = window == 0 ? SMP_X1 : window == 1 ? SMP_X2 : SMP_X_END;
-            per_x = static_cast<float>(SMP_BINS) / (x1 - x0);
+        auto bin_start = [&](int b) {
+            return b < HALF ? static_cast<float>(b) / NEAR : SMP_X_MID + static_cast<float>(b - HALF) / FAR;
         };
-        auto first_level = [&](int window) {
-            if (window == loaded) return;
-            loaded = window;
+        auto first_level = [&]() {
+            if (loaded) return;
+            loaded = true;
             clear();
             for (int s = 0; s < steps; ++s) {
                 float x[8];
-                int bin[8];
-                bool any = false;
                 ck.load(s * 256 + l * 8, x);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    bin[j] = bin_of(x[j]);
-                    any |= bin[j] >= 0;
-                }
-                if (!__any_sync(0xffffffffu, any)) continue;
                 u64 v[8];
                 if (by_weight) {
 #pragma unroll
                     for (int j = 0; j < 8; j += 2) smp_weight2(x[j], x[j + 1], rw, tabs, sh.tab, v[j], v[j + 1]);
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (bin[j] >= 0) smp_hist_add(sh.hist[hb], bin[j], by_count, by_weight, by_weight ? v[j] : 0ull);
+                for (int j = 0; j < 8; ++j) {
+                    const int bin = bin_of(x[j]);
+                    if (bin >= 0) smp_hist_add(sh.hist[hb], bin, by_count, by_weight, by_weight ? v[j] : 0ull);
+                }
             }
             totals(sh.l0c, sh.l0w, &tot_c, &tot_w, false, 0u);
         };
 
         // the key and the number of equal logits at which `target` is reached
         auto search = [&](bool count, u64 target, uint32_t *key, uint32_t *ties, u64 *kept_w) {
-            const u64 end1 = count ? sum.c1 : sum.w1, end2 = count ? sum.c2 : sum.w2;
-            const int window = target <= end1 ? 0 : target <= end2 ? 1 : 2;
-            uint32_t base_c = window == 0 ? 0u : window == 1 ? sum.c1 : sum.c2;
-            u64 base_w = window == 0 ? 0ull : window == 1 ? sum.w1 : sum.w2;
-            set_window(window);
+            uint32_t base_c = 0;
+            u64 base_w = 0;
             // keys that include those of x from near_x to far_x, with room for the roundings
             uint32_t klo, khi;
             auto key_range = [&](float near_x, float far_x) {
@@ -883,16 +849,16 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                 if (zhi < m) khi = smp_key<T>(zhi);
                 if (zlo > -3e38f) klo = smp_key<T>(zlo);
             };
-            key_range(x0, x1);
-            int b0 = -1;   // the bin that is searched; -1: the window has so few keys that each gets its bin
+            key_range(0.f, SMP_X_END);
+            int b0 = -1;   // the bin that is searched; -1: there are so few keys that each gets its bin
             if (khi - klo >= SMP_BINS) {
-                first_level(window);
-                find(sh.l0c, sh.l0w, tot_c, tot_w, count, target - (count ? static_cast<u64>(base_c) : base_w));
+                first_level();
+                find(sh.l0c, sh.l0w, tot_c, tot_w, count, target);
                 b0 = sh.bin;
-                base_c += sh.bc;
-                base_w += sh.bw;
+                base_c = sh.bc;
+                base_w = sh.bw;
                 __syncthreads();
-                key_range(x0 + static_cast<float>(b0) / per_x, x0 + static_cast<float>(b0 + 1) / per_x);
+                key_range(bin_start(b0), bin_start(b0 + 1));
             }
             for (int level = 0; klo != khi && level < 4; ++level) {   // 8 bits of the key at a time
                 const int bits = 32 - __clz(khi - klo);
