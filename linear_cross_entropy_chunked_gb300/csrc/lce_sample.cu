@@ -41,6 +41,9 @@ constexpr float SMP_X_END = 31.f;                    // exp(-31) < 2^-44 rounds 
 constexpr float SMP_X_MID = 8.f;
 // A short list of the largest logits, in which most cuts lie: per CTA, and in all.
 constexpr int SMP_LIST_CTA = 256, SMP_LIST = SMP_THREADS;
+constexpr int SMP_MAX_CTA = 1 << 17;                 // logits of a CTA: its histograms' limbs fit 32 bits
+constexpr int SMP_SWEEPS = SMP_MAX_CTA / SMP_WARPS / 256;
+static_assert(SMP_SWEEPS == 32, "one lane per sweep of a warp");
 constexpr int SMP_LIMB = 15;                         // bits per limb of a weight: 2^17 limbs fit 32 bits
 
 constexpr int SMP_STEP_BITS = 8, SMP_STEPS = 1 << SMP_STEP_BITS;   // the exponential's table: 2^(-j / 256)
@@ -329,6 +332,8 @@ struct SmpShared {
     SmpSums part[SMP_WARPS];              // of every warp of this CTA
     uint32_t listed;                      // entries of `list` (or more, if it overflowed)
     float t0;
+    u64 sweep_w[SMP_SWEEPS];              // sums of the sweeps over one warp's part
+    uint32_t sweep_t[SMP_SWEEPS];
     unsigned tab[SMP_STEPS];
 };
 
@@ -979,16 +984,13 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
         if (l >= o) before_t += v;
     }
     before_t -= lane_t;
-    u64 lane_w = 0, my_before = 0;
-    uint32_t my_ties_before = 0;
+    const uint32_t lane_t0 = before_t;
+    u64 lane_w = 0;
 #pragma unroll
     for (int q = 0; q < PER_LANE; ++q) {
-        if (l * PER_LANE + q == me) {
-            my_before = lane_w;
-            my_ties_before = before_t;
-        }
         const uint32_t room = before_t < cut_ties ? cut_ties - before_t : 0u;
-        lane_w += ew[q] + static_cast<u64>(et[q] < room ? et[q] : room) * tie_w;
+        ew[q] += static_cast<u64>(et[q] < room ? et[q] : room) * tie_w;
+        lane_w += ew[q];
         before_t += et[q];
     }
     u64 incl = lane_w;
@@ -998,57 +1000,88 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
         if (l >= o) incl += v;
     }
     const u64 total = __shfl_sync(0xffffffffu, incl, 31);
-    const int owner = me / PER_LANE;
-    const u64 my_first = __shfl_sync(0xffffffffu, my_before + incl - lane_w, owner);
-    my_ties_before = __shfl_sync(0xffffffffu, my_ties_before, owner);
-    const uint32_t my_room = my_ties_before < cut_ties ? cut_ties - my_ties_before : 0u;
-    const u64 my_sum = above + static_cast<u64>(ties < my_room ? ties : my_room) * tie_w;
 
-    // the first index whose cumulative weight exceeds u * total
+    // The first index whose cumulative weight exceeds u * total: the warp in whose part it lies, ...
     const u64 target = draw_target(total);
-    if (target >= my_first && target - my_first < my_sum) {
-        // the sweep in which the target lies: sums of several sweeps at once, whose loads and
-        // shuffles do not wait for one another
-        constexpr int GROUP = 4;
-        u64 run = my_first;
-        uint32_t seen = my_ties_before;
-        int sweep = steps == 1 ? 0 : -1;
-        for (int s0 = 0; sweep < 0 && s0 < steps; s0 += GROUP) {
-            u64 sums[GROUP];
-            uint32_t same[GROUP];
+    const int lane = __ffs(__ballot_sync(0xffffffffu, incl > target)) - 1;   // (always one: total > target)
+    u64 run = incl - lane_w;   // kept weight and ties before the part
+    uint32_t seen = lane_t0;
+    int part = l * PER_LANE;
+    bool passed = true;
 #pragma unroll
-            for (int g = 0; g < GROUP; ++g) {
+    for (int q = 0; q < PER_LANE; ++q) {
+        passed = passed && run + ew[q] <= target;
+        if (passed) {
+            run += ew[q];
+            seen += et[q];
+            ++part;
+        }
+    }
+    run = __shfl_sync(0xffffffffu, run, lane);
+    seen = __shfl_sync(0xffffffffu, seen, lane);
+    part = __shfl_sync(0xffffffffu, part, lane);
+    if (part / SMP_WARPS != static_cast<int>(rank)) return;   // (nothing of a peer's is touched after the exchange)
+    // ... the sweep of that part, whose sums the CTA's warps form side by side (one warp
+    // alone took 5 of 72 us for 64 rows of 128256 with top-p), ...
+    {
+        const long long first = static_cast<long long>(part) * chunk;
+        const long long left = p.V - first;
+        ck.n = left <= 0 ? 0 : left < chunk ? static_cast<int>(left) : chunk;
+        if constexpr (SMEM) {
+            ck.p = reinterpret_cast<const T *>(smp_dyn) + static_cast<size_t>(part % SMP_WARPS) * chunk;
+        } else {
+            ck.p = static_cast<const T *>(p.Z) + r * p.ld + (ck.n > 0 ? first : 0);
+            ck.aligned = (reinterpret_cast<uintptr_t>(ck.p) & 15u) == 0;
+        }
+        const int sweeps = (ck.n + 255) / 256;
+        int sweep = 0;
+        if (sweeps > 1) {
+            for (int s = w; s < sweeps; s += SMP_WARPS) {
                 float x[8];
-                u64 v[8];
-                ck.load((s0 + g) * 256 + l * 8, x);   // (nothing past the end)
+                u64 v[8], sum = 0;
+                uint32_t same = 0;
+                ck.load(s * 256 + l * 8, x);
                 kept_weights(x, v);
-                sums[g] = 0;
-                same[g] = 0;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    sums[g] += v[j];
-                    same[g] += have_cut && x[j] == cut ? 1u : 0u;
+                    sum += v[j];
+                    same += have_cut && x[j] == cut ? 1u : 0u;
+                }
+                sum = warp_sum64(sum);
+                if (have_cut) same = __reduce_add_sync(0xffffffffu, same);
+                if (l == 0) {
+                    sh.sweep_w[s] = sum;
+                    sh.sweep_t[s] = same;
                 }
             }
+            __syncthreads();
+            if (w != 0) return;
+            u64 sum = l < sweeps ? sh.sweep_w[l] : 0ull;
+            const uint32_t same = l < sweeps ? sh.sweep_t[l] : 0u;
+            uint32_t upto = same;
 #pragma unroll
-            for (int g = 0; g < GROUP; ++g) {
-                sums[g] = warp_sum64(sums[g]);
-                if (have_cut) same[g] = __reduce_add_sync(0xffffffffu, same[g]);
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t c = __shfl_up_sync(0xffffffffu, upto, o);
+                if (l >= o) upto += c;
             }
+            const uint32_t before = seen + upto - same;
+            const uint32_t room = before < cut_ties ? cut_ties - before : 0u;
+            sum += static_cast<u64>(same < room ? same : room) * tie_w;
+            u64 in = sum;
 #pragma unroll
-            for (int g = 0; g < GROUP; ++g) {
-                if (sweep >= 0) continue;
-                const uint32_t room = seen < cut_ties ? cut_ties - seen : 0u;
-                const u64 all = sums[g] + static_cast<u64>(same[g] < room ? same[g] : room) * tie_w;
-                if (run + all > target) {
-                    sweep = s0 + g;
-                } else {
-                    run += all;
-                    seen += same[g];
-                }
+            for (int o = 1; o < 32; o <<= 1) {
+                const u64 c = shfl_up64(in, o);
+                if (l >= o) in += c;
             }
+            // (one is always found, unless Z changes meanwhile)
+            sweep = max(__ffs(__ballot_sync(0xffffffffu, run + in > target)) - 1, 0);
+            run += __shfl_sync(0xffffffffu, in - sum, sweep);
+            seen = __shfl_sync(0xffffffffu, before, sweep);
+        } else if (w != 0) {
+            return;
         }
-        const int i = max(sweep, 0) * 256 + l * 8;   // (always found, unless Z changes meanwhile)
+        // ... and the index
+        const int i = sweep * 256 + l * 8;
         float x[8];
         u64 v[8];
         uint32_t tmask = 0;
@@ -1095,7 +1128,6 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
             answer(first + i + at, z, total);
         }
     }
-    // (nothing of a peer's is touched after the sums' exchange: a CTA may leave)
 }
 
 using SampleKernel = void (*)(const SampleParams, const SampleTables, const int);
@@ -1112,7 +1144,6 @@ SampleKernel sample_kernel(int dtype, bool smem, bool search) {
 
 constexpr int SMP_MAX_DYN = 160 * 1024;   // a CTA's logits; the rest of its shared memory is static
 constexpr int SMP_TWO_DYN = 83 * 1024;    // the same when two CTAs share an SM
-constexpr int SMP_MAX_CTA = 1 << 17;      // logits of a CTA: its histograms' limbs fit 32 bits
 static_assert(SMP_MAX_V <= static_cast<long long>(SMP_MAX_CTA) * SMP_MAX_CLUSTER, "the longest row must fit");
 
 }  // namespace
