@@ -37,7 +37,7 @@ constexpr int SMP_MAX_CLUSTER = 8;
 constexpr int SMP_BINS = 256;
 constexpr int SMP_ONE_SHIFT = 43;                    // weight of the largest logit: 2^43
 constexpr float SMP_X_END = 31.f;                    // exp(-31) < 2^-44 rounds to weight 0
-// Bins of x in which a cut is searched: half of them for 0 .. 8, half for 8 .. 31.
+// Bins of x in which a cut is searched: half of them up to 8, half from there to 31.
 constexpr float SMP_X_MID = 8.f;
 // A short list of the largest logits, in which most cuts lie: per CTA, and in all.
 constexpr int SMP_LIST_CTA = 256, SMP_LIST = SMP_THREADS;
@@ -586,15 +586,18 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
             for (int s = 0; s < steps; ++s) {
                 float x[8];
                 ck.load(s * 256 + l * 8, x);
-                u64 v[8];
                 if (weights) {
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2) smp_weight2(x[j], x[j + 1], rw, tabs, sh.tab, v[j], v[j + 1]);
+                    for (int j = 0; j < 8; j += 2) {
+                        u64 v0, v1;
+                        smp_weight2(x[j], x[j + 1], rw, tabs, sh.tab, v0, v1);
+                        ws += v0;
+                        ws += v1;
+                    }
                 }
+                if (counts) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (counts) c += smp_x(x[j], rw) < SMP_X_END ? 1u : 0u;
-                    if (weights) ws += v[j];
+                    for (int j = 0; j < 8; ++j) c += smp_x(x[j], rw) < SMP_X_END ? 1u : 0u;
                 }
                 if (collect) {
                     bool any = false;
@@ -607,7 +610,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                             const uint32_t at = atomicAdd(&sh.listed, 1u);
                             const uint32_t index = static_cast<uint32_t>(first) + s * 256 + l * 8 + j;
                             if (at < SMP_LIST_CTA) sh.list[at] = (static_cast<u64>(smp_key<T>(x[j])) << 32) | ~index;
-                            if (weights) wl += v[j];
+                            if (weights) wl += smp_weight(x[j], rw, tabs, sh.tab);   // (few: cheaper than 8 kept)
                         }
                     }
                 }
@@ -808,16 +811,18 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
         bool loaded = false;
         uint32_t tot_c = 0;
         u64 tot_w = 0;
-        constexpr int HALF = SMP_BINS / 2;
-        constexpr float NEAR = HALF / SMP_X_MID, FAR = HALF / (SMP_X_END - SMP_X_MID);   // bins per unit of x
+        // bin: the lesser of two lines in x, rounded to nearest by adding SMP_ROUND (a conversion
+        // runs at a fraction of the rate)
+        constexpr float NEAR = SMP_BINS / 2 / SMP_X_MID, FAR = (SMP_BINS / 2 - 1) / (SMP_X_END - SMP_X_MID);
+        constexpr float FAR_0 = SMP_BINS / 2 - SMP_X_MID * FAR;
         auto bin_of = [&](float z) {
             const float xx = smp_x(z, rw);
-            if (!(xx < SMP_X_END)) return -1;
-            return xx < SMP_X_MID ? static_cast<int>(xx * NEAR)
-                                  : min(HALF + static_cast<int>((xx - SMP_X_MID) * FAR), SMP_BINS - 1);
+            const float y = fminf(xx * NEAR, fmaf(xx, FAR, FAR_0));
+            return xx < SMP_X_END ? __float_as_int(y + SMP_ROUND) & (SMP_BINS - 1) : -1;
         };
         auto bin_start = [&](int b) {
-            return b < HALF ? static_cast<float>(b) / NEAR : SMP_X_MID + static_cast<float>(b - HALF) / FAR;
+            const float y = static_cast<float>(b) - 0.5f;
+            return fmaxf(y < SMP_BINS / 2 ? y / NEAR : (y - FAR_0) / FAR, 0.f);
         };
         auto first_level = [&]() {
             if (loaded) return;
@@ -826,15 +831,13 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
             for (int s = 0; s < steps; ++s) {
                 float x[8];
                 ck.load(s * 256 + l * 8, x);
-                u64 v[8];
-                if (by_weight) {
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2) smp_weight2(x[j], x[j + 1], rw, tabs, sh.tab, v[j], v[j + 1]);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int bin = bin_of(x[j]);
-                    if (bin >= 0) smp_hist_add(sh.hist[hb], bin, by_count, by_weight, by_weight ? v[j] : 0ull);
+                for (int j = 0; j < 8; j += 2) {
+                    u64 v0 = 0, v1 = 0;
+                    if (by_weight) smp_weight2(x[j], x[j + 1], rw, tabs, sh.tab, v0, v1);
+                    const int b0 = bin_of(x[j]), b1 = bin_of(x[j + 1]);
+                    if (b0 >= 0) smp_hist_add(sh.hist[hb], b0, by_count, by_weight, v0);
+                    if (b1 >= 0) smp_hist_add(sh.hist[hb], b1, by_count, by_weight, v1);
                 }
             }
             totals(sh.l0c, sh.l0w, &tot_c, &tot_w, false, 0u);
@@ -932,10 +935,15 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
     auto kept_weights = [&](const float (&x)[8], u64 (&v)[8]) {
 #pragma unroll
         for (int j = 0; j < 8; j += 2) smp_weight2(x[j], x[j + 1], rw, tabs, sh.tab, v[j], v[j + 1]);
-        if (have_cut || w_min) {
+        if (have_cut) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (!(x[j] > cut) || v[j] < w_min) v[j] = 0ull;
+                if (!(x[j] > cut)) v[j] = 0ull;
+        }
+        if (w_min) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (v[j] < w_min) v[j] = 0ull;
         }
     };
 
