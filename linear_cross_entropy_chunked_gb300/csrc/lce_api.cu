@@ -1144,8 +1144,14 @@ lce_status fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t sa_ro
     p.N = static_cast<int>(N);
     p.KB = static_cast<int>(cdiv(K, 128));
     const long long pair_tiles = cdiv(M, 256) * cdiv(N, 256), tiles = cdiv(M, 128) * cdiv(N, 128);
-    const bool pair = M > 128 && pairs > 0 && pair_tiles >= pairs / 2;
+    // Pairs of CTAs as soon as 128 x 128 tiles would not all run at once (us, tiles / pairs: 512 x 4864 x 4096,
+    // 152 tiles, 18.5 / 20.2; 1531 x 1600 x 4096, 156 tiles, 29.0 / 20.2; 200 x 32000 x 4096 52 / 40;
+    // 256 x 4864 x 4096 14.9 / 19.7). Up to 128 rows half of a pair would have none.
+    const bool pair = M > 128 && pairs > 0 && tiles > sms;
     if (tiles > 0x7fffffffll) return LCE_ERR_INVALID_ARG;
+    // A tile is split along k over 2, 4 or 8 CTAs while all run at once and each keeps 2 k blocks (us,
+    // split in 1 / 2 / 4 / 8: 8 x 1600 x 50257, 13 tiles, 126 / 67 / 37 / 23; 64 x 4096 x 4096, 32 tiles, 16.9 /
+    // 13.4 / 9.7 / 22.7; 64 x 12800 x 4096, 100 tiles, 18.6 / 29.2 / 29.5 / 54).
     int split = 1;
     if (!pair)
         while (split < 8 && tiles * split * 2 <= sms && p.KB >= split * 4) split *= 2;
@@ -1154,7 +1160,8 @@ lce_status fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t sa_ro
     p.tiles = static_cast<int>(pair ? pair_tiles : tiles);
     p.a_box_rows = pair || M >= 128 ? 128 : static_cast<int>(align_up(static_cast<size_t>(M), 8));
     p.n_bulk = static_cast<int>(N / (16 / elem) * (16 / elem));
-    // what 192 KB hold of A's rows and 128 rows of B (a multiple of 1 KB each), as barriers allow
+    // what 192 KB hold of A's rows and 128 rows of B (a multiple of 1 KB each), as barriers allow (6 stages /
+    // 11: 1 x 128256 x 4096 86.7 / 83.7 us, 64 x 128256 x 4096 96.3 / 94.9, 1 x 32000 x 4096 27.6 / 28.0)
     p.stages = std::min(11, 6 * 32768 / (p.a_box_rows * 128 + 16384));
     p.sa = sa;
     p.sb = sb;
@@ -1162,6 +1169,7 @@ lce_status fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t sa_ro
     p.sa_block = sa_block;
     p.sb_row = sb_row;
     p.sb_block = sb_block;
+    // (as quantize_fp8 stores them: 4096 x 8192 x 4096 183 us, one by one 241)
     p.sb_vec = sb_row == 1 && sb_block % 4 == 0 && aligned16(sb) ? 1 : 0;
     p.C = out;
     p.ldc = ldc;

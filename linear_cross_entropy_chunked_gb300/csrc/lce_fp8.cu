@@ -22,7 +22,10 @@ namespace lce {
 // One CTA per 128 x 128 tile of X, which its threads hold in registers (8 x 8 values
 // each), so X is read once for up to two outputs: row blocks or tiles in X's own layout,
 // and the same of X^T (blocks along X's rows), turned through shared memory. Bound by
-// HBM bandwidth: 2 (4) bytes read and 1 or 2 written per value.
+// HBM bandwidth: 2 (4) bytes read and 1 or 2 written per value. Measured: 4096 x 50256 bf16 in row
+// blocks 111 us (5.6 TB/s), X^T 121 us (5.1 TB/s). Rows of 16-bit values that do not start on 16
+// bytes are loaded value by value: 50257 columns take 240 us (vectors shifted into place
+// between lanes took the same).
 
 namespace {
 
@@ -81,28 +84,6 @@ template <typename T> struct QtVec {
             for (int j = 0; j < 4; ++j)
                 w[j] = (2 * j < n ? h[2 * j] : 0u) | ((2 * j + 1 < n ? static_cast<uint32_t>(h[2 * j + 1]) : 0u) << 16);
         }
-    }
-    // The same for a row that does not start on a 16-byte boundary, by a half-warp whose lane i takes
-    // values 8 i .. 8 i + 7: aligned vectors, of which each lane shifts its own and the next
-    // lane's together (the last lane loads its next one).
-    __device__ __forceinline__ void load_shifted(const T *row, int i, bool last) {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(row);
-        const uint32_t off = static_cast<uint32_t>(a & 15u);   // even
-        const uint4 *v = reinterpret_cast<const uint4 *>(a - off) + i;
-        const uint4 u = *v;
-        uint4 nx = make_uint4(__shfl_down_sync(0xffffffffu, u.x, 1, 16), __shfl_down_sync(0xffffffffu, u.y, 1, 16),
-                              __shfl_down_sync(0xffffffffu, u.z, 1, 16), __shfl_down_sync(0xffffffffu, u.w, 1, 16));
-        if (last) nx = v[1];
-        // words off / 4 .. off / 4 + 4 of the eight, then the odd halfword
-        uint32_t y[6] = {u.x, u.y, u.z, u.w, nx.x, nx.y};
-        uint32_t z[5];
-        if (off & 8u) {
-            y[0] = u.z; y[1] = u.w; y[2] = nx.x; y[3] = nx.y; y[4] = nx.z; y[5] = nx.w;
-        }
-#pragma unroll
-        for (int j = 0; j < 5; ++j) z[j] = off & 4u ? y[j + 1] : y[j];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = off & 2u ? __funnelshift_r(z[j], z[j + 1], 16) : z[j];
     }
     // largest |x| of column pair j, as two 16-bit values
     __device__ __forceinline__ uint32_t abs2(int j) const { return w[j] & 0x7fff7fffu; }
@@ -170,19 +151,9 @@ __global__ void __launch_bounds__(QT_THREADS, sizeof(T) == 4 ? 2 : 3)
     const int nc = p.C - c0 < 128 ? static_cast<int>(p.C - c0) : 128;
     const T *X = static_cast<const T *>(p.X) + r0 * p.ld + c0;
     V x[8];
-    // Rows that start anywhere: the aligned vectors that hold a whole tile's rows, which reach up
-    // to 16 bytes past it on either side, lie within X.
-    const bool shifted = PACKED && !p.vec && nr == 128 && nc == 128 && tile > 0 &&
-                         (c0 + 136 <= p.C || r0 + 128 < p.R);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const int r = g * 8 + k;
-        if constexpr (PACKED) {
-            if (shifted) {
-                x[k].load_shifted(X + static_cast<long long>(r) * p.ld, i, i == 15);
-                continue;
-            }
-        }
         if (r < nr && i * 8 < nc) x[k].load(X + static_cast<long long>(r) * p.ld + i * 8, nc - i * 8, p.vec != 0);
         else memset(&x[k], 0, sizeof(V));
     }
@@ -351,11 +322,20 @@ cudaError_t launch_fp8_quantize(const Fp8QuantParams &p, int dtype, bool tile, c
 // and half of B's), for products with many tiles. Otherwise 128 x 128 tiles, one CTA
 // each; few tiles are split along k over a cluster of up to 8 CTAs, whose fp32 sums are
 // added through distributed shared memory in rank order.
+// Measured with tile scales: 4096 x 8192 x 4096 113 us (2440 TFLOP/s), 4096 x 128256 x 4096 1610 us
+// (2680 TFLOP/s), 64 x 128256 x 4096 95 us (5.7 TB/s), 1 x 32000 x 4096 28 us (4.7 TB/s; 250 tiles are
+// 1.6 per SM). Pairs are bound by the operands' way from L2 into shared memory (32 KB per SM
+// and k block in 0.40 us; with a quarter of the MMAs and no reads of TMEM 4096 x 8192 x 4096 takes 89 us),
+// then by the handing over of TMEM buffers. Few rows: by HBM.
+//
 // B_ROWS: B's scales are per row (gradient of a weight); every warp brings those of its
 // columns into shared memory of its own. With a whole row of 128 columns per thread, as
 // the tiles' path has it, every thread would read all 128 scales per k block: 512 bytes per warp
 // and load, 1024 cycles of the shared memory's return path for the CTA. So TMEM is read in the
 // layout of matrix fragments: a thread holds 4 rows x 32 columns and reads a quarter of the scales.
+// 4096 x 8192 x 4096 takes 183 us, 32000 x 4096 x 2048 389 us: twice the multiplications per value, and
+// two warps per scheduler that do not hide one another's latency (149 us without scale loads
+// and products; no registers for more columns ahead).
 // Every mbarrier wait is bounded, as in the bf16 GEMM. The waits for TMEM buffers acquire at
 // CTA scope and their remote arrivals are relaxed: no memory is handed over with them (the
 // tcgen05 fences order TMEM), and cluster scope costs a flush or an L1 invalidation per
@@ -376,7 +356,9 @@ constexpr int F8_THREADS = 384;
 // 256 * 216 + 128 * 72 = 384 * 168.
 constexpr int F8_REGS = 168, F8_REGS_CONSUMER = 216, F8_REGS_OTHER = 72;
 static_assert(256 * F8_REGS_CONSUMER + 128 * F8_REGS_OTHER <= F8_THREADS * F8_REGS, "register split");
-constexpr int F8_GROUP = 16;               // row tiles that run together (they share B in L2)
+// Row tiles that run together (they share B in L2): 16384 x 32000 x 4096 takes 1612 us with 16, 1614 with
+// 4 or 8 and 1841 with 64; 4096 x 8192 x 4096 114, 118 to 120 and 114.
+constexpr int F8_GROUP = 16;
 
 // Instruction descriptor of tcgen05.mma kind::f8f6f4, e4m3 x e4m3 -> fp32, both K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
