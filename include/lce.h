@@ -289,11 +289,14 @@ lce_status lce_sample_logits(const void *Z, int z_dtype, int64_t ld, int64_t N, 
  * dlogits W (dlogits in rows, W^T in tiles); dW = dlogits^T x (both transposed, in rows).
  * A, B, out 16-byte aligned; lda, ldb and ldc's bytes multiples of 16; K, lda, ldb in
  * values = bytes. Columns of `out` from N on are left as they were. Workspace: a header
- * for the device status (lce_read_status), lce_fp8_matmul_workspace_size bytes. */
+ * for the device status (lce_read_status), lce_fp8_matmul_workspace_size bytes; with
+ * lce_fp8_matmul_best_workspace_size bytes (which asks the current device) products with few
+ * tiles of out and a long K are also shared out along K, their fp32 parts kept there. */
 lce_status lce_fp8_quantize(const void *X, int x_dtype, int64_t ld, int64_t R, int64_t C, int tiles,
                             void *q, int64_t ldq, float *scale, void *qt, int64_t ldqt,
                             float *scale_t, lce_stream_t stream);
 lce_status lce_fp8_matmul_workspace_size(size_t *bytes);
+lce_status lce_fp8_matmul_best_workspace_size(int64_t M, int64_t N, int64_t K, int b_rows, size_t *bytes);
 lce_status lce_fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t sa_row,
                           int64_t sa_block, const void *B, int64_t ldb, const float *sb,
                           int64_t sb_row, int64_t sb_block, int b_rows, int64_t M, int64_t N,

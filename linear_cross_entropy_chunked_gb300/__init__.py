@@ -46,6 +46,7 @@ from .fp8 import (  # noqa: F401
     FP8Weight,
     fp8_linear,
     fp8_matmul,
+    fp8_matmul_workspace_size,
     fp8_weight,
     quantize_fp8,
 )

@@ -58,6 +58,7 @@ EXPORTED = (
     "lce_sample_logits",
     "lce_fp8_quantize",
     "lce_fp8_matmul_workspace_size",
+    "lce_fp8_matmul_best_workspace_size",
     "lce_fp8_matmul",
     "lce_fp8_linear_workspace_size",
     "lce_fp8_linear",
@@ -155,6 +156,7 @@ def lib() -> ctypes.CDLL:
     L.lce_fp8_quantize.argtypes = [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp,
                                    _vp, _i64, _vp, _vp]
     L.lce_fp8_matmul_workspace_size.argtypes = [_sz]
+    L.lce_fp8_matmul_best_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.c_int, _sz]
     L.lce_fp8_matmul.argtypes = [_vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, ctypes.c_int,
                                  _i64, _i64, _i64, _vp, _i64, ctypes.c_int, _vp, ctypes.c_size_t, _vp]
     L.lce_fp8_linear_workspace_size.argtypes = [_i64, _i64, _sz]
@@ -187,6 +189,7 @@ def lib() -> ctypes.CDLL:
                  "lce_fwd_bwd_sharded", "lce_noalloc_read_status", "lce_forward_noalloc",
                  "lce_sample_logits", "lce_grad_norm_workspace_size", "lce_grad_norm",
                  "lce_clip_grad_norm", "lce_fp8_quantize", "lce_fp8_matmul_workspace_size",
+                 "lce_fp8_matmul_best_workspace_size",
                  "lce_fp8_matmul", "lce_fp8_linear_workspace_size", "lce_fp8_linear"):
         getattr(L, name).restype = ctypes.c_int
     _LIB = L

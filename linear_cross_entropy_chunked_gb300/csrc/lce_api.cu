@@ -1121,6 +1121,35 @@ lce_status fp8_matmul_check(const void *A, int64_t lda, const float *sa, int64_t
     return LCE_OK;
 }
 
+// In how many parts of k the tiles of a product by CTA pairs are taken (tile scales only): what the
+// last, partly filled wave of tiles leaves idle is shared out. One wave of tiles takes 0.46 us per
+// k block, the parts are written and read at about 5 bytes per ns, and their sum is one
+// launch. (us, one part / as chosen: 1531 x 1600 x 50257, 42 tiles for 76 pairs, 182 / 145; 700 x 4001 x 33001
+// 124 / 102; 1537 x 1701 x 20000 79 / 69; 2049 x 1290 x 50000 184 / 165.)
+int fp8_parts(long long tiles, long long M, long long N, long long KB, int pairs) {
+    int best = 1;
+    double best_us = 1e30;
+    for (int n = 1; n <= 8 && KB >= 16 * n; ++n) {
+        const double us = 0.46 * static_cast<double>(cdiv(tiles * n, pairs)) * static_cast<double>(cdiv(KB, n)) +
+                          (n > 1 ? 5.0 + 8.0 * n * static_cast<double>(M) * static_cast<double>(N) / 5e6 : 0.0);
+        if (us < best_us * 0.97) {
+            best = n;
+            best_us = us;
+        }
+    }
+    return best;
+}
+bool fp8_pairs(int64_t M, int64_t N, int sms, int pairs) {
+    // Pairs of CTAs as soon as 128 x 128 tiles would not all run at once (us, tiles / pairs: 512 x 4864 x 4096,
+    // 152 tiles, 18.5 / 20.2; 1531 x 1600 x 4096, 156 tiles, 29.0 / 20.2; 200 x 32000 x 4096 52 / 40;
+    // 256 x 4864 x 4096 14.9 / 19.7). Up to 128 rows half of a pair would have none.
+    return M > 128 && pairs > 0 && cdiv(M, 128) * cdiv(N, 128) > sms;
+}
+size_t fp8_parts_bytes(int64_t M, int64_t N, int parts) {
+    return parts > 1 ? sizeof(float) * static_cast<size_t>(parts) * cdiv(M, 256) * 256 *
+                           align_up(static_cast<size_t>(N), 32) : 0;
+}
+
 // after_quantize: A comes from the quantisation launched just before on the same stream,
 // which the product's prologue may overlap
 lce_status fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t sa_row, int64_t sa_block,
@@ -1144,10 +1173,7 @@ lce_status fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t sa_ro
     p.N = static_cast<int>(N);
     p.KB = static_cast<int>(cdiv(K, 128));
     const long long pair_tiles = cdiv(M, 256) * cdiv(N, 256), tiles = cdiv(M, 128) * cdiv(N, 128);
-    // Pairs of CTAs as soon as 128 x 128 tiles would not all run at once (us, tiles / pairs: 512 x 4864 x 4096,
-    // 152 tiles, 18.5 / 20.2; 1531 x 1600 x 4096, 156 tiles, 29.0 / 20.2; 200 x 32000 x 4096 52 / 40;
-    // 256 x 4864 x 4096 14.9 / 19.7). Up to 128 rows half of a pair would have none.
-    const bool pair = M > 128 && pairs > 0 && tiles > sms;
+    const bool pair = fp8_pairs(M, N, sms, pairs);
     if (tiles > 0x7fffffffll) return LCE_ERR_INVALID_ARG;
     // A tile is split along k over 2, 4 or 8 CTAs while all run at once and each keeps 2 k blocks (us,
     // split in 1 / 2 / 4 / 8: 8 x 1600 x 50257, 13 tiles, 126 / 67 / 37 / 23; 64 x 4096 x 4096, 32 tiles, 16.9 /
@@ -1176,15 +1202,27 @@ lce_status fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t sa_ro
     p.c_type = c_dtype;
     p.hdr = static_cast<int *>(ws);
     p.timeout_ns = kDefaultTimeoutNs;
-    const MapType ct = c_dtype == CE_FP32 ? MAP_F32 : c_dtype == CE_FP16 ? MAP_F16 : MAP_BF16;
+    p.parts = pair && !b_rows ? fp8_parts(pair_tiles, M, N, p.KB, pairs) : 1;
+    if (p.parts > 1 && ws_bytes < 1024 + fp8_parts_bytes(M, N, p.parts)) p.parts = 1;
+    if (p.parts > 1) {
+        p.C = static_cast<uint8_t *>(ws) + 1024;
+        p.ldc = static_cast<long long>(align_up(static_cast<size_t>(N), 32));
+        p.c_type = CE_FP32;
+        p.n_bulk = static_cast<int>(p.ldc);
+    }
+    const MapType ct = p.c_type == CE_FP32 ? MAP_F32 : c_dtype == CE_FP16 ? MAP_F16 : MAP_BF16;
+    const long long c_rows = p.parts > 1 ? static_cast<long long>(p.parts) * p.m_tiles * 256 : M;
     if (!encode_2d(&p.tmA, A, K, M, lda, 128, p.a_box_rows, MAP_U8) ||
         !encode_2d(&p.tmB, B, K, N, ldb, 128, 128, MAP_U8) ||
-        (p.n_bulk > 0 && !encode_store_2d(&p.tmC, out, p.n_bulk, M, ldc * elem, ct, 32)))
+        (p.n_bulk > 0 &&
+         !encode_store_2d(&p.tmC, p.C, p.n_bulk, c_rows, p.ldc * (p.c_type == CE_FP32 ? 4 : 2), ct, 32)))
         return LCE_ERR_CUDA;
     const int cluster = pair ? 2 : split;
     const int most = pair ? pairs : split > 1 ? p.tiles : sms;
-    const int clusters = p.tiles < most ? p.tiles : most;
+    const long long units = static_cast<long long>(p.tiles) * p.parts;
+    const int clusters = static_cast<int>(units < most ? units : most);
     LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_fp8_matmul(p, pair, b_rows != 0, cluster, clusters, after_quantize, s));
+    if (p.parts > 1) LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_fp8_parts(p, out, ldc, c_dtype, s));
     return LCE_OK;
 }
 
@@ -1712,6 +1750,16 @@ lce_status lce_fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t s
                       ldc, c_dtype, ws, ws_bytes, false, stream);
 }
 
+lce_status lce_fp8_matmul_best_workspace_size(int64_t M, int64_t N, int64_t K, int b_rows, size_t *bytes) {
+    if (!bytes || M < 0 || N < 0 || K <= 0 || M > MAX_V || N > MAX_V || K > MAX_V) return LCE_ERR_INVALID_ARG;
+    int sms = 0, pairs = 0;
+    const lce_status st = init_device(&sms, &pairs);
+    if (st != LCE_OK) return st;
+    *bytes = 1024;
+    if (!b_rows && fp8_pairs(M, N, sms, pairs))
+        *bytes += fp8_parts_bytes(M, N, fp8_parts(cdiv(M, 256) * cdiv(N, 256), M, N, cdiv(K, 128), pairs));
+    return LCE_OK;
+}
 lce_status lce_fp8_linear_workspace_size(int64_t M, int64_t K, size_t *bytes) {
     if (!bytes || M < 0 || K <= 0 || M > MAX_V || K > MAX_V) return LCE_ERR_INVALID_ARG;
     *bytes = 1024 + align_up(sizeof(float) * static_cast<size_t>(M) * cdiv(K, 128), 1024) +

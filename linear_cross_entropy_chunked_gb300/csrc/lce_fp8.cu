@@ -322,6 +322,8 @@ cudaError_t launch_fp8_quantize(const Fp8QuantParams &p, int dtype, bool tile, c
 // and half of B's), for products with many tiles. Otherwise 128 x 128 tiles, one CTA
 // each; few tiles are split along k over a cluster of up to 8 CTAs, whose fp32 sums are
 // added through distributed shared memory in rank order.
+// PARTS: pairs with a long k and few tiles (gradients of an input) take every tile in
+// several parts of k, which write fp32 sums into the workspace; lce_fp8_parts_kernel adds them in order.
 // Measured with tile scales: 4096 x 8192 x 4096 113 us (2440 TFLOP/s), 4096 x 128256 x 4096 1610 us
 // (2680 TFLOP/s), 64 x 128256 x 4096 95 us (5.7 TB/s), 1 x 32000 x 4096 28 us (4.7 TB/s; 250 tiles are
 // 1.6 per SM). Pairs are bound by the operands' way from L2 into shared memory (32 KB per SM
@@ -407,7 +409,26 @@ __device__ __forceinline__ void f8_tile(const Fp8GemmParams &p, int t, int *mt, 
     *mt = grp * F8_GROUP + (t - *nt * rows);
 }
 
-template <bool PAIR, bool B_ROWS>
+// 4 columns of the result, of which n exist, at element `at` of C.
+__device__ __forceinline__ void f8_store4(void *C, long long at, int n, const float4 &a, int c_type) {
+    if (c_type == CE_FP32) {
+        const float f[4] = {a.x, a.y, a.z, a.w};
+        float *o = static_cast<float *>(C) + at;
+        if (n >= 4) *reinterpret_cast<float4 *>(o) = a;
+        else
+            for (int j = 0; j < n; ++j) o[j] = f[j];
+    } else {
+        uint16_t *o = static_cast<uint16_t *>(C) + at;
+        uint2 u;
+        u.x = c_type == CE_FP16 ? pack_f16x2(a.x, a.y) : pack_bf16x2(a.x, a.y);
+        u.y = c_type == CE_FP16 ? pack_f16x2(a.z, a.w) : pack_bf16x2(a.z, a.w);
+        if (n >= 4) *reinterpret_cast<uint2 *>(o) = u;
+        else
+            for (int j = 0; j < n; ++j) o[j] = static_cast<uint16_t>((j < 2 ? u.x : u.y) >> (16 * (j & 1)));
+    }
+}
+
+template <bool PAIR, bool B_ROWS, bool PARTS>
 __global__ void __launch_bounds__(F8_THREADS, 1)
     lce_fp8_matmul_kernel(const __grid_constant__ Fp8GemmParams p) {
     constexpr int CL = PAIR ? 2 : 1;
@@ -434,10 +455,16 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     const uint32_t crank = PAIR ? rank : 0u;
     const bool leader = crank == 0;
     const int cid = static_cast<int>(blockIdx.x / csize), ncl = static_cast<int>(gridDim.x / csize);
-    // this CTA's k blocks: all, or its part of a split product
-    const int kb0 = PAIR ? 0 : static_cast<int>(static_cast<long long>(p.KB) * rank / csize);
-    const int kb1 = PAIR ? p.KB : static_cast<int>(static_cast<long long>(p.KB) * (rank + 1) / csize);
-    const int nk = kb1 - kb0;
+    // k blocks of this CTA (of unit t, PARTS): all, or its part of a split product
+    auto k_begin = [&](int t) {
+        if constexpr (PARTS) return static_cast<int>(static_cast<long long>(p.KB) * (t / p.tiles) / p.parts);
+        else return PAIR ? 0 : static_cast<int>(static_cast<long long>(p.KB) * rank / csize);
+    };
+    auto k_end = [&](int t) {
+        if constexpr (PARTS) return static_cast<int>(static_cast<long long>(p.KB) * (t / p.tiles + 1) / p.parts);
+        else return PAIR ? p.KB : static_cast<int>(static_cast<long long>(p.KB) * (rank + 1) / csize);
+    };
+    const int units = PARTS ? p.tiles * p.parts : p.tiles;
     // A single token's A takes 1 KB of a stage, not 16: more stages, more bytes of B under way.
     // (The MMA reads 128 rows of A all the same, the rest of them out of B: rows of no output.)
     const int a_bytes = PAIR ? F8_OP_BYTES : p.a_box_rows * F8_BK;
@@ -497,9 +524,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             int issued = 0;
             bool ok = true;
             const uint32_t bytes = static_cast<uint32_t>(stage_bytes);
-            for (int t = cid; ok && t < p.tiles; t += ncl) {
+            for (int t = cid; ok && t < units; t += ncl) {
                 int mt, nt;
-                f8_tile(p, t, &mt, &nt);
+                f8_tile(p, PARTS ? t % p.tiles : t, &mt, &nt);
+                const int kb0 = k_begin(t), kb1 = k_end(t);
                 const int ya = mt * (CL * 128) + static_cast<int>(crank) * 128;
                 const int yb = nt * BNT + static_cast<int>(crank) * 128;
                 for (int kb = kb0; kb < kb1; ++kb) {
@@ -553,7 +581,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             bool ok = true, any_mma = false;
             constexpr uint32_t idesc = idesc_e4m3(CL * 128, BNT);
             constexpr uint16_t both = static_cast<uint16_t>((1u << CL) - 1u);
-            for (int t = cid; ok && t < p.tiles; t += ncl) {
+            for (int t = cid; ok && t < units; t += ncl) {
+                const int nk = k_end(t) - k_begin(t);
                 for (int kb = 0; kb < nk; ++kb) {
                     const uint32_t sA = smem_u32(smem + stage * stage_bytes);
                     const uint64_t ad = sdesc(sA, 16u, 1024u);
@@ -606,9 +635,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         uint32_t phase = 0;
         int par = 0;
         bool ok = true;
-        for (int t = cid; ok && t < p.tiles; t += ncl) {
+        for (int t = cid; ok && t < units; t += ncl) {
             int mt, nt;
-            f8_tile(p, t, &mt, &nt);
+            f8_tile(p, PARTS ? t % p.tiles : t, &mt, &nt);
+            const int kb0 = k_begin(t), kb1 = k_end(t);
             const int row0 = mt * (CL * 128) + static_cast<int>(crank) * 128 + quarter * 32;
             const int col0 = nt * BNT + half * COLS;
             const bool active = row0 < p.M && col0 < p.N;   // warp-uniform: some output of this warp exists
@@ -836,7 +866,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0 && bx < p.n_bulk) {
-                            tma_store_2d(&p.tmC, box, bx, row0);
+                            tma_store_2d(&p.tmC, box, bx, PARTS ? row0 + t / p.tiles * (p.m_tiles * 256) : row0);
                             bulk_commit();
                         }
                         // a bulk store writes whole 16-byte pieces of a row: what N leaves in its last
@@ -882,23 +912,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                 a.z += v.z;
                 a.w += v.w;
             }
-            const float f[4] = {a.x, a.y, a.z, a.w};
-            const int n = p.N - col;
-            if (p.c_type == CE_FP32) {
-                float *o = static_cast<float *>(p.C) + row * p.ldc + col;
-                if (n >= 4) *reinterpret_cast<float4 *>(o) = a;
-                else
-                    for (int j = 0; j < n; ++j) o[j] = f[j];
-            } else {
-                uint16_t *o = static_cast<uint16_t *>(p.C) + row * p.ldc + col;
-                uint2 u;
-                u.x = p.c_type == CE_FP16 ? pack_f16x2(a.x, a.y) : pack_bf16x2(a.x, a.y);
-                u.y = p.c_type == CE_FP16 ? pack_f16x2(a.z, a.w) : pack_bf16x2(a.z, a.w);
-                if (n >= 4) *reinterpret_cast<uint2 *>(o) = u;
-                else
-                    for (int j = 0; j < n; ++j)
-                        o[j] = static_cast<uint16_t>((j < 2 ? u.x : u.y) >> (16 * (j & 1)));
-            }
+            f8_store4(p.C, row * p.ldc + col, p.N - col, a, p.c_type);
         }
         cluster_sync_all();   // no CTA leaves while a peer may still read its partial sums
     }
@@ -915,26 +929,49 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     }
 }
 
+// Adds the parts of a product: 4 columns per thread. Bound by L2.
+constexpr int FP_THREADS = 256;
+__global__ void __launch_bounds__(FP_THREADS)
+    lce_fp8_parts_kernel(const float *part, const int parts, const long long part_size, const int ld, const int M,
+                         const int N, void *C, const long long ldc, const int c_type) {
+    const int vecs = ld / 4;
+    const long long i = static_cast<long long>(blockIdx.x) * FP_THREADS + threadIdx.x;
+    const int row = static_cast<int>(i / vecs), col = static_cast<int>(i % vecs) * 4;
+    if (row >= M || col >= N) return;
+    const float *src = part + static_cast<long long>(row) * ld + col;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q = 0; q < parts; ++q) {
+        const float4 v = *reinterpret_cast<const float4 *>(src + q * part_size);
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+    }
+    f8_store4(C, row * ldc + col, N - col, a, c_type);
+}
+
 using Fp8Kernel = void (*)(const Fp8GemmParams);
-Fp8Kernel fp8_kernel(bool pair, bool b_rows) {
-    if (pair) return b_rows ? lce_fp8_matmul_kernel<true, true> : lce_fp8_matmul_kernel<true, false>;
-    return b_rows ? lce_fp8_matmul_kernel<false, true> : lce_fp8_matmul_kernel<false, false>;
+Fp8Kernel fp8_kernel(bool pair, bool b_rows, bool parts) {
+    if (parts) return lce_fp8_matmul_kernel<true, false, true>;
+    if (pair) return b_rows ? lce_fp8_matmul_kernel<true, true, false> : lce_fp8_matmul_kernel<true, false, false>;
+    return b_rows ? lce_fp8_matmul_kernel<false, true, false> : lce_fp8_matmul_kernel<false, false, false>;
 }
 
 }  // namespace
 
 cudaError_t fp8_set_attributes() {
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 5; ++k) {
+        const bool parts = k == 4;
+        const Fp8Kernel f = fp8_kernel(k & 1, k & 2, parts);
         cudaError_t e;
-        if (k & 1) {
+        if ((k & 1) || parts) {
             // the register split waits forever for registers that the launch does not have
             cudaFuncAttributes fa{};
-            e = cudaFuncGetAttributes(&fa, fp8_kernel(true, k & 2));
+            e = cudaFuncGetAttributes(&fa, f);
             if (e != cudaSuccess) return e;
             if (fa.numRegs < F8_REGS) return cudaErrorInvalidKernelImage;
         }
-        e = cudaFuncSetAttribute(
-            fp8_kernel(k & 1, k & 2), cudaFuncAttributeMaxDynamicSharedMemorySize, F8_SMEM);
+        e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, F8_SMEM);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -959,7 +996,15 @@ cudaError_t launch_fp8_matmul(const Fp8GemmParams &p, bool pair, bool b_rows, in
         at[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.numAttrs = 2;
     }
-    return cudaLaunchKernelEx(&cfg, fp8_kernel(pair, b_rows), p);
+    return cudaLaunchKernelEx(&cfg, fp8_kernel(pair, b_rows, p.parts > 1), p);
+}
+
+cudaError_t launch_fp8_parts(const Fp8GemmParams &p, void *out, long long ldc, int c_type, cudaStream_t s) {
+    const long long n = static_cast<long long>(p.M) * (p.ldc / 4);
+    lce_fp8_parts_kernel<<<static_cast<unsigned>((n + FP_THREADS - 1) / FP_THREADS), FP_THREADS, 0, s>>>(
+        static_cast<const float *>(p.C), p.parts, static_cast<long long>(p.m_tiles) * 256 * p.ldc,
+        static_cast<int>(p.ldc), p.M, p.N, out, ldc, c_type);
+    return cudaGetLastError();
 }
 
 }  // namespace lce

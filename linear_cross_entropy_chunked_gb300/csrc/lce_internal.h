@@ -313,6 +313,7 @@ struct Fp8GemmParams {
     int m_tiles, n_tiles, tiles;
     int a_box_rows;            // rows of A's load box
     int stages;                // of the pipeline (one CTA per tile)
+    int parts;                 // of k in which each tile is taken (pairs): C is then [parts][256 m_tiles][ldc]
     const float *sa;           // of A's row m and block b: sa[m * sa_row + b * sa_block]
     const float *sb;           // of B's row (or 128 rows) n and block b
     long long sa_row, sa_block, sb_row, sb_block;
@@ -371,6 +372,8 @@ cudaError_t launch_fp8_quantize(const Fp8QuantParams &p, int dtype, bool tile, c
 // launch may overlap this one's prologue; the kernel waits for its end)
 cudaError_t launch_fp8_matmul(const Fp8GemmParams &p, bool pair, bool b_rows, int cluster, int clusters,
                               bool overlap, cudaStream_t s);
+// Adds p's parts into the result.
+cudaError_t launch_fp8_parts(const Fp8GemmParams &p, void *out, long long ldc, int c_type, cudaStream_t s);
 
 constexpr float LOG2E_F = 1.4426950408889634f;
 

@@ -7,6 +7,7 @@ multiple of 16, scale fp32 [R, ceil(C / 128)] (row blocks: activations, gradient
 quantize_fp8 stored block by block: the product reads those of consecutive rows at once)."""
 from __future__ import annotations
 
+import ctypes
 from typing import NamedTuple, Optional
 
 import torch
@@ -120,12 +121,22 @@ def _check_operand(name, q, scale, rows_only):
     return _pad16(ld) if R <= 1 else ld, rows
 
 
+def fp8_matmul_workspace_size(M, N, K, rows=False):
+    """Bytes of a workspace for fp8_matmul ([M, K] by [N, K]; rows: b's scales are per row) with which
+    products with few tiles and a long K are shared out along K, on the current device."""
+    out = ctypes.c_size_t(0)
+    _b._check(_b.lib().lce_fp8_matmul_best_workspace_size(M, N, K, 1 if rows else 0, ctypes.byref(out)),
+              "lce_fp8_matmul_best_workspace_size")
+    return out.value
+
+
 def _matmul(a, a_scale, lda, b, b_scale, ldb, b_rows, out, ws, s):
     M, K = a.shape
     N = b.shape[0]
     ldc = out.stride(0) if M > 1 else -(-N // 8) * 8
     if ws is None:
-        ws = torch.empty(_WS_BYTES, dtype=torch.uint8, device=a.device)
+        nbytes = fp8_matmul_workspace_size(M, N, K, b_rows) if M > BLOCK else _WS_BYTES
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=a.device)
     _b._check(_b.lib().lce_fp8_matmul(a.data_ptr(), lda, a_scale.data_ptr(), *a_scale.stride(), b.data_ptr(),
                                       ldb, b_scale.data_ptr(), *b_scale.stride(), 1 if b_rows else 0, M, N, K,
                                       out.data_ptr(), ldc, _b._CE_DTYPES[out.dtype], ws.data_ptr(), ws.numel(),
@@ -144,7 +155,8 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, ws=No
     b [N, K] with scales per row and block or per tile [ceil(N / 128), ceil(K / 128)]; any
     fp32 scales, fp32 sums, rounded once to out_dtype (bf16, fp16 or fp32). The result's
     row stride is N rounded up to 16 bytes. out: where to write it (row stride a multiple of
-    16 bytes). ws: a uint8 tensor of 1024 bytes whose device status read_status returns."""
+    16 bytes). ws: a uint8 tensor of at least 1024 bytes whose device status read_status returns
+    (fp8_matmul_workspace_size says with how many no product is slower than without ws)."""
     lda, _ = _check_operand("a", a, a_scale, True)
     ldb, b_rows = _check_operand("b", b, b_scale, False)
     if a.shape[1] != b.shape[1] or a.device != b.device:
@@ -160,7 +172,7 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, ws=No
         raise TypeError("out_dtype must be bfloat16, float16 or float32")
     if ws is not None and (ws.device != a.device or ws.dtype != torch.uint8 or not ws.is_contiguous()
                            or ws.numel() < _WS_BYTES or ws.data_ptr() % 16):
-        raise ValueError(f"ws must be a contiguous, 16-byte aligned uint8 tensor of {_WS_BYTES} bytes")
+        raise ValueError(f"ws must be a contiguous, 16-byte aligned uint8 tensor of at least {_WS_BYTES} bytes")
     with _b._on(a.device, stream) as s:
         if out is None:
             out = _empty_out(a.shape[0], b.shape[0], out_dtype, a.device)

@@ -296,3 +296,53 @@ def test_no_rows():
     assert z.shape == (0, 300)
     dx, dw = torch.autograd.grad(z, (x, w), torch.empty(0, 300, dtype=torch.bfloat16, device="cuda"))
     assert dx.shape == (0, 64) and (dw == 0).all()
+
+
+@pytest.mark.parametrize("out_dtype", list(DTYPES))
+@pytest.mark.parametrize("m,n,k", [(1537, 1701, 20000), (700, 4001, 33001), (2049, 1290, 50000)])
+def test_few_tiles_and_a_long_k(m, n, k, out_dtype):
+    # parts of k, added from the workspace; a small workspace gives the product in one part
+    (a, sa), (b, sb) = operand(m, k, 1, False), operand(n, k, 2, True)
+    t = DTYPES[out_dtype]
+    size = lce.fp8_matmul_workspace_size(m, n, k)
+    assert size > 1024 and lce.fp8_matmul_workspace_size(m, n, k, rows=True) == 1024
+    wide = torch.full((m, 4096), 7.0, dtype=t, device="cuda")
+    out = wide[:, :n]
+    guard = torch.full((size + 4096,), 85, dtype=torch.uint8, device="cuda")
+    ws = guard[2048:2048 + size]
+    lce.fp8_matmul(a, sa, b, sb, out=out, ws=ws)
+    assert lce.read_status(ws) == 0 and (wide[:, n:] == 7).all()
+    assert (guard[:2048] == 85).all() and (guard[2048 + size:] == 85).all()
+    one = lce.fp8_matmul(a, sa, b, sb, out_dtype=t, ws=torch.empty(1024, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(out, lce.fp8_matmul(a, sa, b, sb, out_dtype=t))
+    A = a.double() * sa.double().repeat_interleave(128, 1)[:, :k]
+    B = b.double() * sb.double().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+    want, S = A @ B.T, A.abs() @ B.abs().T
+    blocks = -(-k // 128)
+    # (the bound of the module's head: the parts' sums add up to as many blocks, and at most 8 more)
+    bound = (128 + blocks + 4 + 8) * 2.0 ** -23 * S + torch.finfo(t).eps / 2 * want.abs()
+    # rounding to nearest gives infinity from half a step past the type's largest value on; the bf16 and fp32
+    # results lie far below theirs
+    edge = torch.finfo(t).max * (1 + torch.finfo(t).eps / 4)
+    over, finite = want.abs() - bound >= edge, want.abs() + bound < edge
+    for got in (out, one):
+        assert ((got.double() - want).abs() <= bound * (1 + 2.0 ** -10))[finite].all()
+        assert (got.double()[over] == want[over].sign() * float("inf")).all()
+
+
+def test_parts_in_a_graph_and_a_gradient():
+    # the gradient of an input whose layer is narrow, eager and captured
+    X = rand(1537, 1600, 1).cuda()
+    w8 = lce.fp8_weight(rand(20000, 1600, 2).cuda())
+    dZ = rand(1537, 20000, 3).cuda()
+    Xg = X.clone().requires_grad_()
+    (dX,) = torch.autograd.grad(lce.fp8_linear(Xg, w8), Xg, dZ)
+    q, s = lce.quantize_fp8(dZ)
+    want = lce.fp8_matmul(q, s, w8.q_t, w8.scale_t)
+    assert torch.equal(dX, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = lce.fp8_matmul(q, s, w8.q_t, w8.scale_t)
+    out.zero_()
+    g.replay()
+    assert torch.equal(out, want)

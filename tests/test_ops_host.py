@@ -245,3 +245,13 @@ def test_oracle_clip():
         assert abs(norm - want.item()) < 1e-12
         for p, s in zip(params, scaled):
             np.testing.assert_allclose(p.grad.numpy(), s, rtol=1e-12)
+
+
+def test_matmul_best_workspace_arguments(L):
+    n = ctypes.c_size_t(0)
+    size = L.lce_fp8_matmul_best_workspace_size
+    assert size(5, 5, 300, 0, None) == INVALID
+    assert size(-1, 5, 300, 0, ctypes.byref(n)) == INVALID
+    assert size(5, -1, 300, 0, ctypes.byref(n)) == INVALID
+    assert size(5, 5, 0, 0, ctypes.byref(n)) == INVALID
+    assert size(5, (1 << 30) + 1, 300, 0, ctypes.byref(n)) == INVALID
