@@ -194,33 +194,80 @@ def _logits(X, q, scale, s):
     return Z
 
 
+class _At(NamedTuple):
+    """An operand in a buffer of several: addresses, row stride and the scales' strides."""
+    q: int
+    ld: int
+    scale: int
+    row: int
+    block: int
+    end: int
+
+
+def _at(base, R, C, tiles):
+    """Lays the operand [R, C] out from address `base` on (256-byte steps)."""
+    ld = _pad16(C)
+    scale = base + (R * ld + 255) // 256 * 256
+    kb = _blocks(C)
+    end = scale + (4 * (_blocks(R) if tiles else R) * kb + 255) // 256 * 256
+    return _At(base, ld, scale, kb if tiles else 1, 1 if tiles else R, end)
+
+
+def _quantize_at(X, tiles, own, transposed, s):
+    R, C = X.shape
+    if R:
+        _b._check(_b.lib().lce_fp8_quantize(
+            X.data_ptr(), _b._CE_DTYPES[X.dtype], X.stride(0) if R > 1 else C, R, C, tiles,
+            own.q if own else None, _pad16(C), own.scale if own else None,
+            transposed.q if transposed else None, _pad16(R), transposed.scale if transposed else None, s),
+            "lce_fp8_quantize")
+
+
+def _matmul_at(a, b, b_rows, M, N, K, out, ws, ws_bytes, s):
+    ldc = out.stride(0) if M > 1 else -(-N // 8) * 8
+    _b._check(_b.lib().lce_fp8_matmul(a.q, a.ld, a.scale, a.row, a.block, b.q, b.ld, b.scale, b.row, b.block,
+                                      1 if b_rows else 0, M, N, K, out.data_ptr(), ldc,
+                                      _b._CE_DTYPES[out.dtype], ws, ws_bytes, s), "lce_fp8_matmul")
+
+
+def _ws_bytes(M, N, K):
+    return fp8_matmul_workspace_size(M, N, K) if M > BLOCK else _WS_BYTES
+
+
 class FP8LinearFunction(torch.autograd.Function):
     """Z = X W^T with X in row blocks and W in tiles of e4m3; rounding is passed through:
     dX = dZ W (dZ in row blocks, W^T in tiles) and, for a trained W, dW = dZ^T X (both in
-    blocks along the rows of X)."""
+    blocks along the rows of X). What lives as long is allocated at once: the operands of this
+    pass in one buffer, those of the backward pass in another."""
 
     @staticmethod
     def forward(ctx, X, W, q, scale, q_t, scale_t):
         need_dX, need_dW = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
-        with _b._on(X.device, None) as s:
-            if W is not None:
-                (q, scale), (q_t, scale_t) = _quantize(W, True, True, need_dX, s)
-            xt = xts = None
-            if need_dW:   # X's transpose for dW comes from the same pass over X
-                (xq, xs), (xt, xts) = _quantize(X, False, True, True, s)
-                Z = _empty_out(X.shape[0], q.shape[0], X.dtype, X.device)
-                ldw = q.stride(0) if q.shape[0] > 1 else _pad16(q.shape[1])
-                _matmul(xq, xs, _pad16(X.shape[1]), q, scale, ldw, False, Z, None, s)
-            else:
-                Z = _logits(X, q, scale, s)
-        ctx.save_for_backward(q_t if need_dX else None, scale_t if need_dX else None, xt, xts)
         ctx.x_dtype, ctx.w_dtype = X.dtype, None if W is None else W.dtype
+        with _b._on(X.device, None) as s:
+            if W is None:
+                ctx.save_for_backward(q_t, scale_t)
+                return _logits(X, q, scale, s)
+            (M, D), V = X.shape, W.shape[0]
+            x, w = _at(0, M, D, False), _at(0, V, D, True)
+            wt = _at(0, D, V, True).end if need_dX else 0
+            xt = _at(0, D, M, False).end if need_dW else 0
+            nbytes = _ws_bytes(M, V, D)
+            here = torch.empty(x.end + w.end + nbytes, dtype=torch.uint8, device=X.device)
+            kept = torch.empty(wt + xt, dtype=torch.uint8, device=X.device)
+            x = _at(here.data_ptr(), M, D, False)
+            w = _at(x.end, V, D, True)
+            _quantize_at(W, True, w, _at(kept.data_ptr(), D, V, True) if need_dX else None, s)
+            _quantize_at(X, False, x, _at(kept.data_ptr() + wt, D, M, False) if need_dW else None, s)
+            Z = _empty_out(M, V, X.dtype, X.device)
+            _matmul_at(x, w, False, M, V, D, Z, w.end, nbytes, s)
+        ctx.save_for_backward(kept)
+        ctx.D = D
         return Z
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dZ):
-        wt, wts, xt, xts = ctx.saved_tensors
         need_dX, need_dW = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
         if not (need_dX or need_dW):
             return None, None, None, None, None, None
@@ -229,17 +276,29 @@ class FP8LinearFunction(torch.autograd.Function):
         M, V = dZ.shape
         dX = dW = None
         with _b._on(dZ.device, None) as s:
-            (zq, zs), (zt, zts) = _quantize(dZ, False, need_dX, need_dW, s)
+            if ctx.w_dtype is None:
+                wq, ws = ctx.saved_tensors
+                D = wq.shape[0]
+                wt = _At(wq.data_ptr(), wq.stride(0) if D > 1 else _pad16(V), ws.data_ptr(), *ws.stride(), 0)
+            else:
+                (kept,), D = ctx.saved_tensors, ctx.D
+                wt = _at(kept.data_ptr(), D, V, True)
+                xt = _at(wt.end if need_dX else kept.data_ptr(), D, M, False)
+            nbytes = max(_ws_bytes(M, D, V) if need_dX else 0, _WS_BYTES)
+            z, zt = (_at(0, M, V, False).end if need_dX else 0), (_at(0, V, M, False).end if need_dW else 0)
+            here = torch.empty(z + zt + nbytes, dtype=torch.uint8, device=dZ.device)
+            at = here.data_ptr()
+            z, zt, at = _at(at, M, V, False), _at(at + z, V, M, False), at + z + zt
+            _quantize_at(dZ, False, z if need_dX else None, zt if need_dW else None, s)
             if need_dX:
-                dX = _empty_out(M, wt.shape[0], ctx.x_dtype, dZ.device)
-                ldw = wt.stride(0) if wt.shape[0] > 1 else _pad16(V)
-                _matmul(zq, zs, _pad16(V), wt, wts, ldw, False, dX, None, s)
+                dX = _empty_out(M, D, ctx.x_dtype, dZ.device)
+                _matmul_at(z, wt, False, M, D, V, dX, at, nbytes, s)
             if need_dW:
                 if M == 0:
-                    dW = torch.zeros(V, xt.shape[0], dtype=ctx.w_dtype, device=dZ.device)
+                    dW = torch.zeros(V, D, dtype=ctx.w_dtype, device=dZ.device)
                 else:
-                    dW = _empty_out(V, xt.shape[0], ctx.w_dtype, dZ.device)
-                    _matmul(zt, zts, _pad16(M), xt, xts, _pad16(M), True, dW, None, s)
+                    dW = _empty_out(V, D, ctx.w_dtype, dZ.device)
+                    _matmul_at(zt, xt, True, V, D, M, dW, at, nbytes, s)
         return dX, dW, None, None, None, None
 
 
