@@ -279,6 +279,8 @@ template <int CAP> struct ClipTable {
     int first[CAP + 1];    // first chunk
     int n;
 };
+// A list of few tensors goes by a smaller table: 56 tensors of 5000 values take 7.6 us, by the large
+// one, whose 29 KB of parameters go with every launch, 7.8.
 constexpr int CLIP_FEW_TENSORS = 64;
 constexpr int CLIP_MAX_TENSORS = 1024;   // per launch
 constexpr long long CLIP_MAX_CHUNKS = 1ll << 30;   // per launch
