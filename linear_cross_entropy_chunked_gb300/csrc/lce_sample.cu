@@ -26,9 +26,9 @@
 // Measured: 1 x 32000 bf16 5.7 us, 64 x 128256 bf16 18 us, 256 x 128256 bf16 61 us and fp32 67 us
 // (1.9 TB/s; the read alone would take 19 us). What takes the time: about 35 instructions per logit
 // for the exponential, and a CTA's start, exchanges and tail, which the second CTA of an SM
-// covers in part. 64 x 128256 bf16 with top-k 50 takes 16 us; with top-p 0.9 of flat rows, whose
-// cut lies beyond the list, 70 us: the sums end at 19, the histogram at 39, the keys of its bin
-// at 53, the sums of what is kept and the draw at 70.
+// covers in part. 64 x 128256 bf16 with top-k 50 takes 15 us; with top-p 0.9 of flat rows, whose
+// cut lies beyond the list, 60 us, in three parts: the histogram, the keys of its bin, and the
+// sums of what is kept with the draw.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -321,13 +321,12 @@ __device__ __forceinline__ u64 warp_sum64(u64 v) {
 struct alignas(16) SmpSums {
     u64 w;                 // weight of all
     u64 wlist;             // ... of the logits on the list
-    uint32_t c;            // logits of x < SMP_X_END
     uint32_t list;         // logits on the list (more than SMP_LIST_CTA: it overflowed)
 };
 struct SmpShared {
     uint32_t hist[2][4][SMP_BINS];        // counts, three limbs of the weights; read by the peers
     float wmax[SMP_PARTS];                // largest logits of the warps' parts, of all warps of the cluster
-    SmpSums sums[2][SMP_MAX_CLUSTER];     // of every CTA of the cluster
+    SmpSums sums[SMP_MAX_CLUSTER];        // of every CTA of the cluster
     uint4 wslot[SMP_MAX_CLUSTER * SMP_WARPS];   // per warp of the cluster: sum above the cut, ties
     u64 list[SMP_LIST_CTA];               // key and inverted index; rank 0 reads the peers'
     u64 all[SMP_LIST], allw[SMP_LIST];    // rank 0: the whole list, and its weights
@@ -554,7 +553,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
         // 64 x 128256 bf16 15.9 and 35.0 us, 1 x 32000 9.4 and 16.2.)
         constexpr int groups = 32;
         const int want = by_count ? top_k : groups - 1;           // (top-p: about 100 logits)
-        const bool use_list = want <= SMP_PARTS;
+        bool use_list = want <= SMP_PARTS;
         float t0 = INFINITY;
         if (want <= groups) {
             float v = wm[0];
@@ -570,6 +569,18 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                     v = keep_max ? fmaxf(v, o) : fminf(v, o);
                 }
             t0 = __shfl_sync(0xffffffffu, v, want - 1);
+            if (!by_count) {
+                // Top-p of a flat row goes to the search at once: where the logits at the threshold, TAIL of
+                // them, would outweigh what the largest may leave to the rest. (An estimate: either way
+                // is right for every row, and every warp of the cluster forms the same one. With top-p 0.9
+                // 64 x 128256 bf16 takes 60.4 us so and 74.6 with the list first; 1 x 32000 at a temperature
+                // of 0.5, which the list holds, 10.8 and by the search 17.4.)
+                constexpr float TAIL = 400.f;
+                float e = __expf(-smp_x(v, rw));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
+                use_list = !(TAIL * __expf(-smp_x(t0, rw)) * top_p > (1.f - top_p) * e);
+            }
         } else if (use_list) {
 #pragma unroll
             for (int q = 0; q < SMP_MAX_CLUSTER; ++q) {
@@ -588,11 +599,11 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
         __syncthreads();
         if (use_list) t0 = fmaxf(want <= groups ? t0 : sh.t0, -3.402823466e38f);   // (masked ones stay out)
 
-        // one pass: sums over the row, and the list
-        int xs = 0;
-        auto sums_pass = [&](bool collect, bool counts, bool weights) {
+        // one pass: the list, and (top-p alone) weights
+        u64 pool = 0;        // weight of what top-k keeps
+        if (use_list) {
+            const bool weights = !by_count;
             u64 ws = 0, wl = 0;
-            uint32_t c = 0;
             for (int s = 0; s < steps; ++s) {
                 float x[8];
                 ck.load(s * 256 + l * 8, x);
@@ -605,23 +616,17 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                         ws += v1;
                     }
                 }
-                if (counts) {
+                bool any = false;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) c += smp_x(x[j], rw) < SMP_X_END ? 1u : 0u;
-                }
-                if (collect) {
-                    bool any = false;
+                for (int j = 0; j < 8; ++j) any |= x[j] >= t0;
+                if (__any_sync(0xffffffffu, any)) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) any |= x[j] >= t0;
-                    if (__any_sync(0xffffffffu, any)) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            if (!(x[j] >= t0)) continue;
-                            const uint32_t at = atomicAdd(&sh.listed, 1u);
-                            const uint32_t index = static_cast<uint32_t>(first) + s * 256 + l * 8 + j;
-                            if (at < SMP_LIST_CTA) sh.list[at] = (static_cast<u64>(smp_key<T>(x[j])) << 32) | ~index;
-                            if (weights) wl += smp_weight(x[j], rw, tabs, sh.tab);   // (few: cheaper than 8 kept)
-                        }
+                    for (int j = 0; j < 8; ++j) {
+                        if (!(x[j] >= t0)) continue;
+                        const uint32_t at = atomicAdd(&sh.listed, 1u);
+                        const uint32_t index = static_cast<uint32_t>(first) + s * 256 + l * 8 + j;
+                        if (at < SMP_LIST_CTA) sh.list[at] = (static_cast<u64>(smp_key<T>(x[j])) << 32) | ~index;
+                        if (weights) wl += smp_weight(x[j], rw, tabs, sh.tab);   // (few: cheaper than 8 kept)
                     }
                 }
             }
@@ -629,104 +634,91 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                 ws = warp_sum64(ws);
                 wl = warp_sum64(wl);
             }
-            if (counts) c = __reduce_add_sync(0xffffffffu, c);
-            if (l == 0) sh.part[w] = SmpSums{ws, wl, c, 0};
+            if (l == 0) sh.part[w] = SmpSums{ws, wl, 0};
             __syncthreads();
             // lane k of warp 0 gives the CTA's sums to CTA k
             if (w == 0) {
-                SmpSums o = l < SMP_WARPS ? sh.part[l] : SmpSums{0, 0, 0, 0};
+                SmpSums o = l < SMP_WARPS ? sh.part[l] : SmpSums{0, 0, 0};
                 o.w = warp_sum64(o.w);
                 o.wlist = warp_sum64(o.wlist);
-                o.c = __reduce_add_sync(0xffffffffu, o.c);
                 o.list = sh.listed;
                 if (l < static_cast<int>(cl)) {
-                    const uint32_t at = map_to_rank(&sh.sums[xs][rank], l);
+                    const uint32_t at = map_to_rank(&sh.sums[rank], l);
                     auto hi = [](u64 v) { return static_cast<uint32_t>(v >> 32); };
                     auto lo = [](u64 v) { return static_cast<uint32_t>(v); };
                     st_cluster_v4(at, lo(o.w), hi(o.w), lo(o.wlist), hi(o.wlist));
-                    st_cluster_v4(at + 16, o.c, o.list, 0u, 0u);
+                    st_cluster_v4(at + 16, o.list, 0u, 0u, 0u);
                 }
             }
             cluster_sync_all();
-            SmpSums all = {0, 0, 0, 0};
+            SmpSums sum = {0, 0, 0};
             bool over = false;
             for (uint32_t k = 0; k < cl; ++k) {
-                const SmpSums &o = sh.sums[xs][k];
-                all.w += o.w;
-                all.wlist += o.wlist;
-                all.c += o.c;
-                all.list += o.list;
+                const SmpSums &o = sh.sums[k];
+                sum.w += o.w;
+                sum.wlist += o.wlist;
+                sum.list += o.list;
                 over |= o.list > SMP_LIST_CTA;
             }
-            if (over || all.list > SMP_LIST) all.list = 0xffffffffu;
-            xs ^= 1;
-            return all;
-        };
-        SmpSums sum = sums_pass(use_list, !use_list, by_weight && !(use_list && by_count));
-
-        // with top-k the list holds all that it keeps; with top-p alone, all that p keeps if it
-        // weighs enough
-        if (use_list && sum.list != 0xffffffffu && (by_count || sum.wlist >= share(sum.w))) {
-            if (rank == 0) {
-                // thread i: entry i of the list
-                const int n_list = static_cast<int>(sum.list);
-                u64 c = 0, wt = 0;
-                float z = 0.f;
-                if (t < n_list) {
-                    int at = t;
-                    uint32_t k = 0;
-                    while (at >= static_cast<int>(sh.sums[xs ^ 1][k].list)) at -= static_cast<int>(sh.sums[xs ^ 1][k++].list);
-                    c = ld_cluster_u64(map_to_rank(&sh.list[at], k));
-                    z = smp_unkey<T>(static_cast<uint32_t>(c >> 32));
-                    wt = smp_weight(z, rw, tabs, sh.tab);
-                    sh.all[t] = c;
-                    sh.allw[t] = wt;
-                }
-                __syncthreads();
-                int before = 0;    // entries and weight before this one in the order
-                u64 before_w = 0;
-                if (t < n_list)
-                    for (int j = 0; j < n_list; ++j)
-                        if (sh.all[j] > c) {
-                            ++before;
-                            before_w += sh.allw[j];
-                        }
-                // sum over the CTA of one value per thread
-                auto block_sum = [&](u64 v) {
-                    v = warp_sum64(v);
+            // with top-k the list holds all that it keeps; with top-p alone, all that p keeps if it
+            // weighs enough
+            if (!over && sum.list <= SMP_LIST && (by_count || sum.wlist >= share(sum.w))) {
+                if (rank == 0) {
+                    // thread i: entry i of the list
+                    const int n_list = static_cast<int>(sum.list);
+                    u64 c = 0, wt = 0;
+                    float z = 0.f;
+                    if (t < n_list) {
+                        int at = t;
+                        uint32_t k = 0;
+                        while (at >= static_cast<int>(sh.sums[k].list)) at -= static_cast<int>(sh.sums[k++].list);
+                        c = ld_cluster_u64(map_to_rank(&sh.list[at], k));
+                        z = smp_unkey<T>(static_cast<uint32_t>(c >> 32));
+                        wt = smp_weight(z, rw, tabs, sh.tab);
+                        sh.all[t] = c;
+                        sh.allw[t] = wt;
+                    }
                     __syncthreads();
-                    if (l == 0) sh.wsum[w] = v;
+                    int before = 0;    // entries and weight before this one in the order
+                    u64 before_w = 0;
+                    if (t < n_list)
+                        for (int j = 0; j < n_list; ++j)
+                            if (sh.all[j] > c) {
+                                ++before;
+                                before_w += sh.allw[j];
+                            }
+                    // sum over the CTA of one value per thread
+                    auto block_sum = [&](u64 v) {
+                        v = warp_sum64(v);
+                        __syncthreads();
+                        if (l == 0) sh.wsum[w] = v;
+                        __syncthreads();
+                        u64 a = 0;
+                        for (int k = 0; k < SMP_WARPS; ++k) a += sh.wsum[k];
+                        return a;
+                    };
+                    bool keep = t < n_list && (!by_count || before < top_k);
+                    if (by_weight) {
+                        const u64 end = share(by_count ? block_sum(keep ? wt : 0ull) : sum.w);
+                        keep = keep && before_w < end;
+                    }
+                    keep = keep && wt >= w_min;
+                    const u64 total = block_sum(keep ? wt : 0ull);   // (all have read sh.allw)
+                    if (t < n_list) sh.allw[t] = keep ? wt : 0ull;
                     __syncthreads();
-                    u64 a = 0;
-                    for (int k = 0; k < SMP_WARPS; ++k) a += sh.wsum[k];
-                    return a;
-                };
-                bool keep = t < n_list && (!by_count || before < top_k);
-                if (by_weight) {
-                    const u64 end = share(by_count ? block_sum(keep ? wt : 0ull) : sum.w);
-                    keep = keep && before_w < end;
+                    const u64 target = draw_target(total);
+                    const uint32_t index = ~static_cast<uint32_t>(c);
+                    if (keep) {
+                        u64 upto = wt;   // kept weight up to and including this index
+                        for (int j = 0; j < n_list; ++j)
+                            if (~static_cast<uint32_t>(sh.all[j]) < index) upto += sh.allw[j];
+                        if (upto > target && upto - wt <= target) answer(index, z, total);
+                    }
                 }
-                keep = keep && wt >= w_min;
-                const u64 total = block_sum(keep ? wt : 0ull);   // (all have read sh.allw)
-                if (t < n_list) sh.allw[t] = keep ? wt : 0ull;
-                __syncthreads();
-                const u64 target = draw_target(total);
-                const uint32_t index = ~static_cast<uint32_t>(c);
-                if (keep) {
-                    u64 upto = wt;   // kept weight up to and including this index
-                    for (int j = 0; j < n_list; ++j)
-                        if (~static_cast<uint32_t>(sh.all[j]) < index) upto += sh.allw[j];
-                    if (upto > target && upto - wt <= target) answer(index, z, total);
-                }
+                cluster_sync_all();   // rank 0 has read the peers' lists
+                return;
             }
-            cluster_sync_all();   // rank 0 has read the peers' lists
-            return;
         }
-        if (use_list && by_count) {   // too many for the list: sums are needed after all
-            if (t == 0) sh.listed = 0;
-            sum = sums_pass(false, true, by_weight);
-        }
-
         // ---- the general search: a histogram of x, then of the keys in the bin that holds the cut
         int hb = 0;   // histogram in use
         auto clear = [&]() {
@@ -818,7 +810,6 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
         };
 
         // first level: bins of x
-        bool loaded = false;
         uint32_t tot_c = 0;
         u64 tot_w = 0;
         // bin: the lesser of two lines in x, rounded to nearest by adding SMP_ROUND (a conversion
@@ -835,8 +826,6 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
             return fmaxf(y < SMP_BINS / 2 ? y / NEAR : (y - FAR_0) / FAR, 0.f);
         };
         auto first_level = [&]() {
-            if (loaded) return;
-            loaded = true;
             clear();
             for (int s = 0; s < steps; ++s) {
                 float x[8];
@@ -855,8 +844,6 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
 
         // the key and the number of equal logits at which `target` is reached
         auto search = [&](bool count, u64 target, uint32_t *key, uint32_t *ties, u64 *kept_w) {
-            uint32_t base_c = 0;
-            u64 base_w = 0;
             // keys that include those of x from near_x to far_x, with room for the roundings
             uint32_t klo, khi;
             auto key_range = [&](float near_x, float far_x) {
@@ -867,17 +854,12 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                 if (zhi < m) khi = smp_key<T>(zhi);
                 if (zlo > -3e38f) klo = smp_key<T>(zlo);
             };
-            key_range(0.f, SMP_X_END);
-            int b0 = -1;   // the bin that is searched; -1: there are so few keys that each gets its bin
-            if (khi - klo >= SMP_BINS) {
-                first_level();
-                find(sh.l0c, sh.l0w, tot_c, tot_w, count, target);
-                b0 = sh.bin;
-                base_c = sh.bc;
-                base_w = sh.bw;
-                __syncthreads();
-                key_range(bin_start(b0), bin_start(b0 + 1));
-            }
+            find(sh.l0c, sh.l0w, tot_c, tot_w, count, target);
+            const int b0 = sh.bin;
+            uint32_t base_c = sh.bc;
+            u64 base_w = sh.bw;
+            __syncthreads();
+            key_range(bin_start(b0), bin_start(b0 + 1));
             for (int level = 0; klo != khi && level < 4; ++level) {   // 8 bits of the key at a time
                 const int bits = 32 - __clz(khi - klo);
                 const int shift = bits > 8 ? bits - 8 : 0;
@@ -895,7 +877,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
                         if (!(x[j] >= zlo && x[j] <= zhi)) continue;
                         const uint32_t k = smp_key<T>(x[j]);
                         const int in = bin_of(x[j]);
-                        if (!(k >= klo && k <= khi && in >= 0 && (b0 < 0 || in == b0))) continue;
+                        if (!(k >= klo && k <= khi && in == b0)) continue;
                         if (shift == 0) atomicAdd(&sh.hist[hb][0][khi - k], 1u);
                         else
                             smp_hist_add(sh.hist[hb], static_cast<int>((khi - k) >> shift), by_count, by_weight,
@@ -921,8 +903,9 @@ __global__ void __launch_bounds__(SMP_THREADS, 2)
             *kept_w = base_w + static_cast<u64>(*ties) * one;
         };
 
-        u64 pool = sum.w;   // weight of what top-k keeps
-        if (by_count && static_cast<uint32_t>(top_k) < sum.c) {
+        first_level();
+        pool = tot_w;
+        if (by_count && static_cast<uint32_t>(top_k) < tot_c) {
             search(true, static_cast<u64>(top_k), &cut_key, &cut_ties, &pool);
             have_cut = true;
         }
