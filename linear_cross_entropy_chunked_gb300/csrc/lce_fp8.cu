@@ -24,8 +24,8 @@ namespace lce {
 // and the same of X^T (blocks along X's rows), turned through shared memory. Bound by
 // HBM bandwidth: 2 (4) bytes read and 1 or 2 written per value. Measured: 4096 x 50256 bf16 in row
 // blocks 111 us (5.6 TB/s), X^T 121 us (5.1 TB/s). Rows of 16-bit values that do not start on 16
-// bytes are loaded value by value: 50257 columns take 240 us (vectors shifted into place
-// between lanes took the same).
+// bytes come by aligned words: 50257 columns take 157 us (value by value 236; by vectors that lanes
+// shift into place between them 242).
 
 namespace {
 
@@ -78,6 +78,18 @@ template <typename T> struct QtVec {
         if (vec && n >= 8) {
             const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p));
             w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+        } else if (n >= 8) {
+            // a row that starts anywhere: the aligned words that hold the values
+            const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+            const bool odd = (a & 2u) != 0;
+            const uint32_t *u = reinterpret_cast<const uint32_t *>(a - (a & 2u));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = u[j];
+            if (odd) {
+                const uint32_t end = u[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], j < 3 ? w[j + 1] : end, 16);
+            }
         } else {
             const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
 #pragma unroll
