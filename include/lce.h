@@ -291,7 +291,8 @@ lce_status lce_sample_logits(const void *Z, int z_dtype, int64_t ld, int64_t N, 
  * values = bytes. Columns of `out` from N on are left as they were. Workspace: a header
  * for the device status (lce_read_status), lce_fp8_matmul_workspace_size bytes; with
  * lce_fp8_matmul_best_workspace_size bytes (which asks the current device) products with few
- * tiles of out and a long K are also shared out along K, their fp32 parts kept there. */
+ * tiles of out and a long K are also shared out along K, their fp32 parts kept there. Calls that
+ * may run at the same time need a workspace each. */
 lce_status lce_fp8_quantize(const void *X, int x_dtype, int64_t ld, int64_t R, int64_t C, int tiles,
                             void *q, int64_t ldq, float *scale, void *qt, int64_t ldqt,
                             float *scale_t, lce_stream_t stream);

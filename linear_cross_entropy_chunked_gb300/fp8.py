@@ -156,7 +156,8 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, ws=No
     fp32 scales, fp32 sums, rounded once to out_dtype (bf16, fp16 or fp32). The result's
     row stride is N rounded up to 16 bytes. out: where to write it (row stride a multiple of
     16 bytes). ws: a uint8 tensor of at least 1024 bytes whose device status read_status returns
-    (fp8_matmul_workspace_size says with how many no product is slower than without ws)."""
+    (fp8_matmul_workspace_size says with how many no product is slower than without ws); calls
+    that may run at the same time need one each."""
     lda, _ = _check_operand("a", a, a_scale, True)
     ldb, b_rows = _check_operand("b", b, b_scale, False)
     if a.shape[1] != b.shape[1] or a.device != b.device:
