@@ -346,3 +346,29 @@ def test_parts_in_a_graph_and_a_gradient():
     out.zero_()
     g.replay()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("m,d,v", [(1, 128, 300), (40, 200, 129), (300, 264, 1001)])
+def test_either_gradient_alone(m, d, v):
+    X, W, dZ = rand(m, d, 1).cuda(), rand(v, d, 2).cuda(), rand(m, v, 3).cuda()
+    both = [t.clone().requires_grad_() for t in (X, W)]
+    dX, dW = torch.autograd.grad(lce.fp8_linear(*both), both, dZ)
+    Xg, Wg = X.clone().requires_grad_(), W.clone().requires_grad_()
+    (a,) = torch.autograd.grad(lce.fp8_linear(Xg, W), Xg, dZ)
+    (b,) = torch.autograd.grad(lce.fp8_linear(X, Wg), Wg, dZ)
+    (c,) = torch.autograd.grad(lce.fp8_linear(Xg, lce.fp8_weight(W)), Xg, dZ)
+    assert torch.equal(a, dX) and torch.equal(b, dW) and torch.equal(c, dX)
+
+
+def test_training_on_another_stream_and_twice_through_one_graph():
+    X, W, dZ = rand(64, 256, 1).cuda().requires_grad_(), rand(500, 256, 2).cuda().requires_grad_(), rand(64, 500, 3).cuda()
+    want = torch.autograd.grad(lce.fp8_linear(X, W), (X, W), dZ)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        Z = lce.fp8_linear(X, W)
+        first = torch.autograd.grad(Z, (X, W), dZ, retain_graph=True)
+        second = torch.autograd.grad(Z, (X, W), dZ)
+    torch.cuda.current_stream().wait_stream(side)
+    for got in (first, second):
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
