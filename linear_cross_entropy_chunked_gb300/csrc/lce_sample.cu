@@ -17,6 +17,8 @@
 // to a relative error of about 2^-31: the sum of border displacements over a row
 // of 2^17 equally likely tokens is about 1e-8, which bounds the chance that u falls
 // on the wrong side of one. An fp32 softmax would put it at about 1e-2.
+// A weight is cut, not rounded, to its unit (which saves three instructions per logit): a border
+// moves by less than 2^-43 of the largest weight per token, 1.5e-8 over 2^17 of them.
 //
 // Bound: one read of the logits. A cluster of CTAs holds a row in shared memory,
 // so every later pass (the search for the cut, the sums, the draw) stays on chip; the
