@@ -306,7 +306,9 @@ lce_status lce_fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t s
 
 /* Both in one call: out = X W^T for X [M][ldx] (x_dtype, K columns), which is quantised to row
  * blocks in the workspace, and W [N][ldw] in tiles; the rest as for lce_fp8_matmul.
- * Workspace: lce_fp8_linear_workspace_size(M, K) bytes, 16-byte aligned. */
+ * Workspace: lce_fp8_linear_workspace_size(M, K) bytes, 16-byte aligned; the product is shared out along K
+ * where that size rounded up to 1024 is followed by the bytes that
+ * lce_fp8_matmul_best_workspace_size(M, N, K, 0) has beyond 1024. */
 lce_status lce_fp8_linear_workspace_size(int64_t M, int64_t K, size_t *bytes);
 lce_status lce_fp8_linear(const void *X, int x_dtype, int64_t ldx, const void *W, int64_t ldw,
                           const float *sw, int64_t sw_row, int64_t sw_block, int64_t M, int64_t N,

@@ -1150,12 +1150,15 @@ size_t fp8_parts_bytes(int64_t M, int64_t N, int parts) {
                            align_up(static_cast<size_t>(N), 32) : 0;
 }
 
+// ws: the header and what follows it; parts: where the sums of a product in parts may lie (fp32, 16-byte
+// aligned; nothing else of this call), parts_bytes long
 // after_quantize: A comes from the quantisation launched just before on the same stream,
 // which the product's prologue may overlap
 lce_status fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t sa_row, int64_t sa_block,
                       const void *B, int64_t ldb, const float *sb, int64_t sb_row, int64_t sb_block,
                       int b_rows, int64_t M, int64_t N, int64_t K, void *out, int64_t ldc, int c_dtype,
-                      void *ws, size_t ws_bytes, bool after_quantize, lce_stream_t stream) {
+                      void *ws, size_t ws_bytes, void *parts, size_t parts_bytes, bool after_quantize,
+                      lce_stream_t stream) {
     lce_status st = fp8_matmul_check(A, lda, sa, sa_row, sa_block, B, ldb, sb, sb_row, sb_block, M, N, K, out, ldc,
                                      c_dtype, ws, ws_bytes);
     if (st != LCE_OK) return st;
@@ -1203,9 +1206,9 @@ lce_status fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t sa_ro
     p.hdr = static_cast<int *>(ws);
     p.timeout_ns = kDefaultTimeoutNs;
     p.parts = pair && !b_rows ? fp8_parts(pair_tiles, M, N, p.KB, pairs) : 1;
-    if (p.parts > 1 && ws_bytes < 1024 + fp8_parts_bytes(M, N, p.parts)) p.parts = 1;
+    if (p.parts > 1 && parts_bytes < fp8_parts_bytes(M, N, p.parts)) p.parts = 1;
     if (p.parts > 1) {
-        p.C = static_cast<uint8_t *>(ws) + 1024;
+        p.C = parts;
         p.ldc = static_cast<long long>(align_up(static_cast<size_t>(N), 32));
         p.c_type = CE_FP32;
         p.n_bulk = static_cast<int>(p.ldc);
@@ -1747,7 +1750,8 @@ lce_status lce_fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t s
                           lce_stream_t stream) {
     g_launches = 0;
     return fp8_matmul(A, lda, sa, sa_row, sa_block, B, ldb, sb, sb_row, sb_block, b_rows, M, N, K, out,
-                      ldc, c_dtype, ws, ws_bytes, false, stream);
+                      ldc, c_dtype, ws, ws_bytes, static_cast<uint8_t *>(ws) + 1024,
+                      ws_bytes > 1024 ? ws_bytes - 1024 : 0, false, stream);
 }
 
 lce_status lce_fp8_matmul_best_workspace_size(int64_t M, int64_t N, int64_t K, int b_rows, size_t *bytes) {
@@ -1787,8 +1791,10 @@ lce_status lce_fp8_linear(const void *X, int x_dtype, int64_t ldx, const void *W
     if (st != LCE_OK) return st;
     st = lce_fp8_quantize(X, x_dtype, ldx, M, K, 0, xq, ldq, sx, nullptr, 0, nullptr, stream);
     if (st != LCE_OK) return st;
-    return fp8_matmul(xq, ldq, sx, 1, M, W, ldw, sw, sw_row, sw_block, 0, M, N, K, out, ldc, c_dtype, ws,
-                      ws_bytes, M > 0, stream);
+    // (sums of parts lie behind X, which the product is reading)
+    const size_t behind = align_up(need, 1024);
+    return fp8_matmul(xq, ldq, sx, 1, M, W, ldw, sw, sw_row, sw_block, 0, M, N, K, out, ldc, c_dtype, ws, ws_bytes,
+                      w + behind, ws_bytes > behind ? ws_bytes - behind : 0, M > 0, stream);
 }
 
 lce_status lce_grad_norm_workspace_size(int64_t n, size_t *bytes) {

@@ -187,6 +187,9 @@ def _logits(X, q, scale, s):
     Z = _empty_out(M, V, X.dtype, X.device)
     code = _b._CE_DTYPES[X.dtype]
     nbytes = _WS_BYTES + (4 * M * _blocks(D) + 1023) // 1024 * 1024 + M * _pad16(D)
+    parts = _ws_bytes(M, V, D) - _WS_BYTES   # (shared out along D as with a weight that is quantised here)
+    if parts:
+        nbytes = (nbytes + 1023) // 1024 * 1024 + parts
     ws = torch.empty(nbytes, dtype=torch.uint8, device=X.device)
     _b._check(_b.lib().lce_fp8_linear(
         X.data_ptr(), code, X.stride(0) if M > 1 else D, q.data_ptr(), q.stride(0) if V > 1 else _pad16(D),
