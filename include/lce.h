@@ -255,7 +255,7 @@ lce_status lce_ce_logits(const void *Z, int z_dtype, int64_t ld, const int64_t *
  * min_p as 0.
  * temperature / top_k / top_p / min_p: one value per row on the device, or NULL for
  * the value that follows in *_all for every row.
- * Cumulative weights are exact sums of weights cut to multiples of 2^-43 of the largest, so a
+ * Cumulative weights are exact sums of weights rounded to multiples of 2^-43 of the largest, so a
  * token does not depend on the order of a sum and is the same in every run.
  * V up to 2^20. Z needs the alignment of its elements only (faster with 16-byte
  * aligned rows). No workspace, one launch, nothing is kept between calls. */

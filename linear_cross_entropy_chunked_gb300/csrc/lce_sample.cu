@@ -14,23 +14,27 @@
 // sum, and a border of the cumulative distribution must lie where the formula
 // puts it. So weights are whole numbers, w_i in units of 2^-43 (64-bit sums
 // of up to 2^20 tokens are exact and the same in any order), and exp is computed
-// to a relative error of about 2^-31: the sum of border displacements over a row
-// of 2^17 equally likely tokens is about 1e-8, which bounds the chance that u falls
-// on the wrong side of one. An fp32 softmax would put it at about 1e-2.
-// A weight is cut, not rounded, to its unit (which saves three instructions per logit): a border
-// moves by less than 2^-43 of the largest weight per token, 1.5e-8 over 2^17 of them.
+// to a relative error of about 2^-31. A weight is rounded to its unit, to nearest, so that the errors of a
+// row's tokens have no common sign. The chance that u falls on the wrong side of a border, which is the sum
+// over all borders of how far they are off: 1e-8 for 2^17 equally likely tokens, 1e-6 for 128256 normal
+// logits with a few likely ones at temperature 0.7, 5e-7 for 128256 tokens 16 below a single likely one, 2e-5
+// for 2^20 of those. (Weights cut to their unit would have it at 8e-5, 5e-4 and 2e-2 in the last three, the
+// exponential in fp32 with exact sums at 4e-4, 4e-6 and 2e-4, an fp32 softmax at about 1e-2. Equal
+// logits are rounded alike: 1e-4 and 7e-3 for 128256 and 2^20 of them 16 below a single one.)
 //
 // Bound: one read of the logits. A cluster of CTAs holds a row in shared memory,
 // so every later pass (the search for the cut, the sums, the draw) stays on chip; the
 // CTAs exchange maxima, histograms and sums through distributed shared memory. Rows
 // longer than the cluster's shared memory, and long rows of large batches, for which small
 // clusters are faster, are read again from L2 instead.
-// Measured: 1 x 32000 bf16 5.7 us, 64 x 128256 bf16 18 us, 256 x 128256 bf16 61 us and fp32 67 us
-// (1.9 TB/s; the read alone would take 19 us). What takes the time: about 35 instructions per logit
-// for the exponential, and a CTA's start, exchanges and tail, which the second CTA of an SM
-// covers in part. 64 x 128256 bf16 with top-k 50 takes 15 us; with top-p 0.9 of flat rows, whose
-// cut lies beyond the list, 60 us, in three parts: the histogram, the keys of its bin, and the
-// sums of what is kept with the draw.
+// Measured: 1 x 32000 bf16 6.0 us, 64 x 128256 bf16 20 us, 256 x 128256 bf16 66 us and fp32 73 us
+// (1.8 TB/s; the read alone would take 19 us). What takes the time: about 37 instructions per logit
+// for the exponential (its rounding is 3 of them: with cut weights these four take 5.9, 19, 62 and 67), and a
+// CTA's start, exchanges and tail, which the second CTA of an SM
+// covers in part. 64 x 128256 bf16 with top-k 50 takes 17 us; with top-p 0.9 of flat rows, whose
+// cut lies beyond the list, 63 us, in three parts: the histogram, the keys of its bin, and the
+// sums of what is kept with the draw. (Figures further down that compare variants of this kernel were taken
+// with cut weights.)
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -59,7 +63,6 @@ static_assert(SMP_SWEEPS == 32, "one lane per sweep of a warp");
 constexpr int SMP_LIMB = 15;                         // bits per limb of a weight: 2^17 limbs fit 32 bits
 
 constexpr int SMP_STEP_BITS = 8, SMP_STEPS = 1 << SMP_STEP_BITS;   // the exponential's table: 2^(-j / 256)
-constexpr float SMP_X_CLAMP = 31.18f;                // n = 11516, a shift by 63: weight 0
 
 constexpr float SMP_ROUND = 12582912.f;              // 1.5 * 2^23
 
@@ -230,16 +233,22 @@ __device__ __forceinline__ float smp_x(float z, const SmpRow &r) {
 }
 
 // exp(-(m - z) / temperature) in units of 2^-43 of two logits (in packed fp32 arithmetic, which
-// halves the instructions). x is carried in two floats (xh + xl, from m - z = d + dl exactly);
+// halves the instructions). x is carried in two floats (x + xl, from m - z = d + dl exactly);
 // x = n ln(2) / 256 + rr, exp(-x) = 2^-(n / 256) * (1 + q) with q = exp(-rr) - 1, |rr| < 0.0014.
-// Table and 1 + q are whole numbers of 31 bits (2^-31), their product exact; the shift by
-// n / 256 cuts what lies below a unit. The largest logit's weight is 2^43 exactly. (A table
+// Table and 1 + q are whole numbers of 31 bits (2^-31), their product exact; half a unit is
+// added to it, and the shift by n / 256 leaves whole units. The largest logit's weight is 2^43 exactly. (A table
 // of 64 needs one more term of q, and a conversion for the whole number of 1 + q that here
 // comes out of the last addition's rounding: |q| < 2^22 units.) NaN has weight 0.
 __device__ __forceinline__ u64 smp_finish(float kf, float q31, const unsigned *tab) {
     const unsigned n = static_cast<unsigned>(__float_as_int(kf));
     const unsigned f = static_cast<unsigned>(__float_as_int(q31)) + (0x80000000u - 0x4b400000u);
-    return (static_cast<u64>(tab[n & (SMP_STEPS - 1)]) * f) >> ((n >> SMP_STEP_BITS) & 63);
+    // 19 and more. From 64 on, and for any x beyond, infinite ones and NaN too, PTX's shift gives 0
+    // whatever is shifted (64 x 128256 bf16 20.3 us; with x held at 32 first 20.6)
+    const unsigned shift = (n - 0x4b400000u) >> SMP_STEP_BITS;
+    u64 half, w;
+    asm("shl.b64 %0, %1, %2;" : "=l"(half) : "l"(1ull), "r"(shift - 1));
+    asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"(static_cast<u64>(tab[n & (SMP_STEPS - 1)]) * f + half), "r"(shift));
+    return w;
 }
 __device__ __forceinline__ void smp_weight2(float z0, float z1, const SmpRow &r, const SampleTables &c,
                                             const unsigned *tab, u64 &w0, u64 &w1) {
@@ -252,12 +261,10 @@ __device__ __forceinline__ void smp_weight2(float z0, float z1, const SmpRow &r,
     float2 xl = __ffma2_rn(d, ih, __fmul2_rn(x, minus));
     xl = __ffma2_rn(d, two(r.il), xl);
     xl = __ffma2_rn(dl, ih, xl);
-    // (beyond the end, and for a temperature of infinity, x is a number again: no NaN below)
-    const float2 xh = make_float2(fminf(x.x, SMP_X_CLAMP), fminf(x.y, SMP_X_CLAMP));
-    const float2 k = __ffma2_rn(xh, c.inv, c.magic);
+    const float2 k = __ffma2_rn(x, c.inv, c.magic);
     const float2 nf = __fadd2_rn(k, c.mmagic);
     xl = __ffma2_rn(nf, c.mc3, xl);
-    float2 rr = __ffma2_rn(nf, c.mc1, xh);              // exact
+    float2 rr = __ffma2_rn(nf, c.mc1, x);               // exact
     rr = __fadd2_rn(__ffma2_rn(nf, c.mc2, rr), xl);
     float2 q = __ffma2_rn(rr, c.p3, c.p2);
     q = __ffma2_rn(rr, q, c.p1);

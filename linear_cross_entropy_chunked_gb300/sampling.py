@@ -32,8 +32,9 @@ def sample_logits(Z, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=N
     top_p, min-p the tokens at least min_p times as likely as the first; the token is
     the first, by index, at which the kept probability exceeds u, and logprobs the log
     of its share of it. temperature 0 is greedy. -inf and NaN logits are never drawn; a
-    row of nothing else gives token -1 and logprob -inf. The same inputs give the same
-    tokens in every run. tokens / logprobs: where to write them. V up to 2^20."""
+    row of nothing else gives token -1 and logprob -inf. Weights are rounded to multiples of
+    2^-43 of the largest and their sums exact: the same inputs give the same tokens in every
+    run. tokens / logprobs: where to write them. V up to 2^20."""
     if not (Z.is_cuda and u.is_cuda):
         raise ValueError("Z and u must be CUDA tensors (there is no CPU path)")
     if Z.dtype not in _b._CE_DTYPES or u.dtype != torch.float32:
