@@ -322,8 +322,8 @@ lce_status lce_fp8_linear(const void *X, int x_dtype, int64_t ldx, const void *W
  * read before the call returns; so is outs (NULL: in place), whose tensors have the
  * dtypes of their gradients. *norm is a device fp32 word. A NaN or an infinity among
  * the gradients reaches the norm, and a norm that is NaN (infinite) makes the factor NaN
- * (0), as the formula says. Squares are formed in fp32: values above 1.8e19 give an
- * infinite 2-norm. Where the factor is 1, tensors in place are not written.
+ * (0), as the formula says. Finite gradients of any size have the norm that the formula gives,
+ * infinite only where it exceeds fp32's largest number. Where the factor is 1, tensors in place are not written.
  * A tensor that is written may overlap no other tensor of the call, except that an
  * output may be its own gradient: LCE_ERR_INVALID_ARG. Tensors need the alignment of their
  * elements only. The result does not depend on the run. Work: one read for the

@@ -13,7 +13,10 @@
 // another buffer took 1.18 ms; so it takes 1.00 ms, the norm at 6.9 TB/s, the scaling at 6.0.
 // Sums: fp32 over the 64 bytes a thread holds of one chunk, which go into a compensated
 // fp32 pair per thread; fp64 across threads and CTAs, always in the same order, so a norm is
-// the same in every run. Every CTA of the scaling launch adds up the CTAs' partial sums
+// the same in every run. Squares of large and of tiny values do not fit fp32: where a thread's sum of a
+// chunk's squares leaves [2^-100, 2^100] it is formed again in fp64 (from L1), so that the 2-norm is right
+// for all values of the types; between these borders, squares lost below fp32's numbers are under 2^-44 of
+// the sum, and a thread's sum over its chunks (2^21 at most) stays below 2^121. Every CTA of the scaling launch adds up the CTAs' partial sums
 // itself (a few KB from L2), which saves a launch in between. The scaling runs through the
 // chunks backwards: the end of the list, which the norm has just read, is still in L2.
 #include "lce_internal.h"
@@ -25,6 +28,7 @@ namespace {
 constexpr int CLIP_THREADS = 512;
 constexpr int CLIP_VECS = 4;                                   // 16-byte vectors per thread and chunk
 constexpr int CLIP_CHUNK = CLIP_THREADS * CLIP_VECS * 16;      // 32 KB
+constexpr int CLIP_CTAS_PER_SM = 4;    // 2048 threads: 128 KB of loads in flight per SM
 
 // A tensor's values seen as the 16-byte vectors of the 128-byte lines that hold them (a warp
 // reads whole lines): vectors at both ends may be partly or wholly outside.
@@ -180,6 +184,22 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *red) {
     return __reduce_max_sync(0xffffffffu, l < CLIP_THREADS / 32 ? red[l] : 0u);
 }
 
+// Sums of a thread's squares outside these go by fp64.
+constexpr float CLIP_SQ_MIN = 0x1p-100f, CLIP_SQ_MAX = 0x1p100f;
+
+// Squares of the thread's values of a chunk in fp64.
+__device__ __forceinline__ double clip_squares(const ClipSpan &s, long long o) {
+    double a = 0.0;
+#pragma unroll 1
+    for (int q = 0; q < CLIP_VECS; ++q) {
+        float x[8];
+        clip_unpack(clip_load<false>(s, o + q * CLIP_THREADS * 16), s.dtype, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a += static_cast<double>(x[j]) * static_cast<double>(x[j]);
+    }
+    return a;
+}
+
 // Adds v to the pair (s, c): s + c is the sum to about twice fp32's precision.
 __device__ __forceinline__ void add_pair(float &s, float &c, float v) {
     const float n = s + v;
@@ -189,11 +209,13 @@ __device__ __forceinline__ void add_pair(float &s, float &c, float v) {
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(CLIP_THREADS)
+__global__ void __launch_bounds__(CLIP_THREADS, CLIP_CTAS_PER_SM)
     lce_grad_norm_kernel(const __grid_constant__ ClipTable<CAP> tb, const int kind, double *part) {
     __shared__ double red[CLIP_THREADS / 32];
     __shared__ uint32_t redm[CLIP_THREADS / 32];
+    __shared__ double wide[CLIP_THREADS];   // a thread's squares that did not fit fp32
     const int total = tb.first[tb.n];
+    wide[threadIdx.x] = 0.0;
     float s = 0.f, c = 0.f;
     uint32_t mx = 0u;
     int i = clip_find(tb, blockIdx.x);
@@ -208,8 +230,10 @@ __global__ void __launch_bounds__(CLIP_THREADS)
 #pragma unroll
         for (int q = 0; q < CLIP_VECS; ++q) v[q] = clip_load<false>(sp, o + q * CLIP_THREADS * 16);
         float a = 0.f, b = 0.f;
+        uint32_t any = 0u;
 #pragma unroll
         for (int q = 0; q < CLIP_VECS; ++q) {
+            any |= v[q].x | v[q].y | v[q].z | v[q].w;
             float x[8];
             clip_unpack(v[q], sp.dtype, x);
             if (kind == CLIP_NORM_2) {
@@ -229,6 +253,10 @@ __global__ void __launch_bounds__(CLIP_THREADS)
                 for (int j = 0; j < 8; ++j) mx = max(mx, clip_bits(x[j]));
             }
         }
+        if (kind == CLIP_NORM_2 && !(a + b >= CLIP_SQ_MIN && a + b <= CLIP_SQ_MAX)) {
+            if (any & (sp.dtype == CE_FP32 ? 0x7fffffffu : 0x7fff7fffu)) wide[threadIdx.x] += clip_squares(sp, o);
+            continue;
+        }
         add_pair(s, c, a + b);
     }
     if (kind == CLIP_NORM_INF) {
@@ -236,7 +264,8 @@ __global__ void __launch_bounds__(CLIP_THREADS)
         if (threadIdx.x == 0) part[blockIdx.x] = static_cast<double>(__uint_as_float(mx));
     } else {
         // (an infinite sum has no correction)
-        const double v = static_cast<double>(s) + (fabsf(s) < INFINITY ? static_cast<double>(c) : 0.0);
+        const double v = static_cast<double>(s) + (fabsf(s) < INFINITY ? static_cast<double>(c) : 0.0) +
+                         wide[threadIdx.x];
         const double sum = block_sum(v, red);
         if (threadIdx.x == 0) part[blockIdx.x] = sum;
     }
@@ -286,8 +315,6 @@ __global__ void __launch_bounds__(CLIP_THREADS)
         for (int q = 0; q < CLIP_VECS; ++q) clip_store(sp, o + q * CLIP_THREADS * 16, clip_scale(v[q], sp.dtype, f));
     }
 }
-
-constexpr int CLIP_CTAS_PER_SM = 4;    // 2048 threads: 128 KB of loads in flight per SM
 
 template <int CAP>
 void fill_table(ClipTable<CAP> &tb, const ClipItem *items, int n) {
