@@ -79,16 +79,23 @@ template <typename T> struct QtVec {
             const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p));
             w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
         } else if (n >= 8) {
-            // a row that starts anywhere: the aligned words that hold the values
+            // a row that starts anywhere: aligned words, of an odd address the first and the last value
+            // alone (no byte beside the values is read)
             const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-            const bool odd = (a & 2u) != 0;
-            const uint32_t *u = reinterpret_cast<const uint32_t *>(a - (a & 2u));
+            if (a & 2u) {
+                const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+                const uint32_t *u = reinterpret_cast<const uint32_t *>(a + 2);
+                const uint32_t first = h[0], last = h[7];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = u[j];
-            if (odd) {
-                const uint32_t end = u[4];
+                for (int j = 0; j < 3; ++j) w[j] = u[j];
+                w[3] = __funnelshift_r(w[2], last, 16);
+                w[2] = __funnelshift_r(w[1], w[2], 16);
+                w[1] = __funnelshift_r(w[0], w[1], 16);
+                w[0] = first | (w[0] << 16);
+            } else {
+                const uint32_t *u = reinterpret_cast<const uint32_t *>(a);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], j < 3 ? w[j + 1] : end, 16);
+                for (int j = 0; j < 4; ++j) w[j] = u[j];
             }
         } else {
             const uint16_t *h = reinterpret_cast<const uint16_t *>(p);

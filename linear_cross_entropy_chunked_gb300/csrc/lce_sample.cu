@@ -134,15 +134,19 @@ template <typename T> __device__ __forceinline__ void smp_load_vec(const T *p, f
         smp_unpack(*reinterpret_cast<const uint4 *>(p), x, static_cast<const T *>(nullptr));
     }
 }
-// 8 logits of 16 bits from any address: the aligned words that hold them.
+// 8 logits of 16 bits from any address, by words where they are aligned and no byte beside them: of an odd
+// address the first and the last logit come alone.
 __device__ __forceinline__ uint4 smp_load_words(const void *p) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    const uint32_t *u = reinterpret_cast<const uint32_t *>(a - (a & 2u));
-    uint4 w = make_uint4(u[0], u[1], u[2], u[3]);
-    if (a & 2u)
-        w = make_uint4(__funnelshift_r(w.x, w.y, 16), __funnelshift_r(w.y, w.z, 16), __funnelshift_r(w.z, w.w, 16),
-                       __funnelshift_r(w.w, u[4], 16));
-    return w;
+    if (a & 2u) {
+        const uint32_t first = *static_cast<const uint16_t *>(p), last = static_cast<const uint16_t *>(p)[7];
+        const uint32_t *u = reinterpret_cast<const uint32_t *>(a + 2);
+        const uint32_t w0 = u[0], w1 = u[1], w2 = u[2];
+        return make_uint4(first | (w0 << 16), __funnelshift_r(w0, w1, 16), __funnelshift_r(w1, w2, 16),
+                          (w2 >> 16) | (last << 16));
+    }
+    const uint32_t *u = reinterpret_cast<const uint32_t *>(a);
+    return make_uint4(u[0], u[1], u[2], u[3]);
 }
 // 8 logits from global memory; those past `n` are -infinity. (Rows that start anywhere by words:
 // 512 x 50257 fp16 62.5 us, value by value 67.9.)
