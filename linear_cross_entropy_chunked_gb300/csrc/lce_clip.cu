@@ -13,12 +13,15 @@
 // another buffer took 1.18 ms; so it takes 1.00 ms, the norm at 6.9 TB/s, the scaling at 6.0.
 // Sums: fp32 over the 64 bytes a thread holds of one chunk, which go into a compensated
 // fp32 pair per thread; fp64 across threads and CTAs, always in the same order, so a norm is
-// the same in every run. Squares of large and of tiny values do not fit fp32: where a thread's sum of a
-// chunk's squares leaves [2^-100, 2^100] it is formed again in fp64 (from L1), so that the 2-norm is right
-// for all values of the types; between these borders, squares lost below fp32's numbers are under 2^-44 of
-// the sum, and a thread's sum over its chunks (2^21 at most) stays below 2^121. Every CTA of the scaling launch adds up the CTAs' partial sums
-// itself (a few KB from L2), which saves a launch in between. The scaling runs through the
-// chunks backwards: the end of the list, which the norm has just read, is still in L2.
+// the same in every run. Squares of large and of tiny values do not fit fp32: where a thread's sum
+// of a chunk's squares leaves [2^-100, 2^100] it is formed again from scaled values (read from L1) and
+// added up in fp64, so that the 2-norm is right for all values of the types (200M fp32 of 1e-3 152 us,
+// of 1e-20 166 us; with fp64 squares in place of scaled ones 1483). Between these borders, squares lost
+// below fp32's numbers are under 2^-44 of the sum, and a thread's sum over its chunks (2^21 at most)
+// stays below 2^121.
+// Every CTA of the scaling launch adds up the CTAs' partial sums itself (a few KB from L2), which
+// saves a launch in between. The scaling runs through the chunks backwards: the end of the list, which
+// the norm has just read, is still in L2.
 #include "lce_internal.h"
 
 namespace lce {
@@ -184,20 +187,26 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *red) {
     return __reduce_max_sync(0xffffffffu, l < CLIP_THREADS / 32 ? red[l] : 0u);
 }
 
-// Sums of a thread's squares outside these go by fp64.
+// Sums of a thread's squares outside these are formed again from values times 2^-80 or 2^80.
 constexpr float CLIP_SQ_MIN = 0x1p-100f, CLIP_SQ_MAX = 0x1p100f;
 
-// Squares of the thread's values of a chunk in fp64.
-__device__ __forceinline__ double clip_squares(const ClipSpan &s, long long o) {
-    double a = 0.0;
+// The thread's squares of a chunk, `large` or small. Large: the largest value is at least 2^47, and
+// 2^48 at most after scaling, so what is lost is below 2^-83 of the sum. Small: values below 2^-50 are below
+// 2^30 after scaling, and the square of the smallest, 2^-149, is 2^-138.
+__device__ __forceinline__ double clip_squares(const ClipSpan &s, long long o, bool large) {
+    const float f = large ? 0x1p-80f : 0x1p80f;
+    float a = 0.f, b = 0.f;
 #pragma unroll 1
     for (int q = 0; q < CLIP_VECS; ++q) {
         float x[8];
         clip_unpack(clip_load<false>(s, o + q * CLIP_THREADS * 16), s.dtype, x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a += static_cast<double>(x[j]) * static_cast<double>(x[j]);
+        for (int j = 0; j < 8; j += 2) {
+            a = fmaf(x[j] * f, x[j] * f, a);
+            b = fmaf(x[j + 1] * f, x[j + 1] * f, b);
+        }
     }
-    return a;
+    return static_cast<double>(a + b) * (large ? 0x1p160 : 0x1p-160);
 }
 
 // Adds v to the pair (s, c): s + c is the sum to about twice fp32's precision.
@@ -254,7 +263,8 @@ __global__ void __launch_bounds__(CLIP_THREADS, CLIP_CTAS_PER_SM)
             }
         }
         if (kind == CLIP_NORM_2 && !(a + b >= CLIP_SQ_MIN && a + b <= CLIP_SQ_MAX)) {
-            if (any & (sp.dtype == CE_FP32 ? 0x7fffffffu : 0x7fff7fffu)) wide[threadIdx.x] += clip_squares(sp, o);
+            if (any & (sp.dtype == CE_FP32 ? 0x7fffffffu : 0x7fff7fffu))
+                wide[threadIdx.x] += clip_squares(sp, o, !(a + b < CLIP_SQ_MIN));
             continue;
         }
         add_pair(s, c, a + b);
