@@ -37,6 +37,7 @@ constexpr int kMaxDevices = 64;
 bool g_dev_ready[kMaxDevices] = {};
 int g_dev_sms[kMaxDevices] = {};
 int g_dev_pairs[kMaxDevices] = {};   // co-resident CTA pairs of the GEMM kernel (0: no pairs)
+bool g_dev_fp8[kMaxDevices] = {};    // the 8-bit product's kernels can run (else only its calls fail)
 
 // GEMM tiles run on CTA pairs (tcgen05 cta_group::2, 256 x 256 tiles) when the
 // device can co-schedule them; LCE_GEMM_CLUSTER=1 selects one CTA per 128 x 256
@@ -71,7 +72,8 @@ lce_status init_device(int *sms, int *pairs) {
         if (aux_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
         if (ce_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
         if (sample_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
-        if (fp8_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
+        g_dev_fp8[dev] = fp8_set_attributes() == cudaSuccess;
+        if (!g_dev_fp8[dev]) cudaGetLastError();
         int np = 0;
         if (gemm_max_pairs(&np) != cudaSuccess) {
             cudaGetLastError();
@@ -84,6 +86,14 @@ lce_status init_device(int *sms, int *pairs) {
     *sms = g_dev_sms[dev];
     *pairs = cluster_choice() == 2 ? g_dev_pairs[dev] : 0;
     return LCE_OK;
+}
+
+// Whether the 8-bit product's kernels can run on the current device, which init_device has set up.
+bool fp8_ready() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+    std::lock_guard<std::mutex> lock(g_mu);
+    return g_dev_fp8[dev];
 }
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -1166,6 +1176,7 @@ lce_status fp8_matmul(const void *A, int64_t lda, const float *sa, int64_t sa_ro
     int sms = 0, pairs = 0;
     st = init_device(&sms, &pairs);
     if (st != LCE_OK) return st;
+    if (!fp8_ready()) return LCE_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (M == 0 || N == 0)
         return cudaMemsetAsync(ws, 0, sizeof(int), s) == cudaSuccess ? LCE_OK : LCE_ERR_CUDA;
