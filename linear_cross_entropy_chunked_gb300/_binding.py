@@ -229,6 +229,15 @@ class _on:
         return False
 
 
+def _wrote(tensors):
+    """Tells autograd that the library has written to these tensors of the caller: a backward
+    pass that saved one refuses to run, as after torch's own in-place operations."""
+    try:
+        torch.autograd.graph.increment_version(tensors)
+    except RuntimeError:   # inference tensors, of which no graph can have saved one, keep no version
+        torch.autograd.graph.increment_version([t for t in tensors if not t.is_inference()])
+
+
 def _check(st: int, what: str):
     if st != 0:
         raise LCEError(st, what)

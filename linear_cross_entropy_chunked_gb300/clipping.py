@@ -93,7 +93,8 @@ def clip_grad_norm(grads, max_norm, norm_type=2.0, eps=1e-6, out=None, ws=None, 
     dtypes, sizes and layouts, and returns their norm (1, 2 or inf over all values; a device fp32
     scalar; the host does not wait). The factor is formed on the device: gradients
     whose norm is below max_norm stay as they are and are not written in place. A norm
-    that is NaN (infinite) makes the factor NaN (0)."""
+    that is NaN (infinite) makes the factor NaN (0). To autograd the tensors count as written
+    either way: a backward pass that saved one of them refuses to run afterwards."""
     kind = _kind(norm_type)
     max_norm, eps = float(max_norm), float(eps)
     if not max_norm >= 0.0 or not 0.0 <= eps < math.inf:
@@ -113,4 +114,5 @@ def clip_grad_norm(grads, max_norm, norm_type=2.0, eps=1e-6, out=None, ws=None, 
         _b._check(_b.lib().lce_clip_grad_norm(_at(ptrs), _at(sizes), _at(codes), dst, n, kind, max_norm, eps,
                                               norm.data_ptr(), ws.data_ptr(), ws_bytes, s),
                   "lce_clip_grad_norm")
+    _b._wrote(grads if out is None else out)
     return norm

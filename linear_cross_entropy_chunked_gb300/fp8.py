@@ -176,8 +176,11 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, ws=No
         raise ValueError(f"ws must be a contiguous, 16-byte aligned uint8 tensor of at least {_WS_BYTES} bytes")
     with _b._on(a.device, stream) as s:
         if out is None:
-            out = _empty_out(a.shape[0], b.shape[0], out_dtype, a.device)
-        return _matmul(a, a_scale, lda, b, b_scale, ldb, b_rows, out, ws, s)
+            return _matmul(a, a_scale, lda, b, b_scale, ldb, b_rows,
+                           _empty_out(a.shape[0], b.shape[0], out_dtype, a.device), ws, s)
+        _matmul(a, a_scale, lda, b, b_scale, ldb, b_rows, out, ws, s)
+    _b._wrote((out,))
+    return out
 
 
 def _logits(X, q, scale, s):

@@ -58,6 +58,7 @@ def sample_logits(Z, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=N
         raise ValueError("top_k must be a whole number, 0 for all tokens")
     if not 0.0 <= p_all <= 1.0 or not 0.0 <= q_all <= 1.0:
         raise ValueError("top_p and min_p must lie in [0, 1]")
+    given = [t for t in (tokens, logprobs) if t is not None]
     with _b._on(dev, stream) as s:
         if tokens is None:
             tokens = torch.empty(N, dtype=torch.int64, device=dev)
@@ -73,4 +74,6 @@ def sample_logits(Z, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=N
                                              t, k, p, q, t_all, min(int(k_all), V), p_all, q_all,
                                              tokens.data_ptr(), logprobs.data_ptr(), s),
                   "lce_sample_logits")
+    if given:
+        _b._wrote(given)
     return tokens, logprobs
