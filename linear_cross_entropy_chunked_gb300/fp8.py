@@ -183,7 +183,12 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, ws=No
     return out
 
 
-def _logits(X, q, scale, s):
+def _collect(status, ws, at=0):
+    """Adds the device status in the workspace header at byte `at` of ws to the caller's."""
+    status[:4].view(torch.int32).bitwise_or_(ws[at:at + 4].view(torch.int32))
+
+
+def _logits(X, q, scale, status, s):
     """X W^T on the current device and stream, for W's tiles."""
     M, D = X.shape
     V = q.shape[0]
@@ -198,6 +203,8 @@ def _logits(X, q, scale, s):
         X.data_ptr(), code, X.stride(0) if M > 1 else D, q.data_ptr(), q.stride(0) if V > 1 else _pad16(D),
         scale.data_ptr(), *scale.stride(), M, V, D, Z.data_ptr(), Z.stride(0) if M > 1 else -(-V // 8) * 8, code,
         ws.data_ptr(), nbytes, s), "lce_fp8_linear")
+    if status is not None:
+        _collect(status, ws)
     return Z
 
 
@@ -248,13 +255,13 @@ class FP8LinearFunction(torch.autograd.Function):
     pass in one buffer, those of the backward pass in another."""
 
     @staticmethod
-    def forward(ctx, X, W, q, scale, q_t, scale_t):
+    def forward(ctx, X, W, q, scale, q_t, scale_t, status=None):
         need_dX, need_dW = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
-        ctx.x_dtype, ctx.w_dtype = X.dtype, None if W is None else W.dtype
+        ctx.x_dtype, ctx.w_dtype, ctx.status = X.dtype, None if W is None else W.dtype, status
         with _b._on(X.device, None) as s:
             if W is None:
                 ctx.save_for_backward(q_t, scale_t)
-                return _logits(X, q, scale, s)
+                return _logits(X, q, scale, status, s)
             (M, D), V = X.shape, W.shape[0]
             x, w = _at(0, M, D, False), _at(0, V, D, True)
             wt = _at(0, D, V, True).end if need_dX else 0
@@ -268,6 +275,8 @@ class FP8LinearFunction(torch.autograd.Function):
             _quantize_at(X, False, x, _at(kept.data_ptr() + wt, D, M, False) if need_dW else None, s)
             Z = _empty_out(M, V, X.dtype, X.device)
             _matmul_at(x, w, False, M, V, D, Z, w.end, nbytes, s)
+            if status is not None:
+                _collect(status, here, w.end - here.data_ptr())
         ctx.save_for_backward(kept)
         ctx.D = D
         return Z
@@ -277,7 +286,7 @@ class FP8LinearFunction(torch.autograd.Function):
     def backward(ctx, dZ):
         need_dX, need_dW = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
         if not (need_dX or need_dW):
-            return None, None, None, None, None, None
+            return (None,) * 7
         if dZ.stride(1) != 1 or (dZ.shape[0] > 1 and dZ.stride(0) < dZ.shape[1]):
             dZ = dZ.contiguous()
         M, V = dZ.shape
@@ -300,24 +309,35 @@ class FP8LinearFunction(torch.autograd.Function):
             if need_dX:
                 dX = _empty_out(M, D, ctx.x_dtype, dZ.device)
                 _matmul_at(z, wt, False, M, D, V, dX, at, nbytes, s)
+                if ctx.status is not None:
+                    _collect(ctx.status, here, at - here.data_ptr())
             if need_dW:
                 if M == 0:
                     dW = torch.zeros(V, D, dtype=ctx.w_dtype, device=dZ.device)
                 else:
                     dW = _empty_out(V, D, ctx.w_dtype, dZ.device)
                     _matmul_at(zt, xt, True, V, D, M, dW, at, nbytes, s)
-        return dX, dW, None, None, None, None
+                    if ctx.status is not None:
+                        _collect(ctx.status, here, at - here.data_ptr())
+        return dX, dW, None, None, None, None, None
 
 
-def fp8_linear(X, W):
+def fp8_linear(X, W, status=None):
     """X W^T computed in e4m3 with blocks of 128, in X's dtype: logits [M, V] for the hidden
     states X [M, D] (bf16, fp16 or fp32). W: a weight [V, D] (bf16, fp16 or fp32), quantised in
     the call and differentiable, or an FP8Weight, which is frozen (its transpose is needed
     where X requires a gradient). Differentiable in X and W; the gradients are
-    products in e4m3 too, and have no derivatives themselves. The logits' row stride is V rounded up to 16 bytes. (A backward pass
+    products in e4m3 too, and have no derivatives themselves. The logits' row stride is V rounded up
+    to 16 bytes. status: a uint8 tensor of at least 1024 bytes, zeros at first, that collects the device
+    status of the layer's products, the forward's and the backward's, until read_status(status)
+    returns and clears it (a product whose bounded wait ran out has wrong results; without `status`
+    that is not noticed). (A backward pass
     is captured into a CUDA graph as any other of torch's: no eager graph of the same leaves may
     live meanwhile; X.detach().requires_grad_() gives a leaf of its own.)"""
     _check_dense_rows("X", X, _b._CE_DTYPES, "bfloat16, float16 or float32")
+    if status is not None and (status.device != X.device or status.dtype != torch.uint8 or status.data_ptr() % 16
+                               or not status.is_contiguous() or status.dim() != 1 or status.numel() < _WS_BYTES):
+        raise ValueError(f"status must be a 16-byte aligned uint8 tensor of at least {_WS_BYTES} bytes on the device of X")
     D = X.shape[1]
     if isinstance(W, FP8Weight):
         q, scale = W.q, W.scale
@@ -329,16 +349,16 @@ def fp8_linear(X, W):
             raise ValueError("the scales of W must be per tile of 128 x 128")
         if not (X.requires_grad and torch.is_grad_enabled()):
             with _b._on(X.device, None) as s:
-                return _logits(X, q, scale, s)
+                return _logits(X, q, scale, status, s)
         if W.q_t is None or W.scale_t is None:
             raise ValueError("the gradient of X needs W's transpose (fp8_weight(W, transpose=True))")
         _check_operand("W's transpose", W.q_t, W.scale_t, False)
         if W.q_t.shape != (D, V) or W.q_t.device != X.device or W.scale_t.shape != (_blocks(D), _blocks(V)):
             raise ValueError("W's transpose must be [D, V] in tiles of 128 x 128")
-        return FP8LinearFunction.apply(X, None, q, scale, W.q_t, W.scale_t)
+        return FP8LinearFunction.apply(X, None, q, scale, W.q_t, W.scale_t, status)
     _check_dense_rows("W", W, _b._CE_DTYPES, "bfloat16, float16 or float32, or an FP8Weight")
     if D != W.shape[1] or X.device != W.device or W.shape[0] == 0:
         raise ValueError(f"X{tuple(X.shape)} and W{tuple(W.shape)} must share their columns and device")
     if not torch.is_grad_enabled():   # (no transposes for a backward pass that cannot come)
         X, W = X.detach(), W.detach()
-    return FP8LinearFunction.apply(X, W, None, None, None, None)
+    return FP8LinearFunction.apply(X, W, None, None, None, None, status)
