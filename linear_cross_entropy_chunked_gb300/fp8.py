@@ -328,7 +328,7 @@ def fp8_linear(X, W, status=None):
     the call and differentiable, or an FP8Weight, which is frozen (its transpose is needed
     where X requires a gradient). Differentiable in X and W; the gradients are
     products in e4m3 too, and have no derivatives themselves. The logits' row stride is V rounded up
-    to 16 bytes. status: a uint8 tensor of at least 1024 bytes, zeros at first, that collects the device
+    to 16 bytes, the gradients' D. status: a uint8 tensor of at least 1024 bytes, zeros at first, that collects the device
     status of the layer's products, the forward's and the backward's, until read_status(status)
     returns and clears it (a product whose bounded wait ran out has wrong results; without `status`
     that is not noticed). (A backward pass
