@@ -215,6 +215,8 @@ class _on:
         self._dev, self._stream, self._entered = dev, stream, ()
 
     def __enter__(self):
+        if self._stream is not None and self._stream.device != self._dev:
+            raise ValueError(f"stream belongs to {self._stream.device}, the tensors to {self._dev}")
         if self._dev.index is not None and self._dev.index != torch.cuda.current_device():
             self._entered += (torch.cuda.device(self._dev),)
             self._entered[-1].__enter__()
