@@ -254,11 +254,11 @@ struct SampleParams {
     long long *tokens;        // [N]
     float *logprobs;          // [N] or null
 };
-// 2^(-j / 64) in units of 2^-31; ln(2) / 64 in three parts (negative), its inverse, the
-// number that rounds to whole numbers, and the polynomial of exp
+// 2^(-j / 256) in units of 2^-31; ln(2) / 256 in three parts (the last negative), its inverse
+// (negative), the number that rounds to whole numbers, and the polynomial of exp
 struct SampleTables {
     unsigned fix[256];
-    float2 mc1, mc2, mc3, inv, magic, mmagic, p3, p2, p1, round;
+    float2 c1, c2, mc3, ninv, magic, mmagic, p3, p2, p1, round;
 };
 constexpr long long SMP_MAX_V = 1ll << 20;   // weights of 2^43 in 64-bit sums
 

@@ -27,9 +27,9 @@
 // CTAs exchange maxima, histograms and sums through distributed shared memory. Rows
 // longer than the cluster's shared memory, and long rows of large batches, for which small
 // clusters are faster, are read again from L2 instead.
-// Measured: 1 x 32000 bf16 6.0 us, 64 x 128256 bf16 20 us, 256 x 128256 bf16 66 us and fp32 73 us
-// (1.8 TB/s; the read alone would take 19 us). What takes the time: about 37 instructions per logit
-// for the exponential (its rounding is 3 of them: with cut weights these four take 5.9, 19, 62 and 67), and a
+// Measured: 1 x 32000 bf16 5.8 us, 64 x 128256 bf16 20 us, 256 x 128256 bf16 65 us and fp32 70 us
+// (1.9 TB/s; the read alone would take 19 us). What takes the time: about 36 instructions per logit,
+// nearly all for the exponential (3 of them round it; with cut weights the last two take 62 and 67 us), and a
 // CTA's start, exchanges and tail, which the second CTA of an SM
 // covers in part. 64 x 128256 bf16 with top-k 50 takes 17 us; with top-p 0.9 of flat rows, whose
 // cut lies beyond the list, 63 us, in three parts: the histogram, the keys of its bin, and the
@@ -82,20 +82,20 @@ SampleTables make_sample_tables() {
     const double c1 = std::floor(step / ulp) * ulp;
     const float c2 = static_cast<float>(step - c1);
     auto two = [](double v) { return make_float2(static_cast<float>(v), static_cast<float>(v)); };
-    t.mc1 = two(-c1);
-    t.mc2 = two(-c2);
+    t.c1 = two(c1);
+    t.c2 = two(c2);
     t.mc3 = two(-(step - c1 - static_cast<double>(c2)));
-    t.inv = two(SMP_STEPS / ln2);
+    t.ninv = two(-SMP_STEPS / ln2);
     // 1.5 * 2^23 rounds what it is added to to a whole number n, kept in its low bits; 19 is
     // added to the n / 256 there: the shift from units of 2^-62 to 2^-43
     const float magic = SMP_ROUND + 19 * SMP_STEPS;
     t.magic = two(magic);
     t.mmagic = two(-magic);
-    // exp(-r) - 1 = r (-1 + r (1 / 2 - r / 6)) in units of 2^-31, to 2^-42
+    // exp(r) - 1 = r (1 + r (1 / 2 + r / 6)) in units of 2^-31, to 2^-42
     const double S = 2147483648.0;
-    t.p3 = two(-S / 6);
+    t.p3 = two(S / 6);
     t.p2 = two(S / 2);
-    t.p1 = two(-S);
+    t.p1 = two(S);
     t.round = two(SMP_ROUND);
     return t;
 }
@@ -149,7 +149,7 @@ __device__ __forceinline__ uint4 smp_load_words(const void *p) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 // 8 logits from global memory; those past `n` are -infinity. (Rows that start anywhere by words:
-// 512 x 50257 fp16 66.8 us; with cut weights 63, and value by value 67.9.)
+// 512 x 50257 fp16 65.6 us; with cut weights 63, and value by value 67.9.)
 template <typename T>
 __device__ __forceinline__ void smp_load_global(const T *p, int n, bool aligned, float (&x)[8]) {
     if (aligned && n >= 8) {
@@ -237,8 +237,9 @@ __device__ __forceinline__ float smp_x(float z, const SmpRow &r) {
 }
 
 // exp(-(m - z) / temperature) in units of 2^-43 of two logits (in packed fp32 arithmetic, which
-// halves the instructions). x is carried in two floats (x + xl, from m - z = d + dl exactly);
-// x = n ln(2) / 256 + rr, exp(-x) = 2^-(n / 256) * (1 + q) with q = exp(-rr) - 1, |rr| < 0.0014.
+// halves the instructions). x is carried in two floats (-nx + xl, from m - z = d + dl exactly);
+// x = n ln(2) / 256 - rr, exp(-x) = 2^-(n / 256) * (1 + q) with q = exp(rr) - 1, |rr| < 0.0014. (With -x in
+// place of x no product by -1 is needed for xl: 256 x 128256 fp32 69.9 us for 72.5.)
 // Table and 1 + q are whole numbers of 31 bits (2^-31), their product exact; half a unit is
 // added to it, and the shift by n / 256 leaves whole units. The largest logit's weight is 2^43 exactly. (A table
 // of 64 needs one more term of q, and a conversion for the whole number of 1 + q that here
@@ -261,15 +262,15 @@ __device__ __forceinline__ void smp_weight2(float z0, float z1, const SmpRow &r,
     const float2 d = __ffma2_rn(z, minus, m);
     const float2 bb = __ffma2_rn(m, minus, d);
     const float2 dl = __ffma2_rn(__fadd2_rn(z, bb), minus, __ffma2_rn(__ffma2_rn(bb, minus, d), minus, m));
-    const float2 x = __fmul2_rn(d, ih);
-    float2 xl = __ffma2_rn(d, ih, __fmul2_rn(x, minus));
+    const float2 nx = __fmul2_rn(d, two(-r.ih));
+    float2 xl = __ffma2_rn(d, ih, nx);
     xl = __ffma2_rn(d, two(r.il), xl);
     xl = __ffma2_rn(dl, ih, xl);
-    const float2 k = __ffma2_rn(x, c.inv, c.magic);
+    const float2 k = __ffma2_rn(nx, c.ninv, c.magic);
     const float2 nf = __fadd2_rn(k, c.mmagic);
     xl = __ffma2_rn(nf, c.mc3, xl);
-    float2 rr = __ffma2_rn(nf, c.mc1, x);               // exact
-    rr = __fadd2_rn(__ffma2_rn(nf, c.mc2, rr), xl);
+    float2 rr = __ffma2_rn(nf, c.c1, nx);               // (exact wherever the weight is not 0)
+    rr = __ffma2_rn(xl, minus, __ffma2_rn(nf, c.c2, rr));
     float2 q = __ffma2_rn(rr, c.p3, c.p2);
     q = __ffma2_rn(rr, q, c.p1);
     q = __ffma2_rn(rr, q, c.round);
