@@ -24,7 +24,7 @@ namespace lce {
 // and the same of X^T (blocks along X's rows), turned through shared memory. Bound by
 // HBM bandwidth: 2 (4) bytes read and 1 or 2 written per value. Measured: 4096 x 50256 bf16 in row
 // blocks 111 us (5.6 TB/s), X^T 121 us (5.1 TB/s). Rows of 16-bit values that do not start on 16
-// bytes come by aligned words: 50257 columns take 157 us (value by value 236; by vectors that lanes
+// bytes come by aligned words: 50257 columns take 158 us (value by value 236; by vectors that lanes
 // shift into place between them 242).
 
 namespace {
@@ -344,7 +344,7 @@ cudaError_t launch_fp8_quantize(const Fp8QuantParams &p, int dtype, bool tile, c
 // PARTS: pairs with a long k and few tiles (gradients of an input) take every tile in
 // several parts of k, which write fp32 sums into the workspace; lce_fp8_parts_kernel adds them in order.
 // Measured with tile scales: 4096 x 8192 x 4096 113 us (2440 TFLOP/s), 4096 x 128256 x 4096 1610 us
-// (2680 TFLOP/s), 64 x 128256 x 4096 95 us (5.7 TB/s), 1 x 32000 x 4096 28 us (4.7 TB/s; 250 tiles are
+// (2680 TFLOP/s; 1700 to 1870 in a row, when the power limit holds the clocks down), 64 x 128256 x 4096 95 us (5.7 TB/s), 1 x 32000 x 4096 28 us (4.7 TB/s; 250 tiles are
 // 1.6 per SM). Pairs are bound by the operands' way from L2 into shared memory (32 KB per SM
 // and k block in 0.40 us; with a quarter of the MMAs and no reads of TMEM 4096 x 8192 x 4096 takes 89 us),
 // then by the handing over of TMEM buffers. Few rows: by HBM.

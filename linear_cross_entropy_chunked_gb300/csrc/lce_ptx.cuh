@@ -5,8 +5,8 @@
 //
 // Every wait here is bounded by a wall-clock limit read from %globaltimer; on
 // expiry the waiting CTA records FLAG_TIMEOUT in the workspace header and its
-// later waits return false at once, so a kernel can leave cleanly instead of
-// hanging the device.
+// later waits return false (after about a hundred polls), so a kernel can leave cleanly
+// instead of hanging the device.
 #pragma once
 #include "lce_internal.h"
 
@@ -63,7 +63,7 @@ struct Abort {
 constexpr int MBAR_POLLS = 64;
 
 // Bounded wait for the phase with the given parity. Returns false (and makes
-// every later wait of the CTA return false at once) when the limit runs out.
+// every later wait of the CTA give up after its first polls) when the limit runs out.
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const Abort &ab) {
     const uint32_t a = smem_u32(bar);
     if (mbar_try_wait(a, parity)) return true;
