@@ -74,3 +74,34 @@ def test_workspaces_of_any_size(m, n, k):
         assert (guard[:2048] == 85).all() and (guard[2048 + size:] == 85).all()
     check(whole, q, s, w8)
     check(shared, q, s, w8)
+
+
+def test_in_parts_captured_and_with_a_gradient():
+    m, n, k = 2560, 1024, 20000
+    X, W = make(m, n, k)
+    w8 = lce.fp8_weight(W)
+    with torch.no_grad():
+        want = lce.fp8_linear(X, w8)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = lce.fp8_linear(X, w8)
+    for _ in range(3):
+        got.zero_()
+        graph.replay()
+        assert torch.equal(got, want)
+    Xg = X.clone().requires_grad_()
+    Z = lce.fp8_linear(Xg, w8)
+    assert torch.equal(Z, want)
+    dZ = torch.randn(m, n, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).bfloat16()
+    (dX,) = torch.autograd.grad(Z, Xg, dZ)
+    q, s = lce.quantize_fp8(dZ)
+    assert torch.equal(dX, lce.fp8_matmul(q, s, w8.q_t, w8.scale_t))
+    side = torch.cuda.Stream()                 # two at once, each with a workspace of its own
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.no_grad():
+        for _ in range(4):
+            with torch.cuda.stream(side):
+                a = lce.fp8_linear(X, w8)
+            b = lce.fp8_linear(X, w8)
+            torch.cuda.synchronize()
+            assert torch.equal(a, want) and torch.equal(b, want)

@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import linear_cross_entropy_chunked_gb300 as lce
+from oracle import ops_oracle
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +87,22 @@ def test_far_logits_have_no_weight(dtype):
         z = z.flip(0)                          # the one token last: a weight before it would be drawn at u = 0
         tokens, logprobs = lce.sample_logits(z.cuda().expand(n, -1).contiguous(), (u * 0).cuda(), temperature=t)
         assert (tokens == v - 1).all() and (logprobs == 0).all(), t
+
+
+@pytest.mark.parametrize("settings", [{}, {"top_p": 0.5}, {"top_k": 700}, {"min_p": 0.5}])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_ends_of_the_temperature(dtype, settings):
+    # an infinite one makes all finite logits equally likely (the first by index are kept), a huge one nearly so;
+    # masked logits stay out, and a tiny one leaves the largest logit alone
+    n, v = 9, 3000
+    g = torch.Generator().manual_seed(7)
+    z = (torch.randn(n, v, generator=g) * 3).to(dtype)
+    z[:, ::5] = -float("inf")
+    z[:, 3::5] = float("nan")
+    t = torch.tensor([float("inf"), 1e38, 1e30, 3e-39, 1e-37, 1e-30, 1.0, 1e5, 3.4e38])
+    u = torch.rand(n, generator=g)
+    ref = ops_oracle.sample(z.double().numpy(), u.double().numpy(), t.double().numpy(), **settings)
+    tokens, logprobs = lce.sample_logits(z.cuda(), u.cuda(), temperature=t.cuda(), **settings)
+    np.testing.assert_array_equal(tokens.cpu().numpy(), ref["tokens"])
+    err = np.abs(logprobs.cpu().double().numpy() - ref["logprobs"])
+    assert (err <= 2.0 ** -22 * (ref["x"] + ref["ls"] + 1)).all()
