@@ -67,8 +67,9 @@ typedef enum lce_status {
     LCE_ERR_LABEL_RANGE = 4,   /* device: some label outside [0,V) and != ignore_index */
     LCE_ERR_TIMEOUT = 5,       /* device: a bounded pipeline wait ran out; outputs invalid */
     LCE_ERR_CUDA = 6,          /* a CUDA runtime call failed */
-    LCE_ERR_UNSUPPORTED = 7    /* current device is not sm_103, or an option combination
+    LCE_ERR_UNSUPPORTED = 7,   /* current device is not sm_103, or an option combination
                                   the library does not offer (fp16 with reduction NONE) */
+    LCE_ERR_OFFSETS = 8        /* device: offsets of sequences that decrease or leave [0, N] */
 } lce_status;
 
 /* Same type as cudaStream_t. NULL means the legacy default stream. */
@@ -237,6 +238,88 @@ lce_status lce_ce_logits(const void *Z, int z_dtype, int64_t ld, const int64_t *
                          int64_t N, int64_t V, int64_t ignore_index, int reduction,
                          const float *dloss, float *loss, float *lse, void *dZ,
                          void *ws, size_t ws_bytes, lce_stream_t stream);
+
+/* The clipped policy loss with a KL term. With logp_i = z_{i,y_i} / T - log sum_j exp(z_ij / T) the
+ * log probability of row i's drawn token y_i:
+ *   r = exp(logp - old),  f = r A,  h = min(max(r, 1 - clip_low), 1 + clip_high) A
+ *   loss_i = w (-min(f, h) + beta (exp(d) - 1 - d)),  d = ref - logp
+ *   loss = sum_i loss_i, divided by the number of counting rows for reduction MEAN
+ * and its gradient, the logits' G_ij = (p_ij - 1[j = y_i]) * c_i with
+ *   c_i = (dloss / (N_valid T)) w ((f <= h ? f : 0) + beta (exp(d) - 1)).
+ * advantages, old_logprobs, ref_logprobs, weights, logprobs: fp32 [N] on the device, 4-byte aligned. old_logprobs
+ * NULL: r = 1 (the tokens were drawn from this very policy); ref_logprobs may be NULL where
+ * beta is 0 and is not read then; weights NULL: 1 (a mean over sequences has 1 / (tokens of
+ * its sequence * sequences) there, with reduction SUM). An advantage of 0 gives 0 even where r
+ * overflows. Rows with y = ignore_index (or outside [0, V), which flags LCE_ERR_LABEL_RANGE) do
+ * not count: logprobs 0, loss 0, gradient 0, whatever the row holds (infinities and NaN too).
+ * logprobs [N]: logp, the old_logprobs of later steps. 0 <= clip_low <= 1; clip_high,
+ * beta >= 0; temperature > 0. dloss, reduction, ignore_index as above; with reduction NONE loss is
+ * loss_i [N] and dloss [N] or NULL.
+ *
+ * lce_policy_fwd_bwd: over the head, as lce_fwd_bwd_opt (6 N D V flops, chunk by chunk, the
+ * logits never in memory; flags but LCE_INPUT_FP16, for whose gradients the c_i have no
+ * known range: LCE_ERR_UNSUPPORTED). Workspace: lce_workspace_size_opt(..., flags).
+ * lce_policy_forward: loss and logprobs alone, workspace lce_forward_workspace_size.
+ * lce_policy_logits: over given logits (z_dtype as for lce_ce_logits): one read of the
+ * counting rows and one write of dZ (NULL: no gradient; Z itself: in place), V up to 524288 (16-bit) or
+ * 262144 (fp32) (more: a second read). Z, dZ: rows of any stride ld >= V from any element
+ * on, both at the same address modulo 16. Workspace: lce_ce_logits_workspace_size(N). */
+lce_status lce_policy_forward(const void *H, const void *W, const int64_t *y, const float *advantages,
+                              const float *old_logprobs, const float *ref_logprobs, const float *weights,
+                              float clip_low, float clip_high, float beta, float temperature, int64_t N,
+                              int64_t D, int64_t V, int64_t ignore_index, int64_t chunk, int reduction,
+                              float *loss, float *logprobs, void *ws, size_t ws_bytes, lce_stream_t stream);
+lce_status lce_policy_fwd_bwd(const void *H, const void *W, const int64_t *y, const float *advantages,
+                              const float *old_logprobs, const float *ref_logprobs, const float *weights,
+                              float clip_low, float clip_high, float beta, float temperature,
+                              const float *dloss, int64_t N, int64_t D, int64_t V, int64_t ignore_index,
+                              int64_t chunk, int reduction, int flags, float *loss, float *logprobs, void *dH,
+                              float *dW, void *ws, size_t ws_bytes, lce_stream_t stream);
+lce_status lce_policy_logits(const void *Z, int z_dtype, int64_t ld, const int64_t *y, const float *advantages,
+                             const float *old_logprobs, const float *ref_logprobs, const float *weights,
+                             float clip_low, float clip_high, float beta, float temperature, const float *dloss,
+                             int64_t N, int64_t V, int64_t ignore_index, int reduction, float *loss,
+                             float *logprobs, void *dZ, void *ws, size_t ws_bytes, lce_stream_t stream);
+
+/* The preference loss of paired log ratios. The rows of sequence s are offsets[s] ..
+ * offsets[s + 1] - 1 (offsets: int64 [2 pairs + 1] on the device, not decreasing, within [0, N]); the chosen
+ * sequence of pair k is sequence k, the rejected one sequence pairs + k. With L_s the sum of
+ * logp_i over the counting rows of s (average = 1: their mean; 0 without any):
+ *   m = beta ((L_c - R_c) - (L_r - R_r))
+ *   loss_k = -((1 - label_smoothing) log sigmoid(m) + label_smoothing log sigmoid(-m))
+ * with R = ref_logprobs, fp32 [2 pairs] (NULL: 0); loss: the mean or the sum over the pairs, or
+ * (reduction NONE) loss_k [pairs], with dloss [pairs] or NULL. seq_logprobs [2 pairs]: L, which is what a
+ * reference model's call gives as ref_logprobs. Rows of no sequence, and rows whose label is
+ * ignore_index, add nothing and have gradients of 0, whatever they hold. Offsets that
+ * decrease or leave [0, N] flag LCE_ERR_OFFSETS and count as the largest up to there, within [0, N].
+ *
+ * lce_preference_fwd_bwd: over the head; dH and dW both NULL: loss and seq_logprobs alone. A gradient needs
+ * every row's log probability first: the logits that the chunk buffers hold then (all, for
+ * N <= 2 chunk, or N <= chunk with LCE_LOW_MEMORY) are kept over that, the others computed again
+ * (6NDV flops, up to 8NDV). Flags but LCE_INPUT_FP16. Workspace: lce_preference_workspace_size
+ * (gradient = 0: without dH and dW).
+ * lce_preference_logits: over given logits, laid out as for lce_policy_logits: two reads of
+ * the counting rows, one write. */
+lce_status lce_preference_workspace_size(int64_t N, int64_t D, int64_t V, int64_t chunk, int64_t pairs, int flags,
+                                         int gradient, size_t *bytes);
+lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y, const int64_t *offsets,
+                                  int64_t pairs, const float *ref_logprobs, float beta, float label_smoothing,
+                                  int average, const float *dloss, int64_t N, int64_t D, int64_t V,
+                                  int64_t ignore_index, int64_t chunk, int reduction, int flags, float *loss,
+                                  float *seq_logprobs, void *dH, float *dW, void *ws, size_t ws_bytes,
+                                  lce_stream_t stream);
+lce_status lce_preference_logits_workspace_size(int64_t N, int64_t pairs, size_t *bytes);
+lce_status lce_preference_logits(const void *Z, int z_dtype, int64_t ld, const int64_t *y, const int64_t *offsets,
+                                 int64_t pairs, const float *ref_logprobs, float beta, float label_smoothing,
+                                 int average, const float *dloss, int64_t N, int64_t V, int64_t ignore_index,
+                                 int reduction, float *loss, float *seq_logprobs, void *dZ, void *ws,
+                                 size_t ws_bytes, lce_stream_t stream);
+
+/* dst[i] = src[i] * *scale for n values (types as z_dtype above, formed in fp32 and rounded once): gradients
+ * for an upstream gradient of 1 made those for *scale, a device fp32 number. dst may be src where the
+ * types are the same; the two may not overlap otherwise. Alignment of the elements. */
+lce_status lce_scale(const void *src, int src_dtype, const float *scale, int64_t n, void *dst, int dst_dtype,
+                     lce_stream_t stream);
 
 /* One token per row of logits Z [N][ld] (first V columns used, ld >= V elements;
  * z_dtype as for lce_ce_logits), drawn by inversion from u [N], one given uniform

@@ -39,6 +39,17 @@ from ._binding import (  # noqa: F401
     workspace_size,
     workspace_size_opt,
 )
+from .answers import (  # noqa: F401
+    AnswerLossFunction,
+    linear_policy_loss,
+    linear_preference_loss,
+    policy_forward,
+    policy_fwd_bwd,
+    policy_logits,
+    preference_fwd_bwd,
+    preference_logits,
+    preference_workspace_size,
+)
 from .build_lib import LIB_PATH, build  # noqa: F401
 from .clipping import clip_grad_norm, grad_norm  # noqa: F401
 from .fp8 import (  # noqa: F401

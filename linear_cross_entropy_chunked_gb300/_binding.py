@@ -26,6 +26,7 @@ STATUS_NAMES = {
     5: "LCE_ERR_TIMEOUT",
     6: "LCE_ERR_CUDA",
     7: "LCE_ERR_UNSUPPORTED",
+    8: "LCE_ERR_OFFSETS",
 }
 
 # Every function the C ABI (include/lce.h) exports.
@@ -55,6 +56,14 @@ EXPORTED = (
     "lce_norm_fwd_bwd",
     "lce_norm_workspace_size_opt",
     "lce_norm_fwd_bwd_opt",
+    "lce_policy_forward",
+    "lce_policy_fwd_bwd",
+    "lce_policy_logits",
+    "lce_preference_workspace_size",
+    "lce_preference_fwd_bwd",
+    "lce_preference_logits_workspace_size",
+    "lce_preference_logits",
+    "lce_scale",
     "lce_sample_logits",
     "lce_fp8_quantize",
     "lce_fp8_matmul_workspace_size",
@@ -151,6 +160,21 @@ def lib() -> ctypes.CDLL:
     L.lce_norm_fwd_bwd_opt.argtypes = [_vp, _vp, _f, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64,
                                        ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp,
                                        ctypes.c_size_t, _vp]
+    _i = ctypes.c_int
+    pol = [_vp, _vp, _vp, _vp, _f, _f, _f, _f]   # advantages .. temperature
+    L.lce_policy_forward.argtypes = [_vp, _vp, _vp, *pol, _i64, _i64, _i64, _i64, _i64, _i, _vp, _vp, _vp,
+                                     ctypes.c_size_t, _vp]
+    L.lce_policy_fwd_bwd.argtypes = [_vp, _vp, _vp, *pol, _vp, _i64, _i64, _i64, _i64, _i64, _i, _i, _vp, _vp, _vp,
+                                     _vp, _vp, ctypes.c_size_t, _vp]
+    L.lce_policy_logits.argtypes = [_vp, _i, _i64, _vp, *pol, _vp, _i64, _i64, _i64, _i, _vp, _vp, _vp, _vp,
+                                    ctypes.c_size_t, _vp]
+    L.lce_preference_workspace_size.argtypes = [_i64, _i64, _i64, _i64, _i64, _i, _i, _sz]
+    L.lce_preference_fwd_bwd.argtypes = [_vp, _vp, _vp, _vp, _i64, _vp, _f, _f, _i, _vp, _i64, _i64, _i64, _i64, _i64,
+                                         _i, _i, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    L.lce_preference_logits_workspace_size.argtypes = [_i64, _i64, _sz]
+    L.lce_preference_logits.argtypes = [_vp, _i, _i64, _vp, _vp, _i64, _vp, _f, _f, _i, _vp, _i64, _i64, _i64, _i,
+                                        _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    L.lce_scale.argtypes = [_vp, _i, _vp, _i64, _vp, _i, _vp]
     L.lce_sample_logits.argtypes = [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _f,
                                     ctypes.c_int32, _f, _f, _vp, _vp, _vp]
     L.lce_fp8_quantize.argtypes = [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _vp, _i64, _vp,
@@ -190,7 +214,10 @@ def lib() -> ctypes.CDLL:
                  "lce_sample_logits", "lce_grad_norm_workspace_size", "lce_grad_norm",
                  "lce_clip_grad_norm", "lce_fp8_quantize", "lce_fp8_matmul_workspace_size",
                  "lce_fp8_matmul_best_workspace_size",
-                 "lce_fp8_matmul", "lce_fp8_linear_workspace_size", "lce_fp8_linear"):
+                 "lce_fp8_matmul", "lce_fp8_linear_workspace_size", "lce_fp8_linear",
+                 "lce_policy_forward", "lce_policy_fwd_bwd", "lce_policy_logits",
+                 "lce_preference_workspace_size", "lce_preference_fwd_bwd",
+                 "lce_preference_logits_workspace_size", "lce_preference_logits", "lce_scale"):
         getattr(L, name).restype = ctypes.c_int
     _LIB = L
     return L

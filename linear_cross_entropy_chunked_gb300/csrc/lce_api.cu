@@ -71,6 +71,7 @@ lce_status init_device(int *sms, int *pairs) {
         if (gemm_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
         if (aux_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
         if (ce_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
+        if (answers_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
         if (sample_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
         g_dev_fp8[dev] = fp8_set_attributes() == cudaSuccess;
         if (!g_dev_fp8[dev]) cudaGetLastError();
@@ -292,6 +293,12 @@ struct Ctx {
     MapType t16;         // the 16-bit map type of this call
     cudaStream_t s;
     CUtensorMap tmH_K, tmW_K, tmW_MN;
+    // losses on answers: the policy (pol.adv) and its temperature, or the rows' coefficients of a
+    // preference; what a row that adds nothing holds then reaches no gradient
+    PolicyParams pol{};
+    float inv_t = 1.f;
+    bool answers = false;
+    const float *coef = nullptr;
 };
 
 // Row of H (c.H) where the chunk starting at row0 begins.
@@ -442,6 +449,7 @@ void base_params(const Ctx &c, GemmParams &p, long long row0, long long rows, in
     p.dloss_per_row = c.reduction == LCE_REDUCTION_NONE ? 1 : 0;
     p.mean = c.reduction == LCE_REDUCTION_MEAN ? 1 : 0;
     p.f16 = c.f16 ? 1 : 0;
+    p.inv_t = c.inv_t;
 }
 
 // The logits launches of the chunk at row0 (MODE_LSE / _LSE_P / _G epilogue, P' or G
@@ -512,6 +520,14 @@ int dh_parts(const Ctx &c, long long rows, bool alone) {
     return sp < c.L.dh_splits ? sp : c.L.dh_splits;
 }
 
+// Which rows of the chunk at row0 the transpose leaves out.
+void set_row_filter(const Ctx &c, long long row0, TransposeParams &tp) {
+    tp.y = c.answers && !c.coef ? c.y + row0 : nullptr;
+    tp.V = c.V;
+    tp.ignore_index = c.ign;
+    tp.coef = c.coef ? c.coef + row0 : nullptr;
+}
+
 // H chunk^T into columns col0 .. col0 + rows - 1 of H^T (the K-major B operand of
 // the dW tiles; col0 = C for the second chunk of a pair).
 lce_status run_transpose(const Ctx &c, long long row0, long long rows, long long col0) {
@@ -523,6 +539,7 @@ lce_status run_transpose(const Ctx &c, long long row0, long long rows, long long
     tp.ld_t = c.L.ldt;
     tp.rows = static_cast<int>(rows);
     tp.cols = static_cast<int>(c.D);
+    set_row_filter(c, row0, tp);
     LCE_LAUNCH_KIND(LCE_KERNEL_MERGE, c.s, launch_transpose(tp, c.s));
     return LCE_OK;
 }
@@ -727,9 +744,8 @@ lce_status run_grad(const Ctx &c, long long row0, long long rows, int slot, void
     return LCE_OK;
 }
 
-lce_status run_merge(const Ctx &c, long long row0, long long rows, float *lse,
-                     const float *dloss, float *loss_rows) {
-    MergeParams m;
+void merge_params(const Ctx &c, long long row0, long long rows, float *lse, const float *dloss,
+                  float *loss_rows, MergeParams &m) {
     m.parts = c.parts;
     m.nparts = c.L.nparts;
     m.zy = c.zy;
@@ -747,6 +763,14 @@ lce_status run_merge(const Ctx &c, long long row0, long long rows, float *lse,
     m.f16 = c.f16 ? 1 : 0;
     m.lse = lse;
     m.loss_rows = loss_rows;
+    m.pol = c.pol;
+    m.zero_rows = c.answers ? 1 : 0;
+}
+
+lce_status run_merge(const Ctx &c, long long row0, long long rows, float *lse,
+                     const float *dloss, float *loss_rows) {
+    MergeParams m;
+    merge_params(c, row0, rows, lse, dloss, loss_rows, m);
     LCE_LAUNCH_KIND(LCE_KERNEL_MERGE, c.s, launch_merge(m, c.s));
     return LCE_OK;
 }
@@ -759,24 +783,8 @@ lce_status run_prep(const Ctx &c, long long row0, long long rows, float *lse,
                     long long ht_col0 = 0) {
     PrepParams pp;
     memset(&pp, 0, sizeof(pp));
-    MergeParams &m = pp.m;
-    m.parts = c.parts;
-    m.nparts = c.L.nparts;
-    m.zy = c.zy;
-    m.G = G;
-    m.ldg = c.L.ldg;
-    m.rows = static_cast<int>(rows);
-    m.row0 = static_cast<int>(row0);
-    m.V = static_cast<int>(c.V);
-    m.ignore_index = c.ign;
-    m.y = c.y;
-    m.hdr = c.hdr;
-    m.dloss = dloss;
-    m.dloss_per_row = c.reduction == LCE_REDUCTION_NONE ? 1 : 0;
-    m.mean = c.reduction == LCE_REDUCTION_MEAN ? 1 : 0;
-    m.f16 = c.f16 ? 1 : 0;
-    m.lse = lse;
-    m.loss_rows = loss_rows;
+    merge_params(c, row0, rows, lse, dloss, loss_rows, pp.m);
+    pp.m.G = G;
     pp.ldg = c.L.ldg;
     pp.segs = static_cast<int>(cdiv(cdiv(c.V, 8), PREP_VEC_PER_CTA));
     if (transpose) {
@@ -786,6 +794,7 @@ lce_status run_prep(const Ctx &c, long long row0, long long rows, float *lse,
         pp.tp.ld_t = c.L.ldt;
         pp.tp.rows = static_cast<int>(rows);
         pp.tp.cols = static_cast<int>(c.D);
+        set_row_filter(c, row0, pp.tp);
         pp.tt_x = static_cast<int>(cdiv(c.D, 64));
     }
     LCE_LAUNCH_KIND(LCE_KERNEL_MERGE, c.s, launch_prep(pp, c.s));
@@ -808,6 +817,66 @@ inline bool paired(const Ctx &c, bool h_chunked_ok = false) {
 // chunk k's dH tiles leave free (chunk k in buffer k % 2).
 inline bool frozen_overlapped(const Ctx &c) {
     return c.pairs > 0 && c.L.frozen_w && c.L.nbuf == 2 && !c.h_chunked;
+}
+
+// The gradients of chunks 0 .. n - 1 from a saved lse: each chunk's logits again, G straight
+// from their epilogue, then the contractions. acc_dw0: dW is added to from the first one on.
+lce_status backward_chunks(const Ctx &c, long long n, const float *lse, const float *dloss,
+                           __nv_bfloat16 *dHb, bool acc_dh, float *dW, bool acc_dw0) {
+    if (n <= 0) return LCE_OK;
+    if (frozen_overlapped(c)) {
+        LCE_TRY(run_logits(c, MODE_G, 0, chunk_rows(c, 0), 0, lse, dloss, c.Gb[0]));
+        for (long long k = 0; k < n; ++k) {
+            const long long r0 = k * c.L.C, n0 = chunk_rows(c, k);
+            GradSpec g{c.Gb[k & 1], c.Gb[k & 1], 0, true, true};
+            LogitsSpec next{};
+            if (k + 1 < n) {
+                next = LogitsSpec{MODE_G, r0 + c.L.C, chunk_rows(c, k + 1),
+                                  static_cast<int>(2 * k + 2), lse, dloss, c.Gb[(k + 1) & 1]};
+                g.beside = &next;
+            }
+            LCE_TRY(run_grad(c, r0, n0, static_cast<int>(2 * k + 1), dHb + r0 * c.D, acc_dh, dW,
+                             false, dloss, g));
+        }
+        return LCE_OK;
+    }
+    if (paired(c)) {
+        // chunks in pairs (a, b): a's G (G epilogue) into buffer 0, its H^T into
+        // columns 0..C-1; a's dH tiles, with b's logits (G into buffer 1) on the pairs
+        // they leave free; b's H^T into columns C.., then b's dH beside one dW
+        // contraction over both chunks (K = C + rows_b). An odd last chunk runs by itself.
+        for (long long a = 0; a < n; a += 2) {
+            const long long ra = a * c.L.C, na = chunk_rows(c, a);
+            const bool has_b = a + 1 < n;
+            const bool acc = a > 0 || acc_dw0;
+            LCE_TRY(run_logits(c, MODE_G, ra, na, static_cast<int>(2 * a), lse, dloss, c.Gb[0]));
+            LCE_TRY(run_transpose(c, ra, na, 0));
+            if (!has_b) {
+                LCE_TRY(run_grad(c, ra, na, static_cast<int>(2 * a + 1), dHb + ra * c.D, acc_dh, dW,
+                                 acc, dloss, GradSpec{c.Gb[0], c.Gb[0], na, true, false}));
+                break;
+            }
+            const long long b = a + 1, rb = b * c.L.C, nb = chunk_rows(c, b);
+            // a's dH tiles, with b's logits tiles on the pairs they leave free
+            const LogitsSpec lb{MODE_G, rb, nb, static_cast<int>(2 * b), lse, dloss, c.Gb[1]};
+            GradSpec ga{c.Gb[0], c.Gb[0], 0, true, true};
+            ga.beside = &lb;
+            LCE_TRY(run_grad(c, ra, na, static_cast<int>(2 * a + 1), dHb + ra * c.D, acc_dh, dW,
+                             acc, dloss, ga));
+            LCE_TRY(run_transpose(c, rb, nb, c.L.C));
+            LCE_TRY(run_grad(c, rb, nb, static_cast<int>(2 * b + 1), dHb + rb * c.D, acc_dh, dW,
+                             acc, dloss, GradSpec{c.Gb[1], c.Gb[0], c.L.C + nb, true, false}));
+        }
+        return LCE_OK;
+    }
+    for (long long k = 0; k < n; ++k) {
+        const long long row0 = k * c.L.C;
+        const long long rows = chunk_rows(c, k);
+        LCE_TRY(run_logits(c, MODE_G, row0, rows, static_cast<int>(2 * k), lse, dloss, c.Gb[0]));
+        LCE_TRY(run_grad(c, row0, rows, static_cast<int>(2 * k + 1), dHb + row0 * c.D, acc_dh, dW,
+                         k > 0 || acc_dw0, dloss, GradSpec{c.Gb[0], c.Gb[0], rows, false, false}));
+    }
+    return LCE_OK;
 }
 
 }  // namespace
@@ -915,11 +984,10 @@ lce_status lce_backward_opt(const void *H, const void *W, const int64_t *y, cons
     if ((!frozen && !dW) || (N > 0 && (!lse || !dH))) return LCE_ERR_INVALID_ARG;
     if ((dW && !aligned16(dW)) || (dH && !aligned16(dH)) || (lse && !aligned16(lse)))
         return LCE_ERR_ALIGNMENT;
-    const bool acc_dh = (flags & LCE_ACCUMULATE_DH) != 0;
     const bool low_mem = (flags & LCE_LOW_MEMORY) != 0;
     Layout L0;
     if (!make_layout(N, D, V, chunk, L0, frozen, low_mem)) return LCE_ERR_INVALID_ARG;
-    if (acc_dh && ws_bytes < L0.total + acc_dh_bytes(L0, D)) return LCE_ERR_WORKSPACE;
+    if ((flags & LCE_ACCUMULATE_DH) && ws_bytes < L0.total + acc_dh_bytes(L0, D)) return LCE_ERR_WORKSPACE;
     Ctx c;
     LCE_TRY(setup(c, H, W, y, N, D, V, ignore_index, chunk, ws, ws_bytes, stream, false, f16,
                   frozen, false, low_mem));
@@ -929,61 +997,8 @@ lce_status lce_backward_opt(const void *H, const void *W, const int64_t *y, cons
         if (cudaMemsetAsync(dW, 0, sizeof(float) * static_cast<size_t>(V) * D, c.s) != cudaSuccess)
             return LCE_ERR_CUDA;
     }
-    const bool acc_dw0 = (flags & LCE_ACCUMULATE_DW) != 0;
-    __nv_bfloat16 *dHb = static_cast<__nv_bfloat16 *>(dH);
-    if (frozen_overlapped(c)) {
-        LCE_TRY(run_logits(c, MODE_G, 0, chunk_rows(c, 0), 0, lse, dloss, c.Gb[0]));
-        for (long long k = 0; k < c.L.nchunks; ++k) {
-            const long long r0 = k * c.L.C, n0 = chunk_rows(c, k);
-            GradSpec g{c.Gb[k & 1], c.Gb[k & 1], 0, true, true};
-            LogitsSpec next{};
-            if (k + 1 < c.L.nchunks) {
-                next = LogitsSpec{MODE_G, r0 + c.L.C, chunk_rows(c, k + 1),
-                                  static_cast<int>(2 * k + 2), lse, dloss, c.Gb[(k + 1) & 1]};
-                g.beside = &next;
-            }
-            LCE_TRY(run_grad(c, r0, n0, static_cast<int>(2 * k + 1), dHb + r0 * c.D, acc_dh, dW,
-                             false, dloss, g));
-        }
-        return LCE_OK;
-    }
-    if (paired(c)) {
-        // chunks in pairs (a, b): a's G (G epilogue) into buffer 0, its H^T into
-        // columns 0..C-1; a's dH tiles, with b's logits (G into buffer 1) on the pairs
-        // they leave free; b's H^T into columns C.., then b's dH beside one dW
-        // contraction over both chunks (K = C + rows_b). An odd last chunk runs by itself.
-        for (long long a = 0; a < c.L.nchunks; a += 2) {
-            const long long ra = a * c.L.C, na = chunk_rows(c, a);
-            const bool has_b = a + 1 < c.L.nchunks;
-            const bool acc = a > 0 || acc_dw0;
-            LCE_TRY(run_logits(c, MODE_G, ra, na, static_cast<int>(2 * a), lse, dloss, c.Gb[0]));
-            LCE_TRY(run_transpose(c, ra, na, 0));
-            if (!has_b) {
-                LCE_TRY(run_grad(c, ra, na, static_cast<int>(2 * a + 1), dHb + ra * c.D, acc_dh, dW,
-                                 acc, dloss, GradSpec{c.Gb[0], c.Gb[0], na, true, false}));
-                break;
-            }
-            const long long b = a + 1, rb = b * c.L.C, nb = chunk_rows(c, b);
-            // a's dH tiles, with b's logits tiles on the pairs they leave free
-            const LogitsSpec lb{MODE_G, rb, nb, static_cast<int>(2 * b), lse, dloss, c.Gb[1]};
-            GradSpec ga{c.Gb[0], c.Gb[0], 0, true, true};
-            ga.beside = &lb;
-            LCE_TRY(run_grad(c, ra, na, static_cast<int>(2 * a + 1), dHb + ra * c.D, acc_dh, dW,
-                             acc, dloss, ga));
-            LCE_TRY(run_transpose(c, rb, nb, c.L.C));
-            LCE_TRY(run_grad(c, rb, nb, static_cast<int>(2 * b + 1), dHb + rb * c.D, acc_dh, dW,
-                             acc, dloss, GradSpec{c.Gb[1], c.Gb[0], c.L.C + nb, true, false}));
-        }
-        return LCE_OK;
-    }
-    for (long long k = 0; k < c.L.nchunks; ++k) {
-        const long long row0 = k * c.L.C;
-        const long long rows = chunk_rows(c, k);
-        LCE_TRY(run_logits(c, MODE_G, row0, rows, static_cast<int>(2 * k), lse, dloss, c.Gb[0]));
-        LCE_TRY(run_grad(c, row0, rows, static_cast<int>(2 * k + 1), dHb + row0 * c.D, acc_dh, dW,
-                         k > 0 || acc_dw0, dloss, GradSpec{c.Gb[0], c.Gb[0], rows, false, false}));
-    }
-    return LCE_OK;
+    return backward_chunks(c, c.L.nchunks, lse, dloss, static_cast<__nv_bfloat16 *>(dH),
+                           (flags & LCE_ACCUMULATE_DH) != 0, dW, (flags & LCE_ACCUMULATE_DW) != 0);
 }
 
 lce_status lce_backward_ex(const void *H, const void *W, const int64_t *y, const float *lse,
@@ -1007,12 +1022,13 @@ lce_status lce_backward(const void *H, const void *W, const int64_t *y, const fl
 namespace {
 
 // The fused call; n_valid_total (device int64, or null) replaces this call's own
-// count of valid rows as the normaliser of the mean.
+// count of valid rows as the normaliser of the mean; pol: the policy loss in place of the
+// cross-entropy (lse is then not written).
 lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const float *dloss,
                         int64_t N, int64_t D, int64_t V, int64_t ignore_index, int64_t chunk,
                         int reduction, int flags, float *loss, float *lse, void *dH, float *dW,
                         void *ws, size_t ws_bytes, lce_stream_t stream,
-                        const int64_t *n_valid_total) {
+                        const int64_t *n_valid_total, const PolicyParams *pol = nullptr) {
     g_launches = 0;
     if (reduction < LCE_REDUCTION_MEAN || reduction > LCE_REDUCTION_NONE) return LCE_ERR_INVALID_ARG;
     if (flags & ~LCE_FLAGS_ALL) return LCE_ERR_INVALID_ARG;
@@ -1021,7 +1037,7 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
     const bool none = reduction == LCE_REDUCTION_NONE;
     if (frozen && (flags & LCE_ACCUMULATE_DW)) return LCE_ERR_INVALID_ARG;
     if (f16 && none) return LCE_ERR_UNSUPPORTED;
-    if ((!none && !loss) || (!frozen && !dW) || (N > 0 && (!lse || !dH || !loss)))
+    if ((!none && !loss) || (!frozen && !dW) || (N > 0 && ((!lse && !pol) || !dH || !loss)))
         return LCE_ERR_INVALID_ARG;
     if ((loss && !aligned16(loss)) || (dW && !aligned16(dW)) || (dH && !aligned16(dH)) ||
         (lse && !aligned16(lse)))
@@ -1035,6 +1051,11 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
     LCE_TRY(setup(c, H, W, y, N, D, V, ignore_index, chunk, ws, ws_bytes, stream, false, f16,
                   frozen, false, low_mem));
     c.reduction = reduction;
+    if (pol) {
+        c.pol = *pol;
+        c.inv_t = pol->inv_t;
+        c.answers = true;
+    }
     if (n_valid_total) LCE_LAUNCH(launch_set_nvalid(reinterpret_cast<const long long *>(n_valid_total),
                                                     c.hdr, c.s));
     if (frozen) dW = nullptr;
@@ -1111,6 +1132,110 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
         LCE_LAUNCH(launch_loss_finalize(c.loss_rows, c.N, c.hdr, loss,
                                         reduction == LCE_REDUCTION_MEAN, c.s));
     return LCE_OK;
+}
+
+// Checks of the policy's vectors and numbers (advantages may be null with no rows).
+lce_status policy_check(int64_t N, const float *advantages, const float *old_logprobs, const float *ref_logprobs,
+                        const float *weights, float clip_low, float clip_high, float beta, float temperature,
+                        const float *logprobs) {
+    if (N > 0 && (!advantages || !logprobs)) return LCE_ERR_INVALID_ARG;
+    if (!(clip_low >= 0.f && clip_low <= 1.f) || !(clip_high >= 0.f && clip_high < INFINITY) ||
+        !(beta >= 0.f && beta < INFINITY) || !(temperature > 0.f && temperature < INFINITY) ||
+        !(1.f / temperature < INFINITY))
+        return LCE_ERR_INVALID_ARG;
+    if (N > 0 && beta != 0.f && !ref_logprobs) return LCE_ERR_INVALID_ARG;
+    const uintptr_t words = reinterpret_cast<uintptr_t>(advantages) | reinterpret_cast<uintptr_t>(old_logprobs) |
+                            reinterpret_cast<uintptr_t>(ref_logprobs) | reinterpret_cast<uintptr_t>(weights) |
+                            reinterpret_cast<uintptr_t>(logprobs);
+    return words % 4 ? LCE_ERR_ALIGNMENT : LCE_OK;
+}
+
+PolicyParams policy_params(const float *advantages, const float *old_logprobs, const float *ref_logprobs,
+                           const float *weights, float clip_low, float clip_high, float beta, float temperature,
+                           float *logprobs) {
+    PolicyParams p;
+    p.adv = advantages;
+    p.old_logp = old_logprobs;
+    p.ref_logp = beta != 0.f ? ref_logprobs : nullptr;
+    p.weight = weights;
+    p.lo = 1.f - clip_low;
+    p.hi = 1.f + clip_high;
+    p.beta = beta;
+    p.inv_t = 1.f / temperature;
+    p.logp = logprobs;
+    return p;
+}
+
+// Workspace of a preference over the head: the loss path's layout (the forward's share of it
+// without gradients), then lse and the coefficient of each row, the pairs' losses, and the slab
+// partials and target logits of a second chunk that is kept between the phases.
+struct PrefLayout {
+    Layout L;
+    size_t off_lse = 0, off_coef = 0, off_pair = 0, off_parts = 0, off_zy = 0, total = 0;
+};
+
+bool make_pref_layout(int64_t N, int64_t D, int64_t V, int64_t chunk, int64_t pairs, int flags, bool grad,
+                      PrefLayout &P) {
+    const bool frozen = (flags & LCE_FROZEN_W) != 0, low_mem = (flags & LCE_LOW_MEMORY) != 0;
+    if (!make_layout(N, D, V, chunk, P.L, frozen, low_mem) || pairs <= 0 || pairs > (1ll << 24)) return false;
+    const size_t rows = sizeof(float) * static_cast<size_t>(N > 0 ? N : 1);
+    size_t off = grad ? P.L.total + ((flags & LCE_ACCUMULATE_DH) ? acc_dh_bytes(P.L, D) : 0) : P.L.fwd_total;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += align_up(bytes, 1024);
+        return at;
+    };
+    P.off_lse = take(rows);
+    P.off_pair = take(sizeof(float) * static_cast<size_t>(pairs));
+    if (grad) {
+        P.off_coef = take(rows);
+        if (P.L.nbuf == 2) {
+            P.off_parts = take(sizeof(float2) * static_cast<size_t>(P.L.C) * P.L.nparts);
+            P.off_zy = take(sizeof(float) * static_cast<size_t>(P.L.C));
+        }
+    }
+    P.total = off;
+    return true;
+}
+
+lce_status preference_check(const int64_t *offsets, int64_t pairs, const float *ref_logprobs, float beta,
+                            float label_smoothing, int reduction, const float *dloss, const float *loss,
+                            const float *seq_logprobs) {
+    if (reduction < LCE_REDUCTION_MEAN || reduction > LCE_REDUCTION_NONE) return LCE_ERR_INVALID_ARG;
+    if (pairs <= 0 || !offsets || !loss || !seq_logprobs) return LCE_ERR_INVALID_ARG;
+    if (!(beta > -INFINITY && beta < INFINITY) || !(label_smoothing >= 0.f && label_smoothing <= 1.f))
+        return LCE_ERR_INVALID_ARG;
+    const uintptr_t words = reinterpret_cast<uintptr_t>(ref_logprobs) | reinterpret_cast<uintptr_t>(dloss) |
+                            reinterpret_cast<uintptr_t>(loss) | reinterpret_cast<uintptr_t>(seq_logprobs);
+    return words % 4 || reinterpret_cast<uintptr_t>(offsets) % 8 ? LCE_ERR_ALIGNMENT : LCE_OK;
+}
+
+PairParams pair_params(const int64_t *offsets, int64_t pairs, int64_t N, int64_t V, int64_t ign, const int64_t *y,
+                       const float *loss_rows, const float *ref, float beta, float smoothing, int average,
+                       const float *dloss, int reduction, float *loss, float *seq, float *pair_loss, float *coef,
+                       int *hdr) {
+    const bool none = reduction == LCE_REDUCTION_NONE;
+    PairParams p;
+    p.offsets = reinterpret_cast<const long long *>(offsets);
+    p.pairs = pairs;
+    p.N = N;
+    p.V = V;
+    p.ignore_index = ign;
+    p.y = reinterpret_cast<const long long *>(y);
+    p.loss_rows = loss_rows;
+    p.ref = ref;
+    p.beta = beta;
+    p.smoothing = smoothing;
+    p.average = average ? 1 : 0;
+    p.dloss = dloss;
+    p.dloss_per_pair = none ? 1 : 0;
+    p.mean = reduction == LCE_REDUCTION_MEAN ? 1 : 0;
+    p.seq_logp = seq;
+    p.pair_loss = none ? loss : pair_loss;
+    p.loss = none ? nullptr : loss;
+    p.coef = coef;
+    p.hdr = hdr;
+    return p;
 }
 
 // ---- 8-bit product
@@ -1393,6 +1518,144 @@ lce_status lce_fwd_bwd(const void *H, const void *W, const int64_t *y, const flo
                           lse, dH, dW, ws, ws_bytes, stream);
 }
 
+lce_status lce_policy_forward(const void *H, const void *W, const int64_t *y, const float *advantages,
+                              const float *old_logprobs, const float *ref_logprobs, const float *weights,
+                              float clip_low, float clip_high, float beta, float temperature, int64_t N,
+                              int64_t D, int64_t V, int64_t ignore_index, int64_t chunk, int reduction,
+                              float *loss, float *logprobs, void *ws, size_t ws_bytes, lce_stream_t stream) {
+    g_launches = 0;
+    if (reduction < LCE_REDUCTION_MEAN || reduction > LCE_REDUCTION_NONE) return LCE_ERR_INVALID_ARG;
+    const bool none = reduction == LCE_REDUCTION_NONE;
+    if (!loss && (N > 0 || !none)) return LCE_ERR_INVALID_ARG;
+    if (loss && !aligned16(loss)) return LCE_ERR_ALIGNMENT;
+    LCE_TRY(policy_check(N, advantages, old_logprobs, ref_logprobs, weights, clip_low, clip_high, beta,
+                         temperature, logprobs));
+    Ctx c;
+    LCE_TRY(setup(c, H, W, y, N, D, V, ignore_index, chunk, ws, ws_bytes, stream, false, false, false, true));
+    c.reduction = reduction;
+    c.pol = policy_params(advantages, old_logprobs, ref_logprobs, weights, clip_low, clip_high, beta,
+                          temperature, logprobs);
+    c.inv_t = c.pol.inv_t;
+    for (long long k = 0; k < c.L.nchunks; ++k) {
+        LCE_TRY(run_logits(c, MODE_LSE, k * c.L.C, chunk_rows(c, k), static_cast<int>(k), nullptr, nullptr,
+                           c.Gb[0]));
+        LCE_TRY(run_merge(c, k * c.L.C, chunk_rows(c, k), nullptr, nullptr, none ? loss : c.loss_rows));
+    }
+    if (!none)
+        LCE_LAUNCH(launch_loss_finalize(c.loss_rows, c.N, c.hdr, loss, reduction == LCE_REDUCTION_MEAN, c.s));
+    return LCE_OK;
+}
+
+lce_status lce_policy_fwd_bwd(const void *H, const void *W, const int64_t *y, const float *advantages,
+                              const float *old_logprobs, const float *ref_logprobs, const float *weights,
+                              float clip_low, float clip_high, float beta, float temperature,
+                              const float *dloss, int64_t N, int64_t D, int64_t V, int64_t ignore_index,
+                              int64_t chunk, int reduction, int flags, float *loss, float *logprobs, void *dH,
+                              float *dW, void *ws, size_t ws_bytes, lce_stream_t stream) {
+    g_launches = 0;
+    // (16-bit floats: a policy's coefficients have no range that fp16 gradients could be scaled by)
+    if (flags & LCE_INPUT_FP16) return LCE_ERR_UNSUPPORTED;
+    LCE_TRY(policy_check(N, advantages, old_logprobs, ref_logprobs, weights, clip_low, clip_high, beta,
+                         temperature, logprobs));
+    const PolicyParams pol = policy_params(advantages, old_logprobs, ref_logprobs, weights, clip_low, clip_high,
+                                           beta, temperature, logprobs);
+    return fwd_bwd_impl(H, W, y, dloss, N, D, V, ignore_index, chunk, reduction, flags, loss, nullptr, dH, dW, ws,
+                        ws_bytes, stream, nullptr, &pol);
+}
+
+lce_status lce_preference_workspace_size(int64_t N, int64_t D, int64_t V, int64_t chunk, int64_t pairs, int flags,
+                                         int gradient, size_t *bytes) {
+    PrefLayout P;
+    if (!bytes || (flags & ~LCE_FLAGS_ALL) ||
+        !make_pref_layout(N, D, V, chunk, pairs, flags, gradient != 0, P))
+        return LCE_ERR_INVALID_ARG;
+    *bytes = P.total;
+    return LCE_OK;
+}
+
+// Phases: every chunk's logits and the rows' log probabilities; the pairs; the gradients. What the
+// last chunks (as many as there are chunk buffers) have in their buffers stays there over the
+// pairs, so that their logits are not computed again: with no more rows than the buffers hold, none are.
+lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y, const int64_t *offsets,
+                                  int64_t pairs, const float *ref_logprobs, float beta, float label_smoothing,
+                                  int average, const float *dloss, int64_t N, int64_t D, int64_t V,
+                                  int64_t ignore_index, int64_t chunk, int reduction, int flags, float *loss,
+                                  float *seq_logprobs, void *dH, float *dW, void *ws, size_t ws_bytes,
+                                  lce_stream_t stream) {
+    g_launches = 0;
+    if (flags & ~LCE_FLAGS_ALL) return LCE_ERR_INVALID_ARG;
+    if (flags & LCE_INPUT_FP16) return LCE_ERR_UNSUPPORTED;
+    const bool grad = dH != nullptr || dW != nullptr;
+    const bool frozen = (flags & LCE_FROZEN_W) != 0 || !grad;
+    const bool acc_dh = (flags & LCE_ACCUMULATE_DH) != 0, acc_dw0 = (flags & LCE_ACCUMULATE_DW) != 0;
+    const bool low_mem = (flags & LCE_LOW_MEMORY) != 0;
+    if ((flags & LCE_FROZEN_W) && acc_dw0) return LCE_ERR_INVALID_ARG;
+    LCE_TRY(preference_check(offsets, pairs, ref_logprobs, beta, label_smoothing, reduction, dloss, loss,
+                             seq_logprobs));
+    if (grad && ((N > 0 && !dH) || (!frozen && !dW))) return LCE_ERR_INVALID_ARG;
+    if ((dH && !aligned16(dH)) || (dW && !aligned16(dW))) return LCE_ERR_ALIGNMENT;
+    PrefLayout P;
+    if (!make_pref_layout(N, D, V, chunk, pairs, flags, grad, P)) return LCE_ERR_INVALID_ARG;
+    if (!ws) return LCE_ERR_INVALID_ARG;
+    if (ws_bytes < P.total) return LCE_ERR_WORKSPACE;
+    Ctx c;
+    LCE_TRY(setup(c, H, W, y, N, D, V, ignore_index, chunk, ws, ws_bytes, stream, false, false,
+                  (flags & LCE_FROZEN_W) != 0, !grad, low_mem));
+    c.reduction = LCE_REDUCTION_NONE;   // (of the rows: each has a coefficient of its own)
+    c.answers = true;
+    float *lse = reinterpret_cast<float *>(c.ws + P.off_lse);
+    float *coef = grad ? reinterpret_cast<float *>(c.ws + P.off_coef) : nullptr;
+    if (frozen) dW = nullptr;
+    const long long n = c.L.nchunks;
+    if (n == 0 && dW && !acc_dw0 &&
+        cudaMemsetAsync(dW, 0, sizeof(float) * static_cast<size_t>(V) * D, c.s) != cudaSuccess)
+        return LCE_ERR_CUDA;
+    // the chunks from `keep` on stay in the buffers: the last pair (or the odd last one), or the last
+    const bool two = grad && (paired(c) || frozen_overlapped(c));
+    const long long keep = !grad || n == 0 ? n : two ? (n - 1) / 2 * 2 : n - 1;
+    struct Kept {
+        float2 *parts;
+        float *zy;
+    };
+    const Kept kept[2] = {{c.parts, c.zy},
+                          {reinterpret_cast<float2 *>(c.ws + P.off_parts), reinterpret_cast<float *>(c.ws + P.off_zy)}};
+    auto use = [&](long long j) {
+        c.parts = kept[j].parts;
+        c.zy = kept[j].zy;
+    };
+    for (long long k = 0; k < n; ++k) {
+        const long long j = k < keep ? 0 : k - keep;
+        use(j);
+        LCE_TRY(run_logits(c, k < keep ? MODE_LSE : MODE_LSE_P, k * c.L.C, chunk_rows(c, k), static_cast<int>(k),
+                           nullptr, nullptr, c.Gb[j]));
+        LCE_TRY(run_merge(c, k * c.L.C, chunk_rows(c, k), lse, nullptr, c.loss_rows));
+    }
+    LCE_LAUNCH(launch_pairs(pair_params(offsets, pairs, N, V, ignore_index, y, c.loss_rows, ref_logprobs, beta,
+                                        label_smoothing, average, dloss, reduction, loss, seq_logprobs,
+                                        reinterpret_cast<float *>(c.ws + P.off_pair), coef, c.hdr), c.s));
+    if (!grad || n == 0) return LCE_OK;
+    // the tile counters start again
+    if (cudaMemsetAsync(c.hdr + HDR_COUNTERS, 0, c.L.hdr_bytes - sizeof(int) * HDR_COUNTERS, c.s) != cudaSuccess)
+        return LCE_ERR_CUDA;
+    c.coef = coef;
+    __nv_bfloat16 *dHb = static_cast<__nv_bfloat16 *>(dH);
+    for (long long k = keep; k < n; ++k) {
+        use(k - keep);
+        LCE_TRY(run_prep(c, k * c.L.C, chunk_rows(c, k), nullptr, coef, c.loss_rows, c.Gb[k - keep], !frozen,
+                         (k - keep) * c.L.C));
+    }
+    for (long long k = keep; k < n; ++k) {
+        const long long j = k - keep, row0 = k * c.L.C, rows = chunk_rows(c, k);
+        // (W trained, two chunks: the first one's dH alone, the second's beside one dW over both)
+        const bool alone = frozen || k + 1 < n;
+        const GradSpec g{c.Gb[j], c.Gb[0], alone ? 0 : j * c.L.C + rows, true, alone && (two || !frozen)};
+        LCE_TRY(run_grad(c, row0, rows, static_cast<int>(2 * k + 1), dHb + row0 * c.D, acc_dh, dW, acc_dw0, coef,
+                         g));
+    }
+    use(0);
+    return backward_chunks(c, keep, lse, coef, dHb, acc_dh, dW, true);
+}
+
 lce_status lce_rmsnorm_forward(const void *X, const void *gamma, int64_t N, int64_t D, float eps,
                                void *H, float *rstd, lce_stream_t stream) {
     g_launches = 0;
@@ -1670,6 +1933,133 @@ lce_status lce_ce_logits(const void *Z, int z_dtype, int64_t ld, const int64_t *
     return LCE_OK;
 }
 
+namespace {
+
+// Checks that both losses over logits share; the element size.
+lce_status answer_logits_check(const void *Z, int z_dtype, int64_t ld, const int64_t *y, int64_t N, int64_t V,
+                               const float *dloss, const float *loss, const void *dZ, const void *ws) {
+    if (N < 0 || N > 0x7fffffffll || V <= 0 || V > MAX_V || ld < V || !ws) return LCE_ERR_INVALID_ARG;
+    if (z_dtype < CE_BF16 || z_dtype > CE_FP16 || (N > 0 && (!Z || !y))) return LCE_ERR_INVALID_ARG;
+    const uintptr_t z = reinterpret_cast<uintptr_t>(Z), d = reinterpret_cast<uintptr_t>(dZ);
+    if (z % (z_dtype == CE_FP32 ? 4 : 2) || reinterpret_cast<uintptr_t>(y) % 8 || !aligned16(ws) ||
+        (reinterpret_cast<uintptr_t>(dloss) | reinterpret_cast<uintptr_t>(loss)) % 4)
+        return LCE_ERR_ALIGNMENT;
+    if (dZ && z % 16 != d % 16) return LCE_ERR_ALIGNMENT;
+    return LCE_OK;
+}
+
+AnswerParams answer_params(const void *Z, int z_dtype, int64_t ld, const int64_t *y, int64_t N, int64_t V,
+                           int64_t ign, int *hdr) {
+    AnswerParams p;
+    memset(&p, 0, sizeof(p));
+    p.Z = Z;
+    p.ld = ld;
+    p.dtype = z_dtype;
+    p.N = N;
+    p.V = V;
+    p.ignore_index = ign;
+    p.y = reinterpret_cast<const long long *>(y);
+    p.hdr = hdr;
+    p.pol.inv_t = 1.f;
+    return p;
+}
+
+}  // namespace
+
+lce_status lce_policy_logits(const void *Z, int z_dtype, int64_t ld, const int64_t *y, const float *advantages,
+                             const float *old_logprobs, const float *ref_logprobs, const float *weights,
+                             float clip_low, float clip_high, float beta, float temperature, const float *dloss,
+                             int64_t N, int64_t V, int64_t ignore_index, int reduction, float *loss,
+                             float *logprobs, void *dZ, void *ws, size_t ws_bytes, lce_stream_t stream) {
+    g_launches = 0;
+    if (reduction < LCE_REDUCTION_MEAN || reduction > LCE_REDUCTION_NONE) return LCE_ERR_INVALID_ARG;
+    const bool none = reduction == LCE_REDUCTION_NONE;
+    if (!loss && (N > 0 || !none)) return LCE_ERR_INVALID_ARG;
+    LCE_TRY(policy_check(N, advantages, old_logprobs, ref_logprobs, weights, clip_low, clip_high, beta,
+                         temperature, logprobs));
+    LCE_TRY(answer_logits_check(Z, z_dtype, ld, y, N, V, dloss, loss, dZ, ws));
+    size_t need = 0;
+    lce_ce_logits_workspace_size(N, &need);
+    if (ws_bytes < need) return LCE_ERR_WORKSPACE;
+    int sms = 0, pairs = 0;
+    LCE_TRY(init_device(&sms, &pairs));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    AnswerParams p = answer_params(Z, z_dtype, ld, y, N, V, ignore_index, reinterpret_cast<int *>(w));
+    p.dZ = dZ;
+    p.dloss = dloss;
+    p.dloss_per_row = none ? 1 : 0;
+    p.mean = reduction == LCE_REDUCTION_MEAN ? 1 : 0;
+    p.pol = policy_params(advantages, old_logprobs, ref_logprobs, weights, clip_low, clip_high, beta, temperature,
+                          logprobs);
+    p.loss_rows = none ? loss : reinterpret_cast<float *>(w + 1024);
+    p.loss = none ? nullptr : loss;
+    LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_answer_scan(p.y, N, V, ignore_index, p.hdr, s));
+    if (N > 0) LCE_LAUNCH_KIND(LCE_KERNEL_MERGE, s, launch_answer_rows(p, sms, s));
+    else if (loss && cudaMemsetAsync(loss, 0, sizeof(float), s) != cudaSuccess) return LCE_ERR_CUDA;
+    return LCE_OK;
+}
+
+lce_status lce_preference_logits_workspace_size(int64_t N, int64_t pairs, size_t *bytes) {
+    if (!bytes || N < 0 || N > 0x7fffffffll || pairs <= 0 || pairs > (1ll << 24)) return LCE_ERR_INVALID_ARG;
+    const size_t rows = align_up(sizeof(float) * static_cast<size_t>(N > 0 ? N : 1), 1024);
+    *bytes = 1024 + 4 * rows + align_up(sizeof(float) * static_cast<size_t>(pairs), 1024);
+    return LCE_OK;
+}
+
+lce_status lce_preference_logits(const void *Z, int z_dtype, int64_t ld, const int64_t *y, const int64_t *offsets,
+                                 int64_t pairs_, const float *ref_logprobs, float beta, float label_smoothing,
+                                 int average, const float *dloss, int64_t N, int64_t V, int64_t ignore_index,
+                                 int reduction, float *loss, float *seq_logprobs, void *dZ, void *ws,
+                                 size_t ws_bytes, lce_stream_t stream) {
+    g_launches = 0;
+    LCE_TRY(preference_check(offsets, pairs_, ref_logprobs, beta, label_smoothing, reduction, dloss, loss,
+                             seq_logprobs));
+    LCE_TRY(answer_logits_check(Z, z_dtype, ld, y, N, V, dloss, loss, dZ, ws));
+    size_t need = 0;
+    LCE_TRY(lce_preference_logits_workspace_size(N, pairs_, &need));
+    if (ws_bytes < need) return LCE_ERR_WORKSPACE;
+    int sms = 0, pairs = 0;
+    LCE_TRY(init_device(&sms, &pairs));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    const size_t rows = align_up(sizeof(float) * static_cast<size_t>(N > 0 ? N : 1), 1024);
+    AnswerParams p = answer_params(Z, z_dtype, ld, y, N, V, ignore_index, reinterpret_cast<int *>(w));
+    p.loss_rows = reinterpret_cast<float *>(w + 1024);
+    float *coef = reinterpret_cast<float *>(w + 1024 + rows);
+    p.max_sum = reinterpret_cast<float2 *>(w + 1024 + 2 * rows);
+    float *pair_loss = reinterpret_cast<float *>(w + 1024 + 4 * rows);
+    LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_answer_scan(p.y, N, V, ignore_index, p.hdr, s));
+    if (N > 0) LCE_LAUNCH_KIND(LCE_KERNEL_MERGE, s, launch_answer_rows(p, sms, s));
+    LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s,
+                    launch_pairs(pair_params(offsets, pairs_, N, V, ignore_index, y, p.loss_rows, ref_logprobs, beta,
+                                             label_smoothing, average, dloss, reduction, loss, seq_logprobs,
+                                             pair_loss, dZ ? coef : nullptr, p.hdr), s));
+    if (dZ && N > 0) {
+        p.dZ = dZ;
+        p.coef = coef;
+        LCE_LAUNCH_KIND(LCE_KERNEL_MERGE, s, launch_answer_grad(p, sms, s));
+    }
+    return LCE_OK;
+}
+
+lce_status lce_scale(const void *src, int src_dtype, const float *scale, int64_t n, void *dst, int dst_dtype,
+                     lce_stream_t stream) {
+    g_launches = 0;
+    if (n < 0 || src_dtype < CE_BF16 || src_dtype > CE_FP16 || dst_dtype < CE_BF16 || dst_dtype > CE_FP16 ||
+        !scale || (n > 0 && (!src || !dst)))
+        return LCE_ERR_INVALID_ARG;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(src), b = reinterpret_cast<uintptr_t>(dst);
+    const uintptr_t ea = src_dtype == CE_FP32 ? 4 : 2, eb = dst_dtype == CE_FP32 ? 4 : 2;
+    if (a % ea || b % eb || reinterpret_cast<uintptr_t>(scale) % 4) return LCE_ERR_ALIGNMENT;
+    if (n > 0 && !(a == b && src_dtype == dst_dtype) && a < b + eb * n && b < a + ea * n) return LCE_ERR_INVALID_ARG;
+    int sms = 0, pairs = 0;
+    LCE_TRY(init_device(&sms, &pairs));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (n > 0) LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_scale(src, src_dtype, scale, n, dst, dst_dtype, sms, s));
+    return LCE_OK;
+}
+
 lce_status lce_sample_logits(const void *Z, int z_dtype, int64_t ld, int64_t N, int64_t V,
                              const float *u, const float *temperature, const int32_t *top_k,
                              const float *top_p, const float *min_p, float temperature_all,
@@ -1863,6 +2253,7 @@ lce_status lce_read_status(const void *ws, lce_stream_t stream) {
             return LCE_ERR_CUDA;
     }
     if (flag & FLAG_TIMEOUT) return LCE_ERR_TIMEOUT;
+    if (flag & FLAG_OFFSETS) return LCE_ERR_OFFSETS;
     if (flag & FLAG_LABEL) return LCE_ERR_LABEL_RANGE;
     return LCE_OK;
 }
@@ -1877,6 +2268,7 @@ const char *lce_status_string(lce_status s) {
         case LCE_ERR_TIMEOUT: return "device pipeline wait timed out";
         case LCE_ERR_CUDA: return "CUDA runtime error";
         case LCE_ERR_UNSUPPORTED: return "device is not sm_103";
+        case LCE_ERR_OFFSETS: return "offsets of sequences decrease or leave the rows";
     }
     return "unknown status";
 }

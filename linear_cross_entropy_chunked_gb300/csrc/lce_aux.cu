@@ -163,8 +163,10 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_merge_kernel(const MergePar
     const long long yv = p.y[grow];
     const bool y_ok = yv != p.ignore_index && yv >= 0 && yv < p.V;
     if (t == 0) {
-        p.lse[grow] = lse;
-        p.loss_rows[grow] = y_ok ? lse - p.zy[r] : 0.f;
+        if (p.lse) p.lse[grow] = lse;
+        const float logp = y_ok ? p.zy[r] - lse : 0.f;
+        if (p.pol.logp) p.pol.logp[grow] = logp;
+        p.loss_rows[grow] = !y_ok ? 0.f : p.pol.adv ? lce_policy_row(p.pol, grow, logp).loss : lse - p.zy[r];
     }
 }
 
@@ -173,6 +175,14 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_merge_kernel(const MergePar
 // operand of the dW contraction).
 
 constexpr int TT = 64;
+// Whether row r of the chunk is transposed as it is (else as zeros).
+__device__ __forceinline__ bool row_counts(const TransposeParams &p, int r) {
+    if (p.coef && p.coef[r] == 0.f) return false;
+    if (!p.y) return true;
+    const long long v = p.y[r];
+    return v != p.ignore_index && v >= 0 && v < p.V;
+}
+
 constexpr int TSTRIDE = 66;   // bf16 elements per staged row: conflict-free row writes, 2-way column reads
 
 __global__ void __launch_bounds__(256) lce_transpose_kernel(const TransposeParams p) {
@@ -186,7 +196,7 @@ __global__ void __launch_bounds__(256) lce_transpose_kernel(const TransposeParam
         const int rr = k >> 3, cb = (k & 7) * 8;
         const int r = r0 + rr, c = c0 + cb;
         uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (r < p.rows && c < p.cols)
+        if (r < p.rows && c < p.cols && row_counts(p, r))
             u = *reinterpret_cast<const uint4 *>(p.src + static_cast<size_t>(r) * p.ld_src + c);
         uint32_t *dst = reinterpret_cast<uint32_t *>(tile + rr * TSTRIDE + cb);
         dst[0] = u.x;
@@ -246,7 +256,7 @@ __device__ __forceinline__ void transpose_tile(const TransposeParams &p, int c0,
         const int rr = k >> 3, cb = (k & 7) * 8;
         const int r = r0 + rr, c = c0 + cb;
         uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (r < p.rows && c < p.cols)
+        if (r < p.rows && c < p.cols && row_counts(p, r))
             u = *reinterpret_cast<const uint4 *>(p.src + static_cast<size_t>(r) * p.ld_src + c);
         uint32_t *dst = reinterpret_cast<uint32_t *>(tile + rr * TSTRIDE + cb);
         dst[0] = u.x;
@@ -316,12 +326,21 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_prep_kernel(const PrepParam
     const int grow = m.row0 + r;
     const long long yv = m.y[grow];
     const bool y_ok = yv != m.ignore_index && yv >= 0 && yv < m.V;
-    if (seg == 0 && threadIdx.x == 0) {
-        m.lse[grow] = lse;
-        m.loss_rows[grow] = y_ok ? lse - m.zy[r] : 0.f;
+    float scale = lce_store_scale(m.dloss, m.dloss_per_row, m.mean, m.hdr[HDR_NVALID], grow, y_ok,
+                                  m.f16);
+    const float logp = y_ok ? m.zy[r] - lse : 0.f;
+    float row_loss = y_ok ? lse - m.zy[r] : 0.f;
+    if (m.pol.adv && y_ok) {
+        const PolicyRow pr = lce_policy_row(m.pol, grow, logp);
+        row_loss = pr.loss;
+        scale *= -pr.slope * m.pol.inv_t;
     }
-    const float scale = lce_store_scale(m.dloss, m.dloss_per_row, m.mean, m.hdr[HDR_NVALID], grow,
-                                        y_ok, m.f16);
+    if (seg == 0 && threadIdx.x == 0) {
+        if (m.lse) m.lse[grow] = lse;
+        if (m.pol.logp) m.pol.logp[grow] = logp;
+        m.loss_rows[grow] = row_loss;
+    }
+    const bool zero = m.zero_rows && scale == 0.f;
     const float lse2 = lse * LOG2E_F;
     const int ycol = y_ok ? static_cast<int>(yv) : -1;
     // the factor exp(m_p - lse) * s of each 128-column slab of the segment, once (a
@@ -364,6 +383,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_prep_kernel(const PrepParam
                 wv[q] = *reinterpret_cast<uint32_t *>(&h);
             }
         }
+        if (zero) u = make_uint4(0u, 0u, 0u, 0u);
         row[v0 + v] = u;
     }
 }

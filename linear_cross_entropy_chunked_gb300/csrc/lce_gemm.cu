@@ -236,6 +236,7 @@ __device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Tile 
     if (row_ok) yv = p.y[p.row0 + r];
     const bool y_ok = row_ok && yv != p.ignore_index && yv >= 0 && yv < p.V;
     const int yl = y_ok ? static_cast<int>(yv - col0) : -1;   // local target column
+    const float k2 = LOG2E * p.inv_t;           // logits to exponents of 2
 
     if constexpr (MODE == MODE_G) {
         if (ncols <= 0 || !box_rows) return;
@@ -245,6 +246,8 @@ __device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Tile 
                                     p.row0 + r, y_ok, p.f16);
             lse2 = p.lse[p.row0 + r] * LOG2E;
         }
+        // a row that adds nothing is zeros, whatever its logits are
+        const int rcols = scale != 0.f ? ncols : 0;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
             const bool box_ok = (c >> 1) * 64 < ncols;
@@ -254,7 +257,7 @@ __device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Tile 
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
                 const int cj = c * 32 + j;
-                float g = (cj < ncols) ? ex2(fmaf(v[j], LOG2E, -lse2)) * scale : 0.f;
+                float g = (cj < rcols) ? ex2(fmaf(v[j], k2, -lse2)) * scale : 0.f;
                 if (cj == yl) g -= scale;
                 v[j] = g;
             }
@@ -277,7 +280,7 @@ __device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Tile 
             }
         }
         // pass 2: sum of exp(z - m); optionally store P' = exp(z - m) as bf16
-        const float m2 = (ncols > 0) ? m * LOG2E : 0.f;
+        const float m2 = (ncols > 0) ? m * k2 : 0.f;
         float s = 0.f;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -286,7 +289,7 @@ __device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Tile 
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
                 const int cj = c * 32 + j;
-                v[j] = (cj < ncols) ? ex2(fmaf(v[j], LOG2E, -m2)) : 0.f;
+                v[j] = (cj < ncols) ? ex2(fmaf(v[j], k2, -m2)) : 0.f;
                 s += v[j];
             }
             if constexpr (MODE == MODE_LSE_P) {
@@ -298,8 +301,8 @@ __device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Tile 
             }
         }
         if (row_ok && ncols > 0) {
-            p.parts[static_cast<size_t>(r) * p.nparts + col0 / PART_COLS] = make_float2(m, s);
-            if (yl >= 0 && yl < 128) p.zy[r] = zt;
+            p.parts[static_cast<size_t>(r) * p.nparts + col0 / PART_COLS] = make_float2(m * p.inv_t, s);
+            if (yl >= 0 && yl < 128) p.zy[r] = zt * p.inv_t;
         }
     }
 }

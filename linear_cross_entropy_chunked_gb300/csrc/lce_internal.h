@@ -100,14 +100,61 @@ __device__ __forceinline__ float lce_out_scale(const float *dloss, int mean, int
     return d / F16_G_SCALE;
 }
 
+// The clipped policy loss (lce_policy_*): what the log probability of a row's label is
+// worth, in place of the cross-entropy. Null pointers: no such term.
+struct PolicyParams {
+    const float *adv;          // [N] advantages; null: the row loss is the cross-entropy
+    const float *old_logp;     // [N] or null (the ratio is 1)
+    const float *ref_logp;     // [N] or null (no KL term)
+    const float *weight;       // [N] or null (1)
+    float lo, hi;              // the ratio is held between them: 1 - clip_low, 1 + clip_high
+    float beta;                // of the KL term (0: ref_logp is not read)
+    float inv_t;               // 1 / temperature of the softmax
+    float *logp;               // [N] output: log probability of the label, 0 where the row does not count
+};
+
+// Loss of a counting row and its derivative by the label's log probability, both times the
+// row's weight:
+//   r = exp(logp - old), f = r A, h = clamp(r, lo, hi) A
+//   loss  = -min(f, h) + beta (e^d - 1 - d),  d = ref - logp
+//   slope = -(f <= h ? f : 0) - beta (e^d - 1)
+// The ratio is compared, not passed through min and max, so that a NaN stays one; an advantage
+// of 0 gives 0 even where the ratio overflows.
+struct PolicyRow {
+    float loss, slope;
+};
+__device__ __forceinline__ PolicyRow lce_policy_row(const PolicyParams &p, long long i, float logp) {
+    const float a = p.adv[i];
+    const float r = p.old_logp ? expf(logp - p.old_logp[i]) : (logp == logp ? 1.f : logp);
+    const float f = r * a;
+    const float h = (r < p.lo ? p.lo : r > p.hi ? p.hi : r) * a;
+    PolicyRow o;
+    o.loss = f <= h ? -f : -h;
+    o.slope = f <= h ? -f : h * 0.f;
+    if (p.ref_logp && p.beta != 0.f) {
+        const float d = p.ref_logp[i] - logp;
+        const float e = expm1f(d);
+        o.loss += p.beta * (d == INFINITY ? d : e - d);
+        o.slope -= p.beta * e;
+    }
+    if (p.weight) {
+        const float w = p.weight[i];
+        o.loss *= w;
+        o.slope *= w;
+    }
+    return o;
+}
+
 // Workspace header (int32 words).
 enum : int {
     HDR_FLAG = 0,       // bit 0: label out of range, bit 1: pipeline wait timed out
     HDR_NVALID = 1,
+    HDR_DONE = 2,       // parts of a launch that have finished (the last one adds up the loss)
     HDR_COUNTERS = 16,  // one dynamic tile counter per GEMM launch of a call
 };
 constexpr int FLAG_LABEL = 1;
 constexpr int FLAG_TIMEOUT = 2;
+constexpr int FLAG_OFFSETS = 4;   // offsets of sequences that decrease or leave the rows
 
 struct GemmParams {
     CUtensorMap tmA0;      // logits A = H (K-major) | dH A = G (K-major)
@@ -148,6 +195,7 @@ struct GemmParams {
     // offset s * split_rows of the tmS0 map (k_splits <= 1: one part, no offset)
     int k_splits, kb_per_split, split_rows;
     int f16;               // 1: fp16 operands (H, W, G) and fp16 P' / G / dH stores
+    float inv_t;           // the logits are multiplied by it in the logits epilogues (1 / temperature)
     unsigned long long timeout_ns;
 };
 
@@ -165,8 +213,10 @@ struct MergeParams {
     int dloss_per_row;
     int mean;
     int f16;               // fp16 inputs: slab factors use lce_store_scale
-    float *lse;            // global [N]
+    float *lse;            // global [N]; null: not written
     float *loss_rows;      // global [N] (the caller's loss vector for reduction none)
+    PolicyParams pol;      // pol.adv: the policy loss in place of the cross-entropy
+    int zero_rows;         // 1: rows of G whose scale is 0 become zeros whatever P' holds
 };
 
 struct TransposeParams {
@@ -175,6 +225,11 @@ struct TransposeParams {
     __nv_bfloat16 *dst_t;       // [cols][ld_t]
     int ld_t;
     int rows, cols;
+    // rows that add nothing become zeros whatever they hold: those whose label does not count
+    // (y, of the chunk's rows, or null), those whose coefficient is 0 (coef, or null)
+    const long long *y;
+    long long V, ignore_index;
+    const float *coef;
 };
 
 
@@ -212,6 +267,44 @@ struct CELogitsParams {
     int mean;
     float *lse;            // [N]
     float *loss_rows;      // [N]
+};
+
+// Losses on answers over logits Z [N][ld] (lce_answers.cu).
+struct AnswerParams {
+    const void *Z;
+    void *dZ;              // null: no gradient; may equal Z. Rows lie as Z's do (ld, and the address mod 16)
+    long long ld;
+    int dtype;             // CE_BF16, CE_FP32 or CE_FP16
+    long long N, V;
+    long long ignore_index;
+    const long long *y;
+    int *hdr;
+    const float *dloss;
+    int dloss_per_row, mean;
+    PolicyParams pol;      // adv null: the row loss is -log p of the label, and there is no gradient
+    float2 *max_sum;       // [N] or null: the row's largest logit and the sum of exp(z - it)
+    float *loss_rows;      // [N]
+    float *loss;           // the sum of the row losses (over N_valid where `mean`), or null
+    // the gradient of a preference: row i of dZ is (p - onehot) coef[i]
+    const float *coef;
+};
+// Pairs of sequences: the rows of sequence s are offsets[s] .. offsets[s + 1] - 1, the chosen
+// one of pair k is sequence k, the rejected one sequence pairs + k.
+struct PairParams {
+    const long long *offsets;   // [2 pairs + 1]
+    long long pairs, N, V, ignore_index;
+    const long long *y;
+    const float *loss_rows;     // [N]: -log p of each counting row
+    const float *ref;           // [2 pairs] or null (0)
+    float beta, smoothing;
+    int average;                // log probabilities per counting row
+    const float *dloss;         // null, one number, or one per pair
+    int dloss_per_pair, mean;
+    float *seq_logp;            // [2 pairs]
+    float *pair_loss;           // [pairs]
+    float *loss;                // or null
+    float *coef;                // [N] or null
+    int *hdr;
 };
 
 // final RMSNorm (forward and backward row kernels)
@@ -345,6 +438,17 @@ cudaError_t launch_transpose(const TransposeParams &p, cudaStream_t s);
 cudaError_t launch_prep(const PrepParams &p, cudaStream_t s);
 cudaError_t launch_loss_finalize(const float *loss_rows, long long N, const int *hdr,
                                  float *loss, int mean, cudaStream_t s);
+// Answers over logits: the scan of the labels (which clears the header), the rows' losses (and
+// the policy's gradient), the pairs, and the preference's gradient.
+cudaError_t launch_answer_scan(const long long *y, long long N, long long V, long long ign, int *hdr,
+                               cudaStream_t s);
+cudaError_t launch_answer_rows(const AnswerParams &p, int sms, cudaStream_t s);
+cudaError_t launch_answer_grad(const AnswerParams &p, int sms, cudaStream_t s);
+cudaError_t launch_pairs(const PairParams &p, cudaStream_t s);
+// dst[i] = src[i] * *scale
+cudaError_t launch_scale(const void *src, int src_dtype, const float *scale, long long n, void *dst, int dst_dtype,
+                         int sms, cudaStream_t s);
+cudaError_t answers_set_attributes();
 cudaError_t launch_ce_logits(const CELogitsParams &p, int sms, cudaStream_t s);
 cudaError_t gemm_set_attributes();
 cudaError_t aux_set_attributes();
