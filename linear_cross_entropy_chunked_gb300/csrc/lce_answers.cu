@@ -340,6 +340,11 @@ __global__ void __launch_bounds__(ANS_THREADS, 1)
         const long long si = rank == 0 ? rs.scalar(t, p.V) : -1;
         bad |= !mbar_wait(&lbar[buf], lpar, ab);
         if (!y_ok) {
+            // every thread has seen this phase of the buffer's barrier before it can go on by two more
+            if (__syncthreads_or(bad)) {
+                aborted = true;
+                break;
+            }
             if (t == 0) {
                 issue(it + nbuf, buf, y_ahead);
                 y_ahead = label(it + nbuf + 1);

@@ -163,6 +163,30 @@ def test_masked_logits_and_rows_that_do_not_count(dtype):
     assert np.array_equal(cpu64(dZ[10:]) * 9, cpu64(dZ[10:]) * 9)
 
 
+@pytest.mark.parametrize("n,v,ignored", [(5000, 65, 0.5), (3001, 33, 0.95), (2000, 5003, 0.4), (1021, 50257, 0.4)])
+def test_many_rows_of_which_some_do_not_count(n, v, ignored):
+    # (several rows per CTA, in every order of counting ones and others: no wait runs out)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    Z = torch.randn(n, v, generator=g, device="cuda").half()
+    y = torch.randint(0, v, (n,), generator=g, device="cuda")
+    y[torch.rand(n, generator=g, device="cuda") < ignored] = -100
+    a = torch.randn(n, generator=g, device="cuda")
+    ws = torch.empty(65536, dtype=torch.uint8, device="cuda")
+    loss, logprobs, dZ = lce.policy_logits(Z, y, a, ws=ws)
+    assert lce.read_status(ws) == 0
+    z, ok = Z.double(), y >= 0
+    lp = torch.log_softmax(z, 1)
+    want = torch.where(ok, lp.gather(1, y.clamp(min=0)[:, None])[:, 0], 0.0)
+    lb = logp_bound(np.array([[0.0, 14.0]]), 1.0, v)
+    assert (logprobs - want).abs().max() <= lb
+    p = lp.exp_()
+    p[ok, y[ok]] -= 1.0
+    p *= torch.where(ok, a.double() / ok.sum(), 0.0)[:, None]
+    bound = 2.0 ** -11 * p.abs() + 2 * TINY[torch.float16] + 4 * lb * (a.double().abs() / ok.sum())[:, None] * p.abs().clamp(min=1e-9)
+    assert ((dZ.double() - p).abs() <= bound + 4 * lb * a.abs().max() / ok.sum()).all()
+    assert not dZ[~ok].any()
+
+
 def test_no_rows_and_no_counting_rows():
     f = torch.empty(0, device="cuda")
     loss, logprobs, dZ = lce.policy_logits(torch.empty(0, 50, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda"), f)

@@ -75,6 +75,24 @@ def test_logits(n, v, pairs, layout, dtype):
     assert torch.equal(again[0], loss) and torch.equal(again[1], seq) and torch.equal(Z, dZ)
 
 
+@pytest.mark.parametrize("n,v,ignored", [(5000, 65, 0.5), (2000, 5003, 0.4), (1021, 50257, 0.4)])
+def test_many_rows_of_which_some_do_not_count(n, v, ignored):
+    g = torch.Generator(device="cuda").manual_seed(n)
+    Z = torch.randn(n, v, generator=g, device="cuda").half()
+    y = torch.randint(0, v, (n,), generator=g, device="cuda")
+    y[torch.rand(n, generator=g, device="cuda") < ignored] = -100
+    off = answers(n, 9, n)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    loss, seq, dZ = lce.preference_logits(Z, y, off.cuda(), ws=ws)
+    assert lce.read_status(ws) == 0
+    lp = torch.log_softmax(Z.double(), 1).gather(1, y.clamp(min=0)[:, None])[:, 0]
+    lp = torch.where(y >= 0, lp, 0.0).cpu()
+    want = torch.stack([lp[a:b].sum() for a, b in zip(off, off[1:])])
+    lb = logp_bound(np.array([[0.0, 14.0]]), 1.0, v)
+    assert ((seq.cpu() - want).abs() <= lb * (off[1:] - off[:-1]).clamp(min=1) + 2.0 ** -22 * want.abs()).all()
+    assert torch.isfinite(dZ).all() and not dZ[y < 0].any()
+
+
 @pytest.mark.parametrize("v,dtype", [(600001, torch.float16), (262149, torch.float32)], ids=str)
 def test_rows_beyond_the_registers(v, dtype):
     z, y, off = case(4, v, 1, 1, ignored=0.0)
