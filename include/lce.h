@@ -261,8 +261,8 @@ lce_status lce_ce_logits(const void *Z, int z_dtype, int64_t ld, const int64_t *
  * known range: LCE_ERR_UNSUPPORTED). Workspace: lce_workspace_size_opt(..., flags).
  * lce_policy_forward: loss and logprobs alone, workspace lce_forward_workspace_size.
  * lce_policy_logits: over given logits (z_dtype as for lce_ce_logits): one read of the
- * counting rows and one write of dZ (NULL: no gradient; Z itself: in place), V up to 524288 (16-bit) or
- * 262144 (fp32) (more: a second read). Z, dZ: rows of any stride ld >= V from any element
+ * counting rows and one write of dZ (NULL: no gradient; Z itself: in place), V up to 450000 (16-bit) or
+ * 225000 (fp32) (more: a second read). Z, dZ: rows of any stride ld >= V from any element
  * on, both at the same address modulo 16. Workspace: lce_ce_logits_workspace_size(N). */
 lce_status lce_policy_forward(const void *H, const void *W, const int64_t *y, const float *advantages,
                               const float *old_logprobs, const float *ref_logprobs, const float *weights,

@@ -27,7 +27,6 @@ constexpr int ANS_THREADS = 512;
 constexpr int ANS_WARPS = ANS_THREADS / 32;
 constexpr int ANS_MAX_CLUSTER = 8;
 constexpr int ANS_MAX_BUF = 3;
-constexpr int ANS_MAX_VPT = 16;                  // 16-byte vectors per thread
 constexpr uint32_t ANS_COPY_BYTES = 32768;       // bytes per bulk copy instruction
 constexpr uint64_t ANS_WAIT_NS = 2000000000ull;  // bound of every wait (2 s)
 constexpr int STREAM_THREADS = 1024;
@@ -245,28 +244,39 @@ __global__ void __launch_bounds__(1024) lce_answer_scan_kernel(const long long *
 }
 
 // ------------------------------------------------------------------ rows, cluster kernel
-// A cluster of 1 to 8 CTAs takes one row at a time; rank k owns the vectors [k sv, (k + 1) sv)
-// of it, rank 0 also the values beside them (one per thread). Per row, in each CTA:
-//   * bulk copies have brought the vectors into a buffer; the threads move theirs into
-//     registers, whereupon the buffer is filled again with the row nbuf steps ahead;
-//   * max, then the sum of exp((z - max) / T);
-//   * (max, sum, label's logit if it lies here) goes to every CTA of the cluster by st.async;
-//   * the label's log probability, the row's loss and its slope, in every thread; the gradient
-//     exp((z - max) / T) * (scale / sum) - onehot * scale from the registers. The exponentials are
-//     formed again, not kept: they are the very numbers that were summed, and 16-bit logits would
-//     have to round them.
+// A cluster of 1, 2, 4 or 8 CTAs takes one row at a time; rank k owns the vectors [k sv, (k + 1) sv)
+// of it, rank 0 also the values beside them. The logits stay in shared memory from the copy that
+// brings them to the gradient: nbuf buffers hold a row that comes, one that is summed and one
+// whose gradient is written. Rows that count go through three stages:
+//   * a producer warp starts the bulk copies of a row as soon as a buffer is free;
+//   * 16 warps sum row i: per thread the maximum and the sum of exp((z - maximum) / T), merged over
+//     the warp and left for the manager; then they write the gradient of row i - 1,
+//     exp((z - max) / T) * (scale / sum), the label's less `scale`. (The exponentials are formed twice:
+//     kept in 16 bits they would be rounded.)
+//   * a manager warp merges the warps' parts, exchanges (max, sum, the label's logit) with the cluster's
+//     other CTAs by st.async, and forms the log probability, the row's loss and the gradient's
+//     scale once, while the 16 warps are at another row.
+// Every sum has a fixed order. Rows that do not count take no buffer: their zeros are written on the way.
 
-template <typename T, int VPT>
-__global__ void __launch_bounds__(ANS_THREADS, 1)
+struct RowResult {
+    float M, f, scale, zl;   // maximum, scale / sum, scale, the label's logit
+};
+
+template <typename T>
+__global__ void __launch_bounds__(ANS_THREADS + 64, 1)
     lce_answer_rows_kernel(const __grid_constant__ AnswerParams p, const int sv, const int nbuf) {
     using CV = Vec<T>;
     constexpr int EL = CV::ELEMS;
     extern __shared__ __align__(128) uint8_t ans_smem[];
     __shared__ __align__(8) uint64_t lbar[ANS_MAX_BUF];    // a row's copies landed
-    __shared__ __align__(8) uint64_t xbar[2];              // every CTA's (max, sum, logit) landed
+    __shared__ __align__(8) uint64_t ebar[ANS_MAX_BUF];    // every warp is done with the buffer
+    __shared__ __align__(8) uint64_t sbar[2];              // every warp's part of the row is there
+    __shared__ __align__(8) uint64_t xbar[2];              // every CTA's part of the row landed
+    __shared__ __align__(8) uint64_t rbar[2];              // the row's result is there
     __shared__ __align__(16) float4 xslot[2][ANS_MAX_CLUSTER];
-    __shared__ float s_red_m[ANS_WARPS], s_red_s[ANS_WARPS];
-    __shared__ float2 s_red_d[ANS_WARPS];
+    __shared__ __align__(16) RowResult s_res[2];
+    __shared__ float2 s_part[2][ANS_WARPS];
+    __shared__ float2 s_red[ANS_WARPS + 2];
     __shared__ int s_abort, s_last;
 
     const int t = threadIdx.x, w = t >> 5, l = t & 31;
@@ -274,12 +284,19 @@ __global__ void __launch_bounds__(ANS_THREADS, 1)
     const long long cid = cluster_id(), ncl = cluster_count();
     const Abort ab{&s_abort, p.hdr, ANS_WAIT_NS};
     const T *Z = static_cast<const T *>(p.Z);
+    const float k2 = LOG2E_F * p.pol.inv_t;
 
     if (t == 0) {
         s_abort = 0;
-        for (int b = 0; b < nbuf; ++b) mbar_init(&lbar[b], 1);
-        mbar_init(&xbar[0], 1);
-        mbar_init(&xbar[1], 1);
+        for (int b = 0; b < nbuf; ++b) {
+            mbar_init(&lbar[b], 1);
+            mbar_init(&ebar[b], ANS_WARPS);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sbar[b], ANS_WARPS);
+            mbar_init(&xbar[b], 1);
+            mbar_init(&rbar[b], 1);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -291,209 +308,247 @@ __global__ void __launch_bounds__(ANS_THREADS, 1)
         const long long n = rs.nvec - v0;
         return n <= 0 ? 0 : n < sv ? static_cast<int>(n) : sv;
     };
-    // thread 0: starts the copies of the cluster's it-th row, whose label is yi, into buffer b
-    long long issued = 0;
-    auto issue = [&](long long it, int b, long long yi) {
-        const long long r = cid + it * ncl;
-        if (r >= p.N) return;
-        issued = it + 1;
-        const RowSplit<T> rs(Z + r * p.ld, p.V);
-        const uint32_t bytes = label_counts(yi, p.V, p.ignore_index) ? vectors(rs) * 16u : 0u;
-        if (bytes == 0) {
-            mbar_arrive(&lbar[b]);
-            return;
-        }
-        mbar_arrive_expect_tx(&lbar[b], bytes);
-        const uint8_t *src = reinterpret_cast<const uint8_t *>(rs.row + rs.head + v0 * EL);
-        const uint32_t dst = smem_u32(ans_smem + static_cast<size_t>(b) * sv * 16);
-        for (uint32_t off = 0; off < bytes; off += ANS_COPY_BYTES)
-            bulk_copy(dst + off, src + off, bytes - off < ANS_COPY_BYTES ? bytes - off : ANS_COPY_BYTES,
-                      smem_u32(&lbar[b]));
-    };
-    auto label = [&](long long it) -> long long {
-        const long long r = cid + it * ncl;
-        return r < p.N ? p.y[r] : p.ignore_index;
-    };
-    long long y_ahead = 0;   // thread 0: the label of the row that is issued next
-    if (t == 0) {
-        for (int j = 0; j < nbuf; ++j) issue(j, j, label(j));
-        y_ahead = label(nbuf);
-    }
+    auto label = [&](long long r) -> long long { return r < p.N ? p.y[r] : p.ignore_index; };
+    auto counts = [&](long long yv) -> bool { return label_counts(yv, p.V, p.ignore_index); };
+    auto buffer = [&](int b) -> uint8_t * { return ans_smem + static_cast<size_t>(b) * sv * 16; };
+    // (a wait that runs out ends the loop for a whole warp: its lanes decide together)
 
-    wait_for_previous_grid();   // the header
-    const int nvalid = p.hdr[HDR_NVALID];
-    const float k2 = LOG2E_F * p.pol.inv_t;
-    const float2 kk = make_float2(k2, k2);
-    int buf = 0, xs = 0;
-    uint32_t lpar = 0, xpar = 0;
-    bool bad = false, aborted = false;
-    long long it = 0, y_next = label(0);
-    for (; cid + it * ncl < p.N; ++it) {
-        const long long r = cid + it * ncl;
-        const long long yv = y_next;
-        y_next = label(it + 1);
-        const RowSplit<T> rs(Z + r * p.ld, p.V);
-        const int nvec = vectors(rs);
-        const bool y_ok = label_counts(yv, p.V, p.ignore_index);
-        T *drow = p.dZ ? static_cast<T *>(p.dZ) + r * p.ld : nullptr;
-        uint4 *dvec = reinterpret_cast<uint4 *>(drow + rs.head) + v0;   // (not used where dZ is null)
-        const long long si = rank == 0 ? rs.scalar(t, p.V) : -1;
-        bad |= !mbar_wait(&lbar[buf], lpar, ab);
-        if (!y_ok) {
-            // every thread has seen this phase of the buffer's barrier before it can go on by two more
-            if (__syncthreads_or(bad)) {
-                aborted = true;
-                break;
+    if (w == ANS_WARPS) {
+        // the producer
+        if (l == 0) {
+            int b = 0;
+            uint32_t par = 1;   // (the buffers are free at first)
+            long long issued = 0, y_next = label(cid);
+            for (long long r = cid; r < p.N; r += ncl) {
+                const long long yv = y_next;
+                y_next = label(r + ncl);
+                if (!counts(yv)) continue;
+                if (!mbar_wait(&ebar[b], par, ab)) break;
+                const RowSplit<T> rs(Z + r * p.ld, p.V);
+                const uint32_t bytes = vectors(rs) * 16u;
+                ++issued;
+                if (bytes == 0) {
+                    mbar_arrive(&lbar[b]);
+                } else {
+                    fence_proxy_async_smem();
+                    mbar_arrive_expect_tx(&lbar[b], bytes);
+                    const uint8_t *src = reinterpret_cast<const uint8_t *>(rs.row + rs.head + v0 * EL);
+                    const uint32_t dst = smem_u32(buffer(b));
+                    for (uint32_t off = 0; off < bytes; off += ANS_COPY_BYTES)
+                        bulk_copy(dst + off, src + off, bytes - off < ANS_COPY_BYTES ? bytes - off : ANS_COPY_BYTES,
+                                  smem_u32(&lbar[b]));
+                }
+                if (++b == nbuf) {
+                    b = 0;
+                    par ^= 1u;
+                }
             }
-            if (t == 0) {
-                issue(it + nbuf, buf, y_ahead);
-                y_ahead = label(it + nbuf + 1);
-                if (rank == 0) {
+            // copies that nobody waited for (after a wait that ran out) may still be landing
+            for (long long j = issued > nbuf ? issued - nbuf : 0; j < issued; ++j)
+                mbar_wait_drain(&lbar[j % nbuf], static_cast<uint32_t>((j / nbuf) & 1), ANS_WAIT_NS);
+        }
+    } else if (w == ANS_WARPS + 1) {
+        // the manager
+        int b = 0, xs = 0;
+        uint32_t lpar = 0, xpar = 0;
+        long long y_next = label(cid);
+        wait_for_previous_grid();   // the header
+        const int nvalid = p.hdr[HDR_NVALID];
+        for (long long r = cid; r < p.N; r += ncl) {
+            const long long yv = y_next;
+            y_next = label(r + ncl);
+            if (!counts(yv)) {
+                if (l == 0 && rank == 0) {
                     p.loss_rows[r] = 0.f;
                     if (p.pol.logp) p.pol.logp[r] = 0.f;
                     if (p.max_sum) p.max_sum[r] = make_float2(0.f, 1.f);
                 }
+                continue;
             }
-            if (drow) {
-                for (int v = t; v < nvec; v += ANS_THREADS) dvec[v] = make_uint4(0u, 0u, 0u, 0u);
-                if (si >= 0) drow[si] = CV::from(0.f);
+            const RowSplit<T> rs(Z + r * p.ld, p.V);
+            if (!__all_sync(0xffffffffu, mbar_wait(&lbar[b], lpar, ab))) break;
+            // the label's logit, if it lies here
+            float zl = 0.f;
+            if (yv >= rs.head && yv < rs.tail0) {
+                const long long yi = yv - rs.head - v0 * EL;
+                if (yi >= 0 && yi < static_cast<long long>(vectors(rs)) * EL)
+                    zl = static_cast<float>(reinterpret_cast<const T *>(buffer(b))[yi]);
+            } else if (rank == 0) {
+                zl = static_cast<float>(rs.row[yv]);
             }
-        } else {
-            const uint4 *sg = reinterpret_cast<const uint4 *>(ans_smem + static_cast<size_t>(buf) * sv * 16);
-            // where the label's logit lies: in a vector of this CTA, or beside the vectors (rank 0)
-            const long long yi = yv - rs.head - v0 * EL;
-            const bool in_vec = yv >= rs.head && yv < rs.tail0;
-            const int yl = in_vec && yi >= 0 && yi < static_cast<long long>(nvec) * EL ? static_cast<int>(yi) : -1;
-            uint4 d[VPT];
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int v = t + k * ANS_THREADS;
-                d[k] = v < nvec ? sg[v] : make_uint4(CV::NEG_INF, CV::NEG_INF, CV::NEG_INF, CV::NEG_INF);
-            }
-            const float xsc = si >= 0 ? static_cast<float>(rs.row[si]) : -INFINITY;
-            float zy = 0.f;
-            if (t == 0) {
-                if (yl >= 0) zy = static_cast<float>(reinterpret_cast<const T *>(sg)[yl]);
-                else if (rank == 0 && !in_vec) zy = static_cast<float>(rs.row[yv]);
-                mbar_arrive_expect_tx(&xbar[xs], cl * 16u);
-            }
-            float m = xsc;
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) m = CV::max2(d[k], m);
-            m = wmax(m);
-            if (l == 0) s_red_m[w] = m;
-            // every thread holds its vectors: the buffer may be filled again; also the abort vote
-            if (__syncthreads_or(bad)) {
-                aborted = true;
-                break;
-            }
-            if (t == 0) {
-                fence_proxy_async_smem();
-                issue(it + nbuf, buf, y_ahead);
-                y_ahead = label(it + nbuf + 1);
-            }
-            m = wmax(l < ANS_WARPS ? s_red_m[l] : -INFINITY);
-            // (the distance from the maximum first: its product with k2 may be beyond fp32, as for a row
-            // of the type's lowest value; with nothing here every exponential is 0)
-            const float nm = m == -INFINITY ? 0.f : -m;
-            const float2 nm2 = make_float2(nm, nm);
-            float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < VPT; ++k)
-#pragma unroll
-                for (int q = 0; q < CV::PAIRS; ++q) {
-                    const float2 a = __fmul2_rn(__fadd2_rn(CV::pair(d[k], q), nm2), kk);
-                    const float2 e = make_float2(exp2_fast(a.x), exp2_fast(a.y));
-                    if (q & 1) acc1 = __fadd2_rn(acc1, e);
-                    else acc0 = __fadd2_rn(acc0, e);
-                }
-            const float2 acc = __fadd2_rn(acc0, acc1);
-            float s = wsum(acc.x + acc.y + exp2_fast((xsc + nm) * k2));
-            if (l == 0) s_red_s[w] = s;
-            __syncthreads();
-            s = wsum(l < ANS_WARPS ? s_red_s[l] : 0.f);
-            zy = __shfl_sync(0xffffffffu, zy, 0);   // (warp 0 sends: its lane 0 has it)
-            if (w == 0 && l < static_cast<int>(cl))
-                st_async_f32x4(map_to_rank(&xslot[xs][rank], l), m, s, zy, 0.f, map_to_rank(&xbar[xs], l));
-            const bool xok = mbar_wait_cluster(&xbar[xs], xpar, ab);
-            bad |= !xok;
-            if (xok) {
-                // lane k holds rank k's part; the maximum, the sum in rank order, the one logit
-                const float4 x = l < static_cast<int>(cl) ? xslot[xs][l] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-                float M = x.x;
-#pragma unroll
-                for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-                float S = x.x == -INFINITY ? x.y : x.y * exp2f((x.x - M) * k2);   // (0, or a NaN)
-                float zl = x.z;
-#pragma unroll
-                for (int o = 4; o > 0; o >>= 1) {
-                    S += __shfl_xor_sync(0xffffffffu, S, o);
-                    zl += __shfl_xor_sync(0xffffffffu, zl, o);
-                }
-                M = __shfl_sync(0xffffffffu, M, 0);
-                S = __shfl_sync(0xffffffffu, S, 0);
-                zl = __shfl_sync(0xffffffffu, zl, 0);
-                const float logp = (zl - M) * p.pol.inv_t - logf(S);
-                PolicyRow pr{-logp, 0.f};
-                if (p.pol.adv) pr = lce_policy_row(p.pol, r, logp);
-                if (t == 0 && rank == 0) {
+            if (l == 0) mbar_arrive_expect_tx(&xbar[xs], cl * 16u);
+            if (!__all_sync(0xffffffffu, mbar_wait(&sbar[xs], xpar, ab))) break;
+            float2 x = l < ANS_WARPS ? s_part[xs][l] : make_float2(-INFINITY, 0.f);
+            float M = wmax(x.x);
+            float S = wsum(x.x == -INFINITY ? x.y : x.y * exp2_fast((x.x - M) * k2));   // (0, or a NaN, without a logit)
+            if (l < static_cast<int>(cl))
+                st_async_f32x4(map_to_rank(&xslot[xs][rank], l), M, S, zl, 0.f, map_to_rank(&xbar[xs], l));
+            if (!__all_sync(0xffffffffu, mbar_wait_cluster(&xbar[xs], xpar, ab))) break;
+            const float4 q = l < static_cast<int>(cl) ? xslot[xs][l] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+            M = wmax(q.x);
+            S = wsum(q.x == -INFINITY ? q.y : q.y * exp2_fast((q.x - M) * k2));
+            zl = wsum(q.z);
+            const float logp = (zl - M) * p.pol.inv_t - logf(S);
+            PolicyRow pr{-logp, 0.f};
+            if (p.pol.adv) pr = lce_policy_row(p.pol, r, logp);
+            if (l == 0) {
+                const float scale = -pr.slope * p.pol.inv_t *
+                                    lce_row_scale(p.dloss, p.dloss_per_row, p.mean, nvalid, r, true);
+                s_res[xs] = RowResult{M, scale / S, scale, zl};
+                mbar_arrive(&rbar[xs]);
+                if (rank == 0) {
                     p.loss_rows[r] = pr.loss;
                     if (p.pol.logp) p.pol.logp[r] = logp;
                     if (p.max_sum) p.max_sum[r] = make_float2(M, S);
                 }
-                if (drow) {
-                    const float scale = -pr.slope * p.pol.inv_t *
-                                        lce_row_scale(p.dloss, p.dloss_per_row, p.mean, nvalid, r, true);
-                    if (scale == 0.f) {
-                        for (int v = t; v < nvec; v += ANS_THREADS) dvec[v] = make_uint4(0u, 0u, 0u, 0u);
-                        if (si >= 0) drow[si] = CV::from(0.f);
-                    } else {
-                        const float f = (m == -INFINITY ? 1.f : exp2f((m - M) * k2)) * (scale / S);
-                        const float2 f2 = make_float2(f, f);
-                        const int vy = yl >= 0 ? yl / EL : -1, jy = yl & (EL - 1);
-#pragma unroll
-                        for (int k = 0; k < VPT; ++k) {
-                            const int v = t + k * ANS_THREADS;
-                            if (v < nvec) {
-                                uint4 out;
-#pragma unroll
-                                for (int q = 0; q < CV::PAIRS; ++q) {
-                                    const float2 a = __fmul2_rn(__fadd2_rn(CV::pair(d[k], q), nm2), kk);
-                                    float2 g = __fmul2_rn(make_float2(exp2_fast(a.x), exp2_fast(a.y)), f2);
-                                    if (v == vy) {
-                                        if (2 * q == jy) g.x -= scale;
-                                        if (2 * q + 1 == jy) g.y -= scale;
-                                    }
-                                    CV::set_pair(out, q, g);
-                                }
-                                dvec[v] = out;
-                            }
-                        }
-                        if (si >= 0) {
-                            float g = exp2_fast((xsc + nm) * k2) * f;
-                            if (si == yv) g -= scale;
-                            drow[si] = CV::from(g);
-                        }
-                    }
-                }
+            }
+            __syncwarp();
+            if (++b == nbuf) {
+                b = 0;
+                lpar ^= 1u;
             }
             xs ^= 1;
             if (xs == 0) xpar ^= 1u;
         }
-        if (++buf == nbuf) {
-            buf = 0;
-            lpar ^= 1u;
+    } else {
+        const float2 kk = make_float2(k2, k2);
+        // the row before, whose gradient is to be written (prev < 0: none), and its buffer
+        long long prev = -1, prev_y = 0;
+        int b = 0, xs = 0, prev_b = 0;
+        uint32_t lpar = 0, rpar = 0;   // rpar: of the previous row's result
+        auto zeros = [&](long long r, const RowSplit<T> &rs) {
+            if (!p.dZ) return;
+            T *drow = static_cast<T *>(p.dZ) + r * p.ld;
+            uint4 *dvec = reinterpret_cast<uint4 *>(drow + rs.head) + v0;
+            const int n = vectors(rs);
+            for (int v = t; v < n; v += ANS_THREADS) dvec[v] = make_uint4(0u, 0u, 0u, 0u);
+            const long long si = rank == 0 && w == 0 ? rs.scalar(t, p.V) : -1;
+            if (si >= 0) drow[si] = CV::from(0.f);
+        };
+        // The gradient of the row before; its buffer is free after that.
+        auto gradient = [&]() -> bool {
+            if (prev < 0) return true;
+            const int xp = xs ^ 1;   // (the exchange slots alternate over the rows that count)
+            if (!__all_sync(0xffffffffu, mbar_wait(&rbar[xp], rpar, ab))) return false;
+            if (p.dZ) {
+                const RowResult res = s_res[xp];
+                const RowSplit<T> rs(Z + prev * p.ld, p.V);
+                if (res.scale == 0.f) {
+                    zeros(prev, rs);
+                } else {
+                    T *drow = static_cast<T *>(p.dZ) + prev * p.ld;
+                    uint4 *dvec = reinterpret_cast<uint4 *>(drow + rs.head) + v0;
+                    const uint4 *sg = reinterpret_cast<const uint4 *>(buffer(prev_b));
+                    const int n = vectors(rs);
+                    const float2 f2 = make_float2(res.f, res.f), nm2 = make_float2(-res.M, -res.M);
+                    auto one = [&](const uint4 &u) {
+                        uint4 out;
+#pragma unroll
+                        for (int q = 0; q < CV::PAIRS; ++q) {
+                            const float2 a = __fmul2_rn(__fadd2_rn(CV::pair(u, q), nm2), kk);
+                            CV::set_pair(out, q, __fmul2_rn(make_float2(exp2_fast(a.x), exp2_fast(a.y)), f2));
+                        }
+                        return out;
+                    };
+                    int v = t;
+                    for (; v + 3 * ANS_THREADS < n; v += 4 * ANS_THREADS) {
+                        uint4 u[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) u[j] = sg[v + j * ANS_THREADS];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) dvec[v + j * ANS_THREADS] = one(u[j]);
+                    }
+                    for (; v < n; v += ANS_THREADS) dvec[v] = one(sg[v]);
+                    const long long si = rank == 0 && w == 0 ? rs.scalar(t, p.V) : -1;
+                    if (si >= 0) drow[si] = CV::from(exp2_fast((static_cast<float>(rs.row[si]) - res.M) * k2) * res.f);
+                    // the label's place again, by the thread that has written it
+                    const long long yi = prev_y - rs.head - v0 * EL;
+                    const bool mine = prev_y >= rs.head && prev_y < rs.tail0
+                                          ? yi >= 0 && yi < static_cast<long long>(n) * EL &&
+                                                static_cast<int>(yi / EL) % ANS_THREADS == t
+                                          : si == prev_y;
+                    if (mine) drow[prev_y] = CV::from(exp2_fast((res.zl - res.M) * k2) * res.f - res.scale);
+                }
+            }
+            __syncwarp();
+            if (l == 0) mbar_arrive(&ebar[prev_b]);
+            if (xp == 1) rpar ^= 1u;
+            prev = -1;
+            return true;
+        };
+        long long y_next = label(cid);
+        bool ok = true;
+        for (long long r = cid; r < p.N; r += ncl) {
+            const long long yv = y_next;
+            y_next = label(r + ncl);
+            const RowSplit<T> rs(Z + r * p.ld, p.V);
+            if (!counts(yv)) {
+                zeros(r, rs);
+                continue;
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(&lbar[b], lpar, ab));
+            if (!ok) break;
+            // this row's maximum and sum, four vectors of each thread at a time
+            const uint4 *sg = reinterpret_cast<const uint4 *>(buffer(b));
+            const int n = vectors(rs);
+            const long long si = rank == 0 && w == 0 ? rs.scalar(t, p.V) : -1;
+            float m = si >= 0 ? static_cast<float>(rs.row[si]) : -INFINITY;
+            float2 acc = make_float2(si >= 0 ? (m == -INFINITY ? 0.f : m == m ? 1.f : m) : 0.f, 0.f);
+            if (m != m) m = -INFINITY;
+            for (int v = t; v < n; v += 4 * ANS_THREADS) {
+                uint4 u[4];
+                float mv = m;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    u[j] = v + j * ANS_THREADS < n ? sg[v + j * ANS_THREADS]
+                                                   : make_uint4(CV::NEG_INF, CV::NEG_INF, CV::NEG_INF, CV::NEG_INF);
+                    mv = CV::max2(u[j], mv);
+                }
+                // (the distance from the maximum first: its product with k2 may be beyond fp32, as for
+                // a row of the type's lowest value; without a logit every exponential is 0)
+                const float nm = mv == -INFINITY ? 0.f : -mv;
+                const float c = m == mv ? 1.f : exp2_fast((m + nm) * k2);
+                acc.x *= c;
+                acc.y *= c;
+                m = mv;
+                const float2 nm2 = make_float2(nm, nm);
+                float2 a1 = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int q = 0; q < CV::PAIRS; ++q) {
+                        const float2 a = __fmul2_rn(__fadd2_rn(CV::pair(u[j], q), nm2), kk);
+                        const float2 e = make_float2(exp2_fast(a.x), exp2_fast(a.y));
+                        if (q & 1) a1 = __fadd2_rn(a1, e);
+                        else acc = __fadd2_rn(acc, e);
+                    }
+                acc = __fadd2_rn(acc, a1);
+            }
+            const float wm = wmax(m);
+            const float s = acc.x + acc.y;
+            const float ws = wsum(m == -INFINITY ? s : s * exp2_fast((m - wm) * k2));   // (0, or a NaN, without a logit)
+            if (l == 0) {
+                s_part[xs][w] = make_float2(wm, ws);
+                mbar_arrive(&sbar[xs]);
+            }
+            __syncwarp();
+            ok = gradient();
+            if (!ok) break;
+            prev = r;
+            prev_y = yv;
+            prev_b = b;
+            if (++b == nbuf) {
+                b = 0;
+                lpar ^= 1u;
+            }
+            xs ^= 1;
         }
+        if (ok) gradient();
     }
-    aborted = __syncthreads_or(aborted || bad);
-    if (aborted && t == 0)
-        // copies of rows it .. issued - 1 may still be landing here
-        for (long long j = it; j < issued; ++j)
-            mbar_wait_drain(&lbar[j % nbuf], static_cast<uint32_t>((j / nbuf) & 1), ANS_WAIT_NS);
     __syncthreads();
     cluster_sync_all();   // no CTA leaves while a peer may still write into its slots
     if (rank == 0 && p.loss && last_to_finish(p.hdr + HDR_DONE, static_cast<int>(ncl), &s_last))
-        write_loss(p, s_red_d);
+        write_loss(p, s_red);
 }
 
 // ------------------------------------------------------------------ rows, streaming kernel
@@ -810,47 +865,31 @@ __global__ void __launch_bounds__(SCALE_THREADS) lce_scale_kernel(const S *src, 
 
 using RowsKernel = void (*)(const AnswerParams, const int, const int);
 
-template <typename T> RowsKernel rows_kernel_of(int vpt) {
-    switch (vpt) {
-        case 1: return lce_answer_rows_kernel<T, 1>;
-        case 2: return lce_answer_rows_kernel<T, 2>;
-        case 4: return lce_answer_rows_kernel<T, 4>;
-        case 8: return lce_answer_rows_kernel<T, 8>;
-        default: return lce_answer_rows_kernel<T, 16>;
-    }
-}
-RowsKernel rows_kernel(int dtype, int vpt) {
-    return dtype == CE_FP32 ? rows_kernel_of<float>(vpt)
-           : dtype == CE_FP16 ? rows_kernel_of<__half>(vpt) : rows_kernel_of<__nv_bfloat16>(vpt);
+RowsKernel rows_kernel(int dtype) {
+    return dtype == CE_FP32 ? lce_answer_rows_kernel<float>
+           : dtype == CE_FP16 ? lce_answer_rows_kernel<__half> : lce_answer_rows_kernel<__nv_bfloat16>;
 }
 
 int g_ans_max_dyn[64];   // per device: dynamic shared memory the cluster kernel may take
 
 struct Shape {
-    int cl = 0, sv = 0, vpt = 0, nbuf = 0;
+    int cl = 0, sv = 0, nbuf = 0;
     size_t smem = 0;
 };
 
-// The smallest cluster whose CTAs hold a row in registers; with so few rows that SMs would
-// idle, a larger one.
+// The smallest cluster of whose rows three buffers fit into a CTA's shared memory, else two; with
+// so few rows that SMs would idle, a larger one.
 bool rows_shape(const AnswerParams &p, int sms, int max_dyn, Shape *o) {
-    const long long el = p.dtype == CE_FP32 ? 4 : 8;
-    const long long nvec = p.V / el;
+    const long long nvec = p.V / (p.dtype == CE_FP32 ? 4 : 8);
+    auto bytes = [&](int cl) { return ((nvec + cl - 1) / cl > 0 ? (nvec + cl - 1) / cl : 1) * 16; };
     int cl = 1;
-    while (cl <= ANS_MAX_CLUSTER && (nvec + cl - 1) / cl > ANS_THREADS * ANS_MAX_VPT) ++cl;
-    if (cl > ANS_MAX_CLUSTER) return false;
+    while (cl < ANS_MAX_CLUSTER && 3 * bytes(cl) > max_dyn) cl *= 2;
+    if (2 * bytes(cl) > max_dyn) return false;
     while (cl < ANS_MAX_CLUSTER && p.N * cl * 2 <= sms && nvec / cl > ANS_THREADS) cl *= 2;
-    if (cl > ANS_MAX_CLUSTER) cl = ANS_MAX_CLUSTER;
     o->cl = cl;
-    o->sv = static_cast<int>((nvec + cl - 1) / cl);
-    if (o->sv < 1) o->sv = 1;
-    o->vpt = 1;
-    while (ANS_THREADS * o->vpt < o->sv) o->vpt *= 2;
-    const size_t bytes = static_cast<size_t>(o->sv) * 16;
-    const long long fit = max_dyn / static_cast<long long>(bytes);
-    if (fit < 1) return false;
-    o->nbuf = fit < ANS_MAX_BUF ? static_cast<int>(fit) : ANS_MAX_BUF;
-    o->smem = o->nbuf * bytes;
+    o->sv = static_cast<int>(bytes(cl) / 16);
+    o->nbuf = max_dyn / bytes(cl) < ANS_MAX_BUF ? 2 : ANS_MAX_BUF;
+    o->smem = o->nbuf * static_cast<size_t>(bytes(cl));
     return true;
 }
 
@@ -866,7 +905,7 @@ cudaLaunchAttribute after_previous() {
 
 cudaError_t launch_rows_cluster(const AnswerParams &p, const Shape &sh, int dev, bool *launched, cudaStream_t s) {
     *launched = false;
-    const RowsKernel fn = rows_kernel(p.dtype, sh.vpt);
+    const RowsKernel fn = rows_kernel(p.dtype);
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = sh.cl;
@@ -875,12 +914,12 @@ cudaError_t launch_rows_cluster(const AnswerParams &p, const Shape &sh, int dev,
     at[1] = after_previous();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(sh.cl);
-    cfg.blockDim = dim3(ANS_THREADS);
+    cfg.blockDim = dim3(ANS_THREADS + 64);
     cfg.dynamicSmemBytes = sh.smem;
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const long long key = (((static_cast<long long>(dev) * 4 + p.dtype) * 32 + sh.vpt) * 16 + sh.cl) * (1ll << 24) +
+    const long long key = ((static_cast<long long>(dev) * 4 + p.dtype) * 16 + sh.cl) * (1ll << 24) +
                           static_cast<long long>(sh.smem);
     int n = -1;
     {
@@ -950,18 +989,17 @@ cudaError_t answers_set_attributes() {
     e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
     if (e != cudaSuccess) return e;
     for (int pass = 0; pass < 2; ++pass)
-        for (int dt = 0; dt < 3; ++dt)
-            for (int vpt = 1; vpt <= ANS_MAX_VPT; vpt *= 2) {
-                if (pass == 0) {
-                    cudaFuncAttributes fa{};
-                    e = cudaFuncGetAttributes(&fa, rows_kernel(dt, vpt));
-                    if (static_cast<int>(fa.sharedSizeBytes) > used) used = static_cast<int>(fa.sharedSizeBytes);
-                } else {
-                    e = cudaFuncSetAttribute(rows_kernel(dt, vpt), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             optin - used - 1024);
-                }
-                if (e != cudaSuccess) return e;
+        for (int dt = 0; dt < 3; ++dt) {
+            if (pass == 0) {
+                cudaFuncAttributes fa{};
+                e = cudaFuncGetAttributes(&fa, rows_kernel(dt));
+                if (static_cast<int>(fa.sharedSizeBytes) > used) used = static_cast<int>(fa.sharedSizeBytes);
+            } else {
+                e = cudaFuncSetAttribute(rows_kernel(dt), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         optin - used - 1024);
             }
+            if (e != cudaSuccess) return e;
+        }
     g_ans_max_dyn[dev] = optin - used - 1024;
     return cudaSuccess;
 }
