@@ -27,6 +27,7 @@ constexpr int ANS_THREADS = 512;
 constexpr int ANS_WARPS = ANS_THREADS / 32;
 constexpr int ANS_MAX_CLUSTER = 8;
 constexpr int ANS_MAX_BUF = 3;
+constexpr int ANS_SLOTS = 4;                     // rows between their sums and their results
 constexpr uint32_t ANS_COPY_BYTES = 32768;       // bytes per bulk copy instruction
 constexpr uint64_t ANS_WAIT_NS = 2000000000ull;  // bound of every wait (2 s)
 constexpr int STREAM_THREADS = 1024;
@@ -42,9 +43,11 @@ template <> struct Vec<__nv_bfloat16> {
         return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
     __device__ static void set_pair(uint4 &u, int q, float2 v) { (&u.x)[q] = pack_bf16x2(v.x, v.y); }
-    __device__ static float max2(const uint4 &u, float m) {
-        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
-        const __nv_bfloat162 a = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    // The largest of N vectors' values and m.
+    template <int N> __device__ static float max_of(const uint4 (&u)[N], float m) {
+        __nv_bfloat162 a = reinterpret_cast<const __nv_bfloat162 *>(&u[0])[0];
+#pragma unroll
+        for (int i = 1; i < 4 * N; ++i) a = __hmax2(a, reinterpret_cast<const __nv_bfloat162 *>(&u[i / 4])[i % 4]);
         return fmaxf(m, fmaxf(__low2float(a), __high2float(a)));
     }
     __device__ static __nv_bfloat16 from(float v) { return __float2bfloat16_rn(v); }
@@ -56,9 +59,10 @@ template <> struct Vec<__half> {
         return __half22float2(reinterpret_cast<const __half2 *>(&u)[q]);
     }
     __device__ static void set_pair(uint4 &u, int q, float2 v) { (&u.x)[q] = pack_f16x2(v.x, v.y); }
-    __device__ static float max2(const uint4 &u, float m) {
-        const __half2 *h = reinterpret_cast<const __half2 *>(&u);
-        const __half2 a = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    template <int N> __device__ static float max_of(const uint4 (&u)[N], float m) {
+        __half2 a = reinterpret_cast<const __half2 *>(&u[0])[0];
+#pragma unroll
+        for (int i = 1; i < 4 * N; ++i) a = __hmax2(a, reinterpret_cast<const __half2 *>(&u[i / 4])[i % 4]);
         return fmaxf(m, fmaxf(__low2float(a), __high2float(a)));
     }
     __device__ static __half from(float v) { return __float2half_rn(v); }
@@ -73,9 +77,12 @@ template <> struct Vec<float> {
         (&u.x)[2 * q] = __float_as_uint(v.x);
         (&u.x)[2 * q + 1] = __float_as_uint(v.y);
     }
-    __device__ static float max2(const uint4 &u, float m) {
-        return fmaxf(fmaxf(m, fmaxf(__uint_as_float(u.x), __uint_as_float(u.y))),
-                     fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+    template <int N> __device__ static float max_of(const uint4 (&u)[N], float m) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            m = fmaxf(fmaxf(m, fmaxf(__uint_as_float(u[i].x), __uint_as_float(u[i].y))),
+                      fmaxf(__uint_as_float(u[i].z), __uint_as_float(u[i].w)));
+        return m;
     }
     __device__ static float from(float v) { return v; }
 };
@@ -88,6 +95,17 @@ __device__ __forceinline__ float wmax(float v) {
 __device__ __forceinline__ float wsum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+// Over groups of G consecutive lanes.
+template <int G> __device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+template <int G> __device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 // A sum kept as two fp32 numbers (what the first addition loses goes into the second): losses of
@@ -167,6 +185,26 @@ template <typename T> struct RowSplit {
     __device__ long long scalar(int t, long long V) const {
         const long long i = t < head ? t : tail0 + (t - head);
         return i < V ? i : -1;
+    }
+};
+
+// exp((z - m) / T) as 2^(z k2 + nm) * c for k2 = log2(e) / T: one fused operation for each logit. nm is
+// -m k2 as fp32 has it and c takes back what that rounding lost, so the result is as exact as
+// the distance from m is. Where m k2 would leave fp32 (a row of the type's lowest value)
+// `far` is set, and the distance is to be formed first.
+struct ExpFrom {
+    float m, k2, nm, c;
+    bool far;
+    __device__ ExpFrom(float m_, float k2_) : m(m_ == -INFINITY ? 0.f : m_), k2(k2_) {
+        nm = -(m * k2);
+        far = !(fabsf(nm) < 1e38f);
+        c = far ? 1.f : exp2_fast(-fmaf(m, k2, nm));
+        if (far) nm = 0.f;
+    }
+    __device__ float operator()(float z) const { return exp2_fast(far ? (z - m) * k2 : fmaf(z, k2, nm)); }
+    __device__ float2 pair(float2 z) const {
+        const float2 a = __ffma2_rn(z, make_float2(k2, k2), make_float2(nm, nm));
+        return make_float2(exp2_fast(a.x), exp2_fast(a.y));
     }
 };
 
@@ -269,13 +307,13 @@ __global__ void __launch_bounds__(ANS_THREADS + 64, 1)
     constexpr int EL = CV::ELEMS;
     extern __shared__ __align__(128) uint8_t ans_smem[];
     __shared__ __align__(8) uint64_t lbar[ANS_MAX_BUF];    // a row's copies landed
-    __shared__ __align__(8) uint64_t ebar[ANS_MAX_BUF];    // every warp is done with the buffer
-    __shared__ __align__(8) uint64_t sbar[2];              // every warp's part of the row is there
-    __shared__ __align__(8) uint64_t xbar[2];              // every CTA's part of the row landed
-    __shared__ __align__(8) uint64_t rbar[2];              // the row's result is there
-    __shared__ __align__(16) float4 xslot[2][ANS_MAX_CLUSTER];
-    __shared__ __align__(16) RowResult s_res[2];
-    __shared__ float2 s_part[2][ANS_WARPS];
+    __shared__ __align__(8) uint64_t ebar[ANS_MAX_BUF];    // every warp, the manager too, is done with the buffer
+    __shared__ __align__(8) uint64_t sbar[ANS_SLOTS];      // every warp's part of the row is there
+    __shared__ __align__(8) uint64_t xbar[ANS_SLOTS];      // every CTA's part of the row landed
+    __shared__ __align__(8) uint64_t rbar[ANS_SLOTS];      // the row's result is there
+    __shared__ __align__(16) float4 xslot[ANS_SLOTS][ANS_MAX_CLUSTER];
+    __shared__ __align__(16) RowResult s_res[ANS_SLOTS];
+    __shared__ float2 s_part[ANS_SLOTS][ANS_WARPS];
     __shared__ float2 s_red[ANS_WARPS + 2];
     __shared__ int s_abort, s_last;
 
@@ -290,9 +328,9 @@ __global__ void __launch_bounds__(ANS_THREADS + 64, 1)
         s_abort = 0;
         for (int b = 0; b < nbuf; ++b) {
             mbar_init(&lbar[b], 1);
-            mbar_init(&ebar[b], ANS_WARPS);
+            mbar_init(&ebar[b], ANS_WARPS + 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < ANS_SLOTS; ++b) {
             mbar_init(&sbar[b], ANS_WARPS);
             mbar_init(&xbar[b], 1);
             mbar_init(&rbar[b], 1);
@@ -376,24 +414,30 @@ __global__ void __launch_bounds__(ANS_THREADS + 64, 1)
             } else if (rank == 0) {
                 zl = static_cast<float>(rs.row[yv]);
             }
-            if (l == 0) mbar_arrive_expect_tx(&xbar[xs], cl * 16u);
+            __syncwarp();
+            if (l == 0) {
+                mbar_arrive(&ebar[b]);
+                mbar_arrive_expect_tx(&xbar[xs], cl * 16u);
+            }
+            const PolicyInputs in = lce_policy_inputs(p.pol, r);
+            const float d = lce_row_scale(p.dloss, p.dloss_per_row, p.mean, nvalid, r, true);
             if (!__all_sync(0xffffffffu, mbar_wait(&sbar[xs], xpar, ab))) break;
-            float2 x = l < ANS_WARPS ? s_part[xs][l] : make_float2(-INFINITY, 0.f);
-            float M = wmax(x.x);
-            float S = wsum(x.x == -INFINITY ? x.y : x.y * exp2_fast((x.x - M) * k2));   // (0, or a NaN, without a logit)
+            const float2 x = s_part[xs][l % ANS_WARPS];
+            float M = group_max<ANS_WARPS>(x.x);
+            float S = group_sum<ANS_WARPS>(x.x == -INFINITY ? x.y : x.y * exp2_fast((x.x - M) * k2));   // (0, or a NaN, without a logit)
             if (l < static_cast<int>(cl))
                 st_async_f32x4(map_to_rank(&xslot[xs][rank], l), M, S, zl, 0.f, map_to_rank(&xbar[xs], l));
             if (!__all_sync(0xffffffffu, mbar_wait_cluster(&xbar[xs], xpar, ab))) break;
-            const float4 q = l < static_cast<int>(cl) ? xslot[xs][l] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-            M = wmax(q.x);
-            S = wsum(q.x == -INFINITY ? q.y : q.y * exp2_fast((q.x - M) * k2));
-            zl = wsum(q.z);
+            const int part = l % ANS_MAX_CLUSTER;
+            const float4 q = part < static_cast<int>(cl) ? xslot[xs][part] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+            M = group_max<ANS_MAX_CLUSTER>(q.x);
+            S = group_sum<ANS_MAX_CLUSTER>(q.x == -INFINITY ? q.y : q.y * exp2_fast((q.x - M) * k2));
+            zl = group_sum<ANS_MAX_CLUSTER>(q.z);
             const float logp = (zl - M) * p.pol.inv_t - logf(S);
             PolicyRow pr{-logp, 0.f};
-            if (p.pol.adv) pr = lce_policy_row(p.pol, r, logp);
+            if (p.pol.adv) pr = lce_policy_row(p.pol, in, logp);
             if (l == 0) {
-                const float scale = -pr.slope * p.pol.inv_t *
-                                    lce_row_scale(p.dloss, p.dloss_per_row, p.mean, nvalid, r, true);
+                const float scale = -pr.slope * p.pol.inv_t * d;
                 s_res[xs] = RowResult{M, scale / S, scale, zl};
                 mbar_arrive(&rbar[xs]);
                 if (rank == 0) {
@@ -407,15 +451,16 @@ __global__ void __launch_bounds__(ANS_THREADS + 64, 1)
                 b = 0;
                 lpar ^= 1u;
             }
-            xs ^= 1;
-            if (xs == 0) xpar ^= 1u;
+            if (++xs == ANS_SLOTS) {
+                xs = 0;
+                xpar ^= 1u;
+            }
         }
     } else {
-        const float2 kk = make_float2(k2, k2);
         // the row before, whose gradient is to be written (prev < 0: none), and its buffer
         long long prev = -1, prev_y = 0;
-        int b = 0, xs = 0, prev_b = 0;
-        uint32_t lpar = 0, rpar = 0;   // rpar: of the previous row's result
+        int b = 0, xs = 0, prev_b = 0, prev_xs = 0;
+        uint32_t lpar = 0, xpar = 0, prev_par = 0;
         auto zeros = [&](long long r, const RowSplit<T> &rs) {
             if (!p.dZ) return;
             T *drow = static_cast<T *>(p.dZ) + r * p.ld;
@@ -428,10 +473,9 @@ __global__ void __launch_bounds__(ANS_THREADS + 64, 1)
         // The gradient of the row before; its buffer is free after that.
         auto gradient = [&]() -> bool {
             if (prev < 0) return true;
-            const int xp = xs ^ 1;   // (the exchange slots alternate over the rows that count)
-            if (!__all_sync(0xffffffffu, mbar_wait(&rbar[xp], rpar, ab))) return false;
+            if (!__all_sync(0xffffffffu, mbar_wait(&rbar[prev_xs], prev_par, ab))) return false;
             if (p.dZ) {
-                const RowResult res = s_res[xp];
+                const RowResult res = s_res[prev_xs];
                 const RowSplit<T> rs(Z + prev * p.ld, p.V);
                 if (res.scale == 0.f) {
                     zeros(prev, rs);
@@ -440,43 +484,49 @@ __global__ void __launch_bounds__(ANS_THREADS + 64, 1)
                     uint4 *dvec = reinterpret_cast<uint4 *>(drow + rs.head) + v0;
                     const uint4 *sg = reinterpret_cast<const uint4 *>(buffer(prev_b));
                     const int n = vectors(rs);
-                    const float2 f2 = make_float2(res.f, res.f), nm2 = make_float2(-res.M, -res.M);
+                    const ExpFrom e(res.M, k2);
+                    const float f = res.f * e.c;
+                    const float2 f2 = make_float2(f, f);
                     auto one = [&](const uint4 &u) {
                         uint4 out;
 #pragma unroll
-                        for (int q = 0; q < CV::PAIRS; ++q) {
-                            const float2 a = __fmul2_rn(__fadd2_rn(CV::pair(u, q), nm2), kk);
-                            CV::set_pair(out, q, __fmul2_rn(make_float2(exp2_fast(a.x), exp2_fast(a.y)), f2));
-                        }
+                        for (int q = 0; q < CV::PAIRS; ++q)
+                            CV::set_pair(out, q, __fmul2_rn(e.pair(CV::pair(u, q)), f2));
                         return out;
                     };
-                    int v = t;
-                    for (; v + 3 * ANS_THREADS < n; v += 4 * ANS_THREADS) {
-                        uint4 u[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) u[j] = sg[v + j * ANS_THREADS];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) dvec[v + j * ANS_THREADS] = one(u[j]);
+                    if (!e.far) {
+#pragma unroll 1
+                        for (int v = t; v < n; v += 2 * ANS_THREADS) {
+                            const bool two = v + ANS_THREADS < n;
+                            const uint4 u0 = sg[v], u1 = two ? sg[v + ANS_THREADS] : u0;
+                            dvec[v] = one(u0);
+                            if (two) dvec[v + ANS_THREADS] = one(u1);
+                        }
+                    } else {
+                        const T *z = reinterpret_cast<const T *>(sg);
+#pragma unroll 1
+                        for (int v = t; v < n; v += ANS_THREADS)
+#pragma unroll 1
+                            for (int i = v * EL; i < (v + 1) * EL; ++i)
+                                reinterpret_cast<T *>(dvec)[i] = CV::from(e(static_cast<float>(z[i])) * f);
                     }
-                    for (; v < n; v += ANS_THREADS) dvec[v] = one(sg[v]);
                     const long long si = rank == 0 && w == 0 ? rs.scalar(t, p.V) : -1;
-                    if (si >= 0) drow[si] = CV::from(exp2_fast((static_cast<float>(rs.row[si]) - res.M) * k2) * res.f);
+                    if (si >= 0) drow[si] = CV::from(e(static_cast<float>(rs.row[si])) * f);
                     // the label's place again, by the thread that has written it
                     const long long yi = prev_y - rs.head - v0 * EL;
                     const bool mine = prev_y >= rs.head && prev_y < rs.tail0
                                           ? yi >= 0 && yi < static_cast<long long>(n) * EL &&
                                                 static_cast<int>(yi / EL) % ANS_THREADS == t
                                           : si == prev_y;
-                    if (mine) drow[prev_y] = CV::from(exp2_fast((res.zl - res.M) * k2) * res.f - res.scale);
+                    if (mine) drow[prev_y] = CV::from(e(res.zl) * f - res.scale);
                 }
             }
             __syncwarp();
             if (l == 0) mbar_arrive(&ebar[prev_b]);
-            if (xp == 1) rpar ^= 1u;
             prev = -1;
             return true;
         };
-        long long y_next = label(cid);
+        long long y_next = label(cid), used = 0;
         bool ok = true;
         for (long long r = cid; r < p.N; r += ncl) {
             const long long yv = y_next;
@@ -493,55 +543,76 @@ __global__ void __launch_bounds__(ANS_THREADS + 64, 1)
             const int n = vectors(rs);
             const long long si = rank == 0 && w == 0 ? rs.scalar(t, p.V) : -1;
             float m = si >= 0 ? static_cast<float>(rs.row[si]) : -INFINITY;
-            float2 acc = make_float2(si >= 0 ? (m == -INFINITY ? 0.f : m == m ? 1.f : m) : 0.f, 0.f);
+            float s = si >= 0 ? (m == -INFINITY ? 0.f : m == m ? 1.f : m) : 0.f;
             if (m != m) m = -INFINITY;
+#pragma unroll 1
             for (int v = t; v < n; v += 4 * ANS_THREADS) {
                 uint4 u[4];
-                float mv = m;
+                if (v + 3 * ANS_THREADS < n) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    u[j] = v + j * ANS_THREADS < n ? sg[v + j * ANS_THREADS]
-                                                   : make_uint4(CV::NEG_INF, CV::NEG_INF, CV::NEG_INF, CV::NEG_INF);
-                    mv = CV::max2(u[j], mv);
+                    for (int j = 0; j < 4; ++j) u[j] = sg[v + j * ANS_THREADS];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        u[j] = v + j * ANS_THREADS < n
+                                   ? sg[v + j * ANS_THREADS]
+                                   : make_uint4(CV::NEG_INF, CV::NEG_INF, CV::NEG_INF, CV::NEG_INF);
                 }
-                // (the distance from the maximum first: its product with k2 may be beyond fp32, as for
-                // a row of the type's lowest value; without a logit every exponential is 0)
-                const float nm = mv == -INFINITY ? 0.f : -mv;
-                const float c = m == mv ? 1.f : exp2_fast((m + nm) * k2);
-                acc.x *= c;
-                acc.y *= c;
+                const float mv = CV::max_of(u, m);
+                const ExpFrom e(mv, k2);
+                float2 a0 = make_float2(0.f, 0.f), a1 = make_float2(0.f, 0.f);
+                if (!e.far) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int q = 0; q < CV::PAIRS; ++q) {
+                            if (q & 1) a1 = __fadd2_rn(a1, e.pair(CV::pair(u[j], q)));
+                            else a0 = __fadd2_rn(a0, e.pair(CV::pair(u[j], q)));
+                        }
+                    a0 = __fadd2_rn(a0, a1);
+                } else {
+                    const T *z = reinterpret_cast<const T *>(sg);
+#pragma unroll 1
+                    for (int i = v; i < n && i < v + 4 * ANS_THREADS; i += ANS_THREADS)
+#pragma unroll 1
+                        for (int j = i * EL; j < (i + 1) * EL; ++j) a0.x += e(static_cast<float>(z[j]));
+                }
+                // (without a logit so far every exponential is 0, or a NaN)
+                s = s * (m == mv ? 1.f : exp2_fast((m - mv) * k2)) + (a0.x + a0.y) * e.c;
                 m = mv;
-                const float2 nm2 = make_float2(nm, nm);
-                float2 a1 = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int q = 0; q < CV::PAIRS; ++q) {
-                        const float2 a = __fmul2_rn(__fadd2_rn(CV::pair(u[j], q), nm2), kk);
-                        const float2 e = make_float2(exp2_fast(a.x), exp2_fast(a.y));
-                        if (q & 1) a1 = __fadd2_rn(a1, e);
-                        else acc = __fadd2_rn(acc, e);
-                    }
-                acc = __fadd2_rn(acc, a1);
             }
             const float wm = wmax(m);
-            const float s = acc.x + acc.y;
             const float ws = wsum(m == -INFINITY ? s : s * exp2_fast((m - wm) * k2));   // (0, or a NaN, without a logit)
+            // (the slot is free: with a gradient every warp has waited for the row before; without
+            // one the row that had it last is waited for here)
+            if (!p.dZ && used >= ANS_SLOTS) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&rbar[xs], xpar ^ 1u, ab));
+                if (!ok) break;
+            }
+            ++used;
             if (l == 0) {
                 s_part[xs][w] = make_float2(wm, ws);
                 mbar_arrive(&sbar[xs]);
+                if (!p.dZ) mbar_arrive(&ebar[b]);   // (no gradient will read it again)
             }
             __syncwarp();
-            ok = gradient();
-            if (!ok) break;
-            prev = r;
-            prev_y = yv;
-            prev_b = b;
+            if (p.dZ) {
+                ok = gradient();
+                if (!ok) break;
+                prev = r;
+                prev_y = yv;
+                prev_b = b;
+                prev_xs = xs;
+                prev_par = xpar;
+            }
             if (++b == nbuf) {
                 b = 0;
                 lpar ^= 1u;
             }
-            xs ^= 1;
+            if (++xs == ANS_SLOTS) {
+                xs = 0;
+                xpar ^= 1u;
+            }
         }
         if (ok) gradient();
     }
@@ -579,40 +650,42 @@ __device__ __forceinline__ void write_gradient(const RowSplit<T> &rs, T *drow, l
         if (t < extra) drow[rs.scalar(static_cast<int>(t), V)] = CV::from(0.f);
         return;
     }
-    const float nm = -M, f = scale / S;
-    const float2 kk = make_float2(k2, k2), nm2 = make_float2(nm, nm), f2 = make_float2(f, f);
+    const ExpFrom e(M, k2);
+    const float f = scale / S * e.c;
+    const float2 f2 = make_float2(f, f);
     const long long yi = yv - rs.head;
     const long long vy = yv >= rs.head && yv < rs.tail0 ? yi / EL : -1;
-    const int jy = static_cast<int>(yi & (EL - 1));
-    auto one = [&](long long v, const uint4 &u) {
+    // the label's place is written again by the thread that wrote it; its logit is read before
+    const bool mine = vy >= 0 ? vy >= t && vy < rs.nvec && (vy - t) % nt == 0
+                              : t < extra && rs.scalar(static_cast<int>(t), V) == yv;
+    const float zy = mine ? static_cast<float>(rs.row[yv]) : 0.f;
+    auto one = [&](const uint4 &u) {
         uint4 out;
 #pragma unroll
-        for (int q = 0; q < CV::PAIRS; ++q) {
-            const float2 a = __fmul2_rn(__fadd2_rn(CV::pair(u, q), nm2), kk);
-            float2 g = __fmul2_rn(make_float2(exp2_fast(a.x), exp2_fast(a.y)), f2);
-            if (v == vy) {
-                if (2 * q == jy) g.x -= scale;
-                if (2 * q + 1 == jy) g.y -= scale;
-            }
-            CV::set_pair(out, q, g);
-        }
-        dst[v] = out;
+        for (int q = 0; q < CV::PAIRS; ++q) CV::set_pair(out, q, __fmul2_rn(e.pair(CV::pair(u, q)), f2));
+        return out;
     };
     long long v = t;
+    if (e.far) {
+#pragma unroll 1
+        for (; v < rs.nvec; v += nt)
+#pragma unroll 1
+            for (int j = 0; j < EL; ++j)
+                drow[rs.head + v * EL + j] = CV::from(e(static_cast<float>(rs.row[rs.head + v * EL + j])) * f);
+    }
     for (; v + 3 * nt < rs.nvec; v += 4 * nt) {
         uint4 u[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) u[j] = src[v + j * nt];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) one(v + j * nt, u[j]);
+        for (int j = 0; j < 4; ++j) dst[v + j * nt] = one(u[j]);
     }
-    for (; v < rs.nvec; v += nt) one(v, src[v]);
+    for (; v < rs.nvec; v += nt) dst[v] = one(src[v]);
     if (t < extra) {
         const long long i = rs.scalar(static_cast<int>(t), V);
-        float g = exp2_fast((static_cast<float>(rs.row[i]) + nm) * k2) * f;
-        if (i == yv) g -= scale;
-        drow[i] = CV::from(g);
+        drow[i] = CV::from(e(static_cast<float>(rs.row[i])) * f);
     }
+    if (mine) drow[yv] = CV::from(e(zy) * f - scale);
 }
 
 template <typename T>
@@ -638,7 +711,8 @@ __global__ void __launch_bounds__(STREAM_THREADS, 1) lce_answer_stream_kernel(co
             float m = -INFINITY, s = 0.f;
             for (long long v = t; v < rs.nvec; v += STREAM_THREADS) {
                 const uint4 u = src[v];
-                const float mv = CV::max2(u, -INFINITY);
+                const uint4 u1[1] = {u};
+                const float mv = CV::max_of(u1, -INFINITY);
                 const float nm = mv == -INFINITY ? 0.f : -mv;
                 float sum = 0.f;
 #pragma unroll

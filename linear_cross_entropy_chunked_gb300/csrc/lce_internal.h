@@ -123,26 +123,32 @@ struct PolicyParams {
 struct PolicyRow {
     float loss, slope;
 };
-__device__ __forceinline__ PolicyRow lce_policy_row(const PolicyParams &p, long long i, float logp) {
-    const float a = p.adv[i];
-    const float r = p.old_logp ? expf(logp - p.old_logp[i]) : (logp == logp ? 1.f : logp);
-    const float f = r * a;
-    const float h = (r < p.lo ? p.lo : r > p.hi ? p.hi : r) * a;
+struct PolicyInputs {   // of a row
+    float a, old_logp, ref_logp, w;
+};
+__device__ __forceinline__ PolicyInputs lce_policy_inputs(const PolicyParams &p, long long i) {
+    return PolicyInputs{p.adv ? p.adv[i] : 0.f, p.old_logp ? p.old_logp[i] : 0.f,
+                        p.ref_logp ? p.ref_logp[i] : 0.f, p.weight ? p.weight[i] : 1.f};
+}
+__device__ __forceinline__ PolicyRow lce_policy_row(const PolicyParams &p, const PolicyInputs &x, float logp) {
+    const float r = p.old_logp ? expf(logp - x.old_logp) : (logp == logp ? 1.f : logp);
+    const float f = r * x.a;
+    const float h = (r < p.lo ? p.lo : r > p.hi ? p.hi : r) * x.a;
     PolicyRow o;
     o.loss = f <= h ? -f : -h;
     o.slope = f <= h ? -f : h * 0.f;
     if (p.ref_logp && p.beta != 0.f) {
-        const float d = p.ref_logp[i] - logp;
+        const float d = x.ref_logp - logp;
         const float e = expm1f(d);
         o.loss += p.beta * (d == INFINITY ? d : e - d);
         o.slope -= p.beta * e;
     }
-    if (p.weight) {
-        const float w = p.weight[i];
-        o.loss *= w;
-        o.slope *= w;
-    }
+    o.loss *= x.w;
+    o.slope *= x.w;
     return o;
+}
+__device__ __forceinline__ PolicyRow lce_policy_row(const PolicyParams &p, long long i, float logp) {
+    return lce_policy_row(p, lce_policy_inputs(p, i), logp);
 }
 
 // Workspace header (int32 words).
