@@ -398,6 +398,26 @@ lce_status lce_fp8_linear(const void *X, int x_dtype, int64_t ldx, const void *W
                           int64_t K, void *out, int64_t ldc, int c_dtype, void *ws, size_t ws_bytes,
                           lce_stream_t stream);
 
+/* Linear layers with 4-bit weights, for answering: W [V][D] as packed values q [V][ldq] (bytes; value
+ * 2 j of a row in the low half of byte j, 2 j + 1 in the high half) and 16-bit scales
+ * [V][lds], one per row and group of 32, 64 or 128 values along D (the last group may be shorter):
+ *   w[v][k] = (q[v][k] - 8) * scale(v, k / group)
+ * ldq: a multiple of 16, at least ceil(D / 32) * 16, of which a row's first ceil(D / 32) * 16 bytes
+ * are read; what lies behind value D - 1 there counts for nothing. D up to 65536.
+ *
+ * lce_int4_quantize: W [V][ldw] (w_dtype as for lce_ce_logits); a group's scale is a seventh of its
+ * largest magnitude in scale_dtype (0 bf16, 2 fp16; 1 for a group of zeros, NaN for one with an
+ * infinity or a NaN), q = 8 + the nearest whole number to w / scale within -8 .. 7 (ties to even).
+ * lce_int4_linear: out [M][ldc] = X W^T for X [M][ldx], both x_dtype (0 bf16, 2 fp16), the type of
+ * the scales: sums of a group in fp32, scaled and added up in fp32, rounded once. X, out, scale need the
+ * alignment of their elements only, q that of 16 bytes. Columns of out from V on are left
+ * as they were. No workspace. */
+lce_status lce_int4_quantize(const void *W, int w_dtype, int64_t ldw, int64_t V, int64_t D, int group, void *q,
+                             int64_t ldq, void *scale, int scale_dtype, int64_t lds, lce_stream_t stream);
+lce_status lce_int4_linear(const void *X, int x_dtype, int64_t ldx, const void *q, int64_t ldq, const void *scale,
+                           int64_t lds, int group, int64_t M, int64_t V, int64_t D, void *out, int64_t ldc,
+                           lce_stream_t stream);
+
 /* The global norm of a list of n gradients and clipping by it:
  *   norm = (sum over all tensors of |g|^p)^(1/p) for p = 2 or 1, or max |g|
  *   out = g * min(1, max_norm / (norm + eps))

@@ -72,6 +72,7 @@ lce_status init_device(int *sms, int *pairs) {
         if (aux_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
         if (ce_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
         if (answers_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
+        if (int4_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
         if (sample_set_attributes() != cudaSuccess) return LCE_ERR_CUDA;
         g_dev_fp8[dev] = fp8_set_attributes() == cudaSuccess;
         if (!g_dev_fp8[dev]) cudaGetLastError();
@@ -2196,6 +2197,75 @@ lce_status lce_fp8_linear(const void *X, int x_dtype, int64_t ldx, const void *W
     const size_t behind = align_up(need, 1024);
     return fp8_matmul(xq, ldq, sx, 1, M, W, ldw, sw, sw_row, sw_block, 0, M, N, K, out, ldc, c_dtype, ws, ws_bytes,
                       w + behind, ws_bytes > behind ? ws_bytes - behind : 0, M > 0, stream);
+}
+
+lce_status lce_int4_quantize(const void *W, int w_dtype, int64_t ldw, int64_t V, int64_t D, int group, void *q,
+                             int64_t ldq, void *scale, int scale_dtype, int64_t lds, lce_stream_t stream) {
+    g_launches = 0;
+    if (w_dtype < CE_BF16 || w_dtype > CE_FP16 || (scale_dtype != CE_BF16 && scale_dtype != CE_FP16))
+        return LCE_ERR_INVALID_ARG;
+    if (group != 32 && group != 64 && group != 128) return LCE_ERR_INVALID_ARG;
+    if (V < 0 || V > 0x7fffffffll || D <= 0 || D > I4_MAX_D || ldw < D || ldq < (D + 31) / 32 * 16 ||
+        lds < cdiv(D, group))
+        return LCE_ERR_INVALID_ARG;
+    if (V > 0 && (!W || !q || !scale)) return LCE_ERR_INVALID_ARG;
+    if (ldq % 16 || !aligned16(q) || reinterpret_cast<uintptr_t>(W) % (w_dtype == CE_FP32 ? 4 : 2) ||
+        reinterpret_cast<uintptr_t>(scale) % 2)
+        return LCE_ERR_ALIGNMENT;
+    int sms = 0, pairs = 0;
+    LCE_TRY(init_device(&sms, &pairs));
+    if (V == 0) return LCE_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    Int4QuantParams p;
+    p.W = W;
+    p.ldw = ldw;
+    p.V = V;
+    p.D = static_cast<int>(D);
+    p.dtype = w_dtype;
+    p.group = group;
+    p.q = static_cast<uint8_t *>(q);
+    p.ldq = ldq;
+    p.scale = scale;
+    p.lds = lds;
+    p.scale_dtype = scale_dtype;
+    LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_int4_quantize(p, s));
+    return LCE_OK;
+}
+
+lce_status lce_int4_linear(const void *X, int x_dtype, int64_t ldx, const void *q, int64_t ldq, const void *scale,
+                           int64_t lds, int group, int64_t M, int64_t V, int64_t D, void *out, int64_t ldc,
+                           lce_stream_t stream) {
+    g_launches = 0;
+    if (x_dtype != CE_BF16 && x_dtype != CE_FP16) return LCE_ERR_INVALID_ARG;
+    if (group != 32 && group != 64 && group != 128) return LCE_ERR_INVALID_ARG;
+    if (M < 0 || M > (1ll << 20) || V <= 0 || V > MAX_V || D <= 0 || D > I4_MAX_D || ldx < D || ldc < V ||
+        ldq < (D + 31) / 32 * 16 || lds < cdiv(D, group))
+        return LCE_ERR_INVALID_ARG;
+    if (!q || !scale || (M > 0 && (!X || !out))) return LCE_ERR_INVALID_ARG;
+    const uintptr_t halves = reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(scale) |
+                             reinterpret_cast<uintptr_t>(out);
+    if (ldq % 16 || !aligned16(q) || halves % 2) return LCE_ERR_ALIGNMENT;
+    int sms = 0, pairs = 0;
+    LCE_TRY(init_device(&sms, &pairs));
+    if (M == 0) return LCE_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    Int4Params p;
+    p.X = X;
+    p.ldx = ldx;
+    p.dtype = x_dtype;
+    p.x_vec = aligned16(X) && ldx % 8 == 0;
+    p.q = static_cast<const uint8_t *>(q);
+    p.ldq = ldq;
+    p.scale = scale;
+    p.lds = lds;
+    p.group = group;
+    p.M = static_cast<int>(M);
+    p.V = static_cast<int>(V);
+    p.D = static_cast<int>(D);
+    p.out = out;
+    p.ldc = ldc;
+    LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_int4(p, sms, s));
+    return LCE_OK;
 }
 
 lce_status lce_grad_norm_workspace_size(int64_t n, size_t *bytes) {

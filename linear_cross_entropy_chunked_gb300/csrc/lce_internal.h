@@ -394,6 +394,34 @@ struct ClipScale {
     float *norm_out;
 };
 
+// 4-bit linear layers (lce_int4.cu).
+struct Int4Params {
+    const void *X;             // [M][ldx], bf16 or fp16
+    long long ldx;
+    int dtype;                 // of X, the scales and the result
+    int x_vec;                 // rows of X are 16-byte aligned
+    const uint8_t *q;          // [V][ldq] bytes: two values each, rows on 16 bytes
+    long long ldq;
+    const void *scale;         // [V][lds]
+    long long lds;
+    int group;                 // 32, 64 or 128 values
+    int M, V, D;
+    void *out;                 // [M][ldc]
+    long long ldc;
+    int units, ks, tokens;     // (set by the launcher)
+};
+constexpr long long I4_MAX_D = 65536;
+struct Int4QuantParams {
+    const void *W;             // [V][ldw]
+    long long ldw, V;
+    int D, dtype, group;
+    uint8_t *q;                // [V][ldq]
+    long long ldq;
+    void *scale;               // [V][lds]
+    long long lds;
+    int scale_dtype;           // CE_BF16 or CE_FP16
+};
+
 // 8-bit linear layers (lce_fp8.cu).
 struct Fp8QuantParams {
     const void *X;             // [R][ld]
@@ -475,6 +503,10 @@ long long clip_chunks(const void *p, long long n, int dtype);
 cudaError_t launch_grad_norm(const ClipItem *items, int n, int kind, double *part, int sms, int *parts,
                              cudaStream_t s);
 cudaError_t launch_grad_scale(const ClipItem *items, int n, const ClipScale &c, int sms, cudaStream_t s);
+
+cudaError_t int4_set_attributes();
+cudaError_t launch_int4(Int4Params p, int sms, cudaStream_t s);
+cudaError_t launch_int4_quantize(const Int4QuantParams &p, cudaStream_t s);
 
 cudaError_t fp8_set_attributes();
 cudaError_t launch_fp8_quantize(const Fp8QuantParams &p, int dtype, bool tile, cudaStream_t s);
