@@ -17,52 +17,67 @@ namespace {
 //   * A warp takes 16 rows x 128 values (a unit) at a time as the A operand of eight m16n8k16 products, the
 //     tokens are the columns of B. Which of the unit's values a product calls its k-th does not
 //     matter as long as both operands agree, so a lane's 16 loaded bytes become its fragments as
-//     they lie: (w >> n) & mask | magic turns nibbles i and i + 4 of a word into two 16-bit floats
-//     16 + q (the nibble lies in the top bits of the mantissa).
-//   * The 24 too many of 16 + q go into the accumulator's start, -24 * (sum of the group's x).
+//     they lie: of a word's nibbles i and i + 4, masked into 16-bit floats 1024 + q or 1024 + 16 q, one
+//     packed fp16 operation makes q - 8, exactly: 5 operations of the half-rate integer pipe per eight values.
+//   * The products are fp16 for bf16 x too (whose 7 bits of mantissa would take 8 such operations): a
+//     token is multiplied by the power of two that brings its largest magnitude below 2^15. bf16's
+//     8 bits fit; what lies below 2^-29 of the largest is rounded to multiples of 2^-39 of it.
 //   * Groups of 64 and 32 values need products that stay inside a group: the four lanes of a row exchange
 //     words (2 or 4 shuffles a row) so that every product's k lie in one group.
 //   * Sums of a group are scaled in fp32 registers and added up over the groups.
-//   * KS warps share a row block's units, RG row blocks go on beside each other; what a warp
-//     reads next is under way four units ahead, over the ends of row blocks too.
+//   * A CTA has a range of row blocks, and of its chunks (16 rows x 4 units) each warp a range of its own, so all
+//     warps have the same to do whatever V and D are. Nothing holds them together: each brings its
+//     chunks by bulk copies (a row's 256 bytes each) into two buffers of its own. A row block that two or
+//     more warps have parts of is added up at the end.
 // x lies in shared memory in the order in which lanes take it (one 16-byte load per word).
 
-constexpr int I4_THREADS = 512;
-constexpr int I4_WARPS = I4_THREADS / 32;
-constexpr int I4_AHEAD = 4;          // units under way per warp
 constexpr int I4_UNIT = 128;         // values of k
+constexpr int I4_CHUNK = 4;          // units of a chunk
+constexpr int I4_ROW = I4_CHUNK * 64 + 64;        // bytes of a chunk's row in shared memory: rows g and g + 1 half a line apart
+constexpr int I4_BUF = 16 * I4_ROW;
+constexpr int I4_MAX_WARPS = 16;
+constexpr uint64_t I4_WAIT_NS = 2000000000ull;    // bound of a wait for copies (2 s)
 
-__device__ __forceinline__ uint32_t lop_and_or(uint32_t a, uint32_t mask, uint32_t bits) { return (a & mask) | bits; }
-
-// 16 + q of nibbles i and i + 4, for i = 0 .. 3.
-template <typename T> __device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&o)[4]);
-template <> __device__ __forceinline__ void nibbles<__nv_bfloat16>(uint32_t w, uint32_t (&o)[4]) {
-    o[0] = lop_and_or(w << 3, 0x00780078u, 0x41804180u);
-    o[1] = lop_and_or(w >> 1, 0x00780078u, 0x41804180u);
-    o[2] = lop_and_or(w >> 5, 0x00780078u, 0x41804180u);
-    o[3] = lop_and_or(w >> 9, 0x00780078u, 0x41804180u);
+// (a & MASK) | bits in one operation: `bits` has to be in a register for that.
+template <uint32_t MASK> __device__ __forceinline__ __half2 and_or(uint32_t a, uint32_t bits) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(a), "n"(MASK), "r"(bits));
+    return *reinterpret_cast<const __half2 *>(&r);
 }
-template <> __device__ __forceinline__ void nibbles<__half>(uint32_t w, uint32_t (&o)[4]) {
-    o[0] = lop_and_or(w << 6, 0x03c003c0u, 0x4c004c00u);
-    o[1] = lop_and_or(w << 2, 0x03c003c0u, 0x4c004c00u);
-    o[2] = lop_and_or(w >> 2, 0x03c003c0u, 0x4c004c00u);
-    o[3] = lop_and_or(w >> 6, 0x03c003c0u, 0x4c004c00u);
+// q - 8 of nibbles i and i + 4 of a word, for i = 0 .. 3, as pairs of fp16; magic: 0x64006400 (1024, twice).
+__device__ __forceinline__ void nibbles(uint32_t w, uint32_t magic, __half2 (&o)[4]) {
+    const __half2 sixteenth = __float2half2_rn(0.0625f);
+    const __half2 off0 = __float2half2_rn(-1032.f), off1 = __float2half2_rn(-72.f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t v = i ? w >> 8 : w;
+        o[2 * i] = __hadd2(and_or<0x000f000fu>(v, magic), off0);
+        o[2 * i + 1] = __hfma2(and_or<0x00f000f0u>(v, magic), sixteenth, off1);
+    }
 }
-constexpr float I4_BIAS = 24.f;   // 16 + q = (q - 8) + 24
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
 
-template <typename T>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-    if constexpr (std::is_same<T, __half>::value)
+// c (+)= A B; `first`: c starts from zero.
+__device__ __forceinline__ void mma16816(float (&c)[4], __half2 a0, __half2 a1, __half2 a2, __half2 a3, uint32_t b0,
+                                         uint32_t b1, bool first) {
+    if (first) {
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                     "{%0, %1, %2, %3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                     "{%0, %1, %2, %3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                     "{%10, %10, %10, %10};"
+                     : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                     : "r"(*reinterpret_cast<uint32_t *>(&a0)), "r"(*reinterpret_cast<uint32_t *>(&a1)),
+                       "r"(*reinterpret_cast<uint32_t *>(&a2)), "r"(*reinterpret_cast<uint32_t *>(&a3)), "r"(b0),
+                       "r"(b1), "f"(0.f));
+        return;
+    }
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(*reinterpret_cast<uint32_t *>(&a0)), "r"(*reinterpret_cast<uint32_t *>(&a1)),
+                   "r"(*reinterpret_cast<uint32_t *>(&a2)), "r"(*reinterpret_cast<uint32_t *>(&a3)), "r"(b0), "r"(b1));
 }
 
 template <typename T> __device__ __forceinline__ float to_float(T v) { return static_cast<float>(v); }
@@ -113,64 +128,129 @@ template <int GROUP> __device__ __forceinline__ void exchange(uint32_t (&u)[4], 
     }
 }
 
-// What a warp holds of one unit: 16 bytes of rows r and r + 8, and those rows' scales.
-template <int GROUP> struct Unit {
-    uint4 q[2];
-    uint16_t s[2][I4_UNIT / GROUP];
-};
-
 template <typename T, int GROUP, int NT>
-__global__ void __launch_bounds__(I4_THREADS, 1) lce_int4_few_kernel(const Int4Params p) {
+__global__ void __launch_bounds__(I4_MAX_WARPS * 32, 1) lce_int4_few_kernel(const Int4Params p) {
     constexpr int PER = I4_UNIT / GROUP;     // groups of a unit
     constexpr int JS = 4 / PER;              // words of a lane per group
-    extern __shared__ __align__(16) uint8_t i4_smem[];
+    constexpr int SC = I4_CHUNK * PER;       // scales of a chunk's row
+    extern __shared__ __align__(128) uint8_t i4_smem[];
+    __shared__ float s_up[16], s_down[16];   // a token's power of two, and its inverse
+    __shared__ unsigned s_max[16];           // the bits of its largest finite magnitude
+    __shared__ __align__(8) uint64_t bars[I4_MAX_WARPS][2];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = lane >> 2, tl = lane & 3;
+    const int threads = blockDim.x, warps = threads / 32;
     const int m0 = blockIdx.y * p.tokens;
     const int mt = p.M - m0 < p.tokens ? p.M - m0 : p.tokens;
     const int units = p.units;
-    // x as 16-byte pieces [unit][word][token][t], sums of x [group][8 NT] (times -24), partial sums of warps
-    uint4 *xw = reinterpret_cast<uint4 *>(i4_smem);
-    float *xs = reinterpret_cast<float *>(i4_smem + static_cast<size_t>(units) * 16 * p.tokens * 16);
-    float4 *part = reinterpret_cast<float4 *>(xs + static_cast<size_t>(units) * PER * 8 * NT);
+    // per warp: two chunks of the weight, two of scales (fp32 [16][SC]); then 256 bytes of zeros, and x as
+    // 16-byte pieces [unit][token][word][t], the words of odd tokens in the order 1 0 3 2 (two tokens' pieces
+    // of a word lie half a line apart)
+    uint8_t *mine = i4_smem + warp * (2 * I4_BUF);
+    float *my_scales = reinterpret_cast<float *>(i4_smem + warps * (2 * I4_BUF)) + warp * (2 * 16 * SC);
+    uint4 *zero = reinterpret_cast<uint4 *>(i4_smem + warps * (2 * I4_BUF + 2 * 16 * SC * 4));
+    uint4 *xw = zero + 16;
 
-    const int ks = p.ks, rg_count = I4_WARPS / ks;
-    const int rg = warp / ks, kw = warp % ks;
     const int blocks = (p.V + 15) / 16;
-    const int step = gridDim.x * rg_count;
     const int row_bytes = (p.D + 31) / 32 * 16;
-    const uint16_t *scale = static_cast<const uint16_t *>(p.scale);
     const int groups = (p.D + GROUP - 1) / GROUP;
+    // the CTA's row blocks, and the warp's chunks of them
+    const int b0 = static_cast<int>(static_cast<long long>(blocks) * blockIdx.x / gridDim.x);
+    const int b1 = static_cast<int>(static_cast<long long>(blocks) * (blockIdx.x + 1) / gridDim.x);
+    const int cpb = (units + I4_CHUNK - 1) / I4_CHUNK;   // chunks of a row block
+    const long long chunks = static_cast<long long>(b1 - b0) * cpb;
+    auto begin_of = [&](int w) -> int { return static_cast<int>(chunks * w / warps); };
+    const int c_end = begin_of(warp + 1);
 
-    // the warp's sequence of (row block, unit): where the next load goes
-    int lb = blockIdx.x * rg_count + rg, lu = kw;
-    Unit<GROUP> ring[I4_AHEAD];
-    auto fetch = [&](Unit<GROUP> &o) {
-        if (lb >= blocks) return;
-        const int at = lu * 64 + tl * 16;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int row = lb * 16 + g + 8 * h < p.V ? lb * 16 + g + 8 * h : p.V - 1;
-            o.q[h] = at < row_bytes
-                         ? __ldcs(reinterpret_cast<const uint4 *>(p.q + static_cast<long long>(row) * p.ldq + at))
-                         : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                o.s[h][i] = lu * PER + i < groups ? scale[static_cast<long long>(row) * p.lds + lu * PER + i]
-                                                  : static_cast<uint16_t>(0);
+    if (t < warps * 2) mbar_init(&bars[t / 2][t % 2], 1);
+    if (t < 16) {
+        zero[t] = make_uint4(0u, 0u, 0u, 0u);
+        s_max[t] = 0u;
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncthreads();
+
+    // what is brought next: chunk nc, which is chunk `nk` of row block `nb`
+    int nc = begin_of(warp), nb = b0 + nc / cpb, nk = nc % cpb;
+    float sc[(16 * SC + 31) / 32];           // the scales that were asked for last
+    auto bring = [&](int buf) {
+        if (nc >= c_end) return;
+        const int at = nk * (I4_CHUNK * 64);
+        const int bytes = row_bytes - at < I4_CHUNK * 64 ? row_bytes - at : I4_CHUNK * 64;
+        uint64_t *bar = &bars[warp][buf];
+        if (lane == 0) mbar_arrive_expect_tx(bar, 16 * bytes);
+        __syncwarp();
+        if (lane < 16) {
+            const int row = nb * 16 + lane < p.V ? nb * 16 + lane : p.V - 1;
+            const uint8_t *src = p.q + static_cast<long long>(row) * p.ldq + at;
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                    smem_u32(mine + buf * I4_BUF + lane * I4_ROW)),
+                "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                : "memory");
         }
-        lu += ks;
-        if (lu >= units) {
-            lu = kw;
-            lb += step;
+#pragma unroll
+        for (int i = 0; i < (16 * SC + 31) / 32; ++i) {
+            const int e = i * 32 + lane, r = e / SC, k = nk * SC + e % SC;
+            const int row = nb * 16 + r < p.V ? nb * 16 + r : p.V - 1;
+            sc[i] = 0.f;
+            if (16 * SC % 32 == 0 || e < 16 * SC)
+                if (k < groups) sc[i] = to_float(static_cast<const T *>(p.scale)[static_cast<long long>(row) * p.lds + k]);
+        }
+        ++nc;
+        if (++nk == cpb) {
+            nk = 0;
+            ++nb;
         }
     };
+    auto keep_scales = [&](int buf) {
 #pragma unroll
-    for (int i = 0; i < I4_AHEAD; ++i) fetch(ring[i]);
+        for (int i = 0; i < (16 * SC + 31) / 32; ++i)
+            if (16 * SC % 32 == 0 || i * 32 + lane < 16 * SC) my_scales[buf * 16 * SC + i * 32 + lane] = sc[i];
+    };
+    bring(0);
+    keep_scales(0);
+    bring(1);
 
     // x into shared memory, beside the first loads
     const T *X = static_cast<const T *>(p.X) + static_cast<long long>(m0) * p.ldx;
-    for (int i = t; i < units * 16 * mt; i += I4_THREADS) {
-        const int tt = i & 3, m = (i >> 2) % mt, uj = (i >> 2) / mt, j = uj & 3, u = uj >> 2;
+    if (std::is_same<T, __nv_bfloat16>::value) {
+        const int per = (p.D + 255) / 256;   // steps of a warp over a token
+#pragma unroll 4
+        for (int i = warp; i < per * mt; i += warps) {
+            const int m = i / per, k = i % per * 256 + lane * 8;
+            const uint16_t *src = reinterpret_cast<const uint16_t *>(X) + static_cast<long long>(m) * p.ldx + k;
+            uint32_t most = 0u;   // (finite bf16 magnitudes order as their bits do)
+            if (p.x_vec && k + 8 <= p.D) {
+                const uint4 q = *reinterpret_cast<const uint4 *>(src);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t v = (&q.x)[e / 2] >> (16 * (e & 1)) & 0x7fffu;
+                    if (v < 0x7f80u && v > most) most = v;
+                }
+            } else {
+                for (int e = 0; e < 8 && k + e < p.D; ++e) {
+                    const uint32_t v = src[e] & 0x7fffu;
+                    if (v < 0x7f80u && v > most) most = v;
+                }
+            }
+            most = __reduce_max_sync(0xffffffffu, most);
+            if (lane == 0) atomicMax(&s_max[m], most);
+        }
+        __syncthreads();
+        if (t < mt) {
+            const float m = __uint_as_float(s_max[t] << 16);
+            int e = 0;
+            if (m > 0.f) frexpf(m, &e);   // m < 2^e
+            const int up = m > 0.f ? (15 - e < 120 ? 15 - e : 120) : 0;
+            s_up[t] = ldexpf(1.f, up);
+            s_down[t] = ldexpf(1.f, -up);
+        }
+    } else if (t < 16) {
+        s_up[t] = s_down[t] = 1.f;
+    }
+    __syncthreads();
+    for (int i = t; i < units * 16 * mt; i += threads) {
+        const int tt = i & 3, j = (i >> 2) & 3, m = (i >> 4) % mt, u = (i >> 4) / mt;
         int c, w;
         word_at<GROUP>(tt, j, &c, &w);
         const int k0 = u * I4_UNIT + c * 32 + w * 8;
@@ -185,69 +265,67 @@ __global__ void __launch_bounds__(I4_THREADS, 1) lce_int4_few_kernel(const Int4P
             for (int e = 0; e < 8; ++e)
                 v[e] = k0 + e < p.D ? reinterpret_cast<const uint16_t *>(src)[e] : static_cast<uint16_t>(0);
         }
+        if (std::is_same<T, __nv_bfloat16>::value) {
+            const float up = s_up[m];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = __half_as_ushort(__float2half_rn(__uint_as_float(static_cast<uint32_t>(v[e]) << 16) * up));
+        }
         // pairs (0, 4), (1, 5), (2, 6), (3, 7): the order in which a word's nibbles come
-        xw[((u * 4 + j) * p.tokens + m) * 4 + tt] =
+        xw[(u * p.tokens + m) * 16 + (j ^ (m & 1)) * 4 + tt] =
             make_uint4(v[0] | (v[4] << 16), v[1] | (v[5] << 16), v[2] | (v[6] << 16), v[3] | (v[7] << 16));
     }
     __syncthreads();
-    for (int i = t; i < units * PER * 8 * NT; i += I4_THREADS) {
-        const int m = i % (8 * NT), gr = i / (8 * NT), u = gr / PER, j0 = gr % PER * JS;
-        float s = 0.f;
-        if (m < mt)
-            for (int j = 0; j < JS; ++j)
-                for (int e = 0; e < 4; ++e) {
-                    const uint4 q = xw[((u * 4 + j0 + j) * p.tokens + m) * 4 + e];
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const uint32_t w = (&q.x)[h];
-                        T lo, hi;
-                        *reinterpret_cast<uint16_t *>(&lo) = static_cast<uint16_t>(w);
-                        *reinterpret_cast<uint16_t *>(&hi) = static_cast<uint16_t>(w >> 16);
-                        s += to_float(lo) + to_float(hi);
-                    }
-                }
-        xs[i] = -I4_BIAS * s;
-    }
-    __syncthreads();
 
-    float acc[NT][4];
-    auto clear = [&]() {
+    float acc[NT][4], head[NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-    };
-    clear();
-    auto compute = [&](const Unit<GROUP> &o, int u) {
-        uint32_t q0[4] = {o.q[0].x, o.q[0].y, o.q[0].z, o.q[0].w}, q1[4] = {o.q[1].x, o.q[1].y, o.q[1].z, o.q[1].w};
+        for (int i = 0; i < 4; ++i) acc[n][i] = head[n][i] = 0.f;
+    // a lane's pieces of x for each 8 tokens: where its even and its odd words are counted from (their order
+    // goes by the token), and the step to the next unit's; lanes of no token read zeros
+    uint32_t xe[NT], xo[NT];
+    int xu[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int m = g + 8 * n;
+        const uint32_t at = smem_u32(m < mt ? xw + m * 16 + tl : zero);
+        xe[n] = at + (m < mt ? (m & 1) * 64 : 0);
+        xo[n] = at - (m < mt ? (m & 1) * 64 : 0);
+        xu[n] = m < mt ? p.tokens * 256 : 0;
+    }
+    uint32_t magic;
+    asm volatile("mov.u32 %0, 0x64006400;" : "=r"(magic));
+    const uint32_t q_at = smem_u32(mine) + g * I4_ROW + tl * 16;
+    // unit u of the row (unit i of the chunk in buffer buf)
+    auto compute = [&](int buf, int i, int u) {
+        const uint4 qa = lds128(q_at + buf * I4_BUF + i * 64), qb = lds128(q_at + buf * I4_BUF + i * 64 + 8 * I4_ROW);
+        const float *ss = my_scales + buf * 16 * SC + g * SC + i * PER;
+        uint32_t q0[4] = {qa.x, qa.y, qa.z, qa.w}, q1[4] = {qb.x, qb.y, qb.z, qb.w};
         exchange<GROUP>(q0, tl);
         exchange<GROUP>(q1, tl);
+        uint32_t x0[NT], x1[NT];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
+        for (int n = 0; n < NT; ++n) {
+            x0[n] = xe[n] + u * xu[n];
+            x1[n] = xo[n] + u * xu[n];
+        }
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
             float c[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float2 b = *reinterpret_cast<const float2 *>(xs + (u * PER + i) * 8 * NT + n * 8 + 2 * tl);
-                c[n][0] = c[n][2] = b.x;
-                c[n][1] = c[n][3] = b.y;
-            }
-#pragma unroll
-            for (int j = i * JS; j < (i + 1) * JS; ++j) {
-                uint32_t a[4], b[4];
-                nibbles<T>(q0[j], a);
-                nibbles<T>(q1[j], b);
+            for (int j = k * JS; j < (k + 1) * JS; ++j) {
+                __half2 a[4], b[4];
+                nibbles(q0[j], magic, a);
+                nibbles(q1[j], magic, b);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                    if (g + 8 * n < mt) x = xw[((u * 4 + j) * p.tokens + g + 8 * n) * 4 + tl];
-                    mma16816<T>(c[n], a[0], b[0], a[1], b[1], x.x, x.y);
-                    mma16816<T>(c[n], a[2], b[2], a[3], b[3], x.z, x.w);
+                    const uint4 v = lds128((j & 1 ? x1[n] : x0[n]) + j * 64);
+                    mma16816(c[n], a[0], b[0], a[1], b[1], v.x, v.y, j == k * JS);
+                    mma16816(c[n], a[2], b[2], a[3], b[3], v.z, v.w, false);
                 }
             }
-            T h0, h1;
-            *reinterpret_cast<uint16_t *>(&h0) = o.s[0][i];
-            *reinterpret_cast<uint16_t *>(&h1) = o.s[1][i];
-            const float s0 = to_float(h0), s1 = to_float(h1);
+            const float s0 = ss[k], s1 = ss[k + 8 * SC];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 acc[n][0] = fmaf(s0, c[n][0], acc[n][0]);
@@ -257,58 +335,90 @@ __global__ void __launch_bounds__(I4_THREADS, 1) lce_int4_few_kernel(const Int4P
             }
         }
     };
-    // The KS warps' sums of a row block added up by one of them (each in its turn) and written. Two sets of
-    // places: a warp that is a row block ahead writes into the other.
-    int turn = 0;
     T *out = static_cast<T *>(p.out);
-    auto finish = [&](int rb) {
-        if (ks > 1) {
-            float4 *mine = part + ((turn & 1) * I4_WARPS + warp) * 32 * NT;
+    bool ok = true;
+    auto write = [&](const float (&a)[NT][4], int rb) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mine[n * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-            named_bar_sync(1 + rg, ks * 32);
-        }
-        if (ks == 1 || turn % ks == kw) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float4 s = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-                if (ks > 1) {
-                    const float4 *from = part + ((turn & 1) * I4_WARPS + rg * ks) * 32 * NT + n * 32 + lane;
-                    s = from[0];
-                    for (int k = 1; k < ks; ++k) {
-                        const float4 o = from[k * 32 * NT];
-                        s.x += o.x;
-                        s.y += o.y;
-                        s.z += o.z;
-                        s.w += o.w;
-                    }
+            for (int i = 0; i < 2; ++i) {
+                const int m = n * 8 + 2 * tl + i;
+                if (m < mt) {
+                    T *o = out + static_cast<long long>(m0 + m) * p.ldc + rb * 16ll + g;
+                    const float down = ok ? s_down[m] : NAN;   // (a wait for copies that ran out is not passed over)
+                    if (rb * 16 + g < p.V) o[0] = from_float<T>(a[n][i] * down);
+                    if (rb * 16 + g + 8 < p.V) o[8] = from_float<T>(a[n][i + 2] * down);
                 }
-                const float v[4] = {s.x, s.y, s.z, s.w};
+            }
+    };
+    const int c_begin = begin_of(warp);
+    int rb = b0 + c_begin / cpb, k = c_begin % cpb, buf = 0;
+    bool from_start = k == 0;   // the row block at hand was begun at its first chunk
+    uint32_t par = 0;
+    for (int c = c_begin; c < c_end; ++c) {
+        const uint32_t bar = smem_u32(&bars[warp][buf]);
+        if (!mbar_try_wait(bar, par)) {
+            const uint64_t t0 = global_timer_ns();
+            while (ok && !mbar_try_wait(bar, par)) ok = global_timer_ns() - t0 <= I4_WAIT_NS;
+            ok = __all_sync(0xffffffffu, ok);
+        }
+        __syncwarp();
+        const int n = units - k * I4_CHUNK;
+        if (n >= I4_CHUNK) {
+#pragma unroll
+            for (int i = 0; i < I4_CHUNK; ++i) compute(buf, i, k * I4_CHUNK + i);
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) compute(buf, i, k * I4_CHUNK + i);
+        }
+        __syncwarp();
+        keep_scales(buf ^ 1);      // (asked for a chunk ago)
+        fence_proxy_async_smem();
+        bring(buf);
+        __syncwarp();
+        buf ^= 1;
+        if (buf == 0) par ^= 1u;
+        if (++k == cpb) {
+            if (from_start) write(acc, rb);
+#pragma unroll
+            for (int n2 = 0; n2 < NT; ++n2)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int m = n * 8 + 2 * tl + (i & 1), row = rb * 16 + g + 8 * (i >> 1);
-                    if (m < mt && row < p.V) out[static_cast<long long>(m0 + m) * p.ldc + row] = from_float<T>(v[i]);
+                    if (!from_start) head[n2][i] = acc[n2][i];
+                    acc[n2][i] = 0.f;
                 }
-            }
+            k = 0;
+            ++rb;
+            from_start = true;
         }
-        ++turn;
-        clear();
-    };
-    int cb = blockIdx.x * rg_count + rg, cu = kw;   // (every warp has units: ks is at most a quarter of them)
-    while (cb < blocks) {
+    }
+    // Row blocks that were shared: the warp that began one adds up the others' parts, in order: what
+    // warps in the middle of it have (all theirs), then the end of it, which the last one began with.
+    __syncthreads();
+    float4 *part = reinterpret_cast<float4 *>(i4_smem);   // [warp][head, rest][NT][lane], over the buffers
 #pragma unroll
-        for (int i = 0; i < I4_AHEAD; ++i) {
-            if (cb < blocks) {
-                compute(ring[i], cu);
-                fetch(ring[i]);
-                cu += ks;
-                if (cu >= units) {
-                    finish(cb);
-                    cu = kw;
-                    cb += step;
+    for (int n = 0; n < NT; ++n) {
+        part[((warp * 2 + 0) * NT + n) * 32 + lane] = make_float4(head[n][0], head[n][1], head[n][2], head[n][3]);
+        part[((warp * 2 + 1) * NT + n) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+    }
+    __syncthreads();
+    if (c_begin < c_end && k > 0 && from_start) {
+        const int end = (rb - b0 + 1) * cpb;   // the row block's last chunk and one
+        for (int w = warp + 1; w < warps; ++w) {
+            const bool whole = begin_of(w + 1) < end;
+            if (begin_of(w) < begin_of(w + 1)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float4 o = part[((w * 2 + (whole ? 1 : 0)) * NT + n) * 32 + lane];
+                    acc[n][0] += o.x;
+                    acc[n][1] += o.y;
+                    acc[n][2] += o.z;
+                    acc[n][3] += o.w;
                 }
             }
+            if (!whole) break;
         }
+        write(acc, rb);
     }
 }
 
@@ -358,21 +468,24 @@ __global__ void __launch_bounds__(I4Q_THREADS) lce_int4_quantize_kernel(const In
         static_cast<S *>(p.scale)[row * p.lds + k0 / p.group] = from_float<S>(any ? NAN : s);
 }
 
-template <typename T, int GROUP> cudaError_t launch_few(const Int4Params &p, int nt, dim3 grid, size_t smem, cudaStream_t s) {
-    if (nt == 1) lce_int4_few_kernel<T, GROUP, 1><<<grid, I4_THREADS, smem, s>>>(p);
-    else lce_int4_few_kernel<T, GROUP, 2><<<grid, I4_THREADS, smem, s>>>(p);
+template <typename T, int GROUP>
+cudaError_t launch_few(const Int4Params &p, int nt, dim3 grid, int threads, size_t smem, cudaStream_t s) {
+    if (nt == 1) lce_int4_few_kernel<T, GROUP, 1><<<grid, threads, smem, s>>>(p);
+    else lce_int4_few_kernel<T, GROUP, 2><<<grid, threads, smem, s>>>(p);
     return cudaGetLastError();
 }
-template <typename T> cudaError_t launch_few_of(const Int4Params &p, int nt, dim3 grid, size_t smem, cudaStream_t s) {
-    return p.group == 128 ? launch_few<T, 128>(p, nt, grid, smem, s)
-           : p.group == 64 ? launch_few<T, 64>(p, nt, grid, smem, s) : launch_few<T, 32>(p, nt, grid, smem, s);
+template <typename T>
+cudaError_t launch_few_of(const Int4Params &p, int nt, dim3 grid, int threads, size_t smem, cudaStream_t s) {
+    return p.group == 128 ? launch_few<T, 128>(p, nt, grid, threads, smem, s)
+           : p.group == 64 ? launch_few<T, 64>(p, nt, grid, threads, smem, s)
+                           : launch_few<T, 32>(p, nt, grid, threads, smem, s);
 }
 
 constexpr int I4_MAX_SMEM = 220 * 1024;
 
-size_t few_smem(const Int4Params &p, int tokens, int nt) {
-    return static_cast<size_t>(p.units) * (256 * tokens + I4_UNIT / p.group * 32 * nt) + 2 * I4_WARPS * 32 * 16 * nt;
-}
+// Shared memory of x for so many tokens, and of a warp.
+size_t few_x_smem(const Int4Params &p, int tokens) { return 256 + static_cast<size_t>(p.units) * 256 * tokens; }
+size_t few_warp_smem(const Int4Params &p) { return 2 * I4_BUF + 2 * 16 * 4 * I4_CHUNK * (I4_UNIT / p.group); }
 
 template <typename T, int GROUP> cudaError_t set_few() {
     cudaError_t e = cudaFuncSetAttribute(lce_int4_few_kernel<T, GROUP, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -404,20 +517,21 @@ cudaError_t int4_set_attributes() {
 
 cudaError_t launch_int4(Int4Params p, int sms, cudaStream_t s) {
     p.units = (p.D + I4_UNIT - 1) / I4_UNIT;
-    // at least four units to a warp, up to eight warps to a row block
-    p.ks = 1;
-    while (p.ks < 8 && p.units >= 8 * p.ks) p.ks *= 2;
+    // as many tokens as leave room for 8 warps, as many warps as there is room for
+    const size_t ws = few_warp_smem(p);
     int tokens = p.M < 16 ? p.M : 16;
-    while (tokens > 1 && few_smem(p, tokens, tokens > 8 ? 2 : 1) > I4_MAX_SMEM) --tokens;
+    while (tokens > 1 && few_x_smem(p, tokens) + 8 * ws > I4_MAX_SMEM) --tokens;
+    const long long room = (static_cast<long long>(I4_MAX_SMEM) - static_cast<long long>(few_x_smem(p, tokens))) /
+                           static_cast<long long>(ws);
+    if (room < 1) return cudaErrorInvalidValue;
+    const int warps = room < I4_MAX_WARPS ? static_cast<int>(room) : I4_MAX_WARPS;
     const int nt = tokens > 8 ? 2 : 1;
     p.tokens = tokens;
-    const int blocks = (p.V + 15) / 16, per = I4_WARPS / p.ks;
-    const int gx = (blocks + per - 1) / per < sms ? (blocks + per - 1) / per : sms;
-    const dim3 grid(gx, (p.M + tokens - 1) / tokens);
-    const size_t smem = few_smem(p, tokens, nt);
-    if (smem > I4_MAX_SMEM) return cudaErrorInvalidValue;
-    return p.dtype == CE_FP16 ? launch_few_of<__half>(p, nt, grid, smem, s)
-                              : launch_few_of<__nv_bfloat16>(p, nt, grid, smem, s);
+    const int blocks = (p.V + 15) / 16;
+    const dim3 grid(blocks < sms ? blocks : sms, (p.M + tokens - 1) / tokens);
+    const size_t smem = few_x_smem(p, tokens) + warps * ws;
+    return p.dtype == CE_FP16 ? launch_few_of<__half>(p, nt, grid, warps * 32, smem, s)
+                              : launch_few_of<__nv_bfloat16>(p, nt, grid, warps * 32, smem, s);
 }
 
 cudaError_t launch_int4_quantize(const Int4QuantParams &p, cudaStream_t s) {

@@ -408,9 +408,9 @@ struct Int4Params {
     int M, V, D;
     void *out;                 // [M][ldc]
     long long ldc;
-    int units, ks, tokens;     // (set by the launcher)
+    int units, tokens;         // of 128 values; per CTA (set by the launcher)
 };
-constexpr long long I4_MAX_D = 65536;
+constexpr long long I4_MAX_D = 65536;   // (one token's values and a warp's buffers fit into shared memory)
 struct Int4QuantParams {
     const void *W;             // [V][ldw]
     long long ldw, V;

@@ -26,8 +26,8 @@ def values(w, d):
 
 
 def check(Z, X, W):
-    """Sums of d products and 24 times a group's x less: at most d + 64 roundings (to nearest or cut) of the
-    magnitudes that are summed, |x| * 39 * scale at most (q + 16 < 32, its bias 24); and one rounding to the type."""
+    """Sums of d products: at most d / 4 + 64 roundings (to nearest or cut) of the magnitudes that are
+    summed; and one rounding to the type."""
     x = X.double().cpu().numpy()
     want = x @ W.T
     d = x.shape[1]
