@@ -12,7 +12,7 @@ namespace lce {
 namespace {
 
 // ------------------------------------------------------------------ few tokens
-// Up to 16 tokens per CTA. Bound by reading the weight, so everything else has to fit into the
+// Up to 8 tokens per CTA. Bound by reading the weight, so everything else has to fit into the
 // time of its bytes: at the measured copy rate an SM gets 23 bytes, 47 weights, a cycle.
 //   * A warp takes 16 rows x 128 values (a unit) at a time as the A operand of eight m16n8k16 products, the
 //     tokens are the columns of B. Which of the unit's values a product calls its k-th does not
@@ -27,14 +27,18 @@ namespace {
 //   * Sums of a group are scaled in fp32 registers and added up over the groups.
 //   * A CTA has a range of row blocks, and of its chunks (16 rows x 4 units) each warp a range of its own, so all
 //     warps have the same to do whatever V and D are. Nothing holds them together: each brings its
-//     chunks by bulk copies (a row's 256 bytes each) into two buffers of its own. A row block that two or
+//     chunks by bulk copies (a row's 256 bytes each) into buffers of its own. A row block that two or
 //     more warps have parts of is added up at the end.
 // x lies in shared memory in the order in which lanes take it (one 16-byte load per word).
 
 constexpr int I4_UNIT = 128;         // values of k
-constexpr int I4_CHUNK = 4;          // units of a chunk
-constexpr int I4_ROW = I4_CHUNK * 64 + 64;        // bytes of a chunk's row in shared memory: rows g and g + 1 half a line apart
-constexpr int I4_BUF = 16 * I4_ROW;
+constexpr int I4_CHUNK = 8;          // units of a chunk
+constexpr int I4_RING = 2;           // chunks of a warp: one at hand, two under way
+// A chunk in shared memory: its even rows, then, half a line (64 bytes) further on than that, its odd rows:
+// the lanes of two rows read different banks.
+constexpr int I4_ROW = I4_CHUNK * 64;
+constexpr int I4_ODD = 8 * I4_ROW + 64;
+constexpr int I4_BUF = 16 * I4_ROW + 128;
 constexpr int I4_MAX_WARPS = 16;
 constexpr uint64_t I4_WAIT_NS = 2000000000ull;    // bound of a wait for copies (2 s)
 
@@ -55,9 +59,16 @@ __device__ __forceinline__ void nibbles(uint32_t w, uint32_t magic, __half2 (&o)
         o[2 * i + 1] = __hfma2(and_or<0x00f000f0u>(v, magic), sixteenth, off1);
     }
 }
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+template <int OFF> __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4 + %5];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr), "n"(OFF));
+    return v;
+}
+template <int OFF> __device__ __forceinline__ float lds32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1 + %2];" : "=f"(v) : "r"(addr), "n"(OFF));
     return v;
 }
 
@@ -65,7 +76,7 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 __device__ __forceinline__ void mma16816(float (&c)[4], __half2 a0, __half2 a1, __half2 a2, __half2 a3, uint32_t b0,
                                          uint32_t b1, bool first) {
     if (first) {
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                      "{%10, %10, %10, %10};"
                      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
                      : "r"(*reinterpret_cast<uint32_t *>(&a0)), "r"(*reinterpret_cast<uint32_t *>(&a1)),
@@ -73,7 +84,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], __half2 a0, __half2 a1, 
                        "r"(b1), "f"(0.f));
         return;
     }
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(*reinterpret_cast<uint32_t *>(&a0)), "r"(*reinterpret_cast<uint32_t *>(&a1)),
@@ -128,26 +139,26 @@ template <int GROUP> __device__ __forceinline__ void exchange(uint32_t (&u)[4], 
     }
 }
 
-template <typename T, int GROUP, int NT>
+template <typename T, int GROUP>
 __global__ void __launch_bounds__(I4_MAX_WARPS * 32, 1) lce_int4_few_kernel(const Int4Params p) {
     constexpr int PER = I4_UNIT / GROUP;     // groups of a unit
     constexpr int JS = 4 / PER;              // words of a lane per group
     constexpr int SC = I4_CHUNK * PER;       // scales of a chunk's row
     extern __shared__ __align__(128) uint8_t i4_smem[];
-    __shared__ float s_up[16], s_down[16];   // a token's power of two, and its inverse
-    __shared__ unsigned s_max[16];           // the bits of its largest finite magnitude
-    __shared__ __align__(8) uint64_t bars[I4_MAX_WARPS][2];
+    __shared__ float s_up[8], s_down[8];   // a token's power of two, and its inverse
+    __shared__ unsigned s_max[8];           // the bits of its largest finite magnitude
+    __shared__ __align__(8) uint64_t bars[I4_MAX_WARPS][I4_RING];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = lane >> 2, tl = lane & 3;
     const int threads = blockDim.x, warps = threads / 32;
     const int m0 = blockIdx.y * p.tokens;
     const int mt = p.M - m0 < p.tokens ? p.M - m0 : p.tokens;
     const int units = p.units;
-    // per warp: two chunks of the weight, two of scales (fp32 [16][SC]); then 256 bytes of zeros, and x as
+    // per warp: the ring's chunks of the weight, and of scales (fp32 [16][SC]); then 256 bytes of zeros, and x as
     // 16-byte pieces [unit][token][word][t], the words of odd tokens in the order 1 0 3 2 (two tokens' pieces
     // of a word lie half a line apart)
-    uint8_t *mine = i4_smem + warp * (2 * I4_BUF);
-    float *my_scales = reinterpret_cast<float *>(i4_smem + warps * (2 * I4_BUF)) + warp * (2 * 16 * SC);
-    uint4 *zero = reinterpret_cast<uint4 *>(i4_smem + warps * (2 * I4_BUF + 2 * 16 * SC * 4));
+    uint8_t *mine = i4_smem + warp * (I4_RING * I4_BUF);
+    float *my_scales = reinterpret_cast<float *>(i4_smem + warps * (I4_RING * I4_BUF)) + warp * (I4_RING * 16 * SC);
+    uint4 *zero = reinterpret_cast<uint4 *>(i4_smem + warps * (I4_RING * (I4_BUF + 16 * SC * 4)));
     uint4 *xw = zero + 16;
 
     const int blocks = (p.V + 15) / 16;
@@ -161,55 +172,69 @@ __global__ void __launch_bounds__(I4_MAX_WARPS * 32, 1) lce_int4_few_kernel(cons
     auto begin_of = [&](int w) -> int { return static_cast<int>(chunks * w / warps); };
     const int c_end = begin_of(warp + 1);
 
-    if (t < warps * 2) mbar_init(&bars[t / 2][t % 2], 1);
+    if (t < warps * I4_RING) mbar_init(&bars[t / I4_RING][t % I4_RING], 1);
     if (t < 16) {
         zero[t] = make_uint4(0u, 0u, 0u, 0u);
-        s_max[t] = 0u;
+        if (t < 8) s_max[t] = 0u;
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
 
-    // what is brought next: chunk nc, which is chunk `nk` of row block `nb`
+    // what is brought next: chunk nc, which is chunk `nk` of row block `nb`; where it lies, for the lane's row (of
+    // 16) and scales
+    constexpr int NS = (16 * SC + 31) / 32;
     int nc = begin_of(warp), nb = b0 + nc / cpb, nk = nc % cpb;
-    float sc[(16 * SC + 31) / 32];           // the scales that were asked for last
+    const uint8_t *src = nullptr;
+    const T *sp[NS];
+    float sc[NS];           // the scales that were asked for last
+    auto rows_at = [&]() {
+        const int row = nb * 16 + (lane & 15) < p.V ? nb * 16 + (lane & 15) : p.V - 1;
+        src = p.q + static_cast<long long>(row) * p.ldq + nk * (I4_CHUNK * 64);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int e = i * 32 + lane, r = nb * 16 + e / SC < p.V ? nb * 16 + e / SC : p.V - 1;
+            sp[i] = static_cast<const T *>(p.scale) + static_cast<long long>(r) * p.lds + nk * SC + e % SC;
+        }
+    };
+    rows_at();
+    const uint32_t bar0 = smem_u32(&bars[warp][0]), to0 = smem_u32(mine) + (lane & 15) / 2 * I4_ROW + (lane & 1) * I4_ODD;
     auto bring = [&](int buf) {
         if (nc >= c_end) return;
-        const int at = nk * (I4_CHUNK * 64);
-        const int bytes = row_bytes - at < I4_CHUNK * 64 ? row_bytes - at : I4_CHUNK * 64;
-        uint64_t *bar = &bars[warp][buf];
-        if (lane == 0) mbar_arrive_expect_tx(bar, 16 * bytes);
+        const int left = row_bytes - nk * (I4_CHUNK * 64);
+        const int bytes = left < I4_CHUNK * 64 ? left : I4_CHUNK * 64;
+        if (lane == 0) mbar_arrive_expect_tx(&bars[warp][buf], 16 * bytes);
         __syncwarp();
-        if (lane < 16) {
-            const int row = nb * 16 + lane < p.V ? nb * 16 + lane : p.V - 1;
-            const uint8_t *src = p.q + static_cast<long long>(row) * p.ldq + at;
+        if (lane < 16)
             asm volatile(
                 "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                    smem_u32(mine + buf * I4_BUF + lane * I4_ROW)),
-                "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                    to0 + buf * I4_BUF),
+                "l"(src), "r"(bytes), "r"(bar0 + buf * 8)
                 : "memory");
-        }
+        src += I4_CHUNK * 64;
+        const int ahead = groups - nk * SC;   // groups from this chunk on
 #pragma unroll
-        for (int i = 0; i < (16 * SC + 31) / 32; ++i) {
-            const int e = i * 32 + lane, r = e / SC, k = nk * SC + e % SC;
-            const int row = nb * 16 + r < p.V ? nb * 16 + r : p.V - 1;
+        for (int i = 0; i < NS; ++i) {
             sc[i] = 0.f;
-            if (16 * SC % 32 == 0 || e < 16 * SC)
-                if (k < groups) sc[i] = to_float(static_cast<const T *>(p.scale)[static_cast<long long>(row) * p.lds + k]);
+            if ((i * 32 + lane) % SC < ahead && (16 * SC % 32 == 0 || i * 32 + lane < 16 * SC)) sc[i] = to_float(*sp[i]);
+            sp[i] += SC;
         }
         ++nc;
         if (++nk == cpb) {
             nk = 0;
             ++nb;
+            rows_at();
         }
     };
     auto keep_scales = [&](int buf) {
 #pragma unroll
-        for (int i = 0; i < (16 * SC + 31) / 32; ++i)
+        for (int i = 0; i < NS; ++i)
             if (16 * SC % 32 == 0 || i * 32 + lane < 16 * SC) my_scales[buf * 16 * SC + i * 32 + lane] = sc[i];
     };
-    bring(0);
-    keep_scales(0);
-    bring(1);
+#pragma unroll
+    for (int i = 0; i < I4_RING; ++i) {
+        bring(i);
+        if (i + 1 < I4_RING) keep_scales(i);
+    }
 
     // x into shared memory, beside the first loads
     const T *X = static_cast<const T *>(p.X) + static_cast<long long>(m0) * p.ldx;
@@ -245,7 +270,7 @@ __global__ void __launch_bounds__(I4_MAX_WARPS * 32, 1) lce_int4_few_kernel(cons
             s_up[t] = ldexpf(1.f, up);
             s_down[t] = ldexpf(1.f, -up);
         }
-    } else if (t < 16) {
+    } else if (t < 8) {
         s_up[t] = s_down[t] = 1.f;
     }
     __syncthreads();
@@ -277,79 +302,52 @@ __global__ void __launch_bounds__(I4_MAX_WARPS * 32, 1) lce_int4_few_kernel(cons
     }
     __syncthreads();
 
-    float acc[NT][4], head[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] = head[n][i] = 0.f;
-    // a lane's pieces of x for each 8 tokens: where its even and its odd words are counted from (their order
-    // goes by the token), and the step to the next unit's; lanes of no token read zeros
-    uint32_t xe[NT], xo[NT];
-    int xu[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int m = g + 8 * n;
-        const uint32_t at = smem_u32(m < mt ? xw + m * 16 + tl : zero);
-        xe[n] = at + (m < mt ? (m & 1) * 64 : 0);
-        xo[n] = at - (m < mt ? (m & 1) * 64 : 0);
-        xu[n] = m < mt ? p.tokens * 256 : 0;
-    }
+    float acc[4] = {}, head[4] = {};
+    // a lane's pieces of x: where its even and its odd words are counted from (their order goes by the
+    // token), and the step to the next unit's; lanes of no token read zeros
+    const uint32_t x_at = smem_u32(g < mt ? xw + g * 16 + tl : zero);
+    const uint32_t swap = g < mt ? (g & 1) * 64 : 0, xu = g < mt ? p.tokens * 256 : 0;
     uint32_t magic;
     asm volatile("mov.u32 %0, 0x64006400;" : "=r"(magic));
-    const uint32_t q_at = smem_u32(mine) + g * I4_ROW + tl * 16;
-    // unit u of the row (unit i of the chunk in buffer buf)
-    auto compute = [&](int buf, int i, int u) {
-        const uint4 qa = lds128(q_at + buf * I4_BUF + i * 64), qb = lds128(q_at + buf * I4_BUF + i * 64 + 8 * I4_ROW);
-        const float *ss = my_scales + buf * 16 * SC + g * SC + i * PER;
+    const uint32_t q_at = smem_u32(mine) + g / 2 * I4_ROW + (g & 1) * I4_ODD + tl * 16, s_at = smem_u32(my_scales) + g * (SC * 4);
+    // a unit: its rows at qs, its scales at ss, its x at x0 (even words) and x1 (odd words)
+    auto compute = [&](uint32_t qs, uint32_t ss, uint32_t x0, uint32_t x1) {
+        const uint4 qa = lds128<0>(qs), qb = lds128<4 * I4_ROW>(qs);
         uint32_t q0[4] = {qa.x, qa.y, qa.z, qa.w}, q1[4] = {qb.x, qb.y, qb.z, qb.w};
         exchange<GROUP>(q0, tl);
         exchange<GROUP>(q1, tl);
-        uint32_t x0[NT], x1[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            x0[n] = xe[n] + u * xu[n];
-            x1[n] = xo[n] + u * xu[n];
-        }
+        const uint4 x[4] = {lds128<0>(x0), lds128<64>(x1), lds128<128>(x0), lds128<192>(x1)};
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
-            float c[NT][4];
+            float c[4], d[4];   // (two chains of products, half as long)
 #pragma unroll
             for (int j = k * JS; j < (k + 1) * JS; ++j) {
                 __half2 a[4], b[4];
                 nibbles(q0[j], magic, a);
                 nibbles(q1[j], magic, b);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint4 v = lds128((j & 1 ? x1[n] : x0[n]) + j * 64);
-                    mma16816(c[n], a[0], b[0], a[1], b[1], v.x, v.y, j == k * JS);
-                    mma16816(c[n], a[2], b[2], a[3], b[3], v.z, v.w, false);
-                }
+                mma16816(c, a[0], b[0], a[1], b[1], x[j].x, x[j].y, j == k * JS);
+                mma16816(d, a[2], b[2], a[3], b[3], x[j].z, x[j].w, j == k * JS);
             }
-            const float s0 = ss[k], s1 = ss[k + 8 * SC];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                acc[n][0] = fmaf(s0, c[n][0], acc[n][0]);
-                acc[n][1] = fmaf(s0, c[n][1], acc[n][1]);
-                acc[n][2] = fmaf(s1, c[n][2], acc[n][2]);
-                acc[n][3] = fmaf(s1, c[n][3], acc[n][3]);
-            }
+            const float s0 = lds32<0>(ss + k * 4), s1 = lds32<8 * SC * 4>(ss + k * 4);
+            acc[0] = fmaf(s0, c[0] + d[0], acc[0]);
+            acc[1] = fmaf(s0, c[1] + d[1], acc[1]);
+            acc[2] = fmaf(s1, c[2] + d[2], acc[2]);
+            acc[3] = fmaf(s1, c[3] + d[3], acc[3]);
         }
     };
     T *out = static_cast<T *>(p.out);
     bool ok = true;
-    auto write = [&](const float (&a)[NT][4], int rb) {
+    auto write = [&](int rb) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int m = n * 8 + 2 * tl + i;
-                if (m < mt) {
-                    T *o = out + static_cast<long long>(m0 + m) * p.ldc + rb * 16ll + g;
-                    const float down = ok ? s_down[m] : NAN;   // (a wait for copies that ran out is not passed over)
-                    if (rb * 16 + g < p.V) o[0] = from_float<T>(a[n][i] * down);
-                    if (rb * 16 + g + 8 < p.V) o[8] = from_float<T>(a[n][i + 2] * down);
-                }
+        for (int i = 0; i < 2; ++i) {
+            const int m = 2 * tl + i;
+            if (m < mt) {
+                T *o = out + static_cast<long long>(m0 + m) * p.ldc + rb * 16ll + g;
+                const float down = ok ? s_down[m] : NAN;   // (a wait for copies that ran out is not passed over)
+                if (rb * 16 + g < p.V) o[0] = from_float<T>(acc[i] * down);
+                if (rb * 16 + g + 8 < p.V) o[8] = from_float<T>(acc[i + 2] * down);
             }
+        }
     };
     const int c_begin = begin_of(warp);
     int rb = b0 + c_begin / cpb, k = c_begin % cpb, buf = 0;
@@ -364,29 +362,31 @@ __global__ void __launch_bounds__(I4_MAX_WARPS * 32, 1) lce_int4_few_kernel(cons
         }
         __syncwarp();
         const int n = units - k * I4_CHUNK;
+        uint32_t qs = q_at + buf * I4_BUF, ss = s_at + buf * (16 * SC * 4);
+        uint32_t x0 = x_at + k * I4_CHUNK * xu + swap, x1 = x0 - 2 * swap;
         if (n >= I4_CHUNK) {
 #pragma unroll
-            for (int i = 0; i < I4_CHUNK; ++i) compute(buf, i, k * I4_CHUNK + i);
+            for (int i = 0; i < I4_CHUNK; ++i) compute(qs + i * 64, ss + i * (PER * 4), x0 + i * xu, x1 + i * xu);
         } else {
 #pragma unroll 1
-            for (int i = 0; i < n; ++i) compute(buf, i, k * I4_CHUNK + i);
+            for (int i = 0; i < n; ++i) compute(qs + i * 64, ss + i * (PER * 4), x0 + i * xu, x1 + i * xu);
         }
         __syncwarp();
-        keep_scales(buf ^ 1);      // (asked for a chunk ago)
+        keep_scales(buf == 0 ? I4_RING - 1 : buf - 1);      // (asked for a chunk ago)
         fence_proxy_async_smem();
         bring(buf);
         __syncwarp();
-        buf ^= 1;
-        if (buf == 0) par ^= 1u;
+        if (++buf == I4_RING) {
+            buf = 0;
+            par ^= 1u;
+        }
         if (++k == cpb) {
-            if (from_start) write(acc, rb);
+            if (from_start) write(rb);
 #pragma unroll
-            for (int n2 = 0; n2 < NT; ++n2)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (!from_start) head[n2][i] = acc[n2][i];
-                    acc[n2][i] = 0.f;
-                }
+            for (int i = 0; i < 4; ++i) {
+                if (!from_start) head[i] = acc[i];
+                acc[i] = 0.f;
+            }
             k = 0;
             ++rb;
             from_start = true;
@@ -395,30 +395,24 @@ __global__ void __launch_bounds__(I4_MAX_WARPS * 32, 1) lce_int4_few_kernel(cons
     // Row blocks that were shared: the warp that began one adds up the others' parts, in order: what
     // warps in the middle of it have (all theirs), then the end of it, which the last one began with.
     __syncthreads();
-    float4 *part = reinterpret_cast<float4 *>(i4_smem);   // [warp][head, rest][NT][lane], over the buffers
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        part[((warp * 2 + 0) * NT + n) * 32 + lane] = make_float4(head[n][0], head[n][1], head[n][2], head[n][3]);
-        part[((warp * 2 + 1) * NT + n) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-    }
+    float4 *part = reinterpret_cast<float4 *>(i4_smem);   // [warp][head, rest][lane], over the buffers
+    part[(warp * 2 + 0) * 32 + lane] = make_float4(head[0], head[1], head[2], head[3]);
+    part[(warp * 2 + 1) * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     __syncthreads();
     if (c_begin < c_end && k > 0 && from_start) {
         const int end = (rb - b0 + 1) * cpb;   // the row block's last chunk and one
         for (int w = warp + 1; w < warps; ++w) {
             const bool whole = begin_of(w + 1) < end;
             if (begin_of(w) < begin_of(w + 1)) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float4 o = part[((w * 2 + (whole ? 1 : 0)) * NT + n) * 32 + lane];
-                    acc[n][0] += o.x;
-                    acc[n][1] += o.y;
-                    acc[n][2] += o.z;
-                    acc[n][3] += o.w;
-                }
+                const float4 o = part[(w * 2 + (whole ? 1 : 0)) * 32 + lane];
+                acc[0] += o.x;
+                acc[1] += o.y;
+                acc[2] += o.z;
+                acc[3] += o.w;
             }
             if (!whole) break;
         }
-        write(acc, rb);
+        write(rb);
     }
 }
 
@@ -468,30 +462,22 @@ __global__ void __launch_bounds__(I4Q_THREADS) lce_int4_quantize_kernel(const In
         static_cast<S *>(p.scale)[row * p.lds + k0 / p.group] = from_float<S>(any ? NAN : s);
 }
 
-template <typename T, int GROUP>
-cudaError_t launch_few(const Int4Params &p, int nt, dim3 grid, int threads, size_t smem, cudaStream_t s) {
-    if (nt == 1) lce_int4_few_kernel<T, GROUP, 1><<<grid, threads, smem, s>>>(p);
-    else lce_int4_few_kernel<T, GROUP, 2><<<grid, threads, smem, s>>>(p);
-    return cudaGetLastError();
-}
 template <typename T>
-cudaError_t launch_few_of(const Int4Params &p, int nt, dim3 grid, int threads, size_t smem, cudaStream_t s) {
-    return p.group == 128 ? launch_few<T, 128>(p, nt, grid, threads, smem, s)
-           : p.group == 64 ? launch_few<T, 64>(p, nt, grid, threads, smem, s)
-                           : launch_few<T, 32>(p, nt, grid, threads, smem, s);
+cudaError_t launch_few_of(const Int4Params &p, dim3 grid, int threads, size_t smem, cudaStream_t s) {
+    if (p.group == 128) lce_int4_few_kernel<T, 128><<<grid, threads, smem, s>>>(p);
+    else if (p.group == 64) lce_int4_few_kernel<T, 64><<<grid, threads, smem, s>>>(p);
+    else lce_int4_few_kernel<T, 32><<<grid, threads, smem, s>>>(p);
+    return cudaGetLastError();
 }
 
 constexpr int I4_MAX_SMEM = 220 * 1024;
 
 // Shared memory of x for so many tokens, and of a warp.
 size_t few_x_smem(const Int4Params &p, int tokens) { return 256 + static_cast<size_t>(p.units) * 256 * tokens; }
-size_t few_warp_smem(const Int4Params &p) { return 2 * I4_BUF + 2 * 16 * 4 * I4_CHUNK * (I4_UNIT / p.group); }
+size_t few_warp_smem(const Int4Params &p) { return I4_RING * (I4_BUF + 16 * 4 * I4_CHUNK * (I4_UNIT / p.group)); }
 
 template <typename T, int GROUP> cudaError_t set_few() {
-    cudaError_t e = cudaFuncSetAttribute(lce_int4_few_kernel<T, GROUP, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         I4_MAX_SMEM);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(lce_int4_few_kernel<T, GROUP, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, I4_MAX_SMEM);
+    return cudaFuncSetAttribute(lce_int4_few_kernel<T, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, I4_MAX_SMEM);
 }
 
 template <typename W> cudaError_t launch_quant(const Int4QuantParams &p, cudaStream_t s) {
@@ -519,19 +505,18 @@ cudaError_t launch_int4(Int4Params p, int sms, cudaStream_t s) {
     p.units = (p.D + I4_UNIT - 1) / I4_UNIT;
     // as many tokens as leave room for 8 warps, as many warps as there is room for
     const size_t ws = few_warp_smem(p);
-    int tokens = p.M < 16 ? p.M : 16;
+    int tokens = p.M < 8 ? p.M : 8;
     while (tokens > 1 && few_x_smem(p, tokens) + 8 * ws > I4_MAX_SMEM) --tokens;
     const long long room = (static_cast<long long>(I4_MAX_SMEM) - static_cast<long long>(few_x_smem(p, tokens))) /
                            static_cast<long long>(ws);
     if (room < 1) return cudaErrorInvalidValue;
     const int warps = room < I4_MAX_WARPS ? static_cast<int>(room) : I4_MAX_WARPS;
-    const int nt = tokens > 8 ? 2 : 1;
     p.tokens = tokens;
     const int blocks = (p.V + 15) / 16;
     const dim3 grid(blocks < sms ? blocks : sms, (p.M + tokens - 1) / tokens);
     const size_t smem = few_x_smem(p, tokens) + warps * ws;
-    return p.dtype == CE_FP16 ? launch_few_of<__half>(p, nt, grid, warps * 32, smem, s)
-                              : launch_few_of<__nv_bfloat16>(p, nt, grid, warps * 32, smem, s);
+    return p.dtype == CE_FP16 ? launch_few_of<__half>(p, grid, warps * 32, smem, s)
+                              : launch_few_of<__nv_bfloat16>(p, grid, warps * 32, smem, s);
 }
 
 cudaError_t launch_int4_quantize(const Int4QuantParams &p, cudaStream_t s) {
