@@ -61,6 +61,6 @@ from .fp8 import (  # noqa: F401
     fp8_weight,
     quantize_fp8,
 )
-from .int4 import Int4Weight, int4_linear, int4_weight  # noqa: F401
+from .int4 import Int4Weight, int4_linear, int4_weight, int4_workspace_size  # noqa: F401
 from .sampling import sample_logits  # noqa: F401
 from .sharded import sharded_fwd_bwd  # noqa: F401

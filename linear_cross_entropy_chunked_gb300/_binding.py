@@ -65,6 +65,7 @@ EXPORTED = (
     "lce_preference_logits",
     "lce_scale",
     "lce_int4_quantize",
+    "lce_int4_linear_workspace_size",
     "lce_int4_linear",
     "lce_sample_logits",
     "lce_fp8_quantize",
@@ -177,7 +178,9 @@ def lib() -> ctypes.CDLL:
     L.lce_preference_logits.argtypes = [_vp, _i, _i64, _vp, _vp, _i64, _vp, _f, _f, _i, _vp, _i64, _i64, _i64, _i,
                                         _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
     L.lce_int4_quantize.argtypes = [_vp, _i, _i64, _i64, _i64, _i, _vp, _i64, _vp, _i, _i64, _vp]
-    L.lce_int4_linear.argtypes = [_vp, _i, _i64, _vp, _i64, _vp, _i64, _i, _i64, _i64, _i64, _vp, _i64, _vp]
+    L.lce_int4_linear.argtypes = [_vp, _i, _i64, _vp, _i64, _vp, _i64, _i, _i64, _i64, _i64, _vp, _i64, _vp,
+                                  ctypes.c_size_t, _vp]
+    L.lce_int4_linear_workspace_size.argtypes = [_i64, _i64, _sz]
     L.lce_scale.argtypes = [_vp, _i, _vp, _i64, _vp, _i, _vp]
     L.lce_sample_logits.argtypes = [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _f,
                                     ctypes.c_int32, _f, _f, _vp, _vp, _vp]
@@ -222,7 +225,7 @@ def lib() -> ctypes.CDLL:
                  "lce_policy_forward", "lce_policy_fwd_bwd", "lce_policy_logits",
                  "lce_preference_workspace_size", "lce_preference_fwd_bwd",
                  "lce_preference_logits_workspace_size", "lce_preference_logits", "lce_scale", "lce_int4_quantize",
-                 "lce_int4_linear"):
+                 "lce_int4_linear_workspace_size", "lce_int4_linear"):
         getattr(L, name).restype = ctypes.c_int
     _LIB = L
     return L

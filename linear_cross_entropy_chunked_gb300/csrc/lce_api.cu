@@ -232,7 +232,8 @@ enum MapType { MAP_BF16, MAP_F16, MAP_F32, MAP_U8 };
 // operand tiles and of the epilogue staging boxes; zero fill out of bounds on
 // loads, clipping on stores.
 bool encode_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
-                const uint64_t *strides_bytes, const uint32_t *box, MapType type) {
+                const uint64_t *strides_bytes, const uint32_t *box, MapType type,
+                CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     cuuint64_t d[3];
     cuuint64_t st[2];
     cuuint32_t bx[3];
@@ -248,7 +249,7 @@ bool encode_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims
                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     CUresult r = g_encode(m, dt,
                           rank, const_cast<void *>(base), d, st, bx, es,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
@@ -2232,39 +2233,86 @@ lce_status lce_int4_quantize(const void *W, int w_dtype, int64_t ldw, int64_t V,
     return LCE_OK;
 }
 
+// (the tokens' layout; with few tokens none is needed, but a caller's one buffer may serve any number)
+lce_status lce_int4_linear_workspace_size(int64_t M, int64_t D, size_t *bytes) {
+    if (!bytes || M < 0 || M > (1ll << 20) || D <= 0 || D > I4_MAX_D) return LCE_ERR_INVALID_ARG;
+    *bytes = 1024 + align_up(4 * static_cast<size_t>(M > 0 ? M : 1), 1024) +
+             static_cast<size_t>(M) * static_cast<size_t>(cdiv(D, 128)) * 256;
+    return LCE_OK;
+}
+
 lce_status lce_int4_linear(const void *X, int x_dtype, int64_t ldx, const void *q, int64_t ldq, const void *scale,
                            int64_t lds, int group, int64_t M, int64_t V, int64_t D, void *out, int64_t ldc,
-                           lce_stream_t stream) {
+                           void *ws, size_t ws_bytes, lce_stream_t stream) {
     g_launches = 0;
     if (x_dtype != CE_BF16 && x_dtype != CE_FP16) return LCE_ERR_INVALID_ARG;
     if (group != 32 && group != 64 && group != 128) return LCE_ERR_INVALID_ARG;
     if (M < 0 || M > (1ll << 20) || V <= 0 || V > MAX_V || D <= 0 || D > I4_MAX_D || ldx < D || ldc < V ||
         ldq < (D + 31) / 32 * 16 || lds < cdiv(D, group))
         return LCE_ERR_INVALID_ARG;
-    if (!q || !scale || (M > 0 && (!X || !out))) return LCE_ERR_INVALID_ARG;
+    if (!q || !scale || !ws || (M > 0 && (!X || !out))) return LCE_ERR_INVALID_ARG;
     const uintptr_t halves = reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(scale) |
                              reinterpret_cast<uintptr_t>(out);
-    if (ldq % 16 || !aligned16(q) || halves % 2) return LCE_ERR_ALIGNMENT;
+    if (ldq % 16 || !aligned16(q) || halves % 2 || !aligned16(ws)) return LCE_ERR_ALIGNMENT;
+    size_t need = 0;
+    lce_int4_linear_workspace_size(M, D, &need);
+    if (ws_bytes < need) return LCE_ERR_WORKSPACE;
     int sms = 0, pairs = 0;
     LCE_TRY(init_device(&sms, &pairs));
     if (M == 0) return LCE_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    Int4Params p;
-    p.X = X;
-    p.ldx = ldx;
-    p.dtype = x_dtype;
-    p.x_vec = aligned16(X) && ldx % 8 == 0;
-    p.q = static_cast<const uint8_t *>(q);
-    p.ldq = ldq;
+    const int x_vec = aligned16(X) && ldx % 8 == 0;
+    const char *force = getenv("LCE_I4");
+    if (M <= 8 && !(force && force[0] == 't')) {
+        Int4Params p;
+        p.X = X;
+        p.ldx = ldx;
+        p.dtype = x_dtype;
+        p.x_vec = x_vec;
+        p.q = static_cast<const uint8_t *>(q);
+        p.ldq = ldq;
+        p.scale = scale;
+        p.lds = lds;
+        p.group = group;
+        p.M = static_cast<int>(M);
+        p.V = static_cast<int>(V);
+        p.D = static_cast<int>(D);
+        p.out = out;
+        p.ldc = ldc;
+        LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_int4(p, sms, s));
+        return LCE_OK;
+    }
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    Int4TileParams p;
+    memset(&p, 0, sizeof(p));
+    const int n = int4_tile_tokens(M);
     p.scale = scale;
     p.lds = lds;
-    p.group = group;
+    p.hdr = reinterpret_cast<int *>(w);
+    p.down = reinterpret_cast<float *>(w + 1024);
+    void *tokens = w + 1024 + align_up(4 * static_cast<size_t>(M), 1024);
+    p.out = out;
+    p.ldc = ldc;
+    p.dtype = x_dtype;
     p.M = static_cast<int>(M);
     p.V = static_cast<int>(V);
     p.D = static_cast<int>(D);
-    p.out = out;
-    p.ldc = ldc;
-    LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_int4(p, sms, s));
+    p.units = static_cast<int>(cdiv(D, 128));
+    p.groups = static_cast<int>(cdiv(D, group));
+    p.per = 128 / group;
+    p.row_tiles = static_cast<int>(cdiv(V, 128));
+    p.token_tiles = static_cast<int>(cdiv(M, n));
+    if (static_cast<long long>(p.row_tiles) * p.token_tiles > 0x7fffffffll) return LCE_ERR_INVALID_ARG;
+    p.timeout_ns = kDefaultTimeoutNs;
+    const uint64_t dims[2] = {static_cast<uint64_t>((D + 31) / 32 * 16), static_cast<uint64_t>(V)};
+    const uint64_t st[1] = {static_cast<uint64_t>(ldq)};
+    const uint32_t box[2] = {64, 128};
+    if (!encode_map(&p.tmQ, q, 2, dims, st, box, MAP_U8, CU_TENSOR_MAP_SWIZZLE_64B)) return LCE_ERR_CUDA;
+    if (!encode_2d(&p.tmX, tokens, static_cast<uint64_t>(p.units) * 128, M, static_cast<uint64_t>(p.units) * 256, 64,
+                   static_cast<uint32_t>(n), MAP_F16))
+        return LCE_ERR_CUDA;
+    LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_int4_tokens(p, X, ldx, x_vec, tokens, s));
+    LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_int4_tiles(p, n, sms, s));
     return LCE_OK;
 }
 

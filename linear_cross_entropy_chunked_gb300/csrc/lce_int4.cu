@@ -416,6 +416,392 @@ __global__ void __launch_bounds__(I4_MAX_WARPS * 32, 1) lce_int4_few_kernel(cons
     }
 }
 
+// ------------------------------------------------------------------ tokens on the 5th-generation tensor cores
+// A CTA takes 128 rows of the weight (the A operand, in TMEM) times N tokens (B, in shared memory) over all of
+// D, 128 values of k a stage:
+//   * a producer warp brings the stage's packed rows (8 KB, 64-byte swizzle) and the tokens' values
+//     (two boxes of 64 x N fp16) by TMA;
+//   * two groups of four warps take turns at turning a stage into fp16 q - 8: a thread has a row, whose 64
+//     bytes become 64 TMEM columns (as above; the k order within eight is that of a word's nibble pairs,
+//     and the tokens were laid out in that order before);
+//   * one warp issues the products: those of a group of k into a TMEM buffer of its own;
+//   * eight warps read each group's sums (a thread has a row and half of the tokens), scale them by the
+//     row's scale of that group and add them up in fp32 registers.
+// TMEM: columns 0-255 the sums' buffers, 256-511 four stages of A. Bound by the weight's bytes for few tokens, by
+// the turning of the weight (about 1.1 operations a value) from some 64 on.
+
+constexpr int I4T_THREADS = 18 * 32;    // 8 warps of sums, 8 of values, the producer, the MMA warp
+constexpr int I4T_Q = 8192;             // bytes of a stage's packed rows
+constexpr int I4T_MAX_STAGES = 16;
+constexpr int I4T_ASLOTS = 4;
+constexpr int I4T_MAX_BUFS = 8;
+constexpr int I4T_PRODUCER = 16, I4T_MMA = 17;
+
+__device__ __forceinline__ void umma_f16_ta(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// 32 columns of the warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
+// NH: tokens of a thread (half of the tile's N); PER: groups of a stage.
+template <int NH, int PER>
+__global__ void __launch_bounds__(I4T_THREADS, 1) lce_int4_kernel(const __grid_constant__ Int4TileParams p) {
+    constexpr int N = 2 * NH;
+    constexpr int DCOLS = N <= 32 ? 32 : N <= 64 ? 64 : 128;
+    constexpr int BUFS = 256 / DCOLS;
+    constexpr int STAGE = I4T_Q + N * 256;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full_bar[I4T_MAX_STAGES];    // a stage's bytes landed
+    // a stage's products have ended: its bytes (its rows were turned before) and its values' TMEM are free, and with
+    // one group a stage its sums are there. (A stage comes around later than its TMEM slot or buffer, so
+    // no phase can be missed.)
+    __shared__ __align__(8) uint64_t done_bar[I4T_MAX_STAGES];
+    __shared__ __align__(8) uint64_t afull_bar[I4T_ASLOTS];       // its values are in TMEM
+    __shared__ __align__(8) uint64_t dfull_bar[I4T_MAX_BUFS];     // a group's sums are there (PER > 1)
+    __shared__ __align__(8) uint64_t dempty_bar[I4T_MAX_BUFS];
+    __shared__ __align__(8) uint64_t drain_bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort_flag;
+
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nstages = p.stages;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < nstages; ++i) {
+            mbar_init(&full_bar[i], 1);
+            mbar_init(&done_bar[i], 1);
+        }
+        for (int i = 0; i < I4T_ASLOTS; ++i) mbar_init(&afull_bar[i], 4);
+        for (int i = 0; i < BUFS; ++i) {
+            mbar_init(&dfull_bar[i], 1);
+            mbar_init(&dempty_bar[i], 8);
+        }
+        mbar_init(&drain_bar, 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == I4T_PRODUCER && lane == 0) {
+        prefetch_tmap(&p.tmQ);
+        prefetch_tmap(&p.tmX);
+    }
+    if (warp == I4T_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    Abort ab;
+    ab.flag_smem = &abort_flag;
+    ab.hdr = p.hdr;
+    ab.limit_ns = p.timeout_ns;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // (the tokens' layout has been written)
+
+    const int items = p.row_tiles * p.token_tiles, nk = p.units;
+    if (warp == I4T_PRODUCER) {
+        if (lane == 0) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 1;
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < items; t += gridDim.x) {
+                const int row0 = t / p.token_tiles * 128, m0 = t % p.token_tiles * N;
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!mbar_wait(&done_bar[stage], phase, ab)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *to = smem + stage * STAGE;
+                    mbar_arrive_expect_tx(&full_bar[stage], STAGE);
+                    tma_load_2d(to, &p.tmQ, &full_bar[stage], kb * 64, row0);
+                    tma_load_2d(to + I4T_Q, &p.tmX, &full_bar[stage], kb * 128, m0);
+                    tma_load_2d(to + I4T_Q + N * 128, &p.tmX, &full_bar[stage], kb * 128 + 64, m0);
+                    ++issued;
+                    if (++stage == nstages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) {
+                // the copies still in flight end (bounded) before the shared memory is given back
+                const int n = issued < nstages ? issued : nstages;
+                for (int j = issued - n; j < issued; ++j)
+                    mbar_wait_drain(&full_bar[j % nstages], static_cast<uint32_t>((j / nstages) & 1), 50000000ull);
+            }
+        }
+    } else if (warp == I4T_MMA) {
+        // (the whole warp goes along; one lane issues)
+        int stage = 0, slot = 0, buf = 0;
+        uint32_t phase = 0, sphase = 0, bphase = 1;
+        bool ok = true, any = false;
+        // D fp32, A and B fp16, both K-major
+        constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+        constexpr int STEPS = 8 / PER;   // products of a group
+        for (int t = blockIdx.x; ok && t < items; t += gridDim.x) {
+            for (int kb = 0; kb < nk; ++kb) {
+                const uint64_t bd = sdesc(smem_u32(smem + stage * STAGE + I4T_Q), 16u, 1024u);
+                const uint32_t a = tmem + 256 + slot * 64;
+                ok = mbar_wait(&full_bar[stage], phase, ab) && mbar_wait(&afull_bar[slot], sphase, ab);
+#pragma unroll
+                for (int g = 0; g < PER; ++g) {
+                    const uint32_t d = tmem + buf * DCOLS;
+                    ok = __all_sync(0xffffffffu, ok && mbar_wait(&dempty_bar[buf], bphase, ab));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = g * STEPS; k < (g + 1) * STEPS; ++k)
+                            umma_f16_ta(d, a + k * 8, bd + static_cast<uint64_t>(k / 4 * (N * 128 / 16) + k % 4 * 2),
+                                        idesc, k > g * STEPS ? 1u : 0u);
+                        if constexpr (PER > 1) umma_commit(&dfull_bar[buf]);
+                        if (g + 1 == PER) umma_commit(&done_bar[stage]);
+                    }
+                    __syncwarp();
+                    any = true;
+                    if (++buf == BUFS) {
+                        buf = 0;
+                        bphase ^= 1;
+                    }
+                }
+                if (!ok) break;
+                if (++stage == nstages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+                if (++slot == I4T_ASLOTS) {
+                    slot = 0;
+                    sphase ^= 1;
+                }
+            }
+        }
+        if (any) {   // every product has ended before TMEM is given back
+            if (elect_one()) umma_commit(&drain_bar);
+            __syncwarp();
+            mbar_wait_drain(&drain_bar, 0, 50000000ull);
+        }
+    } else if (warp >= 8) {
+        // values: this group's stages are every second one
+        const int mine = (warp - 8) >> 2, row = (warp & 3) * 32 + lane;
+        uint32_t magic;
+        asm volatile("mov.u32 %0, 0x64006400;" : "=r"(magic));
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        int it = 0, stage = 0, slot = 0, old = nstages - I4T_ASLOTS;   // old: the stage that had the slot before
+        uint32_t phase = 0, ophase = 1;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < items; t += gridDim.x) {
+            for (int kb = 0; kb < nk; ++kb, ++it) {
+                if ((it & 1) == mine) {
+                    ok = mbar_wait(&full_bar[stage], phase, ab) &&
+                         (it < I4T_ASLOTS || mbar_wait(&done_bar[old], ophase, ab));
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint32_t at = smem_u32(smem + stage * STAGE) + row * 64;
+                    const uint32_t turn = (row >> 1 & 3) << 4;
+                    uint4 q[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) q[c] = lds128<0>(at + ((c << 4) ^ turn));
+                    tc_fence_after();
+                    const uint32_t to = tmem + 256 + slot * 64 + lane_base;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[32];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            __half2 v[4];
+                            nibbles((&q[2 * h + j / 4].x)[j % 4], magic, v);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) r[4 * j + i] = *reinterpret_cast<uint32_t *>(&v[i]);
+                        }
+                        tmem_st32(to + h * 32, r);
+                    }
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&afull_bar[slot]);
+                }
+                if (++stage == nstages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+                if (++slot == I4T_ASLOTS) slot = 0;
+                if (++old == nstages) {
+                    old = 0;
+                    ophase ^= 1;
+                }
+            }
+        }
+    } else {
+        // sums
+        const int half = warp >> 2, row_in = (warp & 3) * 32 + lane;
+        const uint32_t at0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * NH;
+        // (with one group a stage the stages' barriers say that its sums are there)
+        int buf = 0, at_bar = 0;
+        uint32_t bphase = 0;
+        const int nbars = PER == 1 ? nstages : BUFS;
+        uint64_t *bars = PER == 1 ? done_bar : dfull_bar;
+        bool ok = true;
+        const int groups = p.groups;
+        for (int t = blockIdx.x; ok && t < items; t += gridDim.x) {
+            const int row = t / p.token_tiles * 128 + row_in, m0 = t % p.token_tiles * N + half * NH;
+            const uint16_t *sp = static_cast<const uint16_t *>(p.scale) +
+                                 static_cast<long long>(row < p.V ? row : p.V - 1) * p.lds;
+            float2 acc[NH / 2];
+#pragma unroll
+            for (int j = 0; j < NH / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+            // scales four groups ahead
+            uint16_t ahead[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ahead[i] = sp[i < groups ? i : groups - 1];
+            const int all = nk * PER;
+            for (int g0 = 0; ok && g0 < all; g0 += 4) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int g = g0 + i;
+                    if (g < all && ok) {
+                        const uint16_t bits = ahead[i];
+                        ahead[i] = sp[g + 4 < groups ? g + 4 : groups - 1];
+                        const float s = p.dtype == CE_FP16 ? __half2float(__ushort_as_half(bits))
+                                                           : __uint_as_float(static_cast<uint32_t>(bits) << 16);
+                        ok = __all_sync(0xffffffffu, mbar_wait(&bars[at_bar], bphase, ab));
+                        if (ok) {
+                            tc_fence_after();
+                            const float2 s2 = g < groups ? make_float2(s, s) : make_float2(0.f, 0.f);
+#pragma unroll
+                            for (int c = 0; c < NH; c += 24) {
+                                constexpr int MOST = 24;
+                                uint32_t v[MOST];
+#pragma unroll
+                                for (int j = 0; j < MOST; j += 8)
+                                    if (c + j < NH) tmem_ld8(at0 + buf * DCOLS + c + j, v + j);
+                                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                                for (int j = 0; j < MOST; ++j) asm volatile("" : "+r"(v[j]));
+                                if (c + MOST >= NH) {
+                                    tc_fence_before();
+                                    __syncwarp();
+                                    if (lane == 0) mbar_arrive(&dempty_bar[buf]);
+                                }
+#pragma unroll
+                                for (int j = 0; j < MOST; j += 2)
+                                    if (c + j < NH)
+                                        acc[(c + j) / 2] = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
+                                                                      s2, acc[(c + j) / 2]);
+                            }
+                            if (++buf == BUFS) buf = 0;
+                            if (++at_bar == nbars) {
+                                at_bar = 0;
+                                bphase ^= 1;
+                            }
+                        }
+                    }
+                }
+            }
+            if (row < p.V && ok) {
+                uint16_t *out = static_cast<uint16_t *>(p.out) + row;
+#pragma unroll
+                for (int j = 0; j < NH; ++j)
+                    if (m0 + j < p.M) {
+                        const float v = (j & 1 ? acc[j / 2].y : acc[j / 2].x) * p.down[m0 + j];
+                        out[static_cast<long long>(m0 + j) * p.ldc] =
+                            p.dtype == CE_FP16 ? __half_as_ushort(__float2half_rn(v))
+                                               : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+                    }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == I4T_MMA) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+    }
+}
+
+// The tokens for it: a CTA per token; fp16 (bf16 brought below 2^15 by a power of two), eight values in the order 0 4 1
+// 5 2 6 3 7, rows filled up with zeros to whole units.
+constexpr int I4X_THREADS = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(I4X_THREADS) lce_int4_tokens_kernel(const Int4TileParams p, const T *X, long long ldx,
+                                                                      int x_vec, uint4 *to) {
+    __shared__ unsigned s_max;
+    const int t = threadIdx.x, m = blockIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (m == 0 && t < HDR_COUNTERS) p.hdr[t] = 0;
+    const uint16_t *src = reinterpret_cast<const uint16_t *>(X + m * ldx);
+    auto load = [&](int k, uint16_t (&v)[8]) {
+        if (x_vec && k + 8 <= p.D) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(src + k);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = static_cast<uint16_t>((&q.x)[e / 2] >> (16 * (e & 1)));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = k + e < p.D ? src[k + e] : static_cast<uint16_t>(0);
+        }
+    };
+    float up = 1.f, down = 1.f;
+    if (std::is_same<T, __nv_bfloat16>::value) {
+        if (t == 0) s_max = 0u;
+        __syncthreads();
+        uint32_t most = 0u;   // (finite bf16 magnitudes order as their bits do)
+        for (int k = t * 8; k < p.D; k += I4X_THREADS * 8) {
+            uint16_t v[8];
+            load(k, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t a = v[e] & 0x7fffu;
+                if (a < 0x7f80u && a > most) most = a;
+            }
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        if ((t & 31) == 0) atomicMax(&s_max, most);
+        __syncthreads();
+        const float a = __uint_as_float(s_max << 16);
+        int e = 0;
+        if (a > 0.f) {
+            frexpf(a, &e);   // a < 2^e
+            e = 15 - e < 120 ? 15 - e : 120;
+        }
+        up = ldexpf(1.f, e);
+        down = ldexpf(1.f, -e);
+    }
+    if (t == 0) p.down[m] = down;
+    for (int i = t; i < p.units * 16; i += I4X_THREADS) {
+        uint16_t v[8];
+        load(i * 8, v);
+        if (std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = __half_as_ushort(__float2half_rn(__uint_as_float(static_cast<uint32_t>(v[e]) << 16) * up));
+        }
+        to[static_cast<long long>(m) * p.units * 16 + i] =
+            make_uint4(v[0] | (v[4] << 16), v[1] | (v[5] << 16), v[2] | (v[6] << 16), v[3] | (v[7] << 16));
+    }
+}
+
 // ------------------------------------------------------------------ quantisation
 // A warp per row and 256 values: a lane's eight values, the maximum over the lanes of a group.
 
@@ -480,6 +866,21 @@ template <typename T, int GROUP> cudaError_t set_few() {
     return cudaFuncSetAttribute(lce_int4_few_kernel<T, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, I4_MAX_SMEM);
 }
 
+template <int NH, int PER> cudaError_t set_tile() {
+    return cudaFuncSetAttribute(lce_int4_kernel<NH, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, I4_MAX_SMEM);
+}
+template <int NH> cudaError_t set_tiles() {
+    cudaError_t e;
+    if ((e = set_tile<NH, 1>()) != cudaSuccess) return e;
+    if ((e = set_tile<NH, 2>()) != cudaSuccess) return e;
+    return set_tile<NH, 4>();
+}
+template <int NH> cudaError_t launch_tiles_of(const cudaLaunchConfig_t &cfg, const Int4TileParams &p) {
+    return p.per == 1   ? cudaLaunchKernelEx(&cfg, lce_int4_kernel<NH, 1>, p)
+           : p.per == 2 ? cudaLaunchKernelEx(&cfg, lce_int4_kernel<NH, 2>, p)
+                        : cudaLaunchKernelEx(&cfg, lce_int4_kernel<NH, 4>, p);
+}
+
 template <typename W> cudaError_t launch_quant(const Int4QuantParams &p, cudaStream_t s) {
     const long long tasks = p.V * ((p.D + 255ll) / 256);
     const long long blocks = (tasks + I4Q_THREADS / 32 - 1) / (I4Q_THREADS / 32);
@@ -498,7 +899,12 @@ cudaError_t int4_set_attributes() {
     if ((e = set_few<__nv_bfloat16, 32>()) != cudaSuccess) return e;
     if ((e = set_few<__half, 128>()) != cudaSuccess) return e;
     if ((e = set_few<__half, 64>()) != cudaSuccess) return e;
-    return set_few<__half, 32>();
+    if ((e = set_few<__half, 32>()) != cudaSuccess) return e;
+    if ((e = set_tiles<8>()) != cudaSuccess) return e;
+    if ((e = set_tiles<16>()) != cudaSuccess) return e;
+    if ((e = set_tiles<24>()) != cudaSuccess) return e;
+    if ((e = set_tiles<32>()) != cudaSuccess) return e;
+    return set_tiles<48>();
 }
 
 cudaError_t launch_int4(Int4Params p, int sms, cudaStream_t s) {
@@ -517,6 +923,44 @@ cudaError_t launch_int4(Int4Params p, int sms, cudaStream_t s) {
     const size_t smem = few_x_smem(p, tokens) + warps * ws;
     return p.dtype == CE_FP16 ? launch_few_of<__half>(p, grid, warps * 32, smem, s)
                               : launch_few_of<__nv_bfloat16>(p, grid, warps * 32, smem, s);
+}
+
+// Tokens of a tile for M of them, and tiles.
+int int4_tile_tokens(long long M) {
+    const long long tiles = (M + 95) / 96, n = (M + tiles - 1) / tiles;
+    return n <= 16 ? 16 : n <= 32 ? 32 : n <= 48 ? 48 : n <= 64 ? 64 : 96;
+}
+
+cudaError_t launch_int4_tokens(const Int4TileParams &p, const void *X, long long ldx, int x_vec, void *to, cudaStream_t s) {
+    if (p.dtype == CE_FP16)
+        lce_int4_tokens_kernel<__half><<<p.M, I4X_THREADS, 0, s>>>(p, static_cast<const __half *>(X), ldx, x_vec, static_cast<uint4 *>(to));
+    else
+        lce_int4_tokens_kernel<__nv_bfloat16><<<p.M, I4X_THREADS, 0, s>>>(p, static_cast<const __nv_bfloat16 *>(X), ldx, x_vec,
+                                                                         static_cast<uint4 *>(to));
+    return cudaGetLastError();
+}
+
+cudaError_t launch_int4_tiles(Int4TileParams p, int n, int sms, cudaStream_t s) {
+    const int stage = I4T_Q + n * 256;
+    p.stages = (I4_MAX_SMEM - 1024) / stage < I4T_MAX_STAGES ? (I4_MAX_SMEM - 1024) / stage : I4T_MAX_STAGES;
+    const int items = p.row_tiles * p.token_tiles;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(items < sms ? items : sms);
+    cfg.blockDim = dim3(I4T_THREADS);
+    cfg.dynamicSmemBytes = I4_MAX_SMEM;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    switch (n) {
+        case 16: return launch_tiles_of<8>(cfg, p);
+        case 32: return launch_tiles_of<16>(cfg, p);
+        case 48: return launch_tiles_of<24>(cfg, p);
+        case 64: return launch_tiles_of<32>(cfg, p);
+        default: return launch_tiles_of<48>(cfg, p);
+    }
 }
 
 cudaError_t launch_int4_quantize(const Int4QuantParams &p, cudaStream_t s) {

@@ -410,6 +410,21 @@ struct Int4Params {
     long long ldc;
     int units, tokens;         // of 128 values; per CTA (set by the launcher)
 };
+// The same on tcgen05: A the weight's rows, B the tokens as launch_int4_tokens lays them out.
+struct Int4TileParams {
+    CUtensorMap tmQ;           // [V][row bytes] packed rows, boxes of 64 bytes x 128 rows
+    CUtensorMap tmX;           // [M][128 units] fp16, boxes of 64 x N
+    const void *scale;         // [V][lds]
+    long long lds;
+    float *down;               // [M]: what a token's sums are multiplied by
+    void *out;
+    long long ldc;
+    int dtype, M, V, D, units, groups;
+    int per;                   // groups of a unit
+    int row_tiles, token_tiles, stages;
+    int *hdr;
+    unsigned long long timeout_ns;
+};
 constexpr long long I4_MAX_D = 65536;   // (one token's values and a warp's buffers fit into shared memory)
 struct Int4QuantParams {
     const void *W;             // [V][ldw]
@@ -506,6 +521,9 @@ cudaError_t launch_grad_scale(const ClipItem *items, int n, const ClipScale &c, 
 
 cudaError_t int4_set_attributes();
 cudaError_t launch_int4(Int4Params p, int sms, cudaStream_t s);
+int int4_tile_tokens(long long M);
+cudaError_t launch_int4_tokens(const Int4TileParams &p, const void *X, long long ldx, int x_vec, void *to, cudaStream_t s);
+cudaError_t launch_int4_tiles(Int4TileParams p, int n, int sms, cudaStream_t s);
 cudaError_t launch_int4_quantize(const Int4QuantParams &p, cudaStream_t s);
 
 cudaError_t fp8_set_attributes();

@@ -2,6 +2,7 @@
 (lce_int4_quantize, lce_int4_linear). Argument marshalling only."""
 from __future__ import annotations
 
+import ctypes
 from typing import NamedTuple
 
 import torch
@@ -46,6 +47,13 @@ def int4_weight(W, group: int = 128, scale_dtype=None, stream=None) -> Int4Weigh
     return Int4Weight(q[:, :(D + 1) // 2], scale, group)
 
 
+def int4_workspace_size(M, D):
+    """Bytes of a workspace for int4_linear of M tokens of D values."""
+    out = ctypes.c_size_t(0)
+    _b._check(_b.lib().lce_int4_linear_workspace_size(M, D, ctypes.byref(out)), "lce_int4_linear_workspace_size")
+    return out.value
+
+
 def _check_weight(w, X):
     """(V, row stride of q in bytes, row stride of the scales)."""
     D = X.shape[1]
@@ -72,11 +80,13 @@ def _check_weight(w, X):
     return V, ldq, lds
 
 
-def int4_linear(X, w: Int4Weight, out=None, stream=None):
+def int4_linear(X, w: Int4Weight, out=None, ws=None, stream=None):
     """X W^T for the hidden states X [M, D] (bf16 or fp16, unit column stride, any row stride) and a weight in 4
     bits with scales of X's dtype: logits [M, V] in X's dtype, sums in fp32, rounded once. Fastest for few
     tokens, where it reads a quarter of a 16-bit weight's bytes. The logits' row stride is V rounded up to 16 bytes.
-    out: where to write them (unit column stride). No gradients: X may not require one."""
+    out: where to write them (unit column stride). ws: a uint8 tensor of int4_workspace_size(M, D) bytes, whose
+    device status read_status returns; calls that may run at the same time need one each. No gradients: X may not
+    require one."""
     ldx = _check_dense_rows("X", X, _HALVES, "bfloat16 or float16")
     if not isinstance(w, Int4Weight):
         raise TypeError("w must be an Int4Weight (int4_weight)")
@@ -92,10 +102,16 @@ def int4_linear(X, w: Int4Weight, out=None, stream=None):
             raise ValueError("out may not require a gradient")
     with _b._on(X.device, stream) as s:
         Z = _empty_out(M, V, X.dtype, X.device) if out is None else out
+        nbytes = int4_workspace_size(M, D)
+        if ws is None:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=X.device)
+        elif ws.device != X.device or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < nbytes \
+                or ws.data_ptr() % 16:
+            raise ValueError(f"ws must be a contiguous, 16-byte aligned uint8 tensor of at least {nbytes} bytes")
         if M:
             _b._check(_b.lib().lce_int4_linear(
                 X.data_ptr(), _b._CE_DTYPES[X.dtype], ldx, w.q.data_ptr(), ldq, w.scale.data_ptr(), lds, w.group, M,
-                V, D, Z.data_ptr(), Z.stride(0) if M > 1 else V, s), "lce_int4_linear")
+                V, D, Z.data_ptr(), Z.stride(0) if M > 1 else V, ws.data_ptr(), ws.numel(), s), "lce_int4_linear")
     if out is not None:
         _b._wrote((out,))
     return Z
