@@ -232,8 +232,7 @@ enum MapType { MAP_BF16, MAP_F16, MAP_F32, MAP_U8 };
 // operand tiles and of the epilogue staging boxes; zero fill out of bounds on
 // loads, clipping on stores.
 bool encode_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
-                const uint64_t *strides_bytes, const uint32_t *box, MapType type,
-                CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+                const uint64_t *strides_bytes, const uint32_t *box, MapType type) {
     cuuint64_t d[3];
     cuuint64_t st[2];
     cuuint32_t bx[3];
@@ -249,7 +248,7 @@ bool encode_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims
                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     CUresult r = g_encode(m, dt,
                           rank, const_cast<void *>(base), d, st, bx, es,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
@@ -2306,8 +2305,8 @@ lce_status lce_int4_linear(const void *X, int x_dtype, int64_t ldx, const void *
     p.timeout_ns = kDefaultTimeoutNs;
     const uint64_t dims[2] = {static_cast<uint64_t>((D + 31) / 32 * 16), static_cast<uint64_t>(V)};
     const uint64_t st[1] = {static_cast<uint64_t>(ldq)};
-    const uint32_t box[2] = {64, 128};
-    if (!encode_map(&p.tmQ, q, 2, dims, st, box, MAP_U8, CU_TENSOR_MAP_SWIZZLE_64B)) return LCE_ERR_CUDA;
+    const uint32_t box[2] = {128, 128};
+    if (!encode_map(&p.tmQ, q, 2, dims, st, box, MAP_U8)) return LCE_ERR_CUDA;
     if (!encode_2d(&p.tmX, tokens, static_cast<uint64_t>(p.units) * 128, M, static_cast<uint64_t>(p.units) * 256, 64,
                    static_cast<uint32_t>(n), MAP_F16))
         return LCE_ERR_CUDA;

@@ -418,23 +418,23 @@ __global__ void __launch_bounds__(I4_MAX_WARPS * 32, 1) lce_int4_few_kernel(cons
 
 // ------------------------------------------------------------------ tokens on the 5th-generation tensor cores
 // A CTA takes 128 rows of the weight (the A operand, in TMEM) times N tokens (B, in shared memory) over all of
-// D, 128 values of k a stage:
-//   * a producer warp brings the stage's packed rows (8 KB, 64-byte swizzle) and the tokens' values
-//     (two boxes of 64 x N fp16) by TMA;
-//   * two groups of four warps take turns at turning a stage into fp16 q - 8: a thread has a row, whose 64
+// D, 256 values of k a stage:
+//   * a producer warp brings the stage's packed rows (16 KB, 128-byte swizzle) and the tokens' values
+//     (four boxes of 64 x N fp16) by TMA;
+//   * two groups of four warps turn a half of the stage each into fp16 q - 8: a thread has a row, whose 64
 //     bytes become 64 TMEM columns (as above; the k order within eight is that of a word's nibble pairs,
 //     and the tokens were laid out in that order before);
 //   * one warp issues the products: those of a group of k into a TMEM buffer of its own;
-//   * eight warps read each group's sums (a thread has a row and half of the tokens), scale them by the
+//   * eight warps read the groups' sums (a thread has a row and half of the tokens), scale them by the
 //     row's scale of that group and add them up in fp32 registers.
-// TMEM: columns 0-255 the sums' buffers, 256-511 four stages of A. Bound by the weight's bytes for few tokens, by
-// the turning of the weight (about 1.1 operations a value) from some 64 on.
+// TMEM: columns 0-255 the sums' buffers, in two sets that are handed over as a whole, 256-511 two stages of A.
+// A product of 128 x N x 16 takes some 50 cycles up to N = 96, so for few tokens a stage's sixteen take a little
+// longer than its bytes (measured rates: 850 and 700 cycles). What the issuing warp does per stage
+// counts: with 128 values a stage and every barrier of its own, 16 tokens of 4096 x 128256 took 172 us.
 
 constexpr int I4T_THREADS = 18 * 32;    // 8 warps of sums, 8 of values, the producer, the MMA warp
-constexpr int I4T_Q = 8192;             // bytes of a stage's packed rows
-constexpr int I4T_MAX_STAGES = 16;
-constexpr int I4T_ASLOTS = 4;
-constexpr int I4T_MAX_BUFS = 8;
+constexpr int I4T_Q = 16384;            // bytes of a stage's packed rows
+constexpr int I4T_MAX_STAGES = 9;
 constexpr int I4T_PRODUCER = 16, I4T_MMA = 17;
 
 __device__ __forceinline__ void umma_f16_ta(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -462,22 +462,22 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *r) {
                  : "r"(taddr));
 }
 
-// NH: tokens of a thread (half of the tile's N); PER: groups of a stage.
+// NH: tokens of a thread (half of the tile's N); PER: groups of 128 values.
 template <int NH, int PER>
 __global__ void __launch_bounds__(I4T_THREADS, 1) lce_int4_kernel(const __grid_constant__ Int4TileParams p) {
     constexpr int N = 2 * NH;
     constexpr int DCOLS = N <= 32 ? 32 : N <= 64 ? 64 : 128;
-    constexpr int BUFS = 256 / DCOLS;
-    constexpr int STAGE = I4T_Q + N * 256;
+    constexpr int GROUPS = 2 * PER;                              // of a stage
+    constexpr int STEPS = 16 / GROUPS;                           // products of a group
+    constexpr int SET = GROUPS < 128 / DCOLS ? GROUPS : 128 / DCOLS;   // buffers that are handed over together
+    constexpr int SETS = GROUPS / SET;                           // of a stage
+    constexpr int STAGE = I4T_Q + N * 512;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[I4T_MAX_STAGES];    // a stage's bytes landed
-    // a stage's products have ended: its bytes (its rows were turned before) and its values' TMEM are free, and with
-    // one group a stage its sums are there. (A stage comes around later than its TMEM slot or buffer, so
-    // no phase can be missed.)
-    __shared__ __align__(8) uint64_t done_bar[I4T_MAX_STAGES];
-    __shared__ __align__(8) uint64_t afull_bar[I4T_ASLOTS];       // its values are in TMEM
-    __shared__ __align__(8) uint64_t dfull_bar[I4T_MAX_BUFS];     // a group's sums are there (PER > 1)
-    __shared__ __align__(8) uint64_t dempty_bar[I4T_MAX_BUFS];
+    __shared__ __align__(8) uint64_t done_bar[I4T_MAX_STAGES];    // its products have ended: its bytes and its A are free
+    __shared__ __align__(8) uint64_t afull_bar[2];                // its values are in TMEM
+    __shared__ __align__(8) uint64_t dfull_bar[2];                // a set's sums are there
+    __shared__ __align__(8) uint64_t dempty_bar[2];
     __shared__ __align__(8) uint64_t drain_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
@@ -491,8 +491,8 @@ __global__ void __launch_bounds__(I4T_THREADS, 1) lce_int4_kernel(const __grid_c
             mbar_init(&full_bar[i], 1);
             mbar_init(&done_bar[i], 1);
         }
-        for (int i = 0; i < I4T_ASLOTS; ++i) mbar_init(&afull_bar[i], 4);
-        for (int i = 0; i < BUFS; ++i) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&afull_bar[i], 8);
             mbar_init(&dfull_bar[i], 1);
             mbar_init(&dempty_bar[i], 8);
         }
@@ -520,7 +520,9 @@ __global__ void __launch_bounds__(I4T_THREADS, 1) lce_int4_kernel(const __grid_c
     ab.limit_ns = p.timeout_ns;
     asm volatile("griddepcontrol.wait;" ::: "memory");   // (the tokens' layout has been written)
 
-    const int items = p.row_tiles * p.token_tiles, nk = p.units;
+    const int items = p.row_tiles * p.token_tiles, nk = (p.units + 1) / 2;
+    const int mine = static_cast<int>(blockIdx.x) < items ? (items - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1 : 0;
+    const int total = mine * nk;   // stages of this CTA
     if (warp == I4T_PRODUCER) {
         if (lane == 0) {
             int stage = 0, issued = 0;
@@ -535,9 +537,10 @@ __global__ void __launch_bounds__(I4T_THREADS, 1) lce_int4_kernel(const __grid_c
                     }
                     uint8_t *to = smem + stage * STAGE;
                     mbar_arrive_expect_tx(&full_bar[stage], STAGE);
-                    tma_load_2d(to, &p.tmQ, &full_bar[stage], kb * 64, row0);
-                    tma_load_2d(to + I4T_Q, &p.tmX, &full_bar[stage], kb * 128, m0);
-                    tma_load_2d(to + I4T_Q + N * 128, &p.tmX, &full_bar[stage], kb * 128 + 64, m0);
+                    tma_load_2d(to, &p.tmQ, &full_bar[stage], kb * 128, row0);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        tma_load_2d(to + I4T_Q + b * (N * 128), &p.tmX, &full_bar[stage], kb * 256 + b * 64, m0);
                     ++issued;
                     if (++stage == nstages) {
                         stage = 0;
@@ -554,48 +557,47 @@ __global__ void __launch_bounds__(I4T_THREADS, 1) lce_int4_kernel(const __grid_c
         }
     } else if (warp == I4T_MMA) {
         // (the whole warp goes along; one lane issues)
-        int stage = 0, slot = 0, buf = 0;
-        uint32_t phase = 0, sphase = 0, bphase = 1;
+        int stage = 0;
+        uint32_t phase = 0, aphase = 0, dphase = 1;   // (a set's phase: sets alternate, so both flip every second one)
         bool ok = true, any = false;
         // D fp32, A and B fp16, both K-major
         constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
-        constexpr int STEPS = 8 / PER;   // products of a group
-        for (int t = blockIdx.x; ok && t < items; t += gridDim.x) {
-            for (int kb = 0; kb < nk; ++kb) {
-                const uint64_t bd = sdesc(smem_u32(smem + stage * STAGE + I4T_Q), 16u, 1024u);
-                const uint32_t a = tmem + 256 + slot * 64;
-                ok = mbar_wait(&full_bar[stage], phase, ab) && mbar_wait(&afull_bar[slot], sphase, ab);
+        int half = 0, set = 0;
+        for (int it = 0; it < total; ++it) {
+            const uint64_t bd = sdesc(smem_u32(smem + stage * STAGE + I4T_Q), 16u, 1024u);
+            const uint32_t a = tmem + 256 + half * 128;
+            ok = mbar_wait(&full_bar[stage], phase, ab) && mbar_wait(&afull_bar[half], aphase, ab);
 #pragma unroll
-                for (int g = 0; g < PER; ++g) {
-                    const uint32_t d = tmem + buf * DCOLS;
-                    ok = __all_sync(0xffffffffu, ok && mbar_wait(&dempty_bar[buf], bphase, ab));
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = g * STEPS; k < (g + 1) * STEPS; ++k)
-                            umma_f16_ta(d, a + k * 8, bd + static_cast<uint64_t>(k / 4 * (N * 128 / 16) + k % 4 * 2),
-                                        idesc, k > g * STEPS ? 1u : 0u);
-                        if constexpr (PER > 1) umma_commit(&dfull_bar[buf]);
-                        if (g + 1 == PER) umma_commit(&done_bar[stage]);
-                    }
-                    __syncwarp();
-                    any = true;
-                    if (++buf == BUFS) {
-                        buf = 0;
-                        bphase ^= 1;
-                    }
-                }
+            for (int c = 0; c < SETS; ++c) {
+                const uint32_t d = tmem + set * 128;
+                ok = __all_sync(0xffffffffu, ok && mbar_wait(&dempty_bar[set], dphase, ab));
                 if (!ok) break;
-                if (++stage == nstages) {
-                    stage = 0;
-                    phase ^= 1;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int g = 0; g < SET; ++g)
+#pragma unroll
+                        for (int j = 0; j < STEPS; ++j) {
+                            const int k = (c * SET + g) * STEPS + j;   // of the stage's sixteen
+                            umma_f16_ta(d + g * DCOLS, a + k * 8,
+                                        bd + static_cast<uint64_t>(k / 4 * (N * 128 / 16) + k % 4 * 2), idesc,
+                                        j ? 1u : 0u);
+                        }
+                    umma_commit(&dfull_bar[set]);
+                    if (c + 1 == SETS) umma_commit(&done_bar[stage]);
                 }
-                if (++slot == I4T_ASLOTS) {
-                    slot = 0;
-                    sphase ^= 1;
-                }
+                __syncwarp();
+                any = true;
+                set ^= 1;
+                if (set == 0) dphase ^= 1;
             }
+            if (!ok) break;
+            if (++stage == nstages) {
+                stage = 0;
+                phase ^= 1;
+            }
+            half ^= 1;
+            if (half == 0) aphase ^= 1;
         }
         if (any) {   // every product has ended before TMEM is given back
             if (elect_one()) umma_commit(&drain_bar);
@@ -603,65 +605,55 @@ __global__ void __launch_bounds__(I4T_THREADS, 1) lce_int4_kernel(const __grid_c
             mbar_wait_drain(&drain_bar, 0, 50000000ull);
         }
     } else if (warp >= 8) {
-        // values: this group's stages are every second one
-        const int mine = (warp - 8) >> 2, row = (warp & 3) * 32 + lane;
+        // values: this group's half of every stage
+        const int unit = (warp - 8) >> 2, row = (warp & 3) * 32 + lane;
         uint32_t magic;
         asm volatile("mov.u32 %0, 0x64006400;" : "=r"(magic));
-        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        int it = 0, stage = 0, slot = 0, old = nstages - I4T_ASLOTS;   // old: the stage that had the slot before
+        const uint32_t to0 = tmem + 256 + unit * 64 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        int stage = 0, old = nstages - 2, half = 0;   // old: the stage that had this half of A before
         uint32_t phase = 0, ophase = 1;
-        bool ok = true;
-        for (int t = blockIdx.x; ok && t < items; t += gridDim.x) {
-            for (int kb = 0; kb < nk; ++kb, ++it) {
-                if ((it & 1) == mine) {
-                    ok = mbar_wait(&full_bar[stage], phase, ab) &&
-                         (it < I4T_ASLOTS || mbar_wait(&done_bar[old], ophase, ab));
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    const uint32_t at = smem_u32(smem + stage * STAGE) + row * 64;
-                    const uint32_t turn = (row >> 1 & 3) << 4;
-                    uint4 q[4];
+        for (int it = 0; it < total; ++it) {
+            bool ok = mbar_wait(&full_bar[stage], phase, ab) && (it < 2 || mbar_wait(&done_bar[old], ophase, ab));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint32_t at = smem_u32(smem + stage * STAGE) + row * 128;
+            const uint32_t turn = (row & 7) << 4;
+            uint4 q[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) q[c] = lds128<0>(at + ((c << 4) ^ turn));
-                    tc_fence_after();
-                    const uint32_t to = tmem + 256 + slot * 64 + lane_base;
+            for (int c = 0; c < 4; ++c) q[c] = lds128<0>(at + (((unit * 4 + c) << 4) ^ turn));
+            tc_fence_after();
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t r[32];
+            for (int h = 0; h < 2; ++h) {
+                uint32_t r[32];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            __half2 v[4];
-                            nibbles((&q[2 * h + j / 4].x)[j % 4], magic, v);
+                for (int j = 0; j < 8; ++j) {
+                    __half2 v[4];
+                    nibbles((&q[2 * h + j / 4].x)[j % 4], magic, v);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) r[4 * j + i] = *reinterpret_cast<uint32_t *>(&v[i]);
-                        }
-                        tmem_st32(to + h * 32, r);
-                    }
-                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&afull_bar[slot]);
+                    for (int i = 0; i < 4; ++i) r[4 * j + i] = *reinterpret_cast<uint32_t *>(&v[i]);
                 }
-                if (++stage == nstages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-                if (++slot == I4T_ASLOTS) slot = 0;
-                if (++old == nstages) {
-                    old = 0;
-                    ophase ^= 1;
-                }
+                tmem_st32(to0 + half * 128 + h * 32, r);
             }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&afull_bar[half]);
+            if (++stage == nstages) {
+                stage = 0;
+                phase ^= 1;
+            }
+            if (++old == nstages) {
+                old = 0;
+                ophase ^= 1;
+            }
+            half ^= 1;
         }
     } else {
         // sums
         const int half = warp >> 2, row_in = (warp & 3) * 32 + lane;
         const uint32_t at0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * NH;
-        // (with one group a stage the stages' barriers say that its sums are there)
-        int buf = 0, at_bar = 0;
-        uint32_t bphase = 0;
-        const int nbars = PER == 1 ? nstages : BUFS;
-        uint64_t *bars = PER == 1 ? done_bar : dfull_bar;
+        int set = 0;
+        uint32_t dphase = 0;
         bool ok = true;
         const int groups = p.groups;
         for (int t = blockIdx.x; ok && t < items; t += gridDim.x) {
@@ -671,52 +663,55 @@ __global__ void __launch_bounds__(I4T_THREADS, 1) lce_int4_kernel(const __grid_c
             float2 acc[NH / 2];
 #pragma unroll
             for (int j = 0; j < NH / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-            // scales four groups ahead
-            uint16_t ahead[4];
+            // a set's scales are asked for two sets ahead
+            uint16_t ahead[2][SET];
+            auto ask = [&](uint16_t (&o)[SET], int g) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ahead[i] = sp[i < groups ? i : groups - 1];
-            const int all = nk * PER;
-            for (int g0 = 0; ok && g0 < all; g0 += 4) {
+                for (int i = 0; i < SET; ++i) o[i] = g + i < groups ? sp[g + i] : static_cast<uint16_t>(0);
+            };
+            ask(ahead[0], 0);
+            ask(ahead[1], SET);
+            const int all = nk * GROUPS;
+            for (int g0 = 0; ok && g0 < all; g0 += 2 * SET) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int g = g0 + i;
-                    if (g < all && ok) {
-                        const uint16_t bits = ahead[i];
-                        ahead[i] = sp[g + 4 < groups ? g + 4 : groups - 1];
-                        const float s = p.dtype == CE_FP16 ? __half2float(__ushort_as_half(bits))
-                                                           : __uint_as_float(static_cast<uint32_t>(bits) << 16);
-                        ok = __all_sync(0xffffffffu, mbar_wait(&bars[at_bar], bphase, ab));
-                        if (ok) {
-                            tc_fence_after();
-                            const float2 s2 = g < groups ? make_float2(s, s) : make_float2(0.f, 0.f);
+                for (int c = 0; c < 2; ++c) {
+                    if (!ok || g0 + c * SET >= all) continue;
+                    float s[SET];
 #pragma unroll
-                            for (int c = 0; c < NH; c += 24) {
-                                constexpr int MOST = 24;
-                                uint32_t v[MOST];
+                    for (int i = 0; i < SET; ++i)
+                        s[i] = p.dtype == CE_FP16 ? __half2float(__ushort_as_half(ahead[c][i]))
+                                                  : __uint_as_float(static_cast<uint32_t>(ahead[c][i]) << 16);
+                    ask(ahead[c], g0 + (2 + c) * SET);
+                    ok = __all_sync(0xffffffffu, mbar_wait(&dfull_bar[set], dphase, ab));
+                    if (!ok) continue;
+                    tc_fence_after();
 #pragma unroll
-                                for (int j = 0; j < MOST; j += 8)
-                                    if (c + j < NH) tmem_ld8(at0 + buf * DCOLS + c + j, v + j);
-                                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                    for (int i = 0; i < SET; ++i) {
+                        const float2 s2 = make_float2(s[i], s[i]);
+                        constexpr int MOST = 24;   // columns under way
 #pragma unroll
-                                for (int j = 0; j < MOST; ++j) asm volatile("" : "+r"(v[j]));
-                                if (c + MOST >= NH) {
-                                    tc_fence_before();
-                                    __syncwarp();
-                                    if (lane == 0) mbar_arrive(&dempty_bar[buf]);
-                                }
+                        for (int b = 0; b < NH; b += MOST) {
+                            uint32_t v[MOST];
 #pragma unroll
-                                for (int j = 0; j < MOST; j += 2)
-                                    if (c + j < NH)
-                                        acc[(c + j) / 2] = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
-                                                                      s2, acc[(c + j) / 2]);
+                            for (int j = 0; j < MOST; j += 8)
+                                if (b + j < NH) tmem_ld8(at0 + set * 128 + i * DCOLS + b + j, v + j);
+                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                            for (int j = 0; j < MOST; ++j) asm volatile("" : "+r"(v[j]));
+                            if (i + 1 == SET && b + MOST >= NH) {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&dempty_bar[set]);
                             }
-                            if (++buf == BUFS) buf = 0;
-                            if (++at_bar == nbars) {
-                                at_bar = 0;
-                                bphase ^= 1;
-                            }
+#pragma unroll
+                            for (int j = 0; j < MOST; j += 2)
+                                if (b + j < NH)
+                                    acc[(b + j) / 2] = __ffma2_rn(
+                                        make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), s2, acc[(b + j) / 2]);
                         }
                     }
+                    set ^= 1;
+                    if (set == 0) dphase ^= 1;
                 }
             }
             if (row < p.V && ok) {
@@ -941,7 +936,7 @@ cudaError_t launch_int4_tokens(const Int4TileParams &p, const void *X, long long
 }
 
 cudaError_t launch_int4_tiles(Int4TileParams p, int n, int sms, cudaStream_t s) {
-    const int stage = I4T_Q + n * 256;
+    const int stage = I4T_Q + n * 512;
     p.stages = (I4_MAX_SMEM - 1024) / stage < I4T_MAX_STAGES ? (I4_MAX_SMEM - 1024) / stage : I4T_MAX_STAGES;
     const int items = p.row_tiles * p.token_tiles;
     cudaLaunchAttribute at[1];

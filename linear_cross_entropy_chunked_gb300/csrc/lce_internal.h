@@ -412,7 +412,7 @@ struct Int4Params {
 };
 // The same on tcgen05: A the weight's rows, B the tokens as launch_int4_tokens lays them out.
 struct Int4TileParams {
-    CUtensorMap tmQ;           // [V][row bytes] packed rows, boxes of 64 bytes x 128 rows
+    CUtensorMap tmQ;           // [V][row bytes] packed rows, boxes of 128 bytes x 128 rows
     CUtensorMap tmX;           // [M][128 units] fp16, boxes of 64 x N
     const void *scale;         // [V][lds]
     long long lds;
