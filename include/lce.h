@@ -413,11 +413,12 @@ lce_status lce_fp8_linear(const void *X, int x_dtype, int64_t ldx, const void *W
  * power of two into fp16's range, in which what lies below 2^-29 of a token's largest magnitude is rounded to
  * multiples of 2^-39 of it). X, out, scale need the
  * alignment of their elements only, q that of 16 bytes. Columns of out from V on are left
- * as they were. Workspace: lce_int4_linear_workspace_size bytes, 16-byte aligned, with the device status
+ * as they were. Workspace: lce_int4_linear_workspace_size bytes (0 and NULL for few tokens, whose device status
+ * nothing records: results after a wait that ran out are NaN), 16-byte aligned, with the device status
  * (lce_read_status); it keeps nothing; calls that may run at the same time need one each. */
 lce_status lce_int4_quantize(const void *W, int w_dtype, int64_t ldw, int64_t V, int64_t D, int group, void *q,
                              int64_t ldq, void *scale, int scale_dtype, int64_t lds, lce_stream_t stream);
-lce_status lce_int4_linear_workspace_size(int64_t M, int64_t D, size_t *bytes);
+lce_status lce_int4_linear_workspace_size(int64_t M, int64_t D, int group, size_t *bytes);
 lce_status lce_int4_linear(const void *X, int x_dtype, int64_t ldx, const void *q, int64_t ldq, const void *scale,
                            int64_t lds, int group, int64_t M, int64_t V, int64_t D, void *out, int64_t ldc,
                            void *ws, size_t ws_bytes, lce_stream_t stream);

@@ -303,6 +303,8 @@ def _gradient_of_logits(Z, ld, grad, inplace):
         return Z
     at = Z.data_ptr() % 16 // Z.element_size()
     N, V = Z.shape
+    if at == 0:
+        return torch.empty_strided((N, V), (ld, 1), dtype=Z.dtype, device=Z.device)
     buf = torch.empty(at + max(0, (N - 1) * ld + V) if N else 0, dtype=Z.dtype, device=Z.device)
     return torch.as_strided(buf, (N, V), (ld, 1), at)
 

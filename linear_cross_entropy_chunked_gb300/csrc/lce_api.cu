@@ -2232,11 +2232,13 @@ lce_status lce_int4_quantize(const void *W, int w_dtype, int64_t ldw, int64_t V,
     return LCE_OK;
 }
 
-// (the tokens' layout; with few tokens none is needed, but a caller's one buffer may serve any number)
-lce_status lce_int4_linear_workspace_size(int64_t M, int64_t D, size_t *bytes) {
+lce_status lce_int4_linear_workspace_size(int64_t M, int64_t D, int group, size_t *bytes) {
     if (!bytes || M < 0 || M > (1ll << 20) || D <= 0 || D > I4_MAX_D) return LCE_ERR_INVALID_ARG;
-    *bytes = 1024 + align_up(4 * static_cast<size_t>(M > 0 ? M : 1), 1024) +
-             static_cast<size_t>(M) * static_cast<size_t>(cdiv(D, 128)) * 256;
+    if (group != 32 && group != 64 && group != 128) return LCE_ERR_INVALID_ARG;
+    *bytes = M == 0 || int4_few(M, D, group)
+                 ? 0
+                 : 1024 + align_up(4 * static_cast<size_t>(M), 1024) +
+                       static_cast<size_t>(M) * static_cast<size_t>(cdiv(D, 128)) * 256;
     return LCE_OK;
 }
 
@@ -2249,20 +2251,19 @@ lce_status lce_int4_linear(const void *X, int x_dtype, int64_t ldx, const void *
     if (M < 0 || M > (1ll << 20) || V <= 0 || V > MAX_V || D <= 0 || D > I4_MAX_D || ldx < D || ldc < V ||
         ldq < (D + 31) / 32 * 16 || lds < cdiv(D, group))
         return LCE_ERR_INVALID_ARG;
-    if (!q || !scale || !ws || (M > 0 && (!X || !out))) return LCE_ERR_INVALID_ARG;
+    size_t need = 0;
+    LCE_TRY(lce_int4_linear_workspace_size(M, D, group, &need));
+    if (!q || !scale || (need && !ws) || (M > 0 && (!X || !out))) return LCE_ERR_INVALID_ARG;
     const uintptr_t halves = reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(scale) |
                              reinterpret_cast<uintptr_t>(out);
     if (ldq % 16 || !aligned16(q) || halves % 2 || !aligned16(ws)) return LCE_ERR_ALIGNMENT;
-    size_t need = 0;
-    lce_int4_linear_workspace_size(M, D, &need);
     if (ws_bytes < need) return LCE_ERR_WORKSPACE;
     int sms = 0, pairs = 0;
     LCE_TRY(init_device(&sms, &pairs));
     if (M == 0) return LCE_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int x_vec = aligned16(X) && ldx % 8 == 0;
-    const char *force = getenv("LCE_I4");
-    if (M <= 8 && !(force && force[0] == 't')) {
+    if (int4_few(M, D, group)) {
         Int4Params p;
         p.X = X;
         p.ldx = ldx;

@@ -12,7 +12,7 @@ namespace lce {
 namespace {
 
 // ------------------------------------------------------------------ few tokens
-// Up to 8 tokens per CTA. Bound by reading the weight, so everything else has to fit into the
+// Up to 8 tokens. Bound by reading the weight, so everything else has to fit into the
 // time of its bytes: at the measured copy rate an SM gets 23 bytes, 47 weights, a cycle.
 //   * A warp takes 16 rows x 128 values (a unit) at a time as the A operand of eight m16n8k16 products, the
 //     tokens are the columns of B. Which of the unit's values a product calls its k-th does not
@@ -150,8 +150,7 @@ __global__ void __launch_bounds__(I4_MAX_WARPS * 32, 1) lce_int4_few_kernel(cons
     __shared__ __align__(8) uint64_t bars[I4_MAX_WARPS][I4_RING];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = lane >> 2, tl = lane & 3;
     const int threads = blockDim.x, warps = threads / 32;
-    const int m0 = blockIdx.y * p.tokens;
-    const int mt = p.M - m0 < p.tokens ? p.M - m0 : p.tokens;
+    const int mt = p.M;
     const int units = p.units;
     // per warp: the ring's chunks of the weight, and of scales (fp32 [16][SC]); then 256 bytes of zeros, and x as
     // 16-byte pieces [unit][token][word][t], the words of odd tokens in the order 1 0 3 2 (two tokens' pieces
@@ -237,7 +236,7 @@ __global__ void __launch_bounds__(I4_MAX_WARPS * 32, 1) lce_int4_few_kernel(cons
     }
 
     // x into shared memory, beside the first loads
-    const T *X = static_cast<const T *>(p.X) + static_cast<long long>(m0) * p.ldx;
+    const T *X = static_cast<const T *>(p.X);
     if (std::is_same<T, __nv_bfloat16>::value) {
         const int per = (p.D + 255) / 256;   // steps of a warp over a token
 #pragma unroll 4
@@ -297,7 +296,7 @@ __global__ void __launch_bounds__(I4_MAX_WARPS * 32, 1) lce_int4_few_kernel(cons
                 v[e] = __half_as_ushort(__float2half_rn(__uint_as_float(static_cast<uint32_t>(v[e]) << 16) * up));
         }
         // pairs (0, 4), (1, 5), (2, 6), (3, 7): the order in which a word's nibbles come
-        xw[(u * p.tokens + m) * 16 + (j ^ (m & 1)) * 4 + tt] =
+        xw[(u * mt + m) * 16 + (j ^ (m & 1)) * 4 + tt] =
             make_uint4(v[0] | (v[4] << 16), v[1] | (v[5] << 16), v[2] | (v[6] << 16), v[3] | (v[7] << 16));
     }
     __syncthreads();
@@ -306,7 +305,7 @@ __global__ void __launch_bounds__(I4_MAX_WARPS * 32, 1) lce_int4_few_kernel(cons
     // a lane's pieces of x: where its even and its odd words are counted from (their order goes by the
     // token), and the step to the next unit's; lanes of no token read zeros
     const uint32_t x_at = smem_u32(g < mt ? xw + g * 16 + tl : zero);
-    const uint32_t swap = g < mt ? (g & 1) * 64 : 0, xu = g < mt ? p.tokens * 256 : 0;
+    const uint32_t swap = g < mt ? (g & 1) * 64 : 0, xu = g < mt ? mt * 256 : 0;
     uint32_t magic;
     asm volatile("mov.u32 %0, 0x64006400;" : "=r"(magic));
     const uint32_t q_at = smem_u32(mine) + g / 2 * I4_ROW + (g & 1) * I4_ODD + tl * 16, s_at = smem_u32(my_scales) + g * (SC * 4);
@@ -342,7 +341,7 @@ __global__ void __launch_bounds__(I4_MAX_WARPS * 32, 1) lce_int4_few_kernel(cons
         for (int i = 0; i < 2; ++i) {
             const int m = 2 * tl + i;
             if (m < mt) {
-                T *o = out + static_cast<long long>(m0 + m) * p.ldc + rb * 16ll + g;
+                T *o = out + static_cast<long long>(m) * p.ldc + rb * 16ll + g;
                 const float down = ok ? s_down[m] : NAN;   // (a wait for copies that ran out is not passed over)
                 if (rb * 16 + g < p.V) o[0] = from_float<T>(acc[i] * down);
                 if (rb * 16 + g + 8 < p.V) o[8] = from_float<T>(acc[i + 2] * down);
@@ -685,30 +684,35 @@ __global__ void __launch_bounds__(I4T_THREADS, 1) lce_int4_kernel(const __grid_c
                     ok = __all_sync(0xffffffffu, mbar_wait(&dfull_bar[set], dphase, ab));
                     if (!ok) continue;
                     tc_fence_after();
+// pieces of eight columns, four under way at a time
+                    constexpr int PIECES = SET * NH / 8;
 #pragma unroll
-                    for (int i = 0; i < SET; ++i) {
-                        const float2 s2 = make_float2(s[i], s[i]);
-                        constexpr int MOST = 24;   // columns under way
+                    for (int b = 0; b < PIECES; b += 4) {
+                        uint32_t v[32];
 #pragma unroll
-                        for (int b = 0; b < NH; b += MOST) {
-                            uint32_t v[MOST];
+                        for (int j = 0; j < 4; ++j)
+                            if (b + j < PIECES)
+                                tmem_ld8(at0 + set * 128 + (b + j) / (NH / 8) * DCOLS + (b + j) % (NH / 8) * 8, v + 8 * j);
+                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                            for (int j = 0; j < MOST; j += 8)
-                                if (b + j < NH) tmem_ld8(at0 + set * 128 + i * DCOLS + b + j, v + j);
-                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-                            for (int j = 0; j < MOST; ++j) asm volatile("" : "+r"(v[j]));
-                            if (i + 1 == SET && b + MOST >= NH) {
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive(&dempty_bar[set]);
-                            }
-#pragma unroll
-                            for (int j = 0; j < MOST; j += 2)
-                                if (b + j < NH)
-                                    acc[(b + j) / 2] = __ffma2_rn(
-                                        make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), s2, acc[(b + j) / 2]);
+                        for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(v[j]));
+                        if (b + 4 >= PIECES) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&dempty_bar[set]);
                         }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (b + j < PIECES) {
+                                const float si = s[(b + j) / (NH / 8)];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    float2 &o = acc[(b + j) % (NH / 8) * 4 + e];
+                                    o = __ffma2_rn(make_float2(__uint_as_float(v[8 * j + 2 * e]),
+                                                               __uint_as_float(v[8 * j + 2 * e + 1])),
+                                                   make_float2(si, si), o);
+                                }
+                            }
                     }
                     set ^= 1;
                     if (set == 0) dphase ^= 1;
@@ -902,20 +906,28 @@ cudaError_t int4_set_attributes() {
     return set_tiles<48>();
 }
 
+// Whether so many tokens go by the kernel for few. Measured at 128256 x 4096, bf16 (us; tiles / few): groups of
+// 128: 1 token 70 / 62, 2: 71 / 66, 4: 71 / 75; of 64: 1: 90 / 76, 4: 91 / 84; of 32: 1: 153 / 95, 6: 153 / 102, 8 (two
+// passes): 154 / 193. Rows so long that the tokens do not fit beside eight warps' buffers go by tiles too.
+bool int4_few(long long M, long long D, int group) {
+    if (M > (group == 128 ? 2 : group == 64 ? 4 : 6)) return false;
+    Int4Params p;
+    p.units = static_cast<int>((D + I4_UNIT - 1) / I4_UNIT);
+    p.group = group;
+    return M == 1 || few_x_smem(p, static_cast<int>(M)) + 8 * few_warp_smem(p) <= I4_MAX_SMEM;
+}
+
 cudaError_t launch_int4(Int4Params p, int sms, cudaStream_t s) {
     p.units = (p.D + I4_UNIT - 1) / I4_UNIT;
-    // as many tokens as leave room for 8 warps, as many warps as there is room for
+    // as many warps as there is room for
     const size_t ws = few_warp_smem(p);
-    int tokens = p.M < 8 ? p.M : 8;
-    while (tokens > 1 && few_x_smem(p, tokens) + 8 * ws > I4_MAX_SMEM) --tokens;
-    const long long room = (static_cast<long long>(I4_MAX_SMEM) - static_cast<long long>(few_x_smem(p, tokens))) /
+    const long long room = (static_cast<long long>(I4_MAX_SMEM) - static_cast<long long>(few_x_smem(p, p.M))) /
                            static_cast<long long>(ws);
     if (room < 1) return cudaErrorInvalidValue;
     const int warps = room < I4_MAX_WARPS ? static_cast<int>(room) : I4_MAX_WARPS;
-    p.tokens = tokens;
     const int blocks = (p.V + 15) / 16;
-    const dim3 grid(blocks < sms ? blocks : sms, (p.M + tokens - 1) / tokens);
-    const size_t smem = few_x_smem(p, tokens) + warps * ws;
+    const dim3 grid(blocks < sms ? blocks : sms);
+    const size_t smem = few_x_smem(p, p.M) + warps * ws;
     return p.dtype == CE_FP16 ? launch_few_of<__half>(p, grid, warps * 32, smem, s)
                               : launch_few_of<__nv_bfloat16>(p, grid, warps * 32, smem, s);
 }

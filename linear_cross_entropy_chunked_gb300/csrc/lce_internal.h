@@ -408,7 +408,7 @@ struct Int4Params {
     int M, V, D;
     void *out;                 // [M][ldc]
     long long ldc;
-    int units, tokens;         // of 128 values; per CTA (set by the launcher)
+    int units;                 // of 128 values (set by the launcher)
 };
 // The same on tcgen05: A the weight's rows, B the tokens as launch_int4_tokens lays them out.
 struct Int4TileParams {
@@ -521,6 +521,7 @@ cudaError_t launch_grad_scale(const ClipItem *items, int n, const ClipScale &c, 
 
 cudaError_t int4_set_attributes();
 cudaError_t launch_int4(Int4Params p, int sms, cudaStream_t s);
+bool int4_few(long long M, long long D, int group);
 int int4_tile_tokens(long long M);
 cudaError_t launch_int4_tokens(const Int4TileParams &p, const void *X, long long ldx, int x_vec, void *to, cudaStream_t s);
 cudaError_t launch_int4_tiles(Int4TileParams p, int n, int sms, cudaStream_t s);

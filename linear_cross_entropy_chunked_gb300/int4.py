@@ -3,6 +3,7 @@
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
@@ -47,10 +48,12 @@ def int4_weight(W, group: int = 128, scale_dtype=None, stream=None) -> Int4Weigh
     return Int4Weight(q[:, :(D + 1) // 2], scale, group)
 
 
-def int4_workspace_size(M, D):
-    """Bytes of a workspace for int4_linear of M tokens of D values."""
+@functools.lru_cache(maxsize=1024)
+def int4_workspace_size(M, D, group):
+    """Bytes of a workspace for int4_linear of M tokens of D values (0: none is needed)."""
     out = ctypes.c_size_t(0)
-    _b._check(_b.lib().lce_int4_linear_workspace_size(M, D, ctypes.byref(out)), "lce_int4_linear_workspace_size")
+    _b._check(_b.lib().lce_int4_linear_workspace_size(M, D, group, ctypes.byref(out)),
+              "lce_int4_linear_workspace_size")
     return out.value
 
 
@@ -84,8 +87,8 @@ def int4_linear(X, w: Int4Weight, out=None, ws=None, stream=None):
     """X W^T for the hidden states X [M, D] (bf16 or fp16, unit column stride, any row stride) and a weight in 4
     bits with scales of X's dtype: logits [M, V] in X's dtype, sums in fp32, rounded once. Fastest for few
     tokens, where it reads a quarter of a 16-bit weight's bytes. The logits' row stride is V rounded up to 16 bytes.
-    out: where to write them (unit column stride). ws: a uint8 tensor of int4_workspace_size(M, D) bytes, whose
-    device status read_status returns; calls that may run at the same time need one each. No gradients: X may not
+    out: where to write them (unit column stride). ws: a uint8 tensor of int4_workspace_size(M, D, w.group) bytes,
+    whose device status read_status returns (where that is not 0); calls that may run at the same time need one each. No gradients: X may not
     require one."""
     ldx = _check_dense_rows("X", X, _HALVES, "bfloat16 or float16")
     if not isinstance(w, Int4Weight):
@@ -102,16 +105,18 @@ def int4_linear(X, w: Int4Weight, out=None, ws=None, stream=None):
             raise ValueError("out may not require a gradient")
     with _b._on(X.device, stream) as s:
         Z = _empty_out(M, V, X.dtype, X.device) if out is None else out
-        nbytes = int4_workspace_size(M, D)
-        if ws is None:
+        nbytes = int4_workspace_size(M, D, w.group)
+        if ws is not None:
+            if ws.device != X.device or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < nbytes \
+                    or ws.data_ptr() % 16:
+                raise ValueError(f"ws must be a contiguous, 16-byte aligned uint8 tensor of at least {nbytes} bytes")
+        elif nbytes:
             ws = torch.empty(nbytes, dtype=torch.uint8, device=X.device)
-        elif ws.device != X.device or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < nbytes \
-                or ws.data_ptr() % 16:
-            raise ValueError(f"ws must be a contiguous, 16-byte aligned uint8 tensor of at least {nbytes} bytes")
         if M:
             _b._check(_b.lib().lce_int4_linear(
                 X.data_ptr(), _b._CE_DTYPES[X.dtype], ldx, w.q.data_ptr(), ldq, w.scale.data_ptr(), lds, w.group, M,
-                V, D, Z.data_ptr(), Z.stride(0) if M > 1 else V, ws.data_ptr(), ws.numel(), s), "lce_int4_linear")
+                V, D, Z.data_ptr(), Z.stride(0) if M > 1 else V, None if ws is None else ws.data_ptr(),
+                0 if ws is None else ws.numel(), s), "lce_int4_linear")
     if out is not None:
         _b._wrote((out,))
     return Z
