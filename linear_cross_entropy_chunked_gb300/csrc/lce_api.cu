@@ -1946,6 +1946,9 @@ lce_status answer_logits_check(const void *Z, int z_dtype, int64_t ld, const int
         (reinterpret_cast<uintptr_t>(dloss) | reinterpret_cast<uintptr_t>(loss)) % 4)
         return LCE_ERR_ALIGNMENT;
     if (dZ && z % 16 != d % 16) return LCE_ERR_ALIGNMENT;
+    // dZ is Z, or lies beside it
+    const uintptr_t bytes = N > 0 ? ((static_cast<uintptr_t>(N) - 1) * ld + V) * (z_dtype == CE_FP32 ? 4 : 2) : 0;
+    if (dZ && d != z && d < z + bytes && z < d + bytes) return LCE_ERR_INVALID_ARG;
     return LCE_OK;
 }
 
