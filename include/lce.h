@@ -258,12 +258,16 @@ lce_status lce_ce_logits(const void *Z, int z_dtype, int64_t ld, const int64_t *
  *
  * lce_policy_fwd_bwd: over the head, as lce_fwd_bwd_opt (6 N D V flops, chunk by chunk, the
  * logits never in memory; flags but LCE_INPUT_FP16, for whose gradients the c_i have no
- * known range: LCE_ERR_UNSUPPORTED). Workspace: lce_workspace_size_opt(..., flags).
- * lce_policy_forward: loss and logprobs alone, workspace lce_forward_workspace_size.
+ * known range: LCE_ERR_UNSUPPORTED). The rows that count are brought together first (more than 256 rows, and
+ * one chunk or chunks of a multiple of 64 rows): the others cost nothing. Workspace:
+ * lce_policy_workspace_size (gradient = 1).
+ * lce_policy_forward: loss and logprobs alone, workspace with gradient = 0.
  * lce_policy_logits: over given logits (z_dtype as for lce_ce_logits): one read of the
  * counting rows and one write of dZ (NULL: no gradient; Z itself: in place), V up to 450000 (16-bit) or
  * 225000 (fp32) (more: a second read). Z, dZ: rows of any stride ld >= V from any element
  * on, both at the same address modulo 16. Workspace: lce_ce_logits_workspace_size(N). */
+lce_status lce_policy_workspace_size(int64_t N, int64_t D, int64_t V, int64_t chunk, int flags, int gradient,
+                                     size_t *bytes);
 lce_status lce_policy_forward(const void *H, const void *W, const int64_t *y, const float *advantages,
                               const float *old_logprobs, const float *ref_logprobs, const float *weights,
                               float clip_low, float clip_high, float beta, float temperature, int64_t N,
@@ -295,8 +299,8 @@ lce_status lce_policy_logits(const void *Z, int z_dtype, int64_t ld, const int64
  *
  * lce_preference_fwd_bwd: over the head; dH and dW both NULL: loss and seq_logprobs alone. A gradient needs
  * every row's log probability first: the logits that the chunk buffers hold then (all, for
- * N <= 2 chunk, or N <= chunk with LCE_LOW_MEMORY) are kept over that, the others computed again
- * (6NDV flops, up to 8NDV). Flags but LCE_INPUT_FP16. Workspace: lce_preference_workspace_size
+ * no more counting rows than 2 chunk, or chunk with LCE_LOW_MEMORY) are kept over that, the others computed again
+ * (6NDV flops, up to 8NDV). Rows that do not count are left out as by lce_policy_fwd_bwd. Flags but LCE_INPUT_FP16. Workspace: lce_preference_workspace_size
  * (gradient = 0: without dH and dW).
  * lce_preference_logits: over given logits, laid out as for lce_policy_logits: two reads of
  * the counting rows, one write. */

@@ -46,6 +46,7 @@ from .answers import (  # noqa: F401
     policy_forward,
     policy_fwd_bwd,
     policy_logits,
+    policy_workspace_size,
     preference_fwd_bwd,
     preference_logits,
     preference_workspace_size,

@@ -56,6 +56,7 @@ EXPORTED = (
     "lce_norm_fwd_bwd",
     "lce_norm_workspace_size_opt",
     "lce_norm_fwd_bwd_opt",
+    "lce_policy_workspace_size",
     "lce_policy_forward",
     "lce_policy_fwd_bwd",
     "lce_policy_logits",
@@ -165,6 +166,7 @@ def lib() -> ctypes.CDLL:
                                        ctypes.c_size_t, _vp]
     _i = ctypes.c_int
     pol = [_vp, _vp, _vp, _vp, _f, _f, _f, _f]   # advantages .. temperature
+    L.lce_policy_workspace_size.argtypes = [_i64, _i64, _i64, _i64, _i, _i, _sz]
     L.lce_policy_forward.argtypes = [_vp, _vp, _vp, *pol, _i64, _i64, _i64, _i64, _i64, _i, _vp, _vp, _vp,
                                      ctypes.c_size_t, _vp]
     L.lce_policy_fwd_bwd.argtypes = [_vp, _vp, _vp, *pol, _vp, _i64, _i64, _i64, _i64, _i64, _i, _i, _vp, _vp, _vp,
@@ -222,7 +224,7 @@ def lib() -> ctypes.CDLL:
                  "lce_clip_grad_norm", "lce_fp8_quantize", "lce_fp8_matmul_workspace_size",
                  "lce_fp8_matmul_best_workspace_size",
                  "lce_fp8_matmul", "lce_fp8_linear_workspace_size", "lce_fp8_linear",
-                 "lce_policy_forward", "lce_policy_fwd_bwd", "lce_policy_logits",
+                 "lce_policy_workspace_size", "lce_policy_forward", "lce_policy_fwd_bwd", "lce_policy_logits",
                  "lce_preference_workspace_size", "lce_preference_fwd_bwd",
                  "lce_preference_logits_workspace_size", "lce_preference_logits", "lce_scale", "lce_int4_quantize",
                  "lce_int4_linear_workspace_size", "lce_int4_linear"):
@@ -263,6 +265,7 @@ class _on:
         if self._stream is not None:
             self._entered += (torch.cuda.stream(self._stream),)
             self._entered[-1].__enter__()
+            return self._stream.cuda_stream
         return _raw_stream(self._dev.index if self._dev.index is not None else torch.cuda.current_device())
 
     def __exit__(self, *exc):

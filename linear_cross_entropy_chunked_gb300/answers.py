@@ -87,6 +87,13 @@ def _dloss(dloss, reduction, n, dev):
                    torch.float32, dev)
 
 
+def policy_workspace_size(N, D, V, chunk, flags=0, gradient=True):
+    out = ctypes.c_size_t(0)
+    _b._check(_b.lib().lce_policy_workspace_size(N, D, V, chunk, flags, 1 if gradient else 0, ctypes.byref(out)),
+              "lce_policy_workspace_size")
+    return out.value
+
+
 def policy_forward(H, W, y, advantages, old_logprobs=None, ref_logprobs=None, weights=None, clip_low=0.2,
                    clip_high=0.2, beta=0.0, temperature=1.0, chunk: int = 1024,
                    ignore_index: int = _b.IGNORE_INDEX, reduction: str = "mean", loss=None, logprobs=None, ws=None,
@@ -100,7 +107,7 @@ def policy_forward(H, W, y, advantages, old_logprobs=None, ref_logprobs=None, we
         out = _Outputs(dev)
         loss = out.take("loss", loss, _loss_shape(reduction, N))
         logprobs = out.take("logprobs", logprobs, (N,))
-        ws = _workspace(ws, _b.forward_workspace_size(N, D, V, chunk), dev)
+        ws = _workspace(ws, policy_workspace_size(N, D, V, chunk, gradient=False), dev)
         _b._check(_b.lib().lce_policy_forward(
             H.data_ptr(), W.data_ptr(), y.data_ptr(), *args, N, D, V, ignore_index, chunk, red, loss.data_ptr(),
             logprobs.data_ptr(), ws.data_ptr(), ws.numel(), s), "lce_policy_forward")
@@ -138,7 +145,7 @@ def policy_fwd_bwd(H, W, y, advantages, old_logprobs=None, ref_logprobs=None, we
         loss = out.take("loss", loss, _loss_shape(reduction, N))
         logprobs = out.take("logprobs", logprobs, (N,))
         flags, dH, dW = _gradients(out, H, W, dH, dW, accumulate, compute_dW, low_memory)
-        ws = _workspace(ws, _b.workspace_size_opt(N, D, V, chunk, flags), dev)
+        ws = _workspace(ws, policy_workspace_size(N, D, V, chunk, flags), dev)
         _b._check(_b.lib().lce_policy_fwd_bwd(
             H.data_ptr(), W.data_ptr(), y.data_ptr(), *args, d, N, D, V, ignore_index, chunk, red, flags,
             loss.data_ptr(), logprobs.data_ptr(), dH.data_ptr(), None if dW is None else dW.data_ptr(),
@@ -176,7 +183,7 @@ def preference_fwd_bwd(H, W, y, offsets, ref_logprobs=None, beta=0.1, label_smoo
         loss = -((1 - label_smoothing) log sigmoid(m) + label_smoothing log sigmoid(-m))
     reduction: the mean over the pairs, "sum", or "none" (loss [pairs]; dloss [pairs]).
     seq_logprobs [2 pairs]: L; a reference model's, from a call with gradient=False (dH and dW are None
-    then), is the ref_logprobs of this one. Up to 2 chunk rows no logits are computed twice: a
+    then), is the ref_logprobs of this one. Up to 2 chunk counting rows no logits are computed twice: a
     larger chunk is faster and takes more workspace. Rows outside the sequences add nothing."""
     N, D, V = _check_head(H, W, y)
     dev, red = H.device, _b._reduction(reduction)

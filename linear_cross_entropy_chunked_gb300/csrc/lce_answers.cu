@@ -806,7 +806,7 @@ __device__ __forceinline__ void sequence(const PairParams &p, long long begin, l
     int n = 0;
     for (long long i = begin + t; i < end; i += PAIR_THREADS)
         if (label_counts(p.y[i], p.V, p.ignore_index)) {
-            s.add(-p.loss_rows[i]);
+            s.add(-p.loss_rows[p.place ? p.place[i] : i]);
             ++n;
         }
     s.warp();
@@ -882,16 +882,18 @@ __global__ void __launch_bounds__(PAIR_THREADS) lce_pairs_kernel(const __grid_co
         if (m != m) slope = m;
         // p - onehot gets minus the slope of its row
         const float c[2] = {-slope * share[0], slope * share[1]};
+        auto put = [&](long long i, float v) {
+            if (!p.place) p.coef[i] = v;
+            else if (p.place[i] >= 0) p.coef[p.place[i]] = v;
+        };
         for (int q = 0; q < 2; ++q)
             for (long long i = off[2 * q] + t; i < off[2 * q + 1]; i += PAIR_THREADS)
-                p.coef[i] = label_counts(p.y[i], p.V, p.ignore_index) ? c[q] : 0.f;
+                put(i, label_counts(p.y[i], p.V, p.ignore_index) ? c[q] : 0.f);
         // rows before the first sequence and behind the last
         if (k == 0)
-            for (long long i = t; i < p.N; i += PAIR_THREADS)
-                if (i < off[0]) p.coef[i] = 0.f;
-                else break;
+            for (long long i = t; i < p.N && i < off[0]; i += PAIR_THREADS) put(i, 0.f);
         if (k == p.pairs - 1)
-            for (long long i = off[3] + t; i < p.N; i += PAIR_THREADS) p.coef[i] = 0.f;
+            for (long long i = off[3] + t; i < p.N; i += PAIR_THREADS) put(i, 0.f);
     }
     if (p.loss && last_to_finish(p.hdr + HDR_DONE, static_cast<int>(gridDim.x), &s_last)) {
         const double s = block_sum(p.pair_loss, p.pairs, s_red);

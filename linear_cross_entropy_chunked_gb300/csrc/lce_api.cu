@@ -300,6 +300,11 @@ struct Ctx {
     float inv_t = 1.f;
     bool answers = false;
     const float *coef = nullptr;
+    // the rows that count brought together, chunk by chunk into H's buffer (h_chunked): which rows of the
+    // call they are (null: not done), and where H lies
+    const int *index = nullptr;
+    const __nv_bfloat16 *Hrows = nullptr;
+    bool loss_by_index = false;
 };
 
 // Row of H (c.H) where the chunk starting at row0 begins.
@@ -388,7 +393,8 @@ SideStream *side_stream() {
 lce_status setup(Ctx &c, const void *H, const void *W, const int64_t *y, int64_t N, int64_t D,
                  int64_t V, int64_t ign, int64_t chunk, void *ws, size_t ws_bytes,
                  lce_stream_t stream, bool h_chunked = false, bool f16 = false,
-                 bool frozen_w = false, bool fwd_only = false, bool low_mem = false) {
+                 bool frozen_w = false, bool fwd_only = false, bool low_mem = false,
+                 bool scan = true) {
     g_launches = 0;
     if (!make_layout(N, D, V, chunk, c.L, frozen_w, low_mem)) return LCE_ERR_INVALID_ARG;
     if (!ws) return LCE_ERR_INVALID_ARG;
@@ -428,7 +434,7 @@ lce_status setup(Ctx &c, const void *H, const void *W, const int64_t *y, int64_t
     if (N > 0 && !encode_2d(&c.tmH_K, H, D, h_chunked ? c.L.C * c.L.nbuf : N, D * 2, BK, BM, c.t16))
         return LCE_ERR_CUDA;
     if (cudaMemsetAsync(c.ws, 0, c.L.hdr_bytes, c.s) != cudaSuccess) return LCE_ERR_CUDA;
-    LCE_LAUNCH(launch_label_scan(c.y, N, V, ign, c.hdr, c.s));
+    if (scan) LCE_LAUNCH(launch_label_scan(c.y, N, V, ign, c.hdr, c.s));
     return LCE_OK;
 }
 
@@ -451,6 +457,7 @@ void base_params(const Ctx &c, GemmParams &p, long long row0, long long rows, in
     p.mean = c.reduction == LCE_REDUCTION_MEAN ? 1 : 0;
     p.f16 = c.f16 ? 1 : 0;
     p.inv_t = c.inv_t;
+    p.counting = c.index ? c.hdr + HDR_NVALID : nullptr;
 }
 
 // The logits launches of the chunk at row0 (MODE_LSE / _LSE_P / _G epilogue, P' or G
@@ -567,6 +574,8 @@ lce_status run_bwd(const Ctx &c, long long row0, long long rows, int slot, const
     GemmParams p;
     memset(&p, 0, sizeof(p));
     base_params(c, p, row0, rows, slot);
+    p.dw_rows = static_cast<int>(g.dw_rows);
+    p.dw_row0 = static_cast<int>(row0 + rows - g.dw_rows);
     p.G = g.G;
     void *dHc = o.ptr;
     const bool dh_fp32 = o.fp32;
@@ -734,12 +743,17 @@ lce_status run_grad(const Ctx &c, long long row0, long long rows, int slot, void
                     bool acc_dh, float *dW, bool acc_dw, const float *dloss, const GradSpec &g) {
     if (g.dw_only) return run_bwd(c, row0, rows, slot, DhOut{dHc, false, 1, 0}, dW, acc_dw, dloss, g);
     const int want = dh_parts(c, rows, g.dh_alone);
-    if (want <= 1 && !acc_dh)
+    if (want <= 1 && !acc_dh && !c.index)
         return run_bwd(c, row0, rows, slot, DhOut{dHc, false, 1, 0}, dW, acc_dw, dloss, g);
     float *dHp = reinterpret_cast<float *>(c.ws + c.L.off_dHp);
     int parts = 1;
     LCE_TRY(run_bwd(c, row0, rows, slot, DhOut{dHp, true, want, c.L.ldp}, dW, acc_dw, dloss, g,
                     &parts));
+    if (c.index) {
+        LCE_LAUNCH(launch_scatter_dh(dHp, parts, c.L.ldp * c.D, c.index, c.hdr + HDR_NVALID, row0, rows, c.D,
+                                     static_cast<__nv_bfloat16 *>(dHc) - row0 * c.D, acc_dh, c.sms, c.s));
+        return LCE_OK;
+    }
     LCE_LAUNCH(launch_combine_dh(dHp, parts, c.L.ldp * c.D, dHc, rows * c.D, c.f16, acc_dh,
                                  c.sms, c.s));
     return LCE_OK;
@@ -766,6 +780,9 @@ void merge_params(const Ctx &c, long long row0, long long rows, float *lse, cons
     m.loss_rows = loss_rows;
     m.pol = c.pol;
     m.zero_rows = c.answers ? 1 : 0;
+    m.counting = c.index ? c.hdr + HDR_NVALID : nullptr;
+    m.index = c.pol.adv ? c.index : nullptr;   // (a preference's rows go by their place)
+    m.loss_by_index = c.loss_by_index ? 1 : 0;
 }
 
 lce_status run_merge(const Ctx &c, long long row0, long long rows, float *lse,
@@ -811,24 +828,88 @@ inline long long chunk_rows(const Ctx &c, long long k) {
 // Whether chunks are taken in pairs with one dW contraction per pair: CTA pairs,
 // a dW contraction, two chunk buffers (so more than one chunk), H in place.
 inline bool paired(const Ctx &c, bool h_chunked_ok = false) {
-    return c.pairs > 0 && !c.L.frozen_w && c.L.nbuf == 2 && (h_chunked_ok || !c.h_chunked);
+    return c.pairs > 0 && !c.L.frozen_w && c.L.nbuf == 2 && (h_chunked_ok || !c.h_chunked || c.index);
 }
 
 // W frozen with two chunk buffers: chunk k+1's logits tiles run on the CTA pairs
 // chunk k's dH tiles leave free (chunk k in buffer k % 2).
 inline bool frozen_overlapped(const Ctx &c) {
-    return c.pairs > 0 && c.L.frozen_w && c.L.nbuf == 2 && !c.h_chunked;
+    return c.pairs > 0 && c.L.frozen_w && c.L.nbuf == 2 && (!c.h_chunked || c.index);
 }
 
-// The gradients of chunks 0 .. n - 1 from a saved lse: each chunk's logits again, G straight
+// The rows of chunk k that count into their place of H's buffer (nothing to do where H is read in place).
+lce_status bring_rows(const Ctx &c, long long k) {
+    if (!c.index) return LCE_OK;
+    const long long row0 = k * c.L.C;
+    LCE_LAUNCH_KIND(LCE_KERNEL_MERGE, c.s,
+                    launch_gather_rows(c.Hrows, c.index, c.hdr + HDR_NVALID, row0, chunk_rows(c, k), c.D,
+                                       const_cast<__nv_bfloat16 *>(c.H) + h_row(c, row0) * c.D, c.sms, c.s));
+    return LCE_OK;
+}
+
+// Losses on answers bring the rows that count together (prompts and padding are often half of a batch, and their
+// rows cost as much as the others'): which rows they are, their labels, and a chunk's rows of H (a pair's with two
+// chunk buffers), at byte `at` of the workspace. Not done for so few rows that no tile of 256 would be saved, and
+// not where chunks do not end on k blocks of the dW contraction.
+struct GatherLayout {
+    bool on = false;
+    size_t off_index = 0, off_place = 0, off_labels = 0, off_H = 0, end = 0;
+};
+
+GatherLayout gather_layout(const Layout &L, long long N, long long D, size_t at) {
+    GatherLayout g;
+    g.on = N > 256 && (L.nchunks <= 1 || L.C % BK == 0);
+    g.end = at;
+    if (!g.on) return g;
+    auto take = [&](size_t bytes) {
+        const size_t o = g.end;
+        g.end += align_up(bytes, 1024);
+        return o;
+    };
+    g.off_index = take(sizeof(int) * static_cast<size_t>(N));
+    g.off_place = take(sizeof(int) * static_cast<size_t>(N));
+    g.off_labels = take(sizeof(long long) * static_cast<size_t>(N));
+    g.off_H = take(2 * static_cast<size_t>(L.nbuf) * L.C * static_cast<size_t>(D));
+    return g;
+}
+
+// H and y as setup gets them: the caller's, or their places in the workspace.
+lce_status gather_inputs(const GatherLayout &g, const void *&H, const int64_t *&y, void *ws) {
+    if (!g.on) return LCE_OK;
+    if (!H || !y || !ws) return LCE_ERR_INVALID_ARG;
+    if (!aligned16(H) || !aligned16(y)) return LCE_ERR_ALIGNMENT;
+    H = static_cast<uint8_t *>(ws) + g.off_H;
+    y = reinterpret_cast<const int64_t *>(static_cast<uint8_t *>(ws) + g.off_labels);
+    return LCE_OK;
+}
+
+lce_status start_gather(Ctx &c, const GatherLayout &g, const void *H, const int64_t *y) {
+    if (!g.on) return LCE_OK;
+    c.Hrows = static_cast<const __nv_bfloat16 *>(H);
+    c.index = reinterpret_cast<const int *>(c.ws + g.off_index);
+    LCE_LAUNCH(launch_compact(reinterpret_cast<const long long *>(y), c.N, c.V, c.ign, c.hdr,
+                              reinterpret_cast<int *>(c.ws + g.off_index), reinterpret_cast<int *>(c.ws + g.off_place),
+                              reinterpret_cast<long long *>(c.ws + g.off_labels), c.s));
+    return LCE_OK;
+}
+
+#define LCE_ZERO(ptr, bytes)                                                        \
+    do {                                                                            \
+        if (cudaMemsetAsync((ptr), 0, (bytes), c.s) != cudaSuccess) return LCE_ERR_CUDA; \
+    } while (0)
+
+// The gradients of chunks `first` .. n - 1 (first even where chunks go in pairs) from a saved lse: each chunk's logits again, G straight
 // from their epilogue, then the contractions. acc_dw0: dW is added to from the first one on.
-lce_status backward_chunks(const Ctx &c, long long n, const float *lse, const float *dloss,
+lce_status backward_chunks(const Ctx &c, long long first, long long n, const float *lse, const float *dloss,
                            __nv_bfloat16 *dHb, bool acc_dh, float *dW, bool acc_dw0) {
-    if (n <= 0) return LCE_OK;
+    if (n <= first) return LCE_OK;
     if (frozen_overlapped(c)) {
-        LCE_TRY(run_logits(c, MODE_G, 0, chunk_rows(c, 0), 0, lse, dloss, c.Gb[0]));
-        for (long long k = 0; k < n; ++k) {
+        LCE_TRY(bring_rows(c, first));
+        LCE_TRY(run_logits(c, MODE_G, first * c.L.C, chunk_rows(c, first), static_cast<int>(2 * first), lse, dloss,
+                           c.Gb[0]));
+        for (long long k = first; k < n; ++k) {
             const long long r0 = k * c.L.C, n0 = chunk_rows(c, k);
+            if (k + 1 < n) LCE_TRY(bring_rows(c, k + 1));
             GradSpec g{c.Gb[k & 1], c.Gb[k & 1], 0, true, true};
             LogitsSpec next{};
             if (k + 1 < n) {
@@ -846,10 +927,12 @@ lce_status backward_chunks(const Ctx &c, long long n, const float *lse, const fl
         // columns 0..C-1; a's dH tiles, with b's logits (G into buffer 1) on the pairs
         // they leave free; b's H^T into columns C.., then b's dH beside one dW
         // contraction over both chunks (K = C + rows_b). An odd last chunk runs by itself.
-        for (long long a = 0; a < n; a += 2) {
+        for (long long a = first; a < n; a += 2) {
             const long long ra = a * c.L.C, na = chunk_rows(c, a);
             const bool has_b = a + 1 < n;
             const bool acc = a > 0 || acc_dw0;
+            LCE_TRY(bring_rows(c, a));
+            if (has_b) LCE_TRY(bring_rows(c, a + 1));
             LCE_TRY(run_logits(c, MODE_G, ra, na, static_cast<int>(2 * a), lse, dloss, c.Gb[0]));
             LCE_TRY(run_transpose(c, ra, na, 0));
             if (!has_b) {
@@ -870,9 +953,10 @@ lce_status backward_chunks(const Ctx &c, long long n, const float *lse, const fl
         }
         return LCE_OK;
     }
-    for (long long k = 0; k < n; ++k) {
+    for (long long k = first; k < n; ++k) {
         const long long row0 = k * c.L.C;
         const long long rows = chunk_rows(c, k);
+        LCE_TRY(bring_rows(c, k));
         LCE_TRY(run_logits(c, MODE_G, row0, rows, static_cast<int>(2 * k), lse, dloss, c.Gb[0]));
         LCE_TRY(run_grad(c, row0, rows, static_cast<int>(2 * k + 1), dHb + row0 * c.D, acc_dh, dW,
                          k > 0 || acc_dw0, dloss, GradSpec{c.Gb[0], c.Gb[0], rows, false, false}));
@@ -998,7 +1082,7 @@ lce_status lce_backward_opt(const void *H, const void *W, const int64_t *y, cons
         if (cudaMemsetAsync(dW, 0, sizeof(float) * static_cast<size_t>(V) * D, c.s) != cudaSuccess)
             return LCE_ERR_CUDA;
     }
-    return backward_chunks(c, c.L.nchunks, lse, dloss, static_cast<__nv_bfloat16 *>(dH),
+    return backward_chunks(c, 0, c.L.nchunks, lse, dloss, static_cast<__nv_bfloat16 *>(dH),
                            (flags & LCE_ACCUMULATE_DH) != 0, dW, (flags & LCE_ACCUMULATE_DW) != 0);
 }
 
@@ -1048,14 +1132,29 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
     Layout L0;
     if (!make_layout(N, D, V, chunk, L0, frozen, low_mem)) return LCE_ERR_INVALID_ARG;
     if (acc_dh && ws_bytes < L0.total + acc_dh_bytes(L0, D)) return LCE_ERR_WORKSPACE;
+    GatherLayout gl;
+    const void *Hs = H;
+    const int64_t *ys = y;
+    if (pol) {
+        gl = gather_layout(L0, N, D, L0.total + acc_dh_bytes(L0, D));
+        if (gl.on && ws_bytes < gl.end) return LCE_ERR_WORKSPACE;
+        LCE_TRY(gather_inputs(gl, Hs, ys, ws));
+    }
     Ctx c;
-    LCE_TRY(setup(c, H, W, y, N, D, V, ignore_index, chunk, ws, ws_bytes, stream, false, f16,
-                  frozen, false, low_mem));
+    LCE_TRY(setup(c, Hs, W, ys, N, D, V, ignore_index, chunk, ws, ws_bytes, stream, gl.on, f16,
+                  frozen, false, low_mem, !gl.on));
     c.reduction = reduction;
     if (pol) {
         c.pol = *pol;
         c.inv_t = pol->inv_t;
         c.answers = true;
+        LCE_TRY(start_gather(c, gl, H, y));
+        if (gl.on) {   // what rows that do not count have
+            c.loss_by_index = none;
+            LCE_ZERO(none ? loss : c.loss_rows, sizeof(float) * static_cast<size_t>(N));
+            LCE_ZERO(pol->logp, sizeof(float) * static_cast<size_t>(N));
+            if (!acc_dh) LCE_ZERO(dH, 2 * static_cast<size_t>(N) * static_cast<size_t>(D));
+        }
     }
     if (n_valid_total) LCE_LAUNCH(launch_set_nvalid(reinterpret_cast<const long long *>(n_valid_total),
                                                     c.hdr, c.s));
@@ -1070,10 +1169,12 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
     if (frozen_overlapped(c)) {
         // chunk k's dH tiles, with chunk k+1's logits (P' into buffer (k+1) % 2) on
         // the pairs they leave free; then chunk k+1's prep (no H^T: no dW)
+        LCE_TRY(bring_rows(c, 0));
         LCE_TRY(run_logits(c, MODE_LSE_P, 0, chunk_rows(c, 0), 0, nullptr, nullptr, c.Gb[0]));
         LCE_TRY(run_prep(c, 0, chunk_rows(c, 0), lse, dloss, rows_out, c.Gb[0], false));
         for (long long k = 0; k < c.L.nchunks; ++k) {
             const long long r0 = k * c.L.C, n0 = chunk_rows(c, k);
+            if (k + 1 < c.L.nchunks) LCE_TRY(bring_rows(c, k + 1));
             GradSpec g{c.Gb[k & 1], c.Gb[k & 1], 0, true, true};
             LogitsSpec next{};
             if (k + 1 < c.L.nchunks) {
@@ -1097,6 +1198,8 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
             const long long ra = a * c.L.C, na = chunk_rows(c, a);
             const bool has_b = a + 1 < c.L.nchunks;
             const bool acc = a > 0 || acc_dw0;
+            LCE_TRY(bring_rows(c, a));
+            if (has_b) LCE_TRY(bring_rows(c, a + 1));
             LCE_TRY(run_logits(c, MODE_LSE_P, ra, na, static_cast<int>(2 * a), nullptr, nullptr,
                                c.Gb[0]));
             LCE_TRY(run_prep(c, ra, na, lse, dloss, rows_out, c.Gb[0], true, 0));
@@ -1121,6 +1224,7 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
         for (long long k = 0; k < c.L.nchunks; ++k) {
             const long long row0 = k * c.L.C;
             const long long rows = chunk_rows(c, k);
+            LCE_TRY(bring_rows(c, k));
             LCE_TRY(run_logits(c, MODE_LSE_P, row0, rows, static_cast<int>(2 * k), nullptr, nullptr,
                                c.Gb[0]));
             LCE_TRY(run_prep(c, row0, rows, lse, dloss, rows_out, c.Gb[0], !frozen));
@@ -1172,6 +1276,7 @@ PolicyParams policy_params(const float *advantages, const float *old_logprobs, c
 // partials and target logits of a second chunk that is kept between the phases.
 struct PrefLayout {
     Layout L;
+    GatherLayout gather;
     size_t off_lse = 0, off_coef = 0, off_pair = 0, off_parts = 0, off_zy = 0, total = 0;
 };
 
@@ -1180,7 +1285,8 @@ bool make_pref_layout(int64_t N, int64_t D, int64_t V, int64_t chunk, int64_t pa
     const bool frozen = (flags & LCE_FROZEN_W) != 0, low_mem = (flags & LCE_LOW_MEMORY) != 0;
     if (!make_layout(N, D, V, chunk, P.L, frozen, low_mem) || pairs <= 0 || pairs > (1ll << 24)) return false;
     const size_t rows = sizeof(float) * static_cast<size_t>(N > 0 ? N : 1);
-    size_t off = grad ? P.L.total + ((flags & LCE_ACCUMULATE_DH) ? acc_dh_bytes(P.L, D) : 0) : P.L.fwd_total;
+    P.gather = gather_layout(P.L, N, D, grad ? P.L.total + acc_dh_bytes(P.L, D) : P.L.fwd_total);
+    size_t off = P.gather.end;
     auto take = [&](size_t bytes) {
         const size_t at = off;
         off += align_up(bytes, 1024);
@@ -1224,6 +1330,7 @@ PairParams pair_params(const int64_t *offsets, int64_t pairs, int64_t N, int64_t
     p.ignore_index = ign;
     p.y = reinterpret_cast<const long long *>(y);
     p.loss_rows = loss_rows;
+    p.place = nullptr;
     p.ref = ref;
     p.beta = beta;
     p.smoothing = smoothing;
@@ -1519,6 +1626,16 @@ lce_status lce_fwd_bwd(const void *H, const void *W, const int64_t *y, const flo
                           lse, dH, dW, ws, ws_bytes, stream);
 }
 
+lce_status lce_policy_workspace_size(int64_t N, int64_t D, int64_t V, int64_t chunk, int flags, int gradient,
+                                     size_t *bytes) {
+    Layout L;
+    if (!bytes || (flags & ~LCE_FLAGS_ALL) ||
+        !make_layout(N, D, V, chunk, L, gradient && (flags & LCE_FROZEN_W), gradient && (flags & LCE_LOW_MEMORY)))
+        return LCE_ERR_INVALID_ARG;
+    *bytes = gather_layout(L, N, D, gradient ? L.total + acc_dh_bytes(L, D) : L.fwd_total).end;
+    return LCE_OK;
+}
+
 lce_status lce_policy_forward(const void *H, const void *W, const int64_t *y, const float *advantages,
                               const float *old_logprobs, const float *ref_logprobs, const float *weights,
                               float clip_low, float clip_high, float beta, float temperature, int64_t N,
@@ -1531,13 +1648,28 @@ lce_status lce_policy_forward(const void *H, const void *W, const int64_t *y, co
     if (loss && !aligned16(loss)) return LCE_ERR_ALIGNMENT;
     LCE_TRY(policy_check(N, advantages, old_logprobs, ref_logprobs, weights, clip_low, clip_high, beta,
                          temperature, logprobs));
+    Layout L0;
+    if (!make_layout(N, D, V, chunk, L0)) return LCE_ERR_INVALID_ARG;
+    const GatherLayout gl = gather_layout(L0, N, D, L0.fwd_total);
+    if (gl.on && ws_bytes < gl.end) return LCE_ERR_WORKSPACE;
+    const void *Hs = H;
+    const int64_t *ys = y;
+    LCE_TRY(gather_inputs(gl, Hs, ys, ws));
     Ctx c;
-    LCE_TRY(setup(c, H, W, y, N, D, V, ignore_index, chunk, ws, ws_bytes, stream, false, false, false, true));
+    LCE_TRY(setup(c, Hs, W, ys, N, D, V, ignore_index, chunk, ws, ws_bytes, stream, gl.on, false, false, true, false,
+                  !gl.on));
     c.reduction = reduction;
+    LCE_TRY(start_gather(c, gl, H, y));
+    if (gl.on) {   // what rows that do not count have
+        c.loss_by_index = none;
+        LCE_ZERO(none ? loss : c.loss_rows, sizeof(float) * static_cast<size_t>(N));
+        LCE_ZERO(logprobs, sizeof(float) * static_cast<size_t>(N));
+    }
     c.pol = policy_params(advantages, old_logprobs, ref_logprobs, weights, clip_low, clip_high, beta,
                           temperature, logprobs);
     c.inv_t = c.pol.inv_t;
     for (long long k = 0; k < c.L.nchunks; ++k) {
+        LCE_TRY(bring_rows(c, k));
         LCE_TRY(run_logits(c, MODE_LSE, k * c.L.C, chunk_rows(c, k), static_cast<int>(k), nullptr, nullptr,
                            c.Gb[0]));
         LCE_TRY(run_merge(c, k * c.L.C, chunk_rows(c, k), nullptr, nullptr, none ? loss : c.loss_rows));
@@ -1574,9 +1706,9 @@ lce_status lce_preference_workspace_size(int64_t N, int64_t D, int64_t V, int64_
     return LCE_OK;
 }
 
-// Phases: every chunk's logits and the rows' log probabilities; the pairs; the gradients. What the
-// last chunks (as many as there are chunk buffers) have in their buffers stays there over the
-// pairs, so that their logits are not computed again: with no more rows than the buffers hold, none are.
+// Phases: every chunk's logits and the rows' log probabilities; the pairs; the gradients. The first chunks (as many
+// as there are chunk buffers) come last in the first phase and stay in their buffers over the pairs, so
+// that their logits are not computed again: with no more rows than the buffers hold, none are.
 lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y, const int64_t *offsets,
                                   int64_t pairs, const float *ref_logprobs, float beta, float label_smoothing,
                                   int average, const float *dloss, int64_t N, int64_t D, int64_t V,
@@ -1599,9 +1731,14 @@ lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y
     if (!make_pref_layout(N, D, V, chunk, pairs, flags, grad, P)) return LCE_ERR_INVALID_ARG;
     if (!ws) return LCE_ERR_INVALID_ARG;
     if (ws_bytes < P.total) return LCE_ERR_WORKSPACE;
+    const void *Hs = H;
+    const int64_t *ys = y;
+    LCE_TRY(gather_inputs(P.gather, Hs, ys, ws));
     Ctx c;
-    LCE_TRY(setup(c, H, W, y, N, D, V, ignore_index, chunk, ws, ws_bytes, stream, false, false,
-                  (flags & LCE_FROZEN_W) != 0, !grad, low_mem));
+    LCE_TRY(setup(c, Hs, W, ys, N, D, V, ignore_index, chunk, ws, ws_bytes, stream, P.gather.on, false,
+                  (flags & LCE_FROZEN_W) != 0, !grad, low_mem, !P.gather.on));
+    LCE_TRY(start_gather(c, P.gather, H, y));
+    if (P.gather.on && grad && !acc_dh) LCE_ZERO(dH, 2 * static_cast<size_t>(N) * static_cast<size_t>(D));
     c.reduction = LCE_REDUCTION_NONE;   // (of the rows: each has a coefficient of its own)
     c.answers = true;
     float *lse = reinterpret_cast<float *>(c.ws + P.off_lse);
@@ -1611,9 +1748,9 @@ lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y
     if (n == 0 && dW && !acc_dw0 &&
         cudaMemsetAsync(dW, 0, sizeof(float) * static_cast<size_t>(V) * D, c.s) != cudaSuccess)
         return LCE_ERR_CUDA;
-    // the chunks from `keep` on stay in the buffers: the last pair (or the odd last one), or the last
+    // the first `kept_n` chunks stay in the buffers: a pair, or one
     const bool two = grad && (paired(c) || frozen_overlapped(c));
-    const long long keep = !grad || n == 0 ? n : two ? (n - 1) / 2 * 2 : n - 1;
+    const long long kept_n = !grad ? 0 : n < (two ? 2 : 1) ? n : (two ? 2 : 1);
     struct Kept {
         float2 *parts;
         float *zy;
@@ -1624,37 +1761,40 @@ lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y
         c.parts = kept[j].parts;
         c.zy = kept[j].zy;
     };
-    for (long long k = 0; k < n; ++k) {
-        const long long j = k < keep ? 0 : k - keep;
-        use(j);
-        LCE_TRY(run_logits(c, k < keep ? MODE_LSE : MODE_LSE_P, k * c.L.C, chunk_rows(c, k), static_cast<int>(k),
-                           nullptr, nullptr, c.Gb[j]));
+    for (long long i = 0; i < n; ++i) {
+        const long long k = i + kept_n < n ? i + kept_n : i + kept_n - n;   // the kept ones last
+        const bool stays = k < kept_n;
+        use(stays ? k : 0);
+        LCE_TRY(bring_rows(c, k));
+        LCE_TRY(run_logits(c, stays ? MODE_LSE_P : MODE_LSE, k * c.L.C, chunk_rows(c, k), static_cast<int>(k), nullptr,
+                           nullptr, c.Gb[stays ? k : 0]));
         LCE_TRY(run_merge(c, k * c.L.C, chunk_rows(c, k), lse, nullptr, c.loss_rows));
     }
-    LCE_LAUNCH(launch_pairs(pair_params(offsets, pairs, N, V, ignore_index, y, c.loss_rows, ref_logprobs, beta,
-                                        label_smoothing, average, dloss, reduction, loss, seq_logprobs,
-                                        reinterpret_cast<float *>(c.ws + P.off_pair), coef, c.hdr), c.s));
+    PairParams pp = pair_params(offsets, pairs, N, V, ignore_index, y, c.loss_rows, ref_logprobs, beta, label_smoothing,
+                                average, dloss, reduction, loss, seq_logprobs,
+                                reinterpret_cast<float *>(c.ws + P.off_pair), coef, c.hdr);
+    pp.place = c.index ? reinterpret_cast<const int *>(c.ws + P.gather.off_place) : nullptr;
+    LCE_LAUNCH(launch_pairs(pp, c.s));
     if (!grad || n == 0) return LCE_OK;
     // the tile counters start again
     if (cudaMemsetAsync(c.hdr + HDR_COUNTERS, 0, c.L.hdr_bytes - sizeof(int) * HDR_COUNTERS, c.s) != cudaSuccess)
         return LCE_ERR_CUDA;
     c.coef = coef;
     __nv_bfloat16 *dHb = static_cast<__nv_bfloat16 *>(dH);
-    for (long long k = keep; k < n; ++k) {
-        use(k - keep);
-        LCE_TRY(run_prep(c, k * c.L.C, chunk_rows(c, k), nullptr, coef, c.loss_rows, c.Gb[k - keep], !frozen,
-                         (k - keep) * c.L.C));
+    for (long long k = 0; k < kept_n; ++k) {
+        use(k);
+        LCE_TRY(run_prep(c, k * c.L.C, chunk_rows(c, k), nullptr, coef, c.loss_rows, c.Gb[k], !frozen, k * c.L.C));
     }
-    for (long long k = keep; k < n; ++k) {
-        const long long j = k - keep, row0 = k * c.L.C, rows = chunk_rows(c, k);
+    for (long long k = 0; k < kept_n; ++k) {
+        const long long row0 = k * c.L.C, rows = chunk_rows(c, k);
         // (W trained, two chunks: the first one's dH alone, the second's beside one dW over both)
-        const bool alone = frozen || k + 1 < n;
-        const GradSpec g{c.Gb[j], c.Gb[0], alone ? 0 : j * c.L.C + rows, true, alone && (two || !frozen)};
+        const bool alone = frozen || k + 1 < kept_n;
+        const GradSpec g{c.Gb[k], c.Gb[0], alone ? 0 : row0 + rows, true, alone && (two || !frozen)};
         LCE_TRY(run_grad(c, row0, rows, static_cast<int>(2 * k + 1), dHb + row0 * c.D, acc_dh, dW, acc_dw0, coef,
                          g));
     }
     use(0);
-    return backward_chunks(c, keep, lse, coef, dHb, acc_dh, dW, true);
+    return backward_chunks(c, kept_n, n, lse, coef, dHb, acc_dh, dW, true);
 }
 
 lce_status lce_rmsnorm_forward(const void *X, const void *gamma, int64_t N, int64_t D, float eps,

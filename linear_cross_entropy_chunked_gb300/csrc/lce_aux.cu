@@ -38,6 +38,11 @@ __device__ __forceinline__ double warp_sum_d(double v) {
     return v;
 }
 
+// Rows that there are of a chunk at row0: all, or as many of the counting ones as lie in it.
+__device__ __forceinline__ int live_rows(const int *counting, int row0, int rows) {
+    return counting ? max(0, min(rows, *counting - row0)) : rows;
+}
+
 // ------------------------------------------------------------------ label scan
 
 __global__ void __launch_bounds__(1024) lce_label_scan_kernel(const long long *__restrict__ y,
@@ -156,6 +161,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_merge_kernel(const MergePar
     __shared__ float s_bcast;
     const int r = blockIdx.x;          // row within the chunk
     const int t = threadIdx.x;
+    if (r >= live_rows(p.counting, p.row0, p.rows)) return;
     const float2 *parts = p.parts + static_cast<size_t>(r) * p.nparts;
     const float lse = row_lse(parts, p.nparts, s_red, &s_bcast);
 
@@ -163,10 +169,12 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_merge_kernel(const MergePar
     const long long yv = p.y[grow];
     const bool y_ok = yv != p.ignore_index && yv >= 0 && yv < p.V;
     if (t == 0) {
+        const int of = p.index ? p.index[grow] : grow;   // the row of the call
         if (p.lse) p.lse[grow] = lse;
         const float logp = y_ok ? p.zy[r] - lse : 0.f;
-        if (p.pol.logp) p.pol.logp[grow] = logp;
-        p.loss_rows[grow] = !y_ok ? 0.f : p.pol.adv ? lce_policy_row(p.pol, grow, logp).loss : lse - p.zy[r];
+        if (p.pol.logp) p.pol.logp[of] = logp;
+        p.loss_rows[p.loss_by_index ? of : grow] =
+            !y_ok ? 0.f : p.pol.adv ? lce_policy_row(p.pol, of, logp).loss : lse - p.zy[r];
     }
 }
 
@@ -312,6 +320,15 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_prep_kernel(const PrepParam
     const int v0 = seg * PREP_VEC_PER_CTA;
     const int nv = min(PREP_VEC_PER_CTA, nvec - v0);      // > 0: segs covers nvec exactly
     uint4 *row = reinterpret_cast<uint4 *>(m.G + static_cast<size_t>(r) * p.ldg);
+    if (m.counting) {
+        // behind the rows there are: zeros as far as a k block of the dW contraction may reach
+        const int live = live_rows(m.counting, m.row0, m.rows);
+        if (r >= live) {
+            if (r < live + 64)
+                for (int v = threadIdx.x; v < nv; v += MERGE_THREADS) row[v0 + v] = make_uint4(0u, 0u, 0u, 0u);
+            return;
+        }
+    }
     if (threadIdx.x == 0) {
         s_abort = 0;
         mbar_init(&seg_bar, 1);
@@ -326,19 +343,19 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_prep_kernel(const PrepParam
     const int grow = m.row0 + r;
     const long long yv = m.y[grow];
     const bool y_ok = yv != m.ignore_index && yv >= 0 && yv < m.V;
-    float scale = lce_store_scale(m.dloss, m.dloss_per_row, m.mean, m.hdr[HDR_NVALID], grow, y_ok,
-                                  m.f16);
+    const int of = m.index ? m.index[grow] : grow;   // the row of the call
+    float scale = lce_store_scale(m.dloss, m.dloss_per_row, m.mean, m.hdr[HDR_NVALID], of, y_ok, m.f16);
     const float logp = y_ok ? m.zy[r] - lse : 0.f;
     float row_loss = y_ok ? lse - m.zy[r] : 0.f;
     if (m.pol.adv && y_ok) {
-        const PolicyRow pr = lce_policy_row(m.pol, grow, logp);
+        const PolicyRow pr = lce_policy_row(m.pol, of, logp);
         row_loss = pr.loss;
         scale *= -pr.slope * m.pol.inv_t;
     }
     if (seg == 0 && threadIdx.x == 0) {
         if (m.lse) m.lse[grow] = lse;
-        if (m.pol.logp) m.pol.logp[grow] = logp;
-        m.loss_rows[grow] = row_loss;
+        if (m.pol.logp) m.pol.logp[of] = logp;
+        m.loss_rows[m.loss_by_index ? of : grow] = row_loss;
     }
     const bool zero = m.zero_rows && scale == 0.f;
     const float lse2 = lse * LOG2E_F;
@@ -454,6 +471,102 @@ __global__ void __launch_bounds__(256) lce_combine_dh_kernel(const float *__rest
     }
 }
 
+// ------------------------------------------------------------------ rows that count
+// One CTA; each warp has a range of the labels, counts it, and (its first place known) goes over it again.
+__global__ void __launch_bounds__(1024) lce_compact_kernel(const long long *__restrict__ y, int N, long long V,
+                                                           long long ign, int *hdr, int *__restrict__ index,
+                                                           int *__restrict__ place, long long *__restrict__ labels) {
+    __shared__ int s_cnt[32], s_bad[32];
+    const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+    const int per = (N + 1023) / 1024 * 32;   // labels of a warp
+    const int lo = min(N, w * per), hi = min(N, lo + per);
+    int cnt = 0, bad = 0;
+#pragma unroll 4
+    for (int i = lo + l; i < hi; i += 32) {
+        const long long v = y[i];
+        const bool ok = v != ign && v >= 0 && v < V;
+        cnt += ok;
+        bad |= !ok && v != ign;
+    }
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    bad = __reduce_or_sync(0xffffffffu, bad);
+    if (l == 0) {
+        s_cnt[w] = cnt;
+        s_bad[w] = bad;
+    }
+    __syncthreads();
+    const int c = s_cnt[l];
+    int at = __reduce_add_sync(0xffffffffu, l < w ? c : 0);
+    const int all = __reduce_add_sync(0xffffffffu, c);
+    if (threadIdx.x == 0) {
+        int any = 0;
+        for (int k = 0; k < 32; ++k) any |= s_bad[k];
+        hdr[HDR_NVALID] = all;
+        if (any) hdr[HDR_FLAG] = FLAG_LABEL;
+    }
+#pragma unroll 4
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+        const int i = i0 + l;
+        const long long v = i < hi ? y[i] : ign;
+        const bool ok = v != ign && v >= 0 && v < V;
+        const unsigned mask = __ballot_sync(0xffffffffu, ok);
+        const int j = at + __popc(mask & ((1u << l) - 1u));
+        if (ok) {
+            index[j] = i;
+            labels[j] = v;
+        }
+        if (i < hi) place[i] = ok ? j : -1;
+        at += __popc(mask);
+    }
+    for (int j = all + threadIdx.x; j < N; j += 1024) labels[j] = ign;
+}
+
+__global__ void __launch_bounds__(256) lce_gather_rows_kernel(const uint4 *__restrict__ src, const int *__restrict__ index,
+                                                              const int *__restrict__ counting, int row0, int rows,
+                                                              int vecs, uint4 *__restrict__ dst) {
+    const int live = live_rows(counting, row0, rows);
+    const int end = min(rows, live + 64);
+    for (int r = blockIdx.x; r < end; r += gridDim.x) {
+        const bool there = r < live;
+        const uint4 *from = src + static_cast<size_t>(there ? index[row0 + r] : 0) * vecs;
+        uint4 *to = dst + static_cast<size_t>(r) * vecs;
+#pragma unroll 4
+        for (int v = threadIdx.x; v < vecs; v += 256) to[v] = there ? from[v] : make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+template <bool ACC>
+__global__ void __launch_bounds__(256) lce_scatter_dh_kernel(const float *__restrict__ src, int splits, long long stride,
+                                                             const int *__restrict__ index,
+                                                             const int *__restrict__ counting, int row0, int rows,
+                                                             int vecs, uint4 *__restrict__ dst) {
+    const int live = live_rows(counting, row0, rows);
+    const long long n = static_cast<long long>(live) * vecs;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += 256ll * gridDim.x) {
+        float4 a = reinterpret_cast<const float4 *>(src)[2 * i], b = reinterpret_cast<const float4 *>(src)[2 * i + 1];
+        for (int sp = 1; sp < splits; ++sp) {
+            const float4 *q = reinterpret_cast<const float4 *>(src + sp * stride);
+            const float4 c = q[2 * i], e = q[2 * i + 1];
+            a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
+            b.x += e.x; b.y += e.y; b.z += e.z; b.w += e.w;
+        }
+        const float s[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        uint4 *to = dst + static_cast<size_t>(index[row0 + i / vecs]) * vecs + i % vecs;
+        uint4 d = ACC ? *to : make_uint4(0u, 0u, 0u, 0u);
+        uint32_t *w = &d.x;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float lo = s[2 * q], hi = s[2 * q + 1];
+            if constexpr (ACC) {
+                lo += __uint_as_float(w[q] << 16);
+                hi += __uint_as_float(w[q] & 0xffff0000u);
+            }
+            w[q] = pack_bf16x2(lo, hi);
+        }
+        *to = d;
+    }
+}
+
 // ------------------------------------------------------------------ bounded-wait self-test
 // One warp waits, with the same bounded wait the pipelines use, on an mbarrier
 // that nothing signals; the wait runs out after limit_ns, records FLAG_TIMEOUT in
@@ -538,6 +651,34 @@ cudaError_t launch_combine_dh(const float *src, int splits, long long stride, vo
     else if (f16) lce_combine_dh_kernel<true, false><<<g, 256, 0, s>>>(src, splits, stride, dst, nvec);
     else if (accumulate) lce_combine_dh_kernel<false, true><<<g, 256, 0, s>>>(src, splits, stride, dst, nvec);
     else lce_combine_dh_kernel<false, false><<<g, 256, 0, s>>>(src, splits, stride, dst, nvec);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_compact(const long long *y, long long N, long long V, long long ign, int *hdr, int *index,
+                           int *place, long long *labels, cudaStream_t s) {
+    lce_compact_kernel<<<1, 1024, 0, s>>>(y, static_cast<int>(N), V, ign, hdr, index, place, labels);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_gather_rows(const __nv_bfloat16 *src, const int *index, const int *counting, long long row0,
+                               long long rows, long long D, __nv_bfloat16 *dst, int sms, cudaStream_t s) {
+    const int g = static_cast<int>(rows < 8ll * sms ? rows : 8ll * sms);
+    lce_gather_rows_kernel<<<g, 256, 0, s>>>(reinterpret_cast<const uint4 *>(src), index, counting,
+                                             static_cast<int>(row0), static_cast<int>(rows), static_cast<int>(D / 8),
+                                             reinterpret_cast<uint4 *>(dst));
+    return cudaGetLastError();
+}
+
+cudaError_t launch_scatter_dh(const float *src, int splits, long long stride, const int *index, const int *counting,
+                              long long row0, long long rows, long long D, __nv_bfloat16 *dst, bool accumulate,
+                              int sms, cudaStream_t s) {
+    long long blocks = (rows * (D / 8) + 255) / 256;
+    if (blocks > 8ll * sms) blocks = 8ll * sms;
+    const int g = static_cast<int>(blocks), r0 = static_cast<int>(row0), r = static_cast<int>(rows);
+    const int vecs = static_cast<int>(D / 8);
+    uint4 *to = reinterpret_cast<uint4 *>(dst);
+    if (accumulate) lce_scatter_dh_kernel<true><<<g, 256, 0, s>>>(src, splits, stride, index, counting, r0, r, vecs, to);
+    else lce_scatter_dh_kernel<false><<<g, 256, 0, s>>>(src, splits, stride, index, counting, r0, r, vecs, to);
     return cudaGetLastError();
 }
 

@@ -94,10 +94,34 @@ enum : int { TILE_MAIN = 0, TILE_DW = 1 };
 // of a split dH launch), then the many short dW tiles (n fastest, so the tiles
 // that share one G^T slab run together); the dynamic schedule lets the SMs
 // left over by the dH tiles start on dW at once.
+// What of a launch there is: all of it, or (rows that count brought together) as many rows as there are.
+struct Live {
+    int rows, m_blocks0, k_blocks1, total;
+};
+template <int CL> __device__ __forceinline__ Live live_part(const GemmParams &p) {
+    Live lv{p.rows, p.m_blocks0, p.k_blocks1, p.total_tiles};
+    if (p.counting) {
+        const int n = *p.counting;
+        lv.rows = max(0, min(p.rows, n - p.row0));
+        lv.m_blocks0 = min(p.m_blocks0, (lv.rows + BM - 1) / BM);
+        // (the first contraction writes dW: of no rows at all it takes one block, of zeros)
+        const int kr = max(0, min(p.dw_rows, n - p.dw_row0));
+        lv.k_blocks1 = p.k_blocks1 == 0 ? 0 : max(p.dw_accumulate ? 0 : 1, (kr + BK - 1) / BK);
+        if (p.m_blocks1 == 0 || lv.k_blocks1 > 0) {
+            const int splits = p.k_splits > 1 ? p.k_splits : 1;
+            const int rest = p.total_tiles - (p.m_blocks0 + CL - 1) / CL * p.n_blocks0 * splits;
+            lv.total = rest + (lv.m_blocks0 + CL - 1) / CL * p.n_blocks0 * splits;
+        } else {
+            lv.total = 0;   // (a dW launch of its own)
+        }
+    }
+    return lv;
+}
+
 template <int CL>
-__device__ __forceinline__ Tile decode_tile(const GemmParams &p, int t, int crank, bool wide) {
+__device__ __forceinline__ Tile decode_tile(const GemmParams &p, const Live &lv, int t, int crank, bool wide) {
     Tile tl;
-    const int mp0 = (p.m_blocks0 + CL - 1) / CL;
+    const int mp0 = (lv.m_blocks0 + CL - 1) / CL;
     const int nH1 = mp0 * p.n_blocks0;
     const int splits = p.k_splits > 1 ? p.k_splits : 1;
     if (t < nH1 * splits) {
@@ -121,7 +145,7 @@ __device__ __forceinline__ Tile decode_tile(const GemmParams &p, int t, int cran
         tl.n0 = (t % p.n_blocks1) * BN;
         tl.m0 = ((t / p.n_blocks1) * CL + crank) * BM;
         tl.kb0 = 0;
-        tl.nk = p.k_blocks1;
+        tl.nk = lv.k_blocks1;
         tl.srow = 0;
     }
     return tl;
@@ -223,13 +247,14 @@ struct WarpStager {
 };
 
 template <int MODE>
-__device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Tile &tl,
+__device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Live &lv, const Tile &tl,
                                                 uint32_t taddr, int quarter, int half,
                                                 const WarpStager &st) {
     const int r = tl.m0 + quarter * 32 + st.lane;  // row within the chunk
     const int box_y = tl.m0 + quarter * 32;
-    const bool box_rows = box_y < p.rows;       // warp-uniform: any row of the box exists
-    const bool row_ok = r < p.rows;
+    // warp-uniform: any row of the box exists (G: up to whole k blocks of the dW contraction, as zeros)
+    const bool box_rows = box_y < (MODE == MODE_G && p.counting ? (lv.rows + BK - 1) / BK * BK : lv.rows);
+    const bool row_ok = r < lv.rows;
     const int col0 = tl.n0 + half * 128;        // first vocabulary column of this half
     const int ncols = min(128, p.V - col0);     // valid columns (may be <= 0); same for the half
     long long yv = p.ignore_index;
@@ -310,13 +335,13 @@ __device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Tile 
 // Gradient tiles: dH (bf16 / fp16, or fp32 when dh_fp32) or dW (fp32, stored by
 // a call's first dW contraction, reduce-added into dW by the later ones). out_scale: the factor
 // fp16 calls apply here instead of in G (1 for bf16).
-__device__ __forceinline__ void epilogue_grad(const GemmParams &p, const Tile &tl, uint32_t taddr,
+__device__ __forceinline__ void epilogue_grad(const GemmParams &p, const Live &lv, const Tile &tl, uint32_t taddr,
                                               int half, const HalfStager &st, float out_scale) {
     const int col0 = tl.n0 + half * 128;
     if (col0 >= p.D) return;  // this half is past D (same for the 4 warps)
     // a tile entirely past the output rows (the second tile of a CTA pair at an
     // odd row-block count) stores nothing
-    if (tl.m0 >= (tl.type == TILE_MAIN ? p.rows : p.V)) return;
+    if (tl.m0 >= (tl.type == TILE_MAIN ? lv.rows : p.V)) return;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         float v[32];
@@ -448,6 +473,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
     if constexpr (CL == 2) cluster_sync_all();   // the peer's barriers exist from here on
     tc_fence_after();
     const uint32_t tmem_base = tmem_slot;
+    const Live lv = live_part<CL>(p);
 
     Abort ab;
     ab.flag_smem = &abort_flag;
@@ -490,7 +516,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
             int pending_raw = 0;  // leader: counter value fetched for the tile after that
             if (leader) {
                 const int f = atomicAdd(p.tile_counter, 1);
-                t_lead = f < p.total_tiles ? f : -1;
+                t_lead = f < lv.total ? f : -1;
                 ok = publish(t_lead);
                 if (ok && t_lead >= 0) pending_raw = atomicAdd(p.tile_counter, 1);
             }
@@ -500,7 +526,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
                     if (t_lead < 0) break;
                     // publish the next tile (fetched one tile ago), fetch the one after;
                     // the fetched value is first needed a tile from now
-                    const int nxt = pending_raw < p.total_tiles ? pending_raw : -1;
+                    const int nxt = pending_raw < lv.total ? pending_raw : -1;
                     if (!publish(nxt)) { ok = false; break; }
                     if (nxt >= 0) pending_raw = atomicAdd(p.tile_counter, 1);
                     t = t_lead;
@@ -512,7 +538,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
                     if (++sq == SCHED_DEPTH) { sq = 0; sphase ^= 1; }
                     if (t < 0) break;
                 }
-                const Tile tl = decode_tile<CL>(p, t, static_cast<int>(crank), MODE == MODE_DH);
+                const Tile tl = decode_tile<CL>(p, lv, t, static_cast<int>(crank), MODE == MODE_DH);
                 for (int kb = 0; kb < tl.nk; ++kb) {
                     if (!mbar_wait(&empty_bar[stage], phase ^ 1, ab)) { ok = false; break; }
                     uint8_t *sA = smem + stage * P::kStageBytes;
@@ -607,7 +633,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
                 release_on_leader(&sempty_bar[sq]);
                 if (++sq == SCHED_DEPTH) { sq = 0; sphase ^= 1; }
                 if (t < 0) break;
-                const Tile tl = decode_tile<CL>(p, t, 0, MODE == MODE_DH);
+                const Tile tl = decode_tile<CL>(p, lv, t, 0, MODE == MODE_DH);
                 if (!mbar_wait_cluster(&tempty_bar[acc], aphase ^ 1, ab)) { ok = false; break; }
                 // a wide dH tile accumulates into both buffers (acc is 0 at its start)
                 if (MODE == MODE_DH && !mbar_wait_cluster(&tempty_bar[1], aphase ^ 1, ab)) {
@@ -696,7 +722,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
             if (lane == 0) release_on_leader(&sempty_bar[sq]);
             if (++sq == SCHED_DEPTH) { sq = 0; sphase ^= 1; }
             if (t < 0) break;
-            const Tile tl = decode_tile<CL>(p, t, static_cast<int>(crank), MODE == MODE_DH);
+            const Tile tl = decode_tile<CL>(p, lv, t, static_cast<int>(crank), MODE == MODE_DH);
             ok = mbar_wait_cluster(&tfull_bar[acc], aphase, ab);
             if (!named_bar_and(st.bar_id, 128, ok)) break;
             tc_fence_after();
@@ -704,7 +730,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
                                    static_cast<uint32_t>(acc * BN + half * 128);
             if constexpr (MODE == MODE_DH) {
                 // both accumulators of the wide tile: columns n0 .. n0 + 255, then + 256
-                epilogue_grad(p, tl, taddr, half, st, out_scale);
+                epilogue_grad(p, lv, tl, taddr, half, st, out_scale);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) release_on_leader(&tempty_bar[0]);
@@ -713,7 +739,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
                 tc_fence_after();
                 Tile tl2 = tl;
                 tl2.n0 += BN;
-                epilogue_grad(p, tl2, taddr + BN, half, st, out_scale);
+                epilogue_grad(p, lv, tl2, taddr + BN, half, st, out_scale);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) release_on_leader(&tempty_bar[1]);
@@ -721,9 +747,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
                 continue;
             }
             if constexpr (MODE != MODE_BWD && MODE != MODE_DH) {
-                epilogue_logits<MODE>(p, tl, taddr, quarter, half, wst);
+                epilogue_logits<MODE>(p, lv, tl, taddr, quarter, half, wst);
             } else {
-                epilogue_grad(p, tl, taddr, half, st, out_scale);
+                epilogue_grad(p, lv, tl, taddr, half, st, out_scale);
             }
             tc_fence_before();
             __syncwarp();

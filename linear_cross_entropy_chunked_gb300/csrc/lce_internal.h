@@ -202,6 +202,10 @@ struct GemmParams {
     int k_splits, kb_per_split, split_rows;
     int f16;               // 1: fp16 operands (H, W, G) and fp16 P' / G / dH stores
     float inv_t;           // the logits are multiplied by it in the logits epilogues (1 / temperature)
+    // Rows that count brought together (null: all `rows` are there): their number on the device. Tiles and
+    // contractions then end with the rows there are; dw_row0 and dw_rows: the rows of the dW contraction.
+    const int *counting;
+    int dw_row0, dw_rows;
     unsigned long long timeout_ns;
 };
 
@@ -223,6 +227,11 @@ struct MergeParams {
     float *loss_rows;      // global [N] (the caller's loss vector for reduction none)
     PolicyParams pol;      // pol.adv: the policy loss in place of the cross-entropy
     int zero_rows;         // 1: rows of G whose scale is 0 become zeros whatever P' holds
+    // rows that count brought together: their number (null: all are there), and which row of the call each
+    // is (null: the same), by which the policy's vectors, its outputs and a per-row dloss go
+    const int *counting;
+    const int *index;
+    int loss_by_index;     // 1: loss_rows too
 };
 
 struct TransposeParams {
@@ -301,6 +310,7 @@ struct PairParams {
     long long pairs, N, V, ignore_index;
     const long long *y;
     const float *loss_rows;     // [N]: -log p of each counting row
+    const int *place;           // null, or where row i of the call is in loss_rows and coef
     const float *ref;           // [2 pairs] or null (0)
     float beta, smoothing;
     int average;                // log probabilities per counting row
@@ -505,6 +515,17 @@ cudaError_t ce_set_attributes();
 cudaError_t launch_wait_selftest(int *hdr, unsigned long long limit_ns, cudaStream_t s);
 // dst[i] (bf16 / fp16, n elements) = (accumulate ? dst[i] : 0) + the sum over
 // s = 0 .. splits-1, in that order, of src[s * stride + i] (fp32)
+// The rows that count: index[j] = the j-th one, place[i] = where row i is among them (-1: it does not count),
+// labels[j] its label (ignore_index behind the last), their number and the range check into hdr.
+cudaError_t launch_compact(const long long *y, long long N, long long V, long long ign, int *hdr, int *index,
+                           int *place, long long *labels, cudaStream_t s);
+// dst[j][D] = src[index[row0 + j]][D] for the rows there are of [row0, row0 + rows), zeros up to a multiple of 64
+cudaError_t launch_gather_rows(const __nv_bfloat16 *src, const int *index, const int *counting, long long row0,
+                               long long rows, long long D, __nv_bfloat16 *dst, int sms, cudaStream_t s);
+// dst[index[row0 + j]] = (accumulate ? that : 0) + the sum over s of src[s * stride + j D ..], as launch_combine_dh
+cudaError_t launch_scatter_dh(const float *src, int splits, long long stride, const int *index, const int *counting,
+                              long long row0, long long rows, long long D, __nv_bfloat16 *dst, bool accumulate,
+                              int sms, cudaStream_t s);
 cudaError_t launch_combine_dh(const float *src, int splits, long long stride, void *dst,
                               long long n, bool f16, bool accumulate, int sms, cudaStream_t s);
 cudaError_t launch_rmsnorm_fwd(const NormParams &p, cudaStream_t s);

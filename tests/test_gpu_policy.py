@@ -259,6 +259,46 @@ def test_head(n, d, v, chunk, mode):
     assert torch.equal(lp2, logprobs) and torch.equal(l2, loss)
 
 
+@pytest.mark.parametrize("ignored", [0.0, 0.5, 0.97, 2.0])
+@pytest.mark.parametrize("n,chunk", [(300, 1024), (700, 128), (1000, 64), (1000, 192), (513, 512), (257, 64)])
+@pytest.mark.parametrize("mode", ["train", "frozen", "low"])
+def test_rows_brought_together(n, chunk, mode, ignored):
+    # more rows than a tile has: those that count come first, whole chunks may be empty, the last k block of the
+    # weight's contraction is part rows and part nothing; what rows that do not count hold stays there
+    d, v = 72, 333
+    H, W, Z, y, a, old, ref, w = head(n, d, v, n + chunk, ignored=ignored)
+    H[y < 0] = math.nan
+    if ignored == 0.97:
+        y[: n // 2] = -100
+    how = dict(beta=0.05, temperature=0.9)
+    args = [t.cuda() for t in (H, W, y, a, old, ref, w)]
+    kw = dict(chunk=chunk, compute_dW=mode != "frozen", low_memory=mode == "low")
+    loss, logprobs, dH, dW = lce.policy_fwd_bwd(*args, **how, **kw)
+    Z = np.nan_to_num(Z)
+    o = ao.policy(Z, y.numpy(), a.numpy(), old.numpy(), ref.numpy(), w.numpy(), **how)
+    Hz = torch.nan_to_num(H.double())
+    lb = logp_bound(Z, 0.9, v) + 2 * (2 * d + 8) * 2.0 ** -24 * float((Hz.abs() @ W.double().abs().t()).max()) / 0.9
+    assert np.abs(cpu64(logprobs) - o["logprobs"]).max() <= lb
+    assert abs(loss.item() - o["loss"]) <= (2 * lb + 2.0 ** -20) * o["terms"].sum() / max(1, o["ok"].sum())
+    check_gradients(dH, dW, Hz, W, with_coefs(o, y, o["mass"]), lb)
+    assert not dH[y < 0].any()
+    again = lce.policy_fwd_bwd(*args, **how, **kw)
+    assert all(p is q or torch.equal(p, q) for p, q in zip(again, (loss, logprobs, dH, dW)))
+    rows, lp, _, _ = lce.policy_fwd_bwd(*args, **how, **kw, reduction="none")
+    assert torch.equal(lp, logprobs) and not rows[y < 0].any()
+    assert abs(rows.double().sum().item() / max(1, o["ok"].sum()) - o["loss"]) <= 1e-5 * (1 + o["terms"].sum())
+    assert torch.equal(lce.policy_forward(*args, **how, chunk=chunk)[1], logprobs)
+    if mode == "train":
+        more = [torch.ones(n, d, dtype=torch.bfloat16, device="cuda"), torch.ones_like(dW)]
+        lce.policy_fwd_bwd(*args, **how, chunk=chunk, dH=more[0], dW=more[1], accumulate=("dH", "dW"))
+        # every contraction (of a chunk or two) adds to values near 1, each time within 2^-24 of them, here and
+        # once more in this comparison
+        adds = -(-n // chunk) + 2
+        assert (more[1] - 1 - dW).abs().max() <= adds * 2.0 ** -24 * (1 + 2 * dW.abs().max())
+        assert (more[0].float() - 1 - dH.float()).abs().max() <= 2.0 ** -8 * (1.01 + dH.float().abs().max())
+        assert (more[0][y < 0] == 1).all()
+
+
 @pytest.mark.parametrize("n,chunk", [(90, 1024), (300, 64)])
 def test_head_accumulates_and_reduces(n, chunk):
     H, W, Z, y, a, old, ref, w = head(n, 64, 700, n)
