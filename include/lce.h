@@ -259,7 +259,8 @@ lce_status lce_ce_logits(const void *Z, int z_dtype, int64_t ld, const int64_t *
  * lce_policy_fwd_bwd: over the head, as lce_fwd_bwd_opt (6 N D V flops, chunk by chunk, the
  * logits never in memory; flags but LCE_INPUT_FP16, for whose gradients the c_i have no
  * known range: LCE_ERR_UNSUPPORTED). The rows that count are brought together first (more than 256 rows, and
- * one chunk or chunks of a multiple of 64 rows): the others cost nothing. Workspace:
+ * one chunk or chunks of a multiple of 64 rows): the others cost nothing. `chunk` says how much memory is taken, as
+ * for lce_fwd_bwd_opt: without LCE_LOW_MEMORY a chunk buffer of 2 chunk rows. Workspace:
  * lce_policy_workspace_size (gradient = 1).
  * lce_policy_forward: loss and logprobs alone, workspace with gradient = 0.
  * lce_policy_logits: over given logits (z_dtype as for lce_ce_logits): one read of the

@@ -134,7 +134,8 @@ def policy_fwd_bwd(H, W, y, advantages, old_logprobs=None, ref_logprobs=None, we
         loss = w (-min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A) + beta (e^d - 1 - d)),  d = ref - logp
     reduction: the mean over the counting rows, "sum" (a mean over sequences has its weights
     1 / (tokens * sequences)), or "none" (loss [N]; dloss [N]). logprobs [N]: logp, 0 for rows that
-    do not count. dH bf16, dW fp32. The rest as for lce_fwd_bwd."""
+    do not count. dH bf16, dW fp32. chunk: the memory / speed knob: a buffer of 2 chunk rows of logits (low_memory:
+    chunk rows). The rest as for lce_fwd_bwd."""
     N, D, V = _check_head(H, W, y)
     dev, red = H.device, _b._reduction(reduction)
     args = _policy_args(N, dev, advantages, old_logprobs, ref_logprobs, weights, clip_low, clip_high, beta,

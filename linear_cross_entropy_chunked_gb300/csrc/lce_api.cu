@@ -828,13 +828,13 @@ inline long long chunk_rows(const Ctx &c, long long k) {
 // Whether chunks are taken in pairs with one dW contraction per pair: CTA pairs,
 // a dW contraction, two chunk buffers (so more than one chunk), H in place.
 inline bool paired(const Ctx &c, bool h_chunked_ok = false) {
-    return c.pairs > 0 && !c.L.frozen_w && c.L.nbuf == 2 && (h_chunked_ok || !c.h_chunked || c.index);
+    return c.pairs > 0 && !c.L.frozen_w && c.L.nbuf == 2 && (h_chunked_ok || !c.h_chunked);
 }
 
 // W frozen with two chunk buffers: chunk k+1's logits tiles run on the CTA pairs
 // chunk k's dH tiles leave free (chunk k in buffer k % 2).
 inline bool frozen_overlapped(const Ctx &c) {
-    return c.pairs > 0 && c.L.frozen_w && c.L.nbuf == 2 && (!c.h_chunked || c.index);
+    return c.pairs > 0 && c.L.frozen_w && c.L.nbuf == 2 && !c.h_chunked;
 }
 
 // The rows of chunk k that count into their place of H's buffer (nothing to do where H is read in place).
@@ -847,9 +847,18 @@ lce_status bring_rows(const Ctx &c, long long k) {
     return LCE_OK;
 }
 
+// Losses on answers have one chunk buffer. Where a cross-entropy call of that chunk would have two
+// (no LCE_LOW_MEMORY) it holds twice the rows: the same memory, and what two chunks are split in for (the logits
+// of one beside dH of the other) weighs less than contractions of twice the rows do where the rows that count are
+// few: 1072 of 1531 rows x 50257 x 1600 under a frozen head 553 -> MEASURED us.
+long long answer_chunk(long long N, long long chunk, int flags) {
+    if (chunk <= 0 || N <= 0 || chunk >= N) return chunk;
+    return (flags & LCE_LOW_MEMORY) ? chunk : chunk > N / 2 ? N : 2 * chunk;
+}
+
 // Losses on answers bring the rows that count together (prompts and padding are often half of a batch, and their
-// rows cost as much as the others'): which rows they are, their labels, and a chunk's rows of H (a pair's with two
-// chunk buffers), at byte `at` of the workspace. Not done for so few rows that no tile of 256 would be saved, and
+// rows cost as much as the others'): which rows they are, their labels, and a chunk's rows of H, at byte `at` of the
+// workspace. Not done for so few rows that no tile of 256 would be saved, and
 // not where chunks do not end on k blocks of the dW contraction.
 struct GatherLayout {
     bool on = false;
@@ -869,7 +878,7 @@ GatherLayout gather_layout(const Layout &L, long long N, long long D, size_t at)
     g.off_index = take(sizeof(int) * static_cast<size_t>(N));
     g.off_place = take(sizeof(int) * static_cast<size_t>(N));
     g.off_labels = take(sizeof(long long) * static_cast<size_t>(N));
-    g.off_H = take(2 * static_cast<size_t>(L.nbuf) * L.C * static_cast<size_t>(D));
+    g.off_H = take(2 * static_cast<size_t>(L.C) * static_cast<size_t>(D));
     return g;
 }
 
@@ -898,18 +907,15 @@ lce_status start_gather(Ctx &c, const GatherLayout &g, const void *H, const int6
         if (cudaMemsetAsync((ptr), 0, (bytes), c.s) != cudaSuccess) return LCE_ERR_CUDA; \
     } while (0)
 
-// The gradients of chunks `first` .. n - 1 (first even where chunks go in pairs) from a saved lse: each chunk's logits again, G straight
+// The gradients of chunks `first` (0 with two chunk buffers) .. n - 1 from a saved lse: each chunk's logits again, G straight
 // from their epilogue, then the contractions. acc_dw0: dW is added to from the first one on.
 lce_status backward_chunks(const Ctx &c, long long first, long long n, const float *lse, const float *dloss,
                            __nv_bfloat16 *dHb, bool acc_dh, float *dW, bool acc_dw0) {
     if (n <= first) return LCE_OK;
     if (frozen_overlapped(c)) {
-        LCE_TRY(bring_rows(c, first));
-        LCE_TRY(run_logits(c, MODE_G, first * c.L.C, chunk_rows(c, first), static_cast<int>(2 * first), lse, dloss,
-                           c.Gb[0]));
-        for (long long k = first; k < n; ++k) {
+        LCE_TRY(run_logits(c, MODE_G, 0, chunk_rows(c, 0), 0, lse, dloss, c.Gb[0]));
+        for (long long k = 0; k < n; ++k) {
             const long long r0 = k * c.L.C, n0 = chunk_rows(c, k);
-            if (k + 1 < n) LCE_TRY(bring_rows(c, k + 1));
             GradSpec g{c.Gb[k & 1], c.Gb[k & 1], 0, true, true};
             LogitsSpec next{};
             if (k + 1 < n) {
@@ -927,12 +933,10 @@ lce_status backward_chunks(const Ctx &c, long long first, long long n, const flo
         // columns 0..C-1; a's dH tiles, with b's logits (G into buffer 1) on the pairs
         // they leave free; b's H^T into columns C.., then b's dH beside one dW
         // contraction over both chunks (K = C + rows_b). An odd last chunk runs by itself.
-        for (long long a = first; a < n; a += 2) {
+        for (long long a = 0; a < n; a += 2) {
             const long long ra = a * c.L.C, na = chunk_rows(c, a);
             const bool has_b = a + 1 < n;
             const bool acc = a > 0 || acc_dw0;
-            LCE_TRY(bring_rows(c, a));
-            if (has_b) LCE_TRY(bring_rows(c, a + 1));
             LCE_TRY(run_logits(c, MODE_G, ra, na, static_cast<int>(2 * a), lse, dloss, c.Gb[0]));
             LCE_TRY(run_transpose(c, ra, na, 0));
             if (!has_b) {
@@ -1128,7 +1132,8 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
         (lse && !aligned16(lse)))
         return LCE_ERR_ALIGNMENT;
     const bool acc_dh = (flags & LCE_ACCUMULATE_DH) != 0;
-    const bool low_mem = (flags & LCE_LOW_MEMORY) != 0;
+    const bool low_mem = pol || (flags & LCE_LOW_MEMORY) != 0;
+    if (pol) chunk = answer_chunk(N, chunk, flags);
     Layout L0;
     if (!make_layout(N, D, V, chunk, L0, frozen, low_mem)) return LCE_ERR_INVALID_ARG;
     if (acc_dh && ws_bytes < L0.total + acc_dh_bytes(L0, D)) return LCE_ERR_WORKSPACE;
@@ -1169,12 +1174,10 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
     if (frozen_overlapped(c)) {
         // chunk k's dH tiles, with chunk k+1's logits (P' into buffer (k+1) % 2) on
         // the pairs they leave free; then chunk k+1's prep (no H^T: no dW)
-        LCE_TRY(bring_rows(c, 0));
         LCE_TRY(run_logits(c, MODE_LSE_P, 0, chunk_rows(c, 0), 0, nullptr, nullptr, c.Gb[0]));
         LCE_TRY(run_prep(c, 0, chunk_rows(c, 0), lse, dloss, rows_out, c.Gb[0], false));
         for (long long k = 0; k < c.L.nchunks; ++k) {
             const long long r0 = k * c.L.C, n0 = chunk_rows(c, k);
-            if (k + 1 < c.L.nchunks) LCE_TRY(bring_rows(c, k + 1));
             GradSpec g{c.Gb[k & 1], c.Gb[k & 1], 0, true, true};
             LogitsSpec next{};
             if (k + 1 < c.L.nchunks) {
@@ -1198,8 +1201,6 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
             const long long ra = a * c.L.C, na = chunk_rows(c, a);
             const bool has_b = a + 1 < c.L.nchunks;
             const bool acc = a > 0 || acc_dw0;
-            LCE_TRY(bring_rows(c, a));
-            if (has_b) LCE_TRY(bring_rows(c, a + 1));
             LCE_TRY(run_logits(c, MODE_LSE_P, ra, na, static_cast<int>(2 * a), nullptr, nullptr,
                                c.Gb[0]));
             LCE_TRY(run_prep(c, ra, na, lse, dloss, rows_out, c.Gb[0], true, 0));
@@ -1272,18 +1273,17 @@ PolicyParams policy_params(const float *advantages, const float *old_logprobs, c
 }
 
 // Workspace of a preference over the head: the loss path's layout (the forward's share of it
-// without gradients), then lse and the coefficient of each row, the pairs' losses, and the slab
-// partials and target logits of a second chunk that is kept between the phases.
+// without gradients), then lse and the coefficient of each row, and the pairs' losses.
 struct PrefLayout {
     Layout L;
     GatherLayout gather;
-    size_t off_lse = 0, off_coef = 0, off_pair = 0, off_parts = 0, off_zy = 0, total = 0;
+    size_t off_lse = 0, off_coef = 0, off_pair = 0, total = 0;
 };
 
+// (chunk: as answer_chunk has it)
 bool make_pref_layout(int64_t N, int64_t D, int64_t V, int64_t chunk, int64_t pairs, int flags, bool grad,
                       PrefLayout &P) {
-    const bool frozen = (flags & LCE_FROZEN_W) != 0, low_mem = (flags & LCE_LOW_MEMORY) != 0;
-    if (!make_layout(N, D, V, chunk, P.L, frozen, low_mem) || pairs <= 0 || pairs > (1ll << 24)) return false;
+    if (!make_layout(N, D, V, chunk, P.L, (flags & LCE_FROZEN_W) != 0, true) || pairs <= 0 || pairs > (1ll << 24)) return false;
     const size_t rows = sizeof(float) * static_cast<size_t>(N > 0 ? N : 1);
     P.gather = gather_layout(P.L, N, D, grad ? P.L.total + acc_dh_bytes(P.L, D) : P.L.fwd_total);
     size_t off = P.gather.end;
@@ -1294,13 +1294,7 @@ bool make_pref_layout(int64_t N, int64_t D, int64_t V, int64_t chunk, int64_t pa
     };
     P.off_lse = take(rows);
     P.off_pair = take(sizeof(float) * static_cast<size_t>(pairs));
-    if (grad) {
-        P.off_coef = take(rows);
-        if (P.L.nbuf == 2) {
-            P.off_parts = take(sizeof(float2) * static_cast<size_t>(P.L.C) * P.L.nparts);
-            P.off_zy = take(sizeof(float) * static_cast<size_t>(P.L.C));
-        }
-    }
+    if (grad) P.off_coef = take(rows);
     P.total = off;
     return true;
 }
@@ -1630,7 +1624,7 @@ lce_status lce_policy_workspace_size(int64_t N, int64_t D, int64_t V, int64_t ch
                                      size_t *bytes) {
     Layout L;
     if (!bytes || (flags & ~LCE_FLAGS_ALL) ||
-        !make_layout(N, D, V, chunk, L, gradient && (flags & LCE_FROZEN_W), gradient && (flags & LCE_LOW_MEMORY)))
+        !make_layout(N, D, V, gradient ? answer_chunk(N, chunk, flags) : chunk, L, (flags & LCE_FROZEN_W) != 0, true))
         return LCE_ERR_INVALID_ARG;
     *bytes = gather_layout(L, N, D, gradient ? L.total + acc_dh_bytes(L, D) : L.fwd_total).end;
     return LCE_OK;
@@ -1649,14 +1643,14 @@ lce_status lce_policy_forward(const void *H, const void *W, const int64_t *y, co
     LCE_TRY(policy_check(N, advantages, old_logprobs, ref_logprobs, weights, clip_low, clip_high, beta,
                          temperature, logprobs));
     Layout L0;
-    if (!make_layout(N, D, V, chunk, L0)) return LCE_ERR_INVALID_ARG;
+    if (!make_layout(N, D, V, chunk, L0, false, true)) return LCE_ERR_INVALID_ARG;
     const GatherLayout gl = gather_layout(L0, N, D, L0.fwd_total);
     if (gl.on && ws_bytes < gl.end) return LCE_ERR_WORKSPACE;
     const void *Hs = H;
     const int64_t *ys = y;
     LCE_TRY(gather_inputs(gl, Hs, ys, ws));
     Ctx c;
-    LCE_TRY(setup(c, Hs, W, ys, N, D, V, ignore_index, chunk, ws, ws_bytes, stream, gl.on, false, false, true, false,
+    LCE_TRY(setup(c, Hs, W, ys, N, D, V, ignore_index, chunk, ws, ws_bytes, stream, gl.on, false, false, true, true,
                   !gl.on));
     c.reduction = reduction;
     LCE_TRY(start_gather(c, gl, H, y));
@@ -1700,15 +1694,15 @@ lce_status lce_preference_workspace_size(int64_t N, int64_t D, int64_t V, int64_
                                          int gradient, size_t *bytes) {
     PrefLayout P;
     if (!bytes || (flags & ~LCE_FLAGS_ALL) ||
-        !make_pref_layout(N, D, V, chunk, pairs, flags, gradient != 0, P))
+        !make_pref_layout(N, D, V, gradient ? answer_chunk(N, chunk, flags) : chunk, pairs, flags, gradient != 0, P))
         return LCE_ERR_INVALID_ARG;
     *bytes = P.total;
     return LCE_OK;
 }
 
-// Phases: every chunk's logits and the rows' log probabilities; the pairs; the gradients. The first chunks (as many
-// as there are chunk buffers) come last in the first phase and stay in their buffers over the pairs, so
-// that their logits are not computed again: with no more rows than the buffers hold, none are.
+// Phases: every chunk's logits and the rows' log probabilities; the pairs; the gradients. The first chunk comes last in
+// the first phase and stays in the chunk buffer over the pairs, so that its logits are not computed
+// again: with no more rows than the buffer holds, none are.
 lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y, const int64_t *offsets,
                                   int64_t pairs, const float *ref_logprobs, float beta, float label_smoothing,
                                   int average, const float *dloss, int64_t N, int64_t D, int64_t V,
@@ -1721,12 +1715,12 @@ lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y
     const bool grad = dH != nullptr || dW != nullptr;
     const bool frozen = (flags & LCE_FROZEN_W) != 0 || !grad;
     const bool acc_dh = (flags & LCE_ACCUMULATE_DH) != 0, acc_dw0 = (flags & LCE_ACCUMULATE_DW) != 0;
-    const bool low_mem = (flags & LCE_LOW_MEMORY) != 0;
     if ((flags & LCE_FROZEN_W) && acc_dw0) return LCE_ERR_INVALID_ARG;
     LCE_TRY(preference_check(offsets, pairs, ref_logprobs, beta, label_smoothing, reduction, dloss, loss,
                              seq_logprobs));
     if (grad && ((N > 0 && !dH) || (!frozen && !dW))) return LCE_ERR_INVALID_ARG;
     if ((dH && !aligned16(dH)) || (dW && !aligned16(dW))) return LCE_ERR_ALIGNMENT;
+    if (grad) chunk = answer_chunk(N, chunk, flags);
     PrefLayout P;
     if (!make_pref_layout(N, D, V, chunk, pairs, flags, grad, P)) return LCE_ERR_INVALID_ARG;
     if (!ws) return LCE_ERR_INVALID_ARG;
@@ -1736,7 +1730,7 @@ lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y
     LCE_TRY(gather_inputs(P.gather, Hs, ys, ws));
     Ctx c;
     LCE_TRY(setup(c, Hs, W, ys, N, D, V, ignore_index, chunk, ws, ws_bytes, stream, P.gather.on, false,
-                  (flags & LCE_FROZEN_W) != 0, !grad, low_mem, !P.gather.on));
+                  (flags & LCE_FROZEN_W) != 0, !grad, true, !P.gather.on));
     LCE_TRY(start_gather(c, P.gather, H, y));
     if (P.gather.on && grad && !acc_dh) LCE_ZERO(dH, 2 * static_cast<size_t>(N) * static_cast<size_t>(D));
     c.reduction = LCE_REDUCTION_NONE;   // (of the rows: each has a coefficient of its own)
@@ -1748,26 +1742,11 @@ lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y
     if (n == 0 && dW && !acc_dw0 &&
         cudaMemsetAsync(dW, 0, sizeof(float) * static_cast<size_t>(V) * D, c.s) != cudaSuccess)
         return LCE_ERR_CUDA;
-    // the first `kept_n` chunks stay in the buffers: a pair, or one
-    const bool two = grad && (paired(c) || frozen_overlapped(c));
-    const long long kept_n = !grad ? 0 : n < (two ? 2 : 1) ? n : (two ? 2 : 1);
-    struct Kept {
-        float2 *parts;
-        float *zy;
-    };
-    const Kept kept[2] = {{c.parts, c.zy},
-                          {reinterpret_cast<float2 *>(c.ws + P.off_parts), reinterpret_cast<float *>(c.ws + P.off_zy)}};
-    auto use = [&](long long j) {
-        c.parts = kept[j].parts;
-        c.zy = kept[j].zy;
-    };
     for (long long i = 0; i < n; ++i) {
-        const long long k = i + kept_n < n ? i + kept_n : i + kept_n - n;   // the kept ones last
-        const bool stays = k < kept_n;
-        use(stays ? k : 0);
+        const long long k = !grad || i + 1 < n ? (grad ? i + 1 : i) : 0;   // (with gradients the first chunk last)
         LCE_TRY(bring_rows(c, k));
-        LCE_TRY(run_logits(c, stays ? MODE_LSE_P : MODE_LSE, k * c.L.C, chunk_rows(c, k), static_cast<int>(k), nullptr,
-                           nullptr, c.Gb[stays ? k : 0]));
+        LCE_TRY(run_logits(c, grad && k == 0 ? MODE_LSE_P : MODE_LSE, k * c.L.C, chunk_rows(c, k), static_cast<int>(k),
+                           nullptr, nullptr, c.Gb[0]));
         LCE_TRY(run_merge(c, k * c.L.C, chunk_rows(c, k), lse, nullptr, c.loss_rows));
     }
     PairParams pp = pair_params(offsets, pairs, N, V, ignore_index, y, c.loss_rows, ref_logprobs, beta, label_smoothing,
@@ -1781,20 +1760,11 @@ lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y
         return LCE_ERR_CUDA;
     c.coef = coef;
     __nv_bfloat16 *dHb = static_cast<__nv_bfloat16 *>(dH);
-    for (long long k = 0; k < kept_n; ++k) {
-        use(k);
-        LCE_TRY(run_prep(c, k * c.L.C, chunk_rows(c, k), nullptr, coef, c.loss_rows, c.Gb[k], !frozen, k * c.L.C));
-    }
-    for (long long k = 0; k < kept_n; ++k) {
-        const long long row0 = k * c.L.C, rows = chunk_rows(c, k);
-        // (W trained, two chunks: the first one's dH alone, the second's beside one dW over both)
-        const bool alone = frozen || k + 1 < kept_n;
-        const GradSpec g{c.Gb[k], c.Gb[0], alone ? 0 : row0 + rows, true, alone && (two || !frozen)};
-        LCE_TRY(run_grad(c, row0, rows, static_cast<int>(2 * k + 1), dHb + row0 * c.D, acc_dh, dW, acc_dw0, coef,
-                         g));
-    }
-    use(0);
-    return backward_chunks(c, kept_n, n, lse, coef, dHb, acc_dh, dW, true);
+    const long long rows = chunk_rows(c, 0);
+    LCE_TRY(run_prep(c, 0, rows, nullptr, coef, c.loss_rows, c.Gb[0], !frozen));
+    LCE_TRY(run_grad(c, 0, rows, 1, dHb, acc_dh, dW, acc_dw0, coef,
+                     GradSpec{c.Gb[0], c.Gb[0], frozen ? 0 : rows, true, false}));
+    return backward_chunks(c, 1, n, lse, coef, dHb, acc_dh, dW, true);
 }
 
 lce_status lce_rmsnorm_forward(const void *X, const void *gamma, int64_t N, int64_t D, float eps,
