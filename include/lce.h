@@ -170,6 +170,7 @@ lce_status lce_fwd_bwd_ex(const void *H, const void *W, const int64_t *y, const 
  * ignores LCE_LOW_MEMORY: the forward keeps no chunk buffer). Other arguments and
  * outputs as for the _ex entry points. */
 enum {
+    LCE_DW_BF16 = 32,      /* losses on answers only */
     LCE_ACCUMULATE_DW = 1,
     LCE_ACCUMULATE_DH = 2,
     LCE_INPUT_FP16 = 4,
@@ -262,6 +263,8 @@ lce_status lce_ce_logits(const void *Z, int z_dtype, int64_t ld, const int64_t *
  * one chunk or chunks of a multiple of 64 rows): the others cost nothing. `chunk` says how much memory is taken, as
  * for lce_fwd_bwd_opt: without LCE_LOW_MEMORY a chunk buffer of 2 chunk rows. Workspace:
  * lce_policy_workspace_size (gradient = 1).
+ * LCE_DW_BF16: dW is bf16, rounded once from the fp32 sums; where the rows fill one chunk buffer (N <= 2 chunk;
+ * chunk with LCE_LOW_MEMORY), W is trained and dW not added to, else LCE_ERR_UNSUPPORTED.
  * lce_policy_forward: loss and logprobs alone, workspace with gradient = 0.
  * lce_policy_logits: over given logits (z_dtype as for lce_ce_logits): one read of the
  * counting rows and one write of dZ (NULL: no gradient; Z itself: in place), V up to 450000 (16-bit) or
@@ -279,7 +282,7 @@ lce_status lce_policy_fwd_bwd(const void *H, const void *W, const int64_t *y, co
                               float clip_low, float clip_high, float beta, float temperature,
                               const float *dloss, int64_t N, int64_t D, int64_t V, int64_t ignore_index,
                               int64_t chunk, int reduction, int flags, float *loss, float *logprobs, void *dH,
-                              float *dW, void *ws, size_t ws_bytes, lce_stream_t stream);
+                              void *dW, void *ws, size_t ws_bytes, lce_stream_t stream);
 lce_status lce_policy_logits(const void *Z, int z_dtype, int64_t ld, const int64_t *y, const float *advantages,
                              const float *old_logprobs, const float *ref_logprobs, const float *weights,
                              float clip_low, float clip_high, float beta, float temperature, const float *dloss,
@@ -311,7 +314,7 @@ lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y
                                   int64_t pairs, const float *ref_logprobs, float beta, float label_smoothing,
                                   int average, const float *dloss, int64_t N, int64_t D, int64_t V,
                                   int64_t ignore_index, int64_t chunk, int reduction, int flags, float *loss,
-                                  float *seq_logprobs, void *dH, float *dW, void *ws, size_t ws_bytes,
+                                  float *seq_logprobs, void *dH, void *dW, void *ws, size_t ws_bytes,
                                   lce_stream_t stream);
 lce_status lce_preference_logits_workspace_size(int64_t N, int64_t pairs, size_t *bytes);
 lce_status lce_preference_logits(const void *Z, int z_dtype, int64_t ld, const int64_t *y, const int64_t *offsets,

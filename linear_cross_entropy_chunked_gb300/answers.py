@@ -10,6 +10,8 @@ from torch.autograd.function import once_differentiable
 
 from . import _binding as _b
 
+DW_BF16 = 32
+
 
 def _vector(name, t, shape, dtype, dev):
     """Address of a constant of the call (None for None)."""
@@ -115,16 +117,21 @@ def policy_forward(H, W, y, advantages, old_logprobs=None, ref_logprobs=None, we
     return loss, logprobs
 
 
-def _gradients(out, H, W, dH, dW, accumulate, compute_dW, low_memory):
+def _gradients(out, H, W, dH, dW, accumulate, compute_dW, low_memory, dW_dtype):
+    if dW_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("dW_dtype must be float32 or bfloat16")
     flags = _b._acc_flags(accumulate, dH, dW, compute_dW) | (_b.LOW_MEMORY if low_memory else 0)
+    if compute_dW and dW_dtype == torch.bfloat16:
+        flags |= DW_BF16
     dH = out.take("dH", dH, tuple(H.shape), H.dtype)
-    return flags, dH, out.take("dW", dW, tuple(W.shape)) if compute_dW else None
+    return flags, dH, out.take("dW", dW, tuple(W.shape), dW_dtype) if compute_dW else None
 
 
 def policy_fwd_bwd(H, W, y, advantages, old_logprobs=None, ref_logprobs=None, weights=None, clip_low=0.2,
                    clip_high=0.2, beta=0.0, temperature=1.0, dloss=None, chunk: int = 1024,
                    ignore_index: int = _b.IGNORE_INDEX, reduction: str = "mean", loss=None, logprobs=None, dH=None,
-                   dW=None, ws=None, stream=None, accumulate=(), compute_dW: bool = True, low_memory: bool = False):
+                   dW=None, ws=None, stream=None, accumulate=(), compute_dW: bool = True, low_memory: bool = False,
+                   dW_dtype=torch.float32):
     """The clipped policy loss over the head, with its gradients: (loss, logprobs, dH, dW).
 
     H [N, D] and W [V, D] bf16, y [N] the drawn tokens (ignore_index: the row does not count), and
@@ -134,8 +141,9 @@ def policy_fwd_bwd(H, W, y, advantages, old_logprobs=None, ref_logprobs=None, we
         loss = w (-min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A) + beta (e^d - 1 - d)),  d = ref - logp
     reduction: the mean over the counting rows, "sum" (a mean over sequences has its weights
     1 / (tokens * sequences)), or "none" (loss [N]; dloss [N]). logprobs [N]: logp, 0 for rows that
-    do not count. dH bf16, dW fp32. chunk: the memory / speed knob: a buffer of 2 chunk rows of logits (low_memory:
-    chunk rows). The rest as for lce_fwd_bwd."""
+    do not count. dH bf16, dW fp32 (or bf16 by dW_dtype, where the rows fill one buffer and dW is not added
+    to). chunk: the memory / speed knob: a buffer of 2 chunk rows of logits (low_memory: chunk rows).
+    The rest as for lce_fwd_bwd."""
     N, D, V = _check_head(H, W, y)
     dev, red = H.device, _b._reduction(reduction)
     args = _policy_args(N, dev, advantages, old_logprobs, ref_logprobs, weights, clip_low, clip_high, beta,
@@ -145,7 +153,7 @@ def policy_fwd_bwd(H, W, y, advantages, old_logprobs=None, ref_logprobs=None, we
         out = _Outputs(dev)
         loss = out.take("loss", loss, _loss_shape(reduction, N))
         logprobs = out.take("logprobs", logprobs, (N,))
-        flags, dH, dW = _gradients(out, H, W, dH, dW, accumulate, compute_dW, low_memory)
+        flags, dH, dW = _gradients(out, H, W, dH, dW, accumulate, compute_dW, low_memory, dW_dtype)
         ws = _workspace(ws, policy_workspace_size(N, D, V, chunk, flags), dev)
         _b._check(_b.lib().lce_policy_fwd_bwd(
             H.data_ptr(), W.data_ptr(), y.data_ptr(), *args, d, N, D, V, ignore_index, chunk, red, flags,
@@ -172,7 +180,8 @@ def _pairs(offsets, dev):
 def preference_fwd_bwd(H, W, y, offsets, ref_logprobs=None, beta=0.1, label_smoothing=0.0, average: bool = False,
                        dloss=None, chunk: int = 1024, ignore_index: int = _b.IGNORE_INDEX, reduction: str = "mean",
                        loss=None, seq_logprobs=None, dH=None, dW=None, ws=None, stream=None, accumulate=(),
-                       gradient: bool = True, compute_dW: bool = True, low_memory: bool = False):
+                       gradient: bool = True, compute_dW: bool = True, low_memory: bool = False,
+                       dW_dtype=torch.float32):
     """The preference loss of paired log ratios over the head, with its gradients: (loss,
     seq_logprobs, dH, dW).
 
@@ -196,7 +205,7 @@ def preference_fwd_bwd(H, W, y, offsets, ref_logprobs=None, beta=0.1, label_smoo
         loss = out.take("loss", loss, _loss_shape(reduction, P))
         seq_logprobs = out.take("seq_logprobs", seq_logprobs, (2 * P,))
         if gradient:
-            flags, dH, dW = _gradients(out, H, W, dH, dW, accumulate, compute_dW, low_memory)
+            flags, dH, dW = _gradients(out, H, W, dH, dW, accumulate, compute_dW, low_memory, dW_dtype)
         elif dH is not None or dW is not None or accumulate:
             raise ValueError("no gradients were asked for")
         else:
@@ -219,27 +228,53 @@ def _scaled(src, scale, dtype, s):
     return out
 
 
+def _scale_in_place(t, scale, s):
+    _b._check(_b.lib().lce_scale(t.data_ptr(), _b._CE_DTYPES[t.dtype], scale.data_ptr(), t.numel(), t.data_ptr(),
+                                 _b._CE_DTYPES[t.dtype], s), "lce_scale")
+    return t
+
+
 class AnswerLossFunction(torch.autograd.Function):
     """A loss on answers over the head. The forward forms the gradients for an upstream gradient
-    of 1 (fwd_bwd); the backward scales them, which the loss is linear in. A W without
+    of 1 (fwd_bwd), in the dtypes of H and W where that takes one contraction; the backward scales them, which
+    the loss is linear in, in place (nothing is read or written where the upstream gradient is 1; another one
+    rounds once more), and hands them over. A second backward through the same graph forms them again, and so
+    does a backward that is captured without its forward (each replay would scale them once more). A W without
     requires_grad is frozen (no dW work). The log probabilities beside the loss carry no gradient."""
 
     @staticmethod
-    def forward(ctx, H, W, fwd_bwd):
-        loss, logprobs, dH, dW = fwd_bwd(H, W, ctx.needs_input_grad[1])
-        ctx.save_for_backward(dH, dW)
-        ctx.w_dtype = W.dtype
+    def forward(ctx, H, W, fwd_bwd, one, *constants):
+        train = ctx.needs_input_grad[1]
+        how = {"compute_dW": train, "dW_dtype": torch.bfloat16 if train and one else torch.float32}
+        loss, logprobs, *ctx.gradients = fwd_bwd(H, W, *constants, **how)
+        ctx.save_for_backward(H, W, *constants)
+        ctx.fwd_bwd, ctx.how = fwd_bwd, how
+        ctx.captured = H.is_cuda and torch.cuda.is_current_stream_capturing()
         ctx.mark_non_differentiable(logprobs)
         return loss.view(()), logprobs
 
     @staticmethod
     @once_differentiable
     def backward(ctx, g, _):
-        dH, dW = ctx.saved_tensors
+        tensors = ctx.saved_tensors   # (that none was written to since is checked here)
         g = g.to(torch.float32).contiguous()
-        with _b._on(dH.device, None) as s:
-            return (_scaled(dH, g, dH.dtype, s) if ctx.needs_input_grad[0] else None,
-                    _scaled(dW, g, ctx.w_dtype, s) if dW is not None else None, None)
+        with _b._on(tensors[0].device, None) as s:
+            if ctx.gradients is None or torch.cuda.is_current_stream_capturing() != ctx.captured:
+                _, _, dH, dW = ctx.fwd_bwd(*tensors, dloss=g, **ctx.how)
+                dW = dW if dW is None or dW.dtype == tensors[1].dtype else dW.to(tensors[1].dtype)
+            else:
+                (dH, dW), ctx.gradients = ctx.gradients, None
+                if ctx.needs_input_grad[0]:
+                    _scale_in_place(dH, g, s)
+                if dW is not None:
+                    dW = _scale_in_place(dW, g, s) if dW.dtype == tensors[1].dtype else \
+                        _scaled(dW, g, tensors[1].dtype, s)
+        return (dH if ctx.needs_input_grad[0] else None, dW, None, None) + (None,) * (len(tensors) - 2)
+
+
+def _one_buffer(H, chunk, low_memory):
+    """Whether the rows fill one chunk buffer, so that dW is one contraction."""
+    return H.shape[0] <= (1 if low_memory else 2) * chunk
 
 
 def _summed(what, reduction):
@@ -262,8 +297,11 @@ def linear_policy_loss(H, W, y, advantages, old_logprobs=None, ref_logprobs=None
     if not (torch.is_grad_enabled() and (H.requires_grad or W.requires_grad)):
         loss, logprobs = policy_forward(H, W, y, advantages, **how)
         return loss.view(()), logprobs
+    for name in ("old_logprobs", "ref_logprobs", "weights"):
+        del how[name]
     return AnswerLossFunction.apply(
-        H, W, lambda h, w, train: policy_fwd_bwd(h, w, y, advantages, compute_dW=train, low_memory=low_memory, **how))
+        H, W, lambda *t, **more: policy_fwd_bwd(*t, low_memory=low_memory, **how, **more),
+        _one_buffer(H, chunk, low_memory), y, advantages, old_logprobs, ref_logprobs, weights)
 
 
 def linear_preference_loss(H, W, y, offsets, ref_logprobs=None, beta=0.1, label_smoothing=0.0,
@@ -279,8 +317,9 @@ def linear_preference_loss(H, W, y, offsets, ref_logprobs=None, beta=0.1, label_
     if not (torch.is_grad_enabled() and (H.requires_grad or W.requires_grad)):
         loss, seq, _, _ = preference_fwd_bwd(H, W, y, offsets, gradient=False, **how)
         return loss.view(()), seq
-    return AnswerLossFunction.apply(
-        H, W, lambda h, w, train: preference_fwd_bwd(h, w, y, offsets, compute_dW=train, **how))
+    del how["ref_logprobs"]
+    return AnswerLossFunction.apply(H, W, lambda *t, **more: preference_fwd_bwd(*t, **how, **more),
+                                    _one_buffer(H, chunk, low_memory), y, offsets, ref_logprobs)
 
 
 def _check_logits(Z, y):

@@ -798,37 +798,61 @@ __global__ void __launch_bounds__(GRAD_THREADS) lce_answer_grad_kernel(const __g
 
 constexpr int PAIR_THREADS = 256;
 
-// Sum and count of the counting rows begin .. end - 1, in every thread.
-__device__ __forceinline__ void sequence(const PairParams &p, long long begin, long long end, float2 *s_red,
-                                         int *s_cnt, double *sum, int *count) {
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// A sequence's sum of log probabilities, what right label logits would add to it and the weight of that, and its
+// counting rows.
+struct Sequence {
+    double sum, fix, weight;
+    int rows;
+};
+
+// Of the rows begin .. end - 1, in every thread.
+__device__ __forceinline__ Sequence sequence(const PairParams &p, long long begin, long long end, float2 *s_red,
+                                             float2 *s_fix, int *s_cnt) {
     const int t = threadIdx.x, w = t >> 5, l = t & 31;
     Sum2 s;
+    float2 f = make_float2(0.f, 0.f);
     int n = 0;
     for (long long i = begin + t; i < end; i += PAIR_THREADS)
         if (label_counts(p.y[i], p.V, p.ignore_index)) {
-            s.add(-p.loss_rows[p.place ? p.place[i] : i]);
+            const long long at = p.place ? p.place[i] : i;
+            s.add(-p.loss_rows[at]);
+            if (p.fix) {
+                const float2 x = p.fix[at];
+                f.x += x.x;
+                f.y += x.y;
+            }
             ++n;
         }
     s.warp();
+    f.x = lanes_sum(f.x);
+    f.y = lanes_sum(f.y);
     n = __reduce_add_sync(0xffffffffu, n);
     __syncthreads();
     if (l == 0) {
         s_red[w] = make_float2(s.hi, s.lo);
+        s_fix[w] = f;
         s_cnt[w] = n;
     }
     __syncthreads();
-    const float2 x = l < PAIR_THREADS / 32 ? s_red[l] : make_float2(0.f, 0.f);
+    const bool mine = l < PAIR_THREADS / 32;
+    const float2 x = mine ? s_red[l] : make_float2(0.f, 0.f);
+    f = mine ? s_fix[l] : make_float2(0.f, 0.f);
     s.hi = x.x;
     s.lo = x.y;
     s.warp();
-    *sum = s.value();
-    *count = __reduce_add_sync(0xffffffffu, l < PAIR_THREADS / 32 ? s_cnt[l] : 0);
+    return Sequence{s.value(), lanes_sum(f.x), lanes_sum(f.y), __reduce_add_sync(0xffffffffu, mine ? s_cnt[l] : 0)};
 }
 
 // One CTA per pair. Offsets are taken as their running maximum, cut to [0, N]: whatever they
 // hold, the sequences are disjoint and every row gets its coefficient.
 __global__ void __launch_bounds__(PAIR_THREADS) lce_pairs_kernel(const __grid_constant__ PairParams p) {
-    __shared__ float2 s_red[PAIR_THREADS / 32];
+    __shared__ float2 s_red[PAIR_THREADS / 32], s_fix[PAIR_THREADS / 32];
     __shared__ int s_cnt[PAIR_THREADS / 32];
     __shared__ unsigned long long s_off[4];
     __shared__ int s_last;
@@ -851,8 +875,23 @@ __global__ void __launch_bounds__(PAIR_THREADS) lce_pairs_kernel(const __grid_co
                               static_cast<long long>(s_off[2]), static_cast<long long>(s_off[3])};
     double sum[2];
     int n[2];
-    sequence(p, off[0], off[1], s_red, s_cnt, &sum[0], &n[0]);
-    sequence(p, off[2], off[3], s_red, s_cnt, &sum[1], &n[1]);
+    const Sequence chosen = sequence(p, off[0], off[1], s_red, s_fix, s_cnt);
+    const Sequence rejected = sequence(p, off[2], off[3], s_red, s_fix, s_cnt);
+    sum[0] = chosen.sum;
+    sum[1] = rejected.sum;
+    n[0] = chosen.rows;
+    n[1] = rejected.rows;
+    // Over the head, the tensor cores cut their sums over D after each step: a logit z is off by about -3.5e-6 z at D =
+    // 4096, lse by the same on average over what the model would draw, and each row's log probability by 1.4e-5 rms
+    // of z_y's share in it, which sums over hundreds of rows and the margin keep. A right z_y alone
+    // would leave lse's part (-3.5e-5 a row, all of one sign). So z_y is put right but for the mean over the
+    // pair's rows, which is the part that lse has too; the pair's log probabilities add up to what they did.
+    const double weight = chosen.weight + rejected.weight, both = chosen.fix + rejected.fix;
+    if (weight > 0.0) {
+        const double fix[2] = {chosen.fix - both / weight * chosen.weight, rejected.fix - both / weight * rejected.weight};
+        for (int q = 0; q < 2; ++q)
+            if (fabs(fix[q]) < INFINITY) sum[q] += fix[q];
+    }
     float share[2];
     for (int q = 0; q < 2; ++q) {
         share[q] = p.average && n[q] > 0 ? 1.f / static_cast<float>(n[q]) : 1.f;
@@ -881,19 +920,24 @@ __global__ void __launch_bounds__(PAIR_THREADS) lce_pairs_kernel(const __grid_co
         float slope = p.beta * (e * (m >= 0.f ? big : small) - (1.f - e) * (m >= 0.f ? small : big)) * d;
         if (m != m) slope = m;
         // p - onehot gets minus the slope of its row
-        const float c[2] = {-slope * share[0], slope * share[1]};
-        auto put = [&](long long i, float v) {
-            if (!p.place) p.coef[i] = v;
-            else if (p.place[i] >= 0) p.coef[p.place[i]] = v;
+        const float full[2] = {-slope * share[0], slope * share[1]};
+        RoundedScale c[2];
+        for (int q = 0; q < 2; ++q) c[q] = p.ratio ? lce_round_scale(full[q]) : RoundedScale{full[q], 1.f};
+        auto put = [&](long long i, const RoundedScale &v) {
+            const long long at = p.place ? p.place[i] : i;
+            if (at < 0) return;
+            p.coef[at] = v.scale;
+            if (p.ratio) p.ratio[at] = v.ratio;
         };
+        const RoundedScale none{0.f, 1.f};
         for (int q = 0; q < 2; ++q)
             for (long long i = off[2 * q] + t; i < off[2 * q + 1]; i += PAIR_THREADS)
-                put(i, label_counts(p.y[i], p.V, p.ignore_index) ? c[q] : 0.f);
+                put(i, label_counts(p.y[i], p.V, p.ignore_index) ? c[q] : none);
         // rows before the first sequence and behind the last
         if (k == 0)
-            for (long long i = t; i < p.N && i < off[0]; i += PAIR_THREADS) put(i, 0.f);
+            for (long long i = t; i < p.N && i < off[0]; i += PAIR_THREADS) put(i, none);
         if (k == p.pairs - 1)
-            for (long long i = off[3] + t; i < p.N; i += PAIR_THREADS) put(i, 0.f);
+            for (long long i = off[3] + t; i < p.N; i += PAIR_THREADS) put(i, none);
     }
     if (p.loss && last_to_finish(p.hdr + HDR_DONE, static_cast<int>(gridDim.x), &s_last)) {
         const double s = block_sum(p.pair_loss, p.pairs, s_red);
@@ -910,6 +954,7 @@ template <typename S, typename D>
 __global__ void __launch_bounds__(SCALE_THREADS) lce_scale_kernel(const S *src, const float *__restrict__ scale,
                                                                   long long n, D *dst, int vec) {
     const float g = *scale;
+    if (g == 1.f && static_cast<const void *>(src) == static_cast<const void *>(dst)) return;   // (they are that already)
     const long long t = blockIdx.x * static_cast<long long>(SCALE_THREADS) + threadIdx.x;
     const long long nt = static_cast<long long>(gridDim.x) * SCALE_THREADS;
     const long long nv = vec ? n / 8 : 0;

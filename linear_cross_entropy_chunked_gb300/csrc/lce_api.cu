@@ -282,6 +282,8 @@ struct Ctx {
     uint8_t *ws;
     int *hdr;
     float *loss_rows, *zy;
+    float *zx = nullptr;         // [C]: the labels' logits as dot products of their own (the preference loss),
+    float2 *fix = nullptr;       // [N]: what the log probabilities move by with them
     float2 *parts;
     __nv_bfloat16 *Gb[2];   // the chunk buffers (Gb[1] == Gb[0] with one)
     __nv_bfloat16 *HT;
@@ -305,6 +307,8 @@ struct Ctx {
     const int *index = nullptr;
     const __nv_bfloat16 *Hrows = nullptr;
     bool loss_by_index = false;
+    float *ratio = nullptr;      // [N]: what rounding the rows' scales to bf16 left of them
+    bool dw16 = false;           // dW is bf16 (one contraction)
 };
 
 // Row of H (c.H) where the chunk starting at row0 begins.
@@ -534,6 +538,7 @@ void set_row_filter(const Ctx &c, long long row0, TransposeParams &tp) {
     tp.V = c.V;
     tp.ignore_index = c.ign;
     tp.coef = c.coef ? c.coef + row0 : nullptr;
+    tp.ratio = c.ratio ? c.ratio + row0 : nullptr;
 }
 
 // H chunk^T into columns col0 .. col0 + rows - 1 of H^T (the K-major B operand of
@@ -598,7 +603,8 @@ lce_status run_bwd(const Ctx &c, long long row0, long long rows, int slot, const
         if (!encode_map(&p.tmA1, g.Gdw, 3, dims, strides, box, c.t16)) return LCE_ERR_CUDA;
         if (!encode_2d(&p.tmB1, c.HT, g.dw_rows, c.D, 2ull * c.L.ldt, BK, BN / cl, c.t16))
             return LCE_ERR_CUDA;
-        if (!encode_store_2d(&p.tmS1, dW, c.D, c.V, 4ull * c.D, MAP_F32)) return LCE_ERR_CUDA;
+        if (!encode_store_2d(&p.tmS1, dW, c.D, c.V, (c.dw16 ? 2ull : 4ull) * c.D, c.dw16 ? MAP_BF16 : MAP_F32))
+            return LCE_ERR_CUDA;
     }
     if (!encode_2d(&p.tmA0, g.G, c.V, rows, 2ull * c.L.ldg, BK, BM, c.t16)) return LCE_ERR_CUDA;
     p.tmB0 = c.tmW_MN;
@@ -627,6 +633,8 @@ lce_status run_bwd(const Ctx &c, long long row0, long long rows, int slot, const
     p.dloss = dloss;   // fp16: the epilogues apply the uniform part of the scale
     p.dW = dW;
     p.dw_accumulate = accumulate ? 1 : 0;
+    p.dw_16 = c.dw16 ? 1 : 0;
+    p.ratio = c.ratio;
     const int units = cl == 2 ? c.pairs : c.sms;
     // profiling kind: a pair's second chunk (its dH with both chunks' dW), a pair's
     // first chunk (its dH alone), or a chunk's whole gradient phase
@@ -764,6 +772,8 @@ void merge_params(const Ctx &c, long long row0, long long rows, float *lse, cons
     m.parts = c.parts;
     m.nparts = c.L.nparts;
     m.zy = c.zy;
+    m.zx = c.coef ? nullptr : c.zx;   // (with the coefficients the sequences have been added up)
+    m.fix = c.fix;
     m.G = c.Gb[0];
     m.ldg = c.L.ldg;
     m.rows = static_cast<int>(rows);
@@ -783,6 +793,7 @@ void merge_params(const Ctx &c, long long row0, long long rows, float *lse, cons
     m.counting = c.index ? c.hdr + HDR_NVALID : nullptr;
     m.index = c.pol.adv ? c.index : nullptr;   // (a preference's rows go by their place)
     m.loss_by_index = c.loss_by_index ? 1 : 0;
+    m.ratio = c.pol.adv ? c.ratio : nullptr;   // (a preference's coefficients have been rounded already)
 }
 
 lce_status run_merge(const Ctx &c, long long row0, long long rows, float *lse,
@@ -837,20 +848,34 @@ inline bool frozen_overlapped(const Ctx &c) {
     return c.pairs > 0 && c.L.frozen_w && c.L.nbuf == 2 && !c.h_chunked;
 }
 
-// The rows of chunk k that count into their place of H's buffer (nothing to do where H is read in place).
-lce_status bring_rows(const Ctx &c, long long k) {
-    if (!c.index) return LCE_OK;
+// The rows of chunk k that count into their place of H's buffer (nothing to do where H is read in place), and
+// with_labels their labels' logits.
+lce_status bring_rows(const Ctx &c, long long k, bool with_labels) {
+    if (!c.index && !with_labels) return LCE_OK;
     const long long row0 = k * c.L.C;
-    LCE_LAUNCH_KIND(LCE_KERNEL_MERGE, c.s,
-                    launch_gather_rows(c.Hrows, c.index, c.hdr + HDR_NVALID, row0, chunk_rows(c, k), c.D,
-                                       const_cast<__nv_bfloat16 *>(c.H) + h_row(c, row0) * c.D, c.sms, c.s));
+    const __nv_bfloat16 *Hc = c.H + h_row(c, row0) * c.D;
+    GatherParams p;
+    p.src = reinterpret_cast<const uint4 *>(c.index ? c.Hrows : Hc);
+    p.index = c.index;
+    p.counting = c.index ? c.hdr + HDR_NVALID : nullptr;
+    p.dst = reinterpret_cast<uint4 *>(const_cast<__nv_bfloat16 *>(Hc));   // (written with an index only)
+    p.row0 = static_cast<int>(row0);
+    p.rows = static_cast<int>(chunk_rows(c, k));
+    p.vecs = static_cast<int>(c.D / 8);
+    p.W = with_labels ? reinterpret_cast<const uint4 *>(c.W) : nullptr;
+    p.y = c.y + row0;
+    p.V = c.V;
+    p.ignore_index = c.ign;
+    p.inv_t = c.inv_t;
+    p.zx = c.zx;
+    LCE_LAUNCH_KIND(LCE_KERNEL_MERGE, c.s, launch_gather_rows(p, c.sms, c.s));
     return LCE_OK;
 }
 
 // Losses on answers have one chunk buffer. Where a cross-entropy call of that chunk would have two
 // (no LCE_LOW_MEMORY) it holds twice the rows: the same memory, and what two chunks are split in for (the logits
 // of one beside dH of the other) weighs less than contractions of twice the rows do where the rows that count are
-// few: 1072 of 1531 rows x 50257 x 1600 under a frozen head 553 -> MEASURED us.
+// few: 1072 of 1531 rows x 50257 x 1600 under a frozen head 553 -> 375 us.
 long long answer_chunk(long long N, long long chunk, int flags) {
     if (chunk <= 0 || N <= 0 || chunk >= N) return chunk;
     return (flags & LCE_LOW_MEMORY) ? chunk : chunk > N / 2 ? N : 2 * chunk;
@@ -862,19 +887,20 @@ long long answer_chunk(long long N, long long chunk, int flags) {
 // not where chunks do not end on k blocks of the dW contraction.
 struct GatherLayout {
     bool on = false;
-    size_t off_index = 0, off_place = 0, off_labels = 0, off_H = 0, end = 0;
+    size_t off_ratio = 0, off_index = 0, off_place = 0, off_labels = 0, off_H = 0, end = 0;
 };
 
 GatherLayout gather_layout(const Layout &L, long long N, long long D, size_t at) {
     GatherLayout g;
     g.on = N > 256 && (L.nchunks <= 1 || L.C % BK == 0);
     g.end = at;
-    if (!g.on) return g;
     auto take = [&](size_t bytes) {
         const size_t o = g.end;
         g.end += align_up(bytes, 1024);
         return o;
     };
+    g.off_ratio = take(sizeof(float) * static_cast<size_t>(N > 0 ? N : 1));   // (of rows that are not brought together too)
+    if (!g.on) return g;
     g.off_index = take(sizeof(int) * static_cast<size_t>(N));
     g.off_place = take(sizeof(int) * static_cast<size_t>(N));
     g.off_labels = take(sizeof(long long) * static_cast<size_t>(N));
@@ -960,7 +986,7 @@ lce_status backward_chunks(const Ctx &c, long long first, long long n, const flo
     for (long long k = first; k < n; ++k) {
         const long long row0 = k * c.L.C;
         const long long rows = chunk_rows(c, k);
-        LCE_TRY(bring_rows(c, k));
+        LCE_TRY(bring_rows(c, k, false));
         LCE_TRY(run_logits(c, MODE_G, row0, rows, static_cast<int>(2 * k), lse, dloss, c.Gb[0]));
         LCE_TRY(run_grad(c, row0, rows, static_cast<int>(2 * k + 1), dHb + row0 * c.D, acc_dh, dW,
                          k > 0 || acc_dw0, dloss, GradSpec{c.Gb[0], c.Gb[0], rows, false, false}));
@@ -1120,7 +1146,7 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
                         const int64_t *n_valid_total, const PolicyParams *pol = nullptr) {
     g_launches = 0;
     if (reduction < LCE_REDUCTION_MEAN || reduction > LCE_REDUCTION_NONE) return LCE_ERR_INVALID_ARG;
-    if (flags & ~LCE_FLAGS_ALL) return LCE_ERR_INVALID_ARG;
+    if (flags & ~(LCE_FLAGS_ALL | (pol ? LCE_DW_BF16 : 0))) return LCE_ERR_INVALID_ARG;
     const bool f16 = (flags & LCE_INPUT_FP16) != 0;
     const bool frozen = (flags & LCE_FROZEN_W) != 0;
     const bool none = reduction == LCE_REDUCTION_NONE;
@@ -1142,7 +1168,8 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
     const int64_t *ys = y;
     if (pol) {
         gl = gather_layout(L0, N, D, L0.total + acc_dh_bytes(L0, D));
-        if (gl.on && ws_bytes < gl.end) return LCE_ERR_WORKSPACE;
+        if (ws_bytes < gl.end) return LCE_ERR_WORKSPACE;
+        if ((flags & LCE_DW_BF16) && (frozen || (flags & LCE_ACCUMULATE_DW) || L0.nchunks > 1)) return LCE_ERR_UNSUPPORTED;
         LCE_TRY(gather_inputs(gl, Hs, ys, ws));
     }
     Ctx c;
@@ -1153,7 +1180,10 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
         c.pol = *pol;
         c.inv_t = pol->inv_t;
         c.answers = true;
+        c.ratio = reinterpret_cast<float *>(c.ws + gl.off_ratio);
+        c.dw16 = (flags & LCE_DW_BF16) != 0;
         LCE_TRY(start_gather(c, gl, H, y));
+        if (gl.on && !frozen) LCE_ZERO(c.ratio, sizeof(float) * static_cast<size_t>(N));   // (for H^T behind the rows that count)
         if (gl.on) {   // what rows that do not count have
             c.loss_by_index = none;
             LCE_ZERO(none ? loss : c.loss_rows, sizeof(float) * static_cast<size_t>(N));
@@ -1166,7 +1196,7 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
     if (frozen) dW = nullptr;
     float *rows_out = none ? loss : c.loss_rows;
     if (c.L.nchunks == 0 && dW && !(flags & LCE_ACCUMULATE_DW)) {
-        if (cudaMemsetAsync(dW, 0, sizeof(float) * static_cast<size_t>(V) * D, c.s) != cudaSuccess)
+        if (cudaMemsetAsync(dW, 0, (c.dw16 ? 2 : sizeof(float)) * static_cast<size_t>(V) * D, c.s) != cudaSuccess)
             return LCE_ERR_CUDA;
     }
     const bool acc_dw0 = (flags & LCE_ACCUMULATE_DW) != 0;
@@ -1225,13 +1255,14 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
         for (long long k = 0; k < c.L.nchunks; ++k) {
             const long long row0 = k * c.L.C;
             const long long rows = chunk_rows(c, k);
-            LCE_TRY(bring_rows(c, k));
+            LCE_TRY(bring_rows(c, k, false));
             LCE_TRY(run_logits(c, MODE_LSE_P, row0, rows, static_cast<int>(2 * k), nullptr, nullptr,
                                c.Gb[0]));
-            LCE_TRY(run_prep(c, row0, rows, lse, dloss, rows_out, c.Gb[0], !frozen));
+            // (the policy's H^T takes the ratios that the prep leaves)
+            LCE_TRY(run_prep(c, row0, rows, lse, dloss, rows_out, c.Gb[0], !frozen && !pol));
             LCE_TRY(run_grad(c, row0, rows, static_cast<int>(2 * k + 1), dHb + row0 * c.D, acc_dh,
                              dW, k > 0 || acc_dw0, dloss,
-                             GradSpec{c.Gb[0], c.Gb[0], frozen ? 0 : rows, true, false}));
+                             GradSpec{c.Gb[0], c.Gb[0], frozen ? 0 : rows, !pol, false}));
         }
     }
     if (!none)
@@ -1277,7 +1308,7 @@ PolicyParams policy_params(const float *advantages, const float *old_logprobs, c
 struct PrefLayout {
     Layout L;
     GatherLayout gather;
-    size_t off_lse = 0, off_coef = 0, off_pair = 0, total = 0;
+    size_t off_lse = 0, off_zx = 0, off_fix = 0, off_coef = 0, off_pair = 0, total = 0;
 };
 
 // (chunk: as answer_chunk has it)
@@ -1293,6 +1324,8 @@ bool make_pref_layout(int64_t N, int64_t D, int64_t V, int64_t chunk, int64_t pa
         return at;
     };
     P.off_lse = take(rows);
+    P.off_zx = take(sizeof(float) * static_cast<size_t>(P.L.C > 0 ? P.L.C : 1));
+    P.off_fix = take(2 * rows);
     P.off_pair = take(sizeof(float) * static_cast<size_t>(pairs));
     if (grad) P.off_coef = take(rows);
     P.total = off;
@@ -1325,6 +1358,8 @@ PairParams pair_params(const int64_t *offsets, int64_t pairs, int64_t N, int64_t
     p.y = reinterpret_cast<const long long *>(y);
     p.loss_rows = loss_rows;
     p.place = nullptr;
+    p.ratio = nullptr;
+    p.fix = nullptr;
     p.ref = ref;
     p.beta = beta;
     p.smoothing = smoothing;
@@ -1623,7 +1658,7 @@ lce_status lce_fwd_bwd(const void *H, const void *W, const int64_t *y, const flo
 lce_status lce_policy_workspace_size(int64_t N, int64_t D, int64_t V, int64_t chunk, int flags, int gradient,
                                      size_t *bytes) {
     Layout L;
-    if (!bytes || (flags & ~LCE_FLAGS_ALL) ||
+    if (!bytes || (flags & ~(LCE_FLAGS_ALL | LCE_DW_BF16)) ||
         !make_layout(N, D, V, gradient ? answer_chunk(N, chunk, flags) : chunk, L, (flags & LCE_FROZEN_W) != 0, true))
         return LCE_ERR_INVALID_ARG;
     *bytes = gather_layout(L, N, D, gradient ? L.total + acc_dh_bytes(L, D) : L.fwd_total).end;
@@ -1645,7 +1680,7 @@ lce_status lce_policy_forward(const void *H, const void *W, const int64_t *y, co
     Layout L0;
     if (!make_layout(N, D, V, chunk, L0, false, true)) return LCE_ERR_INVALID_ARG;
     const GatherLayout gl = gather_layout(L0, N, D, L0.fwd_total);
-    if (gl.on && ws_bytes < gl.end) return LCE_ERR_WORKSPACE;
+    if (ws_bytes < gl.end) return LCE_ERR_WORKSPACE;
     const void *Hs = H;
     const int64_t *ys = y;
     LCE_TRY(gather_inputs(gl, Hs, ys, ws));
@@ -1663,7 +1698,7 @@ lce_status lce_policy_forward(const void *H, const void *W, const int64_t *y, co
                           temperature, logprobs);
     c.inv_t = c.pol.inv_t;
     for (long long k = 0; k < c.L.nchunks; ++k) {
-        LCE_TRY(bring_rows(c, k));
+        LCE_TRY(bring_rows(c, k, false));
         LCE_TRY(run_logits(c, MODE_LSE, k * c.L.C, chunk_rows(c, k), static_cast<int>(k), nullptr, nullptr,
                            c.Gb[0]));
         LCE_TRY(run_merge(c, k * c.L.C, chunk_rows(c, k), nullptr, nullptr, none ? loss : c.loss_rows));
@@ -1678,7 +1713,7 @@ lce_status lce_policy_fwd_bwd(const void *H, const void *W, const int64_t *y, co
                               float clip_low, float clip_high, float beta, float temperature,
                               const float *dloss, int64_t N, int64_t D, int64_t V, int64_t ignore_index,
                               int64_t chunk, int reduction, int flags, float *loss, float *logprobs, void *dH,
-                              float *dW, void *ws, size_t ws_bytes, lce_stream_t stream) {
+                              void *dW, void *ws, size_t ws_bytes, lce_stream_t stream) {
     g_launches = 0;
     // (16-bit floats: a policy's coefficients have no range that fp16 gradients could be scaled by)
     if (flags & LCE_INPUT_FP16) return LCE_ERR_UNSUPPORTED;
@@ -1686,14 +1721,14 @@ lce_status lce_policy_fwd_bwd(const void *H, const void *W, const int64_t *y, co
                          temperature, logprobs));
     const PolicyParams pol = policy_params(advantages, old_logprobs, ref_logprobs, weights, clip_low, clip_high,
                                            beta, temperature, logprobs);
-    return fwd_bwd_impl(H, W, y, dloss, N, D, V, ignore_index, chunk, reduction, flags, loss, nullptr, dH, dW, ws,
-                        ws_bytes, stream, nullptr, &pol);
+    return fwd_bwd_impl(H, W, y, dloss, N, D, V, ignore_index, chunk, reduction, flags, loss, nullptr, dH,
+                        static_cast<float *>(dW), ws, ws_bytes, stream, nullptr, &pol);
 }
 
 lce_status lce_preference_workspace_size(int64_t N, int64_t D, int64_t V, int64_t chunk, int64_t pairs, int flags,
                                          int gradient, size_t *bytes) {
     PrefLayout P;
-    if (!bytes || (flags & ~LCE_FLAGS_ALL) ||
+    if (!bytes || (flags & ~(LCE_FLAGS_ALL | LCE_DW_BF16)) ||
         !make_pref_layout(N, D, V, gradient ? answer_chunk(N, chunk, flags) : chunk, pairs, flags, gradient != 0, P))
         return LCE_ERR_INVALID_ARG;
     *bytes = P.total;
@@ -1707,10 +1742,11 @@ lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y
                                   int64_t pairs, const float *ref_logprobs, float beta, float label_smoothing,
                                   int average, const float *dloss, int64_t N, int64_t D, int64_t V,
                                   int64_t ignore_index, int64_t chunk, int reduction, int flags, float *loss,
-                                  float *seq_logprobs, void *dH, float *dW, void *ws, size_t ws_bytes,
+                                  float *seq_logprobs, void *dH, void *dW_, void *ws, size_t ws_bytes,
                                   lce_stream_t stream) {
     g_launches = 0;
-    if (flags & ~LCE_FLAGS_ALL) return LCE_ERR_INVALID_ARG;
+    float *dW = static_cast<float *>(dW_);   // (bf16 with LCE_DW_BF16)
+    if (flags & ~(LCE_FLAGS_ALL | LCE_DW_BF16)) return LCE_ERR_INVALID_ARG;
     if (flags & LCE_INPUT_FP16) return LCE_ERR_UNSUPPORTED;
     const bool grad = dH != nullptr || dW != nullptr;
     const bool frozen = (flags & LCE_FROZEN_W) != 0 || !grad;
@@ -1725,6 +1761,7 @@ lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y
     if (!make_pref_layout(N, D, V, chunk, pairs, flags, grad, P)) return LCE_ERR_INVALID_ARG;
     if (!ws) return LCE_ERR_INVALID_ARG;
     if (ws_bytes < P.total) return LCE_ERR_WORKSPACE;
+    if ((flags & LCE_DW_BF16) && (frozen || acc_dw0 || P.L.nchunks > 1)) return LCE_ERR_UNSUPPORTED;
     const void *Hs = H;
     const int64_t *ys = y;
     LCE_TRY(gather_inputs(P.gather, Hs, ys, ws));
@@ -1735,16 +1772,21 @@ lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y
     if (P.gather.on && grad && !acc_dh) LCE_ZERO(dH, 2 * static_cast<size_t>(N) * static_cast<size_t>(D));
     c.reduction = LCE_REDUCTION_NONE;   // (of the rows: each has a coefficient of its own)
     c.answers = true;
+    c.dw16 = (flags & LCE_DW_BF16) != 0;
+    if (grad) c.ratio = reinterpret_cast<float *>(c.ws + P.gather.off_ratio);
+    if (P.gather.on && grad && !frozen) LCE_ZERO(c.ratio, sizeof(float) * static_cast<size_t>(N));
+    c.zx = reinterpret_cast<float *>(c.ws + P.off_zx);
+    c.fix = reinterpret_cast<float2 *>(c.ws + P.off_fix);
     float *lse = reinterpret_cast<float *>(c.ws + P.off_lse);
     float *coef = grad ? reinterpret_cast<float *>(c.ws + P.off_coef) : nullptr;
     if (frozen) dW = nullptr;
     const long long n = c.L.nchunks;
     if (n == 0 && dW && !acc_dw0 &&
-        cudaMemsetAsync(dW, 0, sizeof(float) * static_cast<size_t>(V) * D, c.s) != cudaSuccess)
+        cudaMemsetAsync(dW, 0, (c.dw16 ? 2 : sizeof(float)) * static_cast<size_t>(V) * D, c.s) != cudaSuccess)
         return LCE_ERR_CUDA;
     for (long long i = 0; i < n; ++i) {
         const long long k = !grad || i + 1 < n ? (grad ? i + 1 : i) : 0;   // (with gradients the first chunk last)
-        LCE_TRY(bring_rows(c, k));
+        LCE_TRY(bring_rows(c, k, true));
         LCE_TRY(run_logits(c, grad && k == 0 ? MODE_LSE_P : MODE_LSE, k * c.L.C, chunk_rows(c, k), static_cast<int>(k),
                            nullptr, nullptr, c.Gb[0]));
         LCE_TRY(run_merge(c, k * c.L.C, chunk_rows(c, k), lse, nullptr, c.loss_rows));
@@ -1752,6 +1794,8 @@ lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y
     PairParams pp = pair_params(offsets, pairs, N, V, ignore_index, y, c.loss_rows, ref_logprobs, beta, label_smoothing,
                                 average, dloss, reduction, loss, seq_logprobs,
                                 reinterpret_cast<float *>(c.ws + P.off_pair), coef, c.hdr);
+    pp.ratio = c.ratio;
+    pp.fix = c.fix;
     pp.place = c.index ? reinterpret_cast<const int *>(c.ws + P.gather.off_place) : nullptr;
     LCE_LAUNCH(launch_pairs(pp, c.s));
     if (!grad || n == 0) return LCE_OK;

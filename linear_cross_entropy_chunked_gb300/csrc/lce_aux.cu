@@ -155,6 +155,13 @@ __device__ __forceinline__ float row_lse(const float2 *parts, int nparts, float 
     return *s_bcast;
 }
 
+// What the log probability moves by if the label's logit alone is put right by d = zx - zy: to first order
+// d (1 - p), p = e^logp.
+__device__ __forceinline__ float2 label_fix(const MergeParams &m, int r, float logp) {
+    const float d = m.zx[r] - m.zy[r], q = -expm1f(logp);
+    return fabsf(d) < INFINITY && q > 0.f ? make_float2(d * q, q) : make_float2(0.f, 0.f);
+}
+
 // Forward: one CTA per chunk row, lse_i from the slab partials and the row's loss.
 __global__ void __launch_bounds__(MERGE_THREADS) lce_merge_kernel(const MergeParams p) {
     __shared__ float s_red[MERGE_THREADS / 32];
@@ -172,6 +179,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_merge_kernel(const MergePar
         const int of = p.index ? p.index[grow] : grow;   // the row of the call
         if (p.lse) p.lse[grow] = lse;
         const float logp = y_ok ? p.zy[r] - lse : 0.f;
+        if (p.zx) p.fix[grow] = y_ok ? label_fix(p, r, logp) : make_float2(0.f, 0.f);
         if (p.pol.logp) p.pol.logp[of] = logp;
         p.loss_rows[p.loss_by_index ? of : grow] =
             !y_ok ? 0.f : p.pol.adv ? lce_policy_row(p.pol, of, logp).loss : lse - p.zy[r];
@@ -183,6 +191,10 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_merge_kernel(const MergePar
 // operand of the dW contraction).
 
 constexpr int TT = 64;
+// Two values times a row's ratio.
+__device__ __forceinline__ uint32_t times2(uint32_t w, float f) {
+    return pack_bf16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
+}
 // Whether row r of the chunk is transposed as it is (else as zeros).
 __device__ __forceinline__ bool row_counts(const TransposeParams &p, int r) {
     if (p.coef && p.coef[r] == 0.f) return false;
@@ -204,8 +216,13 @@ __global__ void __launch_bounds__(256) lce_transpose_kernel(const TransposeParam
         const int rr = k >> 3, cb = (k & 7) * 8;
         const int r = r0 + rr, c = c0 + cb;
         uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (r < p.rows && c < p.cols && row_counts(p, r))
+        if (r < p.rows && c < p.cols && row_counts(p, r)) {
             u = *reinterpret_cast<const uint4 *>(p.src + static_cast<size_t>(r) * p.ld_src + c);
+            if (p.ratio) {
+                const float f = p.ratio[r];
+                u = make_uint4(times2(u.x, f), times2(u.y, f), times2(u.z, f), times2(u.w, f));
+            }
+        }
         uint32_t *dst = reinterpret_cast<uint32_t *>(tile + rr * TSTRIDE + cb);
         dst[0] = u.x;
         dst[1] = u.y;
@@ -264,8 +281,13 @@ __device__ __forceinline__ void transpose_tile(const TransposeParams &p, int c0,
         const int rr = k >> 3, cb = (k & 7) * 8;
         const int r = r0 + rr, c = c0 + cb;
         uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (r < p.rows && c < p.cols && row_counts(p, r))
+        if (r < p.rows && c < p.cols && row_counts(p, r)) {
             u = *reinterpret_cast<const uint4 *>(p.src + static_cast<size_t>(r) * p.ld_src + c);
+            if (p.ratio) {
+                const float f = p.ratio[r];
+                u = make_uint4(times2(u.x, f), times2(u.y, f), times2(u.z, f), times2(u.w, f));
+            }
+        }
         uint32_t *dst = reinterpret_cast<uint32_t *>(tile + rr * TSTRIDE + cb);
         dst[0] = u.x;
         dst[1] = u.y;
@@ -351,6 +373,11 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_prep_kernel(const PrepParam
         const PolicyRow pr = lce_policy_row(m.pol, of, logp);
         row_loss = pr.loss;
         scale *= -pr.slope * m.pol.inv_t;
+    }
+    if (m.ratio) {
+        const RoundedScale rs = lce_round_scale(scale);
+        scale = rs.scale;
+        if (seg == 0 && threadIdx.x == 0) m.ratio[grow] = rs.ratio;
     }
     if (seg == 0 && threadIdx.x == 0) {
         if (m.lse) m.lse[grow] = lse;
@@ -521,17 +548,44 @@ __global__ void __launch_bounds__(1024) lce_compact_kernel(const long long *__re
     for (int j = all + threadIdx.x; j < N; j += 1024) labels[j] = ign;
 }
 
-__global__ void __launch_bounds__(256) lce_gather_rows_kernel(const uint4 *__restrict__ src, const int *__restrict__ index,
-                                                              const int *__restrict__ counting, int row0, int rows,
-                                                              int vecs, uint4 *__restrict__ dst) {
-    const int live = live_rows(counting, row0, rows);
-    const int end = min(rows, live + 64);
+// Rows of H into their places, and (for the preference loss) each row's label logit H_i . W[y_i] on the way: products
+// of two bf16 numbers are exact in fp32, D / 256 of them in a thread's sum, then the threads' in a tree.
+__global__ void __launch_bounds__(256) lce_gather_rows_kernel(const GatherParams p) {
+    __shared__ float s_sum[8];
+    const int live = live_rows(p.counting, p.row0, p.rows);
+    const int end = p.index ? min(p.rows, live + 64) : live;
     for (int r = blockIdx.x; r < end; r += gridDim.x) {
         const bool there = r < live;
-        const uint4 *from = src + static_cast<size_t>(there ? index[row0 + r] : 0) * vecs;
-        uint4 *to = dst + static_cast<size_t>(r) * vecs;
+        const uint4 *from = p.src + static_cast<size_t>(!there ? 0 : p.index ? p.index[p.row0 + r] : r) * p.vecs;
+        uint4 *to = p.dst + static_cast<size_t>(r) * p.vecs;
+        const long long label = p.W && there ? p.y[r] : p.ignore_index;
+        const bool counts = label != p.ignore_index && label >= 0 && label < p.V;
+        const uint4 *wr = p.W + static_cast<size_t>(counts ? label : 0) * p.vecs;
+        float sum = 0.f;
 #pragma unroll 4
-        for (int v = threadIdx.x; v < vecs; v += 256) to[v] = there ? from[v] : make_uint4(0u, 0u, 0u, 0u);
+        for (int v = threadIdx.x; v < p.vecs; v += 256) {
+            const uint4 h = there ? from[v] : make_uint4(0u, 0u, 0u, 0u);
+            if (p.index) to[v] = h;
+            if (counts) {
+                const uint4 w = wr[v];
+                const uint32_t *a = &h.x, *b = &w.x;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    sum = fmaf(__uint_as_float(a[q] << 16), __uint_as_float(b[q] << 16), sum);
+                    sum = fmaf(__uint_as_float(a[q] & 0xffff0000u), __uint_as_float(b[q] & 0xffff0000u), sum);
+                }
+            }
+        }
+        if (!p.W) continue;
+        sum = warp_sum(sum);
+        if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = sum;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            float z = 0.f;
+            for (int w = 0; w < 8; ++w) z += s_sum[w];
+            p.zx[r] = z * p.inv_t;
+        }
+        __syncthreads();
     }
 }
 
@@ -660,12 +714,9 @@ cudaError_t launch_compact(const long long *y, long long N, long long V, long lo
     return cudaGetLastError();
 }
 
-cudaError_t launch_gather_rows(const __nv_bfloat16 *src, const int *index, const int *counting, long long row0,
-                               long long rows, long long D, __nv_bfloat16 *dst, int sms, cudaStream_t s) {
-    const int g = static_cast<int>(rows < 8ll * sms ? rows : 8ll * sms);
-    lce_gather_rows_kernel<<<g, 256, 0, s>>>(reinterpret_cast<const uint4 *>(src), index, counting,
-                                             static_cast<int>(row0), static_cast<int>(rows), static_cast<int>(D / 8),
-                                             reinterpret_cast<uint4 *>(dst));
+cudaError_t launch_gather_rows(const GatherParams &p, int sms, cudaStream_t s) {
+    const int g = static_cast<int>(p.rows < 8ll * sms ? p.rows : 8ll * sms);
+    lce_gather_rows_kernel<<<g, 256, 0, s>>>(p);
     return cudaGetLastError();
 }
 

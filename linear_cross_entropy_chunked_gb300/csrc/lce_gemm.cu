@@ -342,6 +342,8 @@ __device__ __forceinline__ void epilogue_grad(const GemmParams &p, const Live &l
     // a tile entirely past the output rows (the second tile of a CTA pair at an
     // odd row-block count) stores nothing
     if (tl.m0 >= (tl.type == TILE_MAIN ? lv.rows : p.V)) return;
+    // (dH's row of this thread, on the path whose rows' scales were rounded)
+    const float ratio = p.ratio && tl.type == TILE_MAIN && tl.m0 + st.row < lv.rows ? p.ratio[p.row0 + tl.m0 + st.row] : 1.f;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         float v[32];
@@ -350,11 +352,15 @@ __device__ __forceinline__ void epilogue_grad(const GemmParams &p, const Live &l
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] *= out_scale;
         }
-        if (tl.type == TILE_MAIN && !p.dh_fp32) {
+        if (ratio != 1.f) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] *= ratio;
+        }
+        if (tl.type == TILE_MAIN ? !p.dh_fp32 : p.dw_16) {
             if (col0 + (c >> 1) * 64 >= p.D) continue;
             if ((c & 1) == 0) st.acquire();
             st.put_h16((c & 1) * 4, v, p.f16);
-            if (c & 1) st.issue(&p.tmS0, ST_STORE, col0 + (c >> 1) * 64, tl.m0);
+            if (c & 1) st.issue(tl.type == TILE_MAIN ? &p.tmS0 : &p.tmS1, ST_STORE, col0 + (c >> 1) * 64, tl.m0);
         } else if (tl.type == TILE_MAIN) {
             if (col0 + c * 32 >= p.D) continue;
             st.acquire();

@@ -151,6 +151,19 @@ __device__ __forceinline__ PolicyRow lce_policy_row(const PolicyParams &p, long 
     return lce_policy_row(p, lce_policy_inputs(p, i), logp);
 }
 
+// A row's scale as a bf16 number, and what that leaves of it as a factor. G = (p - onehot) * scale is stored in bf16,
+// and where the label is unlikely its entry is nearly -scale: with the rounded scale that entry is exact, and
+// the factor is made up for in fp32 on dH's rows and in H's rows for dW. (Rounded with G, a scale that all rows of a
+// sequence share would make up to 2^-9 of all their gradient go missing.)
+struct RoundedScale {
+    float scale, ratio;
+};
+__device__ __forceinline__ RoundedScale lce_round_scale(float s) {
+    const float r = __bfloat162float(__float2bfloat16_rn(s));
+    if (!(fabsf(r) < INFINITY) || r == 0.f) return RoundedScale{s, 1.f};
+    return RoundedScale{r, s / r};
+}
+
 // Workspace header (int32 words).
 enum : int {
     HDR_FLAG = 0,       // bit 0: label out of range, bit 1: pipeline wait timed out
@@ -196,6 +209,8 @@ struct GemmParams {
     float *dW;             // [V][D]
     int dw_accumulate;     // 0: store, 1: add to existing dW
     int dh_fp32;           // 1: dH tiles stored as fp32 (tmS0 an fp32 map)
+    int dw_16;             // 1: dW stored as bf16 (tmS1 a bf16 map; not added to)
+    const float *ratio;    // null, or what row i of dH is multiplied by (global [N])
     // dH launches: the vocabulary (K) range of every dH tile split in k_splits
     // parts of kb_per_split k blocks; part s stores fp32 partial sums at row
     // offset s * split_rows of the tmS0 map (k_splits <= 1: one part, no offset)
@@ -213,6 +228,8 @@ struct MergeParams {
     const float2 *parts;   // [rows][nparts] (max, sumexp) per 128-column slab
     int nparts;
     const float *zy;
+    const float *zx;       // null, or [rows]: the label's logit as an fp32 dot product of its own (zy: the tensor cores'),
+    float2 *fix;           // for which [N] gets what the row's log probability moves by with it: (1 - p) (zx - zy, 1)
     __nv_bfloat16 *G;
     int ldg;
     int rows, row0, V;
@@ -232,6 +249,7 @@ struct MergeParams {
     const int *counting;
     const int *index;
     int loss_by_index;     // 1: loss_rows too
+    float *ratio;          // null, or [N] (as lse): what rounding the row's scale to bf16 left of it
 };
 
 struct TransposeParams {
@@ -245,6 +263,7 @@ struct TransposeParams {
     const long long *y;
     long long V, ignore_index;
     const float *coef;
+    const float *ratio;    // null, or what each row is multiplied by
 };
 
 
@@ -310,7 +329,8 @@ struct PairParams {
     long long pairs, N, V, ignore_index;
     const long long *y;
     const float *loss_rows;     // [N]: -log p of each counting row
-    const int *place;           // null, or where row i of the call is in loss_rows and coef
+    const float2 *fix;          // null, or [N] (as loss_rows): what a right label logit adds to log p, and its weight
+    const int *place;           // null, or where row i of the call is in loss_rows, fix and coef
     const float *ref;           // [2 pairs] or null (0)
     float beta, smoothing;
     int average;                // log probabilities per counting row
@@ -319,7 +339,8 @@ struct PairParams {
     float *seq_logp;            // [2 pairs]
     float *pair_loss;           // [pairs]
     float *loss;                // or null
-    float *coef;                // [N] or null
+    float *coef;                // [N] or null: rounded to bf16, and
+    float *ratio;               // [N]: what the rounding left of it
     int *hdr;
 };
 
@@ -520,8 +541,20 @@ cudaError_t launch_wait_selftest(int *hdr, unsigned long long limit_ns, cudaStre
 cudaError_t launch_compact(const long long *y, long long N, long long V, long long ign, int *hdr, int *index,
                            int *place, long long *labels, cudaStream_t s);
 // dst[j][D] = src[index[row0 + j]][D] for the rows there are of [row0, row0 + rows), zeros up to a multiple of 64
-cudaError_t launch_gather_rows(const __nv_bfloat16 *src, const int *index, const int *counting, long long row0,
-                               long long rows, long long D, __nv_bfloat16 *dst, int sms, cudaStream_t s);
+// What a chunk's rows are brought together from, and (W given) their labels' logits taken from.
+struct GatherParams {
+    const uint4 *src;            // H: the call's (with index) or the chunk's
+    const int *index;            // null: the rows lie there already
+    const int *counting;
+    uint4 *dst;
+    int row0, rows, vecs;
+    const uint4 *W;              // null: no logits
+    const long long *y;          // of the chunk's rows
+    long long V, ignore_index;
+    float inv_t;
+    float *zx;
+};
+cudaError_t launch_gather_rows(const GatherParams &p, int sms, cudaStream_t s);
 // dst[index[row0 + j]] = (accumulate ? that : 0) + the sum over s of src[s * stride + j D ..], as launch_combine_dh
 cudaError_t launch_scatter_dh(const float *src, int splits, long long stride, const int *index, const int *counting,
                               long long row0, long long rows, long long D, __nv_bfloat16 *dst, bool accumulate,
