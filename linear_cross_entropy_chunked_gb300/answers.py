@@ -21,9 +21,13 @@ def _vector(name, t, shape, dtype, dev):
         raise TypeError(f"{name} must be {dtype}")
     if t.device != dev or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)} tensor on the device of the other arguments")
-    if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError(f"{name} is a constant of the loss: detach it")
+    _constant(name, t)
     return t.data_ptr()
+
+
+def _constant(name, t):
+    if t is not None and t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} is a constant of the loss: detach it")
 
 
 def _policy_args(N, dev, advantages, old_logprobs, ref_logprobs, weights, clip_low, clip_high, beta, temperature):
@@ -297,8 +301,9 @@ def linear_policy_loss(H, W, y, advantages, old_logprobs=None, ref_logprobs=None
     if not (torch.is_grad_enabled() and (H.requires_grad or W.requires_grad)):
         loss, logprobs = policy_forward(H, W, y, advantages, **how)
         return loss.view(()), logprobs
+    _constant("advantages", advantages)
     for name in ("old_logprobs", "ref_logprobs", "weights"):
-        del how[name]
+        _constant(name, how.pop(name))
     return AnswerLossFunction.apply(
         H, W, lambda *t, **more: policy_fwd_bwd(*t, low_memory=low_memory, **how, **more),
         _one_buffer(H, chunk, low_memory), y, advantages, old_logprobs, ref_logprobs, weights)
@@ -317,7 +322,7 @@ def linear_preference_loss(H, W, y, offsets, ref_logprobs=None, beta=0.1, label_
     if not (torch.is_grad_enabled() and (H.requires_grad or W.requires_grad)):
         loss, seq, _, _ = preference_fwd_bwd(H, W, y, offsets, gradient=False, **how)
         return loss.view(()), seq
-    del how["ref_logprobs"]
+    _constant("ref_logprobs", how.pop("ref_logprobs"))
     return AnswerLossFunction.apply(H, W, lambda *t, **more: preference_fwd_bwd(*t, **how, **more),
                                     _one_buffer(H, chunk, low_memory), y, offsets, ref_logprobs)
 

@@ -214,7 +214,8 @@ def head(n, d, v, seed, ignored=0.3):
 
 def check_gradients(dH, dW, H, W, o, lb, out_rounding=2.0 ** -8):
     """G is rounded twice to bf16 (as exp(z - slab maximum), then scaled); sums in fp32 of up to 2^17 terms, of
-    which fewer than 2^8 follow one another; dH is rounded once more, dW is fp32."""
+    which fewer than 2^8 follow one another; dH is rounded once more, dW is fp32, but H's rows for it are rounded (times
+    what is left of a row's scale rounded to bf16)."""
     rel = 2 * 2.0 ** -8 + 4 * lb + 2.0 ** -14
     y = np.argmax(np.abs(o["dZ"]), 1)   # (mass takes the onehot from the oracle's own gradient)
     mass = np.abs(o["dZ"]) + 0.0
@@ -227,7 +228,7 @@ def check_gradients(dH, dW, H, W, o, lb, out_rounding=2.0 ** -8):
     assert (np.abs(cpu64(dH) - want) <= rel * (mass @ np.abs(w)) + out_rounding * np.abs(want) + 1e-30).all()
     if dW is not None:
         want = o["dZ"].T @ h
-        assert (np.abs(cpu64(dW) - want) <= rel * (mass.T @ np.abs(h)) + 1e-30).all()
+        assert (np.abs(cpu64(dW) - want) <= (rel + 2.0 ** -8) * (mass.T @ np.abs(h)) + 1e-30).all()
 
 
 def with_coefs(o, y, scale):
