@@ -920,24 +920,19 @@ __global__ void __launch_bounds__(PAIR_THREADS) lce_pairs_kernel(const __grid_co
         float slope = p.beta * (e * (m >= 0.f ? big : small) - (1.f - e) * (m >= 0.f ? small : big)) * d;
         if (m != m) slope = m;
         // p - onehot gets minus the slope of its row
-        const float full[2] = {-slope * share[0], slope * share[1]};
-        RoundedScale c[2];
-        for (int q = 0; q < 2; ++q) c[q] = p.ratio ? lce_round_scale(full[q]) : RoundedScale{full[q], 1.f};
-        auto put = [&](long long i, const RoundedScale &v) {
+        const float c[2] = {-slope * share[0], slope * share[1]};
+        auto put = [&](long long i, float v) {
             const long long at = p.place ? p.place[i] : i;
-            if (at < 0) return;
-            p.coef[at] = v.scale;
-            if (p.ratio) p.ratio[at] = v.ratio;
+            if (at >= 0) p.coef[at] = v;
         };
-        const RoundedScale none{0.f, 1.f};
         for (int q = 0; q < 2; ++q)
             for (long long i = off[2 * q] + t; i < off[2 * q + 1]; i += PAIR_THREADS)
-                put(i, label_counts(p.y[i], p.V, p.ignore_index) ? c[q] : none);
+                put(i, label_counts(p.y[i], p.V, p.ignore_index) ? c[q] : 0.f);
         // rows before the first sequence and behind the last
         if (k == 0)
-            for (long long i = t; i < p.N && i < off[0]; i += PAIR_THREADS) put(i, none);
+            for (long long i = t; i < p.N && i < off[0]; i += PAIR_THREADS) put(i, 0.f);
         if (k == p.pairs - 1)
-            for (long long i = off[3] + t; i < p.N; i += PAIR_THREADS) put(i, none);
+            for (long long i = off[3] + t; i < p.N; i += PAIR_THREADS) put(i, 0.f);
     }
     if (p.loss && last_to_finish(p.hdr + HDR_DONE, static_cast<int>(gridDim.x), &s_last)) {
         const double s = block_sum(p.pair_loss, p.pairs, s_red);

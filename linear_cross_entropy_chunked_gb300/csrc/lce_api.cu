@@ -307,7 +307,7 @@ struct Ctx {
     const int *index = nullptr;
     const __nv_bfloat16 *Hrows = nullptr;
     bool loss_by_index = false;
-    float *ratio = nullptr;      // [N]: what rounding the rows' scales to bf16 left of them
+    LabelRests rests{};          // (losses on answers with gradients)
     bool dw16 = false;           // dW is bf16 (one contraction)
 };
 
@@ -461,6 +461,9 @@ void base_params(const Ctx &c, GemmParams &p, long long row0, long long rows, in
     p.mean = c.reduction == LCE_REDUCTION_MEAN ? 1 : 0;
     p.f16 = c.f16 ? 1 : 0;
     p.inv_t = c.inv_t;
+    p.rests = c.rests;
+    p.Hc = reinterpret_cast<const uint4 *>(c.H + h_row(c, row0) * c.D);
+    p.W = reinterpret_cast<const uint4 *>(c.W);
     p.counting = c.index ? c.hdr + HDR_NVALID : nullptr;
 }
 
@@ -538,7 +541,6 @@ void set_row_filter(const Ctx &c, long long row0, TransposeParams &tp) {
     tp.V = c.V;
     tp.ignore_index = c.ign;
     tp.coef = c.coef ? c.coef + row0 : nullptr;
-    tp.ratio = c.ratio ? c.ratio + row0 : nullptr;
 }
 
 // H chunk^T into columns col0 .. col0 + rows - 1 of H^T (the K-major B operand of
@@ -634,7 +636,6 @@ lce_status run_bwd(const Ctx &c, long long row0, long long rows, int slot, const
     p.dW = dW;
     p.dw_accumulate = accumulate ? 1 : 0;
     p.dw_16 = c.dw16 ? 1 : 0;
-    p.ratio = c.ratio;
     const int units = cl == 2 ? c.pairs : c.sms;
     // profiling kind: a pair's second chunk (its dH with both chunks' dW), a pair's
     // first chunk (its dH alone), or a chunk's whole gradient phase
@@ -750,6 +751,9 @@ lce_status run_bwd(const Ctx &c, long long row0, long long rows, int slot, const
 lce_status run_grad(const Ctx &c, long long row0, long long rows, int slot, void *dHc,
                     bool acc_dh, float *dW, bool acc_dw, const float *dloss, const GradSpec &g) {
     if (g.dw_only) return run_bwd(c, row0, rows, slot, DhOut{dHc, false, 1, 0}, dW, acc_dw, dloss, g);
+    if (c.rests.first)
+        LCE_LAUNCH(launch_label_lists(reinterpret_cast<const long long *>(c.y) + row0, c.index ? c.hdr + HDR_NVALID : nullptr,
+                                      row0, rows, c.V, c.ign, c.rests.first, c.rests.next, c.s));
     const int want = dh_parts(c, rows, g.dh_alone);
     if (want <= 1 && !acc_dh && !c.index)
         return run_bwd(c, row0, rows, slot, DhOut{dHc, false, 1, 0}, dW, acc_dw, dloss, g);
@@ -793,7 +797,7 @@ void merge_params(const Ctx &c, long long row0, long long rows, float *lse, cons
     m.counting = c.index ? c.hdr + HDR_NVALID : nullptr;
     m.index = c.pol.adv ? c.index : nullptr;   // (a preference's rows go by their place)
     m.loss_by_index = c.loss_by_index ? 1 : 0;
-    m.ratio = c.pol.adv ? c.ratio : nullptr;   // (a preference's coefficients have been rounded already)
+    m.rest = c.rests.rest;
 }
 
 lce_status run_merge(const Ctx &c, long long row0, long long rows, float *lse,
@@ -887,10 +891,10 @@ long long answer_chunk(long long N, long long chunk, int flags) {
 // not where chunks do not end on k blocks of the dW contraction.
 struct GatherLayout {
     bool on = false;
-    size_t off_ratio = 0, off_index = 0, off_place = 0, off_labels = 0, off_H = 0, end = 0;
+    size_t off_rest = 0, off_next = 0, off_first = 0, off_index = 0, off_place = 0, off_labels = 0, off_H = 0, end = 0;
 };
 
-GatherLayout gather_layout(const Layout &L, long long N, long long D, size_t at) {
+GatherLayout gather_layout(const Layout &L, long long N, long long D, long long V, bool gradient, size_t at) {
     GatherLayout g;
     g.on = N > 256 && (L.nchunks <= 1 || L.C % BK == 0);
     g.end = at;
@@ -899,13 +903,23 @@ GatherLayout gather_layout(const Layout &L, long long N, long long D, size_t at)
         g.end += align_up(bytes, 1024);
         return o;
     };
-    g.off_ratio = take(sizeof(float) * static_cast<size_t>(N > 0 ? N : 1));   // (of rows that are not brought together too)
+    if (gradient) {   // (of rows that are not brought together too)
+        g.off_rest = take(sizeof(float) * static_cast<size_t>(L.C));
+        g.off_next = take(sizeof(int) * static_cast<size_t>(L.C));
+        g.off_first = take(sizeof(int) * static_cast<size_t>(L.frozen_w ? 0 : V));
+    }
     if (!g.on) return g;
     g.off_index = take(sizeof(int) * static_cast<size_t>(N));
     g.off_place = take(sizeof(int) * static_cast<size_t>(N));
     g.off_labels = take(sizeof(long long) * static_cast<size_t>(N));
     g.off_H = take(2 * static_cast<size_t>(L.C) * static_cast<size_t>(D));
     return g;
+}
+
+void set_rests(Ctx &c, const GatherLayout &g, bool with_dw) {
+    c.rests.rest = reinterpret_cast<float *>(c.ws + g.off_rest);
+    c.rests.next = reinterpret_cast<int *>(c.ws + g.off_next);
+    c.rests.first = with_dw ? reinterpret_cast<int *>(c.ws + g.off_first) : nullptr;
 }
 
 // H and y as setup gets them: the caller's, or their places in the workspace.
@@ -1167,7 +1181,7 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
     const void *Hs = H;
     const int64_t *ys = y;
     if (pol) {
-        gl = gather_layout(L0, N, D, L0.total + acc_dh_bytes(L0, D));
+        gl = gather_layout(L0, N, D, V, true, L0.total + acc_dh_bytes(L0, D));
         if (ws_bytes < gl.end) return LCE_ERR_WORKSPACE;
         if ((flags & LCE_DW_BF16) && (frozen || (flags & LCE_ACCUMULATE_DW) || L0.nchunks > 1)) return LCE_ERR_UNSUPPORTED;
         LCE_TRY(gather_inputs(gl, Hs, ys, ws));
@@ -1180,10 +1194,9 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
         c.pol = *pol;
         c.inv_t = pol->inv_t;
         c.answers = true;
-        c.ratio = reinterpret_cast<float *>(c.ws + gl.off_ratio);
+        set_rests(c, gl, !frozen);
         c.dw16 = (flags & LCE_DW_BF16) != 0;
         LCE_TRY(start_gather(c, gl, H, y));
-        if (gl.on && !frozen) LCE_ZERO(c.ratio, sizeof(float) * static_cast<size_t>(N));   // (for H^T behind the rows that count)
         if (gl.on) {   // what rows that do not count have
             c.loss_by_index = none;
             LCE_ZERO(none ? loss : c.loss_rows, sizeof(float) * static_cast<size_t>(N));
@@ -1258,11 +1271,10 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
             LCE_TRY(bring_rows(c, k, false));
             LCE_TRY(run_logits(c, MODE_LSE_P, row0, rows, static_cast<int>(2 * k), nullptr, nullptr,
                                c.Gb[0]));
-            // (the policy's H^T takes the ratios that the prep leaves)
-            LCE_TRY(run_prep(c, row0, rows, lse, dloss, rows_out, c.Gb[0], !frozen && !pol));
+            LCE_TRY(run_prep(c, row0, rows, lse, dloss, rows_out, c.Gb[0], !frozen));
             LCE_TRY(run_grad(c, row0, rows, static_cast<int>(2 * k + 1), dHb + row0 * c.D, acc_dh,
                              dW, k > 0 || acc_dw0, dloss,
-                             GradSpec{c.Gb[0], c.Gb[0], frozen ? 0 : rows, !pol, false}));
+                             GradSpec{c.Gb[0], c.Gb[0], frozen ? 0 : rows, true, false}));
         }
     }
     if (!none)
@@ -1316,7 +1328,7 @@ bool make_pref_layout(int64_t N, int64_t D, int64_t V, int64_t chunk, int64_t pa
                       PrefLayout &P) {
     if (!make_layout(N, D, V, chunk, P.L, (flags & LCE_FROZEN_W) != 0, true) || pairs <= 0 || pairs > (1ll << 24)) return false;
     const size_t rows = sizeof(float) * static_cast<size_t>(N > 0 ? N : 1);
-    P.gather = gather_layout(P.L, N, D, grad ? P.L.total + acc_dh_bytes(P.L, D) : P.L.fwd_total);
+    P.gather = gather_layout(P.L, N, D, V, grad, grad ? P.L.total + acc_dh_bytes(P.L, D) : P.L.fwd_total);
     size_t off = P.gather.end;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -1358,7 +1370,6 @@ PairParams pair_params(const int64_t *offsets, int64_t pairs, int64_t N, int64_t
     p.y = reinterpret_cast<const long long *>(y);
     p.loss_rows = loss_rows;
     p.place = nullptr;
-    p.ratio = nullptr;
     p.fix = nullptr;
     p.ref = ref;
     p.beta = beta;
@@ -1661,7 +1672,7 @@ lce_status lce_policy_workspace_size(int64_t N, int64_t D, int64_t V, int64_t ch
     if (!bytes || (flags & ~(LCE_FLAGS_ALL | LCE_DW_BF16)) ||
         !make_layout(N, D, V, gradient ? answer_chunk(N, chunk, flags) : chunk, L, (flags & LCE_FROZEN_W) != 0, true))
         return LCE_ERR_INVALID_ARG;
-    *bytes = gather_layout(L, N, D, gradient ? L.total + acc_dh_bytes(L, D) : L.fwd_total).end;
+    *bytes = gather_layout(L, N, D, V, gradient != 0, gradient ? L.total + acc_dh_bytes(L, D) : L.fwd_total).end;
     return LCE_OK;
 }
 
@@ -1679,7 +1690,7 @@ lce_status lce_policy_forward(const void *H, const void *W, const int64_t *y, co
                          temperature, logprobs));
     Layout L0;
     if (!make_layout(N, D, V, chunk, L0, false, true)) return LCE_ERR_INVALID_ARG;
-    const GatherLayout gl = gather_layout(L0, N, D, L0.fwd_total);
+    const GatherLayout gl = gather_layout(L0, N, D, V, false, L0.fwd_total);
     if (ws_bytes < gl.end) return LCE_ERR_WORKSPACE;
     const void *Hs = H;
     const int64_t *ys = y;
@@ -1773,8 +1784,7 @@ lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y
     c.reduction = LCE_REDUCTION_NONE;   // (of the rows: each has a coefficient of its own)
     c.answers = true;
     c.dw16 = (flags & LCE_DW_BF16) != 0;
-    if (grad) c.ratio = reinterpret_cast<float *>(c.ws + P.gather.off_ratio);
-    if (P.gather.on && grad && !frozen) LCE_ZERO(c.ratio, sizeof(float) * static_cast<size_t>(N));
+    if (grad) set_rests(c, P.gather, !frozen);
     c.zx = reinterpret_cast<float *>(c.ws + P.off_zx);
     c.fix = reinterpret_cast<float2 *>(c.ws + P.off_fix);
     float *lse = reinterpret_cast<float *>(c.ws + P.off_lse);
@@ -1794,7 +1804,6 @@ lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y
     PairParams pp = pair_params(offsets, pairs, N, V, ignore_index, y, c.loss_rows, ref_logprobs, beta, label_smoothing,
                                 average, dloss, reduction, loss, seq_logprobs,
                                 reinterpret_cast<float *>(c.ws + P.off_pair), coef, c.hdr);
-    pp.ratio = c.ratio;
     pp.fix = c.fix;
     pp.place = c.index ? reinterpret_cast<const int *>(c.ws + P.gather.off_place) : nullptr;
     LCE_LAUNCH(launch_pairs(pp, c.s));

@@ -191,10 +191,6 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_merge_kernel(const MergePar
 // operand of the dW contraction).
 
 constexpr int TT = 64;
-// Two values times a row's ratio.
-__device__ __forceinline__ uint32_t times2(uint32_t w, float f) {
-    return pack_bf16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
-}
 // Whether row r of the chunk is transposed as it is (else as zeros).
 __device__ __forceinline__ bool row_counts(const TransposeParams &p, int r) {
     if (p.coef && p.coef[r] == 0.f) return false;
@@ -216,13 +212,8 @@ __global__ void __launch_bounds__(256) lce_transpose_kernel(const TransposeParam
         const int rr = k >> 3, cb = (k & 7) * 8;
         const int r = r0 + rr, c = c0 + cb;
         uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (r < p.rows && c < p.cols && row_counts(p, r)) {
+        if (r < p.rows && c < p.cols && row_counts(p, r))
             u = *reinterpret_cast<const uint4 *>(p.src + static_cast<size_t>(r) * p.ld_src + c);
-            if (p.ratio) {
-                const float f = p.ratio[r];
-                u = make_uint4(times2(u.x, f), times2(u.y, f), times2(u.z, f), times2(u.w, f));
-            }
-        }
         uint32_t *dst = reinterpret_cast<uint32_t *>(tile + rr * TSTRIDE + cb);
         dst[0] = u.x;
         dst[1] = u.y;
@@ -281,13 +272,8 @@ __device__ __forceinline__ void transpose_tile(const TransposeParams &p, int c0,
         const int rr = k >> 3, cb = (k & 7) * 8;
         const int r = r0 + rr, c = c0 + cb;
         uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (r < p.rows && c < p.cols && row_counts(p, r)) {
+        if (r < p.rows && c < p.cols && row_counts(p, r))
             u = *reinterpret_cast<const uint4 *>(p.src + static_cast<size_t>(r) * p.ld_src + c);
-            if (p.ratio) {
-                const float f = p.ratio[r];
-                u = make_uint4(times2(u.x, f), times2(u.y, f), times2(u.z, f), times2(u.w, f));
-            }
-        }
         uint32_t *dst = reinterpret_cast<uint32_t *>(tile + rr * TSTRIDE + cb);
         dst[0] = u.x;
         dst[1] = u.y;
@@ -374,17 +360,13 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_prep_kernel(const PrepParam
         row_loss = pr.loss;
         scale *= -pr.slope * m.pol.inv_t;
     }
-    if (m.ratio) {
-        const RoundedScale rs = lce_round_scale(scale);
-        scale = rs.scale;
-        if (seg == 0 && threadIdx.x == 0) m.ratio[grow] = rs.ratio;
-    }
     if (seg == 0 && threadIdx.x == 0) {
         if (m.lse) m.lse[grow] = lse;
         if (m.pol.logp) m.pol.logp[of] = logp;
         m.loss_rows[m.loss_by_index ? of : grow] = row_loss;
     }
     const bool zero = m.zero_rows && scale == 0.f;
+    if (m.rest && (zero || !y_ok) && seg == 0 && threadIdx.x == 0) m.rest[r] = 0.f;
     const float lse2 = lse * LOG2E_F;
     const int ycol = y_ok ? static_cast<int>(yv) : -1;
     // the factor exp(m_p - lse) * s of each 128-column slab of the segment, once (a
@@ -417,8 +399,14 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_prep_kernel(const PrepParam
             else x = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&wv[q]));
             x.x *= f;
             x.y *= f;
-            if (c + 2 * q == ycol) x.x -= scale;
-            if (c + 2 * q + 1 == ycol) x.y -= scale;
+            if (c + 2 * q == ycol) {
+                x.x -= scale;
+                if (m.rest && !zero) m.rest[r] = lce_rest(x.x);
+            }
+            if (c + 2 * q + 1 == ycol) {
+                x.y -= scale;
+                if (m.rest && !zero) m.rest[r] = lce_rest(x.y);
+            }
             if (m.f16) {
                 __half2 h = __floats2half2_rn(x.x, x.y);
                 wv[q] = *reinterpret_cast<uint32_t *>(&h);
@@ -589,6 +577,44 @@ __global__ void __launch_bounds__(256) lce_gather_rows_kernel(const GatherParams
     }
 }
 
+// A thread per row compares its label with all of the chunk (a few us for 2048 rows; n^2 / 4 comparisons are far less than
+// the contractions' n V D). Which rows a list has, and their order, depend on the labels alone.
+__global__ void __launch_bounds__(256) lce_label_lists_kernel(const long long *__restrict__ y, const int *__restrict__ counting,
+                                                              int row0, int rows, long long V, long long ign,
+                                                              int *__restrict__ first, int *__restrict__ next) {
+    __shared__ __align__(16) int s_y[1024];
+    const int live = live_rows(counting, row0, rows);
+    const int r = blockIdx.x * 256 + threadIdx.x;
+    if (static_cast<int>(blockIdx.x) * 256 >= live) return;
+    auto label = [&](int i) {
+        const long long v = i < live ? y[i] : ign;
+        return v != ign && v >= 0 && v < V ? static_cast<int>(v) : -1;
+    };
+    const int mine = label(r);
+    int before = 0, after = -1;
+    for (int j0 = 0; j0 < live; j0 += 1024) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < 1024; i += 256) s_y[i] = label(j0 + i);
+        __syncthreads();
+#pragma unroll 4
+        for (int k = 0; k < 256; ++k) {
+            const int4 q = reinterpret_cast<const int4 *>(s_y)[k];
+            const int v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = j0 + 4 * k + e;
+                if (v[e] == mine) {
+                    before += j < r;
+                    if (j > r && after < 0) after = j;
+                }
+            }
+        }
+    }
+    if (mine < 0) return;
+    if (before == 0) first[mine] = r;
+    next[r] = before + 1 < REST_ROWS ? after : -1;
+}
+
 template <bool ACC>
 __global__ void __launch_bounds__(256) lce_scatter_dh_kernel(const float *__restrict__ src, int splits, long long stride,
                                                              const int *__restrict__ index,
@@ -717,6 +743,15 @@ cudaError_t launch_compact(const long long *y, long long N, long long V, long lo
 cudaError_t launch_gather_rows(const GatherParams &p, int sms, cudaStream_t s) {
     const int g = static_cast<int>(p.rows < 8ll * sms ? p.rows : 8ll * sms);
     lce_gather_rows_kernel<<<g, 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_label_lists(const long long *y, const int *counting, long long row0, long long rows, long long V,
+                               long long ign, int *first, int *next, cudaStream_t s) {
+    const cudaError_t e = cudaMemsetAsync(first, 0xff, sizeof(int) * static_cast<size_t>(V), s);   // -1
+    if (e != cudaSuccess) return e;
+    lce_label_lists_kernel<<<static_cast<unsigned>((rows + 255) / 256), 256, 0, s>>>(
+        y, counting, static_cast<int>(row0), static_cast<int>(rows), V, ign, first, next);
     return cudaGetLastError();
 }
 

@@ -271,8 +271,10 @@ __device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Live 
                                     p.row0 + r, y_ok, p.f16);
             lse2 = p.lse[p.row0 + r] * LOG2E;
         }
+        if (p.rests.rest && row_ok && !y_ok && col0 == 0) p.rests.rest[r] = 0.f;
         // a row that adds nothing is zeros, whatever its logits are
         const int rcols = scale != 0.f ? ncols : 0;
+        float gy = 0.f;   // the label's entry
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
             const bool box_ok = (c >> 1) * 64 < ncols;
@@ -283,13 +285,17 @@ __device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Live 
             for (int j = 0; j < 32; ++j) {
                 const int cj = c * 32 + j;
                 float g = (cj < rcols) ? ex2(fmaf(v[j], k2, -lse2)) * scale : 0.f;
-                if (cj == yl) g -= scale;
+                if (cj == yl) {
+                    g -= scale;
+                    gy = g;
+                }
                 v[j] = g;
             }
             if ((c & 1) == 0) st.acquire();
             st.put_h16((c & 1) * 4, v, p.f16);
             if (c & 1) st.issue(&p.tmS0, col0 + (c >> 1) * 64, box_y);
         }
+        if (p.rests.rest && yl >= 0 && yl < ncols) p.rests.rest[r] = lce_rest(gy);
     } else {
         // pass 1: slab max (and the target logit when it falls in this slab)
         float m = -INFINITY, zt = 0.f;
@@ -332,6 +338,21 @@ __device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Live 
     }
 }
 
+// v += e * the 32 values of a row from column col on (those there are).
+__device__ __forceinline__ void add_rest(float *v, float e, const uint4 *row, int col, int D) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        if (col + q * 8 >= D) break;
+        const uint4 u = __ldg(row + col / 8 + q);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[q * 8 + 2 * k] = fmaf(e, __uint_as_float(w[k] << 16), v[q * 8 + 2 * k]);
+            v[q * 8 + 2 * k + 1] = fmaf(e, __uint_as_float(w[k] & 0xffff0000u), v[q * 8 + 2 * k + 1]);
+        }
+    }
+}
+
 // Gradient tiles: dH (bf16 / fp16, or fp32 when dh_fp32) or dW (fp32, stored by
 // a call's first dW contraction, reduce-added into dW by the later ones). out_scale: the factor
 // fp16 calls apply here instead of in G (1 for bf16).
@@ -342,8 +363,17 @@ __device__ __forceinline__ void epilogue_grad(const GemmParams &p, const Live &l
     // a tile entirely past the output rows (the second tile of a CTA pair at an
     // odd row-block count) stores nothing
     if (tl.m0 >= (tl.type == TILE_MAIN ? lv.rows : p.V)) return;
-    // (dH's row of this thread, on the path whose rows' scales were rounded)
-    const float ratio = p.ratio && tl.type == TILE_MAIN && tl.m0 + st.row < lv.rows ? p.ratio[p.row0 + tl.m0 + st.row] : 1.f;
+    // what rounding left of the label entries of G: this thread's row of dH has one (added in the first part of
+    // the vocabulary), its row of dW those of the rows in its label's list
+    int at = -1;
+    if (p.rests.rest) {
+        const int r = tl.m0 + st.row;
+        if (tl.type == TILE_MAIN) {
+            if (r < lv.rows && tl.srow == 0 && p.rests.rest[r] != 0.f) at = r;
+        } else if (r < p.V) {
+            at = p.rests.first[r];
+        }
+    }
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         float v[32];
@@ -352,9 +382,10 @@ __device__ __forceinline__ void epilogue_grad(const GemmParams &p, const Live &l
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] *= out_scale;
         }
-        if (ratio != 1.f) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] *= ratio;
+        for (int i = at; i >= 0; i = tl.type == TILE_MAIN ? -1 : p.rests.next[i]) {
+            const float e = p.rests.rest[i];
+            const uint4 *row = tl.type == TILE_MAIN ? p.W + p.y[p.row0 + i] * (p.D / 8) : p.Hc + static_cast<size_t>(i) * (p.D / 8);
+            if (e != 0.f) add_rest(v, e, row, col0 + c * 32, p.D);   // (a row whose scale is 0 holds anything)
         }
         if (tl.type == TILE_MAIN ? !p.dh_fp32 : p.dw_16) {
             if (col0 + (c >> 1) * 64 >= p.D) continue;

@@ -151,17 +151,20 @@ __device__ __forceinline__ PolicyRow lce_policy_row(const PolicyParams &p, long 
     return lce_policy_row(p, lce_policy_inputs(p, i), logp);
 }
 
-// A row's scale as a bf16 number, and what that leaves of it as a factor. G = (p - onehot) * scale is stored in bf16,
-// and where the label is unlikely its entry is nearly -scale: with the rounded scale that entry is exact, and
-// the factor is made up for in fp32 on dH's rows and in H's rows for dW. (Rounded with G, a scale that all rows of a
-// sequence share would make up to 2^-9 of all their gradient go missing.)
-struct RoundedScale {
-    float scale, ratio;
+// Losses on answers keep what the rounding of G to bf16 leaves of each row's label entry, (p - 1) scale: where the label is
+// unlikely that entry is nearly all of the row, and half a step of it (2^-9) would be missing from dH's
+// whole row and from dW's row of the label. The gradient epilogues add the remainders in fp32: rest W[y] to the row of
+// dH, and to dW's row v those of the rows whose label it is, from first[v] on by next, REST_ROWS of them at
+// most (of more rows the roundings average out, and one thread would have them all to do).
+constexpr int REST_ROWS = 8;
+struct LabelRests {
+    float *rest;           // [rows of a chunk]; null: not kept
+    int *first;            // [V]: the first row of the chunk with that label, or -1
+    int *next;             // [rows of a chunk]
 };
-__device__ __forceinline__ RoundedScale lce_round_scale(float s) {
-    const float r = __bfloat162float(__float2bfloat16_rn(s));
-    if (!(fabsf(r) < INFINITY) || r == 0.f) return RoundedScale{s, 1.f};
-    return RoundedScale{r, s / r};
+__device__ __forceinline__ float lce_rest(float g) {
+    const float e = g - __bfloat162float(__float2bfloat16_rn(g));
+    return fabsf(e) < INFINITY ? e : 0.f;
 }
 
 // Workspace header (int32 words).
@@ -210,7 +213,8 @@ struct GemmParams {
     int dw_accumulate;     // 0: store, 1: add to existing dW
     int dh_fp32;           // 1: dH tiles stored as fp32 (tmS0 an fp32 map)
     int dw_16;             // 1: dW stored as bf16 (tmS1 a bf16 map; not added to)
-    const float *ratio;    // null, or what row i of dH is multiplied by (global [N])
+    LabelRests rests;      // (written by the G epilogue, read by the gradients' epilogues)
+    const uint4 *Hc, *W;   // with rests: the chunk's rows of H, and W
     // dH launches: the vocabulary (K) range of every dH tile split in k_splits
     // parts of kb_per_split k blocks; part s stores fp32 partial sums at row
     // offset s * split_rows of the tmS0 map (k_splits <= 1: one part, no offset)
@@ -249,7 +253,7 @@ struct MergeParams {
     const int *counting;
     const int *index;
     int loss_by_index;     // 1: loss_rows too
-    float *ratio;          // null, or [N] (as lse): what rounding the row's scale to bf16 left of it
+    float *rest;           // null, or [rows]: what rounding left of the label's entry of G
 };
 
 struct TransposeParams {
@@ -263,7 +267,6 @@ struct TransposeParams {
     const long long *y;
     long long V, ignore_index;
     const float *coef;
-    const float *ratio;    // null, or what each row is multiplied by
 };
 
 
@@ -339,8 +342,7 @@ struct PairParams {
     float *seq_logp;            // [2 pairs]
     float *pair_loss;           // [pairs]
     float *loss;                // or null
-    float *coef;                // [N] or null: rounded to bf16, and
-    float *ratio;               // [N]: what the rounding left of it
+    float *coef;                // [N] or null
     int *hdr;
 };
 
@@ -541,6 +543,9 @@ cudaError_t launch_wait_selftest(int *hdr, unsigned long long limit_ns, cudaStre
 cudaError_t launch_compact(const long long *y, long long N, long long V, long long ign, int *hdr, int *index,
                            int *place, long long *labels, cudaStream_t s);
 // dst[j][D] = src[index[row0 + j]][D] for the rows there are of [row0, row0 + rows), zeros up to a multiple of 64
+// The lists of LabelRests for the chunk's labels y (counting, row0: as for the rows brought together).
+cudaError_t launch_label_lists(const long long *y, const int *counting, long long row0, long long rows, long long V,
+                               long long ign, int *first, int *next, cudaStream_t s);
 // What a chunk's rows are brought together from, and (W given) their labels' logits taken from.
 struct GatherParams {
     const uint4 *src;            // H: the call's (with index) or the chunk's

@@ -46,15 +46,7 @@ def test_a_policy_step(n, d, v, group):
     lb = logp_bound(Z, 0.8, v) + cut_sums(H, W, 0.8)
     assert np.abs(cpu64(logprobs) - o["logprobs"]).max() <= lb
     assert abs(loss.item() - o["loss"]) <= (2 * lb + 2.0 ** -20) * o["terms"].sum() / n
-    coefs = with_coefs(o, tokens.cpu(), o["mass"])
-    check_gradients(H.grad, None, H, W, coefs, lb)
-    # (dW is rounded to bf16)
-    onehot = np.zeros_like(o["p"])
-    onehot[np.arange(n), tokens.cpu().numpy()] = 1.0
-    want = o["dZ"].T @ cpu64(H)
-    mass = (o["mass"][:, None] * (o["p"] + onehot)).T @ np.abs(cpu64(H))
-    bound = (3 * 2.0 ** -8 + 4 * lb + 2.0 ** -14) * mass
-    assert (np.abs(cpu64(W.grad) - want) <= bound + 2.0 ** -8 * (np.abs(want) + bound) + 1e-30).all()
+    check_gradients(H.grad, W.grad, H, W, with_coefs(o, tokens.cpu(), o["mass"]), lb, dw_rounding=2.0 ** -8)
     before = [H.grad.clone(), W.grad.clone()]
     norm = lce.clip_grad_norm([H.grad, W.grad], 0.01)
     want, scaled = ops_oracle.clip([cpu64(b) for b in before], 0.01)

@@ -173,8 +173,8 @@ def test_head(n, d, v, pairs, chunk, mode):
     Hz = torch.nan_to_num(H.double())
     lb = logp_bound(Z, 1.0, v) + 2 * (2 * d + 8) * 2.0 ** -24 * float((Hz.abs() @ W.double().abs().t()).max())
     rel = check(loss, seq, o, off.numpy(), lb, 0.3)
-    coefs = np.where(o["coef"] != 0, np.abs(o["coef"]) + 0.3 / pairs * rel * 2.0 ** 7, 0.0)
-    check_gradients(dH, dW, Hz, W, o | {"coefs": coefs, "y": np.where(o["ok"], y.numpy(), 0)}, lb)
+    check_gradients(dH, dW, Hz, W, o | {"coefs": o["coef"], "y": np.where(o["ok"], y.numpy(), 0),
+                                        "coef_err": np.where(o["coef"] != 0, 0.3 / pairs * rel, 0.0)}, lb)
     assert not cpu64(dH)[o["coef"] == 0].any()
     l2, s2, h2, w2 = lce.preference_fwd_bwd(*args, beta=0.3, label_smoothing=0.1, chunk=chunk, gradient=False)
     assert h2 is None and w2 is None and torch.equal(l2, loss) and torch.equal(s2, seq)
