@@ -112,6 +112,7 @@ struct Layout {
                              // chunks runs once, over both chunks' G (K = 2 chunks)
     size_t gbuf_bytes = 0;   // bytes of one chunk buffer (the two are contiguous)
     bool frozen_w = false;   // no dW contraction (LCE_FROZEN_W)
+    bool answers = false;    // a loss on answers: only some of the rows may count
     int dh_splits = 1;       // vocabulary parts of a full chunk's dH tiles
     long long ldp = 0;       // rows per fp32 dH partial array: chunk rows rounded up to 128
     size_t off_loss_rows = 0, off_zy = 0, off_parts = 0, off_G = 0, off_HT = 0, off_dHp = 0;
@@ -127,19 +128,28 @@ struct Layout {
 // With W frozen the dH tiles have the GPU to themselves: they are split into the
 // most parts (at most DH_MAX_SPLITS) that keep them within one wave of the
 // DH_ALONE_PAIRS CTA pairs a GB300 holds at once (152 SMs).
+// Losses on answers, where some of the rows count and only the device knows how many: into parts for two
+// waves. 1954 of 2777 rows x 50257 x 1600, all in one chunk: 617 us for the gradient in one part (32 of its 44 tiles there,
+// on 76 pairs), 243 in four; 487 of 700 rows: 155 -> 97; 1071 of 1531, where one wave is nearly full: 158 -> 154. (Three
+// waves: 252, 86 and 165.)
 constexpr int DH_ALONE_PAIRS = 76;
+constexpr int DH_ANSWERS_MAX_SPLITS = 16;
 
-int dh_splits_for(long long rows, long long D, long long V, bool frozen_w = false) {
+int dh_splits_for(long long rows, long long D, long long V, bool frozen_w = false, bool answers = false) {
     if (V < DH_SPLIT_MIN_V || rows <= 0) return 1;
     const long long tiles = cdiv(cdiv(rows, BM), 2) * cdiv(D, BN_WIDE);
     long long sp = frozen_w ? DH_ALONE_PAIRS / tiles : cdiv(DH_SPLIT_TILES, tiles);
     if (sp > DH_MAX_SPLITS) sp = DH_MAX_SPLITS;
+    if (answers && frozen_w) {
+        sp = cdiv(2 * DH_ALONE_PAIRS, tiles);
+        if (sp > DH_ANSWERS_MAX_SPLITS) sp = DH_ANSWERS_MAX_SPLITS;
+    }
     if (sp > cdiv(V, BK)) sp = cdiv(V, BK);
     return sp < 1 ? 1 : static_cast<int>(sp);
 }
 
 bool make_layout(long long N, long long D, long long V, long long chunk, Layout &L,
-                 bool frozen_w = false, bool low_mem = false) {
+                 bool frozen_w = false, bool low_mem = false, bool answers = false) {
     if (N < 0 || D <= 0 || V <= 0 || chunk <= 0) return false;
     if (D % 8 != 0) return false;
     if (N > 0x7fffffffll || D > 0x7fffffffll || V > MAX_V) return false;
@@ -179,7 +189,8 @@ bool make_layout(long long N, long long D, long long V, long long chunk, Layout 
     if (!frozen_w) off += align_up(2 * static_cast<size_t>(D) * L.ldt, 1024);
     // fp32 dH partial sums of a split dH contraction, one [ldp][D] array per part
     // (a single array, past `total`, serves callers that accumulate into dH)
-    L.dh_splits = dh_splits_for(L.C, D, V, frozen_w);
+    L.answers = answers;
+    L.dh_splits = dh_splits_for(L.C, D, V, frozen_w, answers);
     // the first chunk of a pair runs its dH tiles alone (split for all pairs)
     if (L.nbuf == 2 && dh_splits_for(L.C, D, V, true) > L.dh_splits)
         L.dh_splits = dh_splits_for(L.C, D, V, true);
@@ -398,9 +409,9 @@ lce_status setup(Ctx &c, const void *H, const void *W, const int64_t *y, int64_t
                  int64_t V, int64_t ign, int64_t chunk, void *ws, size_t ws_bytes,
                  lce_stream_t stream, bool h_chunked = false, bool f16 = false,
                  bool frozen_w = false, bool fwd_only = false, bool low_mem = false,
-                 bool scan = true) {
+                 bool scan = true, bool answers = false) {
     g_launches = 0;
-    if (!make_layout(N, D, V, chunk, c.L, frozen_w, low_mem)) return LCE_ERR_INVALID_ARG;
+    if (!make_layout(N, D, V, chunk, c.L, frozen_w, low_mem, answers)) return LCE_ERR_INVALID_ARG;
     if (!ws) return LCE_ERR_INVALID_ARG;
     if (N > 0 && (!H || !y)) return LCE_ERR_INVALID_ARG;
     if (!W) return LCE_ERR_INVALID_ARG;
@@ -531,7 +542,7 @@ struct DhOut {
 // alone: the dH tiles have the GPU to themselves (no dW tiles beside them).
 int dh_parts(const Ctx &c, long long rows, bool alone) {
     if (c.pairs <= 0) return 1;
-    const int sp = dh_splits_for(rows, c.D, c.V, c.L.frozen_w || alone);
+    const int sp = dh_splits_for(rows, c.D, c.V, c.L.frozen_w || alone, c.L.answers);
     return sp < c.L.dh_splits ? sp : c.L.dh_splits;
 }
 
@@ -763,7 +774,8 @@ lce_status run_grad(const Ctx &c, long long row0, long long rows, int slot, void
                     &parts));
     if (c.index) {
         LCE_LAUNCH(launch_scatter_dh(dHp, parts, c.L.ldp * c.D, c.index, c.hdr + HDR_NVALID, row0, rows, c.D,
-                                     static_cast<__nv_bfloat16 *>(dHc) - row0 * c.D, acc_dh, c.sms, c.s));
+                                     c.rests.rest, reinterpret_cast<const long long *>(c.y) + row0,
+                                     reinterpret_cast<const uint4 *>(c.W), static_cast<__nv_bfloat16 *>(dHc) - row0 * c.D, acc_dh, c.sms, c.s));
         return LCE_OK;
     }
     LCE_LAUNCH(launch_combine_dh(dHp, parts, c.L.ldp * c.D, dHc, rows * c.D, c.f16, acc_dh,
@@ -1175,7 +1187,7 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
     const bool low_mem = pol || (flags & LCE_LOW_MEMORY) != 0;
     if (pol) chunk = answer_chunk(N, chunk, flags);
     Layout L0;
-    if (!make_layout(N, D, V, chunk, L0, frozen, low_mem)) return LCE_ERR_INVALID_ARG;
+    if (!make_layout(N, D, V, chunk, L0, frozen, low_mem, pol != nullptr)) return LCE_ERR_INVALID_ARG;
     if (acc_dh && ws_bytes < L0.total + acc_dh_bytes(L0, D)) return LCE_ERR_WORKSPACE;
     GatherLayout gl;
     const void *Hs = H;
@@ -1188,7 +1200,7 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
     }
     Ctx c;
     LCE_TRY(setup(c, Hs, W, ys, N, D, V, ignore_index, chunk, ws, ws_bytes, stream, gl.on, f16,
-                  frozen, false, low_mem, !gl.on));
+                  frozen, false, low_mem, !gl.on, pol != nullptr));
     c.reduction = reduction;
     if (pol) {
         c.pol = *pol;
@@ -1326,7 +1338,7 @@ struct PrefLayout {
 // (chunk: as answer_chunk has it)
 bool make_pref_layout(int64_t N, int64_t D, int64_t V, int64_t chunk, int64_t pairs, int flags, bool grad,
                       PrefLayout &P) {
-    if (!make_layout(N, D, V, chunk, P.L, (flags & LCE_FROZEN_W) != 0, true) || pairs <= 0 || pairs > (1ll << 24)) return false;
+    if (!make_layout(N, D, V, chunk, P.L, (flags & LCE_FROZEN_W) != 0, true, true) || pairs <= 0 || pairs > (1ll << 24)) return false;
     const size_t rows = sizeof(float) * static_cast<size_t>(N > 0 ? N : 1);
     P.gather = gather_layout(P.L, N, D, V, grad, grad ? P.L.total + acc_dh_bytes(P.L, D) : P.L.fwd_total);
     size_t off = P.gather.end;
@@ -1670,7 +1682,7 @@ lce_status lce_policy_workspace_size(int64_t N, int64_t D, int64_t V, int64_t ch
                                      size_t *bytes) {
     Layout L;
     if (!bytes || (flags & ~(LCE_FLAGS_ALL | LCE_DW_BF16)) ||
-        !make_layout(N, D, V, gradient ? answer_chunk(N, chunk, flags) : chunk, L, (flags & LCE_FROZEN_W) != 0, true))
+        !make_layout(N, D, V, gradient ? answer_chunk(N, chunk, flags) : chunk, L, (flags & LCE_FROZEN_W) != 0, true, true))
         return LCE_ERR_INVALID_ARG;
     *bytes = gather_layout(L, N, D, V, gradient != 0, gradient ? L.total + acc_dh_bytes(L, D) : L.fwd_total).end;
     return LCE_OK;
@@ -1778,7 +1790,7 @@ lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y
     LCE_TRY(gather_inputs(P.gather, Hs, ys, ws));
     Ctx c;
     LCE_TRY(setup(c, Hs, W, ys, N, D, V, ignore_index, chunk, ws, ws_bytes, stream, P.gather.on, false,
-                  (flags & LCE_FROZEN_W) != 0, !grad, true, !P.gather.on));
+                  (flags & LCE_FROZEN_W) != 0, !grad, true, !P.gather.on, true));
     LCE_TRY(start_gather(c, P.gather, H, y));
     if (P.gather.on && grad && !acc_dh) LCE_ZERO(dH, 2 * static_cast<size_t>(N) * static_cast<size_t>(D));
     c.reduction = LCE_REDUCTION_NONE;   // (of the rows: each has a coefficient of its own)

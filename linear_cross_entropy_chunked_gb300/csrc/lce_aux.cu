@@ -615,11 +615,16 @@ __global__ void __launch_bounds__(256) lce_label_lists_kernel(const long long *_
     next[r] = before + 1 < REST_ROWS ? after : -1;
 }
 
+// The rows of dH that were brought together, to theirs of the call's; what rounding left of their label entries is added
+// on the way, whole rows of W at a time (in the gradient's epilogue, a row a thread, it took 13 of 172 us at
+// 1072 rows x 50257 x 1600).
 template <bool ACC>
 __global__ void __launch_bounds__(256) lce_scatter_dh_kernel(const float *__restrict__ src, int splits, long long stride,
                                                              const int *__restrict__ index,
                                                              const int *__restrict__ counting, int row0, int rows,
-                                                             int vecs, uint4 *__restrict__ dst) {
+                                                             int vecs, const float *__restrict__ rest,
+                                                             const long long *__restrict__ y, const uint4 *__restrict__ W,
+                                                             uint4 *__restrict__ dst) {
     const int live = live_rows(counting, row0, rows);
     const long long n = static_cast<long long>(live) * vecs;
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += 256ll * gridDim.x) {
@@ -630,8 +635,19 @@ __global__ void __launch_bounds__(256) lce_scatter_dh_kernel(const float *__rest
             a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
             b.x += e.x; b.y += e.y; b.z += e.z; b.w += e.w;
         }
-        const float s[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        uint4 *to = dst + static_cast<size_t>(index[row0 + i / vecs]) * vecs + i % vecs;
+        float s[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const int r = static_cast<int>(i / vecs), v = static_cast<int>(i % vecs);
+        const float e = rest[r];
+        if (e != 0.f) {
+            const uint4 u = __ldg(W + y[r] * vecs + v);
+            const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                s[2 * q] = fmaf(e, __uint_as_float(x[q] << 16), s[2 * q]);
+                s[2 * q + 1] = fmaf(e, __uint_as_float(x[q] & 0xffff0000u), s[2 * q + 1]);
+            }
+        }
+        uint4 *to = dst + static_cast<size_t>(index[row0 + r]) * vecs + v;
         uint4 d = ACC ? *to : make_uint4(0u, 0u, 0u, 0u);
         uint32_t *w = &d.x;
 #pragma unroll
@@ -756,15 +772,15 @@ cudaError_t launch_label_lists(const long long *y, const int *counting, long lon
 }
 
 cudaError_t launch_scatter_dh(const float *src, int splits, long long stride, const int *index, const int *counting,
-                              long long row0, long long rows, long long D, __nv_bfloat16 *dst, bool accumulate,
-                              int sms, cudaStream_t s) {
+                              long long row0, long long rows, long long D, const float *rest, const long long *y, const uint4 *W,
+                              __nv_bfloat16 *dst, bool accumulate, int sms, cudaStream_t s) {
     long long blocks = (rows * (D / 8) + 255) / 256;
     if (blocks > 8ll * sms) blocks = 8ll * sms;
     const int g = static_cast<int>(blocks), r0 = static_cast<int>(row0), r = static_cast<int>(rows);
     const int vecs = static_cast<int>(D / 8);
     uint4 *to = reinterpret_cast<uint4 *>(dst);
-    if (accumulate) lce_scatter_dh_kernel<true><<<g, 256, 0, s>>>(src, splits, stride, index, counting, r0, r, vecs, to);
-    else lce_scatter_dh_kernel<false><<<g, 256, 0, s>>>(src, splits, stride, index, counting, r0, r, vecs, to);
+    (accumulate ? lce_scatter_dh_kernel<true> : lce_scatter_dh_kernel<false>)<<<g, 256, 0, s>>>(
+        src, splits, stride, index, counting, r0, r, vecs, rest, y, W, to);
     return cudaGetLastError();
 }
 

@@ -364,12 +364,12 @@ __device__ __forceinline__ void epilogue_grad(const GemmParams &p, const Live &l
     // odd row-block count) stores nothing
     if (tl.m0 >= (tl.type == TILE_MAIN ? lv.rows : p.V)) return;
     // what rounding left of the label entries of G: this thread's row of dH has one (added in the first part of
-    // the vocabulary), its row of dW those of the rows in its label's list
+    // the vocabulary; rows brought together get it on their way back), its row of dW those of the rows in its label's list
     int at = -1;
     if (p.rests.rest) {
         const int r = tl.m0 + st.row;
         if (tl.type == TILE_MAIN) {
-            if (r < lv.rows && tl.srow == 0 && p.rests.rest[r] != 0.f) at = r;
+            if (!p.counting && r < lv.rows && tl.srow == 0 && p.rests.rest[r] != 0.f) at = r;
         } else if (r < p.V) {
             at = p.rests.first[r];
         }
@@ -607,11 +607,14 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
                     } else if constexpr (MODE == MODE_DH) {
                         // A = G rows (K-major); B = W, MN-major, two 256-column halves
                         // of which this CTA loads 128 columns each
-                        if (leader) mbar_arrive_expect_tx(fb, 2 * P::kStageBytes);
+                        // (a second half that lies behind D is left out)
+                        const bool one = tl.n0 + BN >= p.D;
+                        if (leader) mbar_arrive_expect_tx(fb, 2 * (P::kStageBytes - (one ? 16384 : 0)));
                         const uint32_t lfb = map_to_rank(fb, 0);
                         tma_load_2d_pair(sA, &p.tmA0, lfb, kx, tl.m0);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
+                            if (h == 1 && one) break;
                             const int nb = tl.n0 + h * BN + static_cast<int>(crank) * (BN / 2);
                             tma_load_2d_pair(sB + h * 16384, &p.tmB0, lfb, nb, kx);
                             tma_load_2d_pair(sB + h * 16384 + 8192, &p.tmB0, lfb, nb + 64, kx);
@@ -703,7 +706,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
                         if constexpr (CL == 2) umma_bf16_pair(d_tmem, a, b, idesc, accumulate);
                         else umma_bf16(d_tmem, a, b, idesc, accumulate);
                         // the second 256-column half: same A, B 16 KB further on
-                        if constexpr (MODE == MODE_DH)
+                        if (MODE == MODE_DH && tl.n0 + BN < p.D)
                             umma_bf16_pair(d_tmem + BN, a, b + static_cast<uint64_t>(16384u >> 4), idesc,
                                            accumulate);
                     }

@@ -153,8 +153,8 @@ __device__ __forceinline__ PolicyRow lce_policy_row(const PolicyParams &p, long 
 
 // Losses on answers keep what the rounding of G to bf16 leaves of each row's label entry, (p - 1) scale: where the label is
 // unlikely that entry is nearly all of the row, and half a step of it (2^-9) would be missing from dH's
-// whole row and from dW's row of the label. The gradient epilogues add the remainders in fp32: rest W[y] to the row of
-// dH, and to dW's row v those of the rows whose label it is, from first[v] on by next, REST_ROWS of them at
+// whole row and from dW's row of the label. The remainders are added in fp32: rest W[y] to the row of
+// dH (in the gradient's epilogue, or where the rows are taken to their places), and, in the epilogue, to dW's row v those of the rows whose label it is, from first[v] on by next, REST_ROWS of them at
 // most (of more rows the roundings average out, and one thread would have them all to do).
 constexpr int REST_ROWS = 8;
 struct LabelRests {
@@ -562,8 +562,8 @@ struct GatherParams {
 cudaError_t launch_gather_rows(const GatherParams &p, int sms, cudaStream_t s);
 // dst[index[row0 + j]] = (accumulate ? that : 0) + the sum over s of src[s * stride + j D ..], as launch_combine_dh
 cudaError_t launch_scatter_dh(const float *src, int splits, long long stride, const int *index, const int *counting,
-                              long long row0, long long rows, long long D, __nv_bfloat16 *dst, bool accumulate,
-                              int sms, cudaStream_t s);
+                              long long row0, long long rows, long long D, const float *rest, const long long *y, const uint4 *W,
+                              __nv_bfloat16 *dst, bool accumulate, int sms, cudaStream_t s);
 cudaError_t launch_combine_dh(const float *src, int splits, long long stride, void *dst,
                               long long n, bool f16, bool accumulate, int sms, cudaStream_t s);
 cudaError_t launch_rmsnorm_fwd(const NormParams &p, cudaStream_t s);
