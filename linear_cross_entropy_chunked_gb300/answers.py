@@ -243,14 +243,16 @@ class AnswerLossFunction(torch.autograd.Function):
     of 1 (fwd_bwd), in the dtypes of H and W where that takes one contraction; the backward scales them, which
     the loss is linear in, in place (nothing is read or written where the upstream gradient is 1; another one
     rounds once more), and hands them over. A second backward through the same graph forms them again, and so
-    does a backward that is captured without its forward (each replay would scale them once more). A W without
+    does a backward that is captured without its forward (each replay would scale them once more; captured in a
+    graph of its own behind that of its forward, it is replayed once for each replay of that). A W without
     requires_grad is frozen (no dW work). The log probabilities beside the loss carry no gradient."""
 
     @staticmethod
     def forward(ctx, H, W, fwd_bwd, one, *constants):
         train = ctx.needs_input_grad[1]
         how = {"compute_dW": train, "dW_dtype": torch.bfloat16 if train and one else torch.float32}
-        loss, logprobs, *ctx.gradients = fwd_bwd(H, W, *constants, **how)
+        loss, logprobs, *gradients = fwd_bwd(H, W, *constants, **how)
+        ctx.gradients = [gradients]   # (taken once, whichever of two threads comes first)
         ctx.save_for_backward(H, W, *constants)
         ctx.fwd_bwd, ctx.how = fwd_bwd, how
         ctx.captured = H.is_cuda and torch.cuda.is_current_stream_capturing()
@@ -263,11 +265,17 @@ class AnswerLossFunction(torch.autograd.Function):
         tensors = ctx.saved_tensors   # (that none was written to since is checked here)
         g = g.to(torch.float32).contiguous()
         with _b._on(tensors[0].device, None) as s:
-            if ctx.gradients is None or torch.cuda.is_current_stream_capturing() != ctx.captured:
+            mine = None
+            if torch.cuda.is_current_stream_capturing() == ctx.captured:
+                try:
+                    mine = ctx.gradients.pop()
+                except IndexError:
+                    pass
+            if mine is None:
                 _, _, dH, dW = ctx.fwd_bwd(*tensors, dloss=g, **ctx.how)
                 dW = dW if dW is None or dW.dtype == tensors[1].dtype else dW.to(tensors[1].dtype)
             else:
-                (dH, dW), ctx.gradients = ctx.gradients, None
+                dH, dW = mine
                 if ctx.needs_input_grad[0]:
                     _scale_in_place(dH, g, s)
                 if dW is not None:

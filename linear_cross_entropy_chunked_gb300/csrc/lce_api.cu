@@ -1295,14 +1295,16 @@ lce_status fwd_bwd_impl(const void *H, const void *W, const int64_t *y, const fl
     return LCE_OK;
 }
 
+// (the largest logit over the temperature has to stay within fp32: logits up to 1.2e19)
+constexpr float POLICY_MIN_TEMPERATURE = 0x1p-64f;
+
 // Checks of the policy's vectors and numbers (advantages may be null with no rows).
 lce_status policy_check(int64_t N, const float *advantages, const float *old_logprobs, const float *ref_logprobs,
                         const float *weights, float clip_low, float clip_high, float beta, float temperature,
                         const float *logprobs) {
     if (N > 0 && (!advantages || !logprobs)) return LCE_ERR_INVALID_ARG;
     if (!(clip_low >= 0.f && clip_low <= 1.f) || !(clip_high >= 0.f && clip_high < INFINITY) ||
-        !(beta >= 0.f && beta < INFINITY) || !(temperature > 0.f && temperature < INFINITY) ||
-        !(1.f / temperature < INFINITY))
+        !(beta >= 0.f && beta < INFINITY) || !(temperature >= POLICY_MIN_TEMPERATURE && temperature < INFINITY))
         return LCE_ERR_INVALID_ARG;
     if (N > 0 && beta != 0.f && !ref_logprobs) return LCE_ERR_INVALID_ARG;
     const uintptr_t words = reinterpret_cast<uintptr_t>(advantages) | reinterpret_cast<uintptr_t>(old_logprobs) |

@@ -38,7 +38,7 @@ def policy_logits(L, Z=FAKE, dtype=0, ld=1000, y=FAKE, N=4, V=1000, red=0, dloss
 BAD_POLICY = [(dict(adv=None), INVALID), (dict(lo=-0.1), INVALID), (dict(lo=1.5), INVALID), (dict(lo=math.nan), INVALID),
               (dict(hi=-0.1), INVALID), (dict(hi=math.inf), INVALID), (dict(beta=-1.0), INVALID), (dict(beta=math.nan), INVALID),
               (dict(beta=0.1), INVALID), (dict(t=0.0), INVALID), (dict(t=-1.0), INVALID), (dict(t=math.inf), INVALID),
-              (dict(t=1e-45), INVALID), (dict(adv=FAKE + 2), ALIGN), (dict(old=FAKE + 1), ALIGN), (dict(ref=FAKE + 2), ALIGN),
+              (dict(t=1e-45), INVALID), (dict(t=5e-20), INVALID), (dict(adv=FAKE + 2), ALIGN), (dict(old=FAKE + 1), ALIGN), (dict(ref=FAKE + 2), ALIGN),
               (dict(w=FAKE + 3), ALIGN), (dict(lp=None), INVALID), (dict(lp=FAKE + 2), ALIGN)]
 
 
@@ -50,6 +50,27 @@ def test_policy_arguments(L, how, want):
     assert L.lce_policy_fwd_bwd(FAKE, FAKE, FAKE, *pol, None, 4, 64, 100, -100, 4, 0, 0, FAKE, h["lp"], FAKE, FAKE, FAKE,
                                 1 << 30, None) == want
     assert L.lce_policy_forward(FAKE, FAKE, FAKE, *pol, 4, 64, 100, -100, 4, 0, FAKE, h["lp"], FAKE, 1 << 30, None) == want
+
+
+def test_16_bit_weight_gradients(L):
+    # one contraction of a trained weight that is not added to (refused before the device is asked)
+    pol = tuple(POLICY.values())
+
+    def policy(N=4, chunk=4, flags=32):
+        return L.lce_policy_fwd_bwd(FAKE, FAKE, FAKE, *pol, None, N, 64, 100, -100, chunk, 0, flags, FAKE, FAKE, FAKE, FAKE, FAKE,
+                                    1 << 40, None)
+
+    def preference(N=4, chunk=4, flags=32):
+        return L.lce_preference_fwd_bwd(FAKE, FAKE, FAKE, FAKE, 1, None, 0.1, 0.0, 0, None, N, 64, 100, -100, chunk, 0, flags, FAKE,
+                                        FAKE, FAKE, FAKE, FAKE, 1 << 40, None)
+    for call in (policy, preference):
+        assert call(N=9) == call(N=5, flags=32 | 16) == call(flags=32 | 1) == call(flags=32 | 8) == UNSUPPORTED
+        assert call(flags=64) == INVALID
+    assert L.lce_fwd_bwd_opt(FAKE, FAKE, FAKE, None, 4, 64, 100, -100, 4, 0, 32, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 40,
+                             None) == INVALID
+    n = ctypes.c_size_t(0)
+    assert L.lce_workspace_size_opt(4, 64, 100, 4, 32, ctypes.byref(n)) == INVALID
+    assert L.lce_policy_workspace_size(4, 64, 100, 4, 32, 1, ctypes.byref(n)) == 0
 
 
 def test_policy_logits_arguments(L):
