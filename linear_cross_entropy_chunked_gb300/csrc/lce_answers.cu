@@ -2,7 +2,7 @@
 //
 //   * rows of given logits: log p of the row's label, the clipped policy loss with its KL term
 //     and the gradient (p - onehot) * scale in one pass over the logits (cluster kernel), or
-//     in two for rows beyond eight CTAs' registers (streaming kernel);
+//     in two for rows beyond eight CTAs' shared memory (streaming kernel);
 //   * pairs: log probabilities added up over each sequence, the loss of the paired log ratios,
 //     and the coefficient that each row's p - onehot gets;
 //   * the gradient of a preference over given logits, once those coefficients are known.
