@@ -193,6 +193,41 @@ def test_captured_steps(which):
         assert torch.equal(p, q)
 
 
+@pytest.mark.parametrize("n,v,chunk", [(600, 9, 1024), (600, 9, 128), (90, 3, 64), (300, 40, 128)])
+def test_labels_that_many_rows_have(n, v, chunk):
+    # lists of more rows than are gone through, rows of weight 0 among them (whose H holds anything where they do not count)
+    H, W, Z, y, a, old, _, w = head(n, 72, v, n + v, ignored=0.2)
+    w[::3] = 0.0
+    H[y < 0] = math.nan
+    args = [t.cuda() for t in (H, W, y, a, old)]
+    loss, logprobs, dH, dW = lce.policy_fwd_bwd(*args, weights=w.cuda(), chunk=chunk)
+    o = ao.policy(np.nan_to_num(Z), y.numpy(), a.numpy(), old.numpy(), weights=w.numpy())
+    Hz = torch.nan_to_num(H.double())
+    lb = logp_bound(np.nan_to_num(Z), 1.0, v) + cut_sums(Hz, W)
+    check_gradients(dH, dW, Hz, W, with_coefs(o, y, o["mass"]), lb)
+    assert all(torch.equal(p, q) for p, q in zip(lce.policy_fwd_bwd(*args, weights=w.cuda(), chunk=chunk)[2:], (dH, dW)))
+
+
+@pytest.mark.parametrize("low_memory", [False, True])
+@pytest.mark.parametrize("n,chunk", [(300, 150), (301, 150), (300, 300), (301, 300), (64, 64), (65, 32), (1, 1)])
+def test_one_buffer_or_more(n, chunk, low_memory):
+    # the largest calls of one contraction, and the smallest of two
+    H, W, _, y, a, old, _, _ = head(n, 64, 701, n + chunk)
+    h, w = H.cuda().requires_grad_(), W.cuda().requires_grad_()
+    rest = [t.cuda() for t in (y, a, old)]
+    loss, _ = lce.linear_policy_loss(h, w, *rest, chunk=chunk, low_memory=low_memory)
+    loss.backward()
+    raw = lce.policy_fwd_bwd(H.cuda(), W.cuda(), *rest, chunk=chunk, low_memory=low_memory)
+    assert torch.equal(h.grad, raw[2]) and torch.equal(w.grad, raw[3].bfloat16())
+    if n < 2:
+        return
+    off = answers(n, 1, n).cuda()
+    h.grad = w.grad = None
+    lce.linear_preference_loss(h, w, rest[0], off, chunk=chunk, low_memory=low_memory)[0].backward()
+    raw = lce.preference_fwd_bwd(H.cuda(), W.cuda(), rest[0], off, chunk=chunk, low_memory=low_memory)
+    assert torch.equal(h.grad, raw[2]) and torch.equal(w.grad, raw[3].bfloat16())
+
+
 def test_two_threads_on_two_streams():
     H, W, _, y, a, old, _, _ = head(260, 64, 3001, 12)
     dev = [t.cuda() for t in (H, W, y, a, old)]
