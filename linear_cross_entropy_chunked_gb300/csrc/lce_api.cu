@@ -471,6 +471,7 @@ void base_params(const Ctx &c, GemmParams &p, long long row0, long long rows, in
     p.dloss_per_row = c.reduction == LCE_REDUCTION_NONE ? 1 : 0;
     p.mean = c.reduction == LCE_REDUCTION_MEAN ? 1 : 0;
     p.f16 = c.f16 ? 1 : 0;
+    p.answers = c.answers ? 1 : 0;
     p.inv_t = c.inv_t;
     p.rests = c.rests;
     p.Hc = reinterpret_cast<const uint4 *>(c.H + h_row(c, row0) * c.D);
@@ -805,7 +806,7 @@ void merge_params(const Ctx &c, long long row0, long long rows, float *lse, cons
     m.lse = lse;
     m.loss_rows = loss_rows;
     m.pol = c.pol;
-    m.zero_rows = c.answers ? 1 : 0;
+    m.answers = c.answers ? 1 : 0;
     m.counting = c.index ? c.hdr + HDR_NVALID : nullptr;
     m.index = c.pol.adv ? c.index : nullptr;   // (a preference's rows go by their place)
     m.loss_by_index = c.loss_by_index ? 1 : 0;
@@ -1722,6 +1723,7 @@ lce_status lce_policy_forward(const void *H, const void *W, const int64_t *y, co
     c.pol = policy_params(advantages, old_logprobs, ref_logprobs, weights, clip_low, clip_high, beta,
                           temperature, logprobs);
     c.inv_t = c.pol.inv_t;
+    c.answers = true;
     for (long long k = 0; k < c.L.nchunks; ++k) {
         LCE_TRY(bring_rows(c, k, false));
         LCE_TRY(run_logits(c, MODE_LSE, k * c.L.C, chunk_rows(c, k), static_cast<int>(k), nullptr, nullptr,

@@ -263,6 +263,7 @@ __device__ __forceinline__ void bulk_copy_to_smem(uint32_t dst, const void *src,
         : "memory");
 }
 
+template <bool ANSWERS>
 __device__ __forceinline__ void transpose_tile(const TransposeParams &p, int c0, int r0,
                                                __nv_bfloat16 *tile) {
     const int tid = threadIdx.x;
@@ -272,7 +273,7 @@ __device__ __forceinline__ void transpose_tile(const TransposeParams &p, int c0,
         const int rr = k >> 3, cb = (k & 7) * 8;
         const int r = r0 + rr, c = c0 + cb;
         uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (r < p.rows && c < p.cols && row_counts(p, r))
+        if (r < p.rows && c < p.cols && (!ANSWERS || row_counts(p, r)))
             u = *reinterpret_cast<const uint4 *>(p.src + static_cast<size_t>(r) * p.ld_src + c);
         uint32_t *dst = reinterpret_cast<uint32_t *>(tile + rr * TSTRIDE + cb);
         dst[0] = u.x;
@@ -307,6 +308,8 @@ constexpr unsigned long long PREP_WAIT_NS = 2000000000ull;       // bound of the
 // The segment of P' comes into shared memory by one bulk copy, issued first, so
 // it is in flight while the row's lse is formed; shared memory rather than
 // registers holds it, which lets 7 CTAs (224 KB of copies) share an SM.
+// ANSWERS: a loss on answers.
+template <bool ANSWERS>
 __global__ void __launch_bounds__(MERGE_THREADS) lce_prep_kernel(const PrepParams p) {
     extern __shared__ __align__(128) uint8_t prep_smem[];   // the segment, or a transpose tile
     __shared__ float s_red[MERGE_THREADS / 32];
@@ -318,7 +321,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_prep_kernel(const PrepParam
     const long long nrow_ctas = static_cast<long long>(m.rows) * p.segs;
     if (blockIdx.x >= nrow_ctas) {
         const int b = static_cast<int>(blockIdx.x - nrow_ctas);
-        transpose_tile(p.tp, (b % p.tt_x) * TT, (b / p.tt_x) * TT,
+        transpose_tile<ANSWERS>(p.tp, (b % p.tt_x) * TT, (b / p.tt_x) * TT,
                        reinterpret_cast<__nv_bfloat16 *>(prep_smem));
         return;
     }
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_prep_kernel(const PrepParam
     const int v0 = seg * PREP_VEC_PER_CTA;
     const int nv = min(PREP_VEC_PER_CTA, nvec - v0);      // > 0: segs covers nvec exactly
     uint4 *row = reinterpret_cast<uint4 *>(m.G + static_cast<size_t>(r) * p.ldg);
-    if (m.counting) {
+    if (ANSWERS && m.counting) {
         // behind the rows there are: zeros as far as a k block of the dW contraction may reach
         const int live = live_rows(m.counting, m.row0, m.rows);
         if (r >= live) {
@@ -351,22 +354,30 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_prep_kernel(const PrepParam
     const int grow = m.row0 + r;
     const long long yv = m.y[grow];
     const bool y_ok = yv != m.ignore_index && yv >= 0 && yv < m.V;
-    const int of = m.index ? m.index[grow] : grow;   // the row of the call
+    const int of = ANSWERS && m.index ? m.index[grow] : grow;   // the row of the call
     float scale = lce_store_scale(m.dloss, m.dloss_per_row, m.mean, m.hdr[HDR_NVALID], of, y_ok, m.f16);
-    const float logp = y_ok ? m.zy[r] - lse : 0.f;
-    float row_loss = y_ok ? lse - m.zy[r] : 0.f;
-    if (m.pol.adv && y_ok) {
-        const PolicyRow pr = lce_policy_row(m.pol, of, logp);
-        row_loss = pr.loss;
-        scale *= -pr.slope * m.pol.inv_t;
+    bool zero = false;
+    float *rest = nullptr;
+    if constexpr (ANSWERS) {
+        const float logp = y_ok ? m.zy[r] - lse : 0.f;
+        float row_loss = y_ok ? lse - m.zy[r] : 0.f;
+        if (m.pol.adv && y_ok) {
+            const PolicyRow pr = lce_policy_row(m.pol, of, logp);
+            row_loss = pr.loss;
+            scale *= -pr.slope * m.pol.inv_t;
+        }
+        if (seg == 0 && threadIdx.x == 0) {
+            if (m.lse) m.lse[grow] = lse;
+            if (m.pol.logp) m.pol.logp[of] = logp;
+            m.loss_rows[m.loss_by_index ? of : grow] = row_loss;
+        }
+        zero = scale == 0.f;   // (whatever P' holds)
+        if ((zero || !y_ok) && seg == 0 && threadIdx.x == 0) m.rest[r] = 0.f;
+        rest = zero ? nullptr : m.rest + r;
+    } else if (seg == 0 && threadIdx.x == 0) {
+        m.lse[grow] = lse;
+        m.loss_rows[grow] = y_ok ? lse - m.zy[r] : 0.f;
     }
-    if (seg == 0 && threadIdx.x == 0) {
-        if (m.lse) m.lse[grow] = lse;
-        if (m.pol.logp) m.pol.logp[of] = logp;
-        m.loss_rows[m.loss_by_index ? of : grow] = row_loss;
-    }
-    const bool zero = m.zero_rows && scale == 0.f;
-    if (m.rest && (zero || !y_ok) && seg == 0 && threadIdx.x == 0) m.rest[r] = 0.f;
     const float lse2 = lse * LOG2E_F;
     const int ycol = y_ok ? static_cast<int>(yv) : -1;
     // the factor exp(m_p - lse) * s of each 128-column slab of the segment, once (a
@@ -401,11 +412,11 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_prep_kernel(const PrepParam
             x.y *= f;
             if (c + 2 * q == ycol) {
                 x.x -= scale;
-                if (m.rest && !zero) m.rest[r] = lce_rest(x.x);
+                if (ANSWERS && rest) *rest = lce_rest(x.x);
             }
             if (c + 2 * q + 1 == ycol) {
                 x.y -= scale;
-                if (m.rest && !zero) m.rest[r] = lce_rest(x.y);
+                if (ANSWERS && rest) *rest = lce_rest(x.y);
             }
             if (m.f16) {
                 __half2 h = __floats2half2_rn(x.x, x.y);
@@ -415,7 +426,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_prep_kernel(const PrepParam
                 wv[q] = *reinterpret_cast<uint32_t *>(&h);
             }
         }
-        if (zero) u = make_uint4(0u, 0u, 0u, 0u);
+        if (ANSWERS && zero) u = make_uint4(0u, 0u, 0u, 0u);
         row[v0 + v] = u;
     }
 }
@@ -724,7 +735,8 @@ cudaError_t launch_prep(const PrepParams &p, cudaStream_t s) {
     const long long grid = row_ctas + tt;
     if (grid <= 0) return cudaSuccess;
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-    lce_prep_kernel<<<static_cast<unsigned>(grid), MERGE_THREADS, PREP_SEG_BYTES, s>>>(p);
+    (p.m.answers ? lce_prep_kernel<true> : lce_prep_kernel<false>)<<<static_cast<unsigned>(grid), MERGE_THREADS,
+                                                                     PREP_SEG_BYTES, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -98,9 +98,9 @@ enum : int { TILE_MAIN = 0, TILE_DW = 1 };
 struct Live {
     int rows, m_blocks0, k_blocks1, total;
 };
-template <int CL> __device__ __forceinline__ Live live_part(const GemmParams &p) {
+template <int CL, bool ANSWERS> __device__ __forceinline__ Live live_part(const GemmParams &p) {
     Live lv{p.rows, p.m_blocks0, p.k_blocks1, p.total_tiles};
-    if (p.counting) {
+    if (ANSWERS && p.counting) {
         const int n = *p.counting;
         lv.rows = max(0, min(p.rows, n - p.row0));
         lv.m_blocks0 = min(p.m_blocks0, (lv.rows + BM - 1) / BM);
@@ -246,14 +246,14 @@ struct WarpStager {
     }
 };
 
-template <int MODE>
+template <int MODE, bool ANSWERS>
 __device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Live &lv, const Tile &tl,
                                                 uint32_t taddr, int quarter, int half,
                                                 const WarpStager &st) {
     const int r = tl.m0 + quarter * 32 + st.lane;  // row within the chunk
     const int box_y = tl.m0 + quarter * 32;
     // warp-uniform: any row of the box exists (G: up to whole k blocks of the dW contraction, as zeros)
-    const bool box_rows = box_y < (MODE == MODE_G && p.counting ? (lv.rows + BK - 1) / BK * BK : lv.rows);
+    const bool box_rows = box_y < (ANSWERS && MODE == MODE_G && p.counting ? (lv.rows + BK - 1) / BK * BK : lv.rows);
     const bool row_ok = r < lv.rows;
     const int col0 = tl.n0 + half * 128;        // first vocabulary column of this half
     const int ncols = min(128, p.V - col0);     // valid columns (may be <= 0); same for the half
@@ -261,7 +261,8 @@ __device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Live 
     if (row_ok) yv = p.y[p.row0 + r];
     const bool y_ok = row_ok && yv != p.ignore_index && yv >= 0 && yv < p.V;
     const int yl = y_ok ? static_cast<int>(yv - col0) : -1;   // local target column
-    const float k2 = LOG2E * p.inv_t;           // logits to exponents of 2
+    const float inv_t = ANSWERS ? p.inv_t : 1.f;
+    const float k2 = LOG2E * inv_t;             // logits to exponents of 2
 
     if constexpr (MODE == MODE_G) {
         if (ncols <= 0 || !box_rows) return;
@@ -271,9 +272,9 @@ __device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Live 
                                     p.row0 + r, y_ok, p.f16);
             lse2 = p.lse[p.row0 + r] * LOG2E;
         }
-        if (p.rests.rest && row_ok && !y_ok && col0 == 0) p.rests.rest[r] = 0.f;
+        if (ANSWERS && p.rests.rest && row_ok && !y_ok && col0 == 0) p.rests.rest[r] = 0.f;
         // a row that adds nothing is zeros, whatever its logits are
-        const int rcols = scale != 0.f ? ncols : 0;
+        const int rcols = !ANSWERS || scale != 0.f ? ncols : 0;
         float gy = 0.f;   // the label's entry
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -287,7 +288,7 @@ __device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Live 
                 float g = (cj < rcols) ? ex2(fmaf(v[j], k2, -lse2)) * scale : 0.f;
                 if (cj == yl) {
                     g -= scale;
-                    gy = g;
+                    if (ANSWERS) gy = g;
                 }
                 v[j] = g;
             }
@@ -295,7 +296,7 @@ __device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Live 
             st.put_h16((c & 1) * 4, v, p.f16);
             if (c & 1) st.issue(&p.tmS0, col0 + (c >> 1) * 64, box_y);
         }
-        if (p.rests.rest && yl >= 0 && yl < ncols) p.rests.rest[r] = lce_rest(gy);
+        if (ANSWERS && p.rests.rest && yl >= 0 && yl < ncols) p.rests.rest[r] = lce_rest(gy);
     } else {
         // pass 1: slab max (and the target logit when it falls in this slab)
         float m = -INFINITY, zt = 0.f;
@@ -332,8 +333,8 @@ __device__ __forceinline__ void epilogue_logits(const GemmParams &p, const Live 
             }
         }
         if (row_ok && ncols > 0) {
-            p.parts[static_cast<size_t>(r) * p.nparts + col0 / PART_COLS] = make_float2(m * p.inv_t, s);
-            if (yl >= 0 && yl < 128) p.zy[r] = zt * p.inv_t;
+            p.parts[static_cast<size_t>(r) * p.nparts + col0 / PART_COLS] = make_float2(m * inv_t, s);
+            if (yl >= 0 && yl < 128) p.zy[r] = zt * inv_t;
         }
     }
 }
@@ -356,6 +357,7 @@ __device__ __forceinline__ void add_rest(float *v, float e, const uint4 *row, in
 // Gradient tiles: dH (bf16 / fp16, or fp32 when dh_fp32) or dW (fp32, stored by
 // a call's first dW contraction, reduce-added into dW by the later ones). out_scale: the factor
 // fp16 calls apply here instead of in G (1 for bf16).
+template <bool ANSWERS>
 __device__ __forceinline__ void epilogue_grad(const GemmParams &p, const Live &lv, const Tile &tl, uint32_t taddr,
                                               int half, const HalfStager &st, float out_scale) {
     const int col0 = tl.n0 + half * 128;
@@ -366,7 +368,7 @@ __device__ __forceinline__ void epilogue_grad(const GemmParams &p, const Live &l
     // what rounding left of the label entries of G: this thread's row of dH has one (added in the first part of
     // the vocabulary; rows brought together get it on their way back), its row of dW those of the rows in its label's list
     int at = -1;
-    if (p.rests.rest) {
+    if (ANSWERS && p.rests.rest) {
         const int r = tl.m0 + st.row;
         if (tl.type == TILE_MAIN) {
             if (!p.counting && r < lv.rows && tl.srow == 0 && p.rests.rest[r] != 0.f) at = r;
@@ -382,12 +384,13 @@ __device__ __forceinline__ void epilogue_grad(const GemmParams &p, const Live &l
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] *= out_scale;
         }
-        for (int i = at; i >= 0; i = tl.type == TILE_MAIN ? -1 : p.rests.next[i]) {
-            const float e = p.rests.rest[i];
-            const uint4 *row = tl.type == TILE_MAIN ? p.W + p.y[p.row0 + i] * (p.D / 8) : p.Hc + static_cast<size_t>(i) * (p.D / 8);
-            if (e != 0.f) add_rest(v, e, row, col0 + c * 32, p.D);   // (a row whose scale is 0 holds anything)
-        }
-        if (tl.type == TILE_MAIN ? !p.dh_fp32 : p.dw_16) {
+        if constexpr (ANSWERS)
+            for (int i = at; i >= 0; i = tl.type == TILE_MAIN ? -1 : p.rests.next[i]) {
+                const float e = p.rests.rest[i];
+                const uint4 *row = tl.type == TILE_MAIN ? p.W + p.y[p.row0 + i] * (p.D / 8) : p.Hc + static_cast<size_t>(i) * (p.D / 8);
+                if (e != 0.f) add_rest(v, e, row, col0 + c * 32, p.D);   // (a row whose scale is 0 holds anything)
+            }
+        if (tl.type == TILE_MAIN ? !p.dh_fp32 : ANSWERS && p.dw_16) {
             if (col0 + (c >> 1) * 64 >= p.D) continue;
             if ((c & 1) == 0) st.acquire();
             st.put_h16((c & 1) * 4, v, p.f16);
@@ -436,7 +439,9 @@ __device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t a, uint
 // 64-deep k block. The leader also fetches the tiles and writes them into both
 // CTAs' schedule rings.
 
-template <int MODE, int CL>
+// ANSWERS: a loss on answers (temperature, rows that count brought together, remainders of the label entries, bf16
+// dW); without, the cross-entropy's kernels are as they would be alone (all of it at run time cost them 1.3 %).
+template <int MODE, int CL, bool ANSWERS>
 __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_constant__ GemmParams p) {
     using P = Pipe<CL, MODE == MODE_DH>;
     static_assert(MODE != MODE_DH || CL == 2, "wide dH tiles run on CTA pairs only");
@@ -510,7 +515,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
     if constexpr (CL == 2) cluster_sync_all();   // the peer's barriers exist from here on
     tc_fence_after();
     const uint32_t tmem_base = tmem_slot;
-    const Live lv = live_part<CL>(p);
+    const Live lv = live_part<CL, ANSWERS>(p);
 
     Abort ab;
     ab.flag_smem = &abort_flag;
@@ -607,8 +612,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
                     } else if constexpr (MODE == MODE_DH) {
                         // A = G rows (K-major); B = W, MN-major, two 256-column halves
                         // of which this CTA loads 128 columns each
-                        // (a second half that lies behind D is left out)
-                        const bool one = tl.n0 + BN >= p.D;
+                        // (ANSWERS: a second half that lies behind D is left out)
+                        const bool one = ANSWERS && tl.n0 + BN >= p.D;
                         if (leader) mbar_arrive_expect_tx(fb, 2 * (P::kStageBytes - (one ? 16384 : 0)));
                         const uint32_t lfb = map_to_rank(fb, 0);
                         tma_load_2d_pair(sA, &p.tmA0, lfb, kx, tl.m0);
@@ -706,7 +711,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
                         if constexpr (CL == 2) umma_bf16_pair(d_tmem, a, b, idesc, accumulate);
                         else umma_bf16(d_tmem, a, b, idesc, accumulate);
                         // the second 256-column half: same A, B 16 KB further on
-                        if (MODE == MODE_DH && tl.n0 + BN < p.D)
+                        if (MODE == MODE_DH && (!ANSWERS || tl.n0 + BN < p.D))
                             umma_bf16_pair(d_tmem + BN, a, b + static_cast<uint64_t>(16384u >> 4), idesc,
                                            accumulate);
                     }
@@ -770,7 +775,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
                                    static_cast<uint32_t>(acc * BN + half * 128);
             if constexpr (MODE == MODE_DH) {
                 // both accumulators of the wide tile: columns n0 .. n0 + 255, then + 256
-                epilogue_grad(p, lv, tl, taddr, half, st, out_scale);
+                epilogue_grad<ANSWERS>(p, lv, tl, taddr, half, st, out_scale);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) release_on_leader(&tempty_bar[0]);
@@ -779,7 +784,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
                 tc_fence_after();
                 Tile tl2 = tl;
                 tl2.n0 += BN;
-                epilogue_grad(p, lv, tl2, taddr + BN, half, st, out_scale);
+                epilogue_grad<ANSWERS>(p, lv, tl2, taddr + BN, half, st, out_scale);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) release_on_leader(&tempty_bar[1]);
@@ -787,9 +792,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
                 continue;
             }
             if constexpr (MODE != MODE_BWD && MODE != MODE_DH) {
-                epilogue_logits<MODE>(p, lv, tl, taddr, quarter, half, wst);
+                epilogue_logits<MODE, ANSWERS>(p, lv, tl, taddr, quarter, half, wst);
             } else {
-                epilogue_grad(p, lv, tl, taddr, half, st, out_scale);
+                epilogue_grad<ANSWERS>(p, lv, tl, taddr, half, st, out_scale);
             }
             tc_fence_before();
             __syncwarp();
@@ -820,8 +825,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) lce_gemm_kernel(const __grid_
 
 template <int MODE, int CL>
 static cudaError_t set_attr() {
-    return cudaFuncSetAttribute(lce_gemm_kernel<MODE, CL>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, GEMM_SMEM_BYTES);
+    const cudaError_t e = cudaFuncSetAttribute(lce_gemm_kernel<MODE, CL, false>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, GEMM_SMEM_BYTES);
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(lce_gemm_kernel<MODE, CL, true>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, GEMM_SMEM_BYTES);
 }
 
 cudaError_t gemm_set_attributes() {
@@ -851,7 +859,8 @@ static cudaError_t launch_one(const GemmParams &p, int grid, cudaStream_t s) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lce_gemm_kernel<MODE, CL>, p);
+    return p.answers ? cudaLaunchKernelEx(&cfg, lce_gemm_kernel<MODE, CL, true>, p)
+                     : cudaLaunchKernelEx(&cfg, lce_gemm_kernel<MODE, CL, false>, p);
 }
 
 cudaError_t launch_gemm(int mode, int cluster, const GemmParams &p, int grid, cudaStream_t s) {
@@ -891,7 +900,7 @@ cudaError_t gemm_max_pairs(int *pairs) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaOccupancyMaxActiveClusters(pairs, lce_gemm_kernel<MODE_BWD, 2>, &cfg);
+    return cudaOccupancyMaxActiveClusters(pairs, lce_gemm_kernel<MODE_BWD, 2, false>, &cfg);
 }
 
 }  // namespace lce

@@ -220,6 +220,7 @@ struct GemmParams {
     // offset s * split_rows of the tmS0 map (k_splits <= 1: one part, no offset)
     int k_splits, kb_per_split, split_rows;
     int f16;               // 1: fp16 operands (H, W, G) and fp16 P' / G / dH stores
+    int answers;           // 1: a loss on answers; what follows up to the wait's limit is read then only
     float inv_t;           // the logits are multiplied by it in the logits epilogues (1 / temperature)
     // Rows that count brought together (null: all `rows` are there): their number on the device. Tiles and
     // contractions then end with the rows there are; dw_row0 and dw_rows: the rows of the dW contraction.
@@ -247,7 +248,7 @@ struct MergeParams {
     float *lse;            // global [N]; null: not written
     float *loss_rows;      // global [N] (the caller's loss vector for reduction none)
     PolicyParams pol;      // pol.adv: the policy loss in place of the cross-entropy
-    int zero_rows;         // 1: rows of G whose scale is 0 become zeros whatever P' holds
+    int answers;           // 1: a loss on answers
     // rows that count brought together: their number (null: all are there), and which row of the call each
     // is (null: the same), by which the policy's vectors, its outputs and a per-row dloss go
     const int *counting;
