@@ -131,8 +131,12 @@ struct Layout {
 // Losses on answers, where some of the rows count and only the device knows how many: into parts for two
 // waves. 1954 of 2777 rows x 50257 x 1600, all in one chunk: 617 us for the gradient in one part (32 of its 44 tiles there,
 // on 76 pairs), 243 in four; 487 of 700 rows: 155 -> 97; 1071 of 1531, where one wave is nearly full: 158 -> 154. (Three
-// waves: 252, 86 and 165.)
+// waves: 252, 86 and 165.) With W trained too where a chunk has more than DH_BESIDE_TILES: the tiles are one long wave then that
+// leaves dW little beside it and gets out of step, which reads W and G again (1843 of 2048 rows x 128256 x 4096, a whole pass:
+// 3800 to 5200 us, among other work 3990 to 4430, in three parts 4030 and 4040 to 4170; 1440 rows: 3130 and 3140 to 3260, in three
+// 3025 and 3120 to 3200). 32 tiles are what dW goes well beside (8000 rows x 32000 x 2048, gradients: 1340 us, in four to six parts 1400).
 constexpr int DH_ALONE_PAIRS = 76;
+constexpr int DH_BESIDE_TILES = 40;
 constexpr int DH_ANSWERS_MAX_SPLITS = 16;
 
 int dh_splits_for(long long rows, long long D, long long V, bool frozen_w = false, bool answers = false) {
@@ -140,7 +144,7 @@ int dh_splits_for(long long rows, long long D, long long V, bool frozen_w = fals
     const long long tiles = cdiv(cdiv(rows, BM), 2) * cdiv(D, BN_WIDE);
     long long sp = frozen_w ? DH_ALONE_PAIRS / tiles : cdiv(DH_SPLIT_TILES, tiles);
     if (sp > DH_MAX_SPLITS) sp = DH_MAX_SPLITS;
-    if (answers && frozen_w) {
+    if (answers && (frozen_w || tiles > DH_BESIDE_TILES)) {
         sp = cdiv(2 * DH_ALONE_PAIRS, tiles);
         if (sp > DH_ANSWERS_MAX_SPLITS) sp = DH_ANSWERS_MAX_SPLITS;
     }
