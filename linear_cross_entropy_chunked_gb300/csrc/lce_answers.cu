@@ -190,20 +190,26 @@ template <typename T> struct RowSplit {
 
 // exp((z - m) / T) as 2^(z k2 + nm) * c for k2 = log2(e) / T: one fused operation for each logit. nm is
 // -m k2 as fp32 has it and c takes back what that rounding lost, so the result is as exact as
-// the distance from m is. Where m k2 would leave fp32 (a row of the type's lowest value)
-// `far` is set, and the distance is to be formed first.
+// the distance from m is. That loss is up to half a unit of nm: an eighth below 2^22, but beyond what a power of two
+// can hold (c 0, the other factor infinite) for masks of -1e10 or a temperature of 1e-9. From 2^22 on `far` is
+// set, and the distance is formed first: one operation more.
+constexpr float EXP_FUSED_BELOW = 0x1p22f;
 struct ExpFrom {
     float m, k2, nm, c;
     bool far;
     __device__ ExpFrom(float m_, float k2_) : m(m_ == -INFINITY ? 0.f : m_), k2(k2_) {
         nm = -(m * k2);
-        far = !(fabsf(nm) < 1e38f);
+        far = !(fabsf(nm) < EXP_FUSED_BELOW);
         c = far ? 1.f : exp2_fast(-fmaf(m, k2, nm));
         if (far) nm = 0.f;
     }
     __device__ float operator()(float z) const { return exp2_fast(far ? (z - m) * k2 : fmaf(z, k2, nm)); }
     __device__ float2 pair(float2 z) const {
         const float2 a = __ffma2_rn(z, make_float2(k2, k2), make_float2(nm, nm));
+        return make_float2(exp2_fast(a.x), exp2_fast(a.y));
+    }
+    __device__ float2 far_pair(float2 z) const {
+        const float2 a = __fmul2_rn(__fadd2_rn(z, make_float2(-m, -m)), make_float2(k2, k2));
         return make_float2(exp2_fast(a.x), exp2_fast(a.y));
     }
 };
@@ -487,11 +493,13 @@ __global__ void __launch_bounds__(ANS_THREADS + 64, 1)
                     const ExpFrom e(res.M, k2);
                     const float f = res.f * e.c;
                     const float2 f2 = make_float2(f, f);
-                    auto one = [&](const uint4 &u) {
+                    auto one = [&](const uint4 &u, auto far) {
                         uint4 out;
 #pragma unroll
-                        for (int q = 0; q < CV::PAIRS; ++q)
-                            CV::set_pair(out, q, __fmul2_rn(e.pair(CV::pair(u, q)), f2));
+                        for (int q = 0; q < CV::PAIRS; ++q) {
+                            const float2 z = CV::pair(u, q);
+                            CV::set_pair(out, q, __fmul2_rn(decltype(far)::value ? e.far_pair(z) : e.pair(z), f2));
+                        }
                         return out;
                     };
                     if (!e.far) {
@@ -499,16 +507,12 @@ __global__ void __launch_bounds__(ANS_THREADS + 64, 1)
                         for (int v = t; v < n; v += 2 * ANS_THREADS) {
                             const bool two = v + ANS_THREADS < n;
                             const uint4 u0 = sg[v], u1 = two ? sg[v + ANS_THREADS] : u0;
-                            dvec[v] = one(u0);
-                            if (two) dvec[v + ANS_THREADS] = one(u1);
+                            dvec[v] = one(u0, std::false_type());
+                            if (two) dvec[v + ANS_THREADS] = one(u1, std::false_type());
                         }
                     } else {
-                        const T *z = reinterpret_cast<const T *>(sg);
 #pragma unroll 1
-                        for (int v = t; v < n; v += ANS_THREADS)
-#pragma unroll 1
-                            for (int i = v * EL; i < (v + 1) * EL; ++i)
-                                reinterpret_cast<T *>(dvec)[i] = CV::from(e(static_cast<float>(z[i])) * f);
+                        for (int v = t; v < n; v += ANS_THREADS) dvec[v] = one(sg[v], std::true_type());
                     }
                     const long long si = rank == 0 && w == 0 ? rs.scalar(t, p.V) : -1;
                     if (si >= 0) drow[si] = CV::from(e(static_cast<float>(rs.row[si])) * f);
@@ -571,11 +575,12 @@ __global__ void __launch_bounds__(ANS_THREADS + 64, 1)
                         }
                     a0 = __fadd2_rn(a0, a1);
                 } else {
-                    const T *z = reinterpret_cast<const T *>(sg);
 #pragma unroll 1
-                    for (int i = v; i < n && i < v + 4 * ANS_THREADS; i += ANS_THREADS)
-#pragma unroll 1
-                        for (int j = i * EL; j < (i + 1) * EL; ++j) a0.x += e(static_cast<float>(z[j]));
+                    for (int i = v; i < n && i < v + 4 * ANS_THREADS; i += ANS_THREADS) {
+                        const uint4 w4 = sg[i];
+#pragma unroll
+                        for (int q = 0; q < CV::PAIRS; ++q) a0 = __fadd2_rn(a0, e.far_pair(CV::pair(w4, q)));
+                    }
                 }
                 // (without a logit so far every exponential is 0, or a NaN)
                 s = s * (m == mv ? 1.f : exp2_fast((m - mv) * k2)) + (a0.x + a0.y) * e.c;
@@ -659,28 +664,28 @@ __device__ __forceinline__ void write_gradient(const RowSplit<T> &rs, T *drow, l
     const bool mine = vy >= 0 ? vy >= t && vy < rs.nvec && (vy - t) % nt == 0
                               : t < extra && rs.scalar(static_cast<int>(t), V) == yv;
     const float zy = mine ? static_cast<float>(rs.row[yv]) : 0.f;
-    auto one = [&](const uint4 &u) {
+    auto one = [&](const uint4 &u, auto far) {
         uint4 out;
 #pragma unroll
-        for (int q = 0; q < CV::PAIRS; ++q) CV::set_pair(out, q, __fmul2_rn(e.pair(CV::pair(u, q)), f2));
+        for (int q = 0; q < CV::PAIRS; ++q) {
+            const float2 z = CV::pair(u, q);
+            CV::set_pair(out, q, __fmul2_rn(decltype(far)::value ? e.far_pair(z) : e.pair(z), f2));
+        }
         return out;
     };
     long long v = t;
     if (e.far) {
 #pragma unroll 1
-        for (; v < rs.nvec; v += nt)
-#pragma unroll 1
-            for (int j = 0; j < EL; ++j)
-                drow[rs.head + v * EL + j] = CV::from(e(static_cast<float>(rs.row[rs.head + v * EL + j])) * f);
+        for (; v < rs.nvec; v += nt) dst[v] = one(src[v], std::true_type());
     }
     for (; v + 3 * nt < rs.nvec; v += 4 * nt) {
         uint4 u[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) u[j] = src[v + j * nt];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) dst[v + j * nt] = one(u[j]);
+        for (int j = 0; j < 4; ++j) dst[v + j * nt] = one(u[j], std::false_type());
     }
-    for (; v < rs.nvec; v += nt) dst[v] = one(src[v]);
+    for (; v < rs.nvec; v += nt) dst[v] = one(src[v], std::false_type());
     if (t < extra) {
         const long long i = rs.scalar(static_cast<int>(t), V);
         drow[i] = CV::from(e(static_cast<float>(rs.row[i])) * f);
