@@ -254,7 +254,8 @@ lce_status lce_ce_logits(const void *Z, int z_dtype, int64_t ld, const int64_t *
  * overflows. Rows with y = ignore_index (or outside [0, V), which flags LCE_ERR_LABEL_RANGE) do
  * not count: logprobs 0, loss 0, gradient 0, whatever the row holds (infinities and NaN too).
  * logprobs [N]: logp, the old_logprobs of later steps. 0 <= clip_low <= 1; clip_high,
- * beta >= 0; temperature >= 2^-64. dloss, reduction, ignore_index as above; with reduction NONE loss is
+ * beta >= 0; temperature >= 2^-64 (the softmax is formed from distances between logits, at any of them; over the
+ * head the logits are the tensor cores' fp32 sums, and log p is off by 1 / temperature times what they are). dloss, reduction, ignore_index as above; with reduction NONE loss is
  * loss_i [N] and dloss [N] or NULL.
  *
  * lce_policy_fwd_bwd: over the head, as lce_fwd_bwd_opt (6 N D V flops, chunk by chunk, the

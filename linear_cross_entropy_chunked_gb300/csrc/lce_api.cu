@@ -792,6 +792,7 @@ void merge_params(const Ctx &c, long long row0, long long rows, float *lse, cons
                   float *loss_rows, MergeParams &m) {
     m.parts = c.parts;
     m.nparts = c.L.nparts;
+    m.inv_t = c.inv_t;
     m.zy = c.zy;
     m.zx = c.coef ? nullptr : c.zx;   // (with the coefficients the sequences have been added up)
     m.fix = c.fix;

@@ -120,9 +120,11 @@ constexpr int MERGE_THREADS = 256;
 // lse of one chunk row from its (max, sumexp) slab partials, by a CTA of
 // MERGE_THREADS threads: M = the maximum of the slab maxima, lse = M + log sum_p
 // s_p exp(m_p - M). The order of every sum is fixed, so each CTA that computes a
-// row's lse gets the same bits. Returns it in every thread.
-__device__ __forceinline__ float row_lse(const float2 *parts, int nparts, float *s_red,
-                                         float *s_bcast) {
+// row's lse gets the same bits. Returns M and lse in every thread; ANSWERS: M and log sum_p
+// s_p exp((m_p - M) / T) alone, distances before the factor k2 = log2(e) / T (lse = M / T + that, which fp32
+// would not hold at small temperatures), with what the slabs' bases are short of m_p k2 taken back.
+template <bool ANSWERS>
+__device__ __forceinline__ float2 row_lse(const float2 *parts, int nparts, float k2, float *s_red, float *s_bcast) {
     const int t = threadIdx.x, w = t >> 5, l = t & 31;
     float m = -INFINITY;
     for (int i = t; i < nparts; i += MERGE_THREADS) m = fmaxf(m, parts[i].x);
@@ -140,7 +142,7 @@ __device__ __forceinline__ float row_lse(const float2 *parts, int nparts, float 
     float s = 0.f;
     for (int i = t; i < nparts; i += MERGE_THREADS) {
         const float2 q = parts[i];
-        s += q.y * exp2f(fmaf(q.x, LOG2E_F, -M2));
+        s += q.y * exp2f(ANSWERS ? fmaf(q.x - M, k2, -lce_base_rest(q.x, k2)) : fmaf(q.x, LOG2E_F, -M2));
     }
     s = warp_sum(s);
     __syncthreads();
@@ -149,10 +151,10 @@ __device__ __forceinline__ float row_lse(const float2 *parts, int nparts, float 
     if (w == 0) {
         s = (l < MERGE_THREADS / 32) ? s_red[l] : 0.f;
         s = warp_sum(s);
-        if (l == 0) *s_bcast = M + logf(s);
+        if (l == 0) *s_bcast = ANSWERS ? logf(s) : M + logf(s);
     }
     __syncthreads();
-    return *s_bcast;
+    return make_float2(M, *s_bcast);
 }
 
 // What the log probability moves by if the label's logit alone is put right by d = zx - zy: to first order
@@ -163,6 +165,7 @@ __device__ __forceinline__ float2 label_fix(const MergeParams &m, int r, float l
 }
 
 // Forward: one CTA per chunk row, lse_i from the slab partials and the row's loss.
+template <bool ANSWERS>
 __global__ void __launch_bounds__(MERGE_THREADS) lce_merge_kernel(const MergeParams p) {
     __shared__ float s_red[MERGE_THREADS / 32];
     __shared__ float s_bcast;
@@ -170,7 +173,8 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_merge_kernel(const MergePar
     const int t = threadIdx.x;
     if (r >= live_rows(p.counting, p.row0, p.rows)) return;
     const float2 *parts = p.parts + static_cast<size_t>(r) * p.nparts;
-    const float lse = row_lse(parts, p.nparts, s_red, &s_bcast);
+    const float2 ml = row_lse<ANSWERS>(parts, p.nparts, LOG2E_F * p.inv_t, s_red, &s_bcast);
+    const float lse = ANSWERS ? fmaf(ml.x, p.inv_t, ml.y) : ml.y;
 
     const int grow = p.row0 + r;
     const long long yv = p.y[grow];
@@ -178,11 +182,11 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_merge_kernel(const MergePar
     if (t == 0) {
         const int of = p.index ? p.index[grow] : grow;   // the row of the call
         if (p.lse) p.lse[grow] = lse;
-        const float logp = y_ok ? p.zy[r] - lse : 0.f;
+        const float logp = !y_ok ? 0.f : ANSWERS ? (p.zy[r] - ml.x) * p.inv_t - ml.y : p.zy[r] - lse;
         if (p.zx) p.fix[grow] = y_ok ? label_fix(p, r, logp) : make_float2(0.f, 0.f);
         if (p.pol.logp) p.pol.logp[of] = logp;
         p.loss_rows[p.loss_by_index ? of : grow] =
-            !y_ok ? 0.f : p.pol.adv ? lce_policy_row(p.pol, of, logp).loss : lse - p.zy[r];
+            !y_ok ? 0.f : p.pol.adv ? lce_policy_row(p.pol, of, logp).loss : ANSWERS ? -logp : lse - p.zy[r];
     }
 }
 
@@ -350,7 +354,9 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_prep_kernel(const PrepParam
     }
     // (row_lse's block barriers also order the barrier's initialisation before the waits)
     const float2 *parts = m.parts + static_cast<size_t>(r) * m.nparts;
-    const float lse = row_lse(parts, m.nparts, s_red, &s_bcast);
+    const float k2 = LOG2E_F * m.inv_t;
+    const float2 ml = row_lse<ANSWERS>(parts, m.nparts, k2, s_red, &s_bcast);
+    const float lse = ANSWERS ? fmaf(ml.x, m.inv_t, ml.y) : ml.y;
     const int grow = m.row0 + r;
     const long long yv = m.y[grow];
     const bool y_ok = yv != m.ignore_index && yv >= 0 && yv < m.V;
@@ -359,8 +365,8 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_prep_kernel(const PrepParam
     bool zero = false;
     float *rest = nullptr;
     if constexpr (ANSWERS) {
-        const float logp = y_ok ? m.zy[r] - lse : 0.f;
-        float row_loss = y_ok ? lse - m.zy[r] : 0.f;
+        const float logp = y_ok ? (m.zy[r] - ml.x) * m.inv_t - ml.y : 0.f;
+        float row_loss = y_ok ? -logp : 0.f;
         if (m.pol.adv && y_ok) {
             const PolicyRow pr = lce_policy_row(m.pol, of, logp);
             row_loss = pr.loss;
@@ -378,16 +384,18 @@ __global__ void __launch_bounds__(MERGE_THREADS) lce_prep_kernel(const PrepParam
         m.lse[grow] = lse;
         m.loss_rows[grow] = y_ok ? lse - m.zy[r] : 0.f;
     }
-    const float lse2 = lse * LOG2E_F;
+    const float lse2 = (ANSWERS ? ml.y : lse) * LOG2E_F;
     const int ycol = y_ok ? static_cast<int>(yv) : -1;
     // the factor exp(m_p - lse) * s of each 128-column slab of the segment, once (a
     // segment starts on a slab boundary: PREP_VEC_PER_CTA * 8 is a multiple of 128)
     const int slab0 = (v0 * 8) / PART_COLS;
     const int nslab = (nv * 8 + PART_COLS - 1) / PART_COLS;
-    if (threadIdx.x < nslab)
-        s_fac[threadIdx.x] = scale != 0.f
-                                 ? exp2f(fmaf(parts[slab0 + threadIdx.x].x, LOG2E_F, -lse2)) * scale
-                                 : 0.f;
+    if (threadIdx.x < nslab) {
+        const float mp = parts[slab0 + threadIdx.x].x;
+        s_fac[threadIdx.x] = scale != 0.f ? exp2f(ANSWERS ? fmaf(mp - ml.x, k2, -lse2 - lce_base_rest(mp, k2))
+                                                          : fmaf(mp, LOG2E_F, -lse2)) * scale
+                                          : 0.f;
+    }
     __syncthreads();
     const Abort ab{&s_abort, const_cast<int *>(m.hdr), PREP_WAIT_NS};
     if (!mbar_wait(&seg_bar, 0, ab)) {
@@ -716,7 +724,7 @@ cudaError_t launch_set_nvalid(const long long *n_total, int *hdr, cudaStream_t s
 
 cudaError_t launch_merge(const MergeParams &p, cudaStream_t s) {
     if (p.rows <= 0) return cudaSuccess;
-    lce_merge_kernel<<<p.rows, MERGE_THREADS, 0, s>>>(p);
+    (p.answers ? lce_merge_kernel<true> : lce_merge_kernel<false>)<<<p.rows, MERGE_THREADS, 0, s>>>(p);
     return cudaGetLastError();
 }
 

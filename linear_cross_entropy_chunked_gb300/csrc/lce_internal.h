@@ -167,6 +167,16 @@ __device__ __forceinline__ float lce_rest(float g) {
     return fabsf(e) < INFINITY ? e : 0.f;
 }
 
+// Losses on answers at a temperature T: P' and the sum of a slab of 128 logits are relative to the slab's largest
+// logit m, as powers of two to z k2 - m k2, k2 = log2(e) / T, with m k2 as fp32 rounds it: one fused operation a
+// logit. That rounding is half a unit of m k2, up to an eighth below 2^22; from there on (T = 1e-6) the distance z - m is formed first.
+// The slab's maximum is kept as it is, and whoever merges slabs subtracts what their base was short of m k2:
+constexpr float BASE_ROUNDED_BELOW = 0x1p22f;
+__device__ __forceinline__ float lce_base_rest(float m, float k2) {
+    const float base = m * k2;
+    return fabsf(base) < BASE_ROUNDED_BELOW ? fmaf(m, k2, -base) : 0.f;
+}
+
 // Workspace header (int32 words).
 enum : int {
     HDR_FLAG = 0,       // bit 0: label out of range, bit 1: pipeline wait timed out
@@ -221,7 +231,7 @@ struct GemmParams {
     int k_splits, kb_per_split, split_rows;
     int f16;               // 1: fp16 operands (H, W, G) and fp16 P' / G / dH stores
     int answers;           // 1: a loss on answers; what follows up to the wait's limit is read then only
-    float inv_t;           // the logits are multiplied by it in the logits epilogues (1 / temperature)
+    float inv_t;           // 1 / temperature: the logits epilogues form exp((z - m) inv_t)
     // Rows that count brought together (null: all `rows` are there): their number on the device. Tiles and
     // contractions then end with the rows there are; dw_row0 and dw_rows: the rows of the dW contraction.
     const int *counting;
@@ -232,6 +242,7 @@ struct GemmParams {
 struct MergeParams {
     const float2 *parts;   // [rows][nparts] (max, sumexp) per 128-column slab
     int nparts;
+    float inv_t;           // losses on answers: 1 / temperature (maxima and zy are logits, sums those of exp((z - m) / T))
     const float *zy;
     const float *zx;       // null, or [rows]: the label's logit as an fp32 dot product of its own (zy: the tensor cores'),
     float2 *fix;           // for which [N] gets what the row's log probability moves by with it: (1 - p) (zx - zy, 1)

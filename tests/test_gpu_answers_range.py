@@ -8,7 +8,7 @@ import torch
 
 import linear_cross_entropy_chunked_gb300 as lce
 from oracle import answers_oracle as ao
-from tests.test_gpu_policy import HALF, TINY, cpu64, rows_like
+from tests.test_gpu_policy import HALF, TINY, check_gradients, cpu64, rows_like, with_coefs
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +143,37 @@ def test_temperatures(v, layout, dtype, temperature):
         got = lce.policy_logits(Z, *args, temperature=temperature, grad=grad)
         check_policy(Z, y.numpy(), got, o, temperature, dtype)
     assert torch.isfinite(got[1]).all()
+
+
+@pytest.mark.parametrize("temperature", [0.05, 1e-3, 1e-4, 1e-5, 1e-6, 1e-9, 2.0 ** -64, 1e9])
+@pytest.mark.parametrize("n,v,chunk", [(7, 129, 1024), (300, 1000, 1024), (400, 5003, 64)])
+def test_temperatures_over_the_head(n, v, chunk, temperature):
+    # values of a quarter to three: every product and sum of a logit is exact, in whichever order it is formed, so
+    # that nothing but the softmax is looked at
+    d = 64
+    g = torch.Generator().manual_seed(n + v)
+    H = (torch.randint(-12, 13, (n, d), generator=g) / 4).bfloat16()
+    W = (torch.randint(-12, 13, (v, d), generator=g) / 4).bfloat16()
+    Z = (H.double() @ W.double().t()).numpy()
+    y = torch.from_numpy(Z.argmax(1))    # the most likely token: log p is 0, or that of a tie
+    y[torch.rand(n, generator=g) < 0.3] = -100
+    y[0] = 3                             # an unlikely one, whose log probability is checked alone
+    a, old, ref = policy_inputs(torch.from_numpy(Z), y, temperature, 2)
+    a[0] = 0.0
+    args = [t.cuda() for t in (H, W, y, a, old)]
+    how = dict(temperature=temperature, chunk=chunk)
+    exact = old.double().numpy()
+    exact[0] = ao.log_softmax_of(Z, y.numpy(), temperature)[0][0]
+    o = ao.policy(Z, y.numpy(), a.numpy(), exact, temperature=temperature)
+    loss, logprobs, dH, dW = lce.policy_fwd_bwd(*args, **how)
+    lb = row_bound(Z, y.numpy(), temperature)
+    assert (np.abs(cpu64(logprobs) - o["logprobs"]) <= np.where(o["ok"], lb, 0.0)).all()
+    lb = lb[1:].max()
+    count = o["ok"].sum()
+    assert abs(loss.item() - o["loss"]) <= (2 * lb + 2.0 ** -20) * o["terms"].sum() / count
+    check_gradients(dH, dW, H, W, with_coefs(o, y, o["mass"]), lb)
+    frozen = lce.policy_fwd_bwd(*args, **how, compute_dW=False)
+    assert torch.equal(frozen[0], loss) and torch.equal(frozen[1], logprobs)
+    check_gradients(frozen[2], None, H, W, with_coefs(o, y, o["mass"]), lb)
+    l2, lp2 = lce.policy_forward(*args, **how)
+    assert torch.equal(lp2, logprobs) and torch.equal(l2, loss)
