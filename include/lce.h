@@ -423,8 +423,8 @@ lce_status lce_fp8_linear(const void *X, int x_dtype, int64_t ldx, const void *W
  * multiples of 2^-39 of it). X, out, scale need the
  * alignment of their elements only, q that of 16 bytes. Columns of out from V on are left
  * as they were. Workspace: lce_int4_linear_workspace_size bytes (0 and NULL for few tokens, whose device status
- * nothing records: results after a wait that ran out are NaN), 16-byte aligned, with the device status
- * (lce_read_status); it keeps nothing; calls that may run at the same time need one each. */
+ * nothing records), 16-byte aligned, with the device status (lce_read_status); results after a wait that ran out are
+ * NaN. It keeps nothing; calls that may run at the same time need one each. */
 lce_status lce_int4_quantize(const void *W, int w_dtype, int64_t ldw, int64_t V, int64_t D, int group, void *q,
                              int64_t ldq, void *scale, int scale_dtype, int64_t lds, lce_stream_t stream);
 lce_status lce_int4_linear_workspace_size(int64_t M, int64_t D, int group, size_t *bytes);
@@ -524,6 +524,14 @@ lce_status lce_read_status(const void *ws, lce_stream_t stream);
  * records the timeout in the header and the kernel returns.
  * lce_read_status(ws) then returns LCE_ERR_TIMEOUT and the stream stays usable. */
 lce_status lce_selftest_wait_timeout(void *ws, size_t ws_bytes, int64_t limit_us,
+                                     lce_stream_t stream);
+
+/* The same for lce_int4_linear with a workspace: its arguments, but no stage of the weight is brought, so that every
+ * wait for one gives up after limit_us microseconds. The call's results are NaN then, and lce_read_status(ws) returns
+ * LCE_ERR_TIMEOUT. Calls that take no workspace: LCE_ERR_INVALID_ARG. */
+lce_status lce_selftest_int4_timeout(const void *X, int x_dtype, int64_t ldx, const void *q, int64_t ldq,
+                                     const void *scale, int64_t lds, int group, int64_t M, int64_t V, int64_t D,
+                                     void *out, int64_t ldc, void *ws, size_t ws_bytes, int64_t limit_us,
                                      lce_stream_t stream);
 
 /* Static string for a status code. */

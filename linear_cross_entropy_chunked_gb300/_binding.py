@@ -79,6 +79,7 @@ EXPORTED = (
     "lce_grad_norm",
     "lce_clip_grad_norm",
     "lce_selftest_wait_timeout",
+    "lce_selftest_int4_timeout",
     "lce_read_status",
     "lce_status_string",
     "lce_version",
@@ -182,6 +183,8 @@ def lib() -> ctypes.CDLL:
     L.lce_int4_quantize.argtypes = [_vp, _i, _i64, _i64, _i64, _i, _vp, _i64, _vp, _i, _i64, _vp]
     L.lce_int4_linear.argtypes = [_vp, _i, _i64, _vp, _i64, _vp, _i64, _i, _i64, _i64, _i64, _vp, _i64, _vp,
                                   ctypes.c_size_t, _vp]
+    L.lce_selftest_int4_timeout.argtypes = [_vp, _i, _i64, _vp, _i64, _vp, _i64, _i, _i64, _i64, _i64, _vp, _i64, _vp,
+                                            ctypes.c_size_t, _i64, _vp]
     L.lce_int4_linear_workspace_size.argtypes = [_i64, _i64, _i, _sz]
     L.lce_scale.argtypes = [_vp, _i, _vp, _i64, _vp, _i, _vp]
     L.lce_sample_logits.argtypes = [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _f,
@@ -215,7 +218,7 @@ def lib() -> ctypes.CDLL:
                  "lce_fwd_bwd_ex", "lce_read_status", "lce_version", "lce_last_launch_count",
                  "lce_ce_logits_workspace_size", "lce_ce_logits", "lce_rmsnorm_forward",
                  "lce_workspace_size_opt", "lce_forward_opt", "lce_backward_opt", "lce_fwd_bwd_opt",
-                 "lce_selftest_wait_timeout",
+                 "lce_selftest_wait_timeout", "lce_selftest_int4_timeout",
                  "lce_rmsnorm_backward_workspace_size", "lce_rmsnorm_backward",
                  "lce_norm_workspace_size", "lce_norm_fwd_bwd", "lce_norm_workspace_size_opt",
                  "lce_norm_fwd_bwd_opt", "lce_forward_workspace_size", "lce_count_valid",

@@ -2429,9 +2429,12 @@ lce_status lce_int4_linear_workspace_size(int64_t M, int64_t D, int group, size_
     return LCE_OK;
 }
 
-lce_status lce_int4_linear(const void *X, int x_dtype, int64_t ldx, const void *q, int64_t ldq, const void *scale,
-                           int64_t lds, int group, int64_t M, int64_t V, int64_t D, void *out, int64_t ldc,
-                           void *ws, size_t ws_bytes, lce_stream_t stream) {
+namespace {
+
+// bring: false for the self-test, whose waits run out after limit_ns.
+lce_status int4_linear(const void *X, int x_dtype, int64_t ldx, const void *q, int64_t ldq, const void *scale,
+                       int64_t lds, int group, int64_t M, int64_t V, int64_t D, void *out, int64_t ldc, void *ws,
+                       size_t ws_bytes, bool bring, unsigned long long limit_ns, lce_stream_t stream) {
     g_launches = 0;
     if (x_dtype != CE_BF16 && x_dtype != CE_FP16) return LCE_ERR_INVALID_ARG;
     if (group != 32 && group != 64 && group != 128) return LCE_ERR_INVALID_ARG;
@@ -2490,7 +2493,8 @@ lce_status lce_int4_linear(const void *X, int x_dtype, int64_t ldx, const void *
     p.row_tiles = static_cast<int>(cdiv(V, 128));
     p.token_tiles = static_cast<int>(cdiv(M, n));
     if (static_cast<long long>(p.row_tiles) * p.token_tiles > 0x7fffffffll) return LCE_ERR_INVALID_ARG;
-    p.timeout_ns = kDefaultTimeoutNs;
+    p.bring = bring ? 1 : 0;
+    p.timeout_ns = limit_ns;
     const uint64_t dims[2] = {static_cast<uint64_t>((D + 31) / 32 * 16), static_cast<uint64_t>(V)};
     const uint64_t st[1] = {static_cast<uint64_t>(ldq)};
     const uint32_t box[2] = {128, 128};
@@ -2501,6 +2505,27 @@ lce_status lce_int4_linear(const void *X, int x_dtype, int64_t ldx, const void *
     LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_int4_tokens(p, X, ldx, x_vec, tokens, s));
     LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_int4_tiles(p, n, sms, s));
     return LCE_OK;
+}
+
+}  // namespace
+
+lce_status lce_int4_linear(const void *X, int x_dtype, int64_t ldx, const void *q, int64_t ldq, const void *scale,
+                           int64_t lds, int group, int64_t M, int64_t V, int64_t D, void *out, int64_t ldc,
+                           void *ws, size_t ws_bytes, lce_stream_t stream) {
+    return int4_linear(X, x_dtype, ldx, q, ldq, scale, lds, group, M, V, D, out, ldc, ws, ws_bytes, true,
+                       kDefaultTimeoutNs, stream);
+}
+
+lce_status lce_selftest_int4_timeout(const void *X, int x_dtype, int64_t ldx, const void *q, int64_t ldq,
+                                     const void *scale, int64_t lds, int group, int64_t M, int64_t V, int64_t D,
+                                     void *out, int64_t ldc, void *ws, size_t ws_bytes, int64_t limit_us,
+                                     lce_stream_t stream) {
+    if (limit_us < 1 || limit_us > 2000000) return LCE_ERR_INVALID_ARG;
+    size_t need = 0;
+    LCE_TRY(lce_int4_linear_workspace_size(M, D, group, &need));
+    if (need == 0) return LCE_ERR_INVALID_ARG;
+    return int4_linear(X, x_dtype, ldx, q, ldq, scale, lds, group, M, V, D, out, ldc, ws, ws_bytes, false,
+                       static_cast<unsigned long long>(limit_us) * 1000ull, stream);
 }
 
 lce_status lce_grad_norm_workspace_size(int64_t n, size_t *bytes) {

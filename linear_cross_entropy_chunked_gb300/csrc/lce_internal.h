@@ -467,6 +467,7 @@ struct Int4TileParams {
     int dtype, M, V, D, units, groups;
     int per;                   // groups of a unit
     int row_tiles, token_tiles, stages;
+    int bring;                 // 0: no stage is brought, so that every wait runs out (self-test)
     int *hdr;
     unsigned long long timeout_ns;
 };
