@@ -415,8 +415,8 @@ lce_status lce_fp8_linear(const void *X, int x_dtype, int64_t ldx, const void *W
  * are read; what lies behind value D - 1 there counts for nothing. D up to 65536.
  *
  * lce_int4_quantize: W [V][ldw] (w_dtype as for lce_ce_logits); a group's scale is a seventh of its
- * largest magnitude in scale_dtype (0 bf16, 2 fp16; 1 for a group of zeros, NaN for one with an
- * infinity or a NaN), q = 8 + the nearest whole number to w / scale within -8 .. 7 (ties to even).
+ * largest magnitude in scale_dtype (0 bf16, 2 fp16; within that type's smallest and largest positive number; 1 for a
+ * group of zeros, NaN for one with an infinity or a NaN), q = 8 + the nearest whole number to w / scale within -8 .. 7 (ties to even).
  * lce_int4_linear: out [M][ldc] = X W^T for X [M][ldx], both x_dtype (0 bf16, 2 fp16), the type of
  * the scales: sums of a group in fp32, scaled and added up in fp32, rounded once (bf16 tokens are multiplied by a
  * power of two into fp16's range, in which what lies below 2^-29 of a token's largest magnitude is rounded to

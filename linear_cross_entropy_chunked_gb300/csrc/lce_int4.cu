@@ -819,6 +819,14 @@ __global__ void __launch_bounds__(I4X_THREADS) lce_int4_tokens_kernel(const Int4
 
 constexpr int I4Q_THREADS = 256;
 
+template <typename S> struct ScaleRange;
+template <> struct ScaleRange<__nv_bfloat16> {
+    static constexpr float smallest = 0x1p-133f, largest = 0x1.fep127f;
+};
+template <> struct ScaleRange<__half> {
+    static constexpr float smallest = 0x1p-24f, largest = 65504.f;
+};
+
 template <typename W, typename S>
 __global__ void __launch_bounds__(I4Q_THREADS) lce_int4_quantize_kernel(const Int4QuantParams p) {
     const int lane = threadIdx.x & 31;
@@ -842,11 +850,12 @@ __global__ void __launch_bounds__(I4Q_THREADS) lce_int4_quantize_kernel(const In
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         any |= __shfl_xor_sync(0xffffffffu, any, o);
     }
-    // a seventh of the largest magnitude, as the scale's type has it; a group that holds an infinity or a
-    // NaN gets a NaN
-    const S s16 = from_float<S>(amax / 7.f);
-    float s = to_float(s16);
-    if (!(s > 0.f)) s = 1.f;
+    // a seventh of the largest magnitude, as the scale's type has it, within its smallest and largest positive
+    // number (fp16 has neither a seventh of 1e-7 nor of 1e6): values beyond are -8 or 7 of the largest, and
+    // those below half the smallest are 0; a group that holds an infinity or a NaN gets a NaN
+    using Range = ScaleRange<S>;
+    const S s16 = from_float<S>(fminf(fmaxf(amax / 7.f, Range::smallest), Range::largest));
+    const float s = amax > 0.f ? to_float(s16) : 1.f;
     if (k0 < (p.D + 31) / 32 * 32) {
         uint32_t q = 0;
 #pragma unroll

@@ -29,8 +29,8 @@ def _row_bytes(D):
 
 def int4_weight(W, group: int = 128, scale_dtype=None, stream=None) -> Int4Weight:
     """W [V, D] (bf16, fp16 or fp32, unit column stride, any row stride) in 4 bits: a group's scale is a
-    seventh of its largest magnitude, in scale_dtype (bf16 or fp16; default: W's, bf16 for fp32); the values
-    are the nearest whole numbers within -8 .. 7, ties to even."""
+    seventh of its largest magnitude, in scale_dtype (bf16 or fp16; default: W's, bf16 for fp32), within that type's
+    smallest and largest positive number; the values are the nearest whole numbers within -8 .. 7, ties to even."""
     ldw = _check_dense_rows("W", W, _b._CE_DTYPES, "bfloat16, float16 or float32")
     if group not in GROUPS:
         raise ValueError(f"group must be one of {GROUPS}")
