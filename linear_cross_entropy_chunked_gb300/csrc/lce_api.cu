@@ -1340,7 +1340,7 @@ PolicyParams policy_params(const float *advantages, const float *old_logprobs, c
 struct PrefLayout {
     Layout L;
     GatherLayout gather;
-    size_t off_lse = 0, off_zx = 0, off_fix = 0, off_coef = 0, off_pair = 0, total = 0;
+    size_t off_lse = 0, off_zx = 0, off_fix = 0, off_coef = 0, off_pair = 0, off_clean = 0, total = 0;
 };
 
 // (chunk: as answer_chunk has it)
@@ -1359,6 +1359,7 @@ bool make_pref_layout(int64_t N, int64_t D, int64_t V, int64_t chunk, int64_t pa
     P.off_zx = take(sizeof(float) * static_cast<size_t>(P.L.C > 0 ? P.L.C : 1));
     P.off_fix = take(2 * rows);
     P.off_pair = take(sizeof(float) * static_cast<size_t>(pairs));
+    P.off_clean = take(sizeof(int) * static_cast<size_t>(2 * pairs + 1));
     if (grad) P.off_coef = take(rows);
     P.total = off;
     return true;
@@ -1378,11 +1379,12 @@ lce_status preference_check(const int64_t *offsets, int64_t pairs, const float *
 
 PairParams pair_params(const int64_t *offsets, int64_t pairs, int64_t N, int64_t V, int64_t ign, const int64_t *y,
                        const float *loss_rows, const float *ref, float beta, float smoothing, int average,
-                       const float *dloss, int reduction, float *loss, float *seq, float *pair_loss, float *coef,
-                       int *hdr) {
+                       const float *dloss, int reduction, float *loss, float *seq, float *pair_loss, int *clean,
+                       float *coef, int *hdr) {
     const bool none = reduction == LCE_REDUCTION_NONE;
     PairParams p;
     p.offsets = reinterpret_cast<const long long *>(offsets);
+    p.clean = pairs > PAIRS_BY_THEMSELVES ? clean : nullptr;
     p.pairs = pairs;
     p.N = N;
     p.V = V;
@@ -1824,9 +1826,11 @@ lce_status lce_preference_fwd_bwd(const void *H, const void *W, const int64_t *y
     }
     PairParams pp = pair_params(offsets, pairs, N, V, ignore_index, y, c.loss_rows, ref_logprobs, beta, label_smoothing,
                                 average, dloss, reduction, loss, seq_logprobs,
-                                reinterpret_cast<float *>(c.ws + P.off_pair), coef, c.hdr);
+                                reinterpret_cast<float *>(c.ws + P.off_pair),
+                                reinterpret_cast<int *>(c.ws + P.off_clean), coef, c.hdr);
     pp.fix = c.fix;
     pp.place = c.index ? reinterpret_cast<const int *>(c.ws + P.gather.off_place) : nullptr;
+    if (pp.clean) LCE_LAUNCH(launch_offsets(pp, c.s));
     LCE_LAUNCH(launch_pairs(pp, c.s));
     if (!grad || n == 0) return LCE_OK;
     // the tile counters start again
@@ -2191,7 +2195,8 @@ lce_status lce_policy_logits(const void *Z, int z_dtype, int64_t ld, const int64
 lce_status lce_preference_logits_workspace_size(int64_t N, int64_t pairs, size_t *bytes) {
     if (!bytes || N < 0 || N > 0x7fffffffll || pairs <= 0 || pairs > (1ll << 24)) return LCE_ERR_INVALID_ARG;
     const size_t rows = align_up(sizeof(float) * static_cast<size_t>(N > 0 ? N : 1), 1024);
-    *bytes = 1024 + 4 * rows + align_up(sizeof(float) * static_cast<size_t>(pairs), 1024);
+    *bytes = 1024 + 4 * rows + align_up(sizeof(float) * static_cast<size_t>(pairs), 1024) +
+             align_up(sizeof(int) * static_cast<size_t>(2 * pairs + 1), 1024);
     return LCE_OK;
 }
 
@@ -2217,12 +2222,14 @@ lce_status lce_preference_logits(const void *Z, int z_dtype, int64_t ld, const i
     float *coef = reinterpret_cast<float *>(w + 1024 + rows);
     p.max_sum = reinterpret_cast<float2 *>(w + 1024 + 2 * rows);
     float *pair_loss = reinterpret_cast<float *>(w + 1024 + 4 * rows);
+    int *clean = reinterpret_cast<int *>(w + 1024 + 4 * rows + align_up(sizeof(float) * static_cast<size_t>(pairs_), 1024));
     LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_answer_scan(p.y, N, V, ignore_index, p.hdr, s));
     if (N > 0) LCE_LAUNCH_KIND(LCE_KERNEL_MERGE, s, launch_answer_rows(p, sms, s));
-    LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s,
-                    launch_pairs(pair_params(offsets, pairs_, N, V, ignore_index, y, p.loss_rows, ref_logprobs, beta,
-                                             label_smoothing, average, dloss, reduction, loss, seq_logprobs,
-                                             pair_loss, dZ ? coef : nullptr, p.hdr), s));
+    const PairParams pp = pair_params(offsets, pairs_, N, V, ignore_index, y, p.loss_rows, ref_logprobs, beta,
+                                      label_smoothing, average, dloss, reduction, loss, seq_logprobs, pair_loss, clean,
+                                      dZ ? coef : nullptr, p.hdr);
+    if (pp.clean) LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_offsets(pp, s));
+    LCE_LAUNCH_KIND(LCE_KERNEL_OTHER, s, launch_pairs(pp, s));
     if (dZ && N > 0) {
         p.dZ = dZ;
         p.coef = coef;

@@ -341,6 +341,7 @@ struct AnswerParams {
 // one of pair k is sequence k, the rejected one sequence pairs + k.
 struct PairParams {
     const long long *offsets;   // [2 pairs + 1]
+    int *clean;                 // null, or [2 pairs + 1]: their running maxima, within [0, N] (launch_offsets)
     long long pairs, N, V, ignore_index;
     const long long *y;
     const float *loss_rows;     // [N]: -log p of each counting row
@@ -539,6 +540,8 @@ cudaError_t launch_answer_scan(const long long *y, long long N, long long V, lon
                                cudaStream_t s);
 cudaError_t launch_answer_rows(const AnswerParams &p, int sms, cudaStream_t s);
 cudaError_t launch_answer_grad(const AnswerParams &p, int sms, cudaStream_t s);
+constexpr long long PAIRS_BY_THEMSELVES = 512;   // without launch_offsets
+cudaError_t launch_offsets(const PairParams &p, cudaStream_t s);
 cudaError_t launch_pairs(const PairParams &p, cudaStream_t s);
 // dst[i] = src[i] * *scale
 cudaError_t launch_scale(const void *src, int src_dtype, const float *scale, long long n, void *dst, int dst_dtype,
