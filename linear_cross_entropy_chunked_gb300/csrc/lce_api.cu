@@ -767,9 +767,12 @@ lce_status run_bwd(const Ctx &c, long long row0, long long rows, int slot, const
 lce_status run_grad(const Ctx &c, long long row0, long long rows, int slot, void *dHc,
                     bool acc_dh, float *dW, bool acc_dw, const float *dloss, const GradSpec &g) {
     if (g.dw_only) return run_bwd(c, row0, rows, slot, DhOut{dHc, false, 1, 0}, dW, acc_dw, dloss, g);
-    if (c.rests.first)
+    if (c.rests.first) {
+        int n = 1;
         LCE_LAUNCH(launch_label_lists(reinterpret_cast<const long long *>(c.y) + row0, c.index ? c.hdr + HDR_NVALID : nullptr,
-                                      row0, rows, c.V, c.ign, c.rests.first, c.rests.next, c.s));
+                                      row0, rows, c.V, c.ign, c.rests.first, c.rests.next, c.sms, &n, c.s));
+        g_launches += n - 1;
+    }
     const int want = dh_parts(c, rows, g.dh_alone);
     if (want <= 1 && !acc_dh && !c.index)
         return run_bwd(c, row0, rows, slot, DhOut{dHc, false, 1, 0}, dW, acc_dw, dloss, g);

@@ -596,8 +596,10 @@ __global__ void __launch_bounds__(256) lce_gather_rows_kernel(const GatherParams
     }
 }
 
-// A thread per row compares its label with all of the chunk (a few us for 2048 rows; n^2 / 4 comparisons are far less than
-// the contractions' n V D). Which rows a list has, and their order, depend on the labels alone.
+// A thread per row compares its label with all of the chunk (a few us for 2048 rows). Which rows a list has, and their order,
+// depend on the labels alone. Chunks of more than LISTS_BY_COMPARING rows go by the kernels behind it (a policy step in one
+// chunk, 1000 x 64: 32768 rows 900 -> 533 us, 131072 rows 7460 -> 1890; 16384 rows, which stay here: 455).
+constexpr long long LISTS_BY_COMPARING = 16384;
 __global__ void __launch_bounds__(256) lce_label_lists_kernel(const long long *__restrict__ y, const int *__restrict__ counting,
                                                               int row0, int rows, long long V, long long ign,
                                                               int *__restrict__ first, int *__restrict__ next) {
@@ -632,6 +634,38 @@ __global__ void __launch_bounds__(256) lce_label_lists_kernel(const long long *_
     if (mine < 0) return;
     if (before == 0) first[mine] = r;
     next[r] = before + 1 < REST_ROWS ? after : -1;
+}
+
+// The same lists in time that grows with the rows: a pass over them finds one more row of every list, the smallest behind
+// the one found before. `step` 0: the first rows (first and next hold LIST_END where there is none yet); step
+// k: the k-th next one, from the end of the list so far, k - 1 steps from its first row, which no thread of this pass writes.
+constexpr int LIST_END = 0x7f7f7f7f;   // (more than any row, and one byte over and over)
+
+__global__ void __launch_bounds__(256) lce_label_step_kernel(const long long *__restrict__ y, const int *__restrict__ counting,
+                                                             int row0, int rows, long long V, long long ign, int step,
+                                                             int *first, int *next) {
+    const int live = live_rows(counting, row0, rows);
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < live; i += 256ll * gridDim.x) {
+        const int r = static_cast<int>(i);
+        const long long v = y[r];
+        if (v == ign || v < 0 || v >= V) continue;
+        int *at = first + v;
+        for (int k = 0; k < step; ++k) {
+            const int e = *at;
+            at = e == LIST_END || e >= r ? nullptr : next + e;   // (a list that ended, or a row that is in it or before its end)
+            if (!at) break;
+        }
+        // (most rows of a frequent label are not the next one: a look, even an old one, saves the operation on one address)
+        if (at && *const_cast<volatile int *>(at) > r) atomicMin(at, r);
+    }
+}
+
+__global__ void __launch_bounds__(256) lce_label_ends_kernel(int *__restrict__ first, long long V, int *__restrict__ next,
+                                                             long long rows) {
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < V || i < rows; i += 256ll * gridDim.x) {
+        if (i < V && first[i] == LIST_END) first[i] = -1;
+        if (i < rows && next[i] == LIST_END) next[i] = -1;
+    }
 }
 
 // The rows of dH that were brought together, to theirs of the call's; what rounding left of their label entries is added
@@ -783,7 +817,21 @@ cudaError_t launch_gather_rows(const GatherParams &p, int sms, cudaStream_t s) {
 }
 
 cudaError_t launch_label_lists(const long long *y, const int *counting, long long row0, long long rows, long long V,
-                               long long ign, int *first, int *next, cudaStream_t s) {
+                               long long ign, int *first, int *next, int sms, int *launches, cudaStream_t s) {
+    *launches = 1;
+    if (rows > LISTS_BY_COMPARING) {
+        if (rows >= LIST_END) return cudaErrorInvalidValue;
+        cudaError_t e = cudaMemsetAsync(first, 0x7f, sizeof(int) * static_cast<size_t>(V), s);   // LIST_END
+        if (e == cudaSuccess) e = cudaMemsetAsync(next, 0x7f, sizeof(int) * static_cast<size_t>(rows), s);
+        if (e != cudaSuccess) return e;
+        auto blocks = [&](long long n) { return static_cast<unsigned>((n + 255) / 256 < 8ll * sms ? (n + 255) / 256 : 8ll * sms); };
+        for (int step = 0; step < REST_ROWS; ++step)
+            lce_label_step_kernel<<<blocks(rows), 256, 0, s>>>(y, counting, static_cast<int>(row0), static_cast<int>(rows), V,
+                                                               ign, step, first, next);
+        lce_label_ends_kernel<<<blocks(V > rows ? V : rows), 256, 0, s>>>(first, V, next, rows);
+        *launches = REST_ROWS + 1;
+        return cudaGetLastError();
+    }
     const cudaError_t e = cudaMemsetAsync(first, 0xff, sizeof(int) * static_cast<size_t>(V), s);   // -1
     if (e != cudaSuccess) return e;
     lce_label_lists_kernel<<<static_cast<unsigned>((rows + 255) / 256), 256, 0, s>>>(

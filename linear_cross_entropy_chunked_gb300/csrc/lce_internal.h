@@ -561,7 +561,7 @@ cudaError_t launch_compact(const long long *y, long long N, long long V, long lo
 // dst[j][D] = src[index[row0 + j]][D] for the rows there are of [row0, row0 + rows), zeros up to a multiple of 64
 // The lists of LabelRests for the chunk's labels y (counting, row0: as for the rows brought together).
 cudaError_t launch_label_lists(const long long *y, const int *counting, long long row0, long long rows, long long V,
-                               long long ign, int *first, int *next, cudaStream_t s);
+                               long long ign, int *first, int *next, int sms, int *launches, cudaStream_t s);
 // What a chunk's rows are brought together from, and (W given) their labels' logits taken from.
 struct GatherParams {
     const uint4 *src;            // H: the call's (with index) or the chunk's
