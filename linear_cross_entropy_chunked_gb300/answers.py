@@ -240,17 +240,18 @@ def _scale_in_place(t, scale, s):
 
 class AnswerLossFunction(torch.autograd.Function):
     """A loss on answers over the head. The forward forms the gradients for an upstream gradient
-    of 1 (fwd_bwd), in the dtypes of H and W where that takes one contraction; the backward scales them, which
-    the loss is linear in, in place (nothing is read or written where the upstream gradient is 1; another one
-    rounds once more), and hands them over. A second backward through the same graph forms them again, and so
-    does a backward that is captured without its forward (each replay would scale them once more; captured in a
-    graph of its own behind that of its forward, it is replayed once for each replay of that). A W without
-    requires_grad is frozen (no dW work). The log probabilities beside the loss carry no gradient."""
+    of 1 (fwd_bwd), dH in H's dtype and dW in the one that it is told; the backward scales them, which
+    the loss is linear in, in place (nothing is read or written where the upstream gradient is 1; one that is no
+    power of two rounds bf16 gradients once more, an fp32 dW only then), and hands them over. A second backward
+    through the same graph forms them again, and so does a backward that is captured without its forward (each
+    replay would scale them once more; captured in a graph of its own behind that of its forward, it is replayed once
+    for each replay of that). A W without requires_grad is frozen (no dW work). The log probabilities beside the loss
+    carry no gradient."""
 
     @staticmethod
-    def forward(ctx, H, W, fwd_bwd, one, *constants):
+    def forward(ctx, H, W, fwd_bwd, dW_dtype, *constants):
         train = ctx.needs_input_grad[1]
-        how = {"compute_dW": train, "dW_dtype": torch.bfloat16 if train and one else torch.float32}
+        how = {"compute_dW": train, "dW_dtype": dW_dtype if train else torch.float32}
         loss, logprobs, *gradients = fwd_bwd(H, W, *constants, **how)
         ctx.gradients = [gradients]   # (taken once, whichever of two threads comes first)
         ctx.save_for_backward(H, W, *constants)
@@ -284,9 +285,16 @@ class AnswerLossFunction(torch.autograd.Function):
         return (dH if ctx.needs_input_grad[0] else None, dW, None, None) + (None,) * (len(tensors) - 2)
 
 
-def _one_buffer(H, chunk, low_memory):
-    """Whether the rows fill one chunk buffer, so that dW is one contraction."""
-    return H.shape[0] <= (1 if low_memory else 2) * chunk
+def _dW_dtype(dtype, H, chunk, low_memory):
+    """bf16 by default where the rows fill one chunk buffer, so that dW is one contraction: a third of the memory traffic."""
+    one = H.shape[0] <= (1 if low_memory else 2) * chunk
+    if dtype is None:
+        return torch.bfloat16 if one else torch.float32
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("dW_dtype must be float32 or bfloat16")
+    if dtype == torch.bfloat16 and not one:
+        raise ValueError("dW_dtype bfloat16 needs rows that fill one chunk buffer")
+    return dtype
 
 
 def _summed(what, reduction):
@@ -297,11 +305,14 @@ def _summed(what, reduction):
 
 def linear_policy_loss(H, W, y, advantages, old_logprobs=None, ref_logprobs=None, weights=None, clip_low=0.2,
                        clip_high=0.2, beta=0.0, temperature=1.0, chunk: int = 1024,
-                       ignore_index: int = _b.IGNORE_INDEX, reduction: str = "mean", low_memory: bool = False):
+                       ignore_index: int = _b.IGNORE_INDEX, reduction: str = "mean", low_memory: bool = False,
+                       dW_dtype=None):
     """(loss, logprobs): the clipped policy loss with a KL term over the head (policy_fwd_bwd says
     what the arguments are), differentiable in H and W for the reductions mean and sum. The
     logprobs [N] are those of the policy as it is now, and carry no gradient. A W with
-    requires_grad False is frozen."""
+    requires_grad False is frozen. dW_dtype: in what the weight's gradient is kept until the upstream gradient is
+    known; None: bf16 where the rows fill one buffer, which is fastest; float32: an upstream gradient of 1 / 3 (a loss over
+    three micro-batches) does not round it a second time."""
     _summed("linear_policy_loss", reduction)
     how = {"old_logprobs": old_logprobs, "ref_logprobs": ref_logprobs, "weights": weights, "clip_low": clip_low,
            "clip_high": clip_high, "beta": beta, "temperature": temperature, "chunk": chunk,
@@ -314,16 +325,17 @@ def linear_policy_loss(H, W, y, advantages, old_logprobs=None, ref_logprobs=None
         _constant(name, how.pop(name))
     return AnswerLossFunction.apply(
         H, W, lambda *t, **more: policy_fwd_bwd(*t, low_memory=low_memory, **how, **more),
-        _one_buffer(H, chunk, low_memory), y, advantages, old_logprobs, ref_logprobs, weights)
+        _dW_dtype(dW_dtype, H, chunk, low_memory), y, advantages, old_logprobs, ref_logprobs, weights)
 
 
 def linear_preference_loss(H, W, y, offsets, ref_logprobs=None, beta=0.1, label_smoothing=0.0,
                            average: bool = False, chunk: int = 1024, ignore_index: int = _b.IGNORE_INDEX,
-                           reduction: str = "mean", low_memory: bool = False):
+                           reduction: str = "mean", low_memory: bool = False, dW_dtype=None):
     """(loss, seq_logprobs): the preference loss of paired log ratios over the head
     (preference_fwd_bwd says what the arguments are), differentiable in H and W for the
     reductions mean and sum. seq_logprobs [2 pairs] carry no gradient; without gradients the call
-    gives a reference model's, which are this one's ref_logprobs. A W with requires_grad False is frozen."""
+    gives a reference model's, which are this one's ref_logprobs. A W with requires_grad False is frozen.
+    dW_dtype: as for linear_policy_loss."""
     _summed("linear_preference_loss", reduction)
     how = {"ref_logprobs": ref_logprobs, "beta": beta, "label_smoothing": label_smoothing, "average": average,
            "chunk": chunk, "ignore_index": ignore_index, "reduction": reduction, "low_memory": low_memory}
@@ -332,7 +344,7 @@ def linear_preference_loss(H, W, y, offsets, ref_logprobs=None, beta=0.1, label_
         return loss.view(()), seq
     _constant("ref_logprobs", how.pop("ref_logprobs"))
     return AnswerLossFunction.apply(H, W, lambda *t, **more: preference_fwd_bwd(*t, **how, **more),
-                                    _one_buffer(H, chunk, low_memory), y, offsets, ref_logprobs)
+                                    _dW_dtype(dW_dtype, H, chunk, low_memory), y, offsets, ref_logprobs)
 
 
 def _check_logits(Z, y):
