@@ -266,7 +266,7 @@ lce_status lce_ce_logits(const void *Z, int z_dtype, int64_t ld, const int64_t *
  * lce_policy_workspace_size (gradient = 1).
  * LCE_DW_BF16: dW is bf16, rounded once from the fp32 sums; where the rows fill one chunk buffer (N <= 2 chunk;
  * chunk with LCE_LOW_MEMORY), W is trained and dW not added to, else LCE_ERR_UNSUPPORTED.
- * lce_policy_forward: loss and logprobs alone, workspace with gradient = 0.
+ * lce_policy_forward: loss and logprobs alone, H and W bf16 too, workspace with gradient = 0.
  * lce_policy_logits: over given logits (z_dtype as for lce_ce_logits): one read of the
  * counting rows and one write of dZ (NULL: no gradient; Z itself: in place), V up to 450000 (16-bit) or
  * 225000 (fp32) (more: a second read). Z, dZ: rows of any stride ld >= V from any element

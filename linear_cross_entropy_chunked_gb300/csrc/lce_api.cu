@@ -134,7 +134,8 @@ struct Layout {
 // waves: 252, 86 and 165.) With W trained too where a chunk has more than DH_BESIDE_TILES: the tiles are one long wave then that
 // leaves dW little beside it and gets out of step, which reads W and G again (1843 of 2048 rows x 128256 x 4096, a whole pass:
 // 3800 to 5200 us, among other work 3990 to 4430, in three parts 4030 and 4040 to 4170; 1440 rows: 3130 and 3140 to 3260, in three
-// 3025 and 3120 to 3200). 32 tiles are what dW goes well beside (8000 rows x 32000 x 2048, gradients: 1340 us, in four to six parts 1400).
+// 3025 and 3120 to 3200; the spread gets narrower, its middle hardly moves). 32 tiles are what dW goes well beside (8000 rows x
+// 32000 x 2048, gradients: 1340 us, in four to six parts 1400); nothing was measured between 32 and 64.
 constexpr int DH_ALONE_PAIRS = 76;
 constexpr int DH_BESIDE_TILES = 40;
 constexpr int DH_ANSWERS_MAX_SPLITS = 16;

@@ -930,7 +930,8 @@ cudaError_t int4_set_attributes() {
 
 // Whether so many tokens go by the kernel for few. Measured at 128256 x 4096, bf16 (us; tiles / few): groups of
 // 128: 1 token 70 / 62, 2: 71 / 66, 4: 71 / 75; of 64: 1: 90 / 76, 4: 91 / 84; of 32: 1: 153 / 95, 6: 153 / 102, 8 (two
-// passes): 154 / 193. Rows so long that the tokens do not fit beside eight warps' buffers go by tiles too.
+// passes): 154 / 193. The rule goes by tokens and groups alone: other D and V were not measured on both sides. Rows so
+// long that the tokens do not fit beside eight warps' buffers go by tiles too.
 bool int4_few(long long M, long long D, int group) {
     if (M > (group == 128 ? 2 : group == 64 ? 4 : 6)) return false;
     Int4Params p;
